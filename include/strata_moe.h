@@ -283,7 +283,13 @@ const char* strata_status_str(strata_status s);
 #define STRATA_KERNEL_HOST_COPY 14     /* copy between page-locked host memory and the workspace (host-buffer calls) */
 #define STRATA_KERNEL_WAIT_SELFTEST 15 /* strata_moe_wait_selftest */
 #define STRATA_KERNEL_BLOB_CRC32 16    /* strata_blob_crc32_device */
-#define STRATA_KERNEL_COUNT 17
+/* strata_moe_ops.h */
+#define STRATA_KERNEL_SELECT 17          /* strata_moe_select */
+#define STRATA_KERNEL_NORM 18            /* strata_moe_norm */
+#define STRATA_KERNEL_COMBINE_NORM 19    /* strata_moe_combine_norm */
+#define STRATA_KERNEL_ADAPTER_SHRINK 20  /* strata_moe_adapters: A_a x */
+#define STRATA_KERNEL_ADAPTER_EXPAND 21  /* strata_moe_adapters: base + scale * B_a (A_a x) */
+#define STRATA_KERNEL_COUNT 22
 
 /* Number of kernels this process has launched through the library so far (all threads). */
 uint64_t strata_moe_launch_count(void);

@@ -1,4 +1,4 @@
-"""Python binding of the GB300 routed-expert MoE block (C ABI in include/strata_moe.h).
+"""Python binding of the GB300 routed-expert MoE block (C ABI in include/strata_moe.h and include/strata_moe_ops.h).
 
 Argument marshalling only: every function has the name of the C entry point it calls, accepts
 torch tensors (device tensors for device pointers), raw integer addresses or None, and raises
@@ -47,6 +47,21 @@ EXPORTS = (
     "strata_moe_profile_recorded",
 )
 
+# Every symbol include/strata_moe_ops.h declares.
+OPS_EXPORTS = ("strata_moe_select", "strata_moe_norm", "strata_moe_combine_norm", "strata_moe_adapters")
+
+# element types, routing scores and flags of include/strata_moe_ops.h
+F32, BF16, F16 = 0, 1, 2
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+POST_NORM, TOKEN_SIGMOID = 1, 2
+SELECT_K_MAX = 32
+SELECT_GROUP_MAX = 32
+NORM_N_MAX = 16384
+NORM_PART_MAX = 32
+ADAPTER_RANK_MAX = 128
+ADAPTER_DIM_MAX = 16384
+ADAPTER_COUNT_MAX = 65536
+
 
 class StrataError(RuntimeError):
     def __init__(self, fn: str, status: int):
@@ -57,6 +72,34 @@ class StrataError(RuntimeError):
 class strata_experts_t(ctypes.Structure):
     _fields_ = [("blobs", ctypes.c_void_p), ("blob_stride", ctypes.c_int64),
                 ("n_expert", ctypes.c_int32), ("q2_offset", ctypes.c_int32), ("shared_blob", ctypes.c_void_p)]
+
+
+class strata_select_t(ctypes.Structure):
+    _fields_ = [("n_expert", ctypes.c_int32), ("top_k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("n_group", ctypes.c_int32), ("top_group", ctypes.c_int32), ("group_sum", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float), ("logits_type", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("logits_stride", ctypes.c_int64)]
+
+
+class strata_norm_t(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("eps", ctypes.c_float), ("x_type", ctypes.c_int32), ("out_type", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
+
+
+class strata_combine_norm_t(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("n_part", ctypes.c_int32), ("flags", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("block_scale", ctypes.c_float), ("part_type", ctypes.c_int32),
+                ("x_type", ctypes.c_int32), ("next_type", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("part_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("next_stride", ctypes.c_int64)]
+
+
+class strata_adapters_t(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("a_stride", ctypes.c_int64),
+                ("b_stride", ctypes.c_int64), ("n_adapter", ctypes.c_int32), ("rank", ctypes.c_int32),
+                ("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32), ("x_type", ctypes.c_int32),
+                ("y_type", ctypes.c_int32), ("x_stride", ctypes.c_int64), ("base_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -102,6 +145,12 @@ def lib():
             "strata_moe_launch_count": (ctypes.c_uint64, []),
             "strata_moe_profile_arm": (ctypes.c_int, [_i32, _i32, _vp, _vp, _i32]),
             "strata_moe_profile_recorded": (_i32, [_i32]),
+            "strata_moe_select": (ctypes.c_int, [ctypes.POINTER(strata_select_t), _vp, _i32, _vp, _vp, _vp, _vp]),
+            "strata_moe_norm": (ctypes.c_int, [ctypes.POINTER(strata_norm_t), _vp, _i32, _vp, _vp, _vp]),
+            "strata_moe_combine_norm": (ctypes.c_int, [ctypes.POINTER(strata_combine_norm_t), _vp, _vp, _vp, _i32, _vp,
+                                                       _vp, _vp, _vp, _vp, _vp, _vp]),
+            "strata_moe_adapters": (ctypes.c_int, [ctypes.POINTER(strata_adapters_t), _vp, _vp, _i32, _vp, _i32, _vp,
+                                                   _vp, _vp, _sz, _vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -247,6 +296,67 @@ def prepare_stack_host(ex_layers, w_router, bias, n_layers, x_host, T, ids, weig
                           _nbytes(ws, ws_bytes), _s(stream)))
 
 
+def select(n_expert: int, top_k: int = K, score: int = SCORE_SOFTMAX, n_group: int = 1, top_group: int = 1,
+           group_sum: int = 1, renorm: bool = True, scale: float = 1.0, logits_type: int = F32,
+           logits_stride=None) -> strata_select_t:
+    """A strata_select_t; logits_stride None: rows of n_expert elements."""
+    return strata_select_t(n_expert, top_k, score, n_group, top_group, group_sum, int(renorm), scale, logits_type, 0,
+                           n_expert if logits_stride is None else logits_stride)
+
+
+def norm(n: int = H, eps: float = 1e-6, x_type: int = F32, out_type: int = F32, x_stride=None,
+         out_stride=None) -> strata_norm_t:
+    """A strata_norm_t; strides None: dense rows."""
+    return strata_norm_t(n, eps, x_type, out_type, n if x_stride is None else x_stride,
+                         n if out_stride is None else out_stride)
+
+
+def combine_norm(n: int = H, n_part: int = K, post_norm: bool = True, token_sigmoid: bool = False, eps: float = 1e-6,
+                 residual_scale: float = 1.0, block_scale: float = 1.0, part_type: int = F32, x_type: int = F32,
+                 next_type: int = F32, part_stride=None, token_stride=None, x_stride=None, out_stride=None,
+                 next_stride=None) -> strata_combine_norm_t:
+    """A strata_combine_norm_t; strides None: dense parts [T][n_part][n] and rows."""
+    ps = n if part_stride is None else part_stride
+    return strata_combine_norm_t(n, n_part, (POST_NORM if post_norm else 0) | (TOKEN_SIGMOID if token_sigmoid else 0), eps,
+                                 residual_scale, block_scale, part_type, x_type, next_type, 0, ps,
+                                 n_part * ps if token_stride is None else token_stride,
+                                 n if x_stride is None else x_stride, n if out_stride is None else out_stride,
+                                 n if next_stride is None else next_stride)
+
+
+def adapters(a, b, n_adapter: int, rank: int, d_in: int = H, d_out: int = H, scale=None, x_type: int = F32,
+             y_type: int = F32, a_stride=None, b_stride=None, x_stride=None, base_stride=None,
+             y_stride=None) -> strata_adapters_t:
+    """A strata_adapters_t for device arrays a [n_adapter][rank][d_in], b [n_adapter][d_out][rank] (bf16) and scale
+    [n_adapter] (tensors or addresses; the caller keeps them alive); strides None: dense."""
+    return strata_adapters_t(_p(a), _p(b), _p(scale), rank * d_in if a_stride is None else a_stride,
+                             d_out * rank if b_stride is None else b_stride, n_adapter, rank, d_in, d_out, x_type, y_type,
+                             d_in if x_stride is None else x_stride, d_out if base_stride is None else base_stride,
+                             d_out if y_stride is None else y_stride)
+
+
+def strata_moe_select(sel, logits, T, bias, ids, weights, stream=None):
+    _check("strata_moe_select", lib().strata_moe_select(ctypes.byref(sel), _p(logits), T, _p(bias), _p(ids), _p(weights),
+                                                        _s(stream)))
+
+
+def strata_moe_norm(nd, x, T, gain, out, stream=None):
+    _check("strata_moe_norm", lib().strata_moe_norm(ctypes.byref(nd), _p(x), T, _p(gain), _p(out), _s(stream)))
+
+
+def strata_moe_combine_norm(cn, parts, part_weights, x, T, post_gain, channel_gate, token_gate, pre_gain, out, next,
+                            stream=None):
+    _check("strata_moe_combine_norm", lib().strata_moe_combine_norm(
+        ctypes.byref(cn), _p(parts), _p(part_weights), _p(x), T, _p(post_gain), _p(channel_gate), _p(token_gate),
+        _p(pre_gain), _p(out), _p(next), _s(stream)))
+
+
+def strata_moe_adapters(ad, seg_off, seg_adapter, n_seg, x, T, base, y, ws, ws_bytes=None, stream=None):
+    _check("strata_moe_adapters", lib().strata_moe_adapters(ctypes.byref(ad), _p(seg_off), _p(seg_adapter), n_seg, _p(x),
+                                                            T, _p(base), _p(y), _p(ws), _nbytes(ws, ws_bytes),
+                                                            _s(stream)))
+
+
 def strata_moe_wait_selftest(ws, limit_ns, ws_bytes=None, stream=None):
     """Run the bounded waits on conditions that never hold (see the header); poll the status after."""
     _check("strata_moe_wait_selftest", lib().strata_moe_wait_selftest(_p(ws), _nbytes(ws, ws_bytes), limit_ns,
@@ -293,7 +403,8 @@ def strata_status_str(status: int) -> str:
 # kernel ids of strata_moe_profile_arm (STRATA_KERNEL_* of the header)
 KERNELS = ("DECODE_LAYER", "ROUTE_DECODE", "ROUTER_PREP", "ROUTER_TC", "TOP_K", "GROUP_HIST", "GROUP_SCAN",
            "GROUP_SCATTER", "TC_PREPARE", "TC_GATHER",
-           "TC_GATEUP", "TC_DOWN", "COMBINE", "PACK", "HOST_COPY", "WAIT_SELFTEST", "BLOB_CRC32")
+           "TC_GATEUP", "TC_DOWN", "COMBINE", "PACK", "HOST_COPY", "WAIT_SELFTEST", "BLOB_CRC32", "SELECT", "NORM",
+           "COMBINE_NORM", "ADAPTER_SHRINK", "ADAPTER_EXPAND")
 KERNEL_ID = {name: i for i, name in enumerate(KERNELS)}
 
 

@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "strata_moe.h"
+#include "strata_moe_ops.h"
 
 namespace strata {
 
@@ -250,7 +251,8 @@ namespace strata {
 enum KernelId : int {
   KID_DECODE_LAYER = 0, KID_ROUTE_DECODE, KID_ROUTER_PREP, KID_ROUTER_TC, KID_TOP_K, KID_GROUP_HIST, KID_GROUP_SCAN,
   KID_GROUP_SCATTER, KID_TC_PREPARE, KID_TC_GATHER, KID_TC_GATEUP, KID_TC_DOWN, KID_COMBINE, KID_PACK, KID_HOST_COPY,
-  KID_WAIT_SELFTEST, KID_BLOB_CRC32, KID_COUNT
+  KID_WAIT_SELFTEST, KID_BLOB_CRC32, KID_SELECT, KID_NORM, KID_COMBINE_NORM, KID_ADAPTER_SHRINK, KID_ADAPTER_EXPAND,
+  KID_COUNT
 };
 void kernel_begin(int kid, cudaStream_t s);
 void kernel_end(int kid, cudaStream_t s);
@@ -340,6 +342,17 @@ struct DecodeNext {
 cudaError_t launch_decode_fused(const strata_experts_t& ex, const uint16_t* w_router, const float* bias,
                                 const float* x, int T, int residual, int alias, float* out, int32_t* ids, float* weights,
                                 const DecodeNext* next, const WsLayout& L, char* ws, cudaStream_t s);
+// The operators of strata_moe_ops.h (arguments checked by ops_abi.cu).
+cudaError_t launch_select(const strata_select_t& sel, const void* logits, int T, const float* bias, int32_t* ids,
+                          float* weights, cudaStream_t s);
+cudaError_t launch_norm(const strata_norm_t& nd, const void* x, int T, const float* gain, void* out, cudaStream_t s);
+cudaError_t launch_combine_norm(const strata_combine_norm_t& cn, const void* parts, const float* part_weights,
+                                const void* x, int T, const float* post_gain, const float* channel_gate,
+                                const float* token_gate, const float* pre_gain, void* out, void* next, cudaStream_t s);
+// v_parts: fp32 scratch of 1024 floats per token.
+cudaError_t launch_adapters(const strata_adapters_t& ad, const int32_t* seg_off, const int32_t* seg_adapter, int n_seg,
+                            const void* x, int T, const void* base, void* y, float* v_parts, int* status,
+                            cudaStream_t s);
 cudaError_t launch_pack_device(const uint8_t* canonical, int64_t src_stride, uint8_t* packed,
                                int64_t dst_stride, int64_t n_blobs, cudaStream_t s);
 }  // namespace strata

@@ -1,0 +1,191 @@
+"""strata_moe_adapters against its formula in 64 bits: ragged segments, every type, ranks and widths, in place, and the
+segments that it refuses on the device."""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+import ops_reference as ref
+import quantized_routed_expert_top10_gb300 as qre
+from gpu_common import workspace
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+KINDS = (qre.F32, qre.BF16, qre.F16)
+
+
+def rnd(*shape, seed=0, std=1.0, kind=qre.F32):
+    g = torch.Generator(DEV).manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device=DEV) * std).to(ref.TORCH[kind])
+
+
+def rows(T, n, stride, kind, seed):
+    return torch.as_strided(rnd(T * stride, seed=seed, kind=kind), (T, n), (stride, 1))
+
+
+class Case:
+    def __init__(self, lens, of, rank, d_in, d_out, xk=qre.F32, yk=qre.F32, n=5, pad=0, before=0, after=0, base=True,
+                 inplace=False, scale=True, seed=1, wpad=0):
+        self.off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32) + before
+        self.of = np.asarray(of, np.int32)
+        self.T = int(self.off[-1]) + after
+        self.rank, self.xk, self.yk = rank, xk, yk
+        self.x = rows(self.T, d_in, d_in + pad, xk, seed)
+        self.y = rows(self.T, d_out, d_out + pad, yk, seed + 1)
+        self.base = self.y if inplace else rows(self.T, d_out, d_out + 2 * pad, yk, seed + 2) if base else None
+        ast, bst = rank * d_in + wpad, rank * d_out + wpad
+        self.a = torch.as_strided(rnd(n * ast, seed=seed + 3, std=d_in ** -0.5, kind=qre.BF16), (n, rank, d_in), (ast, d_in, 1))
+        self.b = torch.as_strided(rnd(n * bst, seed=seed + 4, std=rank ** -0.5, kind=qre.BF16), (n, d_out, rank), (bst, rank, 1))
+        self.scale = rnd(n, seed=seed + 5) if scale else None
+        self.d = qre.adapters(self.a.data_ptr(), self.b.data_ptr(), n, rank, d_in, d_out, self.scale, xk, yk, ast, bst,
+                              d_in + pad, d_out + (pad if inplace else 2 * pad), d_out + pad)
+        self.d_in = d_in
+        self.dev_off, self.dev_of = torch.from_numpy(self.off).to(DEV), torch.from_numpy(self.of).to(DEV)
+        self.ws = workspace(self.T)
+
+    def call(self):
+        qre.strata_moe_adapters(self.d, self.dev_off, self.dev_of, len(self.of), self.x.data_ptr(), self.T,
+                                None if self.base is None else self.base.data_ptr(), self.y.data_ptr(), self.ws)
+
+    def check(self):
+        y0 = ref.to64(self.y)
+        base = None if self.base is None else ref.to64(self.base)
+        before = self.y.clone()
+        self.call()
+        assert qre.strata_poll_status(self.ws) == 0
+        want, delta = ref.adapters(ref.to64(self.x), ref.to64(self.a), ref.to64(self.b),
+                                   None if self.scale is None else ref.to64(self.scale), self.off, self.of, base, y0)
+        got = ref.to64(self.y)
+        assert np.isfinite(got).all()
+        lo, hi = self.off[0], self.off[-1]
+        assert torch.equal(self.y[:lo], before[:lo]) and torch.equal(self.y[hi:], before[hi:])
+        # the product's error by rows as 2-norms, the sum's and the result's rounding value by value
+        err = np.maximum(np.abs(got - want) - (ref.half_step(self.yk) + ref.U) * np.abs(want), 0.0)
+        row = np.sqrt(np.square(err).sum(1))
+        room = ref.adapters_rtol(self.d_in, self.rank, self.yk) * np.sqrt(np.square(delta).sum(1)) * 2 + 1e-30
+        if self.yk == qre.F16:
+            room = room + 2.0 ** -24 * np.sqrt(got.shape[1])
+        assert (row <= room).all(), (np.max(row / room), int(np.argmax(row / room)))
+        none = [i for i, ad in enumerate(self.of) if ad < 0]
+        for i in none:  # no adapter: the base itself
+            s = slice(self.off[i], self.off[i + 1])
+            if self.base is not None:
+                assert torch.equal(self.y[s], before[s] if self.base is self.y else self.base[s])
+            else:
+                assert (self.y[s] == 0).all()
+
+
+RAGGED = ([0, 1, 16, 17, 33, 0, 5, 64, 2, 0], [3, 0, 1, -1, 2, -1, 4, 2, 0, 0])
+
+
+@pytest.mark.parametrize("xk,yk", list(itertools.product(KINDS, KINDS)))
+def test_types(xk, yk):
+    Case(*RAGGED, 16, 2560, 512, xk, yk).check()
+    Case([1], [2], 16, 2560, 2560, xk, yk).check()
+
+
+@pytest.mark.parametrize("rank", [8, 16, 24, 32, 40, 56, 64, 72, 96, 120, 128])
+def test_ranks(rank):
+    Case(*RAGGED, rank, 320, 264).check()
+    Case(*RAGGED, rank, 1000, 96, qre.BF16, qre.BF16).check()
+    Case([300], [1], rank, 640, 640, qre.BF16, qre.F32).check()
+
+
+@pytest.mark.parametrize("d_in,d_out", [(8, 8), (8, 2560), (2560, 8), (24, 40), (248, 256), (264, 1032), (2552, 520), (5120, 24),
+                                        (16384, 16), (16, 16384)])
+def test_widths(d_in, d_out):
+    Case(*RAGGED, 16, d_in, d_out).check()
+    Case([70], [0], 32, d_in, d_out, qre.F16, qre.BF16).check()
+
+
+@pytest.mark.parametrize("lens,of", [
+    ([1], [0]), ([1], [-1]), ([1, 1, 1], [2, 2, 0]), ([16], [1]), ([15, 1], [1, 1]), ([31, 32, 33], [0, 1, 2]), ([64], [4]),
+    ([127, 128, 129], [4, 3, 2]), ([1] * 64, [i % 5 for i in range(64)]), ([0] * 300 + [3] + [0] * 300, [0] * 300 + [1] + [-1] * 300),
+    ([2048], [3]), ([700, 1, 900, 0, 447], [0, -1, 1, 2, 3]), ([1] * 1000, [(i * 7) % 6 - 1 for i in range(1000)])])
+def test_segments(lens, of):
+    Case(lens, of, 16, 264, 136).check()
+    Case(lens, of, 48, 136, 264, qre.BF16, qre.BF16, before=3, after=2).check()
+
+
+def test_largest_call():
+    lens = np.full(32, 256)
+    lens[::2] += 101
+    lens[1::2] -= 101
+    Case(lens, np.arange(32) % 5, 64, 2560, 2560, qre.BF16, qre.BF16).check()
+    Case([8192], [1], 8, 64, 64).check()
+    Case([1] * 8192, [i % 5 for i in range(8192)], 8, 64, 64).check()
+
+
+def test_in_place_no_base_no_scale_strides():
+    for kind in KINDS:
+        Case(*RAGGED, 16, 264, 136, kind, kind, inplace=True, pad=8, before=4, after=9).check()
+        Case(*RAGGED, 16, 264, 136, kind, kind, base=False, pad=16, wpad=8).check()
+        Case(*RAGGED, 24, 136, 264, kind, kind, scale=False, pad=8, wpad=16, after=1).check()
+
+
+def test_no_term_of_an_operand_is_lost():
+    """Whole numbers whose sums all fit 24 bits: the result is exact, so a dropped low term of x or of A x shows."""
+    T, d_in, d_out, rank = 40, 96, 72, 16
+    g = torch.Generator().manual_seed(3)
+    x = torch.zeros(T, d_in)
+    x[torch.arange(T), torch.randint(0, d_in, (T,), generator=g)] = (torch.randint(0, 1 << 22, (T,), generator=g) * 2 + 1).float()
+    a = torch.randint(-1, 2, (1, rank, d_in), generator=g).bfloat16()
+    b = torch.zeros(1, d_out, rank)
+    b[0, torch.arange(d_out), torch.randint(0, rank, (d_out,), generator=g)] = 1.0
+    b = b.bfloat16()
+    want = x.double() @ a[0].double().t() @ b[0].double().t()
+    assert want.abs().max() < 1 << 24 and (want != 0).any()
+    y = torch.empty(T, d_out, device=DEV)
+    xd, ad, bd = x.to(DEV), a.to(DEV), b.to(DEV)
+    off, of = torch.tensor([0, T], dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = workspace(T)
+    qre.strata_moe_adapters(qre.adapters(ad, bd, 1, rank, d_in, d_out), off, of, 1, xd, T, None, y, ws)
+    assert torch.equal(y.cpu().double(), want)
+    # fp16 activations: 11 bits, two terms
+    x16 = (x % 2047).half()
+    want = x16.double() @ a[0].double().t() @ b[0].double().t()
+    qre.strata_moe_adapters(qre.adapters(ad, bd, 1, rank, d_in, d_out, x_type=qre.F16), off, of, 1, x16.to(DEV), T, None, y, ws)
+    assert torch.equal(y.cpu().double(), want)
+
+
+@pytest.mark.parametrize("off,of", [([0, 5, 3, 8], [0, 1, 2]), ([0, 5, 9, 21], [0, 1, 2]), ([-1, 5, 9, 12], [0, 1, 2]),
+                                    ([0, 5, 9, 12], [0, 5, 2]), ([0, 5, 9, 12], [0, 1, -2])])
+def test_bad_segments_set_the_status_and_compute_nothing(off, of):
+    c = Case([20], [0], 16, 64, 64)
+    c.dev_off, c.dev_of = torch.tensor(off, dtype=torch.int32, device=DEV), torch.tensor(of, dtype=torch.int32, device=DEV)
+    c.of = np.asarray(of)
+    y = c.y.clone()
+    c.call()
+    assert qre.STATUS[qre.strata_poll_status(c.ws)] == "STRATA_E_CORRUPT"
+    assert torch.equal(c.y, y)
+    qre.strata_clear_status(c.ws)
+    c.dev_off, c.dev_of = torch.tensor([0, 20], dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    c.of = np.zeros(1, np.int32)
+    c.check()
+
+
+def test_repeats_streams_and_graphs():
+    c = Case([40, 1, 0, 90], [0, 1, 2, 3], 16, 264, 136, before=2, after=1)
+    c.check()
+    first = c.y.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    c.y.zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        c.call()
+    side.synchronize()
+    assert torch.equal(c.y[2:-1], first[2:-1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.call()
+        c.call()
+    c.x.copy_(rnd(*c.x.shape, seed=77))
+    c.y.copy_(first)
+    graph.replay()
+    torch.cuda.synchronize()
+    replayed = c.y.clone()
+    c.y.copy_(first)
+    c.check()
+    assert torch.equal(replayed, c.y)

@@ -1,0 +1,200 @@
+"""strata_moe_norm and strata_moe_combine_norm against their formulas in 64 bits."""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+import ops_reference as ref
+import quantized_routed_expert_top10_gb300 as qre
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+KINDS = (qre.F32, qre.BF16, qre.F16)
+
+
+def rnd(*shape, seed=0, std=1.0, mean=0.0, kind=qre.F32):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * std + mean).to(ref.TORCH[kind]).to(DEV)
+
+
+def padded(T, n, stride, kind, seed=0, offset=0, std=1.0):
+    """A [T][n] view of rows `stride` elements apart that starts `offset` elements into its buffer, and the buffer."""
+    buf = rnd(T * stride + offset, seed=seed, kind=kind, std=std)
+    return buf[offset:offset + T * stride].view(T, stride)[:, :n], buf
+
+
+def run_norm(T, n, xk, ok, gain=True, pad=0, offset=0, eps=1e-6, inplace=False, x=None):
+    stride = n + pad
+    xv, _ = padded(T, n, stride, xk, seed=n, offset=offset)
+    if x is not None:
+        xv.copy_(x)
+    before = ref.to64(xv)
+    ov, obuf = (xv, None) if inplace else padded(T, n, stride, ok, seed=99, offset=offset)
+    keep = None if obuf is None else obuf.clone()
+    gv = rnd(n, seed=3, std=0.2, mean=1.0) if gain else None
+    d = qre.norm(n, eps, xk, ok, stride, stride)
+    qre.strata_moe_norm(d, xv.data_ptr(), T, gv, ov.data_ptr())
+    torch.cuda.synchronize()
+    want, err = ref.rms_norm(before, np.zeros_like(before), eps, None if gv is None else ref.to64(gv))
+    ref.check(ov, want, err, ok, "norm")
+    if obuf is not None and obuf.numel() > T * n:  # nothing beside the rows was written
+        inside = torch.zeros_like(obuf, dtype=torch.bool)
+        inside[offset:offset + T * stride].view(T, stride)[:, :n] = True
+        assert torch.equal(obuf[~inside], keep[~inside])
+
+
+@pytest.mark.parametrize("xk,ok", list(itertools.product(KINDS, KINDS)))
+def test_norm_types(xk, ok):
+    run_norm(5, 2560, xk, ok)
+
+
+@pytest.mark.parametrize("n", [1, 2, 7, 8, 31, 64, 256, 264, 1000, 1001, 2560, 4096, 4104, 5120, 8192, 8200, 16376, 16383, 16384])
+def test_norm_widths(n):
+    for T in (1, 9):
+        run_norm(T, n, qre.F32, qre.F32)
+    run_norm(3, n, qre.BF16, qre.BF16, gain=False)
+
+
+@pytest.mark.parametrize("T", [1, 4, 151, 304, 1000, 8192])
+def test_norm_lengths(T):
+    run_norm(T, 2560, qre.F32, qre.BF16)
+    run_norm(T, 96, qre.F16, qre.F32)
+
+
+def test_norm_strides_alignment_and_in_place():
+    for n, pad, off in ((2560, 8, 0), (2560, 5, 0), (2560, 0, 1), (2560, 8, 3), (777, 0, 0), (64, 3, 5), (200, 8, 8)):
+        for kind in KINDS:
+            run_norm(7, n, kind, kind, pad=pad, offset=off)
+            run_norm(7, n, kind, kind, pad=pad, offset=off, inplace=True)
+
+
+def test_norm_rows_of_zeros_and_large_values():
+    x = torch.zeros(4, 2560)
+    x[1] = 1e-12
+    x[2] = 1e15
+    x[3, 7] = -3.0
+    run_norm(4, 2560, qre.F32, qre.F32, x=x.to(DEV))
+    run_norm(4, 2560, qre.F32, qre.F32, x=x.to(DEV), eps=1e-2)
+
+
+def run_edge(T, n, P, pk=qre.F32, xk=qre.F32, nk=qre.F32, post=True, gain=True, channel=True, token="sigmoid", weights=True,
+             x=True, out=True, nxt=True, pre=True, residual=0.9, block=0.5, pad=0, offset=0, inplace=None, zero_weight=False,
+             eps=1e-6):
+    ps = n + pad
+    ts = P * ps + pad
+    pbuf = rnd(T * ts + offset, seed=P + n, kind=pk)
+    parts = torch.as_strided(pbuf, (T, P, n), (ts, ps, 1), offset)
+    pw = torch.softmax(rnd(T, P, seed=2), 1) if weights else None
+    if zero_weight:  # what a part of weight 0 holds does not matter
+        pw[:, 0] = 0.0
+        parts[:, 0] = float("nan")
+        pw[0] = 0.0
+        parts[0] = float("inf")
+    xs = n + pad
+    xv = padded(T, n, xs, xk, seed=4, offset=offset)[0] if x else None
+    x64 = ref.to64(xv) if x else None
+    ov = None if not out else xv if inplace == "out" else padded(T, n, xs, xk, seed=5, offset=offset)[0]
+    nv = None if not nxt else xv if inplace == "next" else padded(T, n, xs, nk, seed=6, offset=offset)[0]
+    post_gain = rnd(n, seed=7, std=0.1, mean=1.0) if post and gain else None
+    ch = rnd(n, seed=8, std=0.3, mean=0.7) if channel else None
+    tk = rnd(T, seed=9, std=2.0) if token else None
+    pre_gain = rnd(n, seed=10, std=0.1, mean=1.0) if pre and nxt else None
+    d = qre.combine_norm(n, P, post, token == "sigmoid", eps, residual, block, pk, xk, nk, ps, ts, xs, xs, xs)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    qre.strata_moe_combine_norm(d, parts.data_ptr(), pw, ptr(xv), T, post_gain, ch, tk, pre_gain, ptr(ov), ptr(nv))
+    torch.cuda.synchronize()
+    h = lambda t: None if t is None else ref.to64(t)  # noqa: E731
+    r, r_err, nx, nx_err = ref.edge(h(parts), h(pw), x64, post, h(post_gain), h(ch), h(tk), token == "sigmoid", h(pre_gain),
+                                    eps, residual, block)
+    if out:
+        ref.check(ov, r, r_err, xk, "out")
+    if nxt:
+        ref.check(nv, nx, nx_err, nk, "next")
+
+
+@pytest.mark.parametrize("pk,xk,nk", list(itertools.product(KINDS, KINDS, KINDS)))
+def test_edge_types(pk, xk, nk):
+    run_edge(3, 2560, 10, pk, xk, nk)
+
+
+@pytest.mark.parametrize("n", [1, 7, 8, 64, 256, 264, 1000, 1001, 2560, 4104, 8200, 16383, 16384])
+@pytest.mark.parametrize("P", [1, 3, 10])
+def test_edge_widths(n, P):
+    run_edge(2, n, P)
+    run_edge(9, n, P, xk=qre.BF16, nk=qre.BF16)
+
+
+@pytest.mark.parametrize("P", [1, 2, 4, 5, 9, 11, 16, 31, 32])
+def test_edge_part_counts(P):
+    run_edge(3, 2560, P, zero_weight=True)
+    run_edge(3, 640, P, weights=False)
+
+
+@pytest.mark.parametrize("T", [1, 2, 16, 151, 305, 2048])
+def test_edge_lengths(T):
+    run_edge(T, 2560, 10)
+
+
+def test_edge_largest_call():
+    run_edge(8192, 2560, 1, xk=qre.BF16, nk=qre.BF16)
+
+
+def test_edge_options():
+    for post, gain, channel, token, weights, x in itertools.product((0, 1), (0, 1), (0, 1), (None, "raw", "sigmoid"), (0, 1), (0, 1)):
+        run_edge(2, 320, 3, post=bool(post), gain=bool(gain), channel=bool(channel), token=token, weights=bool(weights), x=bool(x))
+    run_edge(4, 2560, 10, out=False)
+    run_edge(4, 2560, 10, nxt=False)
+    run_edge(4, 2560, 10, pre=False)
+    run_edge(4, 2560, 10, residual=0.0, block=-2.0, eps=0.0)
+
+
+def test_edge_strides_alignment_and_in_place():
+    for n, pad, off in ((2560, 8, 0), (2560, 5, 0), (2560, 0, 1), (777, 0, 0), (64, 3, 5), (200, 8, 8)):
+        for kind in KINDS:
+            run_edge(5, n, 4, kind, kind, kind, pad=pad, offset=off)
+            run_edge(5, n, 4, kind, kind, kind, pad=pad, offset=off, inplace="out")
+            run_edge(5, n, 4, kind, kind, kind, pad=pad, offset=off, inplace="next")
+
+
+def test_edge_all_parts_masked_gives_the_residual():
+    n = 2560
+    x = rnd(2, n, seed=1)
+    out = torch.empty_like(x)
+    parts = torch.full((2, 10, n), float("nan"), device=DEV)
+    qre.strata_moe_combine_norm(qre.combine_norm(n, 10), parts, torch.zeros(2, 10, device=DEV), x, 2, None, None, None, None,
+                                out, None)
+    torch.cuda.synchronize()
+    assert torch.equal(out, x)
+
+
+def test_repeats_streams_and_graphs():
+    T, n = 37, 2560
+    parts, pw, x = rnd(T, 10, n, seed=1), torch.softmax(rnd(T, 10, seed=2), 1), rnd(T, n, seed=3)
+    out, nxt = torch.empty_like(x), torch.empty_like(x)
+    d = qre.combine_norm(n, 10)
+
+    def call():
+        qre.strata_moe_combine_norm(d, parts, pw, x, T, None, None, None, None, out, nxt)
+
+    call()
+    torch.cuda.synchronize()
+    first = out.clone(), nxt.clone()
+    out.zero_(), nxt.zero_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    side.synchronize()
+    assert torch.equal(out, first[0]) and torch.equal(nxt, first[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+        qre.strata_moe_norm(qre.norm(n), out, T, None, nxt)  # in the graph, the norm reads what the call before it wrote
+    x.copy_(rnd(T, n, seed=11))
+    graph.replay()
+    torch.cuda.synchronize()
+    call()
+    torch.cuda.synchronize()
+    want, err = ref.rms_norm(ref.to64(out), np.zeros((T, n)), 1e-6, None)
+    ref.check(nxt, want, err, qre.F32, "next")
