@@ -23,7 +23,11 @@ struct SelectArgs {
   float* weights;
   int T, E, k, softmax, G, keep, group_sum, renorm, type;
   float scale;
+  int size, magic;  // experts of a group, ceil(2^20 / size)
 };
+
+// Group of expert e: e / size, exact for e < 512 (e magic / 2^20 is above it by less than e / 2^20 < 1 / 512).
+__device__ __forceinline__ int group_of(const SelectArgs& a, int e) { return (int)((unsigned)e * (unsigned)a.magic >> 20); }
 
 __device__ __forceinline__ double shfl_xor_d(double v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
 __device__ __forceinline__ double warp_sum_d(double v) {
@@ -37,39 +41,36 @@ __device__ __forceinline__ double score_d(float l, bool softmax, float m, double
   return softmax ? exp((double)l - (double)m) / z : 1.0 / (1.0 + exp(-(double)l));
 }
 
-// One token by one warp, every value in 64 bits.  l[j]: logit of expert lane + 32 j (+inf made finite); bit j of
-// `usable`: the expert exists and is not masked.  val: shared [EMAX] doubles of this warp.  Lane i (< k) returns
-// the id of rank i and its score.
-__device__ void select_exact(const SelectArgs& a, const float (&l)[PER], uint32_t usable, double* val, int* out_id,
-                             double* out_p) {
+// Softmax sum in 64 bits over the warp's usable experts.
+__device__ __noinline__ double softmax_sum_d(const float* l, uint32_t usable, float m) {
   const int lane = threadIdx.x & 31;
-  float m = -FLT_MAX;
-#pragma unroll
+  double z = 0.0;
+#pragma unroll 4
   for (int j = 0; j < PER; ++j)
-    if (usable >> j & 1) m = fmaxf(m, l[j]);
-  m = warp_max(m);
-  double z = 1.0;
-  if (a.softmax) {
-    z = 0.0;
-#pragma unroll 1
-    for (int j = 0; j < PER; ++j)
-      if (usable >> j & 1) z += exp((double)l[j] - (double)m);
-    z = warp_sum_d(z);
-  }
+    if (usable >> j & 1) z += exp((double)l[lane + 32 * j] - (double)m);
+  return warp_sum_d(z);
+}
+
+// Token t by one warp, every value in 64 bits.  l: its logits in shared memory (+inf made finite), m the largest usable
+// one; bit j of `usable`: expert lane + 32 j exists and is not masked.  val: shared [EMAX] doubles of this warp.
+__device__ __noinline__ void select_exact(const SelectArgs& a, int t, const float* l, float m, uint32_t usable,
+                                          double* val) {
+  const int lane = threadIdx.x & 31;
+  const double z = a.softmax ? softmax_sum_d(l, usable, m) : 1.0;
   uint32_t here = 0;  // bit j: the expert exists and its group is kept
-#pragma unroll
+#pragma unroll 1
   for (int j = 0; j < PER; ++j) {
     const int e = lane + 32 * j;
     if (e < a.E) {
       here |= 1u << j;
       double v = -INFINITY;
-      if (usable >> j & 1) v = score_d(l[j], a.softmax, m, z) + (a.bias ? (double)__ldg(a.bias + e) : 0.0);
+      if (usable >> j & 1) v = score_d(l[e], a.softmax, m, z) + (a.bias ? (double)__ldg(a.bias + e) : 0.0);
       val[e] = v;
     }
   }
   __syncwarp();
   if (a.G > 1) {
-    const int size = a.E / a.G;
+    const int size = a.size;
     double b0 = -INFINITY, b1 = -INFINITY;
     if (lane < a.G)
       for (int i = 0; i < size; ++i) {
@@ -91,14 +92,14 @@ __device__ void select_exact(const SelectArgs& a, const float (&l)[PER], uint32_
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int e = lane + 32 * j;
-      if (e < a.E && !(kept >> (e / size) & 1)) here &= ~(1u << j);
+      if (e < a.E && !(kept >> group_of(a, e) & 1)) here &= ~(1u << j);
     }
   }
   // k rounds: the warp's largest (key, then lower id) among the experts that remain
   double key[PER];
 #pragma unroll
   for (int j = 0; j < PER; ++j)
-    key[j] = !(here >> j & 1) ? -INFINITY : a.bias ? val[lane + 32 * j] : (usable >> j & 1) ? (double)l[j] : -INFINITY;
+    key[j] = !(here >> j & 1) ? -INFINITY : a.bias ? val[lane + 32 * j] : (usable >> j & 1) ? (double)l[lane + 32 * j] : -INFINITY;
   int mine = 0;
   double mine_p = 0.0;
 #pragma unroll 1
@@ -122,11 +123,8 @@ __device__ void select_exact(const SelectArgs& a, const float (&l)[PER], uint32_
     }
     double p = 0.0;
     if ((be & 31) == lane) {
-      const int jw = be >> 5;
-      here &= ~(1u << jw);
-#pragma unroll
-      for (int j = 0; j < PER; ++j)
-        if (j == jw && (usable >> j & 1)) p = score_d(l[j], a.softmax, m, z);
+      here &= ~(1u << (be >> 5));
+      if (usable >> (be >> 5) & 1) p = score_d(l[be], a.softmax, m, z);
     }
     p = __shfl_sync(0xffffffffu, p, be & 31);
     if (lane == i) {
@@ -134,35 +132,340 @@ __device__ void select_exact(const SelectArgs& a, const float (&l)[PER], uint32_
       mine_p = p;
     }
   }
-  *out_id = mine;
-  *out_p = mine_p;
+  const double sum = warp_sum_d(lane < a.k ? mine_p : 0.0);
+  if (lane < a.k) {
+    a.ids[(int64_t)t * a.k + lane] = mine;
+    a.weights[(int64_t)t * a.k + lane] =
+        (float)((a.renorm ? mine_p / fmax(sum, (double)SUM_MIN) : mine_p) * (double)a.scale);
+  }
 }
 
-__global__ void __launch_bounds__(32 * SEL_WARPS) select_kernel(SelectArgs a) {
-  __shared__ double s_val[SEL_WARPS][EMAX];
+// Rounding of a value of the fp32 pass, in units of u = 2^-24.  A softmax score: the exponential of l - m (its argument
+// rounded: (m - l) u, and (m - l) p <= 0.37 of the largest score; the function 2 u), the sum (the terms' 2 u, 16 + 5
+// additions), its reciprocal and a product: below 34 u of the largest score.  A sigmoid: the exponential 2 u, the sum
+// u, the quotient 4 u.  Adding the bias rounds once more.  (An exponential that leaves the fp32 range: 1e-37.)
+constexpr float U32 = 5.9604645e-8f;
+constexpr float ERR_SOFTMAX = 34.f, ERR_SIGMOID = 8.f;
+
+// A value's place in the choice as an unsigned number: larger values larger numbers (-0 as +0), a masked expert 1, one that
+// does not exist or whose group is dropped 0.
+__device__ __forceinline__ uint32_t value_key(float v) { return logit_key(v + 0.f); }
+
+constexpr int CAND = 64;
+struct SelectScratch {  // one per warp; the padded values (groups) or 64-bit values follow
+  float l[EMAX];
+  uint2 cand[CAND];     // key, id
+  uint2 sel[STRATA_SELECT_K_MAX + 1];
+};
+// Distance of two groups' values in shared memory: lane / L is the group and the L lanes of a group read
+// neighbouring values, so a distance of L modulo 32 puts the warp's 32 reads into 32 banks.
+__host__ __device__ inline int group_lanes(int G) { return G > 16 ? 1 : G > 8 ? 2 : G > 4 ? 4 : G > 2 ? 8 : G > 1 ? 16 : 32; }
+__host__ __device__ inline int group_pitch(int size, int G) { return size + ((group_lanes(G) - size) & 31); }
+inline size_t select_warp_bytes(int E, int G, bool values) {
+  if (!values) return sizeof(SelectScratch);
+  const size_t groups = G > 1 ? sizeof(float) * G * group_pitch(E / G, G) : 0, exact = sizeof(double) * EMAX;
+  return (sizeof(SelectScratch) + (groups > exact ? groups : exact) + 15) / 16 * 16;
+}
+static_assert(sizeof(SelectScratch) % 8 == 0, "64-bit values follow the scratch");
+
+// Groups kept, where the fp32 scores do not decide: the groups' scores in 64 bits, from the two largest values of each
+// (val: the values with a bias, the logits without).  Lane g < G scans group g.  *sure = false if a group's two largest
+// cannot be told from its third.  z: the softmax's sum (without a bias any positive number: the order is the same).
+__device__ __noinline__ uint32_t groups_exact(const SelectArgs& a, const float* l, const float* val, int size, int pitch,
+                                              float m, double z, float err, bool* sure) {
+  const int lane = threadIdx.x & 31;
+  float v0 = -INFINITY, v1 = -INFINITY, v2 = -INFINITY;
+  int e0 = 0, e1 = 0;
+  if (lane < a.G)
+    for (int i = 0; i < size; ++i) {
+      const float v = val[lane * pitch + i];
+      if (v > v0) {
+        v2 = v1; v1 = v0; e1 = e0;
+        v0 = v; e0 = lane * size + i;
+      } else if (v > v1) {
+        v2 = v1;
+        v1 = v; e1 = lane * size + i;
+      } else if (v > v2) {
+        v2 = v;
+      }
+    }
+  const float last = a.group_sum == 2 ? v1 : v0, behind = a.group_sum == 2 ? v2 : v1;
+  const bool clear = !a.bias || behind == -INFINITY ||
+                     last - behind > 2.f * (err + U32 * fmaxf(fabsf(last), fabsf(behind)));
+  *sure = __all_sync(0xffffffffu, clear);
+  double gs = -INFINITY;
+  if (v0 > -INFINITY) gs = score_d(l[e0], a.softmax, m, z) + (a.bias ? (double)__ldg(a.bias + e0) : 0.0);
+  if (a.group_sum == 2 && v1 > -INFINITY) gs += score_d(l[e1], a.softmax, m, z) + (a.bias ? (double)__ldg(a.bias + e1) : 0.0);
+  int rank = 0;
+  for (int g = 0; g < a.G; ++g) {
+    const double o = __shfl_sync(0xffffffffu, gs, g);
+    rank += (o > gs || (o == gs && g < lane)) ? 1 : 0;
+  }
+  return __ballot_sync(0xffffffffu, lane < a.G && rank < a.keep);
+}
+
+// One token per warp.  VALUES: the choice goes by scores (a bias, or groups); otherwise by the logits alone.
+//
+// The pass in fp32 knows how far its values may be off (err), and a choice that this could turn is made again in 64 bits:
+// of the candidates' values, or of the groups' two largest; only where even that is not enough (a mass of near ties) of
+// all.  64-bit arithmetic is slow on this GPU, and a token in about a thousand needs it.
+template <bool VALUES>
+__global__ void __launch_bounds__(32 * SEL_WARPS) select_kernel(const __grid_constant__ SelectArgs a,
+                                                                int warp_bytes) {
+  extern __shared__ __align__(16) char s_all[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * SEL_WARPS + warp;
   if (t >= a.T) return;
+  SelectScratch& sc = *reinterpret_cast<SelectScratch*>(s_all + warp * warp_bytes);
+  float* const val = reinterpret_cast<float*>(&sc + 1);
   const float lowest = lowest_of(a.type);
-  float l[PER];
-  uint32_t usable = 0;
+  float l[PER], b[PER];
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int e = lane + 32 * j;
-    const float v = e < a.E ? load1(a.logits, (int64_t)t * a.stride + e, a.type) : lowest;
-    const float b = a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
-    // a comparison with NaN is false: such an expert is masked
-    if (v > lowest && b > -INFINITY) usable |= 1u << j;
-    l[j] = fminf(v, FLT_MAX);
+    l[j] = e < a.E ? load1(a.logits, (int64_t)t * a.stride + e, a.type) : lowest;
+    b[j] = VALUES && a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
   }
-  int id;
-  double p;
-  select_exact(a, l, usable, s_val[warp], &id, &p);
-  const double sum = warp_sum_d(lane < a.k ? p : 0.0);
-  if (lane < a.k) {
-    a.ids[(int64_t)t * a.k + lane] = id;
-    a.weights[(int64_t)t * a.k + lane] =
-        (float)((a.renorm ? p / fmax(sum, (double)SUM_MIN) : p) * (double)a.scale);
+  uint32_t usable = 0;
+  float m = -FLT_MAX;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    // a comparison with NaN is false: such an expert is masked
+    if (l[j] > lowest && b[j] > -INFINITY) usable |= 1u << j;
+    l[j] = fminf(l[j], FLT_MAX);
+    if (usable >> j & 1) m = fmaxf(m, l[j]);
+    sc.l[lane + 32 * j] = l[j];
+  }
+  m = warp_max(m);
+
+  // values, and the experts' places: the value with a bias, the logit (the score's order) without
+  float inv_z = 1.f, err = 0.f;
+  uint32_t key[PER];
+  if constexpr (VALUES) {
+    float v[PER];
+    if (a.softmax) {
+      float z = 0.f;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        v[j] = usable >> j & 1 ? expf(l[j] - m) : 0.f;
+        z += v[j];
+      }
+      z = warp_sum(z);
+      inv_z = z > 0.f ? 1.f / z : 1.f;
+      err = U32 * ERR_SOFTMAX * inv_z + 1e-37f;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) v[j] = fmaf(v[j], inv_z, b[j]);
+    } else {
+      err = U32 * ERR_SIGMOID + 1e-37f;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) v[j] = __fdividef(1.f, 1.f + expf(-l[j])) + b[j];
+    }
+    uint32_t kept = 0xffffffffu;
+    const int size = a.size;
+    if (a.G > 1) {
+      // each group's two largest: of the values with a bias, of the logits without (the same experts, and
+      // equal scores are then known for what they are)
+      const int pitch = group_pitch(size, a.G), L = group_lanes(a.G);
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const int e = lane + 32 * j;
+        if (e < a.E) val[e + group_of(a, e) * (pitch - size)] = !(usable >> j & 1) ? -INFINITY : a.bias ? v[j] : l[j];
+      }
+      __syncwarp();
+      const int g = lane / L;
+      float k0 = -INFINITY, k1 = -INFINITY;
+      if (g < a.G)
+        for (int i = lane % L; i < size; i += L) {
+          const float w = val[g * pitch + i];
+          k1 = fmaxf(k1, fminf(k0, w));
+          k0 = fmaxf(k0, w);
+        }
+      for (int o = 1; o < L; o <<= 1) {
+        const float w0 = __shfl_xor_sync(0xffffffffu, k0, o), w1 = __shfl_xor_sync(0xffffffffu, k1, o);
+        k1 = fmaxf(fminf(k0, w0), fmaxf(k1, w1));
+        k0 = fmaxf(k0, w0);
+      }
+      float v0 = k0, v1 = k1;
+      if (!a.bias) {
+        v0 = k0 > -INFINITY ? (a.softmax ? expf(k0 - m) * inv_z : __fdividef(1.f, 1.f + expf(-k0))) : k0;
+        v1 = k1 > -INFINITY ? (a.softmax ? expf(k1 - m) * inv_z : __fdividef(1.f, 1.f + expf(-k1))) : k1;
+      }
+      const bool two = a.group_sum == 2 && v1 > -INFINITY;
+      const float gs = two ? v0 + v1 : v0;
+      // the scores' error, the largest of any group's: of two values and of their sum
+      const float ge = warp_max(gs > -INFINITY ? 2.f * err + U32 * (fabsf(v0) + (two ? fabsf(v1) : 0.f) + fabsf(gs)) : 0.f);
+      int rank = 0;
+#pragma unroll 4
+      for (int h = 0; h < a.G; ++h) {
+        const float o = __shfl_sync(0xffffffffu, gs, h * L);
+        rank += (o > gs || (o == gs && h < g)) ? 1 : 0;
+      }
+      const uint32_t in = __ballot_sync(0xffffffffu, g < a.G && rank < a.keep);
+      kept = 0;
+      bool unsure = false;  // this kept group and one that is dropped are too near, and not equal
+      const bool mine = in >> lane & 1u;
+      for (int h = 0; h < a.G; ++h) {
+        const float o = __shfl_sync(0xffffffffu, gs, h * L);
+        const float o0 = __shfl_sync(0xffffffffu, k0, h * L), o1 = __shfl_sync(0xffffffffu, k1, h * L);
+        const bool h_in = in >> (h * L) & 1u;
+        kept |= (h_in ? 1u : 0u) << h;
+        const bool same = !a.bias && o0 == k0 && (a.group_sum == 1 || o1 == k1);
+        if (mine && !h_in && o > -INFINITY && !same && !(gs - o > 2.f * ge)) unsure = true;
+      }
+      if (__any_sync(0xffffffffu, unsure)) {
+        const double z = a.softmax && a.bias ? softmax_sum_d(sc.l, usable, m) : 1.0;
+        bool sure;
+        kept = groups_exact(a, sc.l, val, size, pitch, m, z, err, &sure);
+        if (!sure) {
+          __syncwarp();
+          select_exact(a, t, sc.l, m, usable, reinterpret_cast<double*>(val));
+          return;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int e = lane + 32 * j;
+      const bool there = e < a.E && (a.G == 1 || (kept >> group_of(a, e) & 1u));
+      key[j] = !there ? 0u : !(usable >> j & 1) ? 1u : value_key(a.bias ? v[j] : l[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      key[j] = lane + 32 * j >= a.E ? 0u : !(usable >> j & 1) ? 1u : value_key(l[j]);
+  }
+
+  // candidates: every key not below the k-th largest of the lanes' largest (k lanes hold one at least), and
+  // with a bias not surely below it
+  uint32_t mk = key[0];
+#pragma unroll
+  for (int j = 1; j < PER; ++j) mk = max(mk, key[j]);
+  int r = 0;
+#pragma unroll
+  for (int o = 1; o < 32; ++o) {
+    const int src = (lane + o) & 31;
+    const uint32_t v = __shfl_sync(0xffffffffu, mk, src);
+    r += (v > mk || (v == mk && src < lane)) ? 1 : 0;
+  }
+  uint32_t tau = __shfl_sync(0xffffffffu, mk, __ffs(__ballot_sync(0xffffffffu, r == a.k - 1)) - 1);
+  if (VALUES && a.bias && tau > 1u) {
+    const float f = key_logit(tau);
+    if (f < INFINITY) tau = min(tau, value_key(f - 2.f * err - 4.f * U32 * fabsf(f)));
+  }
+  tau = max(tau, 1u);
+  const uint32_t below = (1u << lane) - 1u;
+  int C = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const bool is = key[j] >= tau;
+    const uint32_t bal = __ballot_sync(0xffffffffu, is);
+    const int pos = C + __popc(bal & below);
+    if (is && pos < CAND) sc.cand[pos] = make_uint2(key[j], (uint32_t)(lane + 32 * j));
+    C += __popc(bal);
+  }
+  __syncwarp();
+  if (C > CAND) {
+    if (VALUES && a.bias) {
+      __syncwarp();
+      select_exact(a, t, sc.l, m, usable, reinterpret_cast<double*>(val));
+      return;
+    }
+    // a mass of equal logits: k rounds of the warp's largest (key, then lower id)
+#pragma unroll 1
+    for (int i = 0; i < a.k; ++i) {
+      uint32_t bk = key[0];
+      int bj = 0;
+#pragma unroll
+      for (int j = 1; j < PER; ++j)
+        if (key[j] > bk) {
+          bk = key[j];
+          bj = j;
+        }
+      const uint32_t mx = __reduce_max_sync(0xffffffffu, bk);
+      const uint32_t id = __reduce_min_sync(0xffffffffu, bk == mx ? (uint32_t)(lane + 32 * bj) : 0xffffffffu);
+      if ((int)(id & 31u) == lane) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+          if (j == (int)(id >> 5)) key[j] = 0u;
+      }
+      if (lane == 0) sc.sel[i] = make_uint2(mx, id);
+    }
+  } else {
+    for (int i = lane; i < C; i += 32) {
+      const uint2 me = sc.cand[i];
+      int rank = 0;
+#pragma unroll 4
+      for (int q = 0; q < C; ++q) {
+        const uint2 o = sc.cand[q];
+        rank += (o.x > me.x || (o.x == me.x && o.y < me.y)) ? 1 : 0;
+      }
+      if (rank <= a.k) sc.sel[rank] = me;
+    }
+  }
+  __syncwarp();
+  if (VALUES && a.bias) {
+    // neighbours in the order whose values fp32 cannot tell apart (the same logit and bias: a true tie)
+    bool unsure = false;
+    if (lane < a.k && lane + 1 < C) {
+      const uint2 p = sc.sel[lane], q = sc.sel[lane + 1];
+      if (q.x > 1u) {
+        const float u = key_logit(p.x), v = key_logit(q.x);
+        unsure = !(u - v > 2.f * err + U32 * (fabsf(u) + fabsf(v))) &&
+                 !(sc.l[p.y] == sc.l[q.y] && __ldg(a.bias + p.y) == __ldg(a.bias + q.y));
+      }
+    }
+    if (__any_sync(0xffffffffu, unsure)) {
+      const double z = a.softmax ? softmax_sum_d(sc.l, usable, m) : 1.0;
+      double mine[CAND / 32];
+#pragma unroll
+      for (int h = 0; h < CAND / 32; ++h) {
+        mine[h] = -INFINITY;
+        if (lane + 32 * h < C) {
+          const uint2 c = sc.cand[lane + 32 * h];
+          if (c.x > 1u) mine[h] = score_d(sc.l[c.y], a.softmax, m, z) + (double)__ldg(a.bias + c.y);
+        }
+      }
+      int rank[CAND / 32] = {0, 0};
+      for (int q = 0; q < C; ++q) {
+        const double o = __shfl_sync(0xffffffffu, q < 32 ? mine[0] : mine[1], q & 31);
+        const uint32_t oe = sc.cand[q].y;
+#pragma unroll
+        for (int h = 0; h < CAND / 32; ++h)
+          if (lane + 32 * h < C) {
+            const uint32_t e = sc.cand[lane + 32 * h].y;
+            rank[h] += (o > mine[h] || (o == mine[h] && oe < e)) ? 1 : 0;
+          }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < CAND / 32; ++h)
+        if (lane + 32 * h < C && rank[h] < a.k) sc.sel[rank[h]] = sc.cand[lane + 32 * h];
+      __syncwarp();
+    }
+  }
+  // weights: without groups or a bias the k largest softmax scores sum to k / E at least, above the clamp, and the
+  // softmax's own sum divides out
+  const bool has = lane < a.k;
+  const uint2 me = sc.sel[has ? lane : 0];
+  float p = 0.f;
+  if (has && me.x > 1u) {
+    const float x = sc.l[me.y];
+    p = a.softmax ? expf(x - m) : 1.f / (1.f + expf(-x));
+  }
+  if (a.softmax && (VALUES || !a.renorm)) {
+    if constexpr (!VALUES) {
+      float z = 0.f;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) z += usable >> j & 1 ? expf(sc.l[lane + 32 * j] - m) : 0.f;
+      z = warp_sum(z);
+      inv_z = z > 0.f ? 1.f / z : 1.f;
+    }
+    p *= inv_z;
+  }
+  const float sum = warp_sum(p);
+  if (has) {
+    a.ids[(int64_t)t * a.k + lane] = (int)me.y;
+    a.weights[(int64_t)t * a.k + lane] = (a.renorm ? p / fmaxf(sum, SUM_MIN) : p) * a.scale;
   }
 }
 
@@ -172,9 +475,15 @@ cudaError_t launch_select(const strata_select_t& sel, const void* logits, int T,
                           float* weights, cudaStream_t s) {
   const SelectArgs a{logits, sel.logits_stride, bias, ids, weights, T, sel.n_expert, sel.top_k,
                      sel.score == STRATA_SCORE_SOFTMAX, sel.n_group, sel.top_group, sel.group_sum, sel.renorm,
-                     sel.logits_type, sel.scale};
-  STRATA_LAUNCH(KID_SELECT, s,
-                select_kernel<<<(T + SEL_WARPS - 1) / SEL_WARPS, 32 * SEL_WARPS, 0, s>>>(a));
+                     sel.logits_type, sel.scale, sel.n_expert / sel.n_group,
+                     ((1 << 20) + sel.n_expert / sel.n_group - 1) / (sel.n_expert / sel.n_group)};
+  const bool values = bias || sel.n_group > 1;
+  const int warp_bytes = (int)select_warp_bytes(sel.n_expert, sel.n_group, values);
+  const dim3 grid((T + SEL_WARPS - 1) / SEL_WARPS), block(32 * SEL_WARPS);
+  kernel_begin(KID_SELECT, s);
+  if (values) select_kernel<true><<<grid, block, SEL_WARPS * warp_bytes, s>>>(a, warp_bytes);
+  else select_kernel<false><<<grid, block, SEL_WARPS * warp_bytes, s>>>(a, warp_bytes);
+  kernel_end(KID_SELECT, s);
   return cudaGetLastError();
 }
 
