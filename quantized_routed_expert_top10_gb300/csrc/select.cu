@@ -12,7 +12,6 @@ namespace strata {
 namespace {
 
 constexpr int SEL_WARPS = 4;          // one token each
-constexpr int PER = EMAX / 32;        // experts of a lane: lane + 32 j
 constexpr float SUM_MIN = 1.f / 16384.f;  // lower clamp of the weights' sum (2^-14)
 
 struct SelectArgs {
@@ -46,7 +45,7 @@ __device__ __noinline__ double softmax_sum_d(const float* l, uint32_t usable, fl
   const int lane = threadIdx.x & 31;
   double z = 0.0;
 #pragma unroll 4
-  for (int j = 0; j < PER; ++j)
+  for (int j = 0; j < EMAX / 32; ++j)
     if (usable >> j & 1) z += exp((double)l[lane + 32 * j] - (double)m);
   return warp_sum_d(z);
 }
@@ -59,7 +58,7 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t, const floa
   const double z = a.softmax ? softmax_sum_d(l, usable, m) : 1.0;
   uint32_t here = 0;  // bit j: the expert exists and its group is kept
 #pragma unroll 1
-  for (int j = 0; j < PER; ++j) {
+  for (int j = 0; j < EMAX / 32; ++j) {
     const int e = lane + 32 * j;
     if (e < a.E) {
       here |= 1u << j;
@@ -90,15 +89,15 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t, const floa
     }
     const uint32_t kept = __ballot_sync(0xffffffffu, lane < a.G && rank < a.keep);
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
+    for (int j = 0; j < EMAX / 32; ++j) {
       const int e = lane + 32 * j;
       if (e < a.E && !(kept >> group_of(a, e) & 1)) here &= ~(1u << j);
     }
   }
   // k rounds: the warp's largest (key, then lower id) among the experts that remain
-  double key[PER];
+  double key[EMAX / 32];
 #pragma unroll
-  for (int j = 0; j < PER; ++j)
+  for (int j = 0; j < EMAX / 32; ++j)
     key[j] = !(here >> j & 1) ? -INFINITY : a.bias ? val[lane + 32 * j] : (usable >> j & 1) ? (double)l[lane + 32 * j] : -INFINITY;
   int mine = 0;
   double mine_p = 0.0;
@@ -107,7 +106,7 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t, const floa
     double bk = -INFINITY;
     int be = EMAX;  // no expert
 #pragma unroll
-    for (int j = 0; j < PER; ++j)
+    for (int j = 0; j < EMAX / 32; ++j)
       if ((here >> j & 1) && (be == EMAX || key[j] > bk)) {
         bk = key[j];
         be = lane + 32 * j;
@@ -140,12 +139,14 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t, const floa
   }
 }
 
-// Rounding of a value of the fp32 pass, in units of u = 2^-24.  A softmax score: the exponential of l - m (its argument
-// rounded: (m - l) u, and (m - l) p <= 0.37 of the largest score; the function 2 u), the sum (the terms' 2 u, 16 + 5
-// additions), its reciprocal and a product: below 34 u of the largest score.  A sigmoid: the exponential 2 u, the sum
-// u, the quotient 4 u.  Adding the bias rounds once more.  (An exponential that leaves the fp32 range: 1e-37.)
+// Rounding of a value of the fp32 pass, in units of u = 2^-24; exponentials are ex2(x log2 e) (the argument's two
+// roundings 1.5 |x| u, the function 4 u).  A softmax score p = exp(-d) / z, d = m - l: (2.5 d + 4) u of it with d's own
+// rounding, where d p <= 0.37 of the largest score; z: the same of each term, where the mean of d over the scores is at
+// most ln 512 = 6.2, and 16 + 5 additions, 41 u; a quotient and a product 3 u: below 52 u of the largest score.  A
+// sigmoid p = 1 / (1 + e): p (1 - p) (1.5 |l| + 4) u <= 1.4 u, the sum u, the quotient 4 u: below 8 u.  Adding the
+// bias rounds once more.  (An exponential that leaves the fp32 range: 1e-37.)
 constexpr float U32 = 5.9604645e-8f;
-constexpr float ERR_SOFTMAX = 34.f, ERR_SIGMOID = 8.f;
+constexpr float ERR_SOFTMAX = 52.f, ERR_SIGMOID = 8.f;
 
 // A value's place in the choice as an unsigned number: larger values larger numbers (-0 as +0), a masked expert 1, one that
 // does not exist or whose group is dropped 0.
@@ -204,269 +205,312 @@ __device__ __noinline__ uint32_t groups_exact(const SelectArgs& a, const float* 
   return __ballot_sync(0xffffffffu, lane < a.G && rank < a.keep);
 }
 
-// One token per warp.  VALUES: the choice goes by scores (a bias, or groups); otherwise by the logits alone.
+__device__ __forceinline__ uint32_t key_of_min(float v) { return __reduce_min_sync(0xffffffffu, value_key(v)); }
+__device__ __forceinline__ uint32_t key_of_max(float v) { return __reduce_max_sync(0xffffffffu, value_key(v)); }
+
+// One token per warp and turn.  VALUES: the choice goes by scores (a bias, or groups); otherwise by the logits alone.
+// PER: experts of a lane (lane + 32 j), E <= 32 PER.
 //
 // The pass in fp32 knows how far its values may be off (err), and a choice that this could turn is made again in 64 bits:
 // of the candidates' values, or of the groups' two largest; only where even that is not enough (a mass of near ties) of
 // all.  64-bit arithmetic is slow on this GPU, and a token in about a thousand needs it.
-template <bool VALUES>
-__global__ void __launch_bounds__(32 * SEL_WARPS) select_kernel(const __grid_constant__ SelectArgs a,
-                                                                int warp_bytes) {
+template <bool VALUES, int PER>
+__global__ void __launch_bounds__(32 * SEL_WARPS, 5) select_kernel(const __grid_constant__ SelectArgs a, int warp_bytes) {
   extern __shared__ __align__(16) char s_all[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x * SEL_WARPS + warp;
-  if (t >= a.T) return;
   SelectScratch& sc = *reinterpret_cast<SelectScratch*>(s_all + warp * warp_bytes);
   float* const val = reinterpret_cast<float*>(&sc + 1);
   const float lowest = lowest_of(a.type);
-  float l[PER], b[PER];
+  const uint32_t below = (1u << lane) - 1u;
+  const int size = a.size, pitch = VALUES ? group_pitch(size, a.G) : 0, L = VALUES ? group_lanes(a.G) : 32;
+  float b[PER];
+  uint32_t open = 0;  // bit j: the expert exists and its bias does not mask it
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int e = lane + 32 * j;
-    l[j] = e < a.E ? load1(a.logits, (int64_t)t * a.stride + e, a.type) : lowest;
     b[j] = VALUES && a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
+    if (e < a.E && b[j] > -INFINITY) open |= 1u << j;
   }
-  uint32_t usable = 0;
-  float m = -FLT_MAX;
+  for (int t = blockIdx.x * SEL_WARPS + warp; t < a.T; t += gridDim.x * SEL_WARPS) {
+    float l[PER];
+    const int64_t row = (int64_t)t * a.stride + lane;
+    if (a.type == STRATA_F32) {
 #pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    // a comparison with NaN is false: such an expert is masked
-    if (l[j] > lowest && b[j] > -INFINITY) usable |= 1u << j;
-    l[j] = fminf(l[j], FLT_MAX);
-    if (usable >> j & 1) m = fmaxf(m, l[j]);
-    sc.l[lane + 32 * j] = l[j];
-  }
-  m = warp_max(m);
-
-  // values, and the experts' places: the value with a bias, the logit (the score's order) without
-  float inv_z = 1.f, err = 0.f;
-  uint32_t key[PER];
-  if constexpr (VALUES) {
-    float v[PER];
-    if (a.softmax) {
-      float z = 0.f;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        v[j] = usable >> j & 1 ? expf(l[j] - m) : 0.f;
-        z += v[j];
-      }
-      z = warp_sum(z);
-      inv_z = z > 0.f ? 1.f / z : 1.f;
-      err = U32 * ERR_SOFTMAX * inv_z + 1e-37f;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) v[j] = fmaf(v[j], inv_z, b[j]);
+      for (int j = 0; j < PER; ++j) l[j] = lane + 32 * j < a.E ? __ldg(static_cast<const float*>(a.logits) + row + 32 * j) : lowest;
     } else {
-      err = U32 * ERR_SIGMOID + 1e-37f;
+      uint16_t raw[PER];
 #pragma unroll
-      for (int j = 0; j < PER; ++j) v[j] = __fdividef(1.f, 1.f + expf(-l[j])) + b[j];
+      for (int j = 0; j < PER; ++j)
+        raw[j] = lane + 32 * j < a.E ? __ldg(static_cast<const uint16_t*>(a.logits) + row + 32 * j) : (uint16_t)0;
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        l[j] = a.type == STRATA_BF16 ? __uint_as_float((uint32_t)raw[j] << 16) : __half2float(__ushort_as_half(raw[j]));
     }
-    uint32_t kept = 0xffffffffu;
-    const int size = a.size;
-    if (a.G > 1) {
-      // each group's two largest: of the values with a bias, of the logits without (the same experts, and
-      // equal scores are then known for what they are)
-      const int pitch = group_pitch(size, a.G), L = group_lanes(a.G);
+    uint32_t usable = 0;
+    float m = -FLT_MAX;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      // a comparison with NaN is false: such an expert is masked
+      const bool ok = l[j] > lowest && (open >> j & 1);
+      if (ok) usable |= 1u << j;
+      l[j] = fminf(l[j], FLT_MAX);
+      if (ok) m = fmaxf(m, l[j]);
+      sc.l[lane + 32 * j] = l[j];
+    }
+    m = warp_max(m);
+
+    // values, and the experts' places: the value with a bias, the logit (the score's order) without
+    float inv_z = 1.f, err = 0.f;
+    uint32_t key[PER];
+    if constexpr (VALUES) {
+      float v[PER];
+      if (a.softmax) {
+        float z = 0.f;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+          v[j] = usable >> j & 1 ? __expf(l[j] - m) : 0.f;
+          z += v[j];
+        }
+        z = warp_sum(z);
+        inv_z = z > 0.f ? 1.f / z : 1.f;
+        err = U32 * ERR_SOFTMAX * inv_z + 1e-37f;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) v[j] = fmaf(v[j], inv_z, b[j]);
+      } else {
+        err = U32 * ERR_SIGMOID + 1e-37f;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) v[j] = __fdividef(1.f, 1.f + __expf(-l[j])) + b[j];
+      }
+      uint32_t in = 0xffffffffu;  // bit of a group's first lane: the group is kept
+      if (a.G > 1) {
+        // each group's two largest: of the values with a bias, of the logits without (the same experts, and
+        // equal scores are then known for what they are)
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+          const int e = lane + 32 * j;
+          if (e < a.E) val[e + group_of(a, e) * (pitch - size)] = !(usable >> j & 1) ? -INFINITY : a.bias ? v[j] : l[j];
+        }
+        __syncwarp();
+        const int g = lane / L;
+        float k0 = -INFINITY, k1 = -INFINITY;
+        if (g < a.G) {
+          const float* at = val + g * pitch;
+#pragma unroll 8
+          for (int i = lane % L; i < size; i += L) {
+            const float w = at[i];
+            k1 = fmaxf(k1, fminf(k0, w));
+            k0 = fmaxf(k0, w);
+          }
+        }
+        for (int o = 1; o < L; o <<= 1) {
+          const float w0 = __shfl_xor_sync(0xffffffffu, k0, o), w1 = __shfl_xor_sync(0xffffffffu, k1, o);
+          k1 = fmaxf(fminf(k0, w0), fmaxf(k1, w1));
+          k0 = fmaxf(k0, w0);
+        }
+        float v0 = k0, v1 = k1;
+        if (!a.bias) {
+          v0 = k0 > -INFINITY ? (a.softmax ? __expf(k0 - m) * inv_z : __fdividef(1.f, 1.f + __expf(-k0))) : k0;
+          v1 = k1 > -INFINITY ? (a.softmax ? __expf(k1 - m) * inv_z : __fdividef(1.f, 1.f + __expf(-k1))) : k1;
+        }
+        const bool two = a.group_sum == 2 && v1 > -INFINITY;
+        const float gs = two ? v0 + v1 : v0;
+        int rank = 0;
+#pragma unroll 4
+        for (int h = 0; h < a.G; ++h) {
+          const float o = __shfl_sync(0xffffffffu, gs, h * L);
+          rank += (o > gs || (o == gs && h < g)) ? 1 : 0;
+        }
+        const bool mine = g < a.G && rank < a.keep;
+        in = __ballot_sync(0xffffffffu, mine);
+        // the scores' error: of two values and of their sum, none of them larger than the largest score or value
+        const float big = key_logit(key_of_max(gs > -INFINITY ? fmaxf(fabsf(gs), fmaxf(fabsf(v0), two ? fabsf(v1) : 0.f)) : 0.f));
+        const float ge = 2.f * err + 3.f * U32 * big;
+        // (a group without a usable expert is no rival, and none is pushed out by one)
+        const float least = key_logit(key_of_min(mine && gs > -INFINITY ? gs : INFINITY));
+        const float rival = key_logit(key_of_max(mine || g >= a.G ? -INFINITY : gs));
+        if (rival > -INFINITY && !(least - rival > 2.f * ge)) {
+          bool unsure = false;  // this kept group and one that is dropped are too near, and not equal
+          for (int h = 0; h < a.G; ++h) {
+            const float o = __shfl_sync(0xffffffffu, gs, h * L);
+            const float o0 = __shfl_sync(0xffffffffu, k0, h * L), o1 = __shfl_sync(0xffffffffu, k1, h * L);
+            const bool same = !a.bias && o0 == k0 && (a.group_sum == 1 || o1 == k1);
+            if (mine && !(in >> (h * L) & 1u) && o > -INFINITY && !same && !(gs - o > 2.f * ge)) unsure = true;
+          }
+          if (__any_sync(0xffffffffu, unsure)) {
+            const double z = a.softmax && a.bias ? softmax_sum_d(sc.l, usable, m) : 1.0;
+            bool sure;
+            const uint32_t kept = groups_exact(a, sc.l, val, size, pitch, m, z, err, &sure);
+            if (!sure) {
+              __syncwarp();
+              select_exact(a, t, sc.l, m, usable, reinterpret_cast<double*>(val));
+              continue;
+            }
+            in = __ballot_sync(0xffffffffu, g < a.G && (kept >> g & 1u));
+          }
+        }
+      }
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         const int e = lane + 32 * j;
-        if (e < a.E) val[e + group_of(a, e) * (pitch - size)] = !(usable >> j & 1) ? -INFINITY : a.bias ? v[j] : l[j];
+        const bool there = e < a.E && (a.G == 1 || (in >> (group_of(a, e) * L) & 1u));
+        key[j] = !there ? 0u : !(usable >> j & 1) ? 1u : value_key(a.bias ? v[j] : l[j]);
       }
-      __syncwarp();
-      const int g = lane / L;
-      float k0 = -INFINITY, k1 = -INFINITY;
-      if (g < a.G)
-        for (int i = lane % L; i < size; i += L) {
-          const float w = val[g * pitch + i];
-          k1 = fmaxf(k1, fminf(k0, w));
-          k0 = fmaxf(k0, w);
-        }
-      for (int o = 1; o < L; o <<= 1) {
-        const float w0 = __shfl_xor_sync(0xffffffffu, k0, o), w1 = __shfl_xor_sync(0xffffffffu, k1, o);
-        k1 = fmaxf(fminf(k0, w0), fmaxf(k1, w1));
-        k0 = fmaxf(k0, w0);
-      }
-      float v0 = k0, v1 = k1;
-      if (!a.bias) {
-        v0 = k0 > -INFINITY ? (a.softmax ? expf(k0 - m) * inv_z : __fdividef(1.f, 1.f + expf(-k0))) : k0;
-        v1 = k1 > -INFINITY ? (a.softmax ? expf(k1 - m) * inv_z : __fdividef(1.f, 1.f + expf(-k1))) : k1;
-      }
-      const bool two = a.group_sum == 2 && v1 > -INFINITY;
-      const float gs = two ? v0 + v1 : v0;
-      // the scores' error, the largest of any group's: of two values and of their sum
-      const float ge = warp_max(gs > -INFINITY ? 2.f * err + U32 * (fabsf(v0) + (two ? fabsf(v1) : 0.f) + fabsf(gs)) : 0.f);
-      int rank = 0;
-#pragma unroll 4
-      for (int h = 0; h < a.G; ++h) {
-        const float o = __shfl_sync(0xffffffffu, gs, h * L);
-        rank += (o > gs || (o == gs && h < g)) ? 1 : 0;
-      }
-      const uint32_t in = __ballot_sync(0xffffffffu, g < a.G && rank < a.keep);
-      kept = 0;
-      bool unsure = false;  // this kept group and one that is dropped are too near, and not equal
-      const bool mine = in >> lane & 1u;
-      for (int h = 0; h < a.G; ++h) {
-        const float o = __shfl_sync(0xffffffffu, gs, h * L);
-        const float o0 = __shfl_sync(0xffffffffu, k0, h * L), o1 = __shfl_sync(0xffffffffu, k1, h * L);
-        const bool h_in = in >> (h * L) & 1u;
-        kept |= (h_in ? 1u : 0u) << h;
-        const bool same = !a.bias && o0 == k0 && (a.group_sum == 1 || o1 == k1);
-        if (mine && !h_in && o > -INFINITY && !same && !(gs - o > 2.f * ge)) unsure = true;
-      }
-      if (__any_sync(0xffffffffu, unsure)) {
-        const double z = a.softmax && a.bias ? softmax_sum_d(sc.l, usable, m) : 1.0;
-        bool sure;
-        kept = groups_exact(a, sc.l, val, size, pitch, m, z, err, &sure);
-        if (!sure) {
-          __syncwarp();
-          select_exact(a, t, sc.l, m, usable, reinterpret_cast<double*>(val));
-          return;
-        }
-      }
-    }
+    } else {
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int e = lane + 32 * j;
-      const bool there = e < a.E && (a.G == 1 || (kept >> group_of(a, e) & 1u));
-      key[j] = !there ? 0u : !(usable >> j & 1) ? 1u : value_key(a.bias ? v[j] : l[j]);
+      for (int j = 0; j < PER; ++j)
+        key[j] = lane + 32 * j >= a.E ? 0u : !(usable >> j & 1) ? 1u : value_key(l[j]);
     }
-  } else {
+
+    // candidates: every usable key not below the k-th largest of the lanes' largest (k lanes hold one at least), and
+    // with a bias not surely below it.  The k-th largest by a bitonic sort of the 32.
+    uint32_t tau = key[0];
+#pragma unroll
+    for (int j = 1; j < PER; ++j) tau = max(tau, key[j]);
+#pragma unroll
+    for (int n = 2; n <= 32; n <<= 1)
+#pragma unroll
+      for (int o = n >> 1; o; o >>= 1) {
+        const uint32_t v = __shfl_xor_sync(0xffffffffu, tau, o);
+        tau = (((lane & o) == 0) == ((lane & n) == 0)) ? max(tau, v) : min(tau, v);
+      }
+    tau = __shfl_sync(0xffffffffu, tau, a.k - 1);
+    if (VALUES && a.bias && tau > 1u) {
+      const float f = key_logit(tau);
+      if (f < INFINITY) tau = min(tau, value_key(f - 2.f * err - 4.f * U32 * fabsf(f)));
+    }
+    const uint32_t thr = max(tau, 2u);
+    uint32_t is = 0;
 #pragma unroll
     for (int j = 0; j < PER; ++j)
-      key[j] = lane + 32 * j >= a.E ? 0u : !(usable >> j & 1) ? 1u : value_key(l[j]);
-  }
-
-  // candidates: every key not below the k-th largest of the lanes' largest (k lanes hold one at least), and
-  // with a bias not surely below it
-  uint32_t mk = key[0];
+      if (key[j] >= thr) is |= 1u << j;
+    int pos = __popc(is);
 #pragma unroll
-  for (int j = 1; j < PER; ++j) mk = max(mk, key[j]);
-  int r = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, pos, o);
+      if (lane >= o) pos += v;
+    }
+    int C = __shfl_sync(0xffffffffu, pos, 31);
+    pos -= __popc(is);
+    if (C <= CAND) {
 #pragma unroll
-  for (int o = 1; o < 32; ++o) {
-    const int src = (lane + o) & 31;
-    const uint32_t v = __shfl_sync(0xffffffffu, mk, src);
-    r += (v > mk || (v == mk && src < lane)) ? 1 : 0;
-  }
-  uint32_t tau = __shfl_sync(0xffffffffu, mk, __ffs(__ballot_sync(0xffffffffu, r == a.k - 1)) - 1);
-  if (VALUES && a.bias && tau > 1u) {
-    const float f = key_logit(tau);
-    if (f < INFINITY) tau = min(tau, value_key(f - 2.f * err - 4.f * U32 * fabsf(f)));
-  }
-  tau = max(tau, 1u);
-  const uint32_t below = (1u << lane) - 1u;
-  int C = 0;
+      for (int j = 0; j < PER; ++j)
+        if (is >> j & 1) sc.cand[pos++] = make_uint2(key[j], (uint32_t)(lane + 32 * j));
+      if (C < a.k) {
+        // fewer usable experts than k: masked ones of the kept groups, lower ids first
 #pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const bool is = key[j] >= tau;
-    const uint32_t bal = __ballot_sync(0xffffffffu, is);
-    const int pos = C + __popc(bal & below);
-    if (is && pos < CAND) sc.cand[pos] = make_uint2(key[j], (uint32_t)(lane + 32 * j));
-    C += __popc(bal);
-  }
-  __syncwarp();
-  if (C > CAND) {
-    if (VALUES && a.bias) {
+        for (int j = 0; j < PER; ++j) {
+          const uint32_t bal = __ballot_sync(0xffffffffu, key[j] == 1u);
+          const int at = C + __popc(bal & below);
+          if (key[j] == 1u && at < a.k) sc.cand[at] = make_uint2(1u, (uint32_t)(lane + 32 * j));
+          C = min(a.k, C + __popc(bal));
+        }
+      }
+      __syncwarp();
+      for (int i = lane; i < C; i += 32) {
+        const uint2 me = sc.cand[i];
+        int rank = 0;
+#pragma unroll 4
+        for (int q = 0; q < C; ++q) {
+          const uint2 o = sc.cand[q];
+          rank += (o.x > me.x || (o.x == me.x && o.y < me.y)) ? 1 : 0;
+        }
+        if (rank <= a.k) sc.sel[rank] = me;
+      }
+    } else if (VALUES && a.bias) {
       __syncwarp();
       select_exact(a, t, sc.l, m, usable, reinterpret_cast<double*>(val));
-      return;
-    }
-    // a mass of equal logits: k rounds of the warp's largest (key, then lower id)
+      continue;
+    } else {
+      // a mass of equal logits: k rounds of the warp's largest (key, then lower id)
 #pragma unroll 1
-    for (int i = 0; i < a.k; ++i) {
-      uint32_t bk = key[0];
-      int bj = 0;
-#pragma unroll
-      for (int j = 1; j < PER; ++j)
-        if (key[j] > bk) {
-          bk = key[j];
-          bj = j;
-        }
-      const uint32_t mx = __reduce_max_sync(0xffffffffu, bk);
-      const uint32_t id = __reduce_min_sync(0xffffffffu, bk == mx ? (uint32_t)(lane + 32 * bj) : 0xffffffffu);
-      if ((int)(id & 31u) == lane) {
+      for (int i = 0; i < a.k; ++i) {
+        uint32_t bk = 0u, bj = 0u;
 #pragma unroll
         for (int j = 0; j < PER; ++j)
-          if (j == (int)(id >> 5)) key[j] = 0u;
-      }
-      if (lane == 0) sc.sel[i] = make_uint2(mx, id);
-    }
-  } else {
-    for (int i = lane; i < C; i += 32) {
-      const uint2 me = sc.cand[i];
-      int rank = 0;
-#pragma unroll 4
-      for (int q = 0; q < C; ++q) {
-        const uint2 o = sc.cand[q];
-        rank += (o.x > me.x || (o.x == me.x && o.y < me.y)) ? 1 : 0;
-      }
-      if (rank <= a.k) sc.sel[rank] = me;
-    }
-  }
-  __syncwarp();
-  if (VALUES && a.bias) {
-    // neighbours in the order whose values fp32 cannot tell apart (the same logit and bias: a true tie)
-    bool unsure = false;
-    if (lane < a.k && lane + 1 < C) {
-      const uint2 p = sc.sel[lane], q = sc.sel[lane + 1];
-      if (q.x > 1u) {
-        const float u = key_logit(p.x), v = key_logit(q.x);
-        unsure = !(u - v > 2.f * err + U32 * (fabsf(u) + fabsf(v))) &&
-                 !(sc.l[p.y] == sc.l[q.y] && __ldg(a.bias + p.y) == __ldg(a.bias + q.y));
-      }
-    }
-    if (__any_sync(0xffffffffu, unsure)) {
-      const double z = a.softmax ? softmax_sum_d(sc.l, usable, m) : 1.0;
-      double mine[CAND / 32];
+          if (key[j] > bk) {
+            bk = key[j];
+            bj = j;
+          }
+        const uint32_t mx = __reduce_max_sync(0xffffffffu, bk);
+        const uint32_t id = __reduce_min_sync(0xffffffffu, bk == mx ? lane + 32u * bj : 0xffffffffu);
 #pragma unroll
-      for (int h = 0; h < CAND / 32; ++h) {
-        mine[h] = -INFINITY;
-        if (lane + 32 * h < C) {
-          const uint2 c = sc.cand[lane + 32 * h];
-          if (c.x > 1u) mine[h] = score_d(sc.l[c.y], a.softmax, m, z) + (double)__ldg(a.bias + c.y);
+        for (int j = 0; j < PER; ++j)
+          if (id == (uint32_t)(lane + 32 * j)) key[j] = 0u;
+        if (lane == 0) sc.sel[i] = make_uint2(mx, id);
+      }
+    }
+    __syncwarp();
+    if (VALUES && a.bias) {
+      // neighbours in the order whose values fp32 cannot tell apart (the same logit and bias: a true tie)
+      bool unsure = false;
+      if (lane < a.k && lane + 1 < C) {
+        const uint2 p = sc.sel[lane], q = sc.sel[lane + 1];
+        if (q.x > 1u) {
+          const float u = key_logit(p.x), v = key_logit(q.x);
+          unsure = !(u - v > 2.f * err + U32 * (fabsf(u) + fabsf(v))) &&
+                   !(sc.l[p.y] == sc.l[q.y] && __ldg(a.bias + p.y) == __ldg(a.bias + q.y));
         }
       }
-      int rank[CAND / 32] = {0, 0};
-      for (int q = 0; q < C; ++q) {
-        const double o = __shfl_sync(0xffffffffu, q < 32 ? mine[0] : mine[1], q & 31);
-        const uint32_t oe = sc.cand[q].y;
+      if (__any_sync(0xffffffffu, unsure)) {
+        const double z = a.softmax ? softmax_sum_d(sc.l, usable, m) : 1.0;
+        double mine[CAND / 32];
+#pragma unroll
+        for (int h = 0; h < CAND / 32; ++h) {
+          mine[h] = -INFINITY;
+          if (lane + 32 * h < C) {
+            const uint2 c = sc.cand[lane + 32 * h];
+            if (c.x > 1u) mine[h] = score_d(sc.l[c.y], a.softmax, m, z) + (double)__ldg(a.bias + c.y);
+          }
+        }
+        int rank[CAND / 32] = {0, 0};
+        for (int q = 0; q < C; ++q) {
+          const double o = __shfl_sync(0xffffffffu, q < 32 ? mine[0] : mine[1], q & 31);
+          const uint32_t oe = sc.cand[q].y;
+#pragma unroll
+          for (int h = 0; h < CAND / 32; ++h)
+            if (lane + 32 * h < C) {
+              const uint32_t e = sc.cand[lane + 32 * h].y;
+              rank[h] += (o > mine[h] || (o == mine[h] && oe < e)) ? 1 : 0;
+            }
+        }
+        __syncwarp();
 #pragma unroll
         for (int h = 0; h < CAND / 32; ++h)
-          if (lane + 32 * h < C) {
-            const uint32_t e = sc.cand[lane + 32 * h].y;
-            rank[h] += (o > mine[h] || (o == mine[h] && oe < e)) ? 1 : 0;
-          }
+          if (lane + 32 * h < C && rank[h] < a.k) sc.sel[rank[h]] = sc.cand[lane + 32 * h];
+        __syncwarp();
       }
-      __syncwarp();
-#pragma unroll
-      for (int h = 0; h < CAND / 32; ++h)
-        if (lane + 32 * h < C && rank[h] < a.k) sc.sel[rank[h]] = sc.cand[lane + 32 * h];
-      __syncwarp();
     }
-  }
-  // weights: without groups or a bias the k largest softmax scores sum to k / E at least, above the clamp, and the
-  // softmax's own sum divides out
-  const bool has = lane < a.k;
-  const uint2 me = sc.sel[has ? lane : 0];
-  float p = 0.f;
-  if (has && me.x > 1u) {
-    const float x = sc.l[me.y];
-    p = a.softmax ? expf(x - m) : 1.f / (1.f + expf(-x));
-  }
-  if (a.softmax && (VALUES || !a.renorm)) {
-    if constexpr (!VALUES) {
-      float z = 0.f;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) z += usable >> j & 1 ? expf(sc.l[lane + 32 * j] - m) : 0.f;
-      z = warp_sum(z);
-      inv_z = z > 0.f ? 1.f / z : 1.f;
+    // weights: without groups or a bias the k largest softmax scores sum to k / E at least, above the clamp, and the
+    // softmax's own sum divides out
+    const bool has = lane < a.k;
+    const uint2 me = sc.sel[has ? lane : 0];
+    float p = 0.f;
+    if (has && me.x > 1u) {
+      const float x = sc.l[me.y];
+      p = a.softmax ? expf(x - m) : 1.f / (1.f + expf(-x));
     }
-    p *= inv_z;
+    if (a.softmax && (VALUES || !a.renorm)) {
+      if constexpr (!VALUES) {
+        float z = 0.f;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) z += usable >> j & 1 ? __expf(sc.l[lane + 32 * j] - m) : 0.f;
+        z = warp_sum(z);
+        inv_z = z > 0.f ? 1.f / z : 1.f;
+      }
+      p *= inv_z;
+    }
+    const float sum = a.renorm ? fmaxf(warp_sum(p), SUM_MIN) : 1.f;
+    if (has) {
+      a.ids[(int64_t)t * a.k + lane] = (int)me.y;
+      a.weights[(int64_t)t * a.k + lane] = p / sum * a.scale;
+    }
+    __syncwarp();
   }
-  const float sum = warp_sum(p);
-  if (has) {
-    a.ids[(int64_t)t * a.k + lane] = (int)me.y;
-    a.weights[(int64_t)t * a.k + lane] = (a.renorm ? p / fmaxf(sum, SUM_MIN) : p) * a.scale;
-  }
+}
+
+template <bool VALUES, int PER>
+void launch_form(const SelectArgs& a, int grid, int warp_bytes, cudaStream_t s) {
+  select_kernel<VALUES, PER><<<grid, 32 * SEL_WARPS, SEL_WARPS * warp_bytes, s>>>(a, warp_bytes);
 }
 
 }  // namespace
@@ -479,10 +523,14 @@ cudaError_t launch_select(const strata_select_t& sel, const void* logits, int T,
                      ((1 << 20) + sel.n_expert / sel.n_group - 1) / (sel.n_expert / sel.n_group)};
   const bool values = bias || sel.n_group > 1;
   const int warp_bytes = (int)select_warp_bytes(sel.n_expert, sel.n_group, values);
-  const dim3 grid((T + SEL_WARPS - 1) / SEL_WARPS), block(32 * SEL_WARPS);
+  // a warp takes ceil(T / what fits the GPU) tokens, so that all end together
+  const int fit = 152 * 5 * SEL_WARPS, turns = (T + fit - 1) / fit;
+  const int warps = (T + turns - 1) / turns, grid = (warps + SEL_WARPS - 1) / SEL_WARPS;
   kernel_begin(KID_SELECT, s);
-  if (values) select_kernel<true><<<grid, block, SEL_WARPS * warp_bytes, s>>>(a, warp_bytes);
-  else select_kernel<false><<<grid, block, SEL_WARPS * warp_bytes, s>>>(a, warp_bytes);
+  if (values && sel.n_expert > 256) launch_form<true, 16>(a, grid, warp_bytes, s);
+  else if (values) launch_form<true, 8>(a, grid, warp_bytes, s);
+  else if (sel.n_expert > 256) launch_form<false, 16>(a, grid, warp_bytes, s);
+  else launch_form<false, 8>(a, grid, warp_bytes, s);
   kernel_end(KID_SELECT, s);
   return cudaGetLastError();
 }
