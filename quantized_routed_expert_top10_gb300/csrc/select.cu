@@ -148,44 +148,91 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t, const floa
 constexpr float U32 = 5.9604645e-8f;
 constexpr float ERR_SOFTMAX = 52.f, ERR_SIGMOID = 8.f;
 
-// A value's place in the choice as an unsigned number: larger values larger numbers (-0 as +0), a masked expert 1, one that
-// does not exist or whose group is dropped 0.
-__device__ __forceinline__ uint32_t value_key(float v) { return logit_key(v + 0.f); }
+// A value's place in the choice as an unsigned number: larger values larger numbers (-0 as +0).  A masked expert has the
+// value -inf, and so the smallest key.
+__device__ __forceinline__ uint32_t value_key(float v) {
+  const int b = __float_as_int(v + 0.f);
+  return (uint32_t)(b ^ ((b >> 31) | (int)0x80000000));
+}
+constexpr uint32_t MASKED = 0x007fffffu;  // value_key(-inf)
+__device__ __forceinline__ float warp_min_key(float v) { return key_logit(__reduce_min_sync(0xffffffffu, value_key(v))); }
+__device__ __forceinline__ float warp_max_key(float v) { return key_logit(__reduce_max_sync(0xffffffffu, value_key(v))); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float LOG2E = 1.44269504f;
+__device__ __forceinline__ float sigmoid_fast(float l) { return rcp(1.f + ex2(l * -LOG2E)); }
 
 constexpr int CAND = 64;
-struct SelectScratch {  // one per warp; the padded values (groups) or 64-bit values follow
+struct SelectScratch {  // one per warp; the 64-bit values of select_exact follow
   float l[EMAX];
-  uint2 cand[CAND];     // key, id
-  uint2 sel[STRATA_SELECT_K_MAX + 1];
+  float val[EMAX + EMAX / 32];  // value of expert e at e + e / 32
+  uint64_t cand[CAND];          // key, then ~id: the larger number comes first
+  uint64_t sel[STRATA_SELECT_K_MAX + 1];
+  int kept[STRATA_SELECT_GROUP_MAX];
 };
-// Distance of two groups' values in shared memory: lane / L is the group and the L lanes of a group read
-// neighbouring values, so a distance of L modulo 32 puts the warp's 32 reads into 32 banks.
-__host__ __device__ inline int group_lanes(int G) { return G > 16 ? 1 : G > 8 ? 2 : G > 4 ? 4 : G > 2 ? 8 : G > 1 ? 16 : 32; }
-__host__ __device__ inline int group_pitch(int size, int G) { return size + ((group_lanes(G) - size) & 31); }
-inline size_t select_warp_bytes(int E, int G, bool values) {
-  if (!values) return sizeof(SelectScratch);
-  const size_t groups = G > 1 ? sizeof(float) * G * group_pitch(E / G, G) : 0, exact = sizeof(double) * EMAX;
-  return (sizeof(SelectScratch) + (groups > exact ? groups : exact) + 15) / 16 * 16;
-}
 static_assert(sizeof(SelectScratch) % 8 == 0, "64-bit values follow the scratch");
+__device__ __forceinline__ int cand_id(uint64_t c) { return (int)~(uint32_t)c; }
+__device__ __forceinline__ uint32_t cand_key(uint64_t c) { return (uint32_t)(c >> 32); }
+
+// Lanes of a group when the groups' values are read, L: all groups fit a warp.
+__device__ __forceinline__ int group_lanes(int G) { return G > 16 ? 1 : G > 8 ? 2 : G > 4 ? 4 : G > 2 ? 8 : G > 1 ? 16 : 32; }
+
+// The logits of token t once more, into shared memory for the 64-bit passes: +inf made finite; returns the usable experts
+// (bit j: expert lane + 32 j) and their largest logit.
+__device__ __noinline__ uint32_t read_row(const SelectArgs& a, int t, float* l, float* m) {
+  const int lane = threadIdx.x & 31;
+  const float lowest = lowest_of(a.type);
+  uint32_t usable = 0;
+  float top = -FLT_MAX, v[EMAX / 32], b[EMAX / 32];
+#pragma unroll
+  for (int j = 0; j < EMAX / 32; ++j) {  // every load is issued before the first is looked at
+    const int e = lane + 32 * j;
+    v[j] = e < a.E ? load1(a.logits, (int64_t)t * a.stride + e, a.type) : lowest;
+    b[j] = a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < EMAX / 32; ++j) {
+    if (v[j] > lowest && b[j] > -INFINITY) {
+      usable |= 1u << j;
+      top = fmaxf(top, fminf(v[j], FLT_MAX));
+    }
+    l[lane + 32 * j] = fminf(v[j], FLT_MAX);
+  }
+  *m = warp_max(top);
+  __syncwarp();
+  return usable;
+}
 
 // Groups kept, where the fp32 scores do not decide: the groups' scores in 64 bits, from the two largest values of each
 // (val: the values with a bias, the logits without).  Lane g < G scans group g.  *sure = false if a group's two largest
-// cannot be told from its third.  z: the softmax's sum (without a bias any positive number: the order is the same).
-__device__ __noinline__ uint32_t groups_exact(const SelectArgs& a, const float* l, const float* val, int size, int pitch,
-                                              float m, double z, float err, bool* sure) {
+// cannot be told from its third.
+__device__ __noinline__ uint32_t groups_exact(const SelectArgs& a, int t, SelectScratch& sc, float err, bool* sure) {
   const int lane = threadIdx.x & 31;
+  float m;
+  const uint32_t usable = read_row(a, t, sc.l, &m);
+  // without a bias the sum divides out
+  const double z = a.softmax && a.bias ? softmax_sum_d(sc.l, usable, m) : 1.0;
   float v0 = -INFINITY, v1 = -INFINITY, v2 = -INFINITY;
   int e0 = 0, e1 = 0;
   if (lane < a.G)
-    for (int i = 0; i < size; ++i) {
-      const float v = val[lane * pitch + i];
+    for (int i = 0; i < a.size; ++i) {
+      const int e = lane * a.size + i;
+      const float v = sc.val[e + (e >> 5)];
       if (v > v0) {
         v2 = v1; v1 = v0; e1 = e0;
-        v0 = v; e0 = lane * size + i;
+        v0 = v; e0 = e;
       } else if (v > v1) {
         v2 = v1;
-        v1 = v; e1 = lane * size + i;
+        v1 = v; e1 = e;
       } else if (v > v2) {
         v2 = v;
       }
@@ -195,8 +242,9 @@ __device__ __noinline__ uint32_t groups_exact(const SelectArgs& a, const float* 
                      last - behind > 2.f * (err + U32 * fmaxf(fabsf(last), fabsf(behind)));
   *sure = __all_sync(0xffffffffu, clear);
   double gs = -INFINITY;
-  if (v0 > -INFINITY) gs = score_d(l[e0], a.softmax, m, z) + (a.bias ? (double)__ldg(a.bias + e0) : 0.0);
-  if (a.group_sum == 2 && v1 > -INFINITY) gs += score_d(l[e1], a.softmax, m, z) + (a.bias ? (double)__ldg(a.bias + e1) : 0.0);
+  if (v0 > -INFINITY) gs = score_d(sc.l[e0], a.softmax, m, z) + (a.bias ? (double)__ldg(a.bias + e0) : 0.0);
+  if (a.group_sum == 2 && v1 > -INFINITY)
+    gs += score_d(sc.l[e1], a.softmax, m, z) + (a.bias ? (double)__ldg(a.bias + e1) : 0.0);
   int rank = 0;
   for (int g = 0; g < a.G; ++g) {
     const double o = __shfl_sync(0xffffffffu, gs, g);
@@ -205,8 +253,45 @@ __device__ __noinline__ uint32_t groups_exact(const SelectArgs& a, const float* 
   return __ballot_sync(0xffffffffu, lane < a.G && rank < a.keep);
 }
 
-__device__ __forceinline__ uint32_t key_of_min(float v) { return __reduce_min_sync(0xffffffffu, value_key(v)); }
-__device__ __forceinline__ uint32_t key_of_max(float v) { return __reduce_max_sync(0xffffffffu, value_key(v)); }
+// The order of C candidates (sc.cand) by their values in 64 bits into sc.sel, where neighbours among the first k are too near
+// for fp32; near neighbours of the same logit and bias are true ties and stay as they are.
+__device__ __noinline__ void order_exact(const SelectArgs& a, int t, SelectScratch& sc, int C, bool near) {
+  const int lane = threadIdx.x & 31;
+  float m;
+  const uint32_t usable = read_row(a, t, sc.l, &m);
+  if (near) {
+    const int p = cand_id(sc.sel[lane]), q = cand_id(sc.sel[lane + 1]);
+    near = !(sc.l[p] == sc.l[q] && __ldg(a.bias + p) == __ldg(a.bias + q));
+  }
+  if (!__any_sync(0xffffffffu, near)) return;
+  const double z = a.softmax ? softmax_sum_d(sc.l, usable, m) : 1.0;
+  double mine[CAND / 32];
+#pragma unroll
+  for (int h = 0; h < CAND / 32; ++h) {
+    mine[h] = -INFINITY;
+    if (lane + 32 * h < C) {
+      const uint64_t c = sc.cand[lane + 32 * h];
+      const int e = cand_id(c);
+      if (cand_key(c) > MASKED) mine[h] = score_d(sc.l[e], a.softmax, m, z) + (double)__ldg(a.bias + e);
+    }
+  }
+  int rank[CAND / 32] = {0, 0};
+  for (int q = 0; q < C; ++q) {
+    const double o = __shfl_sync(0xffffffffu, q < 32 ? mine[0] : mine[1], q & 31);
+    const int oe = cand_id(sc.cand[q]);
+#pragma unroll
+    for (int h = 0; h < CAND / 32; ++h)
+      if (lane + 32 * h < C) {
+        const int e = cand_id(sc.cand[lane + 32 * h]);
+        rank[h] += (o > mine[h] || (o == mine[h] && oe < e)) ? 1 : 0;
+      }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int h = 0; h < CAND / 32; ++h)
+    if (lane + 32 * h < C && rank[h] < a.k) sc.sel[rank[h]] = sc.cand[lane + 32 * h];
+  __syncwarp();
+}
 
 // One token per warp and turn.  VALUES: the choice goes by scores (a bias, or groups); otherwise by the logits alone.
 // PER: experts of a lane (lane + 32 j), E <= 32 PER.
@@ -219,146 +304,164 @@ __global__ void __launch_bounds__(32 * SEL_WARPS, 5) select_kernel(const __grid_
   extern __shared__ __align__(16) char s_all[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   SelectScratch& sc = *reinterpret_cast<SelectScratch*>(s_all + warp * warp_bytes);
-  float* const val = reinterpret_cast<float*>(&sc + 1);
+  double* const exact = reinterpret_cast<double*>(&sc + 1);
   const float lowest = lowest_of(a.type);
   const uint32_t below = (1u << lane) - 1u;
-  const int size = a.size, pitch = VALUES ? group_pitch(size, a.G) : 0, L = VALUES ? group_lanes(a.G) : 32;
+  const bool grouped = VALUES && a.G > 1;
+  const int L = VALUES ? group_lanes(a.G) : 32;
+  const int total = grouped ? a.keep * a.size : a.E;  // experts that may be chosen
   float b[PER];
-  uint32_t open = 0;  // bit j: the expert exists and its bias does not mask it
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int e = lane + 32 * j;
     b[j] = VALUES && a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
-    if (e < a.E && b[j] > -INFINITY) open |= 1u << j;
+    if (!(b[j] > -INFINITY)) b[j] = -INFINITY;  // NaN too: the expert's value is -inf
   }
   for (int t = blockIdx.x * SEL_WARPS + warp; t < a.T; t += gridDim.x * SEL_WARPS) {
-    float l[PER];
+    float v[PER];
     const int64_t row = (int64_t)t * a.stride + lane;
     if (a.type == STRATA_F32) {
 #pragma unroll
-      for (int j = 0; j < PER; ++j) l[j] = lane + 32 * j < a.E ? __ldg(static_cast<const float*>(a.logits) + row + 32 * j) : lowest;
+      for (int j = 0; j < PER; ++j) v[j] = lane + 32 * j < a.E ? __ldg(static_cast<const float*>(a.logits) + row + 32 * j) : lowest;
     } else {
       uint16_t raw[PER];
 #pragma unroll
-      for (int j = 0; j < PER; ++j)
-        raw[j] = lane + 32 * j < a.E ? __ldg(static_cast<const uint16_t*>(a.logits) + row + 32 * j) : (uint16_t)0;
+      for (int j = 0; j < PER; ++j)  // 0xffff: NaN
+        raw[j] = lane + 32 * j < a.E ? __ldg(static_cast<const uint16_t*>(a.logits) + row + 32 * j) : (uint16_t)0xffff;
 #pragma unroll
       for (int j = 0; j < PER; ++j)
-        l[j] = a.type == STRATA_BF16 ? __uint_as_float((uint32_t)raw[j] << 16) : __half2float(__ushort_as_half(raw[j]));
+        v[j] = a.type == STRATA_BF16 ? __uint_as_float((uint32_t)raw[j] << 16) : __half2float(__ushort_as_half(raw[j]));
     }
-    uint32_t usable = 0;
-    float m = -FLT_MAX;
+    // masked logits as -inf (a comparison with NaN is false)
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      // a comparison with NaN is false: such an expert is masked
-      const bool ok = l[j] > lowest && (open >> j & 1);
-      if (ok) usable |= 1u << j;
-      l[j] = fminf(l[j], FLT_MAX);
-      if (ok) m = fmaxf(m, l[j]);
-      sc.l[lane + 32 * j] = l[j];
-    }
-    m = warp_max(m);
+    for (int j = 0; j < PER; ++j) v[j] = v[j] > lowest ? fminf(v[j], FLT_MAX) : -INFINITY;
 
-    // values, and the experts' places: the value with a bias, the logit (the score's order) without
-    float inv_z = 1.f, err = 0.f;
-    uint32_t key[PER];
-    if constexpr (VALUES) {
-      float v[PER];
-      if (a.softmax) {
-        float z = 0.f;
+    // Values: logits, or with a bias scores + bias.  Without groups they stay in registers, with groups they go by
+    // shared memory and only the kept groups' come back.
+    float inv_z = 1.f, err = 0.f, m = 0.f;
+    if (a.softmax) {
+      m = v[0];
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          v[j] = usable >> j & 1 ? __expf(l[j] - m) : 0.f;
-          z += v[j];
-        }
-        z = warp_sum(z);
-        inv_z = z > 0.f ? 1.f / z : 1.f;
-        err = U32 * ERR_SOFTMAX * inv_z + 1e-37f;
+      for (int j = 1; j < PER; ++j) m = fmaxf(m, v[j]);
+      m = warp_max_key(m);
+      if (m == -INFINITY) m = 0.f;
+    }
+    if (a.softmax && (VALUES || !a.renorm)) {
+      float z = 0.f;
+      // an expert that its bias masks is no part of the softmax
+      float mb = m;
+      if (VALUES && a.bias) {
+        mb = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) v[j] = fmaf(v[j], inv_z, b[j]);
-      } else {
-        err = U32 * ERR_SIGMOID + 1e-37f;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) v[j] = __fdividef(1.f, 1.f + __expf(-l[j])) + b[j];
-      }
-      uint32_t in = 0xffffffffu;  // bit of a group's first lane: the group is kept
-      if (a.G > 1) {
-        // each group's two largest: of the values with a bias, of the logits without (the same experts, and
-        // equal scores are then known for what they are)
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          const int e = lane + 32 * j;
-          if (e < a.E) val[e + group_of(a, e) * (pitch - size)] = !(usable >> j & 1) ? -INFINITY : a.bias ? v[j] : l[j];
-        }
-        __syncwarp();
-        const int g = lane / L;
-        float k0 = -INFINITY, k1 = -INFINITY;
-        if (g < a.G) {
-          const float* at = val + g * pitch;
-#pragma unroll 8
-          for (int i = lane % L; i < size; i += L) {
-            const float w = at[i];
-            k1 = fmaxf(k1, fminf(k0, w));
-            k0 = fmaxf(k0, w);
-          }
-        }
-        for (int o = 1; o < L; o <<= 1) {
-          const float w0 = __shfl_xor_sync(0xffffffffu, k0, o), w1 = __shfl_xor_sync(0xffffffffu, k1, o);
-          k1 = fmaxf(fminf(k0, w0), fmaxf(k1, w1));
-          k0 = fmaxf(k0, w0);
-        }
-        float v0 = k0, v1 = k1;
-        if (!a.bias) {
-          v0 = k0 > -INFINITY ? (a.softmax ? __expf(k0 - m) * inv_z : __fdividef(1.f, 1.f + __expf(-k0))) : k0;
-          v1 = k1 > -INFINITY ? (a.softmax ? __expf(k1 - m) * inv_z : __fdividef(1.f, 1.f + __expf(-k1))) : k1;
-        }
-        const bool two = a.group_sum == 2 && v1 > -INFINITY;
-        const float gs = two ? v0 + v1 : v0;
-        int rank = 0;
-#pragma unroll 4
-        for (int h = 0; h < a.G; ++h) {
-          const float o = __shfl_sync(0xffffffffu, gs, h * L);
-          rank += (o > gs || (o == gs && h < g)) ? 1 : 0;
-        }
-        const bool mine = g < a.G && rank < a.keep;
-        in = __ballot_sync(0xffffffffu, mine);
-        // the scores' error: of two values and of their sum, none of them larger than the largest score or value
-        const float big = key_logit(key_of_max(gs > -INFINITY ? fmaxf(fabsf(gs), fmaxf(fabsf(v0), two ? fabsf(v1) : 0.f)) : 0.f));
-        const float ge = 2.f * err + 3.f * U32 * big;
-        // (a group without a usable expert is no rival, and none is pushed out by one)
-        const float least = key_logit(key_of_min(mine && gs > -INFINITY ? gs : INFINITY));
-        const float rival = key_logit(key_of_max(mine || g >= a.G ? -INFINITY : gs));
-        if (rival > -INFINITY && !(least - rival > 2.f * ge)) {
-          bool unsure = false;  // this kept group and one that is dropped are too near, and not equal
-          for (int h = 0; h < a.G; ++h) {
-            const float o = __shfl_sync(0xffffffffu, gs, h * L);
-            const float o0 = __shfl_sync(0xffffffffu, k0, h * L), o1 = __shfl_sync(0xffffffffu, k1, h * L);
-            const bool same = !a.bias && o0 == k0 && (a.group_sum == 1 || o1 == k1);
-            if (mine && !(in >> (h * L) & 1u) && o > -INFINITY && !same && !(gs - o > 2.f * ge)) unsure = true;
-          }
-          if (__any_sync(0xffffffffu, unsure)) {
-            const double z = a.softmax && a.bias ? softmax_sum_d(sc.l, usable, m) : 1.0;
-            bool sure;
-            const uint32_t kept = groups_exact(a, sc.l, val, size, pitch, m, z, err, &sure);
-            if (!sure) {
-              __syncwarp();
-              select_exact(a, t, sc.l, m, usable, reinterpret_cast<double*>(val));
-              continue;
-            }
-            in = __ballot_sync(0xffffffffu, g < a.G && (kept >> g & 1u));
-          }
-        }
+        for (int j = 0; j < PER; ++j)
+          if (b[j] > -INFINITY) mb = fmaxf(mb, v[j]);
+        mb = warp_max_key(mb);
+        if (mb == -INFINITY) mb = 0.f;
+        m = mb;
       }
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
-        const int e = lane + 32 * j;
-        const bool there = e < a.E && (a.G == 1 || (in >> (group_of(a, e) * L) & 1u));
-        key[j] = !there ? 0u : !(usable >> j & 1) ? 1u : value_key(a.bias ? v[j] : l[j]);
+        const float e = VALUES && !(b[j] > -INFINITY) ? 0.f : ex2((v[j] - m) * LOG2E);
+        z += e;
+        if (VALUES && a.bias) v[j] = v[j] > -INFINITY ? e : -INFINITY;
       }
-    } else {
+      z = warp_sum(z);
+      inv_z = z > 0.f ? 1.f / z : 1.f;
+      if (VALUES && a.bias) {
 #pragma unroll
-      for (int j = 0; j < PER; ++j)
-        key[j] = lane + 32 * j >= a.E ? 0u : !(usable >> j & 1) ? 1u : value_key(l[j]);
+        for (int j = 0; j < PER; ++j) v[j] = fmaf(v[j], inv_z, b[j]);
+      }
+      err = U32 * ERR_SOFTMAX * inv_z + 1e-37f;
+    }
+    if (VALUES && !a.softmax) {
+      err = U32 * ERR_SIGMOID + 1e-37f;
+      if (a.bias) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) v[j] = v[j] > -INFINITY ? sigmoid_fast(v[j]) + b[j] : -INFINITY;
+      }
+    }
+
+    uint32_t key[PER];
+    if (grouped) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) sc.val[lane + 33 * j] = v[j];
+      __syncwarp();
+      // each group's two largest, of the values with a bias, of the logits without (the same experts, and equal
+      // scores are then known for what they are)
+      const int g = lane / L;
+      float k0 = -INFINITY, k1 = -INFINITY;
+      if (g < a.G) {
+        const int end = (g + 1) * a.size;
+#pragma unroll 8
+        for (int e = g * a.size + lane % L; e < end; e += L) {
+          const float w = sc.val[e + (e >> 5)];
+          k1 = fmaxf(k1, fminf(k0, w));
+          k0 = fmaxf(k0, w);
+        }
+      }
+      for (int o = 1; o < L; o <<= 1) {
+        const float w0 = __shfl_xor_sync(0xffffffffu, k0, o), w1 = __shfl_xor_sync(0xffffffffu, k1, o);
+        k1 = fmaxf(fminf(k0, w0), fmaxf(k1, w1));
+        k0 = fmaxf(k0, w0);
+      }
+      float v0 = k0, v1 = k1;
+      if (!a.bias) {
+        if (k0 > -INFINITY) v0 = a.softmax ? ex2((k0 - m) * LOG2E) * inv_z : sigmoid_fast(k0);
+        if (k1 > -INFINITY) v1 = a.softmax ? ex2((k1 - m) * LOG2E) * inv_z : sigmoid_fast(k1);
+      }
+      const bool two = a.group_sum == 2 && v1 > -INFINITY;
+      const float gs = two ? v0 + v1 : v0;
+      int rank = 0;
+#pragma unroll 4
+      for (int h = 0; h < a.G; ++h) {
+        const float o = __shfl_sync(0xffffffffu, gs, h * L);
+        rank += (o > gs || (o == gs && h < g)) ? 1 : 0;
+      }
+      const bool mine = g < a.G && rank < a.keep;
+      uint32_t in = __ballot_sync(0xffffffffu, mine);  // L bits a group
+      // the scores' error: of two values and of their sum, none of them larger than `big`
+      const float big = warp_max_key(gs > -INFINITY ? fmaxf(fabsf(gs), fmaxf(fabsf(v0), two ? fabsf(v1) : 0.f)) : 0.f);
+      const float ge = 2.f * err + 3.f * U32 * big;
+      // (a group without a usable expert is no rival, and none is pushed out by one)
+      const float least = warp_min_key(mine && gs > -INFINITY ? gs : INFINITY);
+      const float rival = warp_max_key(mine || g >= a.G ? -INFINITY : gs);
+      if (rival > -INFINITY && !(least - rival > 2.f * ge)) {
+        bool unsure = false;  // this kept group and one that is dropped are too near, and not equal
+        for (int h = 0; h < a.G; ++h) {
+          const float o = __shfl_sync(0xffffffffu, gs, h * L);
+          const float o0 = __shfl_sync(0xffffffffu, k0, h * L), o1 = __shfl_sync(0xffffffffu, k1, h * L);
+          const bool same = !a.bias && o0 == k0 && (a.group_sum == 1 || o1 == k1);
+          if (mine && !(in >> (h * L) & 1u) && o > -INFINITY && !same && !(gs - o > 2.f * ge)) unsure = true;
+        }
+        if (__any_sync(0xffffffffu, unsure)) {
+          bool sure;
+          const uint32_t kept = groups_exact(a, t, sc, err, &sure);
+          if (!sure) {
+            const uint32_t usable = read_row(a, t, sc.l, &m);
+            select_exact(a, t, sc.l, m, usable, exact);
+            continue;
+          }
+          in = __ballot_sync(0xffffffffu, g < a.G && (kept >> g & 1u));
+        }
+      }
+      if ((in >> lane & 1u) && lane % L == 0) sc.kept[__popc(in & below) / L] = g;
+      __syncwarp();
+    }
+    // the expert at place i of those that may be chosen
+    const auto expert_at = [&](int i) {
+      if (!grouped) return i;
+      const int q = group_of(a, i);
+      return sc.kept[q] * a.size + i - q * a.size;
+    };
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      key[j] = MASKED;
+      if (!grouped) {
+        key[j] = value_key(v[j]);
+      } else if (32 * j < total && lane + 32 * j < total) {
+        const int e = expert_at(lane + 32 * j);
+        key[j] = value_key(sc.val[e + (e >> 5)]);
+      }
     }
 
     // candidates: every usable key not below the k-th largest of the lanes' largest (k lanes hold one at least), and
@@ -370,55 +473,58 @@ __global__ void __launch_bounds__(32 * SEL_WARPS, 5) select_kernel(const __grid_
     for (int n = 2; n <= 32; n <<= 1)
 #pragma unroll
       for (int o = n >> 1; o; o >>= 1) {
-        const uint32_t v = __shfl_xor_sync(0xffffffffu, tau, o);
-        tau = (((lane & o) == 0) == ((lane & n) == 0)) ? max(tau, v) : min(tau, v);
+        const uint32_t w = __shfl_xor_sync(0xffffffffu, tau, o);
+        tau = (((lane & o) == 0) == ((lane & n) == 0)) ? max(tau, w) : min(tau, w);
       }
     tau = __shfl_sync(0xffffffffu, tau, a.k - 1);
-    if (VALUES && a.bias && tau > 1u) {
+    if (VALUES && a.bias && tau > MASKED) {
       const float f = key_logit(tau);
       if (f < INFINITY) tau = min(tau, value_key(f - 2.f * err - 4.f * U32 * fabsf(f)));
     }
-    const uint32_t thr = max(tau, 2u);
+    tau = max(tau, MASKED + 1u);
     uint32_t is = 0;
 #pragma unroll
-    for (int j = 0; j < PER; ++j)
-      if (key[j] >= thr) is |= 1u << j;
+    for (int j = 0; j < PER; ++j) {
+      if (grouped && 32 * j >= total) break;
+      if (key[j] >= tau) is |= 1u << j;
+    }
     int pos = __popc(is);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, pos, o);
-      if (lane >= o) pos += v;
+      const int w = __shfl_up_sync(0xffffffffu, pos, o);
+      if (lane >= o) pos += w;
     }
     int C = __shfl_sync(0xffffffffu, pos, 31);
     pos -= __popc(is);
     if (C <= CAND) {
 #pragma unroll
-      for (int j = 0; j < PER; ++j)
-        if (is >> j & 1) sc.cand[pos++] = make_uint2(key[j], (uint32_t)(lane + 32 * j));
+      for (int j = 0; j < PER; ++j) {
+        if (grouped && 32 * j >= total) break;
+        if (is >> j & 1) sc.cand[pos++] = (uint64_t)key[j] << 32 | (uint32_t)~expert_at(lane + 32 * j);
+      }
       if (C < a.k) {
         // fewer usable experts than k: masked ones of the kept groups, lower ids first
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-          const uint32_t bal = __ballot_sync(0xffffffffu, key[j] == 1u);
+          const int i = lane + 32 * j;
+          const bool masked = i < total && key[j] == MASKED;
+          const uint32_t bal = __ballot_sync(0xffffffffu, masked);
           const int at = C + __popc(bal & below);
-          if (key[j] == 1u && at < a.k) sc.cand[at] = make_uint2(1u, (uint32_t)(lane + 32 * j));
+          if (masked && at < a.k) sc.cand[at] = (uint64_t)MASKED << 32 | (uint32_t)~expert_at(i);
           C = min(a.k, C + __popc(bal));
         }
       }
       __syncwarp();
       for (int i = lane; i < C; i += 32) {
-        const uint2 me = sc.cand[i];
+        const uint64_t me = sc.cand[i];
         int rank = 0;
 #pragma unroll 4
-        for (int q = 0; q < C; ++q) {
-          const uint2 o = sc.cand[q];
-          rank += (o.x > me.x || (o.x == me.x && o.y < me.y)) ? 1 : 0;
-        }
+        for (int q = 0; q < C; ++q) rank += sc.cand[q] > me ? 1 : 0;
         if (rank <= a.k) sc.sel[rank] = me;
       }
     } else if (VALUES && a.bias) {
-      __syncwarp();
-      select_exact(a, t, sc.l, m, usable, reinterpret_cast<double*>(val));
+      const uint32_t usable = read_row(a, t, sc.l, &m);
+      select_exact(a, t, sc.l, m, usable, exact);
       continue;
     } else {
       // a mass of equal logits: k rounds of the warp's largest (key, then lower id)
@@ -432,77 +538,37 @@ __global__ void __launch_bounds__(32 * SEL_WARPS, 5) select_kernel(const __grid_
             bj = j;
           }
         const uint32_t mx = __reduce_max_sync(0xffffffffu, bk);
-        const uint32_t id = __reduce_min_sync(0xffffffffu, bk == mx ? lane + 32u * bj : 0xffffffffu);
+        const uint32_t at = __reduce_min_sync(0xffffffffu, bk == mx ? lane + 32u * bj : 0xffffffffu);
 #pragma unroll
         for (int j = 0; j < PER; ++j)
-          if (id == (uint32_t)(lane + 32 * j)) key[j] = 0u;
-        if (lane == 0) sc.sel[i] = make_uint2(mx, id);
+          if (at == (uint32_t)(lane + 32 * j)) key[j] = 0u;
+        if (lane == 0) sc.sel[i] = (uint64_t)mx << 32 | (uint32_t)~expert_at((int)at);
       }
     }
     __syncwarp();
     if (VALUES && a.bias) {
-      // neighbours in the order whose values fp32 cannot tell apart (the same logit and bias: a true tie)
-      bool unsure = false;
+      // neighbours in the order whose values fp32 cannot tell apart
+      bool near = false;
       if (lane < a.k && lane + 1 < C) {
-        const uint2 p = sc.sel[lane], q = sc.sel[lane + 1];
-        if (q.x > 1u) {
-          const float u = key_logit(p.x), v = key_logit(q.x);
-          unsure = !(u - v > 2.f * err + U32 * (fabsf(u) + fabsf(v))) &&
-                   !(sc.l[p.y] == sc.l[q.y] && __ldg(a.bias + p.y) == __ldg(a.bias + q.y));
-        }
+        const uint32_t p = cand_key(sc.sel[lane]), q = cand_key(sc.sel[lane + 1]);
+        const float x = key_logit(p), y = key_logit(q);
+        near = q > MASKED && !(x - y > 2.f * err + U32 * (fabsf(x) + fabsf(y)));
       }
-      if (__any_sync(0xffffffffu, unsure)) {
-        const double z = a.softmax ? softmax_sum_d(sc.l, usable, m) : 1.0;
-        double mine[CAND / 32];
-#pragma unroll
-        for (int h = 0; h < CAND / 32; ++h) {
-          mine[h] = -INFINITY;
-          if (lane + 32 * h < C) {
-            const uint2 c = sc.cand[lane + 32 * h];
-            if (c.x > 1u) mine[h] = score_d(sc.l[c.y], a.softmax, m, z) + (double)__ldg(a.bias + c.y);
-          }
-        }
-        int rank[CAND / 32] = {0, 0};
-        for (int q = 0; q < C; ++q) {
-          const double o = __shfl_sync(0xffffffffu, q < 32 ? mine[0] : mine[1], q & 31);
-          const uint32_t oe = sc.cand[q].y;
-#pragma unroll
-          for (int h = 0; h < CAND / 32; ++h)
-            if (lane + 32 * h < C) {
-              const uint32_t e = sc.cand[lane + 32 * h].y;
-              rank[h] += (o > mine[h] || (o == mine[h] && oe < e)) ? 1 : 0;
-            }
-        }
-        __syncwarp();
-#pragma unroll
-        for (int h = 0; h < CAND / 32; ++h)
-          if (lane + 32 * h < C && rank[h] < a.k) sc.sel[rank[h]] = sc.cand[lane + 32 * h];
-        __syncwarp();
-      }
+      if (__any_sync(0xffffffffu, near)) order_exact(a, t, sc, C, near);
     }
     // weights: without groups or a bias the k largest softmax scores sum to k / E at least, above the clamp, and the
     // softmax's own sum divides out
     const bool has = lane < a.k;
-    const uint2 me = sc.sel[has ? lane : 0];
+    const uint64_t me = sc.sel[has ? lane : 0];
     float p = 0.f;
-    if (has && me.x > 1u) {
-      const float x = sc.l[me.y];
-      p = a.softmax ? expf(x - m) : 1.f / (1.f + expf(-x));
-    }
-    if (a.softmax && (VALUES || !a.renorm)) {
-      if constexpr (!VALUES) {
-        float z = 0.f;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) z += usable >> j & 1 ? __expf(sc.l[lane + 32 * j] - m) : 0.f;
-        z = warp_sum(z);
-        inv_z = z > 0.f ? 1.f / z : 1.f;
-      }
-      p *= inv_z;
+    if (has && cand_key(me) > MASKED) {
+      const float x = fminf(load1(a.logits, row - lane + cand_id(me), a.type), FLT_MAX);
+      p = a.softmax ? expf(x - m) * inv_z : __fdividef(1.f, 1.f + expf(-x));
     }
     const float sum = a.renorm ? fmaxf(warp_sum(p), SUM_MIN) : 1.f;
     if (has) {
-      a.ids[(int64_t)t * a.k + lane] = (int)me.y;
-      a.weights[(int64_t)t * a.k + lane] = p / sum * a.scale;
+      a.ids[(int64_t)t * a.k + lane] = cand_id(me);
+      a.weights[(int64_t)t * a.k + lane] = __fdividef(p, sum) * a.scale;
     }
     __syncwarp();
   }
@@ -522,7 +588,7 @@ cudaError_t launch_select(const strata_select_t& sel, const void* logits, int T,
                      sel.logits_type, sel.scale, sel.n_expert / sel.n_group,
                      ((1 << 20) + sel.n_expert / sel.n_group - 1) / (sel.n_expert / sel.n_group)};
   const bool values = bias || sel.n_group > 1;
-  const int warp_bytes = (int)select_warp_bytes(sel.n_expert, sel.n_group, values);
+  const int warp_bytes = (int)sizeof(SelectScratch) + (bias ? (int)sizeof(double) * EMAX : 0);
   // a warp takes ceil(T / what fits the GPU) tokens, so that all end together
   const int fit = 152 * 5 * SEL_WARPS, turns = (T + fit - 1) / fit;
   const int warps = (T + turns - 1) / turns, grid = (warps + SEL_WARPS - 1) / SEL_WARPS;
