@@ -92,11 +92,23 @@ def test_ranks(rank):
     Case([300], [1], rank, 640, 640, qre.BF16, qre.F32).check()
 
 
+LONG = ([200, 0, 130, 128, 1, 127, 70, 300], [3, 0, 1, -1, 2, 4, 2, 0])
+
+
+@pytest.mark.parametrize("xk,yk", list(itertools.product(KINDS, KINDS)))
+@pytest.mark.parametrize("rank", [8, 16, 40, 64, 72, 128])
+def test_long_segments(xk, yk, rank):
+    Case(*LONG, rank, 520, 392, xk, yk, before=1, after=3).check()
+    Case([129, 300], [1, 1], rank, 2560, 1096, xk, yk, base=False).check()
+    Case(*LONG, rank, 64, 2560, xk, yk, inplace=True, pad=8).check()
+
+
 @pytest.mark.parametrize("d_in,d_out", [(8, 8), (8, 2560), (2560, 8), (24, 40), (248, 256), (264, 1032), (2552, 520), (5120, 24),
                                         (16384, 16), (16, 16384)])
 def test_widths(d_in, d_out):
     Case(*RAGGED, 16, d_in, d_out).check()
     Case([70], [0], 32, d_in, d_out, qre.F16, qre.BF16).check()
+    Case([70, 200], [0, 4], 24, d_in, d_out).check()
 
 
 @pytest.mark.parametrize("lens,of", [
