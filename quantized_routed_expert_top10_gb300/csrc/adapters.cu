@@ -37,33 +37,36 @@ struct Tile {
   int row, rows, adapter;
 };
 
-// Tile number `want` of the segments cut into tiles of `height` tokens, found by the whole CTA; false if there is
-// none or the segments are not valid (recorded in the status word).  Every CTA checks all segments, so either all
-// work or none does.
-__device__ bool find_tile(const AdapterArgs& a, int want, int height, Tile* out) {
+// The segments cut into tiles of `height` tokens, a thread's share of them: the whole CTA calls both.
+struct Segments {
+  int s0, s1;     // this thread's segments
+  int at, count;  // their first tile, and how many
+  int total;      // tiles of all segments; -1: the segments are not valid (recorded in the status word)
+};
+
+// Every CTA checks all segments, so either all work or none does.
+__device__ Segments cut_segments(const AdapterArgs& a, int height) {
   __shared__ int s_warp[AD_WARPS];
-  __shared__ int s_tile[3];
   __shared__ int s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) {
-    s_bad = 0;
-    s_tile[1] = 0;
-  }
+  if (tid == 0) s_bad = 0;
   __syncthreads();
   const int per = (a.n_seg + AD_THREADS - 1) / AD_THREADS;
-  const int s0 = min(tid * per, a.n_seg), s1 = min(s0 + per, a.n_seg);
-  int count = 0;
+  Segments g;
+  g.s0 = min(tid * per, a.n_seg);
+  g.s1 = min(g.s0 + per, a.n_seg);
+  g.count = 0;
   bool bad = false;
-  for (int s = s0; s < s1; ++s) {
+  for (int s = g.s0; s < g.s1; ++s) {
     const int lo = __ldg(a.seg_off + s), hi = __ldg(a.seg_off + s + 1), ad = __ldg(a.seg_adapter + s);
     if (lo < 0 || hi < lo || hi > a.T || ad < -1 || ad >= a.n_adapter) {
       bad = true;
       break;
     }
-    count += (hi - lo + height - 1) / height;
+    g.count += (hi - lo + height - 1) / height;
   }
   if (bad) s_bad = 1;
-  int v = count;
+  int v = g.count;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int n = __shfl_up_sync(0xffffffffu, v, o);
@@ -71,14 +74,27 @@ __device__ bool find_tile(const AdapterArgs& a, int want, int height, Tile* out)
   }
   if (lane == 31) s_warp[warp] = v;
   __syncthreads();
+  g.at = v - g.count;
+  g.total = 0;
+#pragma unroll
+  for (int w = 0; w < AD_WARPS; ++w) {
+    if (w < warp) g.at += s_warp[w];
+    g.total += s_warp[w];
+  }
   if (s_bad) {
     if (tid == 0) set_status(a.status, ST_CORRUPT);
-    return false;
+    g.total = -1;
   }
-  int at = v - count;  // tiles before this thread's segments
-  for (int w = 0; w < warp; ++w) at += s_warp[w];
-  if (want >= at && want < at + count) {
-    for (int s = s0; s < s1; ++s) {
+  return g;
+}
+
+// Tile `want` of [0, total).
+__device__ Tile tile_at(const AdapterArgs& a, const Segments& g, int want, int height) {
+  __shared__ int s_tile[3];
+  __syncthreads();  // the tile before this one has been read
+  if (want >= g.at && want < g.at + g.count) {
+    int at = g.at;
+    for (int s = g.s0; s < g.s1; ++s) {
       const int lo = __ldg(a.seg_off + s), hi = __ldg(a.seg_off + s + 1);
       const int n = (hi - lo + height - 1) / height;
       if (want < at + n) {
@@ -91,8 +107,15 @@ __device__ bool find_tile(const AdapterArgs& a, int want, int height, Tile* out)
     }
   }
   __syncthreads();
-  *out = Tile{s_tile[0], s_tile[1], s_tile[2]};
-  return out->rows > 0;
+  return Tile{s_tile[0], s_tile[1], s_tile[2]};
+}
+
+// The CTA's one tile; false if there is none.
+__device__ bool find_tile(const AdapterArgs& a, int want, int height, Tile* out) {
+  const Segments g = cut_segments(a, height);
+  if (want >= g.total) return false;
+  *out = tile_at(a, g, want, height);
+  return true;
 }
 
 // D (16 x 8, fp32) += A (16 x 16, bf16) * B (16 x 8, bf16).
@@ -282,14 +305,45 @@ __global__ void __launch_bounds__(AD_THREADS) expand_kernel(AdapterArgs a) {
 }
 
 // ---- Tiles of up to 128 tokens on the 5th-generation tensor cores -----------------------------------------
-// Operands go through registers into the tensor cores' K-major shared-memory layout, 16 bytes a thread, so that one kernel
-// serves all three types (a wider activation leaves as its bf16 terms) and any row stride.  TMEM is allocated after
+// Operands are copied 16 bytes a thread into the tensor cores' K-major shared-memory layout (cp.async; an fp16 or fp32 x
+// by registers, which split it into its bf16 terms), so one kernel serves any row stride.  TMEM is allocated after
 // griddep_wait and before the next kernel may start, so no CTA holds it while it waits for another.
 constexpr int TC_ROWS = 128;
 constexpr uint32_t TC_TILE = TC_ROWS * 128;  // 128 rows of 64 bf16
+constexpr int AD_ROW = 144;                  // pitch of a row of 128 bytes of y (16-byte accesses by rows: no bank twice)
+constexpr uint32_t AD_REGION = 32 * AD_ROW;  // a warp's part of a unit: 32 rows
 
 __host__ __device__ __forceinline__ uint32_t idesc_bf16(int M, int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__host__ __device__ constexpr int bf16_terms(int type) { return type == STRATA_F32 ? 3 : type == STRATA_F16 ? 2 : 1; }
+// terms of A x: 16 bits for a 16-bit y, 24 for fp32
+__host__ __device__ constexpr int v_terms(int y_type) { return y_type == STRATA_F32 ? 3 : 2; }
+
+// 16 bytes global -> shared, or zeros.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All of this thread's copy groups but the last n have arrived.
+__device__ __forceinline__ void copy_wait(int n) {
+  if (n >= 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Four floats of shared memory of CTA `rank` of the cluster, at the address that this CTA's `p` has there.
+__device__ __forceinline__ float4 cluster_ld4(const void* p, int rank) {
+  uint32_t at;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
 }
 
 // A wait that ran out is recorded; the CTA's later waits are then skipped (the call's result is void).
@@ -301,26 +355,13 @@ struct Waiter {
   }
 };
 
-// The eight values of a 16-byte (fp32: 32-byte) piece as TERMS bf16 pieces.
-template <int TERMS>
-__device__ __forceinline__ void put_terms(const Raw8& r, int type, uint8_t* tile, uint32_t tile_step, uint32_t off) {
-  if constexpr (TERMS == 1) {
-    *reinterpret_cast<uint4*>(tile + off) = r.lo;
-  } else {
-    float f[8];
-    uint32_t t[TERMS][4];
-    widen8(r, type, f);
-    split8<TERMS>(f, t);
-#pragma unroll
-    for (int i = 0; i < TERMS; ++i)
-      *reinterpret_cast<uint4*>(tile + i * tile_step + off) = make_uint4(t[i][0], t[i][1], t[i][2], t[i][3]);
-  }
-}
-
-// v[slice][token][r] for a tile of up to 128 tokens: D[128 x rank] in TMEM, 64 k a stage.
-template <int TERMS>
-__global__ void __launch_bounds__(AD_THREADS, 2) shrink_tc_kernel(AdapterArgs a, int np, int stages) {
-  constexpr int AHEAD = TERMS == 3 ? 1 : 2;  // stages on their way in registers
+// scale A_a x of a tile of up to 128 tokens, as bf16 terms vt[term][token][r].  One cluster a tile: each CTA takes a slice of
+// d_in, 64 k a stage, into a [128 x rank] accumulator in TMEM; the slices are then added in order over the cluster's
+// shared memory, each CTA finishing its share of the rows.
+template <int XT>
+__global__ void __launch_bounds__(AD_THREADS, XT == STRATA_F32 ? 2 : 3) shrink_tc_kernel(AdapterArgs a, int np, int stages) {
+  constexpr int TERMS = bf16_terms(XT);
+  constexpr int AHEAD = 2;  // stages of x on their way in registers (TERMS > 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   __shared__ uint64_t s_empty[4], s_done;
@@ -328,6 +369,7 @@ __global__ void __launch_bounds__(AD_THREADS, 2) shrink_tc_kernel(AdapterArgs a,
   __shared__ int s_dead;
   Tile tile;
   griddep_wait();
+  // (the same for all CTAs of a cluster)
   if (!find_tile(a, blockIdx.x, TC_ROWS, &tile) || tile.adapter < 0) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t cols = np <= 32 ? 32 : np <= 64 ? 64 : 128;
@@ -346,24 +388,43 @@ __global__ void __launch_bounds__(AD_THREADS, 2) shrink_tc_kernel(AdapterArgs a,
   const int blocks = k0 < k1 ? (k1 - k0 + 63) / 64 : 0;
   const int chunk = tid & 7, row0 = tid >> 3;
   const uint32_t stage_bytes = TERMS * TC_TILE + (uint32_t)np * 128;
-  const Raw8 zero{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-  struct Piece {
-    Raw8 x[4];
-    uint4 w[4];
-  };
-  Piece piece[AHEAD];
-  const auto fetch = [&](int kb, Piece& p) {
-    const int k = k0 + 64 * kb + 8 * chunk;
-    const bool in = k < k1;
+  const int64_t x_size = XT == STRATA_F32 ? 4 : 2;
+  const char* X = static_cast<const char*>(a.x) + ((int64_t)(tile.row + row0) * a.x_stride + k0 + 8 * chunk) * x_size;
+  const uint16_t* W = A + (int64_t)row0 * a.d_in + k0 + 8 * chunk;
+  // what goes by cp.async of k-block kb: A, and a bf16 x
+  const auto copy = [&](int kb) {
+    if (kb < blocks) {
+      uint8_t* at = smem + (kb % stages) * stage_bytes;
+      const bool in = k0 + 64 * kb + 8 * chunk < k1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = row0 + 32 * i;
-      p.x[i] = in && r < tile.rows ? load8(a.x, (int64_t)(tile.row + r) * a.x_stride + k, a.x_type) : zero;
-      if (32 * i < np) p.w[i] = in && r < a.rank ? __ldg(reinterpret_cast<const uint4*>(A + (int64_t)r * a.d_in + k)) : zero.lo;
+      for (int j = 0; j < 4; ++j) {
+        const int r = row0 + 32 * j;
+        const uint32_t off = tc::swz_off(r, chunk);
+        if (TERMS == 1) {
+          const bool ok = in && r < tile.rows;
+          copy16(at + off, ok ? X + (32 * j * a.x_stride + 64 * kb) * x_size : static_cast<const char*>(a.x), ok);
+        }
+        if (r < np) {
+          const bool ok = in && r < a.rank;
+          copy16(at + TERMS * TC_TILE + off, ok ? W + (int64_t)32 * j * a.d_in + 64 * kb : A, ok);
+        }
+      }
     }
+    copy_commit();
   };
+  const Raw8 zero{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  Raw8 piece[AHEAD][4];
+  const auto fetch = [&](int kb, Raw8 (&p)[4]) {
+    const bool in = k0 + 64 * kb + 8 * chunk < k1;
 #pragma unroll
-  for (int i = 0; i < AHEAD; ++i) fetch(i, piece[i]);
+    for (int j = 0; j < 4; ++j)
+      p[j] = in && row0 + 32 * j < tile.rows ? load8(X + (32 * j * a.x_stride + 64 * kb) * x_size, 0, XT) : zero;
+  };
+  if (TERMS > 1) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) fetch(i, piece[i]);
+  }
+  for (int i = 0; i < stages - 1; ++i) copy(i);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -371,22 +432,27 @@ __global__ void __launch_bounds__(AD_THREADS, 2) shrink_tc_kernel(AdapterArgs a,
   const uint32_t tmem = s_tmem;
   const uint32_t idesc = idesc_bf16(TC_ROWS, np);
   const Waiter waiter{a.status, &s_dead};
-  int stage = 0;
-  uint32_t turn = 0;
   for (int kb0 = 0; kb0 < blocks; kb0 += AHEAD) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       const int kb = kb0 + i;
       if (kb >= blocks) break;
-      uint8_t* at = smem + stage * stage_bytes;
-      if (turn) waiter.wait(&s_empty[stage], (turn - 1) & 1);
+      uint8_t* at = smem + (kb % stages) * stage_bytes;
+      if (TERMS > 1) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t off = tc::swz_off(row0 + 32 * j, chunk);
-        put_terms<TERMS>(piece[i].x[j], a.x_type, at, TC_TILE, off);
-        if (row0 + 32 * j < np) *reinterpret_cast<uint4*>(at + TERMS * TC_TILE + off) = piece[i].w[j];
+        for (int j = 0; j < 4; ++j) {
+          float f[8];
+          uint32_t t[TERMS][4];
+          widen8(piece[i][j], XT, f);
+          split8<TERMS>(f, t);
+#pragma unroll
+          for (int e = 0; e < TERMS; ++e)
+            *reinterpret_cast<uint4*>(at + e * TC_TILE + tc::swz_off(row0 + 32 * j, chunk)) =
+                make_uint4(t[e][0], t[e][1], t[e][2], t[e][3]);
+        }
+        fetch(kb + AHEAD, piece[i]);
       }
-      fetch(kb + AHEAD, piece[i]);
+      copy_wait(stages - 2);
       tc::fence_proxy_async_smem();
       __syncthreads();
       if (tid == 0) {
@@ -399,53 +465,86 @@ __global__ void __launch_bounds__(AD_THREADS, 2) shrink_tc_kernel(AdapterArgs a,
           for (int kk = 0; kk < 4; ++kk)
             tc::mma_f16(tmem, ad + 2 * kk, bd + 2 * kk, idesc, (kb > 0 || t < TERMS - 1 || kk > 0) ? 1u : 0u);
         }
-        tc::mma_commit(&s_empty[stage]);
+        tc::mma_commit(&s_empty[kb % stages]);
       }
-      if (++stage == stages) {
-        stage = 0;
-        ++turn;
-      }
+      // the stage of k-block kb - 1 is free once its MMAs are done
+      if (kb > 0) waiter.wait(&s_empty[(kb - 1) % stages], ((kb - 1) / stages) & 1);
+      copy(kb + stages - 1);
     }
   }
+  copy_wait(0);
   if (tid == 0) tc::mma_commit(&s_done);
   waiter.wait(&s_done, 0);
   tc::fence_after_sync();
-  // rows: the warp's TMEM quadrant; columns: warps 0-3 the even 16, warps 4-7 the odd
-  const int row = 32 * (warp & 3) + lane;
-  float* v = a.v + ((int64_t)blockIdx.y * a.T + tile.row + row) * a.rank;
-  for (int c = 16 * (warp >> 2); c < np; c += 32) {
-    float f[16];
-    tc::tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)c, f);
-    if (row < tile.rows)
+  __syncthreads();  // all have seen the last MMA: the stages are free for the sums
+  const int pitch = np + 4;
+  float* const part = reinterpret_cast<float*>(smem);
+  {
+    // rows: the warp's TMEM quadrant; columns: warps 0-3 the even 16, warps 4-7 the odd
+    const int row = 32 * (warp & 3) + lane;
+    for (int c = 16 * (warp >> 2); c < np; c += 32) {
+      float f[16];
+      tc::tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)c, f);
 #pragma unroll
       for (int i = 0; i < 16; i += 4)
-        if (c + i < a.rank)
-          *reinterpret_cast<float4*>(v + c + i) =
-              blocks ? make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(part + row * pitch + c + i) =
+            blocks ? make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
   }
   tc::fence_before_sync();
-  __syncthreads();
+  cluster_sync();
   if (warp == 0) tc::tmem_dealloc(tmem, cols);
+  const float sc = a.scale ? __ldg(a.scale + tile.adapter) : 1.f;
+  const int chunks = a.rank >> 3, vt = v_terms(a.y_type);
+  // the cluster's CTAs share the tile's rows x 8 columns out among their threads
+  for (int at = blockIdx.y * AD_THREADS + tid; at < tile.rows * chunks; at += a.split * AD_THREADS) {
+    const int row = at / chunks, c = 8 * (at - row * chunks);
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < a.split; ++s) {
+      const float4 u0 = cluster_ld4(part + row * pitch + c, s), u1 = cluster_ld4(part + row * pitch + c + 4, s);
+      f[0] += u0.x; f[1] += u0.y; f[2] += u0.z; f[3] += u0.w;
+      f[4] += u1.x; f[5] += u1.y; f[6] += u1.z; f[7] += u1.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= sc;
+    uint32_t t[3][4];
+    split8<3>(f, t);
+    uint16_t* out = reinterpret_cast<uint16_t*>(a.v) + (int64_t)(tile.row + row) * a.rank + c;
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+      if (e < vt) *reinterpret_cast<uint4*>(out + (int64_t)e * a.T * a.rank) = make_uint4(t[e][0], t[e][1], t[e][2], t[e][3]);
+  }
+  cluster_sync();  // no CTA leaves while another reads its sums
 }
 
-// y = base + B_a (scale v) for a tile of up to 128 tokens and `blocks` blocks of 128 columns.  The tile's scaled v (its
-// bf16 terms) stays in shared memory; a block's product is in one of two TMEM accumulators while the block before it is
-// read back, turned to rows of 8 consecutive columns a thread through shared memory, added to base and stored.
-template <int TERMS>
-__global__ void __launch_bounds__(AD_THREADS, 2) expand_tc_kernel(AdapterArgs a, int blocks_per_cta) {
+// y = base + B_a (scale A_a x).  The work is one line of units, CW columns of a tile of up to 128 tokens each, of which every
+// CTA (one an SM) takes an equal stretch.  A tile's scaled A_a x (its bf16 terms) stays in shared memory; B and base of
+// the units ahead are on their way by cp.async, into a ring; a unit's product is in one of two TMEM accumulators while
+// the unit before it is read back, a row a thread, and added to base in shared memory, from where the warp stores it.
+template <int YT>
+__global__ void __launch_bounds__(AD_THREADS, 1) expand_tc_kernel(AdapterArgs a, int ring) {
+  constexpr int TERMS = v_terms(YT);
+  constexpr int SIZE = YT == STRATA_F32 ? 4 : 2;
+  constexpr int HALF = 128 / SIZE, CW = 2 * HALF;  // columns of a warp: 128 bytes of y
+  constexpr int EL = 16 / SIZE;                    // elements of 16 bytes
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   __shared__ uint64_t s_full[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_dead;
-  Tile tile;
   griddep_wait();
-  if (!find_tile(a, blockIdx.x, TC_ROWS, &tile)) return;
-  if (tile.adapter < 0 && a.base == a.y) return;
+  const Segments g = cut_segments(a, TC_ROWS);
+  const int col_blocks = (a.d_out + CW - 1) / CW;
+  const int units = g.total * col_blocks;  // at most 2 * 8,192 tiles of 256
+  const int u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
+  int u = (int)((int64_t)units * blockIdx.x / gridDim.x);
+  if (u >= u1) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool product = tile.adapter >= 0;
-  if (warp == 0 && product) {
-    tc::tmem_alloc(&s_tmem, 256);
+  if (warp == 0) {
+    tc::tmem_alloc(&s_tmem, 2 * CW);
     tc::tmem_relinquish();
   }
   if (tid == 32) {
@@ -454,140 +553,137 @@ __global__ void __launch_bounds__(AD_THREADS, 2) expand_tc_kernel(AdapterArgs a,
     s_dead = 0;
     fence_mbar_init();
   }
-  const int kblocks = (a.rank + 63) / 64, ksteps = (a.rank + 15) / 16, chunks = 2 * ksteps;
-  uint8_t* const sv = smem;                                  // [TERMS][kblocks] tiles
-  uint8_t* const sb = sv + TERMS * kblocks * TC_TILE;        // [2][kblocks] tiles
-  uint8_t* const stage = sb + 2 * kblocks * TC_TILE + warp * 4096;  // 32 rows x 32 fp32
-  const uint16_t* B = a.b + (int64_t)max(tile.adapter, 0) * a.b_stride;
-  const int first = blockIdx.y * blocks_per_cta;
-  const int blocks = min(blocks_per_cta, (a.d_out + 127) / 128 - first);
-  // the block's B rows (columns of y), 16 bytes a thread and turn
-  uint4 w[8];
-  const auto fetch_b = [&](int blk) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (256 * i >= 128 * chunks) break;
-      const int at = tid + 256 * i, r = at / chunks, c = at - r * chunks;
-      const int col = 128 * (first + blk) + r, k = 8 * c;
-      w[i] = product && blk < blocks && col < a.d_out && k < a.rank
-                 ? __ldg(reinterpret_cast<const uint4*>(B + (int64_t)col * a.rank + k))
-                 : make_uint4(0u, 0u, 0u, 0u);
-    }
-  };
-  // base of the warp's next 32 x 32 piece (8 columns of 4 rows a lane)
-  const int q = warp & 3, half = warp >> 2;
-  const int prow = 32 * q + (lane >> 2), pcol = 64 * half + 8 * (lane & 3);
-  const Raw8 zero{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-  Raw8 base[4];
-  const auto fetch_base = [&](int blk, int sub) {
-    const int col = 128 * (first + blk) + 32 * sub + pcol;
-    const bool in = a.base && blk < blocks && col < a.d_out;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = prow + 8 * i;
-      base[i] = in && r < tile.rows ? load8(a.base, (int64_t)(tile.row + r) * a.base_stride + col, a.y_type) : zero;
-    }
-  };
-  fetch_b(0);
-  fetch_base(0, 0);
-  if (product) {
-    const float sc = a.scale ? __ldg(a.scale + tile.adapter) : 1.f;
-    for (int at = tid; at < TC_ROWS * chunks; at += AD_THREADS) {
-      const int r = at / chunks, c = at - r * chunks, k = 8 * c;
-      float f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = 0.f;
-      if (r < tile.rows && k < a.rank)
-        for (int s = 0; s < a.split; ++s) {
-          const float4* p = reinterpret_cast<const float4*>(a.v + ((int64_t)s * a.T + tile.row + r) * a.rank + k);
-          const float4 u0 = __ldcg(p), u1 = __ldcg(p + 1);
-          f[0] += u0.x; f[1] += u0.y; f[2] += u0.z; f[3] += u0.w;
-          f[4] += u1.x; f[5] += u1.y; f[6] += u1.z; f[7] += u1.w;
-        }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] *= sc;
-      uint32_t t[TERMS][4];
-      split8<TERMS>(f, t);
-      const uint32_t off = (uint32_t)(c >> 3) * TC_TILE + tc::swz_off(r, c & 7);
-#pragma unroll
-      for (int i = 0; i < TERMS; ++i)
-        *reinterpret_cast<uint4*>(sv + i * kblocks * TC_TILE + off) = make_uint4(t[i][0], t[i][1], t[i][2], t[i][3]);
-    }
-  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   griddep_launch_dependents();
-  const uint32_t tmem = product ? s_tmem : 0u;
-  const uint32_t idesc = idesc_bf16(TC_ROWS, 128);
+  const uint32_t tmem = s_tmem;
+  const int kblocks = (a.rank + 63) / 64, ksteps = (a.rank + 15) / 16;
+  const uint32_t b_tile = CW * 128, b_slot = kblocks * b_tile;
+  uint8_t* const sv = smem;                                   // [TERMS][kblocks] tiles
+  uint8_t* const sb = sv + TERMS * kblocks * TC_TILE;         // [ring][kblocks] tiles of CW rows
+  uint8_t* const region = sb + ring * b_slot + warp * ring * AD_REGION;  // [ring] of this warp
+  const uint32_t idesc = idesc_bf16(TC_ROWS, CW);
   const Waiter waiter{a.status, &s_dead};
-  for (int blk = 0; blk <= blocks; ++blk) {
-    if (product && blk < blocks) {
-      uint8_t* const tb = sb + (blk & 1) * kblocks * TC_TILE;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (256 * i >= 128 * chunks) break;
-        const int at = tid + 256 * i, r = at / chunks, c = at - r * chunks;
-        if (r < 128) *reinterpret_cast<uint4*>(tb + (uint32_t)(c >> 3) * TC_TILE + tc::swz_off(r, c & 7)) = w[i];
-      }
-      fetch_b(blk + 1);
-      tc::fence_proxy_async_smem();
-      tc::fence_before_sync();  // this thread's reads of the accumulator two blocks back
-      __syncthreads();
-      if (tid == 0) {
-        tc::fence_after_sync();
-        for (int t = TERMS - 1; t >= 0; --t)
-          for (int kk = 0; kk < ksteps; ++kk) {
-            const uint64_t ad = tc::smem_desc_sw128(smem_u32(sv + (t * kblocks + (kk >> 2)) * TC_TILE));
-            const uint64_t bd = tc::smem_desc_sw128(smem_u32(tb + (kk >> 2) * TC_TILE));
-            tc::mma_f16(tmem + 128u * (blk & 1), ad + 2 * (kk & 3), bd + 2 * (kk & 3), idesc,
-                        (t < TERMS - 1 || kk > 0) ? 1u : 0u);
+  const uint16_t* vt = reinterpret_cast<const uint16_t*>(a.v);
+  // the warp's part of a unit: TMEM quadrant q (32 tokens), HALF columns
+  const int q = warp & 3, half = warp >> 2;
+  int n = 0;  // units with a product so far: the next one's accumulator and barrier phase
+  while (u < u1) {
+    const int first = u % col_blocks, blocks = min(col_blocks - first, u1 - u);
+    const Tile tile = tile_at(a, g, u / col_blocks, TC_ROWS);
+    u += blocks;
+    const bool product = tile.adapter >= 0;
+    if (!product && a.base == a.y) continue;
+    const uint16_t* B = a.b + (int64_t)max(tile.adapter, 0) * a.b_stride;
+    const char* base = static_cast<const char*>(a.base);
+    // B (rows: columns of y, 2 or 4 threads each) and the warp's base of unit blk
+    const auto copy = [&](int blk) {
+      if (blk < blocks) {
+        const int c0 = CW * (first + blk), slot = blk % ring;
+        if (product) {
+          constexpr int PER = AD_THREADS / CW;  // threads a row
+          const int r = tid / PER, col = c0 + r;
+          for (int c = tid % PER; c < 2 * ksteps; c += PER) {
+            const bool ok = col < a.d_out && 8 * c < a.rank;
+            copy16(sb + slot * b_slot + (c >> 3) * b_tile + tc::swz_off(r, c & 7),
+                   ok ? B + (int64_t)col * a.rank + 8 * c : B, ok);
           }
-        tc::mma_commit(&s_full[blk & 1]);
+        }
+        const int col = c0 + HALF * half + EL * (lane & 7);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3), row = 32 * q + r;
+          const bool ok = base && row < tile.rows && col < a.d_out;
+          copy16(region + slot * AD_REGION + r * AD_ROW + 16 * (lane & 7),
+                 ok ? base + ((int64_t)(tile.row + row) * a.base_stride + col) * SIZE : static_cast<const char*>(a.y), ok);
+        }
       }
-    }
-    if (blk == 0) continue;
-    const int b = blk - 1;
+      copy_commit();
+    };
     if (product) {
-      waiter.wait(&s_full[b & 1], (b >> 1) & 1);
-      tc::fence_after_sync();
-      __syncwarp();
+      const int r = tid >> 1;
+      for (int e = 0; e < TERMS; ++e)
+        for (int c = tid & 1; c < 2 * ksteps; c += 2) {
+          const bool ok = r < tile.rows && 8 * c < a.rank;
+          copy16(sv + (e * kblocks + (c >> 3)) * TC_TILE + tc::swz_off(r, c & 7),
+                 ok ? vt + ((int64_t)e * a.T + tile.row + r) * a.rank + 8 * c : vt, ok);
+        }
     }
+    for (int i = 0; i < ring - 1; ++i) copy(i);
+    for (int blk = 0; blk <= blocks; ++blk) {
+      if (blk < blocks) {
+        copy_wait(ring - 2);
+        tc::fence_proxy_async_smem();
+        tc::fence_before_sync();  // this thread's reads of the accumulator two units back
+        __syncthreads();
+        if (product && tid == 0) {
+          tc::fence_after_sync();
+          const int acc = (n + blk) & 1;
+          for (int t = TERMS - 1; t >= 0; --t)
+            for (int kk = 0; kk < ksteps; ++kk) {
+              const uint64_t ad = tc::smem_desc_sw128(smem_u32(sv + (t * kblocks + (kk >> 2)) * TC_TILE));
+              const uint64_t bd = tc::smem_desc_sw128(smem_u32(sb + (blk % ring) * b_slot + (kk >> 2) * b_tile));
+              tc::mma_f16(tmem + (uint32_t)(CW * acc), ad + 2 * (kk & 3), bd + 2 * (kk & 3), idesc,
+                          (t < TERMS - 1 || kk > 0) ? 1u : 0u);
+            }
+          tc::mma_commit(&s_full[acc]);
+        }
+      }
+      if (blk > 0) {
+        const int b = blk - 1, acc = (n + b) & 1;
+        uint8_t* const reg = region + (b % ring) * AD_REGION;
+        if (product) {
+          waiter.wait(&s_full[acc], ((n + b) >> 1) & 1);
+          tc::fence_after_sync();
+          __syncwarp();
+          uint8_t* const mine = reg + lane * AD_ROW;
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
-      if (product) {
-        uint32_t u[2][16];
-        const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + 128u * (b & 1) + 64u * half + 32u * sub;
-        tc::tmem_ld16_async(at, u[0]);
-        tc::tmem_ld16_async(at + 16, u[1]);
-        tc::tmem_wait_ld();
+          for (int h = 0; h < HALF; h += 32) {
+            uint32_t d[2][16];
+            const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(CW * acc + HALF * half + h);
+            tc::tmem_ld16_async(at, d[0]);
+            tc::tmem_ld16_async(at + 16, d[1]);
+            tc::tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-              make_uint4(u[c >> 2][4 * (c & 3)], u[c >> 2][4 * (c & 3) + 1], u[c >> 2][4 * (c & 3) + 2], u[c >> 2][4 * (c & 3) + 3]);
+            for (int c = 0; c < 32; c += EL) {
+              uint4* const p = reinterpret_cast<uint4*>(mine + (h + c) * SIZE);
+              uint4 w = *p;
+              uint32_t* const we = &w.x;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (SIZE == 4) {
+                  we[e] = __float_as_uint(__uint_as_float(we[e]) + __uint_as_float(d[(c + e) >> 4][(c + e) & 15]));
+                } else {
+                  const int i = c + 2 * e;
+                  const float2 f = widen2(we[e], YT);
+                  we[e] = narrow2(f.x + __uint_as_float(d[i >> 4][i & 15]), f.y + __uint_as_float(d[i >> 4][(i & 15) + 1]), YT);
+                }
+              }
+              *p = w;
+            }
+          }
+          __syncwarp();
+        }
+        const int col = CW * (first + b) + HALF * half + EL * (lane & 7);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3), row = 32 * q + r;
+          const uint4 w = *reinterpret_cast<const uint4*>(reg + r * AD_ROW + 16 * (lane & 7));
+          if (row < tile.rows && col < a.d_out)
+            *reinterpret_cast<uint4*>(static_cast<char*>(a.y) + ((int64_t)(tile.row + row) * a.y_stride + col) * SIZE) = w;
+        }
         __syncwarp();
       }
-      const int col = 128 * (first + b) + 32 * sub + pcol;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int rr = (lane >> 2) + 8 * i, r = 32 * q + rr;
-        float f[8];
-        widen8(base[i], a.y_type, f);
-        if (product) {
-          const float4 d0 = *reinterpret_cast<const float4*>(stage + rr * 128 + (((2 * (lane & 3)) ^ (rr & 7)) << 4));
-          const float4 d1 = *reinterpret_cast<const float4*>(stage + rr * 128 + (((2 * (lane & 3) + 1) ^ (rr & 7)) << 4));
-          f[0] += d0.x; f[1] += d0.y; f[2] += d0.z; f[3] += d0.w;
-          f[4] += d1.x; f[5] += d1.y; f[6] += d1.z; f[7] += d1.w;
-        }
-        if (r < tile.rows && col < a.d_out) store8(a.y, (int64_t)(tile.row + r) * a.y_stride + col, a.y_type, f);
-      }
-      fetch_base(sub == 0 ? b : b + 1, sub ^ 1);
-      __syncwarp();
+      // into the slot of the unit just stored, whose product's MMAs this thread has waited for
+      if (blk < blocks) copy(blk + ring - 1);
     }
+    copy_wait(0);
+    if (product) n += blocks;
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 0 && product) tc::tmem_dealloc(tmem, 256);
+  if (warp == 0) tc::tmem_dealloc(tmem, 2 * CW);
 }
 
 template <int MT, int TERMS>
@@ -630,44 +726,62 @@ cudaError_t allow_smem(size_t bytes) {
 }
 constexpr size_t TC_SMEM_MAX = 226 * 1024;
 
-template <int TERMS>
+template <int XT>
 cudaError_t launch_shrink_tc(const AdapterArgs& a, int tiles, cudaStream_t s) {
-  cudaError_t err = allow_smem<shrink_tc_kernel<TERMS>>(TC_SMEM_MAX);
+  cudaError_t err = allow_smem<shrink_tc_kernel<XT>>(TC_SMEM_MAX);
   if (err != cudaSuccess) return err;
   const int np = (a.rank + 15) / 16 * 16;
-  const size_t stage = (size_t)TERMS * TC_TILE + (size_t)np * 128;
-  // two CTAs an SM
-  int stages = (int)((110 * 1024) / stage);
+  const size_t stage = (size_t)bf16_terms(XT) * TC_TILE + (size_t)np * 128;
+  const int ctas = XT == STRATA_F32 ? 2 : 3;  // an SM
+  int stages = (int)((226 * 1024 / ctas - 2048) / stage);
   stages = stages > 4 ? 4 : stages < 2 ? 2 : stages;
-  STRATA_LAUNCH(KID_ADAPTER_SHRINK, s,
-                err = launch_pdl(shrink_tc_kernel<TERMS>, dim3(tiles, a.split), AD_THREADS, stages * stage + 1024, s, a, np, stages));
+  const size_t sums = (size_t)TC_ROWS * (np + 4) * sizeof(float);  // take the stages' place
+  const size_t smem = (stages * stage > sums ? stages * stage : sums) + 1024;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(tiles, a.split);
+  cfg.blockDim = dim3(AD_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = a.split;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  STRATA_LAUNCH(KID_ADAPTER_SHRINK, s, err = cudaLaunchKernelEx(&cfg, shrink_tc_kernel<XT>, a, np, stages));
   return err;
 }
 
-template <int TERMS>
+template <int YT>
 cudaError_t launch_expand_tc(const AdapterArgs& a, int tiles, cudaStream_t s) {
-  cudaError_t err = allow_smem<expand_tc_kernel<TERMS>>(TC_SMEM_MAX);
+  cudaError_t err = allow_smem<expand_tc_kernel<YT>>(TC_SMEM_MAX);
   if (err != cudaSuccess) return err;
-  const int kblocks = (a.rank + 63) / 64, col_blocks = (a.d_out + 127) / 128;
-  const size_t smem = (size_t)(TERMS + 2) * kblocks * TC_TILE + AD_WARPS * 4096 + 1024;
-  int per = 1;
-  while (per < col_blocks && tiles * ((col_blocks + per - 1) / per) > 2 * 304) ++per;
-  const dim3 grid(tiles, (col_blocks + per - 1) / per);
-  STRATA_LAUNCH(KID_ADAPTER_EXPAND, s, err = launch_pdl(expand_tc_kernel<TERMS>, grid, AD_THREADS, smem, s, a, per));
+  const int cw = YT == STRATA_F32 ? 64 : 128;
+  const int kblocks = (a.rank + 63) / 64, units = tiles * ((a.d_out + cw - 1) / cw);
+  const size_t fixed = (size_t)v_terms(YT) * kblocks * TC_TILE + 1024;
+  const size_t slot = (size_t)kblocks * cw * 128 + AD_WARPS * AD_REGION;
+  const int ring = fixed + 3 * slot <= TC_SMEM_MAX ? 3 : 2;
+  STRATA_LAUNCH(KID_ADAPTER_EXPAND, s,
+                err = launch_pdl(expand_tc_kernel<YT>, dim3(units < 152 ? units : 152), AD_THREADS, fixed + ring * slot, s, a, ring));
   return err;
 }
 
 cudaError_t launch_tc(AdapterArgs a, cudaStream_t s) {
   const int tiles = a.T / TC_ROWS + (a.n_seg < a.T ? a.n_seg : a.T);
   int split = 1;
-  while (split < SPLIT_MAX && tiles * split < 228 && a.d_in / (2 * split) >= 256 && 2 * split * a.rank <= V_FLOATS) split *= 2;
+  while (split < SPLIT_MAX && 2 * tiles * split <= 152 * (a.x_type == STRATA_F32 ? 2 : 3) && a.d_in / (2 * split) >= 256) split *= 2;
   a.split = split;
   a.k_slice = ((a.d_in + split - 1) / split + 63) / 64 * 64;
-  const cudaError_t err = a.x_type == STRATA_BF16  ? launch_shrink_tc<1>(a, tiles, s)
-                          : a.x_type == STRATA_F16 ? launch_shrink_tc<2>(a, tiles, s)
-                                                   : launch_shrink_tc<3>(a, tiles, s);
+  const cudaError_t err = a.x_type == STRATA_BF16  ? launch_shrink_tc<STRATA_BF16>(a, tiles, s)
+                          : a.x_type == STRATA_F16 ? launch_shrink_tc<STRATA_F16>(a, tiles, s)
+                                                   : launch_shrink_tc<STRATA_F32>(a, tiles, s);
   if (err != cudaSuccess) return err;
-  return a.y_type == STRATA_F32 ? launch_expand_tc<3>(a, tiles, s) : launch_expand_tc<2>(a, tiles, s);
+  return a.y_type == STRATA_F32    ? launch_expand_tc<STRATA_F32>(a, tiles, s)
+         : a.y_type == STRATA_BF16 ? launch_expand_tc<STRATA_BF16>(a, tiles, s)
+                                   : launch_expand_tc<STRATA_F16>(a, tiles, s);
 }
 
 }  // namespace
