@@ -45,13 +45,15 @@ struct Segments {
 };
 
 // Every CTA checks all segments, so either all work or none does.
+template <int THREADS>
 __device__ Segments cut_segments(const AdapterArgs& a, int height) {
-  __shared__ int s_warp[AD_WARPS];
+  constexpr int WARPS = THREADS / 32;
+  __shared__ int s_warp[WARPS];
   __shared__ int s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) s_bad = 0;
   __syncthreads();
-  const int per = (a.n_seg + AD_THREADS - 1) / AD_THREADS;
+  const int per = (a.n_seg + THREADS - 1) / THREADS;
   Segments g;
   g.s0 = min(tid * per, a.n_seg);
   g.s1 = min(g.s0 + per, a.n_seg);
@@ -77,7 +79,7 @@ __device__ Segments cut_segments(const AdapterArgs& a, int height) {
   g.at = v - g.count;
   g.total = 0;
 #pragma unroll
-  for (int w = 0; w < AD_WARPS; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w < warp) g.at += s_warp[w];
     g.total += s_warp[w];
   }
@@ -112,7 +114,7 @@ __device__ Tile tile_at(const AdapterArgs& a, const Segments& g, int want, int h
 
 // The CTA's one tile; false if there is none.
 __device__ bool find_tile(const AdapterArgs& a, int want, int height, Tile* out) {
-  const Segments g = cut_segments(a, height);
+  const Segments g = cut_segments<AD_THREADS>(a, height);
   if (want >= g.total) return false;
   *out = tile_at(a, g, want, height);
   return true;
@@ -310,8 +312,10 @@ __global__ void __launch_bounds__(AD_THREADS) expand_kernel(AdapterArgs a) {
 // griddep_wait and before the next kernel may start, so no CTA holds it while it waits for another.
 constexpr int TC_ROWS = 128;
 constexpr uint32_t TC_TILE = TC_ROWS * 128;  // 128 rows of 64 bf16
-constexpr int AD_ROW = 144;                  // pitch of a row of 128 bytes of y (16-byte accesses by rows: no bank twice)
-constexpr uint32_t AD_REGION = 32 * AD_ROW;  // a warp's part of a unit: 32 rows
+constexpr int EX_WARPS = 16;                 // of an expand CTA
+constexpr int EX_THREADS = 32 * EX_WARPS;
+constexpr int EX_ROW = 80;                   // pitch of a row of 64 bytes of y (16-byte accesses by rows: no bank twice)
+constexpr uint32_t EX_REGION = 32 * EX_ROW;  // a warp's part of a unit: 32 rows
 
 __host__ __device__ __forceinline__ uint32_t idesc_bf16(int M, int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -384,6 +388,7 @@ __global__ void __launch_bounds__(AD_THREADS, XT == STRATA_F32 ? 2 : 3) shrink_t
     fence_mbar_init();
   }
   const uint16_t* A = a.a + (int64_t)tile.adapter * a.a_stride;
+  const float sc = a.scale ? __ldg(a.scale + tile.adapter) : 1.f;
   const int k0 = blockIdx.y * a.k_slice, k1 = min(a.d_in, k0 + a.k_slice);
   const int blocks = k0 < k1 ? (k1 - k0 + 63) / 64 : 0;
   const int chunk = tid & 7, row0 = tid >> 3;
@@ -494,7 +499,6 @@ __global__ void __launch_bounds__(AD_THREADS, XT == STRATA_F32 ? 2 : 3) shrink_t
   tc::fence_before_sync();
   cluster_sync();
   if (warp == 0) tc::tmem_dealloc(tmem, cols);
-  const float sc = a.scale ? __ldg(a.scale + tile.adapter) : 1.f;
   const int chunks = a.rank >> 3, vt = v_terms(a.y_type);
   // the cluster's CTAs share the tile's rows x 8 columns out among their threads
   for (int at = blockIdx.y * AD_THREADS + tid; at < tile.rows * chunks; at += a.split * AD_THREADS) {
@@ -525,23 +529,27 @@ __global__ void __launch_bounds__(AD_THREADS, XT == STRATA_F32 ? 2 : 3) shrink_t
 // the units ahead are on their way by cp.async, into a ring; a unit's product is in one of two TMEM accumulators while
 // the unit before it is read back, a row a thread, and added to base in shared memory, from where the warp stores it.
 template <int YT>
-__global__ void __launch_bounds__(AD_THREADS, 1) expand_tc_kernel(AdapterArgs a, int ring) {
+__global__ void __launch_bounds__(EX_THREADS, 1) expand_tc_kernel(AdapterArgs a, int ring) {
   constexpr int TERMS = v_terms(YT);
   constexpr int SIZE = YT == STRATA_F32 ? 4 : 2;
-  constexpr int HALF = 128 / SIZE, CW = 2 * HALF;  // columns of a warp: 128 bytes of y
-  constexpr int EL = 16 / SIZE;                    // elements of 16 bytes
+  constexpr int PART = 64 / SIZE, CW = 4 * PART;  // columns of a warp (64 bytes of y) and of a unit
+  constexpr int EL = 16 / SIZE;                   // elements of 16 bytes
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   __shared__ uint64_t s_full[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_dead;
-  griddep_wait();
-  const Segments g = cut_segments(a, TC_ROWS);
+  // Until griddep_wait only what the shrink kernel does not write is read; its CTAs let this kernel start after
+  // their own wait for what came before them.
+  const Segments g = cut_segments<EX_THREADS>(a, TC_ROWS);
   const int col_blocks = (a.d_out + CW - 1) / CW;
   const int units = g.total * col_blocks;  // at most 2 * 8,192 tiles of 256
   const int u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
   int u = (int)((int64_t)units * blockIdx.x / gridDim.x);
-  if (u >= u1) return;
+  if (u >= u1) {
+    griddep_wait();
+    return;
+  }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 0) {
     tc::tmem_alloc(&s_tmem, 2 * CW);
@@ -562,13 +570,17 @@ __global__ void __launch_bounds__(AD_THREADS, 1) expand_tc_kernel(AdapterArgs a,
   const uint32_t b_tile = CW * 128, b_slot = kblocks * b_tile;
   uint8_t* const sv = smem;                                   // [TERMS][kblocks] tiles
   uint8_t* const sb = sv + TERMS * kblocks * TC_TILE;         // [ring][kblocks] tiles of CW rows
-  uint8_t* const region = sb + ring * b_slot + warp * ring * AD_REGION;  // [ring] of this warp
+  uint8_t* const region = sb + ring * b_slot + warp * ring * EX_REGION;  // [ring] of this warp
   const uint32_t idesc = idesc_bf16(TC_ROWS, CW);
   const Waiter waiter{a.status, &s_dead};
   const uint16_t* vt = reinterpret_cast<const uint16_t*>(a.v);
-  // the warp's part of a unit: TMEM quadrant q (32 tokens), HALF columns
-  const int q = warp & 3, half = warp >> 2;
+  // the warp's part of a unit: TMEM quadrant q (32 tokens), PART columns; 16 bytes of 4 of its rows a lane when base and y
+  // are moved
+  const int q = warp & 3, part = warp >> 2;
+  const int mrow = 32 * q + (lane >> 2), mcol = PART * part + EL * (lane & 3);
+  uint8_t* const moved = region + (lane >> 2) * EX_ROW + 16 * (lane & 3);
   int n = 0;  // units with a product so far: the next one's accumulator and barrier phase
+  bool waited = false;
   while (u < u1) {
     const int first = u % col_blocks, blocks = min(col_blocks - first, u1 - u);
     const Tile tile = tile_at(a, g, u / col_blocks, TC_ROWS);
@@ -576,44 +588,52 @@ __global__ void __launch_bounds__(AD_THREADS, 1) expand_tc_kernel(AdapterArgs a,
     const bool product = tile.adapter >= 0;
     if (!product && a.base == a.y) continue;
     const uint16_t* B = a.b + (int64_t)max(tile.adapter, 0) * a.b_stride;
-    const char* base = static_cast<const char*>(a.base);
-    // B (rows: columns of y, 2 or 4 threads each) and the warp's base of unit blk
+    const char* base = static_cast<const char*>(a.base) + ((int64_t)(tile.row + mrow) * a.base_stride + CW * first + mcol) * SIZE;
+    char* const y = static_cast<char*>(a.y) + ((int64_t)(tile.row + mrow) * a.y_stride + CW * first + mcol) * SIZE;
+    const int64_t base_step = 8 * a.base_stride * SIZE, y_step = 8 * a.y_stride * SIZE;
+    uint32_t rows = 0;  // bit i: row mrow + 8 i is the tile's
+#pragma unroll
+    for (int i = 0; i < 4; ++i) rows |= (mrow + 8 * i < tile.rows ? 1u : 0u) << i;
+    // B (rows: columns of y, 512 / CW threads each) and the warp's base of unit blk
+    constexpr int PER = EX_THREADS / CW;
+    const int brow = tid / PER;
+    const uint16_t* const b_at = B + (int64_t)(CW * first + brow) * a.rank;
     const auto copy = [&](int blk) {
       if (blk < blocks) {
-        const int c0 = CW * (first + blk), slot = blk % ring;
+        const int slot = blk % ring;
         if (product) {
-          constexpr int PER = AD_THREADS / CW;  // threads a row
-          const int r = tid / PER, col = c0 + r;
+          const bool col = CW * (first + blk) + brow < a.d_out;
           for (int c = tid % PER; c < 2 * ksteps; c += PER) {
-            const bool ok = col < a.d_out && 8 * c < a.rank;
-            copy16(sb + slot * b_slot + (c >> 3) * b_tile + tc::swz_off(r, c & 7),
-                   ok ? B + (int64_t)col * a.rank + 8 * c : B, ok);
+            const bool ok = col && 8 * c < a.rank;
+            copy16(sb + slot * b_slot + (c >> 3) * b_tile + tc::swz_off(brow, c & 7),
+                   ok ? b_at + (int64_t)(CW * blk) * a.rank + 8 * c : B, ok);
           }
         }
-        const int col = c0 + HALF * half + EL * (lane & 7);
+        const bool col = a.base && CW * (first + blk) + mcol < a.d_out;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + (lane >> 3), row = 32 * q + r;
-          const bool ok = base && row < tile.rows && col < a.d_out;
-          copy16(region + slot * AD_REGION + r * AD_ROW + 16 * (lane & 7),
-                 ok ? base + ((int64_t)(tile.row + row) * a.base_stride + col) * SIZE : static_cast<const char*>(a.y), ok);
+        for (int i = 0; i < 4; ++i) {
+          const bool ok = col && (rows >> i & 1u);
+          copy16(moved + slot * EX_REGION + 8 * i * EX_ROW, ok ? base + i * base_step + CW * blk * SIZE : static_cast<const char*>(a.y), ok);
         }
       }
       copy_commit();
     };
+    for (int i = 0; i < ring - 1; ++i) copy(i);
+    if (!waited) griddep_wait();
+    waited = true;
     if (product) {
-      const int r = tid >> 1;
+      const int r = tid >> 2;
       for (int e = 0; e < TERMS; ++e)
-        for (int c = tid & 1; c < 2 * ksteps; c += 2) {
+        for (int c = tid & 3; c < 2 * ksteps; c += 4) {
           const bool ok = r < tile.rows && 8 * c < a.rank;
           copy16(sv + (e * kblocks + (c >> 3)) * TC_TILE + tc::swz_off(r, c & 7),
                  ok ? vt + ((int64_t)e * a.T + tile.row + r) * a.rank + 8 * c : vt, ok);
         }
+      copy_commit();
     }
-    for (int i = 0; i < ring - 1; ++i) copy(i);
     for (int blk = 0; blk <= blocks; ++blk) {
       if (blk < blocks) {
-        copy_wait(ring - 2);
+        copy_wait(blk ? ring - 2 : 0);
         tc::fence_proxy_async_smem();
         tc::fence_before_sync();  // this thread's reads of the accumulator two units back
         __syncthreads();
@@ -632,46 +652,42 @@ __global__ void __launch_bounds__(AD_THREADS, 1) expand_tc_kernel(AdapterArgs a,
       }
       if (blk > 0) {
         const int b = blk - 1, acc = (n + b) & 1;
-        uint8_t* const reg = region + (b % ring) * AD_REGION;
+        const uint32_t slot = (uint32_t)(b % ring) * EX_REGION;
         if (product) {
           waiter.wait(&s_full[acc], ((n + b) >> 1) & 1);
           tc::fence_after_sync();
           __syncwarp();
-          uint8_t* const mine = reg + lane * AD_ROW;
+          uint4* const mine = reinterpret_cast<uint4*>(region + slot + lane * EX_ROW);
+          uint32_t d[PART / 16][16];
+          uint4 w[4];
 #pragma unroll
-          for (int h = 0; h < HALF; h += 32) {
-            uint32_t d[2][16];
-            const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(CW * acc + HALF * half + h);
-            tc::tmem_ld16_async(at, d[0]);
-            tc::tmem_ld16_async(at + 16, d[1]);
-            tc::tmem_wait_ld();
+          for (int h = 0; h < PART / 16; ++h)
+            tc::tmem_ld16_async(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(CW * acc + PART * part + 16 * h), d[h]);
 #pragma unroll
-            for (int c = 0; c < 32; c += EL) {
-              uint4* const p = reinterpret_cast<uint4*>(mine + (h + c) * SIZE);
-              uint4 w = *p;
-              uint32_t* const we = &w.x;
+          for (int c = 0; c < 4; ++c) w[c] = mine[c];
+          tc::tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (SIZE == 4) {
-                  we[e] = __float_as_uint(__uint_as_float(we[e]) + __uint_as_float(d[(c + e) >> 4][(c + e) & 15]));
-                } else {
-                  const int i = c + 2 * e;
-                  const float2 f = widen2(we[e], YT);
-                  we[e] = narrow2(f.x + __uint_as_float(d[i >> 4][i & 15]), f.y + __uint_as_float(d[i >> 4][(i & 15) + 1]), YT);
-                }
+          for (int c = 0; c < 4; ++c) {
+            uint32_t* const we = &w[c].x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (SIZE == 4) {
+                we[e] = __float_as_uint(__uint_as_float(we[e]) + __uint_as_float(d[0][4 * c + e]));
+              } else {
+                const int i = 8 * c + 2 * e;
+                const float2 f = widen2(we[e], YT);
+                we[e] = narrow2(f.x + __uint_as_float(d[i >> 4][i & 15]), f.y + __uint_as_float(d[i >> 4][(i & 15) + 1]), YT);
               }
-              *p = w;
             }
+            mine[c] = w[c];
           }
           __syncwarp();
         }
-        const int col = CW * (first + b) + HALF * half + EL * (lane & 7);
+        const bool col = CW * (first + b) + mcol < a.d_out;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + (lane >> 3), row = 32 * q + r;
-          const uint4 w = *reinterpret_cast<const uint4*>(reg + r * AD_ROW + 16 * (lane & 7));
-          if (row < tile.rows && col < a.d_out)
-            *reinterpret_cast<uint4*>(static_cast<char*>(a.y) + ((int64_t)(tile.row + row) * a.y_stride + col) * SIZE) = w;
+        for (int i = 0; i < 4; ++i) {
+          const uint4 w = *reinterpret_cast<const uint4*>(moved + slot + 8 * i * EX_ROW);
+          if (col && (rows >> i & 1u)) *reinterpret_cast<uint4*>(y + i * y_step + CW * b * SIZE) = w;
         }
         __syncwarp();
       }
@@ -681,6 +697,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1) expand_tc_kernel(AdapterArgs a,
     copy_wait(0);
     if (product) n += blocks;
   }
+  if (!waited) griddep_wait();
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 0) tc::tmem_dealloc(tmem, 2 * CW);
@@ -762,10 +779,10 @@ cudaError_t launch_expand_tc(const AdapterArgs& a, int tiles, cudaStream_t s) {
   const int cw = YT == STRATA_F32 ? 64 : 128;
   const int kblocks = (a.rank + 63) / 64, units = tiles * ((a.d_out + cw - 1) / cw);
   const size_t fixed = (size_t)v_terms(YT) * kblocks * TC_TILE + 1024;
-  const size_t slot = (size_t)kblocks * cw * 128 + AD_WARPS * AD_REGION;
+  const size_t slot = (size_t)kblocks * cw * 128 + EX_WARPS * EX_REGION;
   const int ring = fixed + 3 * slot <= TC_SMEM_MAX ? 3 : 2;
   STRATA_LAUNCH(KID_ADAPTER_EXPAND, s,
-                err = launch_pdl(expand_tc_kernel<YT>, dim3(units < 152 ? units : 152), AD_THREADS, fixed + ring * slot, s, a, ring));
+                err = launch_pdl(expand_tc_kernel<YT>, dim3(units < 152 ? units : 152), EX_THREADS, fixed + ring * slot, s, a, ring));
   return err;
 }
 
