@@ -113,8 +113,9 @@ __device__ Tile tile_at(const AdapterArgs& a, const Segments& g, int want, int h
 }
 
 // The CTA's one tile; false if there is none.
+template <int THREADS>
 __device__ bool find_tile(const AdapterArgs& a, int want, int height, Tile* out) {
-  const Segments g = cut_segments<AD_THREADS>(a, height);
+  const Segments g = cut_segments<THREADS>(a, height);
   if (want >= g.total) return false;
   *out = tile_at(a, g, want, height);
   return true;
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(AD_THREADS) shrink_kernel(AdapterArgs a) {
   Tile tile;
   griddep_launch_dependents();
   griddep_wait();
-  if (!find_tile(a, blockIdx.x, 16 * MT, &tile) || tile.adapter < 0) return;
+  if (!find_tile<AD_THREADS>(a, blockIdx.x, 16 * MT, &tile) || tile.adapter < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int r0 = blockIdx.z * NT * 8;
   const uint16_t* A = a.a + (int64_t)tile.adapter * a.a_stride;
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(AD_THREADS) expand_kernel(AdapterArgs a) {
   Tile tile;
   griddep_launch_dependents();
   griddep_wait();
-  if (!find_tile(a, blockIdx.x, 16 * MT, &tile)) return;
+  if (!find_tile<AD_THREADS>(a, blockIdx.x, 16 * MT, &tile)) return;
   if (tile.adapter < 0 && a.base == a.y) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const uint16_t* B = a.b + (int64_t)max(tile.adapter, 0) * a.b_stride;
@@ -361,9 +362,9 @@ struct Waiter {
 
 // scale A_a x of a tile of up to 128 tokens, as bf16 terms vt[term][token][r].  One cluster a tile: each CTA takes a slice of
 // d_in, 64 k a stage, into a [128 x rank] accumulator in TMEM; the slices are then added in order over the cluster's
-// shared memory, each CTA finishing its share of the rows.
+// shared memory, each CTA finishing its share of the rows.  A warp of its own issues the MMAs.
 template <int XT>
-__global__ void __launch_bounds__(AD_THREADS, XT == STRATA_F32 ? 2 : 3) shrink_tc_kernel(AdapterArgs a, int np, int stages) {
+__global__ void __launch_bounds__(AD_THREADS + 32, XT == STRATA_F32 ? 2 : 3) shrink_tc_kernel(AdapterArgs a, int np, int stages) {
   constexpr int TERMS = bf16_terms(XT);
   constexpr int AHEAD = 2;  // stages of x on their way in registers (TERMS > 1)
   extern __shared__ uint8_t smem_raw[];
@@ -374,8 +375,9 @@ __global__ void __launch_bounds__(AD_THREADS, XT == STRATA_F32 ? 2 : 3) shrink_t
   Tile tile;
   griddep_wait();
   // (the same for all CTAs of a cluster)
-  if (!find_tile(a, blockIdx.x, TC_ROWS, &tile) || tile.adapter < 0) return;
+  if (!find_tile<AD_THREADS + 32>(a, blockIdx.x, TC_ROWS, &tile) || tile.adapter < 0) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool issuer = warp == AD_WARPS;
   const uint32_t cols = np <= 32 ? 32 : np <= 64 ? 64 : 128;
   if (warp == 0) {
     tc::tmem_alloc(&s_tmem, cols);
@@ -425,11 +427,13 @@ __global__ void __launch_bounds__(AD_THREADS, XT == STRATA_F32 ? 2 : 3) shrink_t
     for (int j = 0; j < 4; ++j)
       p[j] = in && row0 + 32 * j < tile.rows ? load8(X + (32 * j * a.x_stride + 64 * kb) * x_size, 0, XT) : zero;
   };
-  if (TERMS > 1) {
+  if (!issuer) {
+    if (TERMS > 1) {
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) fetch(i, piece[i]);
+      for (int i = 0; i < AHEAD; ++i) fetch(i, piece[i]);
+    }
+    for (int i = 0; i < stages - 1; ++i) copy(i);
   }
-  for (int i = 0; i < stages - 1; ++i) copy(i);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -437,54 +441,61 @@ __global__ void __launch_bounds__(AD_THREADS, XT == STRATA_F32 ? 2 : 3) shrink_t
   const uint32_t tmem = s_tmem;
   const uint32_t idesc = idesc_bf16(TC_ROWS, np);
   const Waiter waiter{a.status, &s_dead};
-  for (int kb0 = 0; kb0 < blocks; kb0 += AHEAD) {
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      const int kb = kb0 + i;
-      if (kb >= blocks) break;
-      uint8_t* at = smem + (kb % stages) * stage_bytes;
-      if (TERMS > 1) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float f[8];
-          uint32_t t[TERMS][4];
-          widen8(piece[i][j], XT, f);
-          split8<TERMS>(f, t);
-#pragma unroll
-          for (int e = 0; e < TERMS; ++e)
-            *reinterpret_cast<uint4*>(at + e * TC_TILE + tc::swz_off(row0 + 32 * j, chunk)) =
-                make_uint4(t[e][0], t[e][1], t[e][2], t[e][3]);
-        }
-        fetch(kb + AHEAD, piece[i]);
-      }
-      copy_wait(stages - 2);
-      tc::fence_proxy_async_smem();
-      __syncthreads();
-      if (tid == 0) {
+  if (issuer) {
+    uint64_t desc = tc::smem_desc_sw128(smem_u32(smem));
+    for (int kb = 0, stage = 0; kb < blocks; ++kb) {
+      named_barrier(1, AD_THREADS + 32);  // k-block kb is in shared memory
+      if (lane == 0) {
         tc::fence_after_sync();
-        const uint64_t bd = tc::smem_desc_sw128(smem_u32(at + TERMS * TC_TILE));
+        const uint64_t ad = desc + (uint64_t)(stage * (stage_bytes >> 4)), bd = ad + TERMS * (TC_TILE >> 4);
 #pragma unroll
-        for (int t = TERMS - 1; t >= 0; --t) {
-          const uint64_t ad = tc::smem_desc_sw128(smem_u32(at + t * TC_TILE));
+        for (int t = TERMS - 1; t >= 0; --t)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc::mma_f16(tmem, ad + 2 * kk, bd + 2 * kk, idesc, (kb > 0 || t < TERMS - 1 || kk > 0) ? 1u : 0u);
-        }
-        tc::mma_commit(&s_empty[kb % stages]);
+            tc::mma_f16(tmem, ad + t * (TC_TILE >> 4) + 2 * kk, bd + 2 * kk, idesc, (kb > 0 || t < TERMS - 1 || kk > 0) ? 1u : 0u);
+        tc::mma_commit(&s_empty[stage]);
       }
-      // the stage of k-block kb - 1 is free once its MMAs are done
-      if (kb > 0) waiter.wait(&s_empty[(kb - 1) % stages], ((kb - 1) / stages) & 1);
-      copy(kb + stages - 1);
+      if (++stage == stages) stage = 0;
     }
+    if (lane == 0) tc::mma_commit(&s_done);
+    __syncwarp();
+  } else {
+    for (int kb0 = 0; kb0 < blocks; kb0 += AHEAD) {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int kb = kb0 + i;
+        if (kb >= blocks) break;
+        if (TERMS > 1) {
+          uint8_t* at = smem + (kb % stages) * stage_bytes;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float f[8];
+            uint32_t t[TERMS][4];
+            widen8(piece[i][j], XT, f);
+            split8<TERMS>(f, t);
+#pragma unroll
+            for (int e = 0; e < TERMS; ++e)
+              *reinterpret_cast<uint4*>(at + e * TC_TILE + tc::swz_off(row0 + 32 * j, chunk)) =
+                  make_uint4(t[e][0], t[e][1], t[e][2], t[e][3]);
+          }
+          fetch(kb + AHEAD, piece[i]);
+        }
+        copy_wait(stages - 2);
+        tc::fence_proxy_async_smem();
+        named_barrier(1, AD_THREADS + 32);
+        // the stage of k-block kb - 1 is free once its MMAs are done
+        if (kb > 0) waiter.wait(&s_empty[(kb - 1) % stages], ((kb - 1) / stages) & 1);
+        copy(kb + stages - 1);
+      }
+    }
+    copy_wait(0);
   }
-  copy_wait(0);
-  if (tid == 0) tc::mma_commit(&s_done);
   waiter.wait(&s_done, 0);
   tc::fence_after_sync();
   __syncthreads();  // all have seen the last MMA: the stages are free for the sums
   const int pitch = np + 4;
   float* const part = reinterpret_cast<float*>(smem);
-  {
+  if (!issuer) {
     // rows: the warp's TMEM quadrant; columns: warps 0-3 the even 16, warps 4-7 the odd
     const int row = 32 * (warp & 3) + lane;
     for (int c = 16 * (warp >> 2); c < np; c += 32) {
@@ -501,7 +512,7 @@ __global__ void __launch_bounds__(AD_THREADS, XT == STRATA_F32 ? 2 : 3) shrink_t
   if (warp == 0) tc::tmem_dealloc(tmem, cols);
   const int chunks = a.rank >> 3, vt = v_terms(a.y_type);
   // the cluster's CTAs share the tile's rows x 8 columns out among their threads
-  for (int at = blockIdx.y * AD_THREADS + tid; at < tile.rows * chunks; at += a.split * AD_THREADS) {
+  for (int at = issuer ? tile.rows * chunks : blockIdx.y * AD_THREADS + tid; at < tile.rows * chunks; at += a.split * AD_THREADS) {
     const int row = at / chunks, c = 8 * (at - row * chunks);
     float f[8];
 #pragma unroll
@@ -528,8 +539,9 @@ __global__ void __launch_bounds__(AD_THREADS, XT == STRATA_F32 ? 2 : 3) shrink_t
 // CTA (one an SM) takes an equal stretch.  A tile's scaled A_a x (its bf16 terms) stays in shared memory; B and base of
 // the units ahead are on their way by cp.async, into a ring; a unit's product is in one of two TMEM accumulators while
 // the unit before it is read back, a row a thread, and added to base in shared memory, from where the warp stores it.
+// A warp of its own issues the MMAs.
 template <int YT>
-__global__ void __launch_bounds__(EX_THREADS, 1) expand_tc_kernel(AdapterArgs a, int ring) {
+__global__ void __launch_bounds__(EX_THREADS + 32, 1) expand_tc_kernel(AdapterArgs a, int ring) {
   constexpr int TERMS = v_terms(YT);
   constexpr int SIZE = YT == STRATA_F32 ? 4 : 2;
   constexpr int PART = 64 / SIZE, CW = 4 * PART;  // columns of a warp (64 bytes of y) and of a unit
@@ -541,7 +553,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1) expand_tc_kernel(AdapterArgs a,
   __shared__ int s_dead;
   // Until griddep_wait only what the shrink kernel does not write is read; its CTAs let this kernel start after
   // their own wait for what came before them.
-  const Segments g = cut_segments<EX_THREADS>(a, TC_ROWS);
+  const Segments g = cut_segments<EX_THREADS + 32>(a, TC_ROWS);
   const int col_blocks = (a.d_out + CW - 1) / CW;
   const int units = g.total * col_blocks;  // at most 2 * 8,192 tiles of 256
   const int u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
@@ -551,6 +563,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1) expand_tc_kernel(AdapterArgs a,
     return;
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool issuer = warp == EX_WARPS;
   if (warp == 0) {
     tc::tmem_alloc(&s_tmem, 2 * CW);
     tc::tmem_relinquish();
@@ -572,6 +585,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1) expand_tc_kernel(AdapterArgs a,
   uint8_t* const sb = sv + TERMS * kblocks * TC_TILE;         // [ring][kblocks] tiles of CW rows
   uint8_t* const region = sb + ring * b_slot + warp * ring * EX_REGION;  // [ring] of this warp
   const uint32_t idesc = idesc_bf16(TC_ROWS, CW);
+  const uint64_t v_desc = tc::smem_desc_sw128(smem_u32(sv)), b_desc = tc::smem_desc_sw128(smem_u32(sb));
   const Waiter waiter{a.status, &s_dead};
   const uint16_t* vt = reinterpret_cast<const uint16_t*>(a.v);
   // the warp's part of a unit: TMEM quadrant q (32 tokens), PART columns; 16 bytes of 4 of its rows a lane when base and y
@@ -587,6 +601,30 @@ __global__ void __launch_bounds__(EX_THREADS, 1) expand_tc_kernel(AdapterArgs a,
     u += blocks;
     const bool product = tile.adapter >= 0;
     if (!product && a.base == a.y) continue;
+    if (issuer) {
+      if (!waited) griddep_wait();
+      waited = true;
+      if (product)
+        for (int blk = 0; blk < blocks; ++blk) {
+          named_barrier(1, EX_THREADS + 32);  // A_a x and B of unit blk are in shared memory
+          if (lane == 0) {
+            tc::fence_after_sync();
+            const int acc = (n + blk) & 1;
+            const uint64_t bd = b_desc + (uint64_t)((blk % ring) * (b_slot >> 4));
+#pragma unroll
+            for (int t = TERMS - 1; t >= 0; --t)
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                if (kk < ksteps)
+                  tc::mma_f16(tmem + (uint32_t)(CW * acc), v_desc + (t * kblocks + (kk >> 2)) * (TC_TILE >> 4) + 2 * (kk & 3),
+                              bd + (kk >> 2) * (b_tile >> 4) + 2 * (kk & 3), idesc, (t < TERMS - 1 || kk > 0) ? 1u : 0u);
+            tc::mma_commit(&s_full[acc]);
+          }
+          __syncwarp();
+        }
+      if (product) n += blocks;
+      continue;
+    }
     const uint16_t* B = a.b + (int64_t)max(tile.adapter, 0) * a.b_stride;
     const char* base = static_cast<const char*>(a.base) + ((int64_t)(tile.row + mrow) * a.base_stride + CW * first + mcol) * SIZE;
     char* const y = static_cast<char*>(a.y) + ((int64_t)(tile.row + mrow) * a.y_stride + CW * first + mcol) * SIZE;
@@ -636,19 +674,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1) expand_tc_kernel(AdapterArgs a,
         copy_wait(blk ? ring - 2 : 0);
         tc::fence_proxy_async_smem();
         tc::fence_before_sync();  // this thread's reads of the accumulator two units back
-        __syncthreads();
-        if (product && tid == 0) {
-          tc::fence_after_sync();
-          const int acc = (n + blk) & 1;
-          for (int t = TERMS - 1; t >= 0; --t)
-            for (int kk = 0; kk < ksteps; ++kk) {
-              const uint64_t ad = tc::smem_desc_sw128(smem_u32(sv + (t * kblocks + (kk >> 2)) * TC_TILE));
-              const uint64_t bd = tc::smem_desc_sw128(smem_u32(sb + (blk % ring) * b_slot + (kk >> 2) * b_tile));
-              tc::mma_f16(tmem + (uint32_t)(CW * acc), ad + 2 * (kk & 3), bd + 2 * (kk & 3), idesc,
-                          (t < TERMS - 1 || kk > 0) ? 1u : 0u);
-            }
-          tc::mma_commit(&s_full[acc]);
-        }
+        if (product) named_barrier(1, EX_THREADS + 32);
       }
       if (blk > 0) {
         const int b = blk - 1, acc = (n + b) & 1;
@@ -756,7 +782,7 @@ cudaError_t launch_shrink_tc(const AdapterArgs& a, int tiles, cudaStream_t s) {
   const size_t smem = (stages * stage > sums ? stages * stage : sums) + 1024;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles, a.split);
-  cfg.blockDim = dim3(AD_THREADS);
+  cfg.blockDim = dim3(AD_THREADS + 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -782,7 +808,7 @@ cudaError_t launch_expand_tc(const AdapterArgs& a, int tiles, cudaStream_t s) {
   const size_t slot = (size_t)kblocks * cw * 128 + EX_WARPS * EX_REGION;
   const int ring = fixed + 3 * slot <= TC_SMEM_MAX ? 3 : 2;
   STRATA_LAUNCH(KID_ADAPTER_EXPAND, s,
-                err = launch_pdl(expand_tc_kernel<YT>, dim3(units < 152 ? units : 152), EX_THREADS, fixed + ring * slot, s, a, ring));
+                err = launch_pdl(expand_tc_kernel<YT>, dim3(units < 152 ? units : 152), EX_THREADS + 32, fixed + ring * slot, s, a, ring));
   return err;
 }
 
