@@ -31,6 +31,7 @@ struct AdapterArgs {
   float* v;  // [split][T][rank]
   int* status;
   int n_seg, n_adapter, rank, d_in, d_out, T, x_type, y_type, split, k_slice;
+  int early;  // base goes to L2 while the shrink kernel finishes
 };
 
 struct Tile {
@@ -313,10 +314,6 @@ __global__ void __launch_bounds__(AD_THREADS) expand_kernel(AdapterArgs a) {
 // griddep_wait and before the next kernel may start, so no CTA holds it while it waits for another.
 constexpr int TC_ROWS = 128;
 constexpr uint32_t TC_TILE = TC_ROWS * 128;  // 128 rows of 64 bf16
-constexpr int EX_WARPS = 16;                 // of an expand CTA
-constexpr int EX_THREADS = 32 * EX_WARPS;
-constexpr int EX_ROW = 80;                   // pitch of a row of 64 bytes of y (16-byte accesses by rows: no bank twice)
-constexpr uint32_t EX_REGION = 32 * EX_ROW;  // a warp's part of a unit: 32 rows
 
 __host__ __device__ __forceinline__ uint32_t idesc_bf16(int M, int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -350,6 +347,8 @@ __device__ __forceinline__ float4 cluster_ld4(const void* p, int rank) {
                : "memory");
   return v;
 }
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // A wait that ran out is recorded; the CTA's later waits are then skipped (the call's result is void).
 struct Waiter {
@@ -490,6 +489,14 @@ __global__ void __launch_bounds__(AD_THREADS + 32, XT == STRATA_F32 ? 2 : 3) shr
     }
     copy_wait(0);
   }
+  if (a.early) {
+    // the cluster's share of base, 128 bytes a thread and turn: memory has little else to do until the expand kernel
+    const int64_t size = a.y_type == STRATA_F32 ? 4 : 2;
+    const int lines = (int)((a.d_out * size + 127) / 128), l0 = lines * blockIdx.y / a.split, l1 = lines * (blockIdx.y + 1) / a.split;
+    const char* at = static_cast<const char*>(a.base) + tile.row * a.base_stride * size;
+    for (int r = warp; r < tile.rows; r += AD_WARPS + 1)
+      for (int l = l0 + lane; l < l1; l += 32) prefetch_l2(at + r * a.base_stride * size + 128 * l);
+  }
   waiter.wait(&s_done, 0);
   tc::fence_after_sync();
   __syncthreads();  // all have seen the last MMA: the stages are free for the sums
@@ -535,17 +542,17 @@ __global__ void __launch_bounds__(AD_THREADS + 32, XT == STRATA_F32 ? 2 : 3) shr
   cluster_sync();  // no CTA leaves while another reads its sums
 }
 
-// y = base + B_a (scale A_a x).  The work is one line of units, CW columns of a tile of up to 128 tokens each, of which every
-// CTA (one an SM) takes an equal stretch.  A tile's scaled A_a x (its bf16 terms) stays in shared memory; B and base of
-// the units ahead are on their way by cp.async, into a ring; a unit's product is in one of two TMEM accumulators while
-// the unit before it is read back, a row a thread, and added to base in shared memory, from where the warp stores it.
-// A warp of its own issues the MMAs.
+// y = base + B_a (scale A_a x).  The work is one line of units, 128 columns of a tile of up to 128 tokens each, of which every
+// CTA (two an SM) takes an equal stretch.  A tile's scaled A_a x (its bf16 terms) stays in shared memory, B of the units
+// ahead is on its way by cp.async into a ring; a unit's product is in one of two TMEM accumulators while the unit before it
+// is read back, added to base (on its way in registers for a unit ahead) and stored.  A warp of its own issues the MMAs.
+// The accumulator is read back in the layout of a warp-level MMA's result, 2 of every 8 columns a thread; B's rows are placed
+// so that these are 8 consecutive columns of y: place 8 j + 2 q + b of 32 holds column 8 q + 2 j + b.  So y passes
+// no shared memory, and four lanes read and write 32 columns of a row.
 template <int YT>
-__global__ void __launch_bounds__(EX_THREADS + 32, 1) expand_tc_kernel(AdapterArgs a, int ring) {
+__global__ void __launch_bounds__(AD_THREADS + 32, 2) expand_tc_kernel(AdapterArgs a, int ring) {
   constexpr int TERMS = v_terms(YT);
-  constexpr int SIZE = YT == STRATA_F32 ? 4 : 2;
-  constexpr int PART = 64 / SIZE, CW = 4 * PART;  // columns of a warp (64 bytes of y) and of a unit
-  constexpr int EL = 16 / SIZE;                   // elements of 16 bytes
+  constexpr int CW = 128;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   __shared__ uint64_t s_full[2];
@@ -553,9 +560,9 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 1) expand_tc_kernel(AdapterAr
   __shared__ int s_dead;
   // Until griddep_wait only what the shrink kernel does not write is read; its CTAs let this kernel start after
   // their own wait for what came before them.
-  const Segments g = cut_segments<EX_THREADS + 32>(a, TC_ROWS);
+  const Segments g = cut_segments<AD_THREADS + 32>(a, TC_ROWS);
   const int col_blocks = (a.d_out + CW - 1) / CW;
-  const int units = g.total * col_blocks;  // at most 2 * 8,192 tiles of 256
+  const int units = g.total * col_blocks;  // at most 2 * 8,192 tiles of 128
   const int u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
   int u = (int)((int64_t)units * blockIdx.x / gridDim.x);
   if (u >= u1) {
@@ -563,7 +570,7 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 1) expand_tc_kernel(AdapterAr
     return;
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool issuer = warp == EX_WARPS;
+  const bool issuer = warp == AD_WARPS;
   if (warp == 0) {
     tc::tmem_alloc(&s_tmem, 2 * CW);
     tc::tmem_relinquish();
@@ -580,19 +587,21 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 1) expand_tc_kernel(AdapterAr
   griddep_launch_dependents();
   const uint32_t tmem = s_tmem;
   const int kblocks = (a.rank + 63) / 64, ksteps = (a.rank + 15) / 16;
-  const uint32_t b_tile = CW * 128, b_slot = kblocks * b_tile;
-  uint8_t* const sv = smem;                                   // [TERMS][kblocks] tiles
-  uint8_t* const sb = sv + TERMS * kblocks * TC_TILE;         // [ring][kblocks] tiles of CW rows
-  uint8_t* const region = sb + ring * b_slot + warp * ring * EX_REGION;  // [ring] of this warp
+  const uint32_t b_slot = kblocks * TC_TILE;
+  uint8_t* const sv = smem;                             // [TERMS][kblocks] tiles
+  uint8_t* const sb = sv + TERMS * kblocks * TC_TILE;   // [ring][kblocks] tiles
   const uint32_t idesc = idesc_bf16(TC_ROWS, CW);
   const uint64_t v_desc = tc::smem_desc_sw128(smem_u32(sv)), b_desc = tc::smem_desc_sw128(smem_u32(sb));
   const Waiter waiter{a.status, &s_dead};
   const uint16_t* vt = reinterpret_cast<const uint16_t*>(a.v);
-  // the warp's part of a unit: TMEM quadrant q (32 tokens), PART columns; 16 bytes of 4 of its rows a lane when base and y
-  // are moved
-  const int q = warp & 3, part = warp >> 2;
-  const int mrow = 32 * q + (lane >> 2), mcol = PART * part + EL * (lane & 3);
-  uint8_t* const moved = region + (lane >> 2) * EX_ROW + 16 * (lane & 3);
+  // the warp's part of a unit: TMEM quadrant q4 (32 tokens) and 64 columns in two pieces; a lane has 8 columns of 4 rows of
+  // a piece
+  const int q4 = warp & 3, half = warp >> 2;
+  const int mrow = 32 * q4 + (lane >> 2), mcol = 64 * half + 8 * (lane & 3);
+  // two threads a row of B
+  const int brow = tid >> 1;
+  const int bcol = (brow & ~31) + 8 * ((brow >> 1) & 3) + 2 * ((brow >> 3) & 3) + (brow & 1);
+  const Raw8 zero{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
   int n = 0;  // units with a product so far: the next one's accumulator and barrier phase
   bool waited = false;
   while (u < u1) {
@@ -606,7 +615,7 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 1) expand_tc_kernel(AdapterAr
       waited = true;
       if (product)
         for (int blk = 0; blk < blocks; ++blk) {
-          named_barrier(1, EX_THREADS + 32);  // A_a x and B of unit blk are in shared memory
+          named_barrier(1, AD_THREADS + 32);  // A_a x and B of unit blk are in shared memory
           if (lane == 0) {
             tc::fence_after_sync();
             const int acc = (n + blk) & 1;
@@ -617,7 +626,7 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 1) expand_tc_kernel(AdapterAr
               for (int kk = 0; kk < 8; ++kk)
                 if (kk < ksteps)
                   tc::mma_f16(tmem + (uint32_t)(CW * acc), v_desc + (t * kblocks + (kk >> 2)) * (TC_TILE >> 4) + 2 * (kk & 3),
-                              bd + (kk >> 2) * (b_tile >> 4) + 2 * (kk & 3), idesc, (t < TERMS - 1 || kk > 0) ? 1u : 0u);
+                              bd + (kk >> 2) * (TC_TILE >> 4) + 2 * (kk & 3), idesc, (t < TERMS - 1 || kk > 0) ? 1u : 0u);
             tc::mma_commit(&s_full[acc]);
           }
           __syncwarp();
@@ -626,43 +635,50 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 1) expand_tc_kernel(AdapterAr
       continue;
     }
     const uint16_t* B = a.b + (int64_t)max(tile.adapter, 0) * a.b_stride;
-    const char* base = static_cast<const char*>(a.base) + ((int64_t)(tile.row + mrow) * a.base_stride + CW * first + mcol) * SIZE;
-    char* const y = static_cast<char*>(a.y) + ((int64_t)(tile.row + mrow) * a.y_stride + CW * first + mcol) * SIZE;
-    const int64_t base_step = 8 * a.base_stride * SIZE, y_step = 8 * a.y_stride * SIZE;
+    const int64_t base_at = (int64_t)(tile.row + mrow) * a.base_stride + CW * first + mcol;
+    const int64_t y_at = (int64_t)(tile.row + mrow) * a.y_stride + CW * first + mcol;
     uint32_t rows = 0;  // bit i: row mrow + 8 i is the tile's
 #pragma unroll
     for (int i = 0; i < 4; ++i) rows |= (mrow + 8 * i < tile.rows ? 1u : 0u) << i;
-    // B (rows: columns of y, 512 / CW threads each) and the warp's base of unit blk
-    constexpr int PER = EX_THREADS / CW;
-    const int brow = tid / PER;
-    const uint16_t* const b_at = B + (int64_t)(CW * first + brow) * a.rank;
-    const auto copy = [&](int blk) {
-      if (blk < blocks) {
-        const int slot = blk % ring;
-        if (product) {
-          const bool col = CW * (first + blk) + brow < a.d_out;
-          for (int c = tid % PER; c < 2 * ksteps; c += PER) {
-            const bool ok = col && 8 * c < a.rank;
-            copy16(sb + slot * b_slot + (c >> 3) * b_tile + tc::swz_off(brow, c & 7),
-                   ok ? b_at + (int64_t)(CW * blk) * a.rank + 8 * c : B, ok);
-          }
-        }
-        const bool col = a.base && CW * (first + blk) + mcol < a.d_out;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool ok = col && (rows >> i & 1u);
-          copy16(moved + slot * EX_REGION + 8 * i * EX_ROW, ok ? base + i * base_step + CW * blk * SIZE : static_cast<const char*>(a.y), ok);
+    const uint16_t* const b_at = B + (int64_t)(CW * first + bcol) * a.rank;
+    const auto copy_b = [&](int blk) {
+      if (product && blk < blocks) {
+        uint8_t* const to = sb + (blk % ring) * b_slot;
+        const bool col = CW * (first + blk) + bcol < a.d_out;
+        for (int c = tid & 1; c < 2 * ksteps; c += 2) {
+          const bool ok = col && 8 * c < a.rank;
+          copy16(to + (c >> 3) * TC_TILE + tc::swz_off(brow, c & 7), ok ? b_at + (int64_t)(CW * blk) * a.rank + 8 * c : B, ok);
         }
       }
       copy_commit();
     };
-    for (int i = 0; i < ring - 1; ++i) copy(i);
+    Raw8 base[2][4];
+    const auto fetch_base = [&](int blk, int sub, Raw8 (&to)[4]) {
+      const bool in = a.base && blk < blocks && CW * (first + blk) + 32 * sub + mcol < a.d_out;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        to[i] = in && (rows >> i & 1u) ? load8(a.base, base_at + 8 * i * a.base_stride + CW * blk + 32 * sub, YT) : zero;
+    };
+    // base of units further ahead goes to L2, a row of 128 columns two threads
+    const auto warm = [&](int blk) {
+      const int c0 = CW * (first + blk), size = YT == STRATA_F32 ? 4 : 2;
+      if (a.early || !a.base || blk >= blocks || brow >= tile.rows) return;
+#pragma unroll
+      for (int c = (tid & 1) * 64; c < CW; c += YT == STRATA_F32 ? (c & 32 ? 128 : 32) : 128)
+        if (c0 + c < a.d_out)
+          prefetch_l2(static_cast<const char*>(a.base) + ((tile.row + brow) * a.base_stride + c0 + c) * size);
+    };
+    for (int i = 0; i < ring - 1; ++i) copy_b(i);
+    warm(1);
+    warm(2);
+    fetch_base(0, 0, base[0]);
+    fetch_base(0, 1, base[1]);
     if (!waited) griddep_wait();
     waited = true;
     if (product) {
-      const int r = tid >> 2;
+      const int r = tid >> 1;
       for (int e = 0; e < TERMS; ++e)
-        for (int c = tid & 3; c < 2 * ksteps; c += 4) {
+        for (int c = tid & 1; c < 2 * ksteps; c += 2) {
           const bool ok = r < tile.rows && 8 * c < a.rank;
           copy16(sv + (e * kblocks + (c >> 3)) * TC_TILE + tc::swz_off(r, c & 7),
                  ok ? vt + ((int64_t)e * a.T + tile.row + r) * a.rank + 8 * c : vt, ok);
@@ -670,55 +686,47 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 1) expand_tc_kernel(AdapterAr
       copy_commit();
     }
     for (int blk = 0; blk <= blocks; ++blk) {
-      if (blk < blocks) {
+      if (product && blk < blocks) {
         copy_wait(blk ? ring - 2 : 0);
         tc::fence_proxy_async_smem();
         tc::fence_before_sync();  // this thread's reads of the accumulator two units back
-        if (product) named_barrier(1, EX_THREADS + 32);
+        named_barrier(1, AD_THREADS + 32);
       }
       if (blk > 0) {
         const int b = blk - 1, acc = (n + b) & 1;
-        const uint32_t slot = (uint32_t)(b % ring) * EX_REGION;
         if (product) {
           waiter.wait(&s_full[acc], ((n + b) >> 1) & 1);
           tc::fence_after_sync();
           __syncwarp();
-          uint4* const mine = reinterpret_cast<uint4*>(region + slot + lane * EX_ROW);
-          uint32_t d[PART / 16][16];
-          uint4 w[4];
+        }
 #pragma unroll
-          for (int h = 0; h < PART / 16; ++h)
-            tc::tmem_ld16_async(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(CW * acc + PART * part + 16 * h), d[h]);
+        for (int sub = 0; sub < 2; ++sub) {
+          const bool col = CW * (first + b) + 32 * sub + mcol < a.d_out;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) w[c] = mine[c];
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t* const we = &w[c].x;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (SIZE == 4) {
-                we[e] = __float_as_uint(__uint_as_float(we[e]) + __uint_as_float(d[0][4 * c + e]));
-              } else {
-                const int i = 8 * c + 2 * e;
-                const float2 f = widen2(we[e], YT);
-                we[e] = narrow2(f.x + __uint_as_float(d[i >> 4][i & 15]), f.y + __uint_as_float(d[i >> 4][(i & 15) + 1]), YT);
-              }
+          for (int h = 0; h < 2; ++h) {  // rows mrow + 16 h, + 8
+            uint32_t d[16];
+            if (product) {
+              tc::tmem_ld16x256b_x4_async(tmem + ((uint32_t)(32 * q4 + 16 * h) << 16) + (uint32_t)(CW * acc + 64 * half + 32 * sub), d);
+              tc::tmem_wait_ld();
             }
-            mine[c] = w[c];
-          }
-          __syncwarp();
-        }
-        const bool col = CW * (first + b) + mcol < a.d_out;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 w = *reinterpret_cast<const uint4*>(moved + slot + 8 * i * EX_ROW);
-          if (col && (rows >> i & 1u)) *reinterpret_cast<uint4*>(y + i * y_step + CW * b * SIZE) = w;
+            for (int p = 0; p < 2; ++p) {
+              const int i = 2 * h + p;
+              float f[8];
+              widen8(base[sub][i], YT, f);
+              if (product) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] += __uint_as_float(d[4 * (e >> 1) + 2 * p + (e & 1)]);
+              }
+              if (col && (rows >> i & 1u)) store8(a.y, y_at + 8 * i * a.y_stride + CW * b + 32 * sub, YT, f);
+            }
+          }
+          fetch_base(b + 1, sub, base[sub]);
         }
-        __syncwarp();
       }
       // into the slot of the unit just stored, whose product's MMAs this thread has waited for
-      if (blk < blocks) copy(blk + ring - 1);
+      if (blk < blocks) copy_b(blk + ring - 1);
+      warm(blk + 3);
     }
     copy_wait(0);
     if (product) n += blocks;
@@ -802,13 +810,14 @@ template <int YT>
 cudaError_t launch_expand_tc(const AdapterArgs& a, int tiles, cudaStream_t s) {
   cudaError_t err = allow_smem<expand_tc_kernel<YT>>(TC_SMEM_MAX);
   if (err != cudaSuccess) return err;
-  const int cw = YT == STRATA_F32 ? 64 : 128;
-  const int kblocks = (a.rank + 63) / 64, units = tiles * ((a.d_out + cw - 1) / cw);
-  const size_t fixed = (size_t)v_terms(YT) * kblocks * TC_TILE + 1024;
-  const size_t slot = (size_t)kblocks * cw * 128 + EX_WARPS * EX_REGION;
-  const int ring = fixed + 3 * slot <= TC_SMEM_MAX ? 3 : 2;
+  const int kblocks = (a.rank + 63) / 64, units = tiles * ((a.d_out + 127) / 128);
+  const size_t fixed = (size_t)v_terms(YT) * kblocks * TC_TILE + 1024, slot = (size_t)kblocks * TC_TILE;
+  const size_t half_sm = 113 * 1024;  // two CTAs an SM
+  const int ring = fixed + 2 * slot > half_sm || fixed + 3 * slot <= half_sm ? 3 : 2;
+  const size_t smem = fixed + ring * slot;
+  const int fit = smem <= half_sm ? 304 : 152;
   STRATA_LAUNCH(KID_ADAPTER_EXPAND, s,
-                err = launch_pdl(expand_tc_kernel<YT>, dim3(units < 152 ? units : 152), EX_THREADS + 32, fixed + ring * slot, s, a, ring));
+                err = launch_pdl(expand_tc_kernel<YT>, dim3(units < fit ? units : fit), AD_THREADS + 32, smem, s, a, ring));
   return err;
 }
 
@@ -818,6 +827,8 @@ cudaError_t launch_tc(AdapterArgs a, cudaStream_t s) {
   while (split < SPLIT_MAX && 2 * tiles * split <= 152 * (a.x_type == STRATA_F32 ? 2 : 3) && a.d_in / (2 * split) >= 256) split *= 2;
   a.split = split;
   a.k_slice = ((a.d_in + split - 1) / split + 63) / 64 * 64;
+  // up to a third of the 129 MB L2: x, base and y of a call then fit beside one another
+  a.early = a.base && (int64_t)a.T * a.d_out * (a.y_type == STRATA_F32 ? 4 : 2) <= (int64_t)43 << 20;
   const cudaError_t err = a.x_type == STRATA_BF16  ? launch_shrink_tc<STRATA_BF16>(a, tiles, s)
                           : a.x_type == STRATA_F16 ? launch_shrink_tc<STRATA_F16>(a, tiles, s)
                                                    : launch_shrink_tc<STRATA_F32>(a, tiles, s);
