@@ -333,7 +333,9 @@ __device__ __forceinline__ void copy_wait(int n) {
   else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
   else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
+// (The lanes come together first: loops of different lengths come before.)
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Four floats of shared memory of CTA `rank` of the cluster, at the address that this CTA's `p` has there.
@@ -524,11 +526,21 @@ __global__ void __launch_bounds__(AD_THREADS + 32, XT == STRATA_F32 ? 2 : 3) shr
     float f[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < a.split; ++s) {
-      const float4 u0 = cluster_ld4(part + row * pitch + c, s), u1 = cluster_ld4(part + row * pitch + c + 4, s);
-      f[0] += u0.x; f[1] += u0.y; f[2] += u0.z; f[3] += u0.w;
-      f[4] += u1.x; f[5] += u1.y; f[6] += u1.z; f[7] += u1.w;
+    for (int s0 = 0; s0 < a.split; s0 += 4) {  // four slices' reads at once
+      float4 u0[4], u1[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        u0[s] = u1[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s0 + s < a.split) {
+          u0[s] = cluster_ld4(part + row * pitch + c, s0 + s);
+          u1[s] = cluster_ld4(part + row * pitch + c + 4, s0 + s);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        f[0] += u0[s].x; f[1] += u0[s].y; f[2] += u0[s].z; f[3] += u0[s].w;
+        f[4] += u1[s].x; f[5] += u1[s].y; f[6] += u1[s].z; f[7] += u1[s].w;
+      }
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] *= sc;
