@@ -4,8 +4,6 @@
 // fixed order), and expand, base + B_a (scale v).  Both walk tiles of up to 16 MT tokens of one segment; the products
 // are warp-level bf16 MMAs with fp32 accumulators.  A wider activation is the exact sum of bf16 terms (an fp16 two, an
 // fp32 three), each multiplied on its own.
-#include <atomic>
-
 #include "device_common.cuh"
 #include "elements.cuh"
 #include "tc_common.cuh"
@@ -774,19 +772,6 @@ cudaError_t launch_both(const AdapterArgs& a, int tiles, int col_split, cudaStre
   return cudaGetLastError();
 }
 
-// The dynamic shared memory a kernel may use, raised once per kernel and device.
-template <auto* KERNEL>
-cudaError_t allow_smem(size_t bytes) {
-  static std::atomic<uint64_t> done{0};  // bit d: raised on device d
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-  if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
-  err = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return err;
-}
 constexpr size_t TC_SMEM_MAX = 226 * 1024;
 
 template <int XT>
