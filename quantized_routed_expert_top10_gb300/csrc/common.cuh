@@ -302,6 +302,20 @@ cudaError_t allow_smem(size_t bytes) {
   if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return err;
 }
+// CTAs of `threads` threads (a multiple of 32, up to 1,024) and smem dynamic bytes that an SM holds at once; asked once for
+// each thread count, so a kernel's smem must go with its thread count.  At least 1.
+template <auto* KERNEL>
+int resident_ctas(int threads, size_t smem) {
+  static std::atomic<int> known[33];
+  std::atomic<int>& k = known[threads / 32];
+  int n = k.load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERNEL, threads, smem) != cudaSuccess || n < 1) n = 1;
+    k.store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 #define STRATA_LAUNCH(kid, s, ...) \
   do {                             \
     kernel_begin((kid), (s));      \

@@ -105,8 +105,8 @@ constexpr int NO_PARTS = -1;
 // of a row is read before the first sum (x, and GROUP parts at a time), and a row's threads are few (one warp in a long
 // call), so that many rows are on their way at once and no barrier holds them.
 template <int XT, int PT, int W, int V>
-__global__ void __launch_bounds__(W == 4 ? 512 : 1024) edge_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int GROUP = PT == NO_PARTS ? 1 : 5;
+__global__ void __launch_bounds__(1024) edge_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int GROUP = PT == NO_PARTS || V == 16 ? 1 : W == 4 ? 10 : 5;
   __shared__ float red[2][32];
   const int t = blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= a.T) return;  // whole warps; only one-warp rows share a CTA
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(W == 4 ? 512 : 1024) edge_kernel(const __grid_
 // registers, so that memory never waits for a row's sums; the gains stay in registers where they are few.
 template <int XT, int PT, int V, int AHEAD>
 __global__ void __launch_bounds__(512) edge_stream_kernel(const __grid_constant__ NormArgs a) {
-  constexpr bool PART = PT != NO_PARTS, KEEP = V == 2;
+  constexpr bool PART = PT != NO_PARTS, KEEP = V <= 4;
   __shared__ float red[2][2][32];
   const int tid = threadIdx.x, threads = blockDim.x, units = a.n / 4;
   bool mine[V];
@@ -334,16 +334,24 @@ __global__ void __launch_bounds__(512) edge_stream_kernel(const __grid_constant_
   }
 }
 
+template <int XT, int PT, int V, int AHEAD>
+cudaError_t launch_stream_v(const NormArgs& a, cudaStream_t s) {
+  const int threads = ((a.n / 4 + V - 1) / V + 31) / 32 * 32;
+  const int fit = 152 * resident_ctas<edge_stream_kernel<XT, PT, V, AHEAD>>(threads, 0);
+  edge_stream_kernel<XT, PT, V, AHEAD><<<a.T < fit ? a.T : fit, threads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+// Units a thread and rows ahead (2560 columns, 8,192 rows): without a part (fp32 to bf16) 2 and 2 22.4 us, 2 and 1 25.6, 4 and
+// 1 23.4; with one (fp32, the stream in bf16) 4 and 1 38.6 us, 2 and 1 39.7, 2 and 2 50, 5 and 1 49, 10 and 1 66:
+// more threads a row pay more for its two sums, more registers a thread leave fewer rows on their way.  Few rows are
+// spread over more threads (four rows: 2.3 us).
 template <int XT, int PT>
 cudaError_t launch_stream(const NormArgs& a, cudaStream_t s) {
-  const int units = a.n / 4, V = units <= 1024 ? 2 : units <= 2048 ? 4 : 8;
-  const int threads = ((units + V - 1) / V + 31) / 32 * 32;
-  // CTAs that fit the GPU at about 1,000 threads an SM
-  const int per = threads > 512 ? 1 : 1024 / threads > 24 ? 24 : 1024 / threads, grid = a.T < 152 * per ? a.T : 152 * per;
-  if (V == 2) edge_stream_kernel<XT, PT, 2, 2><<<grid, threads, 0, s>>>(a);
-  else if (V == 4) edge_stream_kernel<XT, PT, 4, 1><<<grid, threads, 0, s>>>(a);
-  else edge_stream_kernel<XT, PT, 8, 1><<<grid, threads, 0, s>>>(a);
-  return cudaGetLastError();
+  const int units = a.n / 4;
+  if (units > 2048) return launch_stream_v<XT, PT, 8, 1>(a, s);
+  if (units > 1024 || (PT != NO_PARTS && a.T > 152)) return launch_stream_v<XT, PT, 4, 1>(a, s);
+  return launch_stream_v<XT, PT, 2, PT == NO_PARTS ? 2 : 1>(a, s);
 }
 
 // ---- Rows with parts, on boundaries of 4 elements -----------------------------------------------------------
@@ -351,11 +359,8 @@ cudaError_t launch_stream(const NormArgs& a, cudaStream_t s) {
 // other than 0 in order and then x; the steps of this row and the next ones are on their way by cp.async into a ring of
 // shared memory, where a thread finds the pieces that it copied itself: no barrier, and memory never waits for
 // a row's sums.  The gains stay in registers where a thread has two units.
-constexpr int ring_slots(int V) { return V == 2 ? 6 : 3; }  // two CTAs an SM, of up to 96 KB; the widest rows one
-
-template <int XT, int PT, int V>
+template <int XT, int PT, int V, int RING>
 __global__ void __launch_bounds__(512) edge_ring_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int RING = ring_slots(V);
   extern __shared__ __align__(16) uint4 s_ring[];  // [ring][V][threads]
   __shared__ float red[2][2][32];
   const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, units = a.n / 4;
@@ -363,7 +368,7 @@ __global__ void __launch_bounds__(512) edge_ring_kernel(const __grid_constant__ 
   bool mine[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) mine[v] = tid + v * threads < units;
-  constexpr bool KEEP = V == 2;
+  constexpr bool KEEP = V <= 4;
   float gains[KEEP ? 2 : 1][KEEP ? V : 1][4];  // of z: post and channel; of next
   if constexpr (KEEP) {
 #pragma unroll
@@ -509,21 +514,27 @@ __global__ void __launch_bounds__(512) edge_ring_kernel(const __grid_constant__ 
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <int XT, int PT, int V>
-cudaError_t launch_ring(const NormArgs& a, int threads, cudaStream_t s) {
-  const int smem = ring_slots(V) * V * threads * 16, fit = smem <= 110 * 1024 ? 304 : 152;
-  const cudaError_t err = allow_smem<edge_ring_kernel<XT, PT, V>>(224 * 1024);
+template <int XT, int PT, int V, int RING>
+cudaError_t launch_ring_v(const NormArgs& a, cudaStream_t s) {
+  const int threads = ((a.n / 4 + V - 1) / V + 31) / 32 * 32, smem = RING * V * threads * 16;
+  const cudaError_t err = allow_smem<edge_ring_kernel<XT, PT, V, RING>>(224 * 1024);
   if (err != cudaSuccess) return err;
-  edge_ring_kernel<XT, PT, V><<<a.T < fit ? a.T : fit, threads, smem, s>>>(a);
+  const int fit = 152 * resident_ctas<edge_ring_kernel<XT, PT, V, RING>>(threads, smem);
+  edge_ring_kernel<XT, PT, V, RING><<<a.T < fit ? a.T : fit, threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
+// Slots: 6 of up to 16 KB, or 3 of up to 64 KB.
 template <int XT, int PT>
-cudaError_t launch_ring_v(const NormArgs& a, cudaStream_t s) {
-  const int units = a.n / 4, V = units <= 1024 ? 2 : units <= 2048 ? 4 : 8;
-  const int threads = ((units + V - 1) / V + 31) / 32 * 32;
-  return V == 2 ? launch_ring<XT, PT, 2>(a, threads, s) : V == 4 ? launch_ring<XT, PT, 4>(a, threads, s)
-                                                                 : launch_ring<XT, PT, 8>(a, threads, s);
+cudaError_t launch_ring(const NormArgs& a, cudaStream_t s) {
+  const int units = a.n / 4;
+  if (units <= 1024 && a.T <= 152) {
+    edge_kernel<XT, PT, 4, 1><<<a.T, (units + 31) / 32 * 32, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  if (units > 2048) return launch_ring_v<XT, PT, 8, 3>(a, s);
+  if (units > 1024) return launch_ring_v<XT, PT, 4, 3>(a, s);
+  return launch_ring_v<XT, PT, 2, 6>(a, s);
 }
 
 // Every row of the operand starts on a boundary of four elements.
@@ -537,7 +548,7 @@ template <int XT, int PT>
 cudaError_t launch_parts(const NormArgs& a, bool vec, cudaStream_t s) {
   if (vec) {
     if constexpr (PT != NO_PARTS)
-      if (a.P > 1) return launch_ring_v<XT, PT>(a, s);
+      if (a.P > 1) return launch_ring<XT, PT>(a, s);
     return launch_stream<XT, PT>(a, s);
   }
   const int V = a.n <= 4096 ? 4 : 16, threads = ((a.n + V - 1) / V + 31) / 32 * 32;
