@@ -39,12 +39,10 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return warp_sum(lane < warps ? red[lane] : 0.f);
 }
 
-// W consecutive elements of type T as a unit, as read: 1, or 4 on a boundary of their size (16 bytes of fp32, so that a
-// warp's accesses are contiguous whatever the types of the operands).
-template <int T, int W>
-struct Unit;
+// 4 consecutive elements of type T on a boundary of their size, as read (16 bytes of fp32, so that a warp's accesses are
+// contiguous whatever the types of the operands).
 template <int T>
-struct Unit<T, 4> {
+struct Unit {
   uint32_t r[T == STRATA_F32 ? 4 : 2];
   __device__ __forceinline__ void load(const void* p, int64_t i) {
     if constexpr (T == STRATA_F32) {
@@ -69,143 +67,85 @@ struct Unit<T, 4> {
     }
   }
 };
-template <int T>
-struct Unit<T, 1> {
-  float r;
-  __device__ __forceinline__ void load(const void* p, int64_t i) { r = load1(p, i, T); }
-  __device__ __forceinline__ void zero() { r = 0.f; }
-  __device__ __forceinline__ void widen(float (&f)[1]) const { f[0] = r; }
-};
-template <int W>
-__device__ __forceinline__ void store_unit(void* p, int64_t i, int type, const float (&f)[W]) {
-  if constexpr (W == 4) {
-    if (type == STRATA_F32) *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(f[0], f[1], f[2], f[3]);
-    else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = make_uint2(narrow2(f[0], f[1], type), narrow2(f[2], f[3], type));
-  } else {
-    store1(p, i, type, f[0]);
-  }
+__device__ __forceinline__ void store_unit(void* p, int64_t i, int type, const float (&f)[4]) {
+  if (type == STRATA_F32) *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(f[0], f[1], f[2], f[3]);
+  else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = make_uint2(narrow2(f[0], f[1], type), narrow2(f[2], f[3], type));
 }
-// f *= g[i .. i + W - 1] (fp32)
-template <int W>
-__device__ __forceinline__ void times(float (&f)[W], const float* g, int i, bool aligned) {
-  if constexpr (W == 4) {
-    if (aligned) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(g + i));
-      f[0] *= a.x; f[1] *= a.y; f[2] *= a.z; f[3] *= a.w;
-      return;
-    }
+// f *= g[i .. i + 3] (fp32)
+__device__ __forceinline__ void times(float (&f)[4], const float* g, int i, bool aligned) {
+  if (aligned) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(g + i));
+    f[0] *= a.x; f[1] *= a.y; f[2] *= a.z; f[3] *= a.w;
+    return;
   }
 #pragma unroll
-  for (int e = 0; e < W; ++e) f[e] *= __ldg(g + i + e);
+  for (int e = 0; e < 4; ++e) f[e] *= __ldg(g + i + e);
 }
 
 constexpr int NO_PARTS = -1;
 
-// One row per blockDim.x threads; a thread holds V units of W elements, blockDim.x units apart.  Memory bounds it: all
-// of a row is read before the first sum (x, and GROUP parts at a time), and a row's threads are few (one warp in a long
-// call), so that many rows are on their way at once and no barrier holds them.
-template <int XT, int PT, int W, int V>
-__global__ void __launch_bounds__(1024) edge_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int GROUP = PT == NO_PARTS || V == 16 ? 1 : W == 4 ? 10 : 5;
+// Few rows with several parts, on boundaries of 4 elements: a CTA a row, a thread one unit of 4 columns, ten parts read at
+// once.
+template <int XT, int PT>
+__global__ void __launch_bounds__(1024) edge_few_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int GROUP = 10;
   __shared__ float red[2][32];
-  const int t = blockIdx.x * blockDim.y + threadIdx.y;
-  if (t >= a.T) return;  // whole warps; only one-warp rows share a CTA
-  const int units = a.n / W, step = blockDim.x;
-  Unit<XT, W> x[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int u = threadIdx.x + v * step;
-    if (a.x && u < units) x[v].load(a.x, (int64_t)t * a.x_stride + (int64_t)u * W);
-    else x[v].zero();
+  const int t = blockIdx.x, u = threadIdx.x, lane = u & 31;
+  const bool in = u < a.n / 4;
+  Unit<XT> x;
+  if (a.x && in) x.load(a.x, (int64_t)t * a.x_stride + u * 4);
+  else x.zero();
+  const float mine = lane >= a.P ? 0.f : a.pw ? __ldg(a.pw + (int64_t)t * a.P + lane) : 1.f;  // P <= 32
+  float g = a.block;
+  if (a.token) {
+    const float s = __ldg(a.token + t);
+    g *= a.sigmoid ? 1.f / (1.f + expf(-s)) : s;
   }
-  float r[V][W];
-  if constexpr (PT != NO_PARTS) {
-    const int lane = threadIdx.x & 31;
-    const float mine = lane >= a.P ? 0.f : a.pw ? __ldg(a.pw + (int64_t)t * a.P + lane) : 1.f;  // P <= 32
-    float g = a.block;
-    if (a.token) {
-      const float s = __ldg(a.token + t);
-      g *= a.sigmoid ? 1.f / (1.f + expf(-s)) : s;
-    }
-    float y[V][W];
+  float y[4] = {0.f, 0.f, 0.f, 0.f}, r[4];
+  for (int k0 = 0; k0 < a.P; k0 += GROUP) {
+    Unit<PT> p[GROUP];
+    float w[GROUP];
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int i = 0; i < W; ++i) y[v][i] = 0.f;
-    for (int k0 = 0; k0 < a.P; k0 += GROUP) {
-      Unit<PT, W> p[GROUP][V];
-      float w[GROUP];
-#pragma unroll
-      for (int k = 0; k < GROUP; ++k) {
-        w[k] = k0 + k < 32 ? __shfl_sync(0xffffffffu, mine, (k0 + k) & 31) : 0.f;
-        const int64_t at = (int64_t)t * a.token_stride + (k0 + k) * a.part_stride;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int u = threadIdx.x + v * step;
-          if (w[k] != 0.f && u < units) p[k][v].load(a.parts, at + (int64_t)u * W);  // (a part of weight 0 is not read)
-          else p[k][v].zero();
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < GROUP; ++k)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float f[W];
-          p[k][v].widen(f);
-#pragma unroll
-          for (int i = 0; i < W; ++i) y[v][i] = fmaf(w[k], f[i], y[v][i]);
-        }
-    }
-    float rn = 1.f;
-    if (a.post) {
-      float ss = 0.f;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < W; ++i) ss = fmaf(y[v][i], y[v][i], ss);
-      rn = rsqrtf(fmaf(row_sum(ss, red[0]), a.inv_n, a.eps));
+    for (int k = 0; k < GROUP; ++k) {
+      w[k] = k0 + k < 32 ? __shfl_sync(0xffffffffu, mine, (k0 + k) & 31) : 0.f;
+      if (w[k] != 0.f && in) p[k].load(a.parts, (int64_t)t * a.token_stride + (k0 + k) * a.part_stride + u * 4);
+      else p[k].zero();
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int u = threadIdx.x + v * step;
-      float z[W], xf[W];
-      x[v].widen(xf);
+    for (int k = 0; k < GROUP; ++k) {
+      float f[4];
+      p[k].widen(f);
 #pragma unroll
-      for (int i = 0; i < W; ++i) z[i] = y[v][i] * rn;
-      if (u < units) {
-        if (a.post_gain) times<W>(z, a.post_gain, u * W, a.gains16);
-        if (a.channel) times<W>(z, a.channel, u * W, a.gains16);
-      }
-#pragma unroll
-      for (int i = 0; i < W; ++i) r[v][i] = u < units ? fmaf(g, z[i], a.residual * xf[i]) : 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) x[v].widen(r[v]);
-  }
-  if (a.out) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int u = threadIdx.x + v * step;
-      if (u < units) store_unit<W>(a.out, (int64_t)t * a.out_stride + (int64_t)u * W, a.x_type, r[v]);
+      for (int e = 0; e < 4; ++e) y[e] = fmaf(w[k], f[e], y[e]);
     }
   }
+  float rn = 1.f;
+  if (a.post) {
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ss = fmaf(y[e], y[e], ss);
+    rn = rsqrtf(fmaf(row_sum(ss, red[0]), a.inv_n, a.eps));
+  }
+  x.widen(r);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] *= rn;
+  if (in) {
+    if (a.post_gain) times(y, a.post_gain, u * 4, a.gains16);
+    if (a.channel) times(y, a.channel, u * 4, a.gains16);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r[e] = in ? fmaf(g, y[e], a.residual * r[e]) : 0.f;
+  if (a.out && in) store_unit(a.out, (int64_t)t * a.out_stride + u * 4, XT, r);
   if (a.next) {
     float ss = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int e = 0; e < 4; ++e) ss = fmaf(r[e], r[e], ss);
+    rn = rsqrtf(fmaf(row_sum(ss, red[1]), a.inv_n, a.eps));
+    if (in) {
 #pragma unroll
-      for (int i = 0; i < W; ++i) ss = fmaf(r[v][i], r[v][i], ss);
-    const float rn = rsqrtf(fmaf(row_sum(ss, red[1]), a.inv_n, a.eps));
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int u = threadIdx.x + v * step;
-      if (u >= units) continue;
-      float f[W];
-#pragma unroll
-      for (int i = 0; i < W; ++i) f[i] = r[v][i] * rn;
-      if (a.pre_gain) times<W>(f, a.pre_gain, u * W, a.gains16);
-      store_unit<W>(a.next, (int64_t)t * a.next_stride + (int64_t)u * W, a.next_type, f);
+      for (int e = 0; e < 4; ++e) r[e] *= rn;
+      if (a.pre_gain) times(r, a.pre_gain, u * 4, a.gains16);
+      store_unit(a.next, (int64_t)t * a.next_stride + u * 4, a.next_type, r);
     }
   }
 }
@@ -228,15 +168,15 @@ __global__ void __launch_bounds__(512) edge_stream_kernel(const __grid_constant_
 #pragma unroll
       for (int e = 0; e < 4; ++e) gains[0][v][e] = gains[1][v][e] = 1.f;
       if (mine[v]) {
-        if (a.post_gain) times<4>(gains[0][v], a.post_gain, at, a.gains16);
-        if (a.channel) times<4>(gains[0][v], a.channel, at, a.gains16);
-        if (a.pre_gain) times<4>(gains[1][v], a.pre_gain, at, a.gains16);
+        if (a.post_gain) times(gains[0][v], a.post_gain, at, a.gains16);
+        if (a.channel) times(gains[0][v], a.channel, at, a.gains16);
+        if (a.pre_gain) times(gains[1][v], a.pre_gain, at, a.gains16);
       }
     }
   }
   struct Row {
-    Unit<XT, 4> x[V];
-    Unit<PART ? PT : XT, 4> p[PART ? V : 1];
+    Unit<XT> x[V];
+    Unit<PART ? PT : XT> p[PART ? V : 1];
     float w, token;
   };
   const auto fetch = [&](int t, Row& row) {
@@ -294,8 +234,8 @@ __global__ void __launch_bounds__(512) edge_stream_kernel(const __grid_constant_
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[v][e] *= gains[0][v][e];
           } else if (mine[v]) {
-            if (a.post_gain) times<4>(y[v], a.post_gain, (tid + v * threads) * 4, a.gains16);
-            if (a.channel) times<4>(y[v], a.channel, (tid + v * threads) * 4, a.gains16);
+            if (a.post_gain) times(y[v], a.post_gain, (tid + v * threads) * 4, a.gains16);
+            if (a.channel) times(y[v], a.channel, (tid + v * threads) * 4, a.gains16);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) r[v][e] = mine[v] ? fmaf(g, y[v][e], a.residual * r[v][e]) : 0.f;
@@ -306,7 +246,7 @@ __global__ void __launch_bounds__(512) edge_stream_kernel(const __grid_constant_
       if (PART && a.out) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
-          if (mine[v]) store_unit<4>(a.out, (int64_t)t * a.out_stride + (tid + v * threads) * 4, XT, r[v]);
+          if (mine[v]) store_unit(a.out, (int64_t)t * a.out_stride + (tid + v * threads) * 4, XT, r[v]);
       }
       if (a.next) {
         float ss = 0.f;
@@ -324,9 +264,9 @@ __global__ void __launch_bounds__(512) edge_stream_kernel(const __grid_constant_
 #pragma unroll
             for (int e = 0; e < 4; ++e) r[v][e] *= gains[1][v][e];
           } else if (a.pre_gain) {
-            times<4>(r[v], a.pre_gain, (tid + v * threads) * 4, a.gains16);
+            times(r[v], a.pre_gain, (tid + v * threads) * 4, a.gains16);
           }
-          store_unit<4>(a.next, (int64_t)t * a.next_stride + (tid + v * threads) * 4, a.next_type, r[v]);
+          store_unit(a.next, (int64_t)t * a.next_stride + (tid + v * threads) * 4, a.next_type, r[v]);
         }
       }
       turn ^= 1;
@@ -377,9 +317,9 @@ __global__ void __launch_bounds__(512) edge_ring_kernel(const __grid_constant__ 
 #pragma unroll
       for (int e = 0; e < 4; ++e) gains[0][v][e] = gains[1][v][e] = 1.f;
       if (mine[v]) {
-        if (a.post_gain) times<4>(gains[0][v], a.post_gain, at, a.gains16);
-        if (a.channel) times<4>(gains[0][v], a.channel, at, a.gains16);
-        if (a.pre_gain) times<4>(gains[1][v], a.pre_gain, at, a.gains16);
+        if (a.post_gain) times(gains[0][v], a.post_gain, at, a.gains16);
+        if (a.channel) times(gains[0][v], a.channel, at, a.gains16);
+        if (a.pre_gain) times(gains[1][v], a.pre_gain, at, a.gains16);
       }
     }
   }
@@ -439,7 +379,7 @@ __global__ void __launch_bounds__(512) edge_ring_kernel(const __grid_constant__ 
 #pragma unroll
       for (int v = 0; v < V; ++v)
         if (mine[v]) {
-          Unit<PT, 4> p;
+          Unit<PT> p;
           float f[4];
           p.load(s_ring + slot * slot_units + v * threads + tid, 0);
           p.widen(f);
@@ -455,7 +395,7 @@ __global__ void __launch_bounds__(512) edge_ring_kernel(const __grid_constant__ 
 #pragma unroll
       for (int v = 0; v < V; ++v)
         if (mine[v]) {
-          Unit<XT, 4> p;
+          Unit<XT> p;
           p.load(s_ring + slot * slot_units + v * threads + tid, 0);
           p.widen(r[v]);
         }
@@ -481,12 +421,12 @@ __global__ void __launch_bounds__(512) edge_ring_kernel(const __grid_constant__ 
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[v][e] *= gains[0][v][e];
       } else if (mine[v]) {
-        if (a.post_gain) times<4>(y[v], a.post_gain, u * 4, a.gains16);
-        if (a.channel) times<4>(y[v], a.channel, u * 4, a.gains16);
+        if (a.post_gain) times(y[v], a.post_gain, u * 4, a.gains16);
+        if (a.channel) times(y[v], a.channel, u * 4, a.gains16);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) r[v][e] = mine[v] ? fmaf(g, y[v][e], a.residual * r[v][e]) : 0.f;
-      if (a.out && mine[v]) store_unit<4>(a.out, (int64_t)t * a.out_stride + (int64_t)u * 4, XT, r[v]);
+      if (a.out && mine[v]) store_unit(a.out, (int64_t)t * a.out_stride + (int64_t)u * 4, XT, r[v]);
     }
     if (a.next) {
       float ss = 0.f;
@@ -505,9 +445,9 @@ __global__ void __launch_bounds__(512) edge_ring_kernel(const __grid_constant__ 
 #pragma unroll
           for (int e = 0; e < 4; ++e) r[v][e] *= gains[1][v][e];
         } else if (a.pre_gain) {
-          times<4>(r[v], a.pre_gain, u * 4, a.gains16);
+          times(r[v], a.pre_gain, u * 4, a.gains16);
         }
-        store_unit<4>(a.next, (int64_t)t * a.next_stride + (int64_t)u * 4, a.next_type, r[v]);
+        store_unit(a.next, (int64_t)t * a.next_stride + (int64_t)u * 4, a.next_type, r[v]);
       }
     }
   }
@@ -529,12 +469,179 @@ template <int XT, int PT>
 cudaError_t launch_ring(const NormArgs& a, cudaStream_t s) {
   const int units = a.n / 4;
   if (units <= 1024 && a.T <= 152) {
-    edge_kernel<XT, PT, 4, 1><<<a.T, (units + 31) / 32 * 32, 0, s>>>(a);
+    edge_few_kernel<XT, PT><<<a.T, (units + 31) / 32 * 32, 0, s>>>(a);
     return cudaGetLastError();
   }
   if (units > 2048) return launch_ring_v<XT, PT, 8, 3>(a, s);
   if (units > 1024) return launch_ring_v<XT, PT, 4, 3>(a, s);
   return launch_ring_v<XT, PT, 2, 6>(a, s);
+}
+
+// ---- Rows that are not on boundaries of 4 elements ----------------------------------------------------------
+// The same line of steps, copied as the 16-byte pieces that hold a row's bytes, wherever in them it starts, and
+// taken out of shared memory a column at a time: a thread has V columns, blockDim.x apart.  A thread reads what others
+// copied, so that a step costs a barrier; it also frees the slot read before.
+template <int XT, int PT, int V, int RING>
+__global__ void __launch_bounds__(512) edge_columns_kernel(const __grid_constant__ NormArgs a, int slot_bytes) {
+  extern __shared__ __align__(16) unsigned char s_bytes[];  // [ring][slot_bytes]
+  __shared__ float red[2][2][32];
+  constexpr bool PARTS = PT != NO_PARTS;
+  constexpr int P_SIZE = PT == STRATA_F32 ? 4 : 2, X_SIZE = XT == STRATA_F32 ? 4 : 2;
+  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31;
+  constexpr bool KEEP = V <= 8;
+  float gains[KEEP ? 2 : 1][KEEP ? V : 1];  // of z: post and channel; of next
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int u = tid + v * threads;
+      gains[0][v] = gains[1][v] = 1.f;
+      if (u < a.n) {
+        if (PARTS && a.post_gain) gains[0][v] = __ldg(a.post_gain + u);
+        if (PARTS && a.channel) gains[0][v] *= __ldg(a.channel + u);
+        if (a.pre_gain) gains[1][v] = __ldg(a.pre_gain + u);
+      }
+    }
+  }
+  const auto weight = [&](int t) { return t >= a.T || lane >= a.P ? 0.f : a.pw ? __ldg(a.pw + (int64_t)t * a.P + lane) : 1.f; };
+  const auto part_at = [&](int t, int k) {
+    return static_cast<const unsigned char*>(a.parts) + ((int64_t)t * a.token_stride + k * a.part_stride) * P_SIZE;
+  };
+  const auto x_at = [&](int t) { return static_cast<const unsigned char*>(a.x) + (int64_t)t * a.x_stride * X_SIZE; };
+  const uint32_t s_mine = smem_u32(s_bytes) + tid * 16;
+  // The pieces of `bytes` bytes at `from`.  The first may begin before the row: a piece that holds one byte of an
+  // allocation lies inside it at that end.  The last is cut at the row's end.
+  const auto copy = [&](int slot, const unsigned char* from, int bytes) {
+    const int off = (int)(reinterpret_cast<uintptr_t>(from) & 15);
+    const unsigned char* at = from - off + tid * 16;
+    uint32_t to = s_mine + slot * slot_bytes;
+    for (int left = bytes + off - tid * 16; left > 0; left -= threads * 16, at += threads * 16, to += threads * 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(at), "r"(left < 16 ? left : 16) : "memory");
+  };
+  int tc = blockIdx.x, cslot = 0;
+  float wc = PARTS ? weight(tc) : 0.f, wn = PARTS ? weight(tc + gridDim.x) : 0.f;
+  uint32_t todo = PARTS ? __ballot_sync(0xffffffffu, wc != 0.f) : 0u;
+  bool x_to_do = a.x != nullptr;
+  const auto copy_next = [&]() {
+    while (tc < a.T && !todo && !x_to_do) {
+      tc += gridDim.x;
+      if constexpr (PARTS) {
+        wc = wn;
+        wn = weight(tc + gridDim.x);
+        todo = __ballot_sync(0xffffffffu, wc != 0.f);
+      }
+      x_to_do = a.x != nullptr;
+    }
+    if (tc < a.T) {
+      if (todo) {
+        const int k = __ffs(todo) - 1;
+        todo &= todo - 1;
+        copy(cslot, part_at(tc, k), a.n * P_SIZE);
+      } else {
+        x_to_do = false;
+        copy(cslot, x_at(tc), a.n * X_SIZE);
+      }
+      cslot = cslot + 1 == RING ? 0 : cslot + 1;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int slot = 0, turn = 0;
+  // the step's bytes as this thread's first column finds them
+  const auto next_slot = [&](const unsigned char* from, int size) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(RING - 2) : "memory");
+    __syncthreads();
+    const unsigned char* const at = s_bytes + slot * slot_bytes + (int)(reinterpret_cast<uintptr_t>(from) & 15) + tid * size;
+    slot = slot + 1 == RING ? 0 : slot + 1;
+    copy_next();  // into the slot read before this one
+    return at;
+  };
+  for (int i = 0; i < RING - 1; ++i) copy_next();
+  float w = PARTS ? weight(blockIdx.x) : 0.f;
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
+    const float w_next = PARTS ? weight(t + gridDim.x) : 0.f;
+    const float tok = PARTS && a.token ? __ldg(a.token + t) : 1.f;
+    float y[V], r[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) y[v] = r[v] = 0.f;
+    if constexpr (PARTS) {
+      for (uint32_t parts = __ballot_sync(0xffffffffu, w != 0.f); parts; parts &= parts - 1) {
+        const int k = __ffs(parts) - 1;
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const unsigned char* const at = next_slot(part_at(t, k), P_SIZE);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (tid + v * threads < a.n) y[v] = fmaf(wk, load1(at, v * threads, PT), y[v]);
+      }
+    }
+    w = w_next;
+    if (a.x) {
+      const unsigned char* const at = next_slot(x_at(t), X_SIZE);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (tid + v * threads < a.n) r[v] = load1(at, v * threads, XT);
+    }
+    if constexpr (PARTS) {
+      const float g = a.block * (!a.token ? 1.f : a.sigmoid ? 1.f / (1.f + expf(-tok)) : tok);
+      float rn = 1.f;
+      if (a.post) {
+        float ss = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) ss = fmaf(y[v], y[v], ss);
+        rn = rsqrtf(fmaf(row_sum(ss, red[turn][0]), a.inv_n, a.eps));
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int u = tid + v * threads;
+        const bool in = u < a.n;
+        float z = y[v] * rn;
+        if constexpr (KEEP) {
+          z *= gains[0][v];
+        } else {
+          if (a.post_gain && in) z *= __ldg(a.post_gain + u);
+          if (a.channel && in) z *= __ldg(a.channel + u);
+        }
+        r[v] = in ? fmaf(g, z, a.residual * r[v]) : 0.f;
+      }
+    }
+    if (PARTS && a.out)
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (tid + v * threads < a.n) store1(a.out, (int64_t)t * a.out_stride + tid + v * threads, XT, r[v]);
+    if (a.next) {
+      float ss = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) ss = fmaf(r[v], r[v], ss);
+      const float rn = rsqrtf(fmaf(row_sum(ss, red[turn][1]), a.inv_n, a.eps));
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int u = tid + v * threads;
+        if (u >= a.n) continue;
+        float f = r[v] * rn;
+        if constexpr (KEEP) f *= gains[1][v];
+        else if (a.pre_gain) f *= __ldg(a.pre_gain + u);
+        store1(a.next, (int64_t)t * a.next_stride + u, a.next_type, f);
+      }
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+template <int XT, int PT, int V, int RING>
+cudaError_t launch_columns_v(const NormArgs& a, cudaStream_t s) {
+  const int threads = ((a.n + V - 1) / V + 31) / 32 * 32;
+  const int size = XT == STRATA_F32 || PT == STRATA_F32 ? 4 : 2, slot = (a.n * size + 15) / 16 * 16 + 16;
+  const cudaError_t err = allow_smem<edge_columns_kernel<XT, PT, V, RING>>(224 * 1024);
+  if (err != cudaSuccess) return err;
+  const int fit = 152 * resident_ctas<edge_columns_kernel<XT, PT, V, RING>>(threads, RING * slot);
+  edge_columns_kernel<XT, PT, V, RING><<<a.T < fit ? a.T : fit, threads, RING * slot, s>>>(a, slot);
+  return cudaGetLastError();
+}
+
+// Slots: 4 of up to 16 KB, or 3 of up to 64 KB.
+template <int XT, int PT>
+cudaError_t launch_columns(const NormArgs& a, cudaStream_t s) {
+  if (a.n > 8192) return launch_columns_v<XT, PT, 32, 3>(a, s);
+  if (a.n > 4096) return launch_columns_v<XT, PT, 16, 3>(a, s);
+  return launch_columns_v<XT, PT, 8, 4>(a, s);
 }
 
 // Every row of the operand starts on a boundary of four elements.
@@ -543,20 +650,11 @@ bool rows4(const void* p, int64_t stride, int type) {
   return !p || (((uintptr_t)p & (4 * size - 1)) == 0 && stride % 4 == 0);
 }
 
-// Rows that are not on boundaries of four elements go element by element.
 template <int XT, int PT>
 cudaError_t launch_parts(const NormArgs& a, bool vec, cudaStream_t s) {
-  if (vec) {
-    if constexpr (PT != NO_PARTS)
-      if (a.P > 1) return launch_ring<XT, PT>(a, s);
-    return launch_stream<XT, PT>(a, s);
-  }
-  const int V = a.n <= 4096 ? 4 : 16, threads = ((a.n + V - 1) / V + 31) / 32 * 32;
-  const int rows = threads == 32 ? 4 : 1;
-  const dim3 block(threads, rows), grid((a.T + rows - 1) / rows);
-  if (V == 4) edge_kernel<XT, PT, 1, 4><<<grid, block, 0, s>>>(a);
-  else edge_kernel<XT, PT, 1, 16><<<grid, block, 0, s>>>(a);
-  return cudaGetLastError();
+  if constexpr (PT != NO_PARTS)
+    if (vec && a.P > 1) return launch_ring<XT, PT>(a, s);
+  return vec ? launch_stream<XT, PT>(a, s) : launch_columns<XT, PT>(a, s);
 }
 
 template <int XT>
