@@ -479,23 +479,32 @@ cudaError_t launch_ring(const NormArgs& a, cudaStream_t s) {
 
 // ---- Rows that are not on boundaries of 4 elements ----------------------------------------------------------
 // The same line of steps, copied as the 16-byte pieces that hold a row's bytes, wherever in them it starts, and
-// taken out of shared memory a column at a time: a thread has V columns, blockDim.x apart.  A thread reads what others
-// copied, so that a step costs a barrier; it also frees the slot read before.
+// taken out of shared memory a column at a time: a warp has 32 V columns in a row, a thread every 32nd (so a row's
+// addresses differ by constants: what bounds these rows is the count of instructions).  A thread reads what others copied,
+// so that a step costs a barrier; it also frees the slot read before.
+template <int T, int V>
+__device__ __forceinline__ void store_columns(void* p, int64_t at, int left, const float (&f)[V]) {
+  void* const to = static_cast<unsigned char*>(p) + at * (T == STRATA_F32 ? 4 : 2);
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (32 * v < left) store1(to, 32 * v, T, f[v]);
+}
 template <int XT, int PT, int V, int RING>
-__global__ void __launch_bounds__(512) edge_columns_kernel(const __grid_constant__ NormArgs a, int slot_bytes) {
+__global__ void __launch_bounds__(512, V <= 8 ? 2 : 1) edge_columns_kernel(const __grid_constant__ NormArgs a, int slot_bytes) {
   extern __shared__ __align__(16) unsigned char s_bytes[];  // [ring][slot_bytes]
   __shared__ float red[2][2][32];
   constexpr bool PARTS = PT != NO_PARTS;
   constexpr int P_SIZE = PT == STRATA_F32 ? 4 : 2, X_SIZE = XT == STRATA_F32 ? 4 : 2;
   const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31;
-  constexpr bool KEEP = V <= 8;
+  const int first = (tid - lane) * V + lane, left = a.n - first;  // its columns: first + 32 v, while 32 v < left
+  constexpr bool KEEP = V <= 16;
   float gains[KEEP ? 2 : 1][KEEP ? V : 1];  // of z: post and channel; of next
   if constexpr (KEEP) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int u = tid + v * threads;
+      const int u = first + 32 * v;
       gains[0][v] = gains[1][v] = 1.f;
-      if (u < a.n) {
+      if (32 * v < left) {
         if (PARTS && a.post_gain) gains[0][v] = __ldg(a.post_gain + u);
         if (PARTS && a.channel) gains[0][v] *= __ldg(a.channel + u);
         if (a.pre_gain) gains[1][v] = __ldg(a.pre_gain + u);
@@ -549,7 +558,7 @@ __global__ void __launch_bounds__(512) edge_columns_kernel(const __grid_constant
   const auto next_slot = [&](const unsigned char* from, int size) {
     asm volatile("cp.async.wait_group %0;" ::"n"(RING - 2) : "memory");
     __syncthreads();
-    const unsigned char* const at = s_bytes + slot * slot_bytes + (int)(reinterpret_cast<uintptr_t>(from) & 15) + tid * size;
+    const unsigned char* const at = s_bytes + slot * slot_bytes + (int)(reinterpret_cast<uintptr_t>(from) & 15) + first * size;
     slot = slot + 1 == RING ? 0 : slot + 1;
     copy_next();  // into the slot read before this one
     return at;
@@ -569,7 +578,7 @@ __global__ void __launch_bounds__(512) edge_columns_kernel(const __grid_constant
         const unsigned char* const at = next_slot(part_at(t, k), P_SIZE);
 #pragma unroll
         for (int v = 0; v < V; ++v)
-          if (tid + v * threads < a.n) y[v] = fmaf(wk, load1(at, v * threads, PT), y[v]);
+          if (32 * v < left) y[v] = fmaf(wk, load1(at, 32 * v, PT), y[v]);
       }
     }
     w = w_next;
@@ -577,7 +586,7 @@ __global__ void __launch_bounds__(512) edge_columns_kernel(const __grid_constant
       const unsigned char* const at = next_slot(x_at(t), X_SIZE);
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (tid + v * threads < a.n) r[v] = load1(at, v * threads, XT);
+        if (32 * v < left) r[v] = load1(at, 32 * v, XT);
     }
     if constexpr (PARTS) {
       const float g = a.block * (!a.token ? 1.f : a.sigmoid ? 1.f / (1.f + expf(-tok)) : tok);
@@ -590,8 +599,8 @@ __global__ void __launch_bounds__(512) edge_columns_kernel(const __grid_constant
       }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int u = tid + v * threads;
-        const bool in = u < a.n;
+        const int u = first + 32 * v;
+        const bool in = 32 * v < left;
         float z = y[v] * rn;
         if constexpr (KEEP) {
           z *= gains[0][v];
@@ -602,10 +611,7 @@ __global__ void __launch_bounds__(512) edge_columns_kernel(const __grid_constant
         r[v] = in ? fmaf(g, z, a.residual * r[v]) : 0.f;
       }
     }
-    if (PARTS && a.out)
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (tid + v * threads < a.n) store1(a.out, (int64_t)t * a.out_stride + tid + v * threads, XT, r[v]);
+    if (PARTS && a.out) store_columns<XT>(a.out, (int64_t)t * a.out_stride + first, left, r);
     if (a.next) {
       float ss = 0.f;
 #pragma unroll
@@ -613,13 +619,14 @@ __global__ void __launch_bounds__(512) edge_columns_kernel(const __grid_constant
       const float rn = rsqrtf(fmaf(row_sum(ss, red[turn][1]), a.inv_n, a.eps));
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int u = tid + v * threads;
-        if (u >= a.n) continue;
-        float f = r[v] * rn;
-        if constexpr (KEEP) f *= gains[1][v];
-        else if (a.pre_gain) f *= __ldg(a.pre_gain + u);
-        store1(a.next, (int64_t)t * a.next_stride + u, a.next_type, f);
+        r[v] *= rn;
+        if constexpr (KEEP) r[v] *= gains[1][v];
+        else if (a.pre_gain && 32 * v < left) r[v] *= __ldg(a.pre_gain + first + 32 * v);
       }
+      const int64_t at = (int64_t)t * a.next_stride + first;
+      if (a.next_type == STRATA_F32) store_columns<STRATA_F32>(a.next, at, left, r);
+      else if (a.next_type == STRATA_BF16) store_columns<STRATA_BF16>(a.next, at, left, r);
+      else store_columns<STRATA_F16>(a.next, at, left, r);
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
