@@ -289,7 +289,8 @@ const char* strata_status_str(strata_status s);
 #define STRATA_KERNEL_COMBINE_NORM 19    /* strata_moe_combine_norm */
 #define STRATA_KERNEL_ADAPTER_SHRINK 20  /* strata_moe_adapters: A_a x */
 #define STRATA_KERNEL_ADAPTER_EXPAND 21  /* strata_moe_adapters: base + scale * B_a (A_a x) */
-#define STRATA_KERNEL_COUNT 22
+#define STRATA_KERNEL_ADAPTERS 22        /* strata_moe_adapters, short segments: both */
+#define STRATA_KERNEL_COUNT 23
 
 /* Number of kernels this process has launched through the library so far (all threads). */
 uint64_t strata_moe_launch_count(void);

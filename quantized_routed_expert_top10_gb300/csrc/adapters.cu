@@ -14,7 +14,7 @@ namespace {
 constexpr int AD_WARPS = 8;
 constexpr int AD_THREADS = 32 * AD_WARPS;
 constexpr int SPLIT_MAX = 8;           // slices of d_in
-constexpr int V_FLOATS = 1024;         // scratch per token: SPLIT_MAX * rank <= 1024
+constexpr int LONG = 32;               // tokens a segment from which the 128-row kernels are taken
 
 struct AdapterArgs {
   const uint16_t* a;
@@ -26,7 +26,7 @@ struct AdapterArgs {
   const void* x;
   const void* base;
   void* y;
-  float* v;  // [split][T][rank]
+  uint16_t* v;  // [term][T][rank]
   int* status;
   int n_seg, n_adapter, rank, d_in, d_out, T, x_type, y_type, split, k_slice;
   int early;  // base goes to L2 while the shrink kernel finishes
@@ -144,102 +144,167 @@ __device__ __forceinline__ void split8(float (&f)[8], uint32_t (&t)[TERMS][4]) {
     }
 }
 
-// Both kernels read operands straight into MMA fragments, 16 bytes a thread.  An MMA's k index may be permuted as long as
+// Operands are read straight into MMA fragments, 16 bytes a thread.  An MMA's k index may be permuted as long as
 // A and B agree: of 32 consecutive k, the thread of quarter q (lane & 3) takes the 8 at 8 q, as k 2q, 2q+1, 2q+8, 2q+9 of
 // two MMAs; so four lanes read 64 contiguous bytes of a row.
 
-// v[slice][token][r] = sum over the slice's k of A_a[r][k] x[token][k].  CTA: one tile, one slice; its warps take 32
-// k each in turn and their sums are added in warp order.
-template <int NT, int MT, int TERMS>
-__global__ void __launch_bounds__(AD_THREADS) shrink_kernel(AdapterArgs a) {
-  __shared__ float s_v[16 * MT * NT * 8];
-  Tile tile;
-  griddep_launch_dependents();
-  griddep_wait();
-  if (!find_tile<AD_THREADS>(a, blockIdx.x, 16 * MT, &tile) || tile.adapter < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int r0 = blockIdx.z * NT * 8;
-  const uint16_t* A = a.a + (int64_t)tile.adapter * a.a_stride;
-  const int k0 = blockIdx.y * a.k_slice, k1 = min(a.d_in, k0 + a.k_slice);
-  float acc[MT][NT][4];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
-  const Raw8 zero{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-  for (int k = k0 + 32 * warp + 8 * q; k - 8 * q < k1; k += 32 * AD_WARPS) {
-    const bool in = k < k1;
-    uint4 w[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int r = r0 + 8 * n + g;
-      w[n] = in && r < a.rank ? __ldg(reinterpret_cast<const uint4*>(A + (int64_t)r * a.d_in + k)) : zero.lo;
-    }
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      uint32_t t0[TERMS][4], t1[TERMS][4];
-      const int row0 = 16 * m + g, row1 = row0 + 8;
-      const Raw8 x0 = in && row0 < tile.rows ? load8(a.x, (int64_t)(tile.row + row0) * a.x_stride + k, a.x_type) : zero;
-      const Raw8 x1 = in && row1 < tile.rows ? load8(a.x, (int64_t)(tile.row + row1) * a.x_stride + k, a.x_type) : zero;
-      if constexpr (TERMS == 1) {
-        t0[0][0] = x0.lo.x; t0[0][1] = x0.lo.y; t0[0][2] = x0.lo.z; t0[0][3] = x0.lo.w;
-        t1[0][0] = x1.lo.x; t1[0][1] = x1.lo.y; t1[0][2] = x1.lo.z; t1[0][3] = x1.lo.w;
-      } else {
-        float f[8];
-        widen8(x0, a.x_type, f);
-        split8<TERMS>(f, t0);
-        widen8(x1, a.x_type, f);
-        split8<TERMS>(f, t1);
-      }
-#pragma unroll
-      for (int i = TERMS - 1; i >= 0; --i) {
-        const uint32_t a0[4] = {t0[i][0], t1[i][0], t0[i][1], t1[i][1]};
-        const uint32_t a1[4] = {t0[i][2], t1[i][2], t0[i][3], t1[i][3]};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma_bf16(acc[m][n], a0, w[n].x, w[n].y);
-          mma_bf16(acc[m][n], a1, w[n].z, w[n].w);
-        }
-      }
-    }
-  }
-  for (int i = threadIdx.x; i < 16 * MT * NT * 8; i += AD_THREADS) s_v[i] = 0.f;
-  for (int w = 0; w < AD_WARPS; ++w) {
-    __syncthreads();
-    if (w != warp) continue;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s_v[(16 * m + g + 8 * (i >> 1)) * (NT * 8) + 8 * n + 2 * q + (i & 1)] += acc[m][n][i];
-  }
-  __syncthreads();
-  const int cols = min(NT * 8, a.rank - r0);
-  float* v = a.v + ((int64_t)blockIdx.y * a.T + tile.row) * a.rank + r0;
-  for (int i = threadIdx.x; i < tile.rows * NT * 8; i += AD_THREADS) {
-    const int row = i / (NT * 8), c = i % (NT * 8);
-    if (c < cols) v[(int64_t)row * a.rank + c] = s_v[i];
-  }
+// (The lanes come together first: loops of different lengths come before.)
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Four floats of shared memory of CTA `rank` of the cluster, at the address that this CTA's `p` has there.
+__device__ __forceinline__ float4 cluster_ld4(const void* p, int rank) {
+  uint32_t at;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
 }
 
-// y = base + B_a (scale v).  CTA: one tile, a share of the columns; a warp takes 32 columns at a time, all tokens of the
-// tile.  Columns may be permuted over the MMAs' n as k above: the thread of quarter q ends with 8 consecutive columns of
-// a row (column 8 q + 2 j + i from MMA j), which it reads and writes 16 bytes at a time.
-template <int MT, int TERMS>
-__global__ void __launch_bounds__(AD_THREADS) expand_kernel(AdapterArgs a) {
+// Short segments: one cluster a tile of up to 16 MT tokens.  Each CTA takes a slice of d_in, its warps 32 k each in turn, and
+// adds their sums in warp order; the slices' sums are read from the cluster's shared memory and added in order by every
+// CTA, which then has all of scale A_a x (fp32) and takes its share of the columns, 32 a warp at a time.  Columns may be permuted
+// over the MMAs' n as k above: the thread of quarter q ends with 8 consecutive columns of a row (column 8 q + 2 j + i
+// from MMA j), which it reads and writes 16 bytes at a time.  B and base of a warp's first columns are on their way from
+// the start where registers allow.  NT: 8 NT ranks at a time.
+template <int NT, int MT, int TERMS>
+__global__ void __launch_bounds__(AD_THREADS, 2) short_kernel(AdapterArgs a) {
+  constexpr int ROWS = 16 * MT, COLS = 8 * NT;
+  constexpr bool EARLY = MT == 1 && NT <= 4;
+  extern __shared__ __align__(16) float s_f[];
+  const int pitch = a.rank + 4;
+  float* const s_warp = s_f;                              // [warp][ROWS][COLS]
+  float* const s_part = s_warp + AD_WARPS * ROWS * COLS;  // [ROWS][pitch]: this CTA's slice
+  float* const s_v = s_part + ROWS * pitch;               // [ROWS][pitch]: scale A_a x
   Tile tile;
   griddep_launch_dependents();
   griddep_wait();
-  if (!find_tile<AD_THREADS>(a, blockIdx.x, 16 * MT, &tile)) return;
-  if (tile.adapter < 0 && a.base == a.y) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const uint16_t* B = a.b + (int64_t)max(tile.adapter, 0) * a.b_stride;
-  const float sc = a.scale && tile.adapter >= 0 ? __ldg(a.scale + tile.adapter) : 1.f;
-  const int rank = tile.adapter >= 0 ? a.rank : 0;
-  for (int c0 = 32 * (blockIdx.y * AD_WARPS + warp); c0 < a.d_out; c0 += 32 * AD_WARPS * gridDim.y) {
+  // (the same for all CTAs of a cluster)
+  if (!find_tile<AD_THREADS>(a, blockIdx.y, ROWS, &tile)) return;
+  const bool product = tile.adapter >= 0;
+  if (!product && a.base == a.y) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+  const uint16_t* const A = a.a + (int64_t)max(tile.adapter, 0) * a.a_stride;
+  const uint16_t* const B = a.b + (int64_t)max(tile.adapter, 0) * a.b_stride;
+  const int rank = product ? a.rank : 0;
+  const Raw8 zero{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  const auto load_b = [&](int c0, int k, uint4 (&w)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = c0 + 8 * (g >> 1) + 2 * j + (g & 1);
+      w[j] = k < rank && c < a.d_out ? __ldg(reinterpret_cast<const uint4*>(B + (int64_t)c * a.rank + k)) : zero.lo;
+    }
+  };
+  const auto load_base = [&](int c0, Raw8 (&b)[2 * MT]) {
+    const int c = c0 + 8 * q;
+#pragma unroll
+    for (int h = 0; h < 2 * MT; ++h) {
+      const int row = g + 8 * h;
+      b[h] = a.base && c < a.d_out && row < tile.rows ? load8(a.base, (int64_t)(tile.row + row) * a.base_stride + c, a.y_type) : zero;
+    }
+  };
+  const int c_first = 32 * (warp * a.split + blockIdx.x), c_step = 32 * AD_WARPS * a.split;
+  uint4 w_first[4];
+  Raw8 base_first[2 * MT];
+  if constexpr (EARLY) {
+    load_b(c_first, 8 * q, w_first);
+    load_base(c_first, base_first);
+  }
+  if (product) {
+    const int k0 = blockIdx.x * a.k_slice, k1 = min(a.d_in, k0 + a.k_slice);
+    for (int r0 = 0; r0 < rank; r0 += COLS) {
+      float acc[MT][NT][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+#pragma unroll (MT == 1 ? 2 : 1)
+      for (int k = k0 + 32 * warp + 8 * q; k - 8 * q < k1; k += 32 * AD_WARPS) {
+        const bool in = k < k1;
+        uint4 w[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int r = r0 + 8 * n + g;
+          w[n] = in && r < rank ? __ldg(reinterpret_cast<const uint4*>(A + (int64_t)r * a.d_in + k)) : zero.lo;
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          uint32_t t0[TERMS][4], t1[TERMS][4];
+          const int row0 = 16 * m + g, row1 = row0 + 8;
+          const Raw8 x0 = in && row0 < tile.rows ? load8(a.x, (int64_t)(tile.row + row0) * a.x_stride + k, a.x_type) : zero;
+          const Raw8 x1 = in && row1 < tile.rows ? load8(a.x, (int64_t)(tile.row + row1) * a.x_stride + k, a.x_type) : zero;
+          if constexpr (TERMS == 1) {
+            t0[0][0] = x0.lo.x; t0[0][1] = x0.lo.y; t0[0][2] = x0.lo.z; t0[0][3] = x0.lo.w;
+            t1[0][0] = x1.lo.x; t1[0][1] = x1.lo.y; t1[0][2] = x1.lo.z; t1[0][3] = x1.lo.w;
+          } else {
+            float f[8];
+            widen8(x0, a.x_type, f);
+            split8<TERMS>(f, t0);
+            widen8(x1, a.x_type, f);
+            split8<TERMS>(f, t1);
+          }
+#pragma unroll
+          for (int i = TERMS - 1; i >= 0; --i) {
+            const uint32_t a0[4] = {t0[i][0], t1[i][0], t0[i][1], t1[i][1]};
+            const uint32_t a1[4] = {t0[i][2], t1[i][2], t0[i][3], t1[i][3]};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma_bf16(acc[m][n], a0, w[n].x, w[n].y);
+              mma_bf16(acc[m][n], a1, w[n].z, w[n].w);
+            }
+          }
+        }
+      }
+      float* const mine = s_warp + warp * ROWS * COLS + 2 * q;
+#pragma unroll
+      for (int h = 0; h < 2 * MT; ++h)
+        if (g + 8 * h < tile.rows)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            *reinterpret_cast<float2*>(mine + (g + 8 * h) * COLS + 8 * n) =
+                make_float2(acc[h >> 1][n][2 * (h & 1)], acc[h >> 1][n][2 * (h & 1) + 1]);
+      __syncthreads();
+      for (int i = tid; i < tile.rows * COLS; i += AD_THREADS) {
+        const int row = i / COLS, c = r0 + i % COLS;
+        float v = 0.f;
+#pragma unroll
+        for (int u = 0; u < AD_WARPS; ++u) v += s_warp[u * ROWS * COLS + i];
+        if (c < rank) s_part[row * pitch + c] = v;
+      }
+      __syncthreads();
+    }
+    cluster_sync();
+    const float sc = a.scale ? __ldg(a.scale + tile.adapter) : 1.f;
+    const int pieces = rank / 4;
+    for (int i = tid; i < tile.rows * pieces; i += AD_THREADS) {
+      const int at = i / pieces * pitch + i % pieces * 4;
+      float4 u[SPLIT_MAX], v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int s = 0; s < SPLIT_MAX; ++s) u[s] = s < a.split ? cluster_ld4(s_part + at, s) : v;
+#pragma unroll
+      for (int s = 0; s < SPLIT_MAX; ++s) v = make_float4(v.x + u[s].x, v.y + u[s].y, v.z + u[s].z, v.w + u[s].w);
+      *reinterpret_cast<float4*>(s_v + at) = make_float4(v.x * sc, v.y * sc, v.z * sc, v.w * sc);
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // waited for at the end: no CTA leaves while its sums are read
+    __syncthreads();
+  }
+  const bool wide = a.y_type == STRATA_F32;  // 24 bits of A_a x, else 16
+  for (int c0 = c_first; c0 < a.d_out; c0 += c_step) {
+    Raw8 base[2 * MT];
+    const bool have = EARLY && c0 == c_first;
+    if (have) {
+#pragma unroll
+      for (int h = 0; h < 2 * MT; ++h) base[h] = base_first[h];
+    } else {
+      load_base(c0, base);
+    }
     float acc[MT][4][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -249,34 +314,32 @@ __global__ void __launch_bounds__(AD_THREADS) expand_kernel(AdapterArgs a) {
         for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.f;
     for (int k = 8 * q; k - 8 * q < rank; k += 32) {
       uint4 w[4];
+      if (have && k < 32) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = c0 + 8 * (g >> 1) + 2 * j + (g & 1);
-        w[j] = k < rank && c < a.d_out ? __ldg(reinterpret_cast<const uint4*>(B + (int64_t)c * rank + k))
-                                       : make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < 4; ++j) w[j] = w_first[j];
+      } else {
+        load_b(c0, k, w);
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        uint32_t t[2][TERMS][4];
+        uint32_t t[2][3][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int row = 16 * m + g + 8 * h;
           float f[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] = 0.f;
-          if (k < rank && row < tile.rows)
-            for (int s = 0; s < a.split; ++s) {
-              const float4* p = reinterpret_cast<const float4*>(a.v + ((int64_t)s * a.T + tile.row + row) * rank + k);
-              const float4 u0 = __ldcg(p), u1 = __ldcg(p + 1);
-              f[0] += u0.x; f[1] += u0.y; f[2] += u0.z; f[3] += u0.w;
-              f[4] += u1.x; f[5] += u1.y; f[6] += u1.z; f[7] += u1.w;
-            }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] *= sc;
-          split8<TERMS>(f, t[h]);
+          if (k < rank && row < tile.rows) {
+            const float4* p = reinterpret_cast<const float4*>(s_v + row * pitch + k);
+            const float4 u0 = p[0], u1 = p[1];
+            f[0] = u0.x; f[1] = u0.y; f[2] = u0.z; f[3] = u0.w;
+            f[4] = u1.x; f[5] = u1.y; f[6] = u1.z; f[7] = u1.w;
+          }
+          split8<3>(f, t[h]);
         }
 #pragma unroll
-        for (int i = TERMS - 1; i >= 0; --i) {
+        for (int i = 2; i >= 0; --i) {
+          if (i == 2 && !wide) continue;
           const uint32_t a0[4] = {t[0][i][0], t[1][i][0], t[0][i][1], t[1][i][1]};
           const uint32_t a1[4] = {t[0][i][2], t[1][i][2], t[0][i][3], t[1][i][3]};
 #pragma unroll
@@ -290,19 +353,19 @@ __global__ void __launch_bounds__(AD_THREADS) expand_kernel(AdapterArgs a) {
     const int c = c0 + 8 * q;
     if (c >= a.d_out) continue;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int h = 0; h < 2 * MT; ++h) {
+      const int row = g + 8 * h;
+      if (row >= tile.rows) continue;
+      float f[8];
+      widen8(base[h], a.y_type, f);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = 16 * m + g + 8 * h;
-        if (row >= tile.rows) continue;
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = 0.f;
-        if (a.base) widen8(load8(a.base, (int64_t)(tile.row + row) * a.base_stride + c, a.y_type), a.y_type, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] += acc[m][i >> 1][2 * h + (i & 1)];
-        store8(a.y, (int64_t)(tile.row + row) * a.y_stride + c, a.y_type, f);
-      }
+      for (int i = 0; i < 8; ++i) f[i] += acc[h >> 1][i >> 1][2 * (h & 1) + (i & 1)];
+      store8(a.y, (int64_t)(tile.row + row) * a.y_stride + c, a.y_type, f);
+    }
+  }
+  if (product) {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
 }
 
@@ -331,23 +394,6 @@ __device__ __forceinline__ void copy_wait(int n) {
   else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
   else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
-// (The lanes come together first: loops of different lengths come before.)
-__device__ __forceinline__ void cluster_sync() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Four floats of shared memory of CTA `rank` of the cluster, at the address that this CTA's `p` has there.
-__device__ __forceinline__ float4 cluster_ld4(const void* p, int rank) {
-  uint32_t at;
-  float4 v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(at)
-               : "memory");
-  return v;
-}
-
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // A wait that ran out is recorded; the CTA's later waits are then skipped (the call's result is void).
@@ -544,7 +590,7 @@ __global__ void __launch_bounds__(AD_THREADS + 32, XT == STRATA_F32 ? 2 : 3) shr
     for (int e = 0; e < 8; ++e) f[e] *= sc;
     uint32_t t[3][4];
     split8<3>(f, t);
-    uint16_t* out = reinterpret_cast<uint16_t*>(a.v) + (int64_t)(tile.row + row) * a.rank + c;
+    uint16_t* out = a.v + (int64_t)(tile.row + row) * a.rank + c;
 #pragma unroll
     for (int e = 0; e < 3; ++e)
       if (e < vt) *reinterpret_cast<uint4*>(out + (int64_t)e * a.T * a.rank) = make_uint4(t[e][0], t[e][1], t[e][2], t[e][3]);
@@ -603,7 +649,7 @@ __global__ void __launch_bounds__(AD_THREADS + 32, 2) expand_tc_kernel(AdapterAr
   const uint32_t idesc = idesc_bf16(TC_ROWS, CW);
   const uint64_t v_desc = tc::smem_desc_sw128(smem_u32(sv)), b_desc = tc::smem_desc_sw128(smem_u32(sb));
   const Waiter waiter{a.status, &s_dead};
-  const uint16_t* vt = reinterpret_cast<const uint16_t*>(a.v);
+  const uint16_t* vt = a.v;
   // the warp's part of a unit: TMEM quadrant q4 (32 tokens) and 64 columns in two pieces; a lane has 8 columns of 4 rows of
   // a piece
   const int q4 = warp & 3, half = warp >> 2;
@@ -747,29 +793,58 @@ __global__ void __launch_bounds__(AD_THREADS + 32, 2) expand_tc_kernel(AdapterAr
   if (warp == 0) tc::tmem_dealloc(tmem, 2 * CW);
 }
 
+// No more tiles than this: a segment of L > 0 tokens has ceil(L / height), at most (L + height - 1) / height.
+int tiles_of(const AdapterArgs& a, int height) {
+  return (a.T + (a.n_seg < a.T ? a.n_seg : a.T) * (height - 1)) / height;
+}
+
+template <int NT, int MT, int TERMS>
+cudaError_t launch_short_v(const AdapterArgs& a, int tiles, cudaStream_t s) {
+  cudaError_t err = allow_smem<short_kernel<NT, MT, TERMS>>(110 * 1024);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.split, tiles);
+  cfg.blockDim = dim3(AD_THREADS);
+  cfg.dynamicSmemBytes = sizeof(float) * 16 * MT * (AD_WARPS * 8 * NT + 2 * (a.rank + 4));
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  STRATA_LAUNCH(KID_ADAPTERS, s, err = cudaLaunchKernelEx(&cfg, short_kernel<NT, MT, TERMS>, a));
+  return err;
+}
+
 template <int MT, int TERMS>
-void launch_shrink(const AdapterArgs& a, int tiles, cudaStream_t s) {
-  // rank in pieces of up to 64
-  const int NT = a.rank <= 16 ? 2 : a.rank <= 32 ? 4 : 8;
-  const dim3 grid(tiles, a.split, (a.rank + 8 * NT - 1) / (8 * NT));
-  if (NT == 2) launch_pdl(shrink_kernel<2, MT, TERMS>, grid, AD_THREADS, 0, s, a);
-  else if (NT == 4) launch_pdl(shrink_kernel<4, MT, TERMS>, grid, AD_THREADS, 0, s, a);
-  else launch_pdl(shrink_kernel<8, MT, TERMS>, grid, AD_THREADS, 0, s, a);
+cudaError_t launch_short_r(const AdapterArgs& a, int tiles, cudaStream_t s) {
+  return a.rank <= 16   ? launch_short_v<2, MT, TERMS>(a, tiles, s)
+         : a.rank <= 32 ? launch_short_v<4, MT, TERMS>(a, tiles, s)
+                        : launch_short_v<8, MT, TERMS>(a, tiles, s);
 }
 
 template <int MT>
-cudaError_t launch_both(const AdapterArgs& a, int tiles, int col_split, cudaStream_t s) {
-  kernel_begin(KID_ADAPTER_SHRINK, s);
-  if (a.x_type == STRATA_BF16) launch_shrink<MT, 1>(a, tiles, s);
-  else if (a.x_type == STRATA_F16) launch_shrink<MT, 2>(a, tiles, s);
-  else launch_shrink<MT, 3>(a, tiles, s);
-  kernel_end(KID_ADAPTER_SHRINK, s);
-  const dim3 grid(tiles, col_split);
-  kernel_begin(KID_ADAPTER_EXPAND, s);
-  if (a.y_type == STRATA_F32) launch_pdl(expand_kernel<MT, 3>, grid, AD_THREADS, 0, s, a);
-  else launch_pdl(expand_kernel<MT, 2>, grid, AD_THREADS, 0, s, a);
-  kernel_end(KID_ADAPTER_EXPAND, s);
-  return cudaGetLastError();
+cudaError_t launch_short(AdapterArgs a, int tiles, cudaStream_t s) {
+  // CTAs a tile: the fewest turns, a warp's 32 k and 32 columns (3 more: what a CTA costs beside them), over the waves of
+  // two CTAs an SM
+  const auto turns = [](int dim, int split) { return ((dim + 31) / 32 + AD_WARPS * split - 1) / (AD_WARPS * split); };
+  int best = 0;
+  for (int split = 1; split <= SPLIT_MAX; ++split) {
+    const int waves = (tiles * split + 303) / 304;
+    const int cost = waves * (turns(a.d_in, split) + turns(a.d_out, split) + 3);
+    if (split == 1 || cost < best) {
+      best = cost;
+      a.split = split;
+    }
+  }
+  a.k_slice = ((a.d_in + 31) / 32 + a.split - 1) / a.split * 32;
+  return a.x_type == STRATA_BF16  ? launch_short_r<MT, 1>(a, tiles, s)
+         : a.x_type == STRATA_F16 ? launch_short_r<MT, 2>(a, tiles, s)
+                                  : launch_short_r<MT, 3>(a, tiles, s);
 }
 
 constexpr size_t TC_SMEM_MAX = 226 * 1024;
@@ -819,7 +894,7 @@ cudaError_t launch_expand_tc(const AdapterArgs& a, int tiles, cudaStream_t s) {
 }
 
 cudaError_t launch_tc(AdapterArgs a, cudaStream_t s) {
-  const int tiles = a.T / TC_ROWS + (a.n_seg < a.T ? a.n_seg : a.T);
+  const int tiles = tiles_of(a, TC_ROWS);
   int split = 1;
   while (split < SPLIT_MAX && 2 * tiles * split <= 152 * (a.x_type == STRATA_F32 ? 2 : 3) && a.d_in / (2 * split) >= 256) split *= 2;
   a.split = split;
@@ -838,26 +913,16 @@ cudaError_t launch_tc(AdapterArgs a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_adapters(const strata_adapters_t& ad, const int32_t* seg_off, const int32_t* seg_adapter, int n_seg,
-                            const void* x, int T, const void* base, void* y, float* v_parts, int* status,
+                            const void* x, int T, const void* base, void* y, uint16_t* v_terms, int* status,
                             cudaStream_t s) {
   AdapterArgs a{};
   a.a = ad.a; a.b = ad.b; a.scale = ad.scale; a.a_stride = ad.a_stride; a.b_stride = ad.b_stride;
   a.x_stride = ad.x_stride; a.base_stride = ad.base_stride; a.y_stride = ad.y_stride;
   a.seg_off = seg_off; a.seg_adapter = seg_adapter; a.n_seg = n_seg; a.n_adapter = ad.n_adapter;
-  a.x = x; a.base = base; a.y = y; a.v = v_parts; a.status = status;
+  a.x = x; a.base = base; a.y = y; a.v = v_terms; a.status = status;
   a.rank = ad.rank; a.d_in = ad.d_in; a.d_out = ad.d_out; a.T = T; a.x_type = ad.x_type; a.y_type = ad.y_type;
-  if (T >= 32 * n_seg) return launch_tc(a, s);
-  // segments of L tokens make ceil(L / height) tiles: at most T / height + (segments that are not empty)
-  const int height = T > 2 * 16 * n_seg ? 32 : 16;
-  const int tiles = T / height + (n_seg < T ? n_seg : T);
-  int split = 1;
-  while (split < SPLIT_MAX && tiles * split < 304 && ad.d_in / (2 * split) >= 256 && 2 * split * ad.rank <= V_FLOATS)
-    split *= 2;
-  a.split = split;
-  a.k_slice = ((ad.d_in + split - 1) / split + 31) / 32 * 32;
-  int col_split = 1;
-  while (tiles * col_split < 304 && 32 * AD_WARPS * col_split < ad.d_out) ++col_split;
-  return height == 32 ? launch_both<2>(a, tiles, col_split, s) : launch_both<1>(a, tiles, col_split, s);
+  if (T >= LONG * n_seg) return launch_tc(a, s);
+  return T > 2 * 16 * n_seg ? launch_short<2>(a, tiles_of(a, 32), s) : launch_short<1>(a, tiles_of(a, 16), s);
 }
 
 }  // namespace strata

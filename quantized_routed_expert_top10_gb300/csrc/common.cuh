@@ -252,7 +252,7 @@ namespace strata {
 enum KernelId : int {
   KID_DECODE_LAYER = 0, KID_ROUTE_DECODE, KID_ROUTER_PREP, KID_ROUTER_TC, KID_TOP_K, KID_GROUP_HIST, KID_GROUP_SCAN,
   KID_GROUP_SCATTER, KID_TC_PREPARE, KID_TC_GATHER, KID_TC_GATEUP, KID_TC_DOWN, KID_COMBINE, KID_PACK, KID_HOST_COPY,
-  KID_WAIT_SELFTEST, KID_BLOB_CRC32, KID_SELECT, KID_NORM, KID_COMBINE_NORM, KID_ADAPTER_SHRINK, KID_ADAPTER_EXPAND,
+  KID_WAIT_SELFTEST, KID_BLOB_CRC32, KID_SELECT, KID_NORM, KID_COMBINE_NORM, KID_ADAPTER_SHRINK, KID_ADAPTER_EXPAND, KID_ADAPTERS,
   KID_COUNT
 };
 void kernel_begin(int kid, cudaStream_t s);
@@ -379,7 +379,7 @@ cudaError_t launch_combine_norm(const strata_combine_norm_t& cn, const void* par
                                 const float* token_gate, const float* pre_gain, void* out, void* next, cudaStream_t s);
 // v_parts: fp32 scratch of 1024 floats per token.
 cudaError_t launch_adapters(const strata_adapters_t& ad, const int32_t* seg_off, const int32_t* seg_adapter, int n_seg,
-                            const void* x, int T, const void* base, void* y, float* v_parts, int* status,
+                            const void* x, int T, const void* base, void* y, uint16_t* v_terms, int* status,
                             cudaStream_t s);
 cudaError_t launch_pack_device(const uint8_t* canonical, int64_t src_stride, uint8_t* packed,
                                int64_t dst_stride, int64_t n_blobs, cudaStream_t s);

@@ -21,7 +21,7 @@ static_assert(KID_DECODE_LAYER == STRATA_KERNEL_DECODE_LAYER && KID_ROUTE_DECODE
                   KID_BLOB_CRC32 == STRATA_KERNEL_BLOB_CRC32 && KID_SELECT == STRATA_KERNEL_SELECT &&
                   KID_NORM == STRATA_KERNEL_NORM && KID_COMBINE_NORM == STRATA_KERNEL_COMBINE_NORM &&
                   KID_ADAPTER_SHRINK == STRATA_KERNEL_ADAPTER_SHRINK &&
-                  KID_ADAPTER_EXPAND == STRATA_KERNEL_ADAPTER_EXPAND &&
+                  KID_ADAPTER_EXPAND == STRATA_KERNEL_ADAPTER_EXPAND && KID_ADAPTERS == STRATA_KERNEL_ADAPTERS &&
                   KID_COUNT == STRATA_KERNEL_COUNT,
               "kernel ids of the ABI and the library differ");
 

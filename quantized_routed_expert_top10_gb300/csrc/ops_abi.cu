@@ -134,7 +134,7 @@ strata_status strata_moe_adapters(const strata_adapters_t* ad, const int32_t* se
   const Span sb = span(base, T, ad->base_stride, ad->d_out, ad->y_type);
   if (overlap(sx, sy) || partly(sb, sy)) return STRATA_E_INVAL;
   char* w = (char*)ws;
-  return launched(launch_adapters(*ad, seg_off, seg_adapter, n_seg, x, T, base, y, (float*)(w + L.logits),
+  return launched(launch_adapters(*ad, seg_off, seg_adapter, n_seg, x, T, base, y, (uint16_t*)(w + L.logits),
                                   (int*)(w + L.status), (cudaStream_t)stream));
 }
 
