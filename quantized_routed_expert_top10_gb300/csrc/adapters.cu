@@ -4,6 +4,8 @@
 // fixed order), and expand, base + B_a (scale v).  Both walk tiles of up to 16 MT tokens of one segment; the products
 // are warp-level bf16 MMAs with fp32 accumulators.  A wider activation is the exact sum of bf16 terms (an fp16 two, an
 // fp32 three), each multiplied on its own.
+#include <atomic>
+
 #include "device_common.cuh"
 #include "elements.cuh"
 #include "tc_common.cuh"
@@ -14,7 +16,7 @@ namespace {
 constexpr int AD_WARPS = 8;
 constexpr int AD_THREADS = 32 * AD_WARPS;
 constexpr int SPLIT_MAX = 8;           // slices of d_in
-constexpr int LONG = 32;               // tokens a segment from which the 128-row kernels are taken
+constexpr int LONG = 32;               // tokens a segment from which 128-row tiles may be taken
 
 struct AdapterArgs {
   const uint16_t* a;
@@ -165,16 +167,19 @@ __device__ __forceinline__ float4 cluster_ld4(const void* p, int rank) {
   return v;
 }
 
-// Short segments: one cluster a tile of up to 16 MT tokens.  Each CTA takes a slice of d_in, its warps 32 k each in turn, and
+// Short segments: one cluster a tile of up to 8 H tokens.  Each CTA takes a slice of d_in, its warps 32 k each in turn, and
 // adds their sums in warp order; the slices' sums are read from the cluster's shared memory and added in order by every
 // CTA, which then has all of scale A_a x (fp32) and takes its share of the columns, 32 a warp at a time.  Columns may be permuted
 // over the MMAs' n as k above: the thread of quarter q ends with 8 consecutive columns of a row (column 8 q + 2 j + i
 // from MMA j), which it reads and writes 16 bytes at a time.  B and base of a warp's first columns are on their way from
 // the start where registers allow.  NT: 8 NT ranks at a time.
-template <int NT, int MT, int TERMS>
+template <int NT, int H, int TERMS, bool WIDE>
 __global__ void __launch_bounds__(AD_THREADS, 2) short_kernel(AdapterArgs a) {
-  constexpr int ROWS = 16 * MT, COLS = 8 * NT;
-  constexpr bool EARLY = MT == 1 && NT <= 4;
+  constexpr int ROWS = 8 * H, COLS = 8 * NT, MT = (H + 1) / 2;
+  constexpr int V_TERMS = WIDE ? 3 : 2;  // of an fp32 y: 24 bits of A_a x, else 16
+  constexpr bool EARLY = H == 1 && NT <= 4;
+  constexpr int XT = TERMS == 1 ? STRATA_BF16 : TERMS == 2 ? STRATA_F16 : STRATA_F32;
+  constexpr int TURNS = H > 1 || NT > 4 ? 1 : NT == 2 ? 3 : 2;  // whose reads are in flight together
   extern __shared__ __align__(16) float s_f[];
   const int pitch = a.rank + 4;
   float* const s_warp = s_f;                              // [warp][ROWS][COLS]
@@ -199,20 +204,20 @@ __global__ void __launch_bounds__(AD_THREADS, 2) short_kernel(AdapterArgs a) {
       w[j] = k < rank && c < a.d_out ? __ldg(reinterpret_cast<const uint4*>(B + (int64_t)c * a.rank + k)) : zero.lo;
     }
   };
-  const auto load_base = [&](int c0, Raw8 (&b)[2 * MT]) {
+  const auto load_base = [&](int c0, Raw8 (&b)[H]) {
     const int c = c0 + 8 * q;
 #pragma unroll
-    for (int h = 0; h < 2 * MT; ++h) {
+    for (int h = 0; h < H; ++h) {
       const int row = g + 8 * h;
-      b[h] = a.base && c < a.d_out && row < tile.rows ? load8(a.base, (int64_t)(tile.row + row) * a.base_stride + c, a.y_type) : zero;
+      b[h] = a.base && c < a.d_out && row < tile.rows ? load8(a.base, (int64_t)(tile.row + row) * a.base_stride + c, WIDE ? STRATA_F32 : a.y_type) : zero;
     }
   };
   const int c_first = 32 * (warp * a.split + blockIdx.x), c_step = 32 * AD_WARPS * a.split;
-  uint4 w_first[4];
-  Raw8 base_first[2 * MT];
+  uint4 w_ahead[4], w_next[4];  // of the warp's next columns and the ones after them
+  Raw8 base_ahead[H], base_next[H];
   if constexpr (EARLY) {
-    load_b(c_first, 8 * q, w_first);
-    load_base(c_first, base_first);
+    load_b(c_first, 8 * q, w_ahead);
+    load_base(c_first, base_ahead);
   }
   if (product) {
     const int k0 = blockIdx.x * a.k_slice, k1 = min(a.d_in, k0 + a.k_slice);
@@ -224,46 +229,66 @@ __global__ void __launch_bounds__(AD_THREADS, 2) short_kernel(AdapterArgs a) {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
-#pragma unroll (MT == 1 ? 2 : 1)
-      for (int k = k0 + 32 * warp + 8 * q; k - 8 * q < k1; k += 32 * AD_WARPS) {
-        const bool in = k < k1;
-        uint4 w[NT];
+      for (int kt = k0 + 32 * warp; kt < k1; kt += TURNS * 32 * AD_WARPS) {
+        uint4 w[TURNS][NT];
+        Raw8 x[TURNS][H];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int r = r0 + 8 * n + g;
-          w[n] = in && r < rank ? __ldg(reinterpret_cast<const uint4*>(A + (int64_t)r * a.d_in + k)) : zero.lo;
-        }
+        for (int u = 0; u < TURNS; ++u) {
+          const int k = kt + u * 32 * AD_WARPS + 8 * q;
+          const bool in = k < k1;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          uint32_t t0[TERMS][4], t1[TERMS][4];
-          const int row0 = 16 * m + g, row1 = row0 + 8;
-          const Raw8 x0 = in && row0 < tile.rows ? load8(a.x, (int64_t)(tile.row + row0) * a.x_stride + k, a.x_type) : zero;
-          const Raw8 x1 = in && row1 < tile.rows ? load8(a.x, (int64_t)(tile.row + row1) * a.x_stride + k, a.x_type) : zero;
-          if constexpr (TERMS == 1) {
-            t0[0][0] = x0.lo.x; t0[0][1] = x0.lo.y; t0[0][2] = x0.lo.z; t0[0][3] = x0.lo.w;
-            t1[0][0] = x1.lo.x; t1[0][1] = x1.lo.y; t1[0][2] = x1.lo.z; t1[0][3] = x1.lo.w;
-          } else {
-            float f[8];
-            widen8(x0, a.x_type, f);
-            split8<TERMS>(f, t0);
-            widen8(x1, a.x_type, f);
-            split8<TERMS>(f, t1);
+          for (int n = 0; n < NT; ++n) {
+            const int r = r0 + 8 * n + g;
+            w[u][n] = in && r < rank ? __ldg(reinterpret_cast<const uint4*>(A + (int64_t)r * a.d_in + k)) : zero.lo;
           }
 #pragma unroll
-          for (int i = TERMS - 1; i >= 0; --i) {
-            const uint32_t a0[4] = {t0[i][0], t1[i][0], t0[i][1], t1[i][1]};
-            const uint32_t a1[4] = {t0[i][2], t1[i][2], t0[i][3], t1[i][3]};
+          for (int h = 0; h < H; ++h) {
+            const int row = g + 8 * h;
+            x[u][h] = in && row < tile.rows ? load8(a.x, (int64_t)(tile.row + row) * a.x_stride + k, XT) : zero;
+          }
+        }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma_bf16(acc[m][n], a0, w[n].x, w[n].y);
-              mma_bf16(acc[m][n], a1, w[n].z, w[n].w);
+        for (int u = 0; u < TURNS; ++u) {
+          if (u && kt + u * 32 * AD_WARPS >= k1) break;
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            uint32_t t[2][TERMS][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (2 * m + h >= H) {
+#pragma unroll
+                for (int i = 0; i < TERMS; ++i) t[h][i][0] = t[h][i][1] = t[h][i][2] = t[h][i][3] = 0u;
+                continue;
+              }
+              const Raw8& f8 = x[u][(2 * m + h) % H];
+              if constexpr (TERMS == 1) {
+                t[h][0][0] = f8.lo.x; t[h][0][1] = f8.lo.y; t[h][0][2] = f8.lo.z; t[h][0][3] = f8.lo.w;
+              } else {
+                float f[8];
+                widen8(f8, XT, f);
+                split8<TERMS>(f, t[h]);
+              }
+            }
+#pragma unroll
+            for (int i = TERMS - 1; i >= 0; --i) {
+              const uint32_t a0[4] = {t[0][i][0], t[1][i][0], t[0][i][1], t[1][i][1]};
+              const uint32_t a1[4] = {t[0][i][2], t[1][i][2], t[0][i][3], t[1][i][3]};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                mma_bf16(acc[m][n], a0, w[u][n].x, w[u][n].y);
+                mma_bf16(acc[m][n], a1, w[u][n].z, w[u][n].w);
+              }
             }
           }
         }
       }
+      if (EARLY && r0 + COLS >= rank) {  // while the sums are exchanged
+        load_b(c_first + c_step, 8 * q, w_next);
+        load_base(c_first + c_step, base_next);
+      }
       float* const mine = s_warp + warp * ROWS * COLS + 2 * q;
 #pragma unroll
-      for (int h = 0; h < 2 * MT; ++h)
+      for (int h = 0; h < H; ++h)
         if (g + 8 * h < tile.rows)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
@@ -292,16 +317,20 @@ __global__ void __launch_bounds__(AD_THREADS, 2) short_kernel(AdapterArgs a) {
       *reinterpret_cast<float4*>(s_v + at) = make_float4(v.x * sc, v.y * sc, v.z * sc, v.w * sc);
     }
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // waited for at the end: no CTA leaves while its sums are read
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // waited for at the end: no CTA leaves while its sums are read
     __syncthreads();
   }
-  const bool wide = a.y_type == STRATA_F32;  // 24 bits of A_a x, else 16
+  if (EARLY && !product) load_base(c_first + c_step, base_next);
   for (int c0 = c_first; c0 < a.d_out; c0 += c_step) {
-    Raw8 base[2 * MT];
-    const bool have = EARLY && c0 == c_first;
-    if (have) {
+    Raw8 base[H];
+    uint4 w[4];
+    if constexpr (EARLY) {  // (rank <= 32: one step of k)
 #pragma unroll
-      for (int h = 0; h < 2 * MT; ++h) base[h] = base_first[h];
+      for (int j = 0; j < 4; ++j) w[j] = w_ahead[j], w_ahead[j] = w_next[j];
+#pragma unroll
+      for (int h = 0; h < H; ++h) base[h] = base_ahead[h], base_ahead[h] = base_next[h];
+      load_b(c0 + 2 * c_step, 8 * q, w_next);
+      load_base(c0 + 2 * c_step, base_next);
     } else {
       load_base(c0, base);
     }
@@ -313,19 +342,18 @@ __global__ void __launch_bounds__(AD_THREADS, 2) short_kernel(AdapterArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.f;
     for (int k = 8 * q; k - 8 * q < rank; k += 32) {
-      uint4 w[4];
-      if (have && k < 32) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = w_first[j];
-      } else {
-        load_b(c0, k, w);
-      }
+      if constexpr (!EARLY) load_b(c0, k, w);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        uint32_t t[2][3][4];
+        uint32_t t[2][V_TERMS][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int row = 16 * m + g + 8 * h;
+          if (2 * m + h >= H) {
+#pragma unroll
+            for (int i = 0; i < V_TERMS; ++i) t[h][i][0] = t[h][i][1] = t[h][i][2] = t[h][i][3] = 0u;
+            continue;
+          }
           float f[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] = 0.f;
@@ -335,11 +363,10 @@ __global__ void __launch_bounds__(AD_THREADS, 2) short_kernel(AdapterArgs a) {
             f[0] = u0.x; f[1] = u0.y; f[2] = u0.z; f[3] = u0.w;
             f[4] = u1.x; f[5] = u1.y; f[6] = u1.z; f[7] = u1.w;
           }
-          split8<3>(f, t[h]);
+          split8<V_TERMS>(f, t[h]);
         }
 #pragma unroll
-        for (int i = 2; i >= 0; --i) {
-          if (i == 2 && !wide) continue;
+        for (int i = V_TERMS - 1; i >= 0; --i) {
           const uint32_t a0[4] = {t[0][i][0], t[1][i][0], t[0][i][1], t[1][i][1]};
           const uint32_t a1[4] = {t[0][i][2], t[1][i][2], t[0][i][3], t[1][i][3]};
 #pragma unroll
@@ -353,14 +380,14 @@ __global__ void __launch_bounds__(AD_THREADS, 2) short_kernel(AdapterArgs a) {
     const int c = c0 + 8 * q;
     if (c >= a.d_out) continue;
 #pragma unroll
-    for (int h = 0; h < 2 * MT; ++h) {
+    for (int h = 0; h < H; ++h) {
       const int row = g + 8 * h;
       if (row >= tile.rows) continue;
       float f[8];
-      widen8(base[h], a.y_type, f);
+      widen8(base[h], WIDE ? STRATA_F32 : a.y_type, f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] += acc[h >> 1][i >> 1][2 * (h & 1) + (i & 1)];
-      store8(a.y, (int64_t)(tile.row + row) * a.y_stride + c, a.y_type, f);
+      store8(a.y, (int64_t)(tile.row + row) * a.y_stride + c, WIDE ? STRATA_F32 : a.y_type, f);
     }
   }
   if (product) {
@@ -798,53 +825,69 @@ int tiles_of(const AdapterArgs& a, int height) {
   return (a.T + (a.n_seg < a.T ? a.n_seg : a.T) * (height - 1)) / height;
 }
 
-template <int NT, int MT, int TERMS>
-cudaError_t launch_short_v(const AdapterArgs& a, int tiles, cudaStream_t s) {
-  cudaError_t err = allow_smem<short_kernel<NT, MT, TERMS>>(110 * 1024);
+// Clusters of `split` CTAs that the device holds at a time (a cluster lies within a part of it, so not all of two CTAs an SM).
+template <int NT, int H, int TERMS, bool WIDE>
+int resident_clusters(cudaLaunchConfig_t cfg, int split) {
+  static std::atomic<int> known[SPLIT_MAX + 1];
+  int n = known[split].load(std::memory_order_relaxed);
+  if (n) return n;
+  cfg.gridDim = dim3(split, 1);
+  cfg.attrs[1].val.clusterDim.x = split;
+  if (cudaOccupancyMaxActiveClusters(&n, short_kernel<NT, H, TERMS, WIDE>, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = 1;
+  }
+  known[split].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+template <int NT, int H, int TERMS, bool WIDE>
+cudaError_t launch_short_v(AdapterArgs a, cudaStream_t s) {
+  cudaError_t err = allow_smem<short_kernel<NT, H, TERMS, WIDE>>(110 * 1024);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.split, tiles);
   cfg.blockDim = dim3(AD_THREADS);
-  cfg.dynamicSmemBytes = sizeof(float) * 16 * MT * (AD_WARPS * 8 * NT + 2 * (a.rank + 4));
+  cfg.dynamicSmemBytes = sizeof(float) * 8 * H * (AD_WARPS * 8 * NT + 2 * (a.rank + 4));
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = a.split;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  attr[1].val.clusterDim.x = attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  STRATA_LAUNCH(KID_ADAPTERS, s, err = cudaLaunchKernelEx(&cfg, short_kernel<NT, MT, TERMS>, a));
+  // CTAs a tile: as many as leave all tiles resident at once, where a segment's last tile is taken to be half full (a second
+  // round costs more than shorter slices gain: 64 single tokens 7.2 us with 4 CTAs each, 11.5 with 5; a tile alone 15.6, 4.1
+  // with 8).  No more than warps have turns.
+  const int m = a.n_seg < a.T ? a.n_seg : a.T, half = a.T / (8 * H) + m / 2, tiles = half > m ? half : m;
+  const int most = ((a.d_in > a.d_out ? a.d_in : a.d_out) + 32 * AD_WARPS - 1) / (32 * AD_WARPS);
+  a.split = 1;
+  while (a.split < SPLIT_MAX && a.split < most && tiles + tiles / 32 <= resident_clusters<NT, H, TERMS, WIDE>(cfg, a.split + 1))
+    ++a.split;
+  a.k_slice = ((a.d_in + 31) / 32 + a.split - 1) / a.split * 32;
+  cfg.gridDim = dim3(a.split, tiles_of(a, 8 * H));
+  attr[1].val.clusterDim.x = a.split;
+  STRATA_LAUNCH(KID_ADAPTERS, s, err = cudaLaunchKernelEx(&cfg, short_kernel<NT, H, TERMS, WIDE>, a));
   return err;
 }
 
-template <int MT, int TERMS>
-cudaError_t launch_short_r(const AdapterArgs& a, int tiles, cudaStream_t s) {
-  return a.rank <= 16   ? launch_short_v<2, MT, TERMS>(a, tiles, s)
-         : a.rank <= 32 ? launch_short_v<4, MT, TERMS>(a, tiles, s)
-                        : launch_short_v<8, MT, TERMS>(a, tiles, s);
+template <int H, int TERMS, bool WIDE>
+cudaError_t launch_short_r(const AdapterArgs& a, cudaStream_t s) {
+  return a.rank <= 16   ? launch_short_v<2, H, TERMS, WIDE>(a, s)
+         : a.rank <= 32 ? launch_short_v<4, H, TERMS, WIDE>(a, s)
+                        : launch_short_v<8, H, TERMS, WIDE>(a, s);
 }
 
-template <int MT>
-cudaError_t launch_short(AdapterArgs a, int tiles, cudaStream_t s) {
-  // CTAs a tile: the fewest turns, a warp's 32 k and 32 columns (3 more: what a CTA costs beside them), over the waves of
-  // two CTAs an SM
-  const auto turns = [](int dim, int split) { return ((dim + 31) / 32 + AD_WARPS * split - 1) / (AD_WARPS * split); };
-  int best = 0;
-  for (int split = 1; split <= SPLIT_MAX; ++split) {
-    const int waves = (tiles * split + 303) / 304;
-    const int cost = waves * (turns(a.d_in, split) + turns(a.d_out, split) + 3);
-    if (split == 1 || cost < best) {
-      best = cost;
-      a.split = split;
-    }
-  }
-  a.k_slice = ((a.d_in + 31) / 32 + a.split - 1) / a.split * 32;
-  return a.x_type == STRATA_BF16  ? launch_short_r<MT, 1>(a, tiles, s)
-         : a.x_type == STRATA_F16 ? launch_short_r<MT, 2>(a, tiles, s)
-                                  : launch_short_r<MT, 3>(a, tiles, s);
+template <int H, int TERMS>
+cudaError_t launch_short_y(const AdapterArgs& a, cudaStream_t s) {
+  return a.y_type == STRATA_F32 ? launch_short_r<H, TERMS, true>(a, s) : launch_short_r<H, TERMS, false>(a, s);
+}
+
+template <int H>
+cudaError_t launch_short(const AdapterArgs& a, cudaStream_t s) {
+  return a.x_type == STRATA_BF16  ? launch_short_y<H, 1>(a, s)
+         : a.x_type == STRATA_F16 ? launch_short_y<H, 2>(a, s)
+                                  : launch_short_y<H, 3>(a, s);
 }
 
 constexpr size_t TC_SMEM_MAX = 226 * 1024;
@@ -921,8 +964,10 @@ cudaError_t launch_adapters(const strata_adapters_t& ad, const int32_t* seg_off,
   a.seg_off = seg_off; a.seg_adapter = seg_adapter; a.n_seg = n_seg; a.n_adapter = ad.n_adapter;
   a.x = x; a.base = base; a.y = y; a.v = v_terms; a.status = status;
   a.rank = ad.rank; a.d_in = ad.d_in; a.d_out = ad.d_out; a.T = T; a.x_type = ad.x_type; a.y_type = ad.y_type;
-  if (T >= LONG * n_seg) return launch_tc(a, s);
-  return T > 2 * 16 * n_seg ? launch_short<2>(a, tiles_of(a, 32), s) : launch_short<1>(a, tiles_of(a, 16), s);
+  // The 128-row kernels cost a call more (about 20 us) and a token's rank less than warp-level MMAs.
+  const bool many = (int64_t)T * a.rank > 256 * 1024 && (a.rank > 64 || a.x_type != STRATA_F32);
+  if (many && T >= LONG * n_seg) return launch_tc(a, s);
+  return T > 8 * n_seg ? launch_short<4>(a, s) : launch_short<1>(a, s);
 }
 
 }  // namespace strata
