@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(AD_THREADS, 2) short_kernel(AdapterArgs a) {
   constexpr int V_TERMS = WIDE ? 3 : 2;  // of an fp32 y: 24 bits of A_a x, else 16
   constexpr bool EARLY = H == 1 && NT <= 4;
   constexpr int XT = TERMS == 1 ? STRATA_BF16 : TERMS == 2 ? STRATA_F16 : STRATA_F32;
-  constexpr int TURNS = H > 1 || NT > 4 ? 1 : NT == 2 ? 3 : 2;  // whose reads are in flight together
+  constexpr int TURNS = H > 1 || NT > 4 ? 1 : NT == 2 && TERMS < 3 ? 3 : 2;  // whose reads are in flight together
   extern __shared__ __align__(16) float s_f[];
   const int pitch = a.rank + 4;
   float* const s_warp = s_f;                              // [warp][ROWS][COLS]
@@ -197,30 +197,37 @@ __global__ void __launch_bounds__(AD_THREADS, 2) short_kernel(AdapterArgs a) {
   const uint16_t* const B = a.b + (int64_t)max(tile.adapter, 0) * a.b_stride;
   const int rank = product ? a.rank : 0;
   const Raw8 zero{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-  const auto load_b = [&](int c0, int k, uint4 (&w)[4]) {
+  // (d_out and the ranks come in eights: the pieces of a column of four MMAs are all inside or all outside.)
+  const uint16_t* const b_at = B + (int64_t)(8 * (g >> 1) + (g & 1)) * a.rank + 8 * q;
+  const auto load_b = [&](int c0, int kk, uint4 (&w)[4]) {
+    const bool in = kk + 8 * q < rank && c0 + 8 * (g >> 1) < a.d_out;
+    const uint16_t* const at = b_at + (int64_t)c0 * a.rank + kk;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = c0 + 8 * (g >> 1) + 2 * j + (g & 1);
-      w[j] = k < rank && c < a.d_out ? __ldg(reinterpret_cast<const uint4*>(B + (int64_t)c * a.rank + k)) : zero.lo;
-    }
+    for (int j = 0; j < 4; ++j) w[j] = in ? __ldg(reinterpret_cast<const uint4*>(at + 2 * j * a.rank)) : zero.lo;
   };
+  constexpr int Y_SIZE = WIDE ? 4 : 2;
+  const char* const base_at = a.base ? static_cast<const char*>(a.base) + ((int64_t)(tile.row + g) * a.base_stride + 8 * q) * Y_SIZE : nullptr;
+  char* const y_at = static_cast<char*>(a.y) + ((int64_t)(tile.row + g) * a.y_stride + 8 * q) * Y_SIZE;
   const auto load_base = [&](int c0, Raw8 (&b)[H]) {
-    const int c = c0 + 8 * q;
+    const bool in = base_at && c0 + 8 * q < a.d_out;
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const int row = g + 8 * h;
-      b[h] = a.base && c < a.d_out && row < tile.rows ? load8(a.base, (int64_t)(tile.row + row) * a.base_stride + c, WIDE ? STRATA_F32 : a.y_type) : zero;
-    }
+    for (int h = 0; h < H; ++h)
+      b[h] = in && g + 8 * h < tile.rows
+                 ? load8(base_at + (8 * h * a.base_stride + c0) * Y_SIZE, 0, WIDE ? STRATA_F32 : STRATA_BF16)  // (as raw bytes)
+                 : zero;
   };
   const int c_first = 32 * (warp * a.split + blockIdx.x), c_step = 32 * AD_WARPS * a.split;
   uint4 w_ahead[4], w_next[4];  // of the warp's next columns and the ones after them
   Raw8 base_ahead[H], base_next[H];
   if constexpr (EARLY) {
-    load_b(c_first, 8 * q, w_ahead);
+    load_b(c_first, 0, w_ahead);
     load_base(c_first, base_ahead);
   }
   if (product) {
     const int k0 = blockIdx.x * a.k_slice, k1 = min(a.d_in, k0 + a.k_slice);
+    constexpr int X_SIZE = TERMS == 3 ? 4 : 2;
+    const uint16_t* const a_at = A + (int64_t)g * a.d_in + 8 * q;
+    const char* const x_at = static_cast<const char*>(a.x) + ((int64_t)(tile.row + g) * a.x_stride + 8 * q) * X_SIZE;
     for (int r0 = 0; r0 < rank; r0 += COLS) {
       float acc[MT][NT][4];
 #pragma unroll
@@ -234,18 +241,15 @@ __global__ void __launch_bounds__(AD_THREADS, 2) short_kernel(AdapterArgs a) {
         Raw8 x[TURNS][H];
 #pragma unroll
         for (int u = 0; u < TURNS; ++u) {
-          const int k = kt + u * 32 * AD_WARPS + 8 * q;
-          const bool in = k < k1;
+          const int k = kt + u * 32 * AD_WARPS;
+          const bool in = k + 8 * q < k1;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const int r = r0 + 8 * n + g;
-            w[u][n] = in && r < rank ? __ldg(reinterpret_cast<const uint4*>(A + (int64_t)r * a.d_in + k)) : zero.lo;
-          }
+          for (int n = 0; n < NT; ++n)
+            w[u][n] = in && r0 + 8 * n + g < rank
+                          ? __ldg(reinterpret_cast<const uint4*>(a_at + (int64_t)(r0 + 8 * n) * a.d_in + k)) : zero.lo;
 #pragma unroll
-          for (int h = 0; h < H; ++h) {
-            const int row = g + 8 * h;
-            x[u][h] = in && row < tile.rows ? load8(a.x, (int64_t)(tile.row + row) * a.x_stride + k, XT) : zero;
-          }
+          for (int h = 0; h < H; ++h)
+            x[u][h] = in && g + 8 * h < tile.rows ? load8(x_at + (8 * h * a.x_stride + k) * X_SIZE, 0, XT) : zero;
         }
 #pragma unroll
         for (int u = 0; u < TURNS; ++u) {
@@ -283,7 +287,7 @@ __global__ void __launch_bounds__(AD_THREADS, 2) short_kernel(AdapterArgs a) {
         }
       }
       if (EARLY && r0 + COLS >= rank) {  // while the sums are exchanged
-        load_b(c_first + c_step, 8 * q, w_next);
+        load_b(c_first + c_step, 0, w_next);
         load_base(c_first + c_step, base_next);
       }
       float* const mine = s_warp + warp * ROWS * COLS + 2 * q;
@@ -321,16 +325,37 @@ __global__ void __launch_bounds__(AD_THREADS, 2) short_kernel(AdapterArgs a) {
     __syncthreads();
   }
   if (EARLY && !product) load_base(c_first + c_step, base_next);
+  // A_a x of rows 16 m .. and k-step kk as MMA operands
+  const auto load_v = [&](int m, int kk, uint32_t (&t)[2][V_TERMS][4]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = 16 * m + g + 8 * h, k = kk + 8 * q;
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = 0.f;
+      if (2 * m + h < H && k < rank && row < tile.rows) {
+        const float4* p = reinterpret_cast<const float4*>(s_v + row * pitch + k);
+        const float4 u0 = p[0], u1 = p[1];
+        f[0] = u0.x; f[1] = u0.y; f[2] = u0.z; f[3] = u0.w;
+        f[4] = u1.x; f[5] = u1.y; f[6] = u1.z; f[7] = u1.w;
+      }
+      split8<V_TERMS>(f, t[h]);
+    }
+  };
+  uint32_t t[MT][2][V_TERMS][4];
+  if constexpr (EARLY) load_v(0, 0, t[0]);  // (rank <= 32: one step of k)
   for (int c0 = c_first; c0 < a.d_out; c0 += c_step) {
     Raw8 base[H];
     uint4 w[4];
-    if constexpr (EARLY) {  // (rank <= 32: one step of k)
+    if constexpr (EARLY) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) w[j] = w_ahead[j], w_ahead[j] = w_next[j];
 #pragma unroll
       for (int h = 0; h < H; ++h) base[h] = base_ahead[h], base_ahead[h] = base_next[h];
-      load_b(c0 + 2 * c_step, 8 * q, w_next);
-      load_base(c0 + 2 * c_step, base_next);
+      if (c0 + 2 * c_step < a.d_out) {
+        load_b(c0 + 2 * c_step, 0, w_next);
+        load_base(c0 + 2 * c_step, base_next);
+      }
     } else {
       load_base(c0, base);
     }
@@ -341,34 +366,18 @@ __global__ void __launch_bounds__(AD_THREADS, 2) short_kernel(AdapterArgs a) {
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.f;
-    for (int k = 8 * q; k - 8 * q < rank; k += 32) {
-      if constexpr (!EARLY) load_b(c0, k, w);
+    for (int kk = 0; kk < rank; kk += 32) {
+      if constexpr (!EARLY) {
+        load_b(c0, kk, w);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) load_v(m, kk, t[m]);
+      }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        uint32_t t[2][V_TERMS][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = 16 * m + g + 8 * h;
-          if (2 * m + h >= H) {
-#pragma unroll
-            for (int i = 0; i < V_TERMS; ++i) t[h][i][0] = t[h][i][1] = t[h][i][2] = t[h][i][3] = 0u;
-            continue;
-          }
-          float f[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = 0.f;
-          if (k < rank && row < tile.rows) {
-            const float4* p = reinterpret_cast<const float4*>(s_v + row * pitch + k);
-            const float4 u0 = p[0], u1 = p[1];
-            f[0] = u0.x; f[1] = u0.y; f[2] = u0.z; f[3] = u0.w;
-            f[4] = u1.x; f[5] = u1.y; f[6] = u1.z; f[7] = u1.w;
-          }
-          split8<V_TERMS>(f, t[h]);
-        }
 #pragma unroll
         for (int i = V_TERMS - 1; i >= 0; --i) {
-          const uint32_t a0[4] = {t[0][i][0], t[1][i][0], t[0][i][1], t[1][i][1]};
-          const uint32_t a1[4] = {t[0][i][2], t[1][i][2], t[0][i][3], t[1][i][3]};
+          const uint32_t a0[4] = {t[m][0][i][0], t[m][1][i][0], t[m][0][i][1], t[m][1][i][1]};
+          const uint32_t a1[4] = {t[m][0][i][2], t[m][1][i][2], t[m][0][i][3], t[m][1][i][3]};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             mma_bf16(acc[m][j], a0, w[j].x, w[j].y);
@@ -376,18 +385,17 @@ __global__ void __launch_bounds__(AD_THREADS, 2) short_kernel(AdapterArgs a) {
           }
         }
       }
+      if (EARLY) break;
     }
-    const int c = c0 + 8 * q;
-    if (c >= a.d_out) continue;
+    if (c0 + 8 * q >= a.d_out) continue;
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      const int row = g + 8 * h;
-      if (row >= tile.rows) continue;
+      if (g + 8 * h >= tile.rows) continue;
       float f[8];
       widen8(base[h], WIDE ? STRATA_F32 : a.y_type, f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] += acc[h >> 1][i >> 1][2 * (h & 1) + (i & 1)];
-      store8(a.y, (int64_t)(tile.row + row) * a.y_stride + c, WIDE ? STRATA_F32 : a.y_type, f);
+      store8(y_at + (8 * h * a.y_stride + c0) * Y_SIZE, 0, WIDE ? STRATA_F32 : a.y_type, f);
     }
   }
   if (product) {
@@ -964,8 +972,10 @@ cudaError_t launch_adapters(const strata_adapters_t& ad, const int32_t* seg_off,
   a.seg_off = seg_off; a.seg_adapter = seg_adapter; a.n_seg = n_seg; a.n_adapter = ad.n_adapter;
   a.x = x; a.base = base; a.y = y; a.v = v_terms; a.status = status;
   a.rank = ad.rank; a.d_in = ad.d_in; a.d_out = ad.d_out; a.T = T; a.x_type = ad.x_type; a.y_type = ad.y_type;
-  // The 128-row kernels cost a call more (about 20 us) and a token's rank less than warp-level MMAs.
-  const bool many = (int64_t)T * a.rank > 256 * 1024 && (a.rank > 64 || a.x_type != STRATA_F32);
+  // The 128-row kernels cost a call more and a token's rank less than warp-level MMAs.  2,560 -> 2,560, bf16, in us, here and
+  // there: rank 32, 8,192 tokens 40 and 46; rank 64, 2,048 tokens 23 and 27, 8,192 tokens 59 and 50; rank 128, 1,024 tokens 35
+  // and 38, 2,048 tokens 57 and 45.  fp32: rank 64, 8,192 tokens 85 and 105; rank 128, 2,048 tokens 71 and 56.
+  const bool many = (int64_t)T * a.rank > 192 * 1024 && a.rank > (a.x_type == STRATA_F32 ? 64 : 32);
   if (many && T >= LONG * n_seg) return launch_tc(a, s);
   return T > 8 * n_seg ? launch_short<4>(a, s) : launch_short<1>(a, s);
 }
