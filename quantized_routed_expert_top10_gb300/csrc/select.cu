@@ -12,6 +12,7 @@ namespace strata {
 namespace {
 
 constexpr int SEL_WARPS = 4;          // one token each
+constexpr int SEL_CTAS = 7;           // an SM
 constexpr float SUM_MIN = 1.f / 16384.f;  // lower clamp of the weights' sum (2^-14)
 
 struct SelectArgs {
@@ -172,14 +173,19 @@ constexpr float LOG2E = 1.44269504f;
 __device__ __forceinline__ float sigmoid_fast(float l) { return rcp(1.f + ex2(l * -LOG2E)); }
 
 constexpr int CAND = 64;
-struct SelectScratch {  // one per warp; the 64-bit values of select_exact follow
-  float l[EMAX];
-  float val[EMAX + EMAX / 32];  // value of expert e at e + e / 32
-  uint64_t cand[CAND];          // key, then ~id: the larger number comes first
-  uint64_t sel[STRATA_SELECT_K_MAX + 1];
-  int kept[STRATA_SELECT_GROUP_MAX];
+struct SelectScratch {  // one per warp
+  float l[EMAX];        // for the 64-bit passes
+  union {
+    struct {
+      float val[EMAX + EMAX / 32];  // value of expert e at e + e / 32
+      uint64_t cand[CAND];          // key, then ~id: the larger number comes first
+      uint64_t sel[STRATA_SELECT_K_MAX + 1];
+      int kept[STRATA_SELECT_GROUP_MAX];
+    };
+    double exact[EMAX];  // select_exact's values
+  };
 };
-static_assert(sizeof(SelectScratch) % 8 == 0, "64-bit values follow the scratch");
+static_assert(sizeof(SelectScratch) % 16 == 0, "one follows another");
 __device__ __forceinline__ int cand_id(uint64_t c) { return (int)~(uint32_t)c; }
 __device__ __forceinline__ uint32_t cand_key(uint64_t c) { return (uint32_t)(c >> 32); }
 
@@ -212,40 +218,59 @@ __device__ __noinline__ uint32_t read_row(const SelectArgs& a, int t, float* l, 
   return usable;
 }
 
+// Logit of expert e of token t, usable, as read_row has it.
+__device__ __forceinline__ float logit_at(const SelectArgs& a, int t, int e) {
+  return fminf(load1(a.logits, (int64_t)t * a.stride + e, a.type), FLT_MAX);
+}
+// A softmax's largest usable logit and its sum where they matter: without a bias the sum divides out, and m may be any.
+__device__ __forceinline__ double softmax_row(const SelectArgs& a, int t, SelectScratch& sc, float* m) {
+  if (!a.softmax || !a.bias) return 1.0;
+  const uint32_t usable = read_row(a, t, sc.l, m);
+  return softmax_sum_d(sc.l, usable, *m);
+}
+
 // Groups kept, where the fp32 scores do not decide: the groups' scores in 64 bits, from the two largest values of each
-// (val: the values with a bias, the logits without).  Lane g < G scans group g.  *sure = false if a group's two largest
-// cannot be told from its third.
-__device__ __noinline__ uint32_t groups_exact(const SelectArgs& a, int t, SelectScratch& sc, float err, bool* sure) {
+// (val: the values with a bias, the logits without).  Lane g < G scans group g.  m: the softmax's largest logit.  *sure = false
+// if a group's two largest cannot be told from its third.
+__device__ __noinline__ uint32_t groups_exact(const SelectArgs& a, int t, SelectScratch& sc, float m, float err, bool* sure) {
   const int lane = threadIdx.x & 31;
-  float m;
-  const uint32_t usable = read_row(a, t, sc.l, &m);
-  // without a bias the sum divides out
-  const double z = a.softmax && a.bias ? softmax_sum_d(sc.l, usable, m) : 1.0;
   float v0 = -INFINITY, v1 = -INFINITY, v2 = -INFINITY;
   int e0 = 0, e1 = 0;
   if (lane < a.G)
+#pragma unroll 8
     for (int i = 0; i < a.size; ++i) {
       const int e = lane * a.size + i;
       const float v = sc.val[e + (e >> 5)];
-      if (v > v0) {
-        v2 = v1; v1 = v0; e1 = e0;
-        v0 = v; e0 = e;
-      } else if (v > v1) {
-        v2 = v1;
-        v1 = v; e1 = e;
-      } else if (v > v2) {
-        v2 = v;
-      }
+      const bool c0 = v > v0, c1 = v > v1;
+      v2 = c1 ? v1 : fmaxf(v2, v);
+      e1 = c0 ? e0 : c1 ? e : e1;
+      v1 = c0 ? v0 : fmaxf(v1, v);
+      e0 = c0 ? e : e0;
+      v0 = fmaxf(v0, v);
     }
-  const float last = a.group_sum == 2 ? v1 : v0, behind = a.group_sum == 2 ? v2 : v1;
+  const bool two = a.group_sum == 2;
+  const float last = two ? v1 : v0, behind = two ? v2 : v1;
   const bool clear = !a.bias || behind == -INFINITY ||
                      last - behind > 2.f * (err + U32 * fmaxf(fabsf(last), fabsf(behind)));
   *sure = __all_sync(0xffffffffu, clear);
-  double gs = -INFINITY;
-  if (v0 > -INFINITY) gs = score_d(sc.l[e0], a.softmax, m, z) + (a.bias ? (double)__ldg(a.bias + e0) : 0.0);
-  if (a.group_sum == 2 && v1 > -INFINITY)
-    gs += score_d(sc.l[e1], a.softmax, m, z) + (a.bias ? (double)__ldg(a.bias + e1) : 0.0);
+  const double z = softmax_row(a, t, sc, &m);
+  const auto value = [&](int e, float v) {
+    return v > -INFINITY ? score_d(logit_at(a, t, e), a.softmax, m, z) + (a.bias ? (double)__ldg(a.bias + e) : 0.0) : -INFINITY;
+  };
+  double gs;
+  if (a.G <= 16) {  // lanes 16 .. take the second values
+    const int e2 = __shfl_sync(0xffffffffu, e1, lane & 15);
+    const float w2 = __shfl_sync(0xffffffffu, v1, lane & 15);
+    const bool second = lane >= 16;
+    gs = value(second ? e2 : e0, second ? (two ? w2 : -INFINITY) : v0);
+    const double other = __shfl_down_sync(0xffffffffu, gs, 16);
+    if (other > -INFINITY) gs += other;
+  } else {
+    gs = value(e0, v0);
+    if (two && v1 > -INFINITY) gs += value(e1, v1);
+  }
   int rank = 0;
+#pragma unroll 4
   for (int g = 0; g < a.G; ++g) {
     const double o = __shfl_sync(0xffffffffu, gs, g);
     rank += (o > gs || (o == gs && g < lane)) ? 1 : 0;
@@ -257,14 +282,13 @@ __device__ __noinline__ uint32_t groups_exact(const SelectArgs& a, int t, Select
 // for fp32; near neighbours of the same logit and bias are true ties and stay as they are.
 __device__ __noinline__ void order_exact(const SelectArgs& a, int t, SelectScratch& sc, int C, bool near) {
   const int lane = threadIdx.x & 31;
-  float m;
-  const uint32_t usable = read_row(a, t, sc.l, &m);
   if (near) {
     const int p = cand_id(sc.sel[lane]), q = cand_id(sc.sel[lane + 1]);
-    near = !(sc.l[p] == sc.l[q] && __ldg(a.bias + p) == __ldg(a.bias + q));
+    near = !(logit_at(a, t, p) == logit_at(a, t, q) && __ldg(a.bias + p) == __ldg(a.bias + q));
   }
   if (!__any_sync(0xffffffffu, near)) return;
-  const double z = a.softmax ? softmax_sum_d(sc.l, usable, m) : 1.0;
+  float m = 0.f;
+  const double z = softmax_row(a, t, sc, &m);
   double mine[CAND / 32];
 #pragma unroll
   for (int h = 0; h < CAND / 32; ++h) {
@@ -272,7 +296,7 @@ __device__ __noinline__ void order_exact(const SelectArgs& a, int t, SelectScrat
     if (lane + 32 * h < C) {
       const uint64_t c = sc.cand[lane + 32 * h];
       const int e = cand_id(c);
-      if (cand_key(c) > MASKED) mine[h] = score_d(sc.l[e], a.softmax, m, z) + (double)__ldg(a.bias + e);
+      if (cand_key(c) > MASKED) mine[h] = score_d(logit_at(a, t, e), a.softmax, m, z) + (double)__ldg(a.bias + e);
     }
   }
   int rank[CAND / 32] = {0, 0};
@@ -300,22 +324,22 @@ __device__ __noinline__ void order_exact(const SelectArgs& a, int t, SelectScrat
 // of the candidates' values, or of the groups' two largest; only where even that is not enough (a mass of near ties) of
 // all.  64-bit arithmetic is slow on this GPU, and a token in about a thousand needs it.
 template <bool VALUES, int PER>
-__global__ void __launch_bounds__(32 * SEL_WARPS, 5) select_kernel(const __grid_constant__ SelectArgs a, int warp_bytes) {
-  extern __shared__ __align__(16) char s_all[];
+__global__ void __launch_bounds__(32 * SEL_WARPS, SEL_CTAS) select_kernel(const __grid_constant__ SelectArgs a) {
+  __shared__ __align__(16) SelectScratch s_all[SEL_WARPS];
+  __shared__ float s_bias[VALUES ? 32 * PER : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  SelectScratch& sc = *reinterpret_cast<SelectScratch*>(s_all + warp * warp_bytes);
-  double* const exact = reinterpret_cast<double*>(&sc + 1);
+  SelectScratch& sc = s_all[warp];
   const float lowest = lowest_of(a.type);
   const uint32_t below = (1u << lane) - 1u;
   const bool grouped = VALUES && a.G > 1;
   const int L = VALUES ? group_lanes(a.G) : 32;
   const int total = grouped ? a.keep * a.size : a.E;  // experts that may be chosen
-  float b[PER];
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const int e = lane + 32 * j;
-    b[j] = VALUES && a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
-    if (!(b[j] > -INFINITY)) b[j] = -INFINITY;  // NaN too: the expert's value is -inf
+  if constexpr (VALUES) {
+    for (int e = threadIdx.x; e < 32 * PER; e += 32 * SEL_WARPS) {
+      const float b = a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
+      s_bias[e] = b > -INFINITY ? b : -INFINITY;  // NaN too: the expert's value is -inf
+    }
+    __syncthreads();
   }
   for (int t = blockIdx.x * SEL_WARPS + warp; t < a.T; t += gridDim.x * SEL_WARPS) {
     float v[PER];
@@ -354,14 +378,14 @@ __global__ void __launch_bounds__(32 * SEL_WARPS, 5) select_kernel(const __grid_
         mb = -INFINITY;
 #pragma unroll
         for (int j = 0; j < PER; ++j)
-          if (b[j] > -INFINITY) mb = fmaxf(mb, v[j]);
+          if (s_bias[lane + 32 * j] > -INFINITY) mb = fmaxf(mb, v[j]);
         mb = warp_max_key(mb);
         if (mb == -INFINITY) mb = 0.f;
         m = mb;
       }
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
-        const float e = VALUES && !(b[j] > -INFINITY) ? 0.f : ex2((v[j] - m) * LOG2E);
+        const float e = VALUES && !(s_bias[lane + 32 * j] > -INFINITY) ? 0.f : ex2((v[j] - m) * LOG2E);
         z += e;
         if (VALUES && a.bias) v[j] = v[j] > -INFINITY ? e : -INFINITY;
       }
@@ -369,7 +393,7 @@ __global__ void __launch_bounds__(32 * SEL_WARPS, 5) select_kernel(const __grid_
       inv_z = z > 0.f ? 1.f / z : 1.f;
       if (VALUES && a.bias) {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) v[j] = fmaf(v[j], inv_z, b[j]);
+        for (int j = 0; j < PER; ++j) v[j] = fmaf(v[j], inv_z, s_bias[lane + 32 * j]);
       }
       err = U32 * ERR_SOFTMAX * inv_z + 1e-37f;
     }
@@ -377,7 +401,7 @@ __global__ void __launch_bounds__(32 * SEL_WARPS, 5) select_kernel(const __grid_
       err = U32 * ERR_SIGMOID + 1e-37f;
       if (a.bias) {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) v[j] = v[j] > -INFINITY ? sigmoid_fast(v[j]) + b[j] : -INFINITY;
+        for (int j = 0; j < PER; ++j) v[j] = v[j] > -INFINITY ? sigmoid_fast(v[j]) + s_bias[lane + 32 * j] : -INFINITY;
       }
     }
 
@@ -435,10 +459,10 @@ __global__ void __launch_bounds__(32 * SEL_WARPS, 5) select_kernel(const __grid_
         }
         if (__any_sync(0xffffffffu, unsure)) {
           bool sure;
-          const uint32_t kept = groups_exact(a, t, sc, err, &sure);
+          const uint32_t kept = groups_exact(a, t, sc, m, err, &sure);
           if (!sure) {
             const uint32_t usable = read_row(a, t, sc.l, &m);
-            select_exact(a, t, sc.l, m, usable, exact);
+            select_exact(a, t, sc.l, m, usable, sc.exact);
             continue;
           }
           in = __ballot_sync(0xffffffffu, g < a.G && (kept >> g & 1u));
@@ -524,7 +548,7 @@ __global__ void __launch_bounds__(32 * SEL_WARPS, 5) select_kernel(const __grid_
       }
     } else if (VALUES && a.bias) {
       const uint32_t usable = read_row(a, t, sc.l, &m);
-      select_exact(a, t, sc.l, m, usable, exact);
+      select_exact(a, t, sc.l, m, usable, sc.exact);
       continue;
     } else {
       // a mass of equal logits: k rounds of the warp's largest (key, then lower id)
@@ -575,8 +599,8 @@ __global__ void __launch_bounds__(32 * SEL_WARPS, 5) select_kernel(const __grid_
 }
 
 template <bool VALUES, int PER>
-void launch_form(const SelectArgs& a, int grid, int warp_bytes, cudaStream_t s) {
-  select_kernel<VALUES, PER><<<grid, 32 * SEL_WARPS, SEL_WARPS * warp_bytes, s>>>(a, warp_bytes);
+void launch_form(const SelectArgs& a, int grid, cudaStream_t s) {
+  select_kernel<VALUES, PER><<<grid, 32 * SEL_WARPS, 0, s>>>(a);
 }
 
 }  // namespace
@@ -588,15 +612,14 @@ cudaError_t launch_select(const strata_select_t& sel, const void* logits, int T,
                      sel.logits_type, sel.scale, sel.n_expert / sel.n_group,
                      ((1 << 20) + sel.n_expert / sel.n_group - 1) / (sel.n_expert / sel.n_group)};
   const bool values = bias || sel.n_group > 1;
-  const int warp_bytes = (int)sizeof(SelectScratch) + (bias ? (int)sizeof(double) * EMAX : 0);
   // a warp takes ceil(T / what fits the GPU) tokens, so that all end together
-  const int fit = 152 * 5 * SEL_WARPS, turns = (T + fit - 1) / fit;
+  const int fit = 152 * SEL_CTAS * SEL_WARPS, turns = (T + fit - 1) / fit;
   const int warps = (T + turns - 1) / turns, grid = (warps + SEL_WARPS - 1) / SEL_WARPS;
   kernel_begin(KID_SELECT, s);
-  if (values && sel.n_expert > 256) launch_form<true, 16>(a, grid, warp_bytes, s);
-  else if (values) launch_form<true, 8>(a, grid, warp_bytes, s);
-  else if (sel.n_expert > 256) launch_form<false, 16>(a, grid, warp_bytes, s);
-  else launch_form<false, 8>(a, grid, warp_bytes, s);
+  if (values && sel.n_expert > 256) launch_form<true, 16>(a, grid, s);
+  else if (values) launch_form<true, 8>(a, grid, s);
+  else if (sel.n_expert > 256) launch_form<false, 16>(a, grid, s);
+  else launch_form<false, 8>(a, grid, s);
   kernel_end(KID_SELECT, s);
   return cudaGetLastError();
 }
