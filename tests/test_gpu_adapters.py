@@ -103,6 +103,40 @@ def test_long_segments(xk, yk, rank):
     Case(*LONG, rank, 64, 2560, xk, yk, inplace=True, pad=8).check()
 
 
+MANY = ([700, 0, 300, 128, 1, 127, 900, 250], [3, 0, 1, -1, 2, 4, 2, 0])  # 2,406 tokens
+
+
+@pytest.mark.parametrize("xk,yk", list(itertools.product(KINDS, KINDS)))
+@pytest.mark.parametrize("rank", [88, 96, 120, 128])
+def test_many_tokens_and_ranks(xk, yk, rank):
+    Case(*MANY, rank, 264, 392, xk, yk, before=1, after=3).check()
+    Case(*MANY, rank, 64, 264, xk, yk, inplace=True, pad=8).check()
+
+
+@pytest.mark.parametrize("xk,yk", [(qre.BF16, qre.BF16), (qre.F16, qre.F32), (qre.BF16, qre.F32), (qre.F16, qre.F16)])
+@pytest.mark.parametrize("rank", [40, 56, 64, 72])
+def test_many_tokens(xk, yk, rank):
+    Case([2000, 127, 0, 2049, 1, 900], [0, 4, 1, 2, -1, 0], rank, 264, 136, xk, yk, after=2).check()
+
+
+FEW = ([0, 1, 8, 9, 17, 0, 3, 2, 0, 1, 1, 7, 0, 5], [3, 0, 1, -1, 2, -1, 4, 2, 0, 0, 1, 1, 2, 2])  # 54 tokens in 14 segments
+
+
+@pytest.mark.parametrize("xk,yk", list(itertools.product(KINDS, KINDS)))
+@pytest.mark.parametrize("rank", [8, 16, 24, 32, 40, 64, 120, 128])
+def test_few_tokens_a_segment(xk, yk, rank):
+    Case(*FEW, rank, 520, 392, xk, yk, before=1, after=3).check()
+    Case(*FEW, rank, 2560, 2088, xk, yk, base=False).check()
+    Case(*FEW, rank, 64, 2560, xk, yk, inplace=True, pad=8).check()
+
+
+@pytest.mark.parametrize("d_in,d_out", [(8, 8), (8, 16384), (16384, 8), (24, 40), (248, 264), (2552, 2568)])
+@pytest.mark.parametrize("lens,of", [([1], [1]), ([8], [0]), ([3, 4], [2, -1]), ([1] * 200, [i % 6 - 1 for i in range(200)])])
+def test_few_tokens_widths(d_in, d_out, lens, of):
+    Case(lens, of, 16, d_in, d_out).check()
+    Case(lens, of, 72, d_in, d_out, qre.BF16, qre.F16).check()
+
+
 @pytest.mark.parametrize("d_in,d_out", [(8, 8), (8, 2560), (2560, 8), (24, 40), (248, 256), (264, 1032), (2552, 520), (5120, 24),
                                         (16384, 16), (16, 16384)])
 def test_widths(d_in, d_out):
@@ -201,3 +235,53 @@ def test_repeats_streams_and_graphs():
     c.y.copy_(first)
     c.check()
     assert torch.equal(replayed, c.y)
+
+
+@pytest.mark.parametrize("T,rank", [(3, 16), (3, 128), (40, 128), (2000, 128)])
+def test_no_term_of_an_operand_is_lost_at_any_length(T, rank):
+    """As above: one value of x a token, one of B a column, whole numbers."""
+    d_in, d_out = 96, 72
+    g = torch.Generator().manual_seed(T)
+    x = torch.zeros(T, d_in)
+    x[torch.arange(T), torch.randint(0, d_in, (T,), generator=g)] = (torch.randint(0, 1 << 22, (T,), generator=g) * 2 + 1).float()
+    a = torch.randint(-1, 2, (1, rank, d_in), generator=g).bfloat16()
+    b = torch.zeros(1, d_out, rank)
+    b[0, torch.arange(d_out), torch.randint(0, rank, (d_out,), generator=g)] = 1.0
+    b = b.bfloat16()
+    ad, bd = a.to(DEV), b.to(DEV)
+    off, of = torch.tensor([0, T], dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = workspace(T)
+    for kind, xs in ((qre.F32, x), (qre.F16, (x % 2047).half()), (qre.BF16, (x % 255).bfloat16())):
+        y = torch.empty(T, d_out, device=DEV)
+        want = xs.double() @ a[0].double().t() @ b[0].double().t()
+        qre.strata_moe_adapters(qre.adapters(ad, bd, 1, rank, d_in, d_out, x_type=kind), off, of, 1, xs.to(DEV), T, None, y, ws)
+        assert torch.equal(y.cpu().double(), want)
+
+
+@pytest.mark.parametrize("lens,rank", [([2000], 128), ([1, 2, 3], 16), ([700, 0, 900, 400], 104)])
+def test_bad_segments_of_any_length_compute_nothing(lens, rank):
+    c = Case(lens, [0] * len(lens), rank, 64, 64)
+    good, y = c.dev_off.clone(), c.y.clone()
+    for off in ([-1], [c.T + 1], [2 ** 31 - 1], [-2 ** 31]):
+        c.dev_off[-1:] = torch.tensor(off, dtype=torch.int32, device=DEV)
+        c.call()
+        assert qre.STATUS[qre.strata_poll_status(c.ws)] == "STRATA_E_CORRUPT"
+        assert torch.equal(c.y, y)
+        qre.strata_clear_status(c.ws)
+    c.dev_off.copy_(good)
+    c.check()
+
+
+def test_repeats_of_long_segments_in_a_graph():
+    c = Case([900, 1, 0, 800], [0, 1, 2, 3], 128, 264, 136, qre.BF16, qre.BF16, before=2, after=1)
+    c.check()
+    first = c.y.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(4):
+            c.call()
+    for _ in range(3):
+        c.y.copy_(first)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(c.y, first)

@@ -136,6 +136,27 @@ def test_edge_lengths(T):
     run_edge(T, 2560, 10)
 
 
+@pytest.mark.parametrize("n", [1, 3, 97, 255, 2559, 4097, 8193])
+@pytest.mark.parametrize("T", [1, 152, 700, 2000])
+def test_odd_rows_of_long_calls(n, T):
+    """Rows off every boundary, more of them than are in flight at once."""
+    T = min(T, 2000 * 2560 // n)
+    run_norm(T, n, qre.F32, qre.BF16)
+    run_norm(T, n, qre.BF16, qre.F16, pad=2, offset=1)
+    run_edge(T, n, 3, qre.BF16, qre.F32, qre.F16, zero_weight=T > 1)
+    run_edge(T, n, 1, qre.F32, qre.BF16, qre.BF16, offset=1, x=n % 2 == 0)
+    run_edge(T, n, 2, qre.F16, qre.F16, qre.F32, pad=1, inplace="out", weights=False)
+
+
+@pytest.mark.parametrize("n,T", [(64, 4000), (640, 1500), (4096, 400), (4100, 400), (8192, 300), (16384, 160)])
+def test_aligned_rows_of_long_calls(n, T):
+    run_norm(T, n, qre.F32, qre.F32, inplace=True)
+    run_norm(T, n, qre.F16, qre.F32)
+    run_edge(T, n, 3, qre.BF16, qre.F32, qre.F16, zero_weight=True)
+    run_edge(T, n, 1, qre.F16, qre.BF16, qre.F32, inplace="out")
+    run_edge(T, n, 2, qre.F32, qre.F16, qre.BF16, x=False)
+
+
 def test_edge_largest_call():
     run_edge(8192, 2560, 1, xk=qre.BF16, nk=qre.BF16)
 
