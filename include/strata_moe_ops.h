@@ -87,8 +87,9 @@ typedef struct strata_norm {
 } strata_norm_t;
 
 /* out[t] = x[t] / sqrt(mean(x[t]^2) + eps) * gain.  gain fp32 [n] or NULL (1).  out may be x itself (same address,
- * type and stride); other overlaps are refused.  Rows need only be aligned to their elements; rows on
- * 16-byte boundaries whose width is a multiple of 8 are moved 16 bytes at a time. */
+ * type and stride); other overlaps are refused.  Rows need only be aligned to their elements; calls whose rows all
+ * start on boundaries of four elements and are a multiple of four wide are the fastest.  The squares and their sum are
+ * fp32: a row whose sum of squares is beyond its range gives zeros. */
 strata_status strata_moe_norm(const strata_norm_t* nd, const void* x, int32_t T, const float* gain, void* out,
                               void* stream);
 
@@ -159,7 +160,8 @@ typedef struct strata_adapters {
  * place, rows without an adapter untouched); other overlaps of y with base or x are refused.
  * x, base, y, a, b on 16-byte boundaries.  Products are exact and their sums in fp32: an fp32 x enters the tensor
  * cores as three bf16 terms (24 significant bits), an fp16 x as two, and A_a x[t] likewise (three terms for
- * an fp32 y, two otherwise).
+ * an fp32 y, two otherwise).  A token whose x or A_a x holds a NaN, an infinity or a number that rounds to bf16's
+ * infinity may give NaN in its whole row; other tokens' rows do not change.
  * n_seg in [0, STRATA_MOE_T_MAX].  A seg_off out of order or outside [0, T], or an adapter outside
  * [-1, n_adapter), sets STRATA_E_CORRUPT in the workspace's status word and the call computes nothing (y keeps
  * its contents).  ws: the workspace of any call with T tokens (strata_moe_workspace_bytes(T), initialised once);

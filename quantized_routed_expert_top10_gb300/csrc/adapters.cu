@@ -4,8 +4,6 @@
 // fixed order), and expand, base + B_a (scale v).  Both walk tiles of up to 16 MT tokens of one segment; the products
 // are warp-level bf16 MMAs with fp32 accumulators.  A wider activation is the exact sum of bf16 terms (an fp16 two, an
 // fp32 three), each multiplied on its own.
-#include <atomic>
-
 #include "device_common.cuh"
 #include "elements.cuh"
 #include "tc_common.cuh"
@@ -429,6 +427,18 @@ __device__ __forceinline__ void copy_wait(int n) {
   else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
   else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
+// 16 lanes x 256 bits x 4 into registers without waiting, in the layout of a warp-level MMA's result: of the 8 columns
+// 8j .. 8j + 7, thread t gets columns 2 (t % 4), + 1 of lane t / 4 in r[4j], r[4j + 1] and of lane t / 4 + 8 in
+// r[4j + 2], r[4j + 3] (lanes counted from the address's lane).
+__device__ __forceinline__ void tmem_ld16x256b_x4_async(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // A wait that ran out is recorded; the CTA's later waits are then skipped (the call's result is void).
@@ -797,7 +807,7 @@ __global__ void __launch_bounds__(AD_THREADS + 32, 2) expand_tc_kernel(AdapterAr
           for (int h = 0; h < 2; ++h) {  // rows mrow + 16 h, + 8
             uint32_t d[16];
             if (product) {
-              tc::tmem_ld16x256b_x4_async(tmem + ((uint32_t)(32 * q4 + 16 * h) << 16) + (uint32_t)(CW * acc + 64 * half + 32 * sub), d);
+              tmem_ld16x256b_x4_async(tmem + ((uint32_t)(32 * q4 + 16 * h) << 16) + (uint32_t)(CW * acc + 64 * half + 32 * sub), d);
               tc::tmem_wait_ld();
             }
 #pragma unroll

@@ -3,12 +3,10 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
 #include "strata_moe.h"
-#include "strata_moe_ops.h"
 
 namespace strata {
 
@@ -252,8 +250,7 @@ namespace strata {
 enum KernelId : int {
   KID_DECODE_LAYER = 0, KID_ROUTE_DECODE, KID_ROUTER_PREP, KID_ROUTER_TC, KID_TOP_K, KID_GROUP_HIST, KID_GROUP_SCAN,
   KID_GROUP_SCATTER, KID_TC_PREPARE, KID_TC_GATHER, KID_TC_GATEUP, KID_TC_DOWN, KID_COMBINE, KID_PACK, KID_HOST_COPY,
-  KID_WAIT_SELFTEST, KID_BLOB_CRC32, KID_SELECT, KID_NORM, KID_COMBINE_NORM, KID_ADAPTER_SHRINK, KID_ADAPTER_EXPAND, KID_ADAPTERS,
-  KID_COUNT
+  KID_WAIT_SELFTEST, KID_BLOB_CRC32, KID_COUNT
 };
 void kernel_begin(int kid, cudaStream_t s);
 void kernel_end(int kid, cudaStream_t s);
@@ -287,33 +284,6 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
-}
-
-// The dynamic shared memory a kernel may use, raised once per kernel and device.
-template <auto* KERNEL>
-cudaError_t allow_smem(size_t bytes) {
-  static std::atomic<uint64_t> done{0};  // bit d: raised on device d
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-  if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
-  err = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return err;
-}
-// CTAs of `threads` threads (a multiple of 32, up to 1,024) and smem dynamic bytes that an SM holds at once; asked once for
-// each thread count, so a kernel's smem must go with its thread count.  At least 1.
-template <auto* KERNEL>
-int resident_ctas(int threads, size_t smem) {
-  static std::atomic<int> known[33];
-  std::atomic<int>& k = known[threads / 32];
-  int n = k.load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERNEL, threads, smem) != cudaSuccess || n < 1) n = 1;
-    k.store(n, std::memory_order_relaxed);
-  }
-  return n;
 }
 
 #define STRATA_LAUNCH(kid, s, ...) \
@@ -370,17 +340,6 @@ struct DecodeNext {
 cudaError_t launch_decode_fused(const strata_experts_t& ex, const uint16_t* w_router, const float* bias,
                                 const float* x, int T, int residual, int alias, float* out, int32_t* ids, float* weights,
                                 const DecodeNext* next, const WsLayout& L, char* ws, cudaStream_t s);
-// The operators of strata_moe_ops.h (arguments checked by ops_abi.cu).
-cudaError_t launch_select(const strata_select_t& sel, const void* logits, int T, const float* bias, int32_t* ids,
-                          float* weights, cudaStream_t s);
-cudaError_t launch_norm(const strata_norm_t& nd, const void* x, int T, const float* gain, void* out, cudaStream_t s);
-cudaError_t launch_combine_norm(const strata_combine_norm_t& cn, const void* parts, const float* part_weights,
-                                const void* x, int T, const float* post_gain, const float* channel_gate,
-                                const float* token_gate, const float* pre_gain, void* out, void* next, cudaStream_t s);
-// v_parts: fp32 scratch of 1024 floats per token.
-cudaError_t launch_adapters(const strata_adapters_t& ad, const int32_t* seg_off, const int32_t* seg_adapter, int n_seg,
-                            const void* x, int T, const void* base, void* y, uint16_t* v_terms, int* status,
-                            cudaStream_t s);
 cudaError_t launch_pack_device(const uint8_t* canonical, int64_t src_stride, uint8_t* packed,
                                int64_t dst_stride, int64_t n_blobs, cudaStream_t s);
 }  // namespace strata

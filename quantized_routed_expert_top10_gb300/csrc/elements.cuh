@@ -3,7 +3,7 @@
 #pragma once
 #include <cuda_bf16.h>
 
-#include "common.cuh"
+#include "ops_common.cuh"
 
 namespace strata {
 

@@ -5,7 +5,7 @@
 // two calls record the caller's CUDA events on the launch's stream around the launch.
 #include <atomic>
 
-#include "common.cuh"
+#include "ops_common.cuh"
 
 namespace strata {
 namespace {
@@ -22,7 +22,7 @@ static_assert(KID_DECODE_LAYER == STRATA_KERNEL_DECODE_LAYER && KID_ROUTE_DECODE
                   KID_NORM == STRATA_KERNEL_NORM && KID_COMBINE_NORM == STRATA_KERNEL_COMBINE_NORM &&
                   KID_ADAPTER_SHRINK == STRATA_KERNEL_ADAPTER_SHRINK &&
                   KID_ADAPTER_EXPAND == STRATA_KERNEL_ADAPTER_EXPAND && KID_ADAPTERS == STRATA_KERNEL_ADAPTERS &&
-                  KID_COUNT == STRATA_KERNEL_COUNT,
+                  KID_END == STRATA_KERNEL_COUNT,
               "kernel ids of the ABI and the library differ");
 
 std::atomic<unsigned long long> g_launches{0};
@@ -35,7 +35,7 @@ struct Armed {
   int n = 0;
   int used = 0;
 };
-thread_local Armed t_armed[KID_COUNT];
+thread_local Armed t_armed[KID_END];
 
 }  // namespace
 
@@ -57,7 +57,7 @@ void kernel_end(int kid, cudaStream_t s) {
 }
 
 bool profiling_armed() {
-  for (int k = 0; k < KID_COUNT; ++k)
+  for (int k = 0; k < KID_END; ++k)
     if (t_armed[k].used < t_armed[k].n) return true;
   return false;
 }
@@ -74,7 +74,7 @@ uint64_t strata_moe_launch_count(void) { return strata::g_launches.load(std::mem
 
 strata_status strata_moe_profile_arm(int32_t kernel, int32_t skip, void* const* start_events, void* const* stop_events,
                                      int32_t n) {
-  if (kernel < 0 || kernel >= strata::KID_COUNT || n < 0 || skip < 0) return STRATA_E_INVAL;
+  if (kernel < 0 || kernel >= strata::KID_END || n < 0 || skip < 0) return STRATA_E_INVAL;
   if (n > 0 && (!start_events || !stop_events)) return STRATA_E_INVAL;
   strata::Armed& a = strata::t_armed[kernel];
   a.start = reinterpret_cast<cudaEvent_t const*>(start_events);
@@ -86,7 +86,7 @@ strata_status strata_moe_profile_arm(int32_t kernel, int32_t skip, void* const* 
 }
 
 int32_t strata_moe_profile_recorded(int32_t kernel) {
-  if (kernel < 0 || kernel >= strata::KID_COUNT) return -1;
+  if (kernel < 0 || kernel >= strata::KID_END) return -1;
   return strata::t_armed[kernel].used;
 }
 

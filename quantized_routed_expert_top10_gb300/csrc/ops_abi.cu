@@ -2,7 +2,7 @@
 // and the launch of each call.
 #include <cmath>
 
-#include "common.cuh"
+#include "ops_common.cuh"
 
 using namespace strata;
 
