@@ -162,22 +162,29 @@ def lib():
 
 def _p(a):
     """Address of a tensor / numpy array / int, or None."""
-    if a is None:
-        return None
-    if isinstance(a, int):
+    if a is None or isinstance(a, int):
         return a
-    if hasattr(a, "data_ptr"):
+    try:
         return a.data_ptr()
+    except AttributeError:
+        pass
     if hasattr(a, "ctypes"):
         return a.ctypes.data
     raise TypeError(f"cannot take the address of {type(a)}")
 
 
+_current = None  # torch's raw handle of a device's current stream, and the current device
+
+
 def _s(stream):
     if stream is None:
-        # the current stream's handle, without the stream object torch.cuda.current_stream() builds (3 us a call)
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # without the stream object that torch.cuda.current_stream() builds (3 us a call)
+        global _current
+        if _current is None:
+            import torch
+            torch.cuda.init()
+            _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        return _current[0](_current[1]())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
