@@ -4,6 +4,13 @@
 // weights to the layer's input; the layers read a normalised activation.  Here the weighted sum, the norm of the
 // block's output, its gates, the scaled residual and the next block's norm are one pass: a row is held in registers
 // between its one read and its one write, both mean squares are sums over its CTA.
+//
+// All forms are bound by memory, or by the launch where rows are few (four rows 2.2 us, one token's ten parts 4.6 us), so each
+// keeps rows on their way while another is summed: CTAs stay and walk the rows, and what comes next is already being read,
+// into registers (one part or none) or a ring in shared memory (several).  A CTA a row without that: 39 us for the
+// norm below, 65 us for ten parts.  On one GB300, 2,560 columns: the norm of 8,192 rows, fp32 to bf16, 22.4 us (5.6 TB/s), a
+// copy of 42 MB and back 15 to 20 us; 2,048 rows of ten fp32 parts 44.3 us (6.2 TB/s, 91% of the measured copy rate); 8,192 rows
+// of one fp32 part with the stream in bf16 38.6 us (5.4 TB/s).
 #include "device_common.cuh"
 #include "elements.cuh"
 
@@ -298,7 +305,7 @@ cudaError_t launch_stream(const NormArgs& a, cudaStream_t s) {
 // A CTA takes every gridDim.x-th row, a thread V units of 4 columns.  What a row needs is a line of steps, its parts of weight
 // other than 0 in order and then x; the steps of this row and the next ones are on their way by cp.async into a ring of
 // shared memory, where a thread finds the pieces that it copied itself: no barrier, and memory never waits for
-// a row's sums.  The gains stay in registers where a thread has two units.
+// a row's sums.  The gains stay in registers where they are few.
 template <int XT, int PT, int V, int RING>
 __global__ void __launch_bounds__(512) edge_ring_kernel(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) uint4 s_ring[];  // [ring][V][threads]
@@ -480,14 +487,25 @@ cudaError_t launch_ring(const NormArgs& a, cudaStream_t s) {
 // ---- Rows that are not on boundaries of 4 elements ----------------------------------------------------------
 // The same line of steps, copied as the 16-byte pieces that hold a row's bytes, wherever in them it starts, and
 // taken out of shared memory a column at a time: a warp has 32 V columns in a row, a thread every 32nd (so a row's
-// addresses differ by constants: what bounds these rows is the count of instructions).  A thread reads what others copied,
-// so that a step costs a barrier; it also frees the slot read before.
+// addresses differ by constants: these rows are bound by the count of instructions, issued in 69% of cycles).  A thread
+// reads what others copied, so that a step costs a barrier; it also frees the slot read before.  2,559 columns: the norm of
+// 8,192 rows from fp32 to bf16 24.4 us (5.1 TB/s), 2,048 rows of ten fp32 parts 52 us (5.2 TB/s).
+// f(v) for a lane's columns, v of V; all of a warp inside its row as a rule.
+template <int V, class F>
+__device__ __forceinline__ void each_column(int left, F f) {
+  if (__all_sync(0xffffffffu, left > 32 * (V - 1))) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) f(v);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (32 * v < left) f(v);
+  }
+}
 template <int T, int V>
 __device__ __forceinline__ void store_columns(void* p, int64_t at, int left, const float (&f)[V]) {
   void* const to = static_cast<unsigned char*>(p) + at * (T == STRATA_F32 ? 4 : 2);
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (32 * v < left) store1(to, 32 * v, T, f[v]);
+  each_column<V>(left, [&](int v) { store1(to, 32 * v, T, f[v]); });
 }
 template <int XT, int PT, int V, int RING>
 __global__ void __launch_bounds__(512, V <= 8 ? 2 : 1) edge_columns_kernel(const __grid_constant__ NormArgs a, int slot_bytes) {
@@ -576,17 +594,13 @@ __global__ void __launch_bounds__(512, V <= 8 ? 2 : 1) edge_columns_kernel(const
         const int k = __ffs(parts) - 1;
         const float wk = __shfl_sync(0xffffffffu, w, k);
         const unsigned char* const at = next_slot(part_at(t, k), P_SIZE);
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (32 * v < left) y[v] = fmaf(wk, load1(at, 32 * v, PT), y[v]);
+        each_column<V>(left, [&](int v) { y[v] = fmaf(wk, load1(at, 32 * v, PT), y[v]); });
       }
     }
     w = w_next;
     if (a.x) {
       const unsigned char* const at = next_slot(x_at(t), X_SIZE);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (32 * v < left) r[v] = load1(at, 32 * v, XT);
+      each_column<V>(left, [&](int v) { r[v] = load1(at, 32 * v, XT); });
     }
     if constexpr (PARTS) {
       const float g = a.block * (!a.token ? 1.f : a.sigmoid ? 1.f / (1.f + expf(-tok)) : tok);
@@ -648,6 +662,9 @@ template <int XT, int PT>
 cudaError_t launch_columns(const NormArgs& a, cudaStream_t s) {
   if (a.n > 8192) return launch_columns_v<XT, PT, 32, 3>(a, s);
   if (a.n > 4096) return launch_columns_v<XT, PT, 16, 3>(a, s);
+  // 2,559 columns in us, a lane 16 or 8 of them: the norm of 8,192 rows 24.8 and 25.4 (bf16 18.9 and 23.5), one part 57 and 66,
+  // 2,048 rows of ten parts 57 and 53.
+  if (a.n > 1024 && a.P <= 1) return launch_columns_v<XT, PT, 16, 3>(a, s);
   return launch_columns_v<XT, PT, 8, 4>(a, s);
 }
 
