@@ -410,8 +410,9 @@ __global__ void __launch_bounds__(AD_THREADS, 2) short_kernel(AdapterArgs a) {
 
 // ---- Tiles of up to 128 tokens on the 5th-generation tensor cores -----------------------------------------
 // Operands are copied 16 bytes a thread into the tensor cores' K-major shared-memory layout (cp.async; an fp16 or fp32 x
-// by registers, which split it into its bf16 terms), so one kernel serves any row stride.  TMEM is allocated after
-// griddep_wait and before the next kernel may start, so no CTA holds it while it waits for another.
+// by registers, which split it into its bf16 terms), so one kernel serves any row stride.  The shrink kernel allocates TMEM after
+// griddep_wait and lets the expand kernel start only then; so an expand CTA, which allocates before its wait, waits for
+// CTAs that have what they need.
 constexpr int TC_ROWS = 128;
 constexpr uint32_t TC_TILE = TC_ROWS * 128;  // 128 rows of 64 bf16
 

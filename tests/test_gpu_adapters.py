@@ -285,3 +285,40 @@ def test_repeats_of_long_segments_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(c.y, first)
+
+
+def test_calls_on_two_streams_at_once():
+    cases = [Case([900, 1, 0, 1100], [0, 1, 2, 3], 128, 520, 392, qre.BF16, qre.BF16, seed=3),
+             Case([1500, 700], [4, 4], 104, 264, 520, qre.F32, qre.F32, seed=9),
+             Case([1] * 100, [i % 5 for i in range(100)], 16, 520, 392, seed=15),
+             Case([40, 3, 90], [1, -1, 1], 24, 264, 136, qre.F16, qre.BF16, seed=21)]
+    for c in cases:
+        c.check()
+    want = [c.y.clone() for c in cases]
+    for c in cases:
+        c.y.zero_()
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                c.call()
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        assert qre.strata_poll_status(c.ws) == 0 and torch.equal(c.y, w)
+
+
+@pytest.mark.parametrize("lens,rank", [([2000, 130], 128), ([40, 33], 16), ([1] * 40, 16)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_bad_numbers_stay_in_their_row(lens, rank, kind):
+    c = Case(lens, [i % 5 for i in range(len(lens))], rank, 264, 136, kind, kind, seed=5)
+    c.call()
+    want = c.y.clone()
+    bad = [0, 7, c.T - 1]
+    for t, v in zip(bad, (float("nan"), float("inf"), float("-inf"))):
+        c.x[t, 3] = v
+    c.call()
+    torch.cuda.synchronize()
+    rest = [t for t in range(c.T) if t not in bad]
+    assert torch.equal(c.y[rest], want[rest])
+    assert not torch.isfinite(c.y[bad].float()).all(1).any()
