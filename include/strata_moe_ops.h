@@ -123,7 +123,8 @@ typedef struct strata_combine_norm {
  *   next = r / sqrt(mean(r^2) + eps) * pre_gain                       (of r before it is rounded into out)
  * A part whose weight is 0 is not read (a masked expert's part may hold anything, or nothing yet).
  * part_weights fp32 [T][n_part]; x, post_gain, channel_gate fp32 [n], token_gate fp32 [T] and pre_gain may be
- * NULL (no residual; factors of 1; post_gain only with STRATA_POST_NORM); out or next may be NULL, not both.
+ * NULL (no residual; factors of 1); out or next may be NULL, not both.  A post_gain without STRATA_POST_NORM, a
+ * pre_gain without next or STRATA_TOKEN_SIGMOID without a token_gate is refused.
  * out or next may be x itself (same address, type and stride); other overlaps are refused.  Alignment as for
  * strata_moe_norm. */
 strata_status strata_moe_combine_norm(const strata_combine_norm_t* cn, const void* parts, const float* part_weights,

@@ -104,3 +104,53 @@ def test_chain_in_one_graph_equals_the_calls():
     assert qre.strata_poll_status(ws) == 0
     for u, v in zip(got, (ids, w, logits, out, nxt)):
         assert torch.equal(u, v)
+
+
+FIRST_IN_CAPTURE = """
+import torch, quantized_routed_expert_top10_gb300 as qre
+T, n, E, rank = 2048, 264, 64, 128
+x, parts = torch.randn(T, n, device="cuda"), torch.randn(T, 2, n, device="cuda")
+odd = torch.randn(T, n + 1, device="cuda")
+gain, logits = torch.ones(n, device="cuda"), torch.randn(T, E, device="cuda")
+a = torch.randn(2, rank, n, device="cuda").bfloat16()
+b = torch.randn(2, n, rank, device="cuda").bfloat16()
+off = torch.tensor([0, 1000, T], dtype=torch.int32, device="cuda")
+few = torch.tensor([0, 3, 20], dtype=torch.int32, device="cuda")
+of = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+ws = torch.empty(qre.strata_moe_workspace_bytes(T), dtype=torch.uint8, device="cuda")
+qre.strata_moe_workspace_init(ws)
+outs = [torch.zeros(T, n, device="cuda") for _ in range(6)]
+odd_out = torch.zeros_like(odd)
+ids, w = torch.zeros(T, 4, dtype=torch.int32, device="cuda"), torch.zeros(T, 4, device="cuda")
+
+def calls():
+    qre.strata_moe_norm(qre.norm(n), x, T, gain, outs[0])
+    qre.strata_moe_norm(qre.norm(n + 1), odd, T, None, odd_out)
+    qre.strata_moe_combine_norm(qre.combine_norm(n, 2), parts, None, x, T, gain, None, None, gain, outs[1], outs[2])
+    qre.strata_moe_combine_norm(qre.combine_norm(n, 1), outs[1], None, x, T, gain, None, None, None, outs[3], None)
+    qre.strata_moe_adapters(qre.adapters(a, b, 2, rank, n, n), off, of, 2, outs[0], T, None, outs[4], ws)
+    qre.strata_moe_adapters(qre.adapters(a, b, 2, rank, n, n), few, of, 2, outs[0], T, None, outs[5], ws)
+    qre.strata_moe_select(qre.select(E, 4, qre.SCORE_SIGMOID, 8, 4, 2), logits, T, None, ids, w)
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    calls()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (*outs, odd_out, ids, w)]
+calls()
+torch.cuda.synchronize()
+assert qre.strata_poll_status(ws) == 0
+assert all(torch.equal(g, t) for g, t in zip(got, (*outs, odd_out, ids, w)))
+assert all(g.abs().sum() > 0 for g in got)
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
