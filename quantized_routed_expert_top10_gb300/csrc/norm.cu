@@ -5,11 +5,12 @@
 // block's output, its gates, the scaled residual and the next block's norm are one pass: a row is held in registers
 // between its one read and its one write, both mean squares are sums over its CTA.
 //
-// All forms are bound by memory, or by the launch where rows are few (four rows 2.2 us, one token's ten parts 4.6 us), so each
+// The kernels may start while the one before them ends (griddep_wait) and let the next one start when their rows are done;
+// started earlier, its CTAs took room from this one's (ten parts 44 -> 47 us).  All forms are bound by memory, or by the launch where rows are few (four rows 2.0 us, one token's ten parts 4.3 us), so each
 // keeps rows on their way while another is summed: CTAs stay and walk the rows, and what comes next is already being read,
 // into registers (one part or none) or a ring in shared memory (several).  A CTA a row without that: 39 us for the
 // norm below, 65 us for ten parts.  On one GB300, 2,560 columns: the norm of 8,192 rows, fp32 to bf16, 22.4 us (5.6 TB/s), a
-// copy of 42 MB and back 15 to 20 us; 2,048 rows of ten fp32 parts 44.3 us (6.2 TB/s, 91% of the measured copy rate); 8,192 rows
+// copy of 42 MB and back 15 to 20 us; 2,048 rows of ten fp32 parts 43.5 us (6.3 TB/s, 92% of the measured copy rate); 8,192 rows
 // of one fp32 part with the stream in bf16 38.6 us (5.4 TB/s).
 #include "device_common.cuh"
 #include "elements.cuh"
@@ -34,6 +35,8 @@ struct NormArgs {
   bool gains16;  // the gains given lie on 16-byte boundaries
 };
 
+// (A row is a CTA's, or where a warp has threads for all of it a warp's: blockDim.x == 32, blockDim.y rows a CTA.)
+//
 // Sum of v over the threads of a row: its warp, or the whole CTA (blockDim.x > 32).  red: 32 floats of shared
 // memory used by this sum alone.
 __device__ __forceinline__ float row_sum(float v, float* red) {
@@ -95,6 +98,8 @@ constexpr int NO_PARTS = -1;
 // once.
 template <int XT, int PT>
 __global__ void __launch_bounds__(1024) edge_few_kernel(const __grid_constant__ NormArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
   constexpr int GROUP = 10;
   __shared__ float red[2][32];
   const int t = blockIdx.x, u = threadIdx.x, lane = u & 31;
@@ -162,6 +167,8 @@ __global__ void __launch_bounds__(1024) edge_few_kernel(const __grid_constant__ 
 // registers, so that memory never waits for a row's sums; the gains stay in registers where they are few.
 template <int XT, int PT, int V, int AHEAD>
 __global__ void __launch_bounds__(512) edge_stream_kernel(const __grid_constant__ NormArgs a) {
+  griddep_wait();
+  const int first_row = blockIdx.x * blockDim.y + threadIdx.y, row_step = gridDim.x * blockDim.y;
   constexpr bool PART = PT != NO_PARTS, KEEP = V <= 4;
   __shared__ float red[2][2][32];
   const int tid = threadIdx.x, threads = blockDim.x, units = a.n / 4;
@@ -204,12 +211,12 @@ __global__ void __launch_bounds__(512) edge_stream_kernel(const __grid_constant_
   };
   Row rows[AHEAD];
 #pragma unroll
-  for (int i = 0; i < AHEAD; ++i) fetch(blockIdx.x + i * gridDim.x, rows[i]);
+  for (int i = 0; i < AHEAD; ++i) fetch(first_row + i * row_step, rows[i]);
   int turn = 0;
-  for (int t0 = blockIdx.x; t0 < a.T; t0 += AHEAD * gridDim.x) {
+  for (int t0 = first_row; t0 < a.T; t0 += AHEAD * row_step) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
-      const int t = t0 + i * gridDim.x;
+      const int t = t0 + i * row_step;
       if (t >= a.T) break;
       float r[V][4];
 #pragma unroll
@@ -223,7 +230,7 @@ __global__ void __launch_bounds__(512) edge_stream_kernel(const __grid_constant_
           for (int e = 0; e < 4; ++e) y[v][e] *= rows[i].w;
         }
         const float token = rows[i].token;
-        fetch(t + AHEAD * gridDim.x, rows[i]);
+        fetch(t + AHEAD * row_step, rows[i]);
         const float g = a.block * (!a.token ? 1.f : a.sigmoid ? 1.f / (1.f + expf(-token)) : token);
         if (a.post) {
           float ss = 0.f;
@@ -248,7 +255,7 @@ __global__ void __launch_bounds__(512) edge_stream_kernel(const __grid_constant_
           for (int e = 0; e < 4; ++e) r[v][e] = mine[v] ? fmaf(g, y[v][e], a.residual * r[v][e]) : 0.f;
         }
       } else {
-        fetch(t + AHEAD * gridDim.x, rows[i]);
+        fetch(t + AHEAD * row_step, rows[i]);
       }
       if (PART && a.out) {
 #pragma unroll
@@ -279,14 +286,19 @@ __global__ void __launch_bounds__(512) edge_stream_kernel(const __grid_constant_
       turn ^= 1;
     }
   }
+  griddep_launch_dependents();
 }
+
+// Rows a CTA: four of one warp each once the SMs have as many, since an SM holds 32 CTAs at most and starts them one by one
+// (8,192 x 100: 3.2 us, a row a CTA 6.7).
+int rows_a_cta(const NormArgs& a, int threads) { return threads == 32 && a.T > 4 * 152 ? 4 : 1; }
 
 template <int XT, int PT, int V, int AHEAD>
 cudaError_t launch_stream_v(const NormArgs& a, cudaStream_t s) {
   const int threads = ((a.n / 4 + V - 1) / V + 31) / 32 * 32;
-  const int fit = 152 * resident_ctas<edge_stream_kernel<XT, PT, V, AHEAD>>(threads, 0);
-  edge_stream_kernel<XT, PT, V, AHEAD><<<a.T < fit ? a.T : fit, threads, 0, s>>>(a);
-  return cudaGetLastError();
+  const int rows = rows_a_cta(a, threads), ctas = (a.T + rows - 1) / rows;
+  const int fit = 152 * resident_ctas<edge_stream_kernel<XT, PT, V, AHEAD>>(threads * rows, 0);
+  return launch_pdl(edge_stream_kernel<XT, PT, V, AHEAD>, ctas < fit ? ctas : fit, dim3(threads, rows), 0, s, a);
 }
 
 // Units a thread and rows ahead (2560 columns, 8,192 rows): without a part (fp32 to bf16) 2 and 2 22.4 us, 2 and 1 25.6, 4 and
@@ -297,7 +309,7 @@ template <int XT, int PT>
 cudaError_t launch_stream(const NormArgs& a, cudaStream_t s) {
   const int units = a.n / 4;
   if (units > 2048) return launch_stream_v<XT, PT, 8, 1>(a, s);
-  if (units > 1024 || (PT != NO_PARTS && a.T > 152)) return launch_stream_v<XT, PT, 4, 1>(a, s);
+  if (units > 1024 || (units > 64 && units <= 128) || (PT != NO_PARTS && a.T > 152)) return launch_stream_v<XT, PT, 4, 1>(a, s);
   return launch_stream_v<XT, PT, 2, PT == NO_PARTS ? 2 : 1>(a, s);
 }
 
@@ -308,10 +320,13 @@ cudaError_t launch_stream(const NormArgs& a, cudaStream_t s) {
 // a row's sums.  The gains stay in registers where they are few.
 template <int XT, int PT, int V, int RING>
 __global__ void __launch_bounds__(512) edge_ring_kernel(const __grid_constant__ NormArgs a) {
-  extern __shared__ __align__(16) uint4 s_ring[];  // [ring][V][threads]
+  griddep_wait();
+  const int first_row = blockIdx.x * blockDim.y + threadIdx.y, row_step = gridDim.x * blockDim.y;
+  extern __shared__ __align__(16) uint4 s_rings[];  // [blockDim.y][ring][V][threads]
   __shared__ float red[2][2][32];
   const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, units = a.n / 4;
   const int slot_units = V * threads;
+  uint4* const s_ring = s_rings + threadIdx.y * RING * slot_units;
   bool mine[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) mine[v] = tid + v * threads < units;
@@ -344,15 +359,15 @@ __global__ void __launch_bounds__(512) edge_ring_kernel(const __grid_constant__ 
       }
   };
   // the step to be copied next: part `ffs(todo)` of row tc, or its x
-  int tc = blockIdx.x, cslot = 0;
-  float wc = weight(tc), wn = weight(tc + gridDim.x);
+  int tc = first_row, cslot = 0;
+  float wc = weight(tc), wn = weight(tc + row_step);
   uint32_t todo = __ballot_sync(0xffffffffu, wc != 0.f);
   bool x_to_do = a.x != nullptr;
   const auto copy_next = [&]() {
     while (tc < a.T && !todo && !x_to_do) {
-      tc += gridDim.x;
+      tc += row_step;
       wc = wn;
-      wn = weight(tc + gridDim.x);
+      wn = weight(tc + row_step);
       todo = __ballot_sync(0xffffffffu, wc != 0.f);
       x_to_do = a.x != nullptr;
     }
@@ -371,9 +386,9 @@ __global__ void __launch_bounds__(512) edge_ring_kernel(const __grid_constant__ 
   };
   for (int i = 0; i < RING - 1; ++i) copy_next();
   int slot = 0, turn = 0;
-  float w = weight(blockIdx.x);
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
-    const float w_next = weight(t + gridDim.x);
+  float w = weight(first_row);
+  for (int t = first_row; t < a.T; t += row_step, turn ^= 1) {
+    const float w_next = weight(t + row_step);
     const float tok = a.token ? __ldg(a.token + t) : 1.f;
     float y[V][4], r[V][4];
 #pragma unroll
@@ -459,16 +474,16 @@ __global__ void __launch_bounds__(512) edge_ring_kernel(const __grid_constant__ 
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+  griddep_launch_dependents();
 }
 
 template <int XT, int PT, int V, int RING>
 cudaError_t launch_ring_v(const NormArgs& a, cudaStream_t s) {
-  const int threads = ((a.n / 4 + V - 1) / V + 31) / 32 * 32, smem = RING * V * threads * 16;
+  const int threads = ((a.n / 4 + V - 1) / V + 31) / 32 * 32, rows = rows_a_cta(a, threads), smem = rows * RING * V * threads * 16;
   const cudaError_t err = allow_smem<edge_ring_kernel<XT, PT, V, RING>>(224 * 1024);
   if (err != cudaSuccess) return err;
-  const int fit = 152 * resident_ctas<edge_ring_kernel<XT, PT, V, RING>>(threads, smem);
-  edge_ring_kernel<XT, PT, V, RING><<<a.T < fit ? a.T : fit, threads, smem, s>>>(a);
-  return cudaGetLastError();
+  const int ctas = (a.T + rows - 1) / rows, fit = 152 * resident_ctas<edge_ring_kernel<XT, PT, V, RING>>(threads * rows, smem);
+  return launch_pdl(edge_ring_kernel<XT, PT, V, RING>, ctas < fit ? ctas : fit, dim3(threads, rows), smem, s, a);
 }
 
 // Slots: 6 of up to 16 KB, or 3 of up to 64 KB.
@@ -476,11 +491,10 @@ template <int XT, int PT>
 cudaError_t launch_ring(const NormArgs& a, cudaStream_t s) {
   const int units = a.n / 4;
   if (units <= 1024 && a.T <= 152) {
-    edge_few_kernel<XT, PT><<<a.T, (units + 31) / 32 * 32, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(edge_few_kernel<XT, PT>, a.T, (units + 31) / 32 * 32, 0, s, a);
   }
   if (units > 2048) return launch_ring_v<XT, PT, 8, 3>(a, s);
-  if (units > 1024) return launch_ring_v<XT, PT, 4, 3>(a, s);
+  if (units > 1024 || (units > 64 && units <= 128)) return launch_ring_v<XT, PT, 4, 3>(a, s);  // (a warp's rows up to 512 wide)
   return launch_ring_v<XT, PT, 2, 6>(a, s);
 }
 
@@ -509,7 +523,10 @@ __device__ __forceinline__ void store_columns(void* p, int64_t at, int left, con
 }
 template <int XT, int PT, int V, int RING>
 __global__ void __launch_bounds__(512, V <= 8 ? 2 : 1) edge_columns_kernel(const __grid_constant__ NormArgs a, int slot_bytes) {
-  extern __shared__ __align__(16) unsigned char s_bytes[];  // [ring][slot_bytes]
+  griddep_wait();
+  const int first_row = blockIdx.x * blockDim.y + threadIdx.y, row_step = gridDim.x * blockDim.y;
+  extern __shared__ __align__(16) unsigned char s_bytes_all[];  // [blockDim.y][ring][slot_bytes]
+  unsigned char* const s_bytes = s_bytes_all + threadIdx.y * RING * slot_bytes;
   __shared__ float red[2][2][32];
   constexpr bool PARTS = PT != NO_PARTS;
   constexpr int P_SIZE = PT == STRATA_F32 ? 4 : 2, X_SIZE = XT == STRATA_F32 ? 4 : 2;
@@ -544,16 +561,16 @@ __global__ void __launch_bounds__(512, V <= 8 ? 2 : 1) edge_columns_kernel(const
     for (int left = bytes + off - tid * 16; left > 0; left -= threads * 16, at += threads * 16, to += threads * 16)
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(at), "r"(left < 16 ? left : 16) : "memory");
   };
-  int tc = blockIdx.x, cslot = 0;
-  float wc = PARTS ? weight(tc) : 0.f, wn = PARTS ? weight(tc + gridDim.x) : 0.f;
+  int tc = first_row, cslot = 0;
+  float wc = PARTS ? weight(tc) : 0.f, wn = PARTS ? weight(tc + row_step) : 0.f;
   uint32_t todo = PARTS ? __ballot_sync(0xffffffffu, wc != 0.f) : 0u;
   bool x_to_do = a.x != nullptr;
   const auto copy_next = [&]() {
     while (tc < a.T && !todo && !x_to_do) {
-      tc += gridDim.x;
+      tc += row_step;
       if constexpr (PARTS) {
         wc = wn;
-        wn = weight(tc + gridDim.x);
+        wn = weight(tc + row_step);
         todo = __ballot_sync(0xffffffffu, wc != 0.f);
       }
       x_to_do = a.x != nullptr;
@@ -575,16 +592,17 @@ __global__ void __launch_bounds__(512, V <= 8 ? 2 : 1) edge_columns_kernel(const
   // the step's bytes as this thread's first column finds them
   const auto next_slot = [&](const unsigned char* from, int size) {
     asm volatile("cp.async.wait_group %0;" ::"n"(RING - 2) : "memory");
-    __syncthreads();
+    if (threads == 32) __syncwarp();
+    else __syncthreads();
     const unsigned char* const at = s_bytes + slot * slot_bytes + (int)(reinterpret_cast<uintptr_t>(from) & 15) + first * size;
     slot = slot + 1 == RING ? 0 : slot + 1;
     copy_next();  // into the slot read before this one
     return at;
   };
   for (int i = 0; i < RING - 1; ++i) copy_next();
-  float w = PARTS ? weight(blockIdx.x) : 0.f;
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
-    const float w_next = PARTS ? weight(t + gridDim.x) : 0.f;
+  float w = PARTS ? weight(first_row) : 0.f;
+  for (int t = first_row; t < a.T; t += row_step, turn ^= 1) {
+    const float w_next = PARTS ? weight(t + row_step) : 0.f;
     const float tok = PARTS && a.token ? __ldg(a.token + t) : 1.f;
     float y[V], r[V];
 #pragma unroll
@@ -644,6 +662,7 @@ __global__ void __launch_bounds__(512, V <= 8 ? 2 : 1) edge_columns_kernel(const
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+  griddep_launch_dependents();
 }
 
 template <int XT, int PT, int V, int RING>
@@ -652,9 +671,9 @@ cudaError_t launch_columns_v(const NormArgs& a, cudaStream_t s) {
   const int size = XT == STRATA_F32 || PT == STRATA_F32 ? 4 : 2, slot = (a.n * size + 15) / 16 * 16 + 16;
   const cudaError_t err = allow_smem<edge_columns_kernel<XT, PT, V, RING>>(224 * 1024);
   if (err != cudaSuccess) return err;
-  const int fit = 152 * resident_ctas<edge_columns_kernel<XT, PT, V, RING>>(threads, RING * slot);
-  edge_columns_kernel<XT, PT, V, RING><<<a.T < fit ? a.T : fit, threads, RING * slot, s>>>(a, slot);
-  return cudaGetLastError();
+  const int rows = rows_a_cta(a, threads), ctas = (a.T + rows - 1) / rows, smem = rows * RING * slot;
+  const int fit = 152 * resident_ctas<edge_columns_kernel<XT, PT, V, RING>>(threads * rows, smem);
+  return launch_pdl(edge_columns_kernel<XT, PT, V, RING>, ctas < fit ? ctas : fit, dim3(threads, rows), smem, s, a, slot);
 }
 
 // Slots: 4 of up to 16 KB, or 3 of up to 64 KB.

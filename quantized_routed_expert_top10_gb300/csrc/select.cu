@@ -331,6 +331,7 @@ __device__ __noinline__ void order_exact(const SelectArgs& a, int t, SelectScrat
 // all.  64-bit arithmetic is slow on this GPU, and a token in about a thousand needs it.
 template <bool VALUES, int PER>
 __global__ void __launch_bounds__(32 * SEL_WARPS, SEL_CTAS) select_kernel(const __grid_constant__ SelectArgs a) {
+  griddep_wait();
   __shared__ __align__(16) SelectScratch s_all[SEL_WARPS];
   __shared__ float s_bias[VALUES ? 32 * PER : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -602,11 +603,12 @@ __global__ void __launch_bounds__(32 * SEL_WARPS, SEL_CTAS) select_kernel(const 
     }
     __syncwarp();
   }
+  griddep_launch_dependents();
 }
 
 template <bool VALUES, int PER>
-void launch_form(const SelectArgs& a, int grid, cudaStream_t s) {
-  select_kernel<VALUES, PER><<<grid, 32 * SEL_WARPS, 0, s>>>(a);
+cudaError_t launch_form(const SelectArgs& a, int grid, cudaStream_t s) {
+  return launch_pdl(select_kernel<VALUES, PER>, grid, 32 * SEL_WARPS, 0, s, a);
 }
 
 }  // namespace
@@ -622,12 +624,11 @@ cudaError_t launch_select(const strata_select_t& sel, const void* logits, int T,
   const int fit = 152 * SEL_CTAS * SEL_WARPS, turns = (T + fit - 1) / fit;
   const int warps = (T + turns - 1) / turns, grid = (warps + SEL_WARPS - 1) / SEL_WARPS;
   kernel_begin(KID_SELECT, s);
-  if (values && sel.n_expert > 256) launch_form<true, 16>(a, grid, s);
-  else if (values) launch_form<true, 8>(a, grid, s);
-  else if (sel.n_expert > 256) launch_form<false, 16>(a, grid, s);
-  else launch_form<false, 8>(a, grid, s);
+  const bool wide = sel.n_expert > 256;
+  const cudaError_t err = values ? (wide ? launch_form<true, 16>(a, grid, s) : launch_form<true, 8>(a, grid, s))
+                                 : (wide ? launch_form<false, 16>(a, grid, s) : launch_form<false, 8>(a, grid, s));
   kernel_end(KID_SELECT, s);
-  return cudaGetLastError();
+  return err;
 }
 
 }  // namespace strata
