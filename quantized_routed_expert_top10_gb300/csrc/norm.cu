@@ -6,12 +6,13 @@
 // between its one read and its one write, both mean squares are sums over its CTA.
 //
 // The kernels may start while the one before them ends (griddep_wait) and let the next one start when their rows are done;
-// started earlier, its CTAs took room from this one's (ten parts 44 -> 47 us).  All forms are bound by memory, or by the launch where rows are few (four rows 2.0 us, one token's ten parts 4.3 us), so each
-// keeps rows on their way while another is summed: CTAs stay and walk the rows, and what comes next is already being read,
-// into registers (one part or none) or a ring in shared memory (several).  A CTA a row without that: 39 us for the
-// norm below, 65 us for ten parts.  On one GB300, 2,560 columns: the norm of 8,192 rows, fp32 to bf16, 22.4 us (5.6 TB/s), a
-// copy of 42 MB and back 15 to 20 us; 2,048 rows of ten fp32 parts 43.5 us (6.3 TB/s, 92% of the measured copy rate); 8,192 rows
-// of one fp32 part with the stream in bf16 38.6 us (5.4 TB/s).
+// started earlier, its CTAs took room from this one's (ten parts 44 -> 47 us).  All forms are bound by memory, or by the
+// launch where rows are few (four rows 2.0 us, one token's ten parts 4.3 us), so each keeps rows on their way while another is
+// summed: CTAs stay and walk the rows, and what comes next is already being read, into registers (one part or none) or a
+// ring in shared memory (several).  A CTA a row without that: 39 us for the norm below, 65 us for ten parts.  On one GB300, 2,560
+// columns: the norm of 8,192 rows, fp32 to bf16, 22.4 us (5.6 TB/s), a copy of 42 MB and back 15 to 20 us; 2,048 rows of ten
+// fp32 parts 43.5 us (6.3 TB/s, 92% of the measured copy rate); 8,192 rows of one fp32 part with the stream in bf16 38.6 us
+// (5.4 TB/s).
 #include "device_common.cuh"
 #include "elements.cuh"
 
