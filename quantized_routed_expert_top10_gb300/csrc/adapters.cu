@@ -7,7 +7,7 @@
 // Segments of few tokens, or few tokens times ranks in all, go by one kernel: tiles of 8, 16 or 32 tokens of one segment, a cluster
 // a tile, warp-level MMAs.  It is bound by the latency of its chain (segments, A and x, the cluster's sum, B and base), which is
 // why everything that a CTA reads is asked for as early as its registers allow: one token 4.3 us, 64 tokens of 64 adapters
-// (10.5 MB of them) 5.8 us; 2,048 ragged fp32 tokens, rank 32, 21 us (3.5 TB/s).  The rest go by two kernels in tiles of 128 tokens on
+// (10.5 MB of them) 5.8 us; 2,048 ragged fp32 tokens, rank 32, 16 us (4.1 TB/s).  The rest go by two kernels in tiles of 128 tokens on
 // the 5th-generation tensor cores, shrink (v = A_a x) and expand (base + B_a (scale v)): 8,192 tokens of 32 adapters of
 // rank 64, 2,560 -> 2,560, bf16, 49.6 us (3.0 TB/s), about 22 and 27, bound by their own latencies at two to three CTAs an SM.
 #include "device_common.cuh"
@@ -990,15 +990,16 @@ cudaError_t launch_adapters(const strata_adapters_t& ad, const int32_t* seg_off,
   a.x = x; a.base = base; a.y = y; a.v = v_terms; a.status = status;
   a.rank = ad.rank; a.d_in = ad.d_in; a.d_out = ad.d_out; a.T = T; a.x_type = ad.x_type; a.y_type = ad.y_type;
   // The 128-row kernels cost a call more and a token's rank less than warp-level MMAs.  2,560 -> 2,560, bf16, in us, here and
-  // there: rank 32, 8,192 tokens 40 and 46; rank 64, 2,048 tokens 23 and 27, 8,192 tokens 59 and 50; rank 128, 1,024 tokens 35
-  // and 38, 2,048 tokens 57 and 45.  fp32: rank 64, 8,192 tokens 85 and 105; rank 128, 2,048 tokens 71 and 56.
+  // there: rank 32, 8,192 tokens 40 and 46; rank 64, 4,096 tokens 31 and 32, 8,192 tokens 59 and 50; rank 128, 2,048 tokens
+  // in 32 segments 29 and 38, in 64 57 and 45.  fp32: rank 64, 8,192 tokens 85 and 105; rank 128, 2,048 tokens in 32 43 and 56.
   const int filled = n_seg < T ? n_seg : T;
   const bool half = T / 16 + filled / 2 <= 152;  // tiles of 16 tokens, two CTAs each, all at once (a last tile half full)
   const bool many = (int64_t)T * a.rank > (half ? 256 : 192) * 1024 && a.rank > (a.x_type == STRATA_F32 ? 64 : 32);
   if (many && T >= LONG * n_seg) return launch_tc(a, s);
-  // Tiles of 8 tokens where segments are as short, else of 16 while the device holds them, else of 32, which read A and B half
-  // as often: 2,048 tokens in 24 segments, fp32, rank 32, 16 us and 21; 4,096 in 32, bf16, rank 16, 19 and 17.
-  if (T <= 8 * n_seg) return launch_short<1>(a, s);
+  // Tiles of 8 tokens where segments are as short or four CTAs a tile fit the device; else of 16 while two each fit; else of 32.
+  // Larger tiles read A and B less often, smaller ones fill the device: 256 tokens in 8 segments, bf16, rank 16 by 8 and 16, 5.7 us
+  // and 6.7; 2,048 in 24, fp32, rank 32 by 16 and 32, 16 us and 21; 4,096 in 32, bf16, rank 16, 19 and 17.
+  if (T <= 8 * n_seg || T / 8 + filled / 2 <= 76) return launch_short<1>(a, s);
   return half ? launch_short<2>(a, s) : launch_short<4>(a, s);
 }
 

@@ -119,6 +119,13 @@ def test_many_tokens(xk, yk, rank):
     Case([2000, 127, 0, 2049, 1, 900], [0, 4, 1, 2, -1, 0], rank, 264, 136, xk, yk, after=2).check()
 
 
+@pytest.mark.parametrize("xk,yk", list(itertools.product(KINDS, KINDS)))
+@pytest.mark.parametrize("rank", [8, 16, 32, 40, 64])
+def test_long_calls_of_small_ranks(xk, yk, rank):
+    Case([800, 0, 300, 33, 1, 127, 900, 450], [3, 0, 1, -1, 2, 4, 2, 0], rank, 264, 136, xk, yk, before=1, after=3).check()
+    Case([1300, 31, 1500], [1, -1, 1], rank, 64, 264, xk, yk, inplace=True, pad=8).check()
+
+
 FEW = ([0, 1, 8, 9, 17, 0, 3, 2, 0, 1, 1, 7, 0, 5], [3, 0, 1, -1, 2, -1, 4, 2, 0, 0, 1, 1, 2, 2])  # 54 tokens in 14 segments
 
 
