@@ -9,7 +9,7 @@
 // why everything that a CTA reads is asked for as early as its registers allow: one token 4.3 us, 64 tokens of 64 adapters
 // (10.5 MB of them) 5.8 us; 2,048 ragged fp32 tokens, rank 32, 16 us (4.1 TB/s).  The rest go by two kernels in tiles of 128 tokens on
 // the 5th-generation tensor cores, shrink (v = A_a x) and expand (base + B_a (scale v)): 8,192 tokens of 32 adapters of
-// rank 64, 2,560 -> 2,560, bf16, 49.6 us (3.0 TB/s), about 22 and 27, bound by their own latencies at two to three CTAs an SM.
+// rank 64, 2,560 -> 2,560, bf16, 46.6 us (3.2 TB/s), about 18 and 28, bound by their own latencies at two to three CTAs an SM.
 #include "device_common.cuh"
 #include "elements.cuh"
 #include "tc_common.cuh"
@@ -35,7 +35,6 @@ struct AdapterArgs {
   uint16_t* v;  // [term][T][rank]
   int* status;
   int n_seg, n_adapter, rank, d_in, d_out, T, x_type, y_type, split, k_slice;
-  int early;  // base goes to L2 while the shrink kernel finishes
 };
 
 struct Tile {
@@ -587,14 +586,6 @@ __global__ void __launch_bounds__(AD_THREADS + 32, XT == STRATA_F32 ? 2 : 3) shr
     }
     copy_wait(0);
   }
-  if (a.early) {
-    // the cluster's share of base, 128 bytes a thread and turn: memory has little else to do until the expand kernel
-    const int64_t size = a.y_type == STRATA_F32 ? 4 : 2;
-    const int lines = (int)((a.d_out * size + 127) / 128), l0 = lines * blockIdx.y / a.split, l1 = lines * (blockIdx.y + 1) / a.split;
-    const char* at = static_cast<const char*>(a.base) + tile.row * a.base_stride * size;
-    for (int r = warp; r < tile.rows; r += AD_WARPS + 1)
-      for (int l = l0 + lane; l < l1; l += 32) prefetch_l2(at + r * a.base_stride * size + 128 * l);
-  }
   waiter.wait(&s_done, 0);
   tc::fence_after_sync();
   __syncthreads();  // all have seen the last MMA: the stages are free for the sums
@@ -767,10 +758,10 @@ __global__ void __launch_bounds__(AD_THREADS + 32, 2) expand_tc_kernel(AdapterAr
       for (int i = 0; i < 4; ++i)
         to[i] = in && (rows >> i & 1u) ? load8(a.base, base_at + 8 * i * a.base_stride + CW * blk + 32 * sub, YT) : zero;
     };
-    // base of units further ahead goes to L2, a row of 128 columns two threads
+    // base of the unit after the next goes to L2 (8,192 tokens: 46.6 us, one further 47.5, none 51), a row of 128 columns two threads
     const auto warm = [&](int blk) {
       const int c0 = CW * (first + blk), size = YT == STRATA_F32 ? 4 : 2;
-      if (a.early || !a.base || blk >= blocks || brow >= tile.rows) return;
+      if (!a.base || blk >= blocks || brow >= tile.rows) return;
 #pragma unroll
       for (int c = (tid & 1) * 64; c < CW; c += YT == STRATA_F32 ? (c & 32 ? 128 : 32) : 128)
         if (c0 + c < a.d_out)
@@ -778,7 +769,6 @@ __global__ void __launch_bounds__(AD_THREADS + 32, 2) expand_tc_kernel(AdapterAr
     };
     for (int i = 0; i < ring - 1; ++i) copy_b(i);
     warm(1);
-    warm(2);
     fetch_base(0, 0, base[0]);
     fetch_base(0, 1, base[1]);
     if (!waited) griddep_wait();
@@ -834,7 +824,7 @@ __global__ void __launch_bounds__(AD_THREADS + 32, 2) expand_tc_kernel(AdapterAr
       }
       // into the slot of the unit just stored, whose product's MMAs this thread has waited for
       if (blk < blocks) copy_b(blk + ring - 1);
-      warm(blk + 3);
+      warm(blk + 2);
     }
     copy_wait(0);
     if (product) n += blocks;
@@ -967,8 +957,6 @@ cudaError_t launch_tc(AdapterArgs a, cudaStream_t s) {
   while (split < SPLIT_MAX && 2 * tiles * split <= 152 * (a.x_type == STRATA_F32 ? 2 : 3) && a.d_in / (2 * split) >= 256) split *= 2;
   a.split = split;
   a.k_slice = ((a.d_in + split - 1) / split + 63) / 64 * 64;
-  // up to a third of the 129 MB L2: x, base and y of a call then fit beside one another
-  a.early = a.base && (int64_t)a.T * a.d_out * (a.y_type == STRATA_F32 ? 4 : 2) <= (int64_t)43 << 20;
   const cudaError_t err = a.x_type == STRATA_BF16  ? launch_shrink_tc<STRATA_BF16>(a, tiles, s)
                           : a.x_type == STRATA_F16 ? launch_shrink_tc<STRATA_F16>(a, tiles, s)
                                                    : launch_shrink_tc<STRATA_F32>(a, tiles, s);
@@ -991,10 +979,11 @@ cudaError_t launch_adapters(const strata_adapters_t& ad, const int32_t* seg_off,
   a.rank = ad.rank; a.d_in = ad.d_in; a.d_out = ad.d_out; a.T = T; a.x_type = ad.x_type; a.y_type = ad.y_type;
   // The 128-row kernels cost a call more and a token's rank less than warp-level MMAs.  2,560 -> 2,560, bf16, in us, here and
   // there: rank 32, 8,192 tokens 40 and 46; rank 64, 4,096 tokens 31 and 32, 8,192 tokens 59 and 50; rank 128, 2,048 tokens
-  // in 32 segments 29 and 38, in 64 57 and 45.  fp32: rank 64, 8,192 tokens 85 and 105; rank 128, 2,048 tokens in 32 43 and 56.
+  // in 32 segments 29 and 38, in 64 57 and 45.  x or y fp32: rank 64, 8,192 tokens 70 to 85 and 85 to 105; rank 128, 2,048 tokens in 32 43 and 56.
   const int filled = n_seg < T ? n_seg : T;
   const bool half = T / 16 + filled / 2 <= 152;  // tiles of 16 tokens, two CTAs each, all at once (a last tile half full)
-  const bool many = (int64_t)T * a.rank > (half ? 256 : 192) * 1024 && a.rank > (a.x_type == STRATA_F32 ? 64 : 32);
+  const bool wide = a.x_type == STRATA_F32 || a.y_type == STRATA_F32;
+  const bool many = (int64_t)T * a.rank > (half ? 256 : 192) * 1024 && a.rank > (wide ? 64 : 32);
   if (many && T >= LONG * n_seg) return launch_tc(a, s);
   // Tiles of 8 tokens where segments are as short or four CTAs a tile fit the device; else of 16 while two each fit; else of 32.
   // Larger tiles read A and B less often, smaller ones fill the device: 256 tokens in 8 segments, bf16, rank 16 by 8 and 16, 5.7 us
