@@ -329,3 +329,45 @@ def test_bad_numbers_stay_in_their_row(lens, rank, kind):
     rest = [t for t in range(c.T) if t not in bad]
     assert torch.equal(c.y[rest], want[rest])
     assert not torch.isfinite(c.y[bad].float()).all(1).any()
+
+
+# Calls that take tiles of 128 tokens: more than 256K tokens x rank.
+@pytest.mark.parametrize("kind", KINDS)
+def test_no_term_of_an_operand_is_lost_in_tiles_of_128(kind):
+    test_no_term_of_an_operand_is_lost_at_any_length(2500 + kind, 128)
+
+
+@pytest.mark.parametrize("lens,rank", [([2500], 128), ([1700, 0, 900, 400], 104)])
+def test_bad_segments_in_tiles_of_128(lens, rank):
+    test_bad_segments_of_any_length_compute_nothing(lens, rank)
+
+
+def test_tiles_of_128_repeat_and_run_at_once():
+    cases = [Case([1400, 1, 0, 1300], [0, 1, 2, 3], 128, 264, 136, qre.BF16, qre.BF16, before=2, after=1),
+             Case([2500, 700], [4, 4], 104, 264, 520, qre.F32, qre.F32, seed=9),
+             Case([2048, 2900], [1, -1], 72, 520, 264, qre.F16, qre.F16, seed=13, inplace=False),
+             Case([1] * 100, [i % 5 for i in range(100)], 16, 520, 392, seed=15)]
+    for c in cases:
+        c.check()
+    want = [c.y.clone() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    graphs = []
+    torch.cuda.synchronize()
+    for c, s in zip(cases, streams):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            c.call()
+            c.call()
+    for _ in range(10):
+        for c, s, g in zip(cases, streams, graphs):
+            with torch.cuda.stream(s):
+                c.call()
+                g.replay()
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        assert qre.strata_poll_status(c.ws) == 0 and torch.equal(c.y, w)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_bad_numbers_stay_in_their_row_in_tiles_of_128(kind):
+    test_bad_numbers_stay_in_their_row([2200, 130], 128, kind)
