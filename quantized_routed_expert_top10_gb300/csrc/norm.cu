@@ -502,7 +502,7 @@ cudaError_t launch_ring(const NormArgs& a, cudaStream_t s) {
 // ---- Rows that are not on boundaries of 4 elements ----------------------------------------------------------
 // The same line of steps, copied as the 16-byte pieces that hold a row's bytes, wherever in them it starts, and
 // taken out of shared memory a column at a time: a warp has 32 V columns in a row, a thread every 32nd (so a row's
-// addresses differ by constants: these rows are bound by the count of instructions, issued in 69% of cycles).  A thread
+// addresses differ by constants: these rows are bound by instructions, issued in 50 to 69% of cycles).  A thread
 // reads what others copied, so that a step costs a barrier; it also frees the slot read before.  2,559 columns: the norm of
 // 8,192 rows from fp32 to bf16 24.4 us (5.1 TB/s), 2,048 rows of ten fp32 parts 52 us (5.2 TB/s).
 // f(v) for a lane's columns, v of V; all of a warp inside its row as a rule.
