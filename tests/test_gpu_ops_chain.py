@@ -154,3 +154,55 @@ def test_first_calls_of_a_process_inside_a_capture():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_IN_CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("odd", [0, 1])
+def test_rows_further_apart_than_32_bits_count(odd):
+    """Rows 2^30 elements and more apart: offsets of elements and bytes beyond 32 bits."""
+    T, n, stride = 4, 264 + odd, (1 << 30) + 8
+    buf = torch.empty((T - 1) * stride + n, dtype=torch.bfloat16, device=DEV)
+    x = torch.as_strided(buf, (T, n), (stride, 1))
+    g = torch.Generator(DEV).manual_seed(3)
+    x.copy_(torch.randn(T, n, generator=g, device=DEV))
+    dense = x.contiguous()
+    K16 = qre.BF16
+
+    def same(call):
+        """call(rows, stride) for the far rows and for dense ones."""
+        far, near = torch.empty(T, n, device=DEV), torch.empty(T, n, device=DEV)
+        call(x, stride, far)
+        call(dense, n, near)
+        torch.cuda.synchronize()
+        assert torch.equal(far, near) and (far != 0).any()
+
+    same(lambda v, st, o: qre.strata_moe_norm(qre.norm(n, x_type=K16, x_stride=st), v.data_ptr(), T, None, o))
+    same(lambda v, st, o: qre.strata_moe_combine_norm(
+        qre.combine_norm(n, 1, x_type=K16, part_type=K16, next_type=qre.F32, part_stride=n, token_stride=st, x_stride=st),
+        v.data_ptr(), None, v.data_ptr(), T, None, None, None, None, None, o))
+    same(lambda v, st, o: qre.strata_moe_combine_norm(
+        qre.combine_norm(n, 4, x_type=K16, part_type=K16, next_type=qre.F32, part_stride=st, token_stride=3 * st + n),
+        v.data_ptr(), None, None, 1, None, None, None, None, None, o[0]) or o[1:].zero_())
+    # written far apart
+    out = torch.empty(T, n, dtype=torch.bfloat16, device=DEV)
+    qre.strata_moe_norm(qre.norm(n, x_type=K16, out_type=K16), dense, T, None, out)
+    qre.strata_moe_norm(qre.norm(n, x_type=K16, out_type=K16, x_stride=stride, out_stride=stride), x.data_ptr(), T, None, x.data_ptr())
+    assert torch.equal(x.contiguous(), out)
+    # routing and adapters (dense rows of eights)
+    if not odd:
+        ids, w, ids2, w2 = (torch.empty(T, 4, dtype=d, device=DEV) for d in (torch.int32, torch.float32) * 2)
+        qre.strata_moe_select(qre.select(n, 4, logits_type=K16, logits_stride=stride), x.data_ptr(), T, None, ids, w)
+        qre.strata_moe_select(qre.select(n, 4, logits_type=K16), out, T, None, ids2, w2)
+        assert torch.equal(ids, ids2) and torch.equal(w, w2)
+        a, b = torch.randn(1, 16, n, device=DEV).bfloat16(), torch.randn(1, n, 16, device=DEV).bfloat16()
+        off, of = torch.tensor([0, T], dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+        ws = workspace(T)
+        near = torch.empty(T, n, device=DEV)
+        far = torch.empty(T, n, device=DEV)
+        qre.strata_moe_adapters(qre.adapters(a, b, 1, 16, n, n, x_type=K16), off, of, 1, out, T, None, near, ws)
+        qre.strata_moe_adapters(qre.adapters(a, b, 1, 16, n, n, x_type=K16, x_stride=stride), off, of, 1, x.data_ptr(), T, None, far, ws)
+        assert torch.equal(far, near)
+        y = torch.empty(T, n, dtype=torch.bfloat16, device=DEV)
+        qre.strata_moe_adapters(qre.adapters(a, b, 1, 16, n, n, y_type=K16), off, of, 1, near, T, out, y, ws)
+        qre.strata_moe_adapters(qre.adapters(a, b, 1, 16, n, n, y_type=K16, base_stride=stride, y_stride=stride), off, of, 1, near, T,
+                                x.data_ptr(), x.data_ptr(), ws)
+        assert torch.equal(x.contiguous(), y)
