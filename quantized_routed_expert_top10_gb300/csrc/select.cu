@@ -400,7 +400,8 @@ __global__ void __launch_bounds__(32 * SEL_WARPS, SEL_CTAS) select_kernel(const 
       inv_z = z > 0.f ? 1.f / z : 1.f;
       if (VALUES && a.bias) {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) v[j] = fmaf(v[j], inv_z, s_bias[lane + 32 * j]);
+        for (int j = 0; j < PER; ++j)  // (a masked expert stays at -inf whatever its bias: -inf + inf would be a NaN)
+          v[j] = v[j] > -INFINITY ? fmaf(v[j], inv_z, s_bias[lane + 32 * j]) : -INFINITY;
       }
       err = U32 * ERR_SOFTMAX * inv_z + 1e-37f;
     }

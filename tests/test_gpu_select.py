@@ -176,3 +176,27 @@ def test_repeats_streams_and_graphs():
     torch.cuda.synchronize()
     want, _, _ = ref.select(ref.to64(l), qre.F32, ref.to64(b), k, SIG, 16, 4, 2)
     np.testing.assert_array_equal(ids.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("score", [SOFT, SIG])
+@pytest.mark.parametrize("kind", [qre.F32, qre.BF16, qre.F16])
+def test_bias_of_infinity_brings_no_masked_expert_back(score, kind):
+    T, E = 48, 64
+    l = randn(T, E, seed=18)
+    for i, mask in enumerate((-np.inf, torch.finfo(ref.TORCH[kind]).min, float("nan"))):
+        l[i::4, 5] = mask
+        l[i::8, 16:28] = mask  # a group of eight and half of the next
+    l[47] = -np.inf
+    b = randn(E, seed=19, std=0.1)
+    b[[5, 22, 40]] = np.inf
+    for groups in (1, 8):
+        G, keep, gsum = GROUPS[groups]
+        for renorm in (True, False):
+            ids, w = run(l, kind, b, 10, score, n_group=G, top_group=keep, group_sum=gsum, renorm=renorm)
+            assert np.isfinite(w).all()
+    rising = torch.arange(32).float().repeat(3, 1) / 8
+    rising[0, 5], rising[1, 5], rising[2, 5] = -np.inf, torch.finfo(ref.TORCH[kind]).min, float("nan")
+    b = torch.zeros(32)
+    b[5] = np.inf
+    ids, _ = run(rising, kind, b, 3, score)
+    assert (ids == [31, 30, 29]).all()
