@@ -442,7 +442,9 @@ __global__ void __launch_bounds__(32 * SEL_WARPS, SEL_CTAS) select_kernel(const 
         if (k1 > -INFINITY) v1 = a.softmax ? ex2((k1 - m) * LOG2E) * inv_z : sigmoid_fast(k1);
       }
       const bool two = a.group_sum == 2 && v1 > -INFINITY;
-      const float gs = two ? v0 + v1 : v0;
+      // (a sum below the fp32 range is its lowest number, not the -inf of a group without a usable expert: sums that were cut
+      // so are equal or nearly, and the groups are then told apart in 64 bits)
+      const float gs = v0 > -INFINITY ? fmaxf(two ? v0 + v1 : v0, -FLT_MAX) : -INFINITY;
       int rank = 0;
 #pragma unroll 4
       for (int h = 0; h < a.G; ++h) {

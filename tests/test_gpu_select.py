@@ -200,3 +200,22 @@ def test_bias_of_infinity_brings_no_masked_expert_back(score, kind):
     b[5] = np.inf
     ids, _ = run(rising, kind, b, 3, score)
     assert (ids == [31, 30, 29]).all()
+
+
+@pytest.mark.parametrize("score", [SOFT, SIG])
+def test_groups_whose_sum_leaves_the_fp32_range(score):
+    # three groups of four, the sums of the last two below fp32's lowest, and above its largest
+    b = torch.zeros(12)
+    b[4:8], b[8:] = -3e38, -2e38
+    ids, _ = run(randn(8, 12, seed=20), qre.F32, b, 6, score, n_group=3, top_group=2, group_sum=2)
+    assert (ids[:, :4] < 4).all() and (ids[:, 4:] >= 8).all()
+    ids, _ = run(randn(8, 12, seed=20), qre.F32, -b, 6, score, n_group=3, top_group=2, group_sum=2)
+    assert (ids[:, :4] // 4 == 1).all() and (ids[:, 4:] >= 8).all()
+    # any finite biases, groups without a usable expert and with one
+    l = randn(64, 64, seed=21)
+    l[::3, 8:16] = -np.inf
+    l[1::3, 17:24] = -np.inf
+    low = -(torch.rand(64, generator=torch.Generator().manual_seed(22)) * 1.6 + 1.8) * 1e38
+    for bias in (low, -low, torch.where(torch.arange(64) % 16 < 8, low, -low), torch.full((64,), torch.finfo(torch.float32).min)):
+        for keep in (1, 3, 7, 8):
+            run(l, qre.F32, bias, 8, score, n_group=8, top_group=keep, group_sum=2)
