@@ -284,13 +284,29 @@ __device__ __noinline__ uint32_t groups_exact(const SelectArgs& a, int t, Select
   return __ballot_sync(0xffffffffu, lane < a.G && rank < a.keep);
 }
 
-// The order of C candidates (sc.cand) by their values in 64 bits into sc.sel, where neighbours among the first k are too near
-// for fp32; near neighbours of the same logit and bias are true ties and stay as they are.
-__device__ __noinline__ void order_exact(const SelectArgs& a, int t, SelectScratch& sc, int C, bool near) {
+// Values x >= y that fp32 cannot tell apart: each is off by err and by the rounding of its sum with the bias.
+__device__ __forceinline__ bool too_near(float x, float y, float err) { return !(x - y > 2.f * err + U32 * (fabsf(x) + fabsf(y))); }
+
+// The order of C candidates (sc.cand) by their values in 64 bits into sc.sel, where neighbours among the first k (near: lane
+// i and i + 1) are too near for fp32; near neighbours of the same logit and bias are true ties and stay as they are.
+__device__ __noinline__ void order_exact(const SelectArgs& a, int t, SelectScratch& sc, int C, bool near, float err) {
   const int lane = threadIdx.x & 31;
-  if (near) {
-    const int p = cand_id(sc.sel[lane]), q = cand_id(sc.sel[lane + 1]);
-    near = !(logit_at(a, t, p) == logit_at(a, t, q) && __ldg(a.bias + p) == __ldg(a.bias + q));
+  const auto same = [&](int p, int q) {
+    return logit_at(a, t, p) == logit_at(a, t, q) && __ldg(a.bias + p) == __ldg(a.bias + q);
+  };
+  bool tie = false;  // of the last one chosen and the first one left
+  if (near && same(cand_id(sc.sel[lane]), cand_id(sc.sel[lane + 1]))) {
+    near = false;
+    tie = lane == a.k - 1;
+  }
+  if (__any_sync(0xffffffffu, tie)) {
+    // behind the first one left may be others too near to the last one chosen
+    const uint64_t last = sc.sel[a.k - 1], left = sc.sel[a.k];
+    const float x = key_logit(cand_key(last));
+    for (int i = lane; i < C; i += 32) {
+      const uint64_t c = sc.cand[i];
+      if (c < left && too_near(x, key_logit(cand_key(c)), err) && !same(cand_id(last), cand_id(c))) near = true;
+    }
   }
   if (!__any_sync(0xffffffffu, near)) return;
   float m = 0.f;
@@ -586,9 +602,9 @@ __global__ void __launch_bounds__(32 * SEL_WARPS, SEL_CTAS) select_kernel(const 
       if (lane < a.k && lane + 1 < C) {
         const uint32_t p = cand_key(sc.sel[lane]), q = cand_key(sc.sel[lane + 1]);
         const float x = key_logit(p), y = key_logit(q);
-        near = q > MASKED && !(x - y > 2.f * err + U32 * (fabsf(x) + fabsf(y)));
+        near = q > MASKED && too_near(x, y, err);
       }
-      if (__any_sync(0xffffffffu, near)) order_exact(a, t, sc, C, near);
+      if (__any_sync(0xffffffffu, near)) order_exact(a, t, sc, C, near, err);
     }
     // weights: without groups or a bias the k largest softmax scores sum to k / E at least, above the clamp, and the
     // softmax's own sum divides out

@@ -219,3 +219,36 @@ def test_groups_whose_sum_leaves_the_fp32_range(score):
     for bias in (low, -low, torch.where(torch.arange(64) % 16 < 8, low, -low), torch.full((64,), torch.finfo(torch.float32).min)):
         for keep in (1, 3, 7, 8):
             run(l, qre.F32, bias, 8, score, n_group=8, top_group=keep, group_sum=2)
+
+
+@pytest.mark.parametrize("ties", [2, 3, 5])
+def test_ties_at_the_end_of_the_choice_hide_no_near_value(ties):
+    """Equal experts on both sides of the end of the k, and another behind them whose value 32 bits cannot tell from theirs."""
+    T, E = 400, 64
+    g = np.random.default_rng(23)
+    l = (np.full((T, E), -4.0) + g.uniform(-0.1, 0.1, (T, E))).astype(np.float32)
+    b = g.uniform(-0.01, 0.01, E).astype(np.float32)
+    b[:32] = b[0]
+    for t in range(T):
+        e = g.choice(32, ties, replace=False)
+        l[t, e] = g.uniform(0.5, 2.0)
+        other = g.integers(32, E)
+        v = 1 / (1 + np.exp(-np.float64(l[t, e[0]]))) + np.float64(b[0]) - np.float64(b[other])
+        l[t, other] = np.float32(np.log(v / (1 - v)))
+        l[t, g.choice(np.setdiff1d(np.arange(E), [*e, other]), 2, replace=False)] = 6.0, 7.0
+    lt, bt = torch.from_numpy(l), torch.from_numpy(b)
+    for k in range(1, ties + 5):
+        run(lt, qre.F32, bt, k, SIG)
+    run(lt, qre.F32, bt, 3, SIG, n_group=8, top_group=8, group_sum=2)
+    # under a softmax: equal largest experts without a bias, another's bias made to fit
+    for t in range(60):
+        row = g.uniform(-1, 1, E)
+        e = np.sort(g.choice(E, ties + 1, replace=False))
+        row[e[:ties]] = 1.5
+        row = row.astype(np.float32)
+        p = np.exp(row.astype(np.float64) - 1.5)
+        p /= p.sum()
+        bias = np.zeros(E, np.float32)
+        bias[e[ties]] = np.float32(p[e[0]] - p[e[ties]])
+        for k in range(1, ties + 1):
+            run(torch.from_numpy(row[None]), qre.F32, torch.from_numpy(bias), k, SOFT)
