@@ -447,6 +447,13 @@ __device__ __forceinline__ void tmem_ld16x256b_x4_async(uint32_t taddr, uint32_t
 }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
+// A barrier of the CTA's producers and its issuer.  bar.sync wants whole warps, and the lanes may come from waits and loops of
+// different lengths.
+__device__ __forceinline__ void stage_barrier() {
+  __syncwarp();
+  named_barrier(1, AD_THREADS + 32);
+}
+
 // A wait that ran out is recorded; the CTA's later waits are then skipped (the call's result is void).
 struct Waiter {
   int* status;
@@ -540,7 +547,7 @@ __global__ void __launch_bounds__(AD_THREADS + 32, XT == STRATA_F32 ? 2 : 3) shr
   if (issuer) {
     uint64_t desc = tc::smem_desc_sw128(smem_u32(smem));
     for (int kb = 0, stage = 0; kb < blocks; ++kb) {
-      named_barrier(1, AD_THREADS + 32);  // k-block kb is in shared memory
+      stage_barrier();  // k-block kb is in shared memory
       if (lane == 0) {
         tc::fence_after_sync();
         const uint64_t ad = desc + (uint64_t)(stage * (stage_bytes >> 4)), bd = ad + TERMS * (TC_TILE >> 4);
@@ -578,7 +585,7 @@ __global__ void __launch_bounds__(AD_THREADS + 32, XT == STRATA_F32 ? 2 : 3) shr
         }
         copy_wait(stages - 2);
         tc::fence_proxy_async_smem();
-        named_barrier(1, AD_THREADS + 32);
+        stage_barrier();
         // the stage of k-block kb - 1 is free once its MMAs are done
         if (kb > 0) waiter.wait(&s_empty[(kb - 1) % stages], ((kb - 1) / stages) & 1);
         copy(kb + stages - 1);
@@ -714,7 +721,7 @@ __global__ void __launch_bounds__(AD_THREADS + 32, 2) expand_tc_kernel(AdapterAr
       waited = true;
       if (product)
         for (int blk = 0; blk < blocks; ++blk) {
-          named_barrier(1, AD_THREADS + 32);  // A_a x and B of unit blk are in shared memory
+          stage_barrier();  // A_a x and B of unit blk are in shared memory
           if (lane == 0) {
             tc::fence_after_sync();
             const int acc = (n + blk) & 1;
@@ -728,7 +735,6 @@ __global__ void __launch_bounds__(AD_THREADS + 32, 2) expand_tc_kernel(AdapterAr
                               bd + (kk >> 2) * (TC_TILE >> 4) + 2 * (kk & 3), idesc, (t < TERMS - 1 || kk > 0) ? 1u : 0u);
             tc::mma_commit(&s_full[acc]);
           }
-          __syncwarp();
         }
       if (product) n += blocks;
       continue;
@@ -788,14 +794,13 @@ __global__ void __launch_bounds__(AD_THREADS + 32, 2) expand_tc_kernel(AdapterAr
         copy_wait(blk ? ring - 2 : 0);
         tc::fence_proxy_async_smem();
         tc::fence_before_sync();  // this thread's reads of the accumulator two units back
-        named_barrier(1, AD_THREADS + 32);
+        stage_barrier();
       }
       if (blk > 0) {
         const int b = blk - 1, acc = (n + b) & 1;
         if (product) {
           waiter.wait(&s_full[acc], ((n + b) >> 1) & 1);
           tc::fence_after_sync();
-          __syncwarp();
         }
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
@@ -804,6 +809,7 @@ __global__ void __launch_bounds__(AD_THREADS + 32, 2) expand_tc_kernel(AdapterAr
           for (int h = 0; h < 2; ++h) {  // rows mrow + 16 h, + 8
             uint32_t d[16];
             if (product) {
+              __syncwarp();  // (lanes whose row or column is outside store nothing)
               tmem_ld16x256b_x4_async(tmem + ((uint32_t)(32 * q4 + 16 * h) << 16) + (uint32_t)(CW * acc + 64 * half + 32 * sub), d);
               tc::tmem_wait_ld();
             }

@@ -371,3 +371,18 @@ def test_tiles_of_128_repeat_and_run_at_once():
 @pytest.mark.parametrize("kind", KINDS)
 def test_bad_numbers_stay_in_their_row_in_tiles_of_128(kind):
     test_bad_numbers_stay_in_their_row([2200, 130], 128, kind)
+
+
+# 2,500 tokens of rank 128 are 20 tiles and 3,000 in six segments up to 29, so d_in is cut into as many slices as a cluster
+# may have CTAs: 8 of 320.
+@pytest.mark.parametrize("xk,yk", list(itertools.product(KINDS, KINDS)))
+def test_slices_of_d_in_in_tiles_of_128(xk, yk):
+    Case([2500], [1], 128, 2560, 264, xk, yk).check()
+    for rank in (72, 104):
+        Case([1200, 0, 900, 128, 1, 771], [3, 0, 1, -1, 2, 4], rank, 2560, 136, xk, yk, before=1, after=3, pad=8).check()
+
+
+@pytest.mark.parametrize("d_in", [512, 520, 1032, 1096, 1544, 2048, 4104])
+def test_slices_of_any_width_in_tiles_of_128(d_in):
+    Case([2500], [1], 128, d_in, 72).check()
+    Case([2500], [1], 128, d_in, 72, qre.BF16, qre.BF16).check()
