@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(AD_THREADS + 32, XT == STRATA_F32 ? 2 : 3) shr
   const uint16_t* A = a.a + (int64_t)tile.adapter * a.a_stride;
   const float sc = a.scale ? __ldg(a.scale + tile.adapter) : 1.f;
   const int k0 = blockIdx.y * a.k_slice, k1 = min(a.d_in, k0 + a.k_slice);
-  const int blocks = k0 < k1 ? (k1 - k0 + 63) / 64 : 0;
+  const int blocks = (k1 - k0 + 63) / 64;  // at least one
   const int chunk = tid & 7, row0 = tid >> 3;
   const uint32_t stage_bytes = TERMS * TC_TILE + (uint32_t)np * 128;
   const int64_t x_size = XT == STRATA_F32 ? 4 : 2;
@@ -606,8 +606,7 @@ __global__ void __launch_bounds__(AD_THREADS + 32, XT == STRATA_F32 ? 2 : 3) shr
       tc::tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)c, f);
 #pragma unroll
       for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<float4*>(part + row * pitch + c + i) =
-            blocks ? make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(part + row * pitch + c + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
     }
   }
   tc::fence_before_sync();
@@ -961,8 +960,9 @@ cudaError_t launch_tc(AdapterArgs a, cudaStream_t s) {
   const int tiles = tiles_of(a, TC_ROWS);
   int split = 1;
   while (split < SPLIT_MAX && 2 * tiles * split <= 152 * (a.x_type == STRATA_F32 ? 2 : 3) && a.d_in / (2 * split) >= 256) split *= 2;
-  a.split = split;
+  // whole blocks of 64 k a slice; every slice has one (no MMAs are committed that were not issued, no sums of nothing added)
   a.k_slice = ((a.d_in + split - 1) / split + 63) / 64 * 64;
+  a.split = (a.d_in + a.k_slice - 1) / a.k_slice;
   const cudaError_t err = a.x_type == STRATA_BF16  ? launch_shrink_tc<STRATA_BF16>(a, tiles, s)
                           : a.x_type == STRATA_F16 ? launch_shrink_tc<STRATA_F16>(a, tiles, s)
                                                    : launch_shrink_tc<STRATA_F32>(a, tiles, s);

@@ -386,3 +386,11 @@ def test_slices_of_d_in_in_tiles_of_128(xk, yk):
 def test_slices_of_any_width_in_tiles_of_128(d_in):
     Case([2500], [1], 128, d_in, 72).check()
     Case([2500], [1], 128, d_in, 72, qre.BF16, qre.BF16).check()
+
+
+@pytest.mark.parametrize("d_in", [2056, 2120, 2568])
+@pytest.mark.parametrize("kind", KINDS)
+def test_widths_that_eight_slices_do_not_divide(d_in, kind):
+    """Slices are whole blocks of 64 columns: 2,056 and 2,120 columns are 7 slices of 320, 2,568 are 7 of 384."""
+    Case([2500], [1], 128, d_in, 72, kind, kind).check()
+    Case([1200, 0, 900, 128, 1, 771], [3, 0, 1, -1, 2, 4], 104, d_in, 136, kind, kind, before=1, after=3, pad=8).check()
