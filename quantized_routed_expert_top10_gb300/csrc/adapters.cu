@@ -396,8 +396,10 @@ __global__ void __launch_bounds__(AD_THREADS, 2) short_kernel(AdapterArgs a) {
       if (g + 8 * h >= tile.rows) continue;
       float f[8];
       widen8(base[h], WIDE ? STRATA_F32 : a.y_type, f);
+      if (product) {  // (without an adapter y is base: -0 + 0 would be +0)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] += acc[h >> 1][i >> 1][2 * (h & 1) + (i & 1)];
+        for (int i = 0; i < 8; ++i) f[i] += acc[h >> 1][i >> 1][2 * (h & 1) + (i & 1)];
+      }
       store8(y_at + (8 * h * a.y_stride + c0) * Y_SIZE, 0, WIDE ? STRATA_F32 : a.y_type, f);
     }
   }

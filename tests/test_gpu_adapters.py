@@ -394,3 +394,33 @@ def test_widths_that_eight_slices_do_not_divide(d_in, kind):
     """Slices are whole blocks of 64 columns: 2,056 and 2,120 columns are 7 slices of 320, 2,568 are 7 of 384."""
     Case([2500], [1], 128, d_in, 72, kind, kind).check()
     Case([1200, 0, 900, 128, 1, 771], [3, 0, 1, -1, 2, 4], 104, d_in, 136, kind, kind, before=1, after=3, pad=8).check()
+
+
+def check_rows_without_an_adapter(lens, of, rank, kind, base=True):
+    c = Case(lens, of, rank, 264, 136, kind, kind, base=base)
+    if base:
+        c.base[:, ::3] = -0.0
+        c.base[:, 1::7] *= torch.finfo(c.base.dtype).tiny  # some below the normal numbers
+        c.base[:, 5] = float("inf")
+    c.call()
+    assert qre.strata_poll_status(c.ws) == 0
+    bits = torch.int32 if kind == qre.F32 else torch.int16
+    for i, ad in enumerate(of):
+        if ad < 0:
+            s = slice(c.off[i], c.off[i + 1])
+            want = c.base[s] if base else torch.zeros_like(c.y[s])
+            assert torch.equal(c.y[s].contiguous().view(bits), want.contiguous().view(bits))
+
+
+@pytest.mark.parametrize("lens,of", [([3, 1, 5], [-1, 0, -1]), ([200, 1100, 300], [-1, 2, -1]), ([1500, 2600, 31], [-1, 2, -1])])
+@pytest.mark.parametrize("kind", KINDS)
+def test_rows_without_an_adapter_keep_base_bit_for_bit(lens, of, kind):
+    for rank in (16, 32):
+        check_rows_without_an_adapter(lens, of, rank, kind)
+        check_rows_without_an_adapter(lens, of, rank, kind, base=False)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_rows_without_an_adapter_keep_base_in_tiles_of_128(kind):
+    check_rows_without_an_adapter([300, 2500, 130], [-1, 2, -1], 128, kind)
+    check_rows_without_an_adapter([300, 2500, 130], [-1, 2, -1], 128, kind, base=False)
