@@ -16,7 +16,9 @@
  * `stream` (of the current device), host-checkable errors returned before anything is enqueued, T == 0 a
  * valid empty call, T <= STRATA_MOE_T_MAX.  No call allocates device memory or synchronises, so all of them
  * can be captured into a CUDA graph.  strata_moe_select, strata_moe_norm and strata_moe_combine_norm use no
- * workspace.  All calls repeat bit for bit.  Descriptors are host structs, read during the call.
+ * workspace.  All calls repeat bit for bit.  Descriptors are host structs, read during the call.  Operands overlap
+ * where a row of one shares a byte with a row of the other: rows that lie between each other, as column ranges of one
+ * buffer do, are fine.
  *
  * Element types (the framework's own activations are fp32): arithmetic is in 32 bits or more whatever the
  * type, and a result is rounded once, when it is stored. */

@@ -17,19 +17,43 @@ inline bool good_stride(int64_t s, int64_t least) { return s >= least && s <= ST
 inline bool good_T(int32_t T) { return T >= 0 && T <= TMAX; }
 inline bool flag(int32_t v) { return v == 0 || v == 1; }
 
-// The bytes an operand of `rows` rows of n elements covers.
-struct Span {
-  const char* p;
-  int64_t bytes, stride;
+// An operand: `rows` rows of `bytes` bytes, `step` >= bytes apart.
+struct Rows {
+  const char* p;  // null: no operand
+  int64_t rows, step, bytes;
   int32_t type;
 };
-Span span(const void* p, int64_t rows, int64_t stride, int64_t n, int32_t type) {
-  return Span{(const char*)p, p ? ((rows - 1) * stride + n) * type_bytes(type) : 0, stride, type};
+Rows rows_of(const void* p, int64_t rows, int64_t stride, int64_t n, int32_t type) {
+  if (!p) return Rows{};  // its stride is not looked at
+  return Rows{(const char*)p, rows, stride * type_bytes(type), n * type_bytes(type), type};
 }
-bool overlap(const Span& a, const Span& b) { return a.p && b.p && a.p < b.p + b.bytes && b.p < a.p + a.bytes; }
+// a / b rounded down, b > 0
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0 ? 1 : 0); }
+
+// Some row of a and some row of b share a byte.  (Rows of one may lie between those of the other, as column ranges of one
+// buffer do.)
+bool overlap(const Rows& a, const Rows& b) {
+  if (!a.p || !b.p) return false;
+  const int64_t d = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p);
+  if (d >= (a.rows - 1) * a.step + a.bytes || -d >= (b.rows - 1) * b.step + b.bytes) return false;
+  // row j of b begins d + j b.step - i a.step behind row i of a; they meet if that is in (-b.bytes, a.bytes)
+  if (a.step == b.step) {  // j - i alone counts, and of its values only the two around -d / step come near enough
+    const int64_t k = floor_div(-d, a.step);
+    for (int64_t c = k; c <= k + 1; ++c)
+      if (c > -a.rows && c < b.rows && d + c * a.step > -b.bytes && d + c * a.step < a.bytes) return true;
+    return false;
+  }
+  for (int64_t i = 0; i < a.rows; ++i) {
+    const int64_t at = i * a.step - d;                       // row i of a, from b's start
+    const int64_t j = floor_div(at - b.bytes, b.step) + 1;  // the first row of b that ends behind it
+    const int64_t first = j > 0 ? j : 0;
+    if (first < b.rows && first * b.step < at + a.bytes) return true;
+  }
+  return false;
+}
 // Overlapping, and not the same array: a call may write an array that it reads row by row.
-bool partly(const Span& a, const Span& b) {
-  return overlap(a, b) && !(a.p == b.p && a.stride == b.stride && a.type == b.type);
+bool partly(const Rows& a, const Rows& b) {
+  return overlap(a, b) && !(a.p == b.p && a.step == b.step && a.type == b.type);
 }
 
 inline strata_status launched(cudaError_t e) { return e == cudaSuccess ? STRATA_OK : STRATA_E_CUDA; }
@@ -52,8 +76,8 @@ strata_status strata_moe_select(const strata_select_t* sel, const void* logits, 
   if (!aligned(logits, type_bytes(sel->logits_type)) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
     return STRATA_E_ALIGN;
   if (T == 0) return STRATA_OK;
-  const Span sl = span(logits, T, sel->logits_stride, E, sel->logits_type);
-  const Span si = span(ids, T, sel->top_k, sel->top_k, STRATA_F32), sw = span(weights, T, sel->top_k, sel->top_k, STRATA_F32);
+  const Rows sl = rows_of(logits, T, sel->logits_stride, E, sel->logits_type);
+  const Rows si = rows_of(ids, T, sel->top_k, sel->top_k, STRATA_F32), sw = rows_of(weights, T, sel->top_k, sel->top_k, STRATA_F32);
   if (overlap(sl, si) || overlap(sl, sw) || overlap(si, sw)) return STRATA_E_INVAL;
   return launched(launch_select(*sel, logits, T, bias, ids, weights, (cudaStream_t)stream));
 }
@@ -68,7 +92,7 @@ strata_status strata_moe_norm(const strata_norm_t* nd, const void* x, int32_t T,
   if (!aligned(x, type_bytes(nd->x_type)) || !aligned(out, type_bytes(nd->out_type)) || !aligned(gain, 4))
     return STRATA_E_ALIGN;
   if (T == 0) return STRATA_OK;
-  if (partly(span(x, T, nd->x_stride, n, nd->x_type), span(out, T, nd->out_stride, n, nd->out_type)))
+  if (partly(rows_of(x, T, nd->x_stride, n, nd->x_type), rows_of(out, T, nd->out_stride, n, nd->out_type)))
     return STRATA_E_INVAL;
   return launched(launch_norm(*nd, x, T, gain, out, (cudaStream_t)stream));
 }
@@ -99,10 +123,14 @@ strata_status strata_moe_combine_norm(const strata_combine_norm_t* cn, const voi
       !aligned(post_gain, 4) || !aligned(channel_gate, 4) || !aligned(token_gate, 4) || !aligned(pre_gain, 4))
     return STRATA_E_ALIGN;
   if (T == 0) return STRATA_OK;
-  const Span sp = span(parts, T, cn->token_stride, (P - 1) * cn->part_stride + n, cn->part_type);
-  const Span sx = span(x, T, cn->x_stride, n, cn->x_type), so = span(out, T, cn->out_stride, n, cn->x_type);
-  const Span sn = span(next, T, cn->next_stride, n, cn->next_type);
-  if (overlap(sp, so) || overlap(sp, sn) || overlap(so, sn) || partly(sx, so) || partly(sx, sn)) return STRATA_E_INVAL;
+  const Rows sx = rows_of(x, T, cn->x_stride, n, cn->x_type), so = rows_of(out, T, cn->out_stride, n, cn->x_type);
+  const Rows sn = rows_of(next, T, cn->next_stride, n, cn->next_type);
+  if (overlap(so, sn) || partly(sx, so) || partly(sx, sn)) return STRATA_E_INVAL;
+  for (int k = 0; k < P; ++k) {
+    const char* p = (const char*)parts + k * cn->part_stride * type_bytes(cn->part_type);
+    const Rows sp = rows_of(p, T, cn->token_stride, n, cn->part_type);
+    if (overlap(sp, so) || overlap(sp, sn)) return STRATA_E_INVAL;
+  }
   return launched(launch_combine_norm(*cn, parts, part_weights, x, T, post_gain, channel_gate, token_gate, pre_gain, out,
                                       next, (cudaStream_t)stream));
 }
@@ -130,8 +158,8 @@ strata_status strata_moe_adapters(const strata_adapters_t* ad, const int32_t* se
   const WsLayout L = ws_layout(T);
   if (ws_bytes < L.total) return STRATA_E_WORKSPACE;
   if (T == 0 || n_seg == 0) return STRATA_OK;
-  const Span sx = span(x, T, ad->x_stride, ad->d_in, ad->x_type), sy = span(y, T, ad->y_stride, ad->d_out, ad->y_type);
-  const Span sb = span(base, T, ad->base_stride, ad->d_out, ad->y_type);
+  const Rows sx = rows_of(x, T, ad->x_stride, ad->d_in, ad->x_type), sy = rows_of(y, T, ad->y_stride, ad->d_out, ad->y_type);
+  const Rows sb = rows_of(base, T, ad->base_stride, ad->d_out, ad->y_type);
   if (overlap(sx, sy) || partly(sb, sy)) return STRATA_E_INVAL;
   char* w = (char*)ws;
   return launched(launch_adapters(*ad, seg_off, seg_adapter, n_seg, x, T, base, y, (uint16_t*)(w + L.logits),

@@ -424,3 +424,29 @@ def test_rows_without_an_adapter_keep_base_bit_for_bit(lens, of, kind):
 def test_rows_without_an_adapter_keep_base_in_tiles_of_128(kind):
     check_rows_without_an_adapter([300, 2500, 130], [-1, 2, -1], 128, kind)
     check_rows_without_an_adapter([300, 2500, 130], [-1, 2, -1], 128, kind, base=False)
+
+
+def check_column_ranges(T, rank):
+    n = 136
+    a, b = rnd(2, rank, n, seed=31, std=n ** -0.5, kind=qre.BF16), rnd(2, n, rank, seed=32, std=rank ** -0.5, kind=qre.BF16)
+    off, of = torch.tensor([0, T // 2, T], dtype=torch.int32, device=DEV), torch.tensor([1, -1], dtype=torch.int32, device=DEV)
+    ws = workspace(T)
+    for kind in KINDS:
+        buf = rnd(T, 3 * n, seed=33, kind=kind)
+        x, base, y = buf[:, :n], buf[:, n:2 * n], buf[:, 2 * n:]
+        x0, base0 = x.contiguous(), base.contiguous()
+        want = torch.empty_like(x0)
+        qre.strata_moe_adapters(qre.adapters(a, b, 2, rank, n, n, x_type=kind, y_type=kind), off, of, 2, x0, T, base0, want, ws)
+        d = qre.adapters(a, b, 2, rank, n, n, x_type=kind, y_type=kind, x_stride=3 * n, base_stride=3 * n, y_stride=3 * n)
+        qre.strata_moe_adapters(d, off, of, 2, x.data_ptr(), T, base.data_ptr(), y.data_ptr(), ws)
+        assert qre.strata_poll_status(ws) == 0
+        assert torch.equal(y, want) and torch.equal(x, x0) and torch.equal(base, base0)
+
+
+@pytest.mark.parametrize("T,rank", [(1, 16), (40, 32), (1500, 16)])
+def test_column_ranges_of_one_buffer(T, rank):
+    check_column_ranges(T, rank)
+
+
+def test_column_ranges_of_one_buffer_in_tiles_of_128():
+    check_column_ranges(2500, 128)

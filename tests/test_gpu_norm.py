@@ -219,3 +219,37 @@ def test_repeats_streams_and_graphs():
     torch.cuda.synchronize()
     want, err = ref.rms_norm(ref.to64(out), np.zeros((T, n)), 1e-6, None)
     ref.check(nxt, want, err, qre.F32, "next")
+
+
+def test_column_ranges_of_one_buffer():
+    """Rows of one operand between the rows of another, as column ranges of one buffer: no element is shared."""
+    for n, T in ((64, 5), (2560, 300), (100, 700), (77, 9)):
+        def halves(seed, kind=qre.F32, count=2):
+            buf = rnd(T, count * n, seed=seed, kind=kind)
+            return buf, [buf[:, i * n:(i + 1) * n] for i in range(count)]
+
+        for kind in KINDS:
+            buf, (x, out) = halves(13, kind)
+            want = torch.empty(T, n, dtype=x.dtype, device=DEV)
+            before = x.clone()
+            qre.strata_moe_norm(qre.norm(n, x_type=kind, out_type=kind), before, T, None, want)
+            qre.strata_moe_norm(qre.norm(n, x_type=kind, out_type=kind, x_stride=2 * n, out_stride=2 * n), x.data_ptr(), T, None,
+                                out.data_ptr())
+            assert torch.equal(out, want) and torch.equal(x, before)
+        # a combine's two parts, its x and both results
+        buf, cols = halves(14, count=5)
+        parts, x = buf[:, :2 * n].contiguous(), cols[2].contiguous()
+        want = [torch.empty(T, n, device=DEV) for _ in range(2)]
+        qre.strata_moe_combine_norm(qre.combine_norm(n, 2), parts, None, x, T, None, None, None, None, *want)
+        qre.strata_moe_combine_norm(qre.combine_norm(n, 2, part_stride=n, token_stride=5 * n, x_stride=5 * n, out_stride=5 * n,
+                                                     next_stride=5 * n), buf, None, cols[2].data_ptr(), T, None, None, None, None,
+                                    cols[3].data_ptr(), cols[4].data_ptr())
+        assert torch.equal(cols[3], want[0]) and torch.equal(cols[4], want[1])
+        assert torch.equal(buf[:, :2 * n], parts) and torch.equal(cols[2], x)
+        # a result in the gap between a token's two parts
+        buf, (p0, gap, p1) = halves(15, count=3)
+        parts = torch.cat([p0, p1], 1)
+        qre.strata_moe_combine_norm(qre.combine_norm(n, 2), parts, None, None, T, None, None, None, None, want[0], None)
+        qre.strata_moe_combine_norm(qre.combine_norm(n, 2, part_stride=2 * n, token_stride=3 * n, out_stride=3 * n), buf, None,
+                                    None, T, None, None, None, None, gap.data_ptr(), None)
+        assert torch.equal(gap, want[0]) and torch.equal(torch.cat([p0, p1], 1), parts)

@@ -184,3 +184,31 @@ def test_binding_raises_with_the_status():
         qre.strata_moe_combine_norm(qre.combine_norm(n_part=0), X, None, Y, 1, None, None, None, None, Z, V, stream=0)
     with pytest.raises(qre.StrataError):
         qre.strata_moe_adapters(qre.adapters(A, A, 1, 4), A, A, 1, X, 1, Y, Z, A, ws_bytes=1 << 40, stream=0)
+
+
+def test_rows_that_meet_are_refused_whatever_their_strides(lib):
+    """Rows that share an element, of operands whose rows lie between each other's."""
+    n, T, s = 64, 9, 4 * 160  # rows of 64 fp32, 160 apart
+
+    def norm(x, out, xs=160, os=160, xt=qre.F32, ot=qre.F32, T=T):
+        return lib.strata_moe_norm(ctypes.byref(qre.norm(n, x_type=xt, out_type=ot, x_stride=xs, out_stride=os)), x, T, None, out, None)
+
+    for shift in (4, 4 * 63, s - 4 * 63, s + 4 * 63, 8 * s, 8 * s - 4 * 63, 8 * s + 4 * 63):
+        assert norm(X, X + shift) == INVAL and norm(X + shift, X) == INVAL, shift
+    # the rows of one meet those of the other once, at the last row, by their strides
+    assert norm(X, X + 256, os=161 - 8) == INVAL and norm(X + 256, X, xs=161 - 8) == INVAL
+    assert norm(X, X + 2 * 512, xs=512, os=96, T=200) == INVAL
+    # bytes count, not elements
+    assert norm(X, X + 128, ot=qre.BF16, os=320) == INVAL
+    # one of the parts, in the middle of a token's
+    d = qre.combine_norm(n, 3, part_stride=160, token_stride=640, out_stride=640, next_stride=640)
+    for at in (0, 160, 320, 640 * 8 + 320, 97, 383):
+        assert lib.strata_moe_combine_norm(ctypes.byref(d), X, None, None, T, None, None, None, None, X + 4 * at, None, None) == INVAL, at
+        assert lib.strata_moe_combine_norm(ctypes.byref(d), X, None, None, T, None, None, None, None, None, X + 4 * at, None) == INVAL, at
+    need = qre.strata_moe_workspace_bytes(T)
+    a = qre.adapters(A, A, 4, 16, n, n, x_stride=160, y_stride=160, base_stride=160)
+    for shift in (32, 4 * 56, s - 4 * 56, 8 * s + 32):
+        assert lib.strata_moe_adapters(ctypes.byref(a), A, A, 2, X, T, None, X + shift, A, need, None) == INVAL, shift
+        assert lib.strata_moe_adapters(ctypes.byref(a), A, A, 2, Y, T, X, X + shift, A, need, None) == INVAL, shift
+    sel = qre.select(n, 10, logits_stride=160)
+    assert lib.strata_moe_select(ctypes.byref(sel), X, 40, None, X + 4 * 64, Z, None) == INVAL
