@@ -91,7 +91,9 @@ typedef struct strata_norm {
 /* out[t] = x[t] / sqrt(mean(x[t]^2) + eps) * gain.  gain fp32 [n] or NULL (1).  out may be x itself (same address,
  * type and stride); other overlaps are refused.  Rows need only be aligned to their elements; calls whose rows all
  * start on boundaries of four elements and are a multiple of four wide are the fastest.  The squares and their sum are
- * fp32: a row whose sum of squares is beyond its range gives zeros. */
+ * fp32: a row whose sum of squares is beyond its range gives zeros, and the squares of numbers under 2^-63 lose bits or
+ * count as 0, which only an eps near 0 shows.  With eps 0 a row without a square above 0 is divided by 0: infinities, and NaN where an element
+ * is 0 (a row of zeros; a token whose parts all have weight 0, at the norm of the block's output). */
 strata_status strata_moe_norm(const strata_norm_t* nd, const void* x, int32_t T, const float* gain, void* out,
                               void* stream);
 
@@ -127,8 +129,8 @@ typedef struct strata_combine_norm {
  * part_weights fp32 [T][n_part]; x, post_gain, channel_gate fp32 [n], token_gate fp32 [T] and pre_gain may be
  * NULL (no residual; factors of 1); out or next may be NULL, not both.  A post_gain without STRATA_POST_NORM, a
  * pre_gain without next or STRATA_TOKEN_SIGMOID without a token_gate is refused.
- * out or next may be x itself (same address, type and stride); other overlaps are refused.  Alignment as for
- * strata_moe_norm. */
+ * out or next may be x itself (same address, type and stride); other overlaps are refused.  Alignment and
+ * the range of both norms as for strata_moe_norm. */
 strata_status strata_moe_combine_norm(const strata_combine_norm_t* cn, const void* parts, const float* part_weights,
                                       const void* x, int32_t T, const float* post_gain, const float* channel_gate,
                                       const float* token_gate, const float* pre_gain, void* out, void* next,

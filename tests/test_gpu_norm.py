@@ -253,3 +253,29 @@ def test_column_ranges_of_one_buffer():
         qre.strata_moe_combine_norm(qre.combine_norm(n, 2, part_stride=2 * n, token_stride=3 * n, out_stride=3 * n), buf, None,
                                     None, T, None, None, None, None, gap.data_ptr(), None)
         assert torch.equal(gap, want[0]) and torch.equal(torch.cat([p0, p1], 1), parts)
+
+
+def test_rows_without_a_mean_square_at_eps_0():
+    """eps 0: a row of zeros, or whose squares vanish in fp32, is divided by 0; the rows beside it are not touched by that."""
+    for n in (2560, 2559, 64):
+        x = torch.randn(6, n, generator=torch.Generator().manual_seed(12))
+        x[1] = 0.0
+        x[3] = 1e-30 * torch.sign(x[3])
+        x[3, ::2] = 0.0
+        x[5] = 1e-12 * x[5]
+        x = x.to(DEV)
+        out, nxt = torch.empty_like(x), torch.empty_like(x)
+        qre.strata_moe_norm(qre.norm(n, 0.0), x, 6, None, out)
+        for P in (1, 2):  # the norm of the block's output is the same one; a token whose parts are all masked is a row of zeros
+            parts = torch.zeros(6, P, n, device=DEV)
+            parts[:, 0] = x
+            pw = torch.zeros(6, P, device=DEV)
+            pw[[0, 3, 5], 0] = 1.0
+            qre.strata_moe_combine_norm(qre.combine_norm(n, P, eps=0.0), parts, pw, None, 6, None, None, None, None, nxt, None)
+            torch.cuda.synchronize()
+            assert nxt[[1, 2, 4]].isnan().all()
+            for v in ((out, nxt) if P == 1 else (nxt,)):
+                assert v[1].isnan().all() and v[3, ::2].isnan().all()
+                assert torch.equal(v[3, 1::2], torch.sign(x[3, 1::2]) * np.inf)
+                want, err = ref.rms_norm(ref.to64(x[[0, 5]]), np.zeros((2, n)), 0.0, None)
+                ref.check(v[[0, 5]], want, err, qre.F32, "norm")
