@@ -848,10 +848,12 @@ int tiles_of(const AdapterArgs& a, int height) {
 }
 
 // Clusters of `split` CTAs that the device holds at a time (a cluster lies within a part of it, so not all of two CTAs an SM).
+// The split decides the order of the sums, so this goes by all that cfg depends on: the kernel, the split and the rank.
 template <int NT, int H, int TERMS, bool WIDE>
-int resident_clusters(cudaLaunchConfig_t cfg, int split) {
-  static std::atomic<int> known[SPLIT_MAX + 1];
-  int n = known[split].load(std::memory_order_relaxed);
+int resident_clusters(cudaLaunchConfig_t cfg, int split, int rank) {
+  static std::atomic<int> known[SPLIT_MAX + 1][STRATA_ADAPTER_RANK_MAX / 8 + 1];
+  std::atomic<int>& k = known[split][rank / 8];
+  int n = k.load(std::memory_order_relaxed);
   if (n) return n;
   cfg.gridDim = dim3(split, 1);
   cfg.attrs[1].val.clusterDim.x = split;
@@ -859,7 +861,7 @@ int resident_clusters(cudaLaunchConfig_t cfg, int split) {
     cudaGetLastError();
     n = 1;
   }
-  known[split].store(n, std::memory_order_relaxed);
+  k.store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -884,7 +886,7 @@ cudaError_t launch_short_v(AdapterArgs a, cudaStream_t s) {
   const int m = a.n_seg < a.T ? a.n_seg : a.T, half = a.T / (8 * H) + m / 2, tiles = half > m ? half : m;
   const int most = ((a.d_in > a.d_out ? a.d_in : a.d_out) + 32 * AD_WARPS - 1) / (32 * AD_WARPS);
   a.split = 1;
-  while (a.split < SPLIT_MAX && a.split < most && tiles + tiles / 32 <= resident_clusters<NT, H, TERMS, WIDE>(cfg, a.split + 1))
+  while (a.split < SPLIT_MAX && a.split < most && tiles + tiles / 32 <= resident_clusters<NT, H, TERMS, WIDE>(cfg, a.split + 1, a.rank))
     ++a.split;
   a.k_slice = ((a.d_in + 31) / 32 + a.split - 1) / a.split * 32;
   cfg.gridDim = dim3(a.split, tiles_of(a, 8 * H));

@@ -669,7 +669,10 @@ __global__ void __launch_bounds__(512, V <= 8 ? 2 : 1) edge_columns_kernel(const
 template <int XT, int PT, int V, int RING>
 cudaError_t launch_columns_v(const NormArgs& a, cudaStream_t s) {
   const int threads = ((a.n + V - 1) / V + 31) / 32 * 32;
-  const int size = XT == STRATA_F32 || PT == STRATA_F32 ? 4 : 2, slot = (a.n * size + 15) / 16 * 16 + 16;
+  // a slot: all of the threads' columns and the 15 bytes that a row may start behind a piece, 16 a warp (so that shared memory
+  // goes with the number of threads alone, as resident_ctas has it)
+  constexpr int SIZE = XT == STRATA_F32 || PT == STRATA_F32 ? 4 : 2;
+  const int slot = threads / 32 * (32 * V * SIZE + 16);
   const cudaError_t err = allow_smem<edge_columns_kernel<XT, PT, V, RING>>(224 * 1024);
   if (err != cudaSuccess) return err;
   const int rows = rows_a_cta(a, threads), ctas = (a.T + rows - 1) / rows, smem = rows * RING * slot;

@@ -450,3 +450,37 @@ def test_column_ranges_of_one_buffer(T, rank):
 
 def test_column_ranges_of_one_buffer_in_tiles_of_128():
     check_column_ranges(2500, 128)
+
+
+FIRST_RANK = """
+import hashlib, sys, torch, quantized_routed_expert_top10_gb300 as qre
+out = {}
+for rank in map(int, sys.argv[1:]):
+    for lens in ([9] * 20, [40] * 5, [100] * 40):
+        T, n = sum(lens), 1032
+        g = torch.Generator("cuda").manual_seed(rank)
+        a, b = (torch.randn(5, rank, n, generator=g, device="cuda").bfloat16() for _ in range(2))
+        x = torch.randn(T, n, generator=g, device="cuda")
+        off = torch.tensor([0] + lens, device="cuda").cumsum(0).int()
+        of = (torch.arange(len(lens), device="cuda") % 5).int()
+        ws = torch.empty(qre.strata_moe_workspace_bytes(T), dtype=torch.uint8, device="cuda")
+        qre.strata_moe_workspace_init(ws)
+        y = torch.empty(T, n, device="cuda")
+        qre.strata_moe_adapters(qre.adapters(a, b, 5, rank, n, n), off, of, len(lens), x, T, None, y, ws)
+        assert qre.strata_poll_status(ws) == 0
+        out[rank, T] = hashlib.sha256(y.cpu().numpy().tobytes()).hexdigest()
+print(sorted(out.items()))
+"""
+
+
+def test_the_rank_of_a_process_first_call_changes_no_bits():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    got = set()
+    for ranks in (("40", "128", "64"), ("128", "64", "40")):
+        r = subprocess.run([sys.executable, "-c", FIRST_RANK, *ranks], cwd=root, capture_output=True, text=True, timeout=300)
+        assert r.returncode == 0, r.stdout + r.stderr
+        got.add(r.stdout)
+    assert len(got) == 1 and "(40, 180)" in got.pop()
