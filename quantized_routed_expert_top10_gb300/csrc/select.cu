@@ -613,7 +613,9 @@ __global__ void __launch_bounds__(32 * SEL_WARPS, SEL_CTAS) select_kernel(const 
     float p = 0.f;
     if (has && cand_key(me) > MASKED) {
       const float x = fminf(load1(a.logits, row - lane + cand_id(me), a.type), FLT_MAX);
-      p = a.softmax ? expf(x - m) * inv_z : __fdividef(1.f, 1.f + expf(-x));
+      const float e = expf(a.softmax ? x - m : -fabsf(x));
+      // (the exponential of -|x|: that of a far negative logit's -x leaves fp32, and the score is then 0 too early)
+      p = a.softmax ? e * inv_z : __fdividef(x < 0.f ? e : 1.f, 1.f + e);
     }
     const float sum = a.renorm ? fmaxf(warp_sum(p), SUM_MIN) : 1.f;
     if (has) {

@@ -252,3 +252,16 @@ def test_ties_at_the_end_of_the_choice_hide_no_near_value(ties):
         bias[e[ties]] = np.float32(p[e[0]] - p[e[ties]])
         for k in range(1, ties + 1):
             run(torch.from_numpy(row[None]), qre.F32, torch.from_numpy(bias), k, SOFT)
+
+
+def test_far_negative_sigmoids_keep_their_weights():
+    """Scores down to the subnormal numbers, which the clamp of the sum raises by 2^14.  (Half a step of a subnormal, 2^-150, times that
+    and the scale is inside run()'s 2^-126.)"""
+    l = torch.linspace(-105, -60, 4 * 64).view(4, 64)
+    for bias in (None, randn(64, seed=24, std=0.1)):
+        for renorm in (True, False):
+            for groups in (1, 8):
+                G, keep, gsum = GROUPS[groups]
+                run(l, qre.F32, bias, 10, SIG, n_group=G, top_group=keep, group_sum=gsum, renorm=renorm, scale=2.5)
+    _, w = run(torch.full((2, 32), -87.5), qre.F32, None, 4, SIG)
+    assert (w > 0).all()
