@@ -21,7 +21,8 @@
  * buffer do, are fine.
  *
  * Element types (the framework's own activations are fp32): arithmetic is in 32 bits or more whatever the
- * type, and a result is rounded once, when it is stored. */
+ * type, and a result is rounded once, when it is stored.  One value between is held in fewer: the adapters' A_a x has 16
+ * bits where y is of a 16-bit type (strata_moe_adapters says so again). */
 #ifndef STRATA_MOE_OPS_H_
 #define STRATA_MOE_OPS_H_
 

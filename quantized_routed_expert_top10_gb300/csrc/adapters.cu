@@ -7,9 +7,9 @@
 // Segments of few tokens, or few tokens times ranks in all, go by one kernel: tiles of 8, 16 or 32 tokens of one segment, a cluster
 // a tile, warp-level MMAs.  It is bound by the latency of its chain (segments, A and x, the cluster's sum, B and base), which is
 // why everything that a CTA reads is asked for as early as its registers allow: one token 4.3 us, 64 tokens of 64 adapters
-// (10.5 MB of them) 5.8 us; 2,048 ragged fp32 tokens, rank 32, 16 us (4.1 TB/s).  The rest go by two kernels in tiles of 128 tokens on
+// (10.5 MB of them) 5.8 us; 2,048 ragged fp32 tokens, rank 32, 19.6 us (3.4 TB/s; 16 us where all of its 66 MB are in L2).  The rest go by two kernels in tiles of 128 tokens on
 // the 5th-generation tensor cores, shrink (v = A_a x) and expand (base + B_a (scale v)): 8,192 tokens of 32 adapters of
-// rank 64, 2,560 -> 2,560, bf16, 46.6 us (3.2 TB/s), about 18 and 28, bound by their own latencies at two to three CTAs an SM.
+// rank 64, 2,560 -> 2,560, bf16, 46.7 us (3.1 TB/s), about 18 and 28, one after the other and each below half of the memory's pace.
 #include "device_common.cuh"
 #include "elements.cuh"
 #include "tc_common.cuh"
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(AD_THREADS, 2) short_kernel(AdapterArgs a) {
 
 // ---- Tiles of up to 128 tokens on the 5th-generation tensor cores -----------------------------------------
 // Operands are copied 16 bytes a thread into the tensor cores' K-major shared-memory layout (cp.async; an fp16 or fp32 x
-// by registers, which split it into its bf16 terms), so one kernel serves any row stride.  The shrink kernel allocates TMEM after
+// by registers, which split it into its bf16 terms); tensor maps, which the strides would allow, were not tried.  The shrink kernel allocates TMEM after
 // griddep_wait and lets the expand kernel start only then; so an expand CTA, which allocates before its wait, waits for
 // CTAs that have what they need.
 constexpr int TC_ROWS = 128;
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(AD_THREADS + 32, 2) expand_tc_kernel(AdapterAr
   // their own wait for what came before them.
   const Segments g = cut_segments<AD_THREADS + 32>(a, TC_ROWS);
   const int col_blocks = (a.d_out + CW - 1) / CW;
-  const int units = g.total * col_blocks;  // at most 2 * 8,192 tiles of 128
+  const int units = g.total * col_blocks;  // far inside 32 bits: a few hundred tiles of 128
   const int u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
   int u = (int)((int64_t)units * blockIdx.x / gridDim.x);
   if (u >= u1) {
@@ -987,9 +987,10 @@ cudaError_t launch_adapters(const strata_adapters_t& ad, const int32_t* seg_off,
   a.seg_off = seg_off; a.seg_adapter = seg_adapter; a.n_seg = n_seg; a.n_adapter = ad.n_adapter;
   a.x = x; a.base = base; a.y = y; a.v = v_terms; a.status = status;
   a.rank = ad.rank; a.d_in = ad.d_in; a.d_out = ad.d_out; a.T = T; a.x_type = ad.x_type; a.y_type = ad.y_type;
-  // The 128-row kernels cost a call more and a token's rank less than warp-level MMAs.  2,560 -> 2,560, bf16, in us, here and
-  // there: rank 32, 8,192 tokens 40 and 46; rank 64, 4,096 tokens 31 and 32, 8,192 tokens 59 and 50; rank 128, 2,048 tokens
-  // in 32 segments 29 and 38, in 64 57 and 45.  x or y fp32: rank 64, 8,192 tokens 70 to 85 and 85 to 105; rank 128, 2,048 tokens in 32 43 and 56.
+  // The 128-row kernels cost a call more and a token's rank less than warp-level MMAs.  (Measured at 2,560 -> 2,560 only: other
+  // widths take the same rule.)  bf16, in us, short and 128-row: rank 32, 8,192 tokens 40 and 46; rank 64, 4,096 tokens 31 and
+  // 32, 8,192 tokens 59 and 50; rank 128, 2,048 tokens in 32 segments 29 and 38, in 64 57 and 45.  x or y fp32: rank 64, 8,192
+  // tokens 70 to 85 and 85 to 105; rank 128, 2,048 tokens in 32 43 and 56.
   const int filled = n_seg < T ? n_seg : T;
   const bool half = T / 16 + filled / 2 <= 152;  // tiles of 16 tokens, two CTAs each, all at once (a last tile half full)
   const bool wide = a.x_type == STRATA_F32 || a.y_type == STRATA_F32;

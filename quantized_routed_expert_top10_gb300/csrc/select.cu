@@ -5,10 +5,12 @@
 // experts, stable descending order, gather, renormalise with a lower clamp.
 //
 // A token is one warp's work: its logits in the warp's registers, 16 a lane for 512 experts, the choice by lane maxima and the
-// few candidates not below the k-th of them.  It is bound by instructions (about 1,500 a token with groups and a bias, issued
-// in 54% of cycles) and, in calls of a few thousand tokens, by the last warp that needs a 64-bit pass; memory is at 7%.
-// 512 experts, top-10: one token 2.5 us, 8,192 tokens with sigmoid scores, a bias and 4 of 16 groups 20.4 us (of which 64-bit
-// passes 3.4).  Seven CTAs an SM: 24.4 us before the passes were shortened; five 24.5, eight (64 registers) 26.8.
+// few candidates not below the k-th of them.  It is bound by the chain of a token (about 1,500 instructions with groups and a
+// bias, issued in 54% of cycles by the 28 warps that an SM holds; two turns at 8,192 tokens, each with its own loads) and by the
+// last warp that needs a 64-bit pass; memory is at 7%.
+// 512 experts, top-10: one token 2.5 us, 8,192 tokens with sigmoid scores, a bias and 4 of 16 groups 20.3 us (of which 64-bit
+// passes 3.4); without groups 16.4, a softmax with a bias 31, a softmax alone 9.4.  Seven CTAs an SM: 24.4 us before the passes
+// were shortened; five 24.5, eight (64 registers) 26.8.
 #include <cfloat>
 
 #include "device_common.cuh"
