@@ -11,6 +11,10 @@
  *                            experts, top-k, renormalised and scaled weights
  *   strata_moe_combine_norm  the weighted sum of the experts' outputs, the norm after the block, its gates,
  *                            the scaled residual and the next block's norm in one pass
+ *   strata_moe_linear        a projection of a few tokens by 4-bit weights with group scales, or by bf16 weights
+ *                            (the router's logits, of any width)
+ *   strata_moe_q4_experts    the routed experts of a few tokens, of any shape, with 4-bit weights: gate, up, SwiGLU,
+ *                            down and the weighted sum
  *
  * The conventions of strata_moe.h hold: device pointers owned by the caller, work only enqueued on
  * `stream` (of the current device), host-checkable errors returned before anything is enqueued, T == 0 a
@@ -175,6 +179,103 @@ typedef struct strata_adapters {
 strata_status strata_moe_adapters(const strata_adapters_t* ad, const int32_t* seg_off, const int32_t* seg_adapter,
                                   int32_t n_seg, const void* x, int32_t T, const void* base, void* y, void* ws,
                                   size_t ws_bytes, void* stream);
+
+/* ---- 4-bit weights with group scales ---------------------------------------------------------------- */
+#define STRATA_Q4_ROWS_MAX 1048576
+#define STRATA_Q4_COLUMNS_MAX 32768
+
+/* The format of a 4-bit matrix w [n_out][d_in]: w[n][k] = scale[n][k / group] * (code[n][k] - zero[n][k / group]), codes and zero
+ * points in 0 .. 15, zero points of 8 where the matrix has none.  As it comes (dense, row-major):
+ *   codes  uint8 [n_out][d_in / 2], column 2i in bits 0-3 and column 2i + 1 in bits 4-7 of byte i
+ *   scales bf16 or fp16 [n_out][d_in / group]
+ *   zeros  uint8 [n_out][d_in / group], one to a byte (its low four bits count), or none
+ * Packed, as the kernels read it: slabs of 16 rows one after the other (a last slab of fewer rows is filled up with zeros), a slab
+ * in chunks of 128 columns (the last may hold 32, 64 or 96), a chunk of nb blocks of 32 columns as
+ *   codes   [2 halves][32 lanes][nb blocks] 32-bit words: lane 4g + c holds row g (half 0) or g + 8 (half 1), columns 8c .. 8c + 7
+ *           of the block, column 2j of them in bits 4j .. 4j + 3 and column 2j + 1 in bits 16 + 4j .. 19 + 4j
+ *   scales  [8 g][128 / group]{row g, row g + 8}
+ *   zeros   [8 g][128 / group]{row g, row g + 8}, bytes, each g padded to 4 of them; only with zeros
+ * A paired matrix is gate and up of an expert at once: its rows are d_ff rows of gate, then d_ff of up, and a slab holds rows
+ * 8s .. 8s + 7 of gate and the same rows of up. */
+typedef struct strata_q4 {
+  int32_t n_out;      /* rows, in [1, 1048576]; paired: 2 * d_ff, a multiple of 16 */
+  int32_t d_in;       /* columns, a multiple of group in [group, 32768] */
+  int32_t group;      /* 32, 64 or 128 */
+  int32_t scale_type; /* STRATA_BF16 or STRATA_F16 */
+  int32_t zeros;      /* 1: with zero points; 0: all are 8 */
+  int32_t paired;     /* 1: gate and up of an expert */
+} strata_q4_t;
+
+/* Bytes of one packed matrix (a multiple of 32); 0 if the format is none of the above. */
+size_t strata_q4_bytes(const strata_q4_t* q);
+
+/* Packs n_matrix matrices of one format that follow one another in codes, scales and zeros (NULL without zero points, and
+ * only then) into packed (strata_q4_bytes each).  strata_pack_q4: host arrays.  strata_pack_q4_device: device arrays, packed on a 16-byte
+ * boundary, n_matrix in [0, 65536]; it only enqueues. */
+strata_status strata_pack_q4(const strata_q4_t* q, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, void* packed,
+                             int64_t n_matrix);
+strata_status strata_pack_q4_device(const strata_q4_t* q, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros,
+                                    void* packed, int64_t n_matrix, void* stream);
+
+/* ---- Projections of a few tokens --------------------------------------------------------------------- */
+#define STRATA_W_Q4 0
+#define STRATA_W_BF16 1
+
+typedef struct strata_linear {
+  const void* w;     /* device: a packed matrix (STRATA_W_Q4), or bf16 rows of d_in elements (STRATA_W_BF16); 16-byte boundary */
+  int64_t w_stride;  /* STRATA_W_BF16: elements between rows, a multiple of 8, >= d_in; STRATA_W_Q4: 0 */
+  strata_q4_t q4;    /* the matrix's format, not paired; STRATA_W_BF16: n_out and d_in alone (d_in a multiple of 8 in [8, 32768]), the rest 0 */
+  int32_t weight;    /* STRATA_W_Q4 or STRATA_W_BF16 */
+  int32_t x_type;    /* element types */
+  int32_t y_type;
+  int32_t reserved;  /* 0 */
+  int64_t x_stride;  /* elements between tokens, a multiple of 8, >= d_in */
+  int64_t y_stride;  /* elements between tokens, >= n_out */
+} strata_linear_t;
+
+/* y[t][n] = sum over k of w[n][k] * x[t][k] + bias[n].  bias fp32 [n_out] or NULL.  x on a 16-byte boundary, y aligned to its elements;
+ * y must not overlap x.  No workspace.  x enters as bf16 terms that add up to it (three for fp32, two for fp16), the products are
+ * exact and their sums fp32.  A token whose x holds a NaN, an infinity or a number that rounds to bf16's infinity may give NaN in its
+ * whole row; other tokens' rows do not change.
+ * Built for few tokens: the weights are read once for up to 24 (bf16), 12 (fp16) or 8 (fp32) of them, and the time of more grows in
+ * proportion. */
+strata_status strata_moe_linear(const strata_linear_t* li, const void* x, int32_t T, const float* bias, void* y, void* stream);
+
+/* ---- Routed experts of a few tokens -------------------------------------------------------------------- */
+#define STRATA_Q4_EXPERTS_T_MAX 64
+#define STRATA_Q4_EXPERTS_DIM_MAX 8192
+#define STRATA_Q4_EXPERTS_E_MAX 1024
+#define STRATA_Q4_EXPERTS_K_MAX 32
+
+typedef struct strata_q4_experts {
+  const void* gate_up;     /* device: expert e's packed gate and up (paired) at gate_up + e * gate_up_stride; 16-byte boundary */
+  const void* down;        /* device: expert e's packed down at down + e * down_stride; 16-byte boundary */
+  int64_t gate_up_stride;  /* bytes, multiples of 16, at least the packed matrix */
+  int64_t down_stride;
+  strata_q4_t gate_up_q4;  /* n_out = 2 * d_ff, d_in = d_model, paired */
+  strata_q4_t down_q4;     /* n_out = d_model, d_in = d_ff; d_model and d_ff at most 8192 */
+  int32_t n_expert;        /* in [1, 1024] */
+  int32_t top_k;           /* experts of a token, in [1, 32] */
+  int32_t x_type;          /* element types */
+  int32_t out_type;
+  int64_t x_stride;        /* elements between tokens, multiples of 8, >= d_model */
+  int64_t out_stride;
+} strata_q4_experts_t;
+
+/* Bytes of a workspace for T tokens; 0 if the descriptor or T is refused.  It holds strata_moe_workspace_init's words at its start and
+ * may be any call's workspace that is large enough for each. */
+size_t strata_moe_q4_experts_workspace_bytes(const strata_q4_experts_t* ex, int32_t T);
+
+/* out[t] = sum over i of weights[t][i] * D_e (silu(G_e x[t]) * (U_e x[t])), e = ids[t][i], in the order of i, silu(z) = z / (1 + exp(-z)).
+ * ids int32 [T][top_k], weights fp32 [T][top_k] (strata_moe_select's).  A slot with an id of -1 or a weight of 0 has no expert:
+ * nothing of it is read; a token without any gets zeros.  An expert may stand twice in a token's list.  A shared expert is one more expert that every
+ * token lists.  T in [0, 64].  x and out on 16-byte boundaries; out must not overlap x.
+ * Products are exact and summed in fp32 as in strata_moe_linear; the hidden values of an expert are held in fp32 and enter the
+ * second product as three bf16 terms for an fp32 out, two (16 bits) otherwise.  NaN and infinities as there.
+ * An id outside [-1, n_expert) sets STRATA_E_CORRUPT in the workspace's status word and the call computes nothing (out keeps its contents).
+ * Calls that share a workspace must not overlap in time. */
+strata_status strata_moe_q4_experts(const strata_q4_experts_t* ex, const int32_t* ids, const float* weights, const void* x, int32_t T,
+                                    void* out, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -48,7 +48,9 @@ EXPORTS = (
 )
 
 # Every symbol include/strata_moe_ops.h declares.
-OPS_EXPORTS = ("strata_moe_select", "strata_moe_norm", "strata_moe_combine_norm", "strata_moe_adapters")
+OPS_EXPORTS = ("strata_moe_select", "strata_moe_norm", "strata_moe_combine_norm", "strata_moe_adapters", "strata_q4_bytes",
+               "strata_pack_q4", "strata_pack_q4_device", "strata_moe_linear", "strata_moe_q4_experts_workspace_bytes",
+               "strata_moe_q4_experts")
 
 # element types, routing scores and flags of include/strata_moe_ops.h
 F32, BF16, F16 = 0, 1, 2
@@ -61,6 +63,13 @@ NORM_PART_MAX = 32
 ADAPTER_RANK_MAX = 128
 ADAPTER_DIM_MAX = 16384
 ADAPTER_COUNT_MAX = 65536
+W_Q4, W_BF16 = 0, 1
+Q4_ROWS_MAX = 1048576
+Q4_COLUMNS_MAX = 32768
+Q4_EXPERTS_T_MAX = 64
+Q4_EXPERTS_DIM_MAX = 8192
+Q4_EXPERTS_E_MAX = 1024
+Q4_EXPERTS_K_MAX = 32
 
 
 class StrataError(RuntimeError):
@@ -100,6 +109,24 @@ class strata_adapters_t(ctypes.Structure):
                 ("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32), ("x_type", ctypes.c_int32),
                 ("y_type", ctypes.c_int32), ("x_stride", ctypes.c_int64), ("base_stride", ctypes.c_int64),
                 ("y_stride", ctypes.c_int64)]
+
+
+class strata_q4_t(ctypes.Structure):
+    _fields_ = [("n_out", ctypes.c_int32), ("d_in", ctypes.c_int32), ("group", ctypes.c_int32), ("scale_type", ctypes.c_int32),
+                ("zeros", ctypes.c_int32), ("paired", ctypes.c_int32)]
+
+
+class strata_linear_t(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("w_stride", ctypes.c_int64), ("q4", strata_q4_t), ("weight", ctypes.c_int32),
+                ("x_type", ctypes.c_int32), ("y_type", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64)]
+
+
+class strata_q4_experts_t(ctypes.Structure):
+    _fields_ = [("gate_up", ctypes.c_void_p), ("down", ctypes.c_void_p), ("gate_up_stride", ctypes.c_int64),
+                ("down_stride", ctypes.c_int64), ("gate_up_q4", strata_q4_t), ("down_q4", strata_q4_t),
+                ("n_expert", ctypes.c_int32), ("top_k", ctypes.c_int32), ("x_type", ctypes.c_int32),
+                ("out_type", ctypes.c_int32), ("x_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -151,6 +178,13 @@ def lib():
                                                        _vp, _vp, _vp, _vp, _vp, _vp]),
             "strata_moe_adapters": (ctypes.c_int, [ctypes.POINTER(strata_adapters_t), _vp, _vp, _i32, _vp, _i32, _vp,
                                                    _vp, _vp, _sz, _vp]),
+            "strata_q4_bytes": (_sz, [ctypes.POINTER(strata_q4_t)]),
+            "strata_pack_q4": (ctypes.c_int, [ctypes.POINTER(strata_q4_t), _vp, _vp, _vp, _vp, _i64]),
+            "strata_pack_q4_device": (ctypes.c_int, [ctypes.POINTER(strata_q4_t), _vp, _vp, _vp, _vp, _i64, _vp]),
+            "strata_moe_linear": (ctypes.c_int, [ctypes.POINTER(strata_linear_t), _vp, _i32, _vp, _vp, _vp]),
+            "strata_moe_q4_experts_workspace_bytes": (_sz, [ctypes.POINTER(strata_q4_experts_t), _i32]),
+            "strata_moe_q4_experts": (ctypes.c_int, [ctypes.POINTER(strata_q4_experts_t), _vp, _vp, _vp, _i32, _vp, _vp, _sz,
+                                                     _vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -365,6 +399,62 @@ def strata_moe_adapters(ad, seg_off, seg_adapter, n_seg, x, T, base, y, ws, ws_b
                                                             _s(stream)))
 
 
+def q4(n_out: int, d_in: int, group: int, zeros: bool = False, scale_type: int = BF16, paired: bool = False) -> strata_q4_t:
+    """A strata_q4_t: a 4-bit matrix of n_out rows and d_in columns; paired: gate and up of an expert (n_out = 2 d_ff)."""
+    return strata_q4_t(n_out, d_in, group, scale_type, int(zeros), int(paired))
+
+
+def strata_q4_bytes(q) -> int:
+    """Bytes of one packed matrix; 0: not a format."""
+    return lib().strata_q4_bytes(ctypes.byref(q))
+
+
+def strata_pack_q4(q, codes, scales, zeros, packed, n_matrix=1):
+    """Pack matrices in host memory (numpy arrays, CPU tensors)."""
+    _check("strata_pack_q4", lib().strata_pack_q4(ctypes.byref(q), _p(codes), _p(scales), _p(zeros), _p(packed), n_matrix))
+
+
+def strata_pack_q4_device(q, codes, scales, zeros, packed, n_matrix=1, stream=None):
+    _check("strata_pack_q4_device", lib().strata_pack_q4_device(ctypes.byref(q), _p(codes), _p(scales), _p(zeros), _p(packed),
+                                                                n_matrix, _s(stream)))
+
+
+def linear_q4(q, packed, x_type: int = F32, y_type: int = F32, x_stride=None, y_stride=None) -> strata_linear_t:
+    """A strata_linear_t for a packed 4-bit matrix (tensor or address; the caller keeps it alive); strides None: dense."""
+    return strata_linear_t(_p(packed), 0, q, W_Q4, x_type, y_type, 0, q.d_in if x_stride is None else x_stride,
+                           q.n_out if y_stride is None else y_stride)
+
+
+def linear_bf16(w, n_out: int, d_in: int, x_type: int = F32, y_type: int = F32, w_stride=None, x_stride=None,
+                y_stride=None) -> strata_linear_t:
+    """A strata_linear_t for bf16 rows w [n_out][d_in] (tensor or address; the caller keeps it alive); strides None: dense."""
+    return strata_linear_t(_p(w), d_in if w_stride is None else w_stride, strata_q4_t(n_out, d_in, 0, 0, 0, 0), W_BF16, x_type,
+                           y_type, 0, d_in if x_stride is None else x_stride, n_out if y_stride is None else y_stride)
+
+
+def q4_experts(gate_up_q4, gate_up, down_q4, down, n_expert: int, top_k: int = K, x_type: int = F32, out_type: int = F32,
+               gate_up_stride=None, down_stride=None, x_stride=None, out_stride=None) -> strata_q4_experts_t:
+    """A strata_q4_experts_t for packed matrices of n_expert experts (tensors or addresses; the caller keeps them alive);
+    strides None: one expert after the other, dense rows."""
+    return strata_q4_experts_t(_p(gate_up), _p(down), strata_q4_bytes(gate_up_q4) if gate_up_stride is None else gate_up_stride,
+                               strata_q4_bytes(down_q4) if down_stride is None else down_stride, gate_up_q4, down_q4, n_expert,
+                               top_k, x_type, out_type, gate_up_q4.d_in if x_stride is None else x_stride,
+                               gate_up_q4.d_in if out_stride is None else out_stride)
+
+
+def strata_moe_linear(li, x, T, bias, y, stream=None):
+    _check("strata_moe_linear", lib().strata_moe_linear(ctypes.byref(li), _p(x), T, _p(bias), _p(y), _s(stream)))
+
+
+def strata_moe_q4_experts_workspace_bytes(ex, T: int) -> int:
+    return lib().strata_moe_q4_experts_workspace_bytes(ctypes.byref(ex), T)
+
+
+def strata_moe_q4_experts(ex, ids, weights, x, T, out, ws, ws_bytes=None, stream=None):
+    _check("strata_moe_q4_experts", lib().strata_moe_q4_experts(ctypes.byref(ex), _p(ids), _p(weights), _p(x), T, _p(out), _p(ws),
+                                                                _nbytes(ws, ws_bytes), _s(stream)))
+
+
 def strata_moe_wait_selftest(ws, limit_ns, ws_bytes=None, stream=None):
     """Run the bounded waits on conditions that never hold (see the header); poll the status after."""
     _check("strata_moe_wait_selftest", lib().strata_moe_wait_selftest(_p(ws), _nbytes(ws, ws_bytes), limit_ns,
@@ -412,7 +502,7 @@ def strata_status_str(status: int) -> str:
 KERNELS = ("DECODE_LAYER", "ROUTE_DECODE", "ROUTER_PREP", "ROUTER_TC", "TOP_K", "GROUP_HIST", "GROUP_SCAN",
            "GROUP_SCATTER", "TC_PREPARE", "TC_GATHER",
            "TC_GATEUP", "TC_DOWN", "COMBINE", "PACK", "HOST_COPY", "WAIT_SELFTEST", "BLOB_CRC32", "SELECT", "NORM",
-           "COMBINE_NORM", "ADAPTER_SHRINK", "ADAPTER_EXPAND", "ADAPTERS")
+           "COMBINE_NORM", "ADAPTER_SHRINK", "ADAPTER_EXPAND", "ADAPTERS", "LINEAR", "Q4_GATE_UP", "Q4_DOWN", "Q4_COMBINE", "PACK_Q4")
 KERNEL_ID = {name: i for i, name in enumerate(KERNELS)}
 
 

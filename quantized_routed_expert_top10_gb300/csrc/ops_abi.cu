@@ -2,7 +2,7 @@
 // and the launch of each call.
 #include <cmath>
 
-#include "ops_common.cuh"
+#include "q4_format.cuh"
 
 using namespace strata;
 
@@ -57,6 +57,20 @@ bool partly(const Rows& a, const Rows& b) {
 }
 
 inline strata_status launched(cudaError_t e) { return e == cudaSuccess ? STRATA_OK : STRATA_E_CUDA; }
+
+// The descriptor's own conditions (T, sizes, types and strides), as the workspace's size needs them.
+bool good_experts(const strata_q4_experts_t* ex, int32_t T) {
+  if (!ex || T < 0 || T > STRATA_Q4_EXPERTS_T_MAX) return false;
+  const strata_q4_t &gu = ex->gate_up_q4, &dn = ex->down_q4;
+  if (!q4::valid(gu) || !q4::valid(dn) || !gu.paired || dn.paired) return false;
+  if (gu.n_out != 2 * (int64_t)dn.d_in || gu.d_in != dn.n_out) return false;
+  if (gu.d_in > STRATA_Q4_EXPERTS_DIM_MAX || dn.d_in > STRATA_Q4_EXPERTS_DIM_MAX) return false;
+  if (ex->n_expert < 1 || ex->n_expert > STRATA_Q4_EXPERTS_E_MAX || ex->top_k < 1 || ex->top_k > STRATA_Q4_EXPERTS_K_MAX)
+    return false;
+  if (!known_type(ex->x_type) || !known_type(ex->out_type)) return false;
+  if (!good_stride(ex->gate_up_stride, q4::matrix_bytes(gu)) || !good_stride(ex->down_stride, q4::matrix_bytes(dn))) return false;
+  return good_stride(ex->x_stride, gu.d_in) && good_stride(ex->out_stride, gu.d_in);
+}
 
 }  // namespace
 
@@ -164,6 +178,69 @@ strata_status strata_moe_adapters(const strata_adapters_t* ad, const int32_t* se
   char* w = (char*)ws;
   return launched(launch_adapters(*ad, seg_off, seg_adapter, n_seg, x, T, base, y, (uint16_t*)(w + L.logits),
                                   (int*)(w + L.status), (cudaStream_t)stream));
+}
+
+size_t strata_q4_bytes(const strata_q4_t* q) { return q && q4::valid(*q) ? (size_t)q4::matrix_bytes(*q) : 0; }
+
+strata_status strata_pack_q4(const strata_q4_t* q, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, void* packed,
+                             int64_t n_matrix) {
+  if (!q || !q4::valid(*q) || !codes || !scales || !packed || n_matrix < 0 || (zeros != nullptr) != (q->zeros != 0))
+    return STRATA_E_INVAL;
+  if (!aligned(scales, 2)) return STRATA_E_ALIGN;
+  pack_q4_host(*q, codes, scales, zeros, (uint8_t*)packed, n_matrix);
+  return STRATA_OK;
+}
+
+strata_status strata_pack_q4_device(const strata_q4_t* q, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros,
+                                    void* packed, int64_t n_matrix, void* stream) {
+  if (!q || !q4::valid(*q) || !codes || !scales || !packed || n_matrix < 0 || n_matrix > 65536 ||
+      (zeros != nullptr) != (q->zeros != 0))
+    return STRATA_E_INVAL;
+  if (!aligned(scales, 2) || !aligned(packed, 16)) return STRATA_E_ALIGN;
+  if (n_matrix == 0) return STRATA_OK;
+  return launched(launch_pack_q4(*q, codes, scales, zeros, (uint8_t*)packed, n_matrix, (cudaStream_t)stream));
+}
+
+strata_status strata_moe_linear(const strata_linear_t* li, const void* x, int32_t T, const float* bias, void* y, void* stream) {
+  if (!li || !good_T(T) || !li->w || !x || !y) return STRATA_E_INVAL;
+  const strata_q4_t& q = li->q4;
+  if (li->weight == STRATA_W_Q4) {
+    if (!q4::valid(q) || q.paired || li->w_stride != 0) return STRATA_E_INVAL;
+  } else if (li->weight == STRATA_W_BF16) {
+    if (q.group || q.scale_type || q.zeros || q.paired || q.n_out < 1 || q.n_out > STRATA_Q4_ROWS_MAX) return STRATA_E_INVAL;
+    if (q.d_in < 8 || q.d_in > STRATA_Q4_COLUMNS_MAX || q.d_in % 8 || !good_stride(li->w_stride, q.d_in)) return STRATA_E_INVAL;
+    if (li->w_stride % 8) return STRATA_E_ALIGN;
+  } else {
+    return STRATA_E_INVAL;
+  }
+  if (!known_type(li->x_type) || !known_type(li->y_type) || li->reserved != 0) return STRATA_E_INVAL;
+  if (!good_stride(li->x_stride, q.d_in) || !good_stride(li->y_stride, q.n_out)) return STRATA_E_INVAL;
+  if (li->x_stride % 8 || !aligned(li->w, 16) || !aligned(x, 16) || !aligned(y, type_bytes(li->y_type)) || !aligned(bias, 4))
+    return STRATA_E_ALIGN;
+  if (T == 0) return STRATA_OK;
+  if (overlap(rows_of(x, T, li->x_stride, q.d_in, li->x_type), rows_of(y, T, li->y_stride, q.n_out, li->y_type)))
+    return STRATA_E_INVAL;
+  return launched(launch_linear(*li, x, T, bias, y, (cudaStream_t)stream));
+}
+
+size_t strata_moe_q4_experts_workspace_bytes(const strata_q4_experts_t* ex, int32_t T) {
+  return good_experts(ex, T) ? DX_END + q4_experts_scratch(*ex, T) : 0;
+}
+
+strata_status strata_moe_q4_experts(const strata_q4_experts_t* ex, const int32_t* ids, const float* weights, const void* x, int32_t T,
+                                    void* out, void* ws, size_t ws_bytes, void* stream) {
+  if (!good_experts(ex, T) || !ids || !weights || !x || !out || !ws || !ex->gate_up || !ex->down) return STRATA_E_INVAL;
+  if (!aligned(ex->gate_up, 16) || !aligned(ex->down, 16) || ex->gate_up_stride % 16 || ex->down_stride % 16 ||
+      ex->x_stride % 8 || ex->out_stride % 8 || !aligned(x, 16) || !aligned(out, 16) || !aligned(ids, 4) || !aligned(weights, 4) ||
+      !aligned(ws, 256))
+    return STRATA_E_ALIGN;
+  // the scratch lies behind the words that other calls keep in a workspace from call to call
+  if (ws_bytes < DX_END + q4_experts_scratch(*ex, T)) return STRATA_E_WORKSPACE;
+  if (T == 0) return STRATA_OK;
+  const int d = ex->gate_up_q4.d_in;
+  if (overlap(rows_of(x, T, ex->x_stride, d, ex->x_type), rows_of(out, T, ex->out_stride, d, ex->out_type))) return STRATA_E_INVAL;
+  return launched(launch_q4_experts(*ex, ids, weights, x, T, out, (char*)ws + DX_END, (int*)((char*)ws + WS_STATUS),
+                                    (cudaStream_t)stream));
 }
 
 }  // extern "C"

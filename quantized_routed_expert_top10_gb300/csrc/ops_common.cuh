@@ -9,7 +9,8 @@ namespace strata {
 
 // Continues KernelId.
 enum OpsKernelId : int {
-  KID_SELECT = KID_COUNT, KID_NORM, KID_COMBINE_NORM, KID_ADAPTER_SHRINK, KID_ADAPTER_EXPAND, KID_ADAPTERS, KID_END
+  KID_SELECT = KID_COUNT, KID_NORM, KID_COMBINE_NORM, KID_ADAPTER_SHRINK, KID_ADAPTER_EXPAND, KID_ADAPTERS, KID_LINEAR,
+  KID_Q4_GATE_UP, KID_Q4_DOWN, KID_Q4_COMBINE, KID_PACK_Q4, KID_END
 };
 
 // The dynamic shared memory a kernel may use, raised once per kernel and device.
@@ -39,6 +40,19 @@ int resident_ctas(int threads, size_t smem) {
   return n;
 }
 
+// Multiprocessors of the current device, asked once for each of the first 64.
+inline cudaError_t sm_count(int* sms) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  *sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (*sms) return cudaSuccess;
+  err = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (err == cudaSuccess && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+  return err;
+}
+
 // The operators of strata_moe_ops.h (arguments checked by ops_abi.cu).
 cudaError_t launch_select(const strata_select_t& sel, const void* logits, int T, const float* bias, int32_t* ids,
                           float* weights, cudaStream_t s);
@@ -50,5 +64,11 @@ cudaError_t launch_combine_norm(const strata_combine_norm_t& cn, const void* par
 cudaError_t launch_adapters(const strata_adapters_t& ad, const int32_t* seg_off, const int32_t* seg_adapter, int n_seg,
                             const void* x, int T, const void* base, void* y, uint16_t* v_terms, int* status,
                             cudaStream_t s);
+
+cudaError_t launch_linear(const strata_linear_t& li, const void* x, int T, const float* bias, void* y, cudaStream_t s);
+// scratch: q4_experts_scratch() bytes.
+size_t q4_experts_scratch(const strata_q4_experts_t& ex, int T);
+cudaError_t launch_q4_experts(const strata_q4_experts_t& ex, const int32_t* ids, const float* weights, const void* x, int T,
+                              void* out, char* scratch, int* status, cudaStream_t s);
 
 }  // namespace strata
