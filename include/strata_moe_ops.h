@@ -25,8 +25,8 @@
  * buffer do, are fine.
  *
  * Element types (the framework's own activations are fp32): arithmetic is in 32 bits or more whatever the
- * type, and a result is rounded once, when it is stored.  One value between is held in fewer: the adapters' A_a x has 16
- * bits where y is of a 16-bit type (strata_moe_adapters says so again). */
+ * type, and a result is rounded once, when it is stored.  Some values between are held in fewer: the adapters' A_a x has 16
+ * bits where y is of a 16-bit type, an fp32 x beside 4-bit weights 22, the experts' hidden values 22 or 11 (the calls say so again). */
 #ifndef STRATA_MOE_OPS_H_
 #define STRATA_MOE_OPS_H_
 
@@ -234,11 +234,11 @@ typedef struct strata_linear {
 } strata_linear_t;
 
 /* y[t][n] = sum over k of w[n][k] * x[t][k] + bias[n].  bias fp32 [n_out] or NULL.  x on a 16-byte boundary, y aligned to its elements;
- * y must not overlap x.  No workspace.  x enters as bf16 terms that add up to it (three for fp32, two for fp16), the products are
- * exact and their sums fp32.  A token whose x holds a NaN, an infinity or a number that rounds to bf16's infinity may give NaN in its
- * whole row; other tokens' rows do not change.
- * Built for few tokens: the weights are read once for up to 24 (bf16), 12 (fp16) or 8 (fp32) of them, and the time of more grows in
- * proportion. */
+ * y must not overlap x.  No workspace.  Products are exact and their sums fp32; an fp32 x enters them with 22 bits beside 4-bit weights (24
+ * beside bf16 ones), a bf16 or fp16 x with all its bits, each down to 2^-40 of the largest of its 128 columns.  A token whose x holds a NaN or an infinity (beside bf16 weights: or a number that rounds to bf16's infinity)
+ * may give NaN in its whole row; other tokens' rows do not change.
+ * Built for few tokens: 4-bit weights are read once for up to 24 (16-bit x) or 12 (fp32) of them, bf16 weights for 24 (bf16), 12 (fp16) or 8 (fp32),
+ * and the time of more grows in proportion. */
 strata_status strata_moe_linear(const strata_linear_t* li, const void* x, int32_t T, const float* bias, void* y, void* stream);
 
 /* ---- Routed experts of a few tokens -------------------------------------------------------------------- */
@@ -271,7 +271,7 @@ size_t strata_moe_q4_experts_workspace_bytes(const strata_q4_experts_t* ex, int3
  * nothing of it is read; a token without any gets zeros.  An expert may stand twice in a token's list.  A shared expert is one more expert that every
  * token lists.  T in [0, 64].  x and out on 16-byte boundaries; out must not overlap x.
  * Products are exact and summed in fp32 as in strata_moe_linear; the hidden values of an expert are held in fp32 and enter the
- * second product as three bf16 terms for an fp32 out, two (16 bits) otherwise.  NaN and infinities as there.
+ * second product with 22 bits, with 11 for a bf16 out.  NaN and infinities as there.
  * An id outside [-1, n_expert) sets STRATA_E_CORRUPT in the workspace's status word and the call computes nothing (out keeps its contents).
  * Calls that share a workspace must not overlap in time. */
 strata_status strata_moe_q4_experts(const strata_q4_experts_t* ex, const int32_t* ids, const float* weights, const void* x, int32_t T,

@@ -1,8 +1,8 @@
 // strata_moe_linear: y = x W^T + bias of a few tokens, W 4-bit with group scales or bf16.
 //
-// One persistent kernel.  A unit is 16 rows of W (a slab) for one block of tokens; S warps share it, each taking every S-th chunk of
-// columns, and join their sums over shared memory.  The tokens' bf16 terms lie in shared memory for all warps of the CTA: all columns at
-// once where they fit, else in panels.
+// One persistent kernel.  A unit is 16 rows of W (a slab) for one block of tokens (up to 24 term columns); S warps share it, each taking
+// every S-th chunk of columns, and join their sums over shared memory.  The grid is units x blocks, so that a CTA lays out the terms of
+// one block once, for all its units: at once where they fit beside the rings, else in panels of columns, unit by unit.
 #include "q4_core.cuh"
 
 namespace strata {
@@ -10,30 +10,108 @@ namespace {
 
 using namespace q4;
 
-constexpr int DEPTH = 4;  // chunks that a warp's ring holds
-
 struct LinearArgs {
   const void* x;
   const float* bias;
   void* y;
   int64_t x_stride, y_stride;
   int T, columns, rows, x_type, y_type;
-  int tokens;      // of a block
-  int split;       // warps to a unit
-  int panel;       // chunks whose activations lie in shared memory at once, a multiple of split
-  int row_stride;  // bytes between rows of terms
-  int part_cols;   // term columns of a block, rounded up to whole tiles
+  int tokens, terms;  // of a block
+  int split;          // warps to a unit
+  int depth;          // chunks in a warp's ring
+  int panel;          // chunks whose activations lie in shared memory at once, a multiple of split
+  int row_stride;     // bytes between rows of terms
+  int scale_stride;   // floats between tokens' scales
+  int part_cols;      // term columns of a block, rounded up to whole tiles
 };
 
+// The units of this CTA for one block of tokens.
 template <int NT, class W>
-__device__ __forceinline__ void linear_chunk(const W& w, uint32_t slot, int ch, uint32_t xs, int row_stride, int cols, uint32_t column0,
-                                             int lane, float (&acc)[TILES_MAX][4]) {
-  uint32_t rows[NT];
-  float (&a)[NT][4] = reinterpret_cast<float (&)[NT][4]>(acc);
+__device__ __forceinline__ void linear_block(const W& w, const LinearArgs& a, char* smem, int t0, int nt) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = a.split, group = warp / S, member = warp % S, n_group = WARPS / S;
+  const int units = (a.rows + ROWS - 1) / ROWS, chunks = (a.columns + W::COLUMNS - 1) / W::COLUMNS;
+  const int steps = (chunks + S - 1) / S;  // of a unit
+  const int first = blockIdx.x * n_group, pass = gridDim.x * n_group;
+  const int rounds = first < units ? (units - first + pass - 1) / pass : 0;
+  const int cols = nt * a.terms;
+
+  Ring ring{smem_u32(smem) + warp * (a.depth * W::SLOT), a.depth, 0, 0, W::SLOT};
+  float* part = reinterpret_cast<float*>(smem + WARPS * a.depth * W::SLOT);
+  const int part_step = a.part_cols * PART_STRIDE;
+  float* scale = part + WARPS * part_step;
+  char* rows = reinterpret_cast<char*>(scale + a.tokens * a.scale_stride);
+
+  // the chunks this warp will need, in the order of the loops below
+  int l_unit = first + group, l_step = 0;
+  const uint8_t* l_at = w.at(l_unit, member, lane);
+  auto load_next = [&]() {
+    const uint32_t slot = ring.next_fill();
+    if (l_unit < units) {
+      const int ch = member + l_step * S;
+      if (ch < chunks) w.load(slot, l_at, l_unit, ch, lane);
+      l_at += S * W::BYTES;
+      if (++l_step == steps) {
+        l_step = 0;
+        l_unit += pass;
+        l_at = w.at(l_unit, member, lane);
+      }
+    }
+    copy_commit();
+  };
+  for (int i = 0; i < a.depth - 1; ++i) load_next();
+
+  uint32_t b[NT];
+  uint2 cs[NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t)  // lanes behind the last column read some row; their sums are not used
-    rows[t] = xs + min(8 * t + (lane >> 2), cols - 1) * row_stride + (lane & 3) * 16;
-  chunk_products<NT>(w, slot, ch, rows, column0, lane, a);
+  for (int t = 0; t < NT; ++t) {  // columns behind the last read some row; their sums are not used
+    b[t] = smem_u32(rows) + min(8 * t + (lane >> 2), cols - 1) * a.row_stride + (lane & 3) * 16;
+    const int c = 8 * t + 2 * (lane & 3);
+    cs[t].x = smem_u32(scale + min(c, cols - 1) / a.terms * a.scale_stride);
+    cs[t].y = smem_u32(scale + min(c + 1, cols - 1) / a.terms * a.scale_stride);
+  }
+  const int panel_steps = a.panel / S;
+  const bool panels = a.panel < chunks;
+  for (int round = 0; round < rounds; ++round) {
+    const int u = first + group + round * pass;
+    float acc[NT][4] = {};
+    int panel_first = 0, panel_left = 0;
+    for (int step = 0; step < steps; ++step) {
+      if (panel_left == 0) {
+        panel_left = panel_steps, panel_first = step * S;
+        if (panels || round == 0) {  // activations of the panel
+          const int c0 = panel_first * W::COLUMNS, c1 = min(c0 + a.panel * W::COLUMNS, (a.columns + BLOCK - 1) / BLOCK * BLOCK);
+          const int halves = 2 * WARPS / min(nt, 2 * WARPS);  // half warps to a token
+          const int half = threadIdx.x >> 4;
+          __syncthreads();
+          if (half < halves * nt)
+            for (int t = half / halves; t < nt; t += 2 * WARPS / halves)
+              stage_row<W::F16>(a.x, (t0 + t) * a.x_stride, a.x_type, a.columns, c0, c1, a.terms, rows + t * a.terms * a.row_stride,
+                                a.row_stride, scale + t * a.scale_stride, half % halves, halves);
+          __syncthreads();
+        }
+      }
+      --panel_left;
+      ring.wait();
+      load_next();  // into the slot of the step before
+      const uint32_t slot = ring.next_use();
+      const int ch = member + step * S;
+      if (u < units && ch < chunks) chunk_products<NT>(w, slot, ch, ch - panel_first, b, cs, lane, acc);
+    }
+    store_part<NT>(part + warp * part_step, lane, acc);
+    group_sync(group, S);
+    if (u < units)
+      for (int i = member * 32 + lane; i < nt * ROWS; i += S * 32) {
+        const int t = i / ROWS, row = i % ROWS, n = u * ROWS + row;
+        if (n < a.rows) {
+          float v = sum_part(part + group * S * part_step, part_step, S, a.terms, t, row);
+          if (a.bias) v += a.bias[n];
+          store1(a.y, (t0 + t) * a.y_stride + n, a.y_type, v);
+        }
+      }
+    group_sync(group, S);
+  }
+  copy_wait<0>();
 }
 
 template <class W>
@@ -41,120 +119,57 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(W w, LinearArgs a) {
   extern __shared__ __align__(128) char smem[];
   griddep_wait();
   griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int S = a.split, group = warp / S, member = warp % S, n_group = WARPS / S;
-  const int units = (a.rows + ROWS - 1) / ROWS, chunks = (a.columns + W::COLUMNS - 1) / W::COLUMNS;
-  const int steps = (chunks + S - 1) / S;  // of a unit
-  const int first = blockIdx.x * n_group, pass = gridDim.x * n_group;
-  const int rounds = first < units ? (units - first + pass - 1) / pass : 0;
-  const int terms = terms_of(a.x_type), blocks = (a.T + a.tokens - 1) / a.tokens;
-
-  const uint32_t ring = smem_u32(smem) + warp * (DEPTH * W::SLOT);
-  float* part = reinterpret_cast<float*>(smem + WARPS * DEPTH * W::SLOT);
-  const int part_step = a.part_cols * PART_STRIDE;
-  char* rows = reinterpret_cast<char*>(part + WARPS * part_step);
-  const uint32_t xs = smem_u32(rows);
-
-  // the chunks this warp will need, in the order of the loops below
-  int l_round = 0, l_step = 0, l_block = 0, l_slot = 0;
-  auto load_next = [&]() {
-    if (l_block < blocks && rounds > 0) {
-      const int u = first + group + l_round * pass, ch = member + l_step * S;
-      if (u < units && ch < chunks) w.load(ring + l_slot * W::SLOT, u, ch, lane);
-      if (++l_step == steps) {
-        l_step = 0;
-        if (++l_round == rounds) l_round = 0, ++l_block;
-      }
-    }
-    l_slot = l_slot + 1 == DEPTH ? 0 : l_slot + 1;
-    copy_commit();
-  };
-  for (int i = 0; i < DEPTH - 1; ++i) load_next();
-
-  const int panel_steps = a.panel / S;
-  const bool panels = a.panel < chunks;
-  int slot = 0;
-  for (int block = 0; block < blocks; ++block) {
-    const int t0 = block * a.tokens, nt = min(a.tokens, a.T - t0), cols = nt * terms;
-    for (int round = 0; round < rounds; ++round) {
-      const int u = first + group + round * pass;
-      float acc[TILES_MAX][4] = {};
-      for (int step = 0; step < steps; ++step) {
-        if (step % panel_steps == 0 && (panels || round == 0)) {  // activations of the next panel
-          const int c0 = step * S * W::COLUMNS, c1 = min(c0 + a.panel * W::COLUMNS, (a.columns + BLOCK - 1) / BLOCK * BLOCK);
-          const int eights = (c1 - c0) / 8;
-          __syncthreads();
-          for (int i = threadIdx.x; i < nt * eights; i += THREADS) {
-            const int t = i / eights, c = (i - t * eights) * 8;
-            stage8(a.x, (t0 + t) * a.x_stride, c0 + c, a.columns, a.x_type, terms, rows + t * terms * a.row_stride + c * 2,
-                   a.row_stride);
-          }
-          __syncthreads();
-        }
-        copy_wait<DEPTH - 2>();
-        load_next();  // into the slot of the step before
-        const int ch = member + step * S;
-        if (u < units && ch < chunks) {
-          const uint32_t at = ring + slot * W::SLOT, column0 = (ch - step / panel_steps * a.panel) * W::COLUMNS;
-          if (cols <= 8) linear_chunk<1>(w, at, ch, xs, a.row_stride, cols, column0, lane, acc);
-          else if (cols <= 16) linear_chunk<2>(w, at, ch, xs, a.row_stride, cols, column0, lane, acc);
-          else linear_chunk<3>(w, at, ch, xs, a.row_stride, cols, column0, lane, acc);
-        }
-        slot = slot + 1 == DEPTH ? 0 : slot + 1;
-      }
-      float* mine = part + warp * part_step;
-      if (cols <= 8) store_part<1>(mine, lane, reinterpret_cast<float (&)[1][4]>(acc));
-      else if (cols <= 16) store_part<2>(mine, lane, reinterpret_cast<float (&)[2][4]>(acc));
-      else store_part<3>(mine, lane, acc);
-      group_sync(group, S);
-      if (u < units)
-        for (int i = member * 32 + lane; i < nt * ROWS; i += S * 32) {
-          const int t = i / ROWS, row = i % ROWS, n = u * ROWS + row;
-          if (n < a.rows) {
-            float v = sum_part(part + group * S * part_step, part_step, S, terms, t, row);
-            if (a.bias) v += a.bias[n];
-            store1(a.y, (t0 + t) * a.y_stride + n, a.y_type, v);
-          }
-        }
-      group_sync(group, S);
-    }
+  for (int t0 = blockIdx.y * a.tokens; t0 < a.T; t0 += gridDim.y * a.tokens) {
+    const int nt = min(a.tokens, a.T - t0), tiles = (nt * a.terms + 7) / 8;
+    __syncthreads();
+    if (tiles == 1) linear_block<1>(w, a, smem, t0, nt);
+    else if (tiles == 2) linear_block<2>(w, a, smem, t0, nt);
+    else linear_block<3>(w, a, smem, t0, nt);
   }
-  copy_wait<0>();
 }
 
 template <class W>
 cudaError_t launch(const W& w, LinearArgs a, cudaStream_t s) {
   const int chunks = (a.columns + W::COLUMNS - 1) / W::COLUMNS, units = (a.rows + ROWS - 1) / ROWS;
-  const int terms = terms_of(a.x_type);
   int sms = 0;
   cudaError_t err = sm_count(&sms);
   if (err != cudaSuccess) return err;
-  a.tokens = 8 * TILES_MAX / terms < a.T ? 8 * TILES_MAX / terms : a.T;
-  a.part_cols = (a.tokens * terms + 7) / 8 * 8;
-  const size_t fixed = (size_t)WARPS * DEPTH * W::SLOT + sizeof(float) * WARPS * a.part_cols * PART_STRIDE;
-  const size_t left = SMEM_MAX - fixed;
-  // as many columns at once as fit; a panel is a whole number of the group's steps
-  const int fit = (int)((left / (a.tokens * terms) - 64) / (2 * W::COLUMNS));  // chunks; 13 at least
-  a.split = choose_split((units + sms - 1) / sms, chunks, fit);
+  a.terms = terms_of(a.x_type, W::F16);
+  a.tokens = 8 * TILES_MAX / a.terms < a.T ? 8 * TILES_MAX / a.terms : a.T;
+  a.part_cols = (a.tokens * a.terms + 7) / 8 * 8;
+  const int blocks = (a.T + a.tokens - 1) / a.tokens;
+  const int gy = blocks < sms ? blocks : sms, gx_most = sms / gy;
+  // a ring of 4 chunks; of 3 where that lets all columns of a block lie in shared memory at once
+  int fit = 0;
+  size_t fixed = 0;
+  for (a.depth = 4;; --a.depth) {
+    fixed = (size_t)WARPS * a.depth * W::SLOT + sizeof(float) * WARPS * a.part_cols * PART_STRIDE;
+    // a chunk of a block's terms and scales; a row's padding
+    fit = (int)((SMEM_MAX - fixed - (size_t)a.tokens * (a.terms * 64 + 16)) / (a.tokens * (a.terms * 2 * W::COLUMNS + sizeof(float))));
+    if (a.depth == 3 || fit >= (chunks + WARPS - 1) / WARPS * WARPS) break;
+  }
+  a.split = choose_split((units + gx_most - 1) / gx_most, chunks, fit);
   a.panel = (chunks + a.split - 1) / a.split * a.split;
   if (fit < a.panel) a.panel = fit / a.split * a.split;
-  const int staged = a.panel * W::COLUMNS;
-  a.row_stride = row_bytes(staged);
-  const size_t smem = fixed + (size_t)a.tokens * terms * a.row_stride;
+  a.row_stride = row_bytes(a.panel * W::COLUMNS);
+  a.scale_stride = (a.panel + 3) / 4 * 4;  // the rows behind the scales on 16-byte boundaries
+  const size_t smem = fixed + a.tokens * (sizeof(float) * a.scale_stride + (size_t)a.terms * a.row_stride);
   err = allow_smem<linear_kernel<W>>(SMEM_MAX);
   if (err != cudaSuccess) return err;
-  const int n_group = WARPS / a.split, ctas = (units + n_group - 1) / n_group;
-  STRATA_LAUNCH(KID_LINEAR, s, err = launch_pdl(linear_kernel<W>, ctas < sms ? ctas : sms, THREADS, smem, s, w, a));
+  const int n_group = WARPS / a.split, most = (units + n_group - 1) / n_group;
+  STRATA_LAUNCH(KID_LINEAR, s,
+                err = launch_pdl(linear_kernel<W>, dim3(most < gx_most ? most : gx_most, gy), THREADS, smem, s, w, a));
   return err;
 }
 
 template <int GROUP>
 cudaError_t launch_q4(const strata_linear_t& li, const LinearArgs& a, cudaStream_t s) {
   const strata_q4_t& q = li.q4;
+  const uint8_t* p = (const uint8_t*)li.w;
   const int64_t slab = slab_bytes(q.d_in, q.group, q.zeros != 0);
-  const bool f16 = q.scale_type == STRATA_F16;
-  if (q.zeros) return launch(Q4<GROUP, true>{(const uint8_t*)li.w, slab, q.d_in, f16}, a, s);
-  return launch(Q4<GROUP, false>{(const uint8_t*)li.w, slab, q.d_in, f16}, a, s);
+  if (q.scale_type == STRATA_F16)
+    return q.zeros ? launch(Q4<GROUP, true, true>{p, slab, q.d_in}, a, s) : launch(Q4<GROUP, false, true>{p, slab, q.d_in}, a, s);
+  return q.zeros ? launch(Q4<GROUP, true, false>{p, slab, q.d_in}, a, s) : launch(Q4<GROUP, false, false>{p, slab, q.d_in}, a, s);
 }
 
 }  // namespace

@@ -2,12 +2,14 @@
 // keeps for itself, 4-bit codes widened to bf16, products by mma.m16n8k16 and the activations' bf16 terms.
 //
 // Mathematics.  y[row] = sum over groups of s[row][group] * (sum over its columns of (code - zero) * x).  code - zero is a whole
-// number of magnitude below 16 and exact in bf16; x enters as 1 to 3 bf16 terms that add up to it exactly (bf16: 1, fp16: 2, fp32: 3),
-// each a column of the products, so all products are exact and their sums fp32; the scale multiplies a group's fp32 sum.
-// What bounds it: the weights' bytes, each read once and by no other warp.  16 rows x 32 columns of codes (256 bytes) are two MMAs
-// for up to 8 columns of terms; at the measured copy rate a scheduler has 44 cycles for them, an MMA takes 8 (measured, 4 warps and
-// more a scheduler or 4 accumulators and more a warp), so up to two tiles of 8 columns cost nothing.  Warp-level MMAs take the
-// operands where dequantisation leaves them, in registers; tcgen05 would have four times the codes' bytes pass shared memory.
+// number of magnitude below 16, exact in fp16; x enters as fp16 terms (stage_row), each a column of the products, so the products are
+// exact and their sums fp32; the scale multiplies a group's fp32 sum, the activations' power of two a chunk's.
+// What bounds it: the weights' bytes, each read once and by no other warp, and close behind them the instructions that widen the codes.
+// 16 rows x 128 columns (1 KB) leave a scheduler 176 cycles at the measured copy rate; widening takes 5 integer instructions a word of 8 codes
+// (2 cycles each) and 4 subtractions, 8 words a lane: 80 cycles of the integer pipe.  (bf16 operands, with 7 mantissa bits, take 7: at 155
+// integer instructions a chunk with everything around them 2.7 TB/s were all that came.)  An MMA takes 8 cycles (measured, with 4 warps a
+// scheduler), 8 a chunk and tile of 8 columns, so two tiles are hidden.  Warp-level MMAs take the operands where widening leaves them, in
+// registers; tcgen05 would have four times the codes' bytes pass shared memory.
 #pragma once
 #include "device_common.cuh"
 #include "elements.cuh"
@@ -18,30 +20,55 @@ namespace q4 {
 
 constexpr int WARPS = 16;           // of a CTA; one CTA an SM
 constexpr int THREADS = 32 * WARPS;
-constexpr int SMEM_MAX = 227 * 1024;
+constexpr int SMEM_MAX = 227 * 1024 - 256;  // dynamic; the rest holds the kernels' static words
 constexpr int TILES_MAX = 3;        // tiles of 8 term columns that a warp accumulates at once
 constexpr int PART_STRIDE = 20;     // floats between two columns of a warp's sums: 16 rows and 4 against bank conflicts
 
 // ---- activations ------------------------------------------------------------------------------------
-// Terms of a type: bf16 holds 8 significant bits, fp16 11, fp32 24.
-__host__ __device__ constexpr int terms_of(int type) { return type == STRATA_BF16 ? 1 : type == STRATA_F16 ? 2 : 3; }
-// Bytes between rows of `columns` (a multiple of 32) bf16 in shared memory: 64 past a multiple of 128, so that the 16-byte
+// How x enters the products.  Beside 4-bit codes: fp16 terms of x divided by a power of two for each token and chunk of 128 columns, so
+// that the largest lies in [2^14, 2^15); one term holds all bits of a bf16 or fp16 (down to 2^-40 of the chunk's largest), two hold 22 of an
+// fp32's 24.  Beside bf16 weights: bf16 terms as they are, 8 bits each.
+__host__ __device__ constexpr int terms_of(int type, bool f16) {
+  return type == STRATA_BF16 ? 1 : type == STRATA_F16 ? (f16 ? 1 : 2) : (f16 ? 2 : 3);
+}
+// Bytes between rows of `columns` (a multiple of 32) terms in shared memory: 64 past a multiple of 128, so that the 16-byte
 // operand loads of 8 lanes, 64 bytes of each of two rows, meet all banks once.
 __host__ __device__ constexpr int row_bytes(int columns) { return (2 * columns) | 64; }
 
-// Columns i .. i + 7 of a row into `terms` rows of shared memory; behind the last column zeros.
-__device__ __forceinline__ void stage8(const void* x, int64_t row0, int i, int columns, int type, int terms, char* dst, int stride) {
-  float f[8] = {};
-  if (i < columns) widen8(load8(x, row0 + i, type), type, f);
-  for (int t = 0; t < terms; ++t) {
-    uint32_t w[4];
+// Columns c0 .. c1 - 1 (c0 a multiple of 128) of row `row0` elements into x, as `terms` rows at dst, by 16 lanes of 8 columns a chunk;
+// behind the last column zeros, up to a whole block of 32.  scale: of chunk c0 / 128 and on (4-bit weights).  `part` of `parts` half warps.
+template <bool F16>
+__device__ __forceinline__ void stage_row(const void* x, int64_t row0, int type, int columns, int c0, int c1, int terms, char* dst, int stride,
+                                          float* scale, int part, int parts) {
+  const int lane = threadIdx.x & 15;
+  const uint32_t half = 0xffffu << (threadIdx.x & 16);
+  for (int c = part * CHUNK; c < c1 - c0; c += parts * CHUNK) {
+    const int i = c + lane * 8;
+    float f[8] = {};
+    if (c0 + i < columns) widen8(load8(x, row0 + c0 + i, type), type, f);
+    if (F16) {
+      uint32_t top = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      w[j] = narrow2(f[2 * j], f[2 * j + 1], STRATA_BF16);
-      f[2 * j] -= __uint_as_float(w[j] << 16);  // exact: the rest has fewer bits
-      f[2 * j + 1] -= __uint_as_float(w[j] & 0xffff0000u);
+      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+      for (int o = 8; o; o /= 2) top = max(top, __shfl_xor_sync(half, top, o));
+      const uint32_t e = max(top >> 23, 15u);  // 2^(e - 127) <= largest; below 2^-112 all count as 2^-112
+      const float up = __uint_as_float((268u - e) << 23);
+      if (lane == 0) scale[c / CHUNK] = __uint_as_float((e - 14u) << 23);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] *= up;
     }
-    *reinterpret_cast<uint4*>(dst + t * stride) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (c0 + i >= (columns + BLOCK - 1) / BLOCK * BLOCK) continue;
+    for (int t = 0; t < terms; ++t) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[j] = narrow2(f[2 * j], f[2 * j + 1], F16 ? STRATA_F16 : STRATA_BF16);
+        const float2 v = widen2(w[j], F16 ? STRATA_F16 : STRATA_BF16);
+        f[2 * j] -= v.x;  // exact: the rest has fewer bits
+        f[2 * j + 1] -= v.y;
+      }
+      *reinterpret_cast<uint4*>(dst + t * stride + i * 2) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
 }
 
@@ -68,93 +95,157 @@ __device__ __forceinline__ uint32_t lds4(uint32_t a) {
 }
 
 // ---- products ----------------------------------------------------------------------------------------
+template <bool F16>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Pair j of a packed word as bf16 code - zero; zero128 holds 128 + zero twice.  0x4300 | code is 128 + code.
-__device__ __forceinline__ uint32_t widen_pair(uint32_t w, int j, uint32_t zero128) {
-  const uint32_t v = ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u;
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&zero128));
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
-__device__ __forceinline__ float2 scales_of(uint32_t w, bool f16) {
-  return f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w))
-             : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+// A packed word as four pairs of fp16 code - zero.  In the mantissa of fp16, 0x6400 | code is 1024 + code and 0x5400 | code << 4 is
+// 64 + code, so two pairs of nibbles need no shift; z0 holds 1024 + zero twice, z1 64 + zero.
+__device__ __forceinline__ void widen_word(uint32_t w, uint32_t z0, uint32_t z1, uint32_t (&a)[4]) {
+  const uint32_t v = w >> 8;
+  a[0] = sub2((w & 0x000f000fu) | 0x64006400u, z0);
+  a[1] = sub2((w & 0x00f000f0u) | 0x54005400u, z1);
+  a[2] = sub2((v & 0x000f000fu) | 0x64006400u, z0);
+  a[3] = sub2((v & 0x00f000f0u) | 0x54005400u, z1);
+}
+
+// z0 and z1 of rows g (byte 0 of z) and g + 8 (byte 1).
+__device__ __forceinline__ void zero_pairs(uint32_t z, uint32_t& z0lo, uint32_t& z1lo, uint32_t& z0hi, uint32_t& z1hi) {
+  const uint32_t l = (z & 15u) * 0x00010001u, h = (z >> 8 & 15u) * 0x00010001u;
+  z0lo = l | 0x64006400u, z1lo = l << 4 | 0x54005400u;
+  z0hi = h | 0x64006400u, z1hi = h << 4 | 0x54005400u;
 }
 
 // 4-bit weights of groups of GROUP columns: a chunk's bytes in the ring and its products.
-template <int GROUP, bool ZEROS>
+template <int GROUP, bool ZEROS, bool SCALE_F16>
 struct Q4 {
+  static constexpr bool F16 = true;  // the products' operands
   static constexpr int COLUMNS = CHUNK;
   static constexpr int SB = scale_bytes(GROUP), ZB = ZEROS ? zero_bytes(GROUP) : 0;
-  static constexpr int SLOT = 1024 + 32 * (SB + ZB);  // of a warp; scales and zero points once for each lane
+  static constexpr int META = meta_bytes(GROUP, ZEROS);
+  static constexpr int SLOT = 1024 + META;
   static constexpr int BYTES = chunk_bytes(GROUP, ZEROS);
 
   const uint8_t* base;  // of the matrix
   int64_t slab;         // bytes of a slab
   int columns;
-  bool f16;             // scales are fp16
 
-  __device__ __forceinline__ int blocks(int ch) const { return min(4, columns / BLOCK - 4 * ch); }
-  __device__ __forceinline__ void load(uint32_t slot, int64_t s, int ch, int lane) const {
-    const uint8_t* p = base + s * slab + (int64_t)ch * BYTES;
-    const int nb = blocks(ch), g = lane >> 2;
-    if (nb == 4) {
-      copy_async<16>(slot + lane * 16, p + lane * 16);
-      copy_async<16>(slot + 512 + lane * 16, p + 512 + lane * 16);
+  // Where this lane's part of chunk ch of slab s begins; the next chunk is BYTES further.
+  __device__ __forceinline__ const uint8_t* at(int64_t s, int ch, int lane) const { return base + s * slab + ch * BYTES + lane * 16; }
+  __device__ __forceinline__ void load(uint32_t slot, const uint8_t* p, int64_t, int ch, int lane) const {
+    const int left = columns - ch * CHUNK;
+    if (left >= CHUNK) {
+      copy_async<16>(slot + lane * 16, p);
+      copy_async<16>(slot + 512 + lane * 16, p + 512);
+      if (lane < META / 16) copy_async<16>(slot + 1024 + lane * 16, p + 1024);
     } else {
+      const int nb = left / BLOCK;
+      p -= lane * 16;
       for (int b = 0; b < nb; ++b) {
         copy_async<4>(slot + lane * 16 + 4 * b, p + (lane * nb + b) * 4);
         copy_async<4>(slot + 512 + lane * 16 + 4 * b, p + 128 * nb + (lane * nb + b) * 4);
       }
+      if (lane < META / 16) copy_async<16>(slot + 1024 + lane * 16, p + 256 * nb + lane * 16);
     }
-    p += 256 * nb;
-    copy_async<SB>(slot + 1024 + lane * SB, p + g * SB);
-    if constexpr (ZEROS) copy_async<ZB>(slot + 1024 + 32 * SB + lane * ZB, p + 8 * SB + g * ZB);
   }
 
-  // acc[tile] += slab x columns; b[tile]: the shared address of this lane's operand row at the chunk's first column.
-  template <int NT, bool WHOLE>
-  __device__ __forceinline__ void products(uint32_t slot, int nb, const uint32_t (&b)[NT], int lane, float (&acc)[NT][4]) const {
+  // acc[tile] += chunk x columns.  b[tile]: shared address of this lane's operand row at the chunk's first column; cs[tile]: the scales of
+  // this lane's two result columns in this chunk.
+  template <int NT>
+  __device__ __forceinline__ void products(uint32_t slot, const uint32_t (&b)[NT], const float2 (&cs)[NT], int lane,
+                                           float (&acc)[NT][4]) const {
+    const int g = lane >> 2;
     const uint4 lo4 = lds16(slot + lane * 16), hi4 = lds16(slot + 512 + lane * 16);
     const uint32_t lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
+    uint32_t scales[4], zeros[2];
+    if constexpr (SB == 16) {
+      const uint4 v = lds16(slot + 1024 + g * 16);
+      scales[0] = v.x, scales[1] = v.y, scales[2] = v.z, scales[3] = v.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < SB / 4; ++i) scales[i] = lds4(slot + 1024 + g * SB + 4 * i);
+    }
+    if constexpr (ZEROS) {
+#pragma unroll
+      for (int i = 0; i < ZB / 4; ++i) zeros[i] = lds4(slot + 1024 + 8 * SB + g * ZB + 4 * i);
+    }
     constexpr int PER = GROUP / BLOCK;
+    float sum[NT][4] = {};
 #pragma unroll
     for (int gr = 0; gr < groups_of(GROUP); ++gr) {
-      if (!WHOLE && gr * PER >= nb) break;
-      const float2 s = scales_of(lds4(slot + 1024 + lane * SB + 4 * gr), f16);
-      uint32_t zlo = 0x43084308u, zhi = 0x43084308u;  // zero point 8
+      uint32_t z0lo = 0x64086408u, z1lo = 0x54805480u, z0hi = z0lo, z1hi = z1lo;  // zero point 8
       if constexpr (ZEROS) {
-        const uint32_t z = lds4(slot + 1024 + 32 * SB + lane * ZB + (gr >> 1) * 4) >> (16 * (gr & 1));
-        zlo = (z & 15u) * 0x00010001u | 0x43004300u;
-        zhi = (z >> 8 & 15u) * 0x00010001u | 0x43004300u;
+        zero_pairs(zeros[gr >> 1] >> (16 * (gr & 1)), z0lo, z1lo, z0hi, z1hi);
       }
       float part[NT][4] = {};
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int k = gr * PER + i;
-        if (!WHOLE && k >= nb) break;
         uint32_t alo[4], ahi[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          alo[j] = widen_pair(lo[k], j, zlo);
-          ahi[j] = widen_pair(hi[k], j, zhi);
-        }
+        widen_word(lo[k], z0lo, z1lo, alo);
+        widen_word(hi[k], z0hi, z1hi, ahi);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const uint4 x = lds16(b[t] + k * 64);
-          mma(part[t], alo[0], ahi[0], alo[1], ahi[1], x.x, x.y);
-          mma(part[t], alo[2], ahi[2], alo[3], ahi[3], x.z, x.w);
+          mma<true>(part[t], alo[0], ahi[0], alo[1], ahi[1], x.x, x.y);
+          mma<true>(part[t], alo[2], ahi[2], alo[3], ahi[3], x.z, x.w);
         }
       }
+      const float2 s = SCALE_F16 ? widen2(scales[gr], STRATA_F16) : widen2(scales[gr], STRATA_BF16);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        acc[t][0] = fmaf(s.x, part[t][0], acc[t][0]);
-        acc[t][1] = fmaf(s.x, part[t][1], acc[t][1]);
-        acc[t][2] = fmaf(s.y, part[t][2], acc[t][2]);
-        acc[t][3] = fmaf(s.y, part[t][3], acc[t][3]);
+        sum[t][0] = fmaf(s.x, part[t][0], sum[t][0]);
+        sum[t][1] = fmaf(s.x, part[t][1], sum[t][1]);
+        sum[t][2] = fmaf(s.y, part[t][2], sum[t][2]);
+        sum[t][3] = fmaf(s.y, part[t][3], sum[t][3]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      acc[t][0] = fmaf(cs[t].x, sum[t][0], acc[t][0]);
+      acc[t][1] = fmaf(cs[t].y, sum[t][1], acc[t][1]);
+      acc[t][2] = fmaf(cs[t].x, sum[t][2], acc[t][2]);
+      acc[t][3] = fmaf(cs[t].y, sum[t][3], acc[t][3]);
+    }
+  }
+
+  // The same for a last chunk of nb (1 to 3) blocks, block by block.
+  template <int NT>
+  __device__ __forceinline__ void tail(uint32_t slot, int nb, const uint32_t (&b)[NT], const float2 (&cs)[NT], int lane,
+                                       float (&acc)[NT][4]) const {
+    const int g = lane >> 2;
+#pragma unroll 1
+    for (int k = 0; k < nb; ++k) {
+      const int gr = k * BLOCK / GROUP;
+      const uint32_t w = lds4(slot + 1024 + g * SB + 4 * gr);
+      const float2 s = SCALE_F16 ? widen2(w, STRATA_F16) : widen2(w, STRATA_BF16);
+      uint32_t z0lo = 0x64086408u, z1lo = 0x54805480u, z0hi = z0lo, z1hi = z1lo;
+      if constexpr (ZEROS)
+        zero_pairs(lds4(slot + 1024 + 8 * SB + g * ZB + 4 * (gr >> 1)) >> (16 * (gr & 1)), z0lo, z1lo, z0hi, z1hi);
+      uint32_t alo[4], ahi[4];
+      widen_word(lds4(slot + lane * 16 + 4 * k), z0lo, z1lo, alo);
+      widen_word(lds4(slot + 512 + lane * 16 + 4 * k), z0hi, z1hi, ahi);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint4 x = lds16(b[t] + k * 64);
+        float part[4] = {};
+        mma<true>(part, alo[0], ahi[0], alo[1], ahi[1], x.x, x.y);
+        mma<true>(part, alo[2], ahi[2], alo[3], ahi[3], x.z, x.w);
+        acc[t][0] = fmaf(cs[t].x * s.x, part[0], acc[t][0]);
+        acc[t][1] = fmaf(cs[t].y * s.x, part[1], acc[t][1]);
+        acc[t][2] = fmaf(cs[t].x * s.y, part[2], acc[t][2]);
+        acc[t][3] = fmaf(cs[t].y * s.y, part[3], acc[t][3]);
       }
     }
   }
@@ -162,50 +253,94 @@ struct Q4 {
 
 // bf16 weights, rows as they are: 64 columns of 16 rows a chunk, 16 bytes a lane, row and block of 32 columns.
 struct Bf16 {
+  static constexpr bool F16 = false;
   static constexpr int COLUMNS = 64;
   static constexpr int SLOT = 2048;
+  static constexpr int BYTES = 2 * COLUMNS;
 
   const uint8_t* base;
   int64_t stride;  // elements
   int columns, rows;
 
-  __device__ __forceinline__ int blocks(int ch) const { return min(2, (columns + BLOCK - 1) / BLOCK - 2 * ch); }
-  __device__ __forceinline__ void load(uint32_t slot, int64_t s, int ch, int lane) const {
+  __device__ __forceinline__ const uint8_t* at(int64_t s, int ch, int lane) const {
+    // a row behind the last reads row 0 and its results are not used
+    const int64_t row = s * ROWS + (lane >> 2);
+    return base + 2 * ((row < rows ? row : 0) * stride) + ch * BYTES + (lane & 3) * 16;
+  }
+  __device__ __forceinline__ void load(uint32_t slot, const uint8_t* p, int64_t s, int ch, int lane) const {
+    const uint8_t* q = s * ROWS + (lane >> 2) + 8 < rows ? p + 16 * stride : p;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // block i / 2, row half i % 2
-      const int64_t row = s * ROWS + (lane >> 2) + 8 * (i & 1);
-      const int col = ch * COLUMNS + (i >> 1) * BLOCK + (lane & 3) * 8;
-      const bool have = row < rows && col < columns;
-      const uint8_t* p = have ? base + 2 * (row * stride + col) : base;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + i * 512 + lane * 16), "l"(p), "r"(have ? 16 : 0)
+      const bool have = ch * COLUMNS + (i >> 1) * BLOCK + (lane & 3) * 8 < columns;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + i * 512 + lane * 16),
+                   "l"(have ? (i & 1 ? q : p) + (i >> 1) * 64 : base), "r"(have ? 16 : 0)
                    : "memory");
     }
   }
-  template <int NT, bool WHOLE>
-  __device__ __forceinline__ void products(uint32_t slot, int nb, const uint32_t (&b)[NT], int lane, float (&acc)[NT][4]) const {
+  template <int NT>
+  __device__ __forceinline__ void products(uint32_t slot, const uint32_t (&b)[NT], const float2 (&)[NT], int lane,
+                                           float (&acc)[NT][4]) const {
+    block<NT>(slot, 0, b, lane, acc);
+    block<NT>(slot, 1, b, lane, acc);
+  }
+  template <int NT>
+  __device__ __forceinline__ void tail(uint32_t slot, int, const uint32_t (&b)[NT], const float2 (&)[NT], int lane,
+                                       float (&acc)[NT][4]) const {
+    block<NT>(slot, 0, b, lane, acc);  // its other block is there, zeros; its operands would not be
+  }
+  template <int NT>
+  __device__ __forceinline__ void block(uint32_t slot, int k, const uint32_t (&b)[NT], int lane, float (&acc)[NT][4]) const {
+    const uint4 lo = lds16(slot + k * 1024 + lane * 16), hi = lds16(slot + k * 1024 + 512 + lane * 16);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (!WHOLE && k >= nb) break;
-      const uint4 lo = lds16(slot + k * 1024 + lane * 16), hi = lds16(slot + k * 1024 + 512 + lane * 16);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const uint4 x = lds16(b[t] + k * 64);
-        mma(acc[t], lo.x, hi.x, lo.y, hi.y, x.x, x.y);
-        mma(acc[t], lo.z, hi.z, lo.w, hi.w, x.z, x.w);
-      }
+    for (int t = 0; t < NT; ++t) {
+      const uint4 x = lds16(b[t] + k * 64);
+      mma<false>(acc[t], lo.x, hi.x, lo.y, hi.y, x.x, x.y);
+      mma<false>(acc[t], lo.z, hi.z, lo.w, hi.w, x.z, x.w);
     }
   }
 };
 
+// A warp's ring of `depth` chunks: filled `depth` - 1 ahead, one group of copies a step whether or not it copies anything.
+struct Ring {
+  uint32_t at;
+  int depth, fill, use, slot_bytes;
+  __device__ __forceinline__ uint32_t next_fill() {
+    const uint32_t a = at + fill * slot_bytes;
+    fill = fill + 1 == depth ? 0 : fill + 1;
+    return a;
+  }
+  __device__ __forceinline__ uint32_t next_use() {
+    const uint32_t a = at + use * slot_bytes;
+    use = use + 1 == depth ? 0 : use + 1;
+    return a;
+  }
+  __device__ __forceinline__ void wait() const {  // for the oldest; its scales were copied by other lanes
+    if (depth == 4) copy_wait<2>();
+    else if (depth == 3) copy_wait<1>();
+    else copy_wait<0>();
+    __syncwarp();
+  }
+};
+
+// One chunk's products: rows[tile] and scales[tile] are this lane's shared addresses for the activations' first column and chunk.
 template <int NT, class W>
-__device__ __forceinline__ void chunk_products(const W& w, uint32_t slot, int ch, const uint32_t (&rows)[NT], uint32_t column0,
-                                               int lane, float (&acc)[NT][4]) {
+__device__ __forceinline__ void chunk_products(const W& w, uint32_t slot, int ch, int staged_ch, const uint32_t (&rows)[NT],
+                                               const uint2 (&scales)[NT], int lane, float (&acc)[NT][4]) {
   uint32_t b[NT];
+  float2 cs[NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) b[t] = rows[t] + column0 * 2;
-  const int nb = w.blocks(ch);
-  if (nb == W::COLUMNS / BLOCK) w.template products<NT, true>(slot, nb, b, lane, acc);
-  else w.template products<NT, false>(slot, nb, b, lane, acc);
+  for (int t = 0; t < NT; ++t) {
+    b[t] = rows[t] + staged_ch * (2 * W::COLUMNS);
+    cs[t] = make_float2(1.f, 1.f);
+    if (W::F16) {
+      cs[t].x = __uint_as_float(lds4(scales[t].x + staged_ch * 4));
+      cs[t].y = __uint_as_float(lds4(scales[t].y + staged_ch * 4));
+    }
+  }
+  // columns of bf16 weights end anywhere: a chunk is whole when its last block has begun
+  const int left = (w.columns - ch * W::COLUMNS + BLOCK - 1) / BLOCK;
+  if (left >= W::COLUMNS / BLOCK) w.template products<NT>(slot, b, cs, lane, acc);
+  else w.template tail<NT>(slot, left, b, cs, lane, acc);
 }
 
 // A warp's sums to its place in shared memory, [column][16 rows].
@@ -240,10 +375,9 @@ __device__ __forceinline__ void group_sync(int group, int S) {
 // which leaves fewer sums to join.
 __host__ __device__ inline int choose_split(int units_of_cta, int chunks, int most = WARPS) {
   int best = 1, cost = 1 << 30;
-  for (int S = 1; S <= WARPS && S <= most; S *= 2) {
-    const int groups = WARPS / S;
-    const int c = (units_of_cta + groups - 1) / groups * ((chunks + S - 1) / S);
-    if (c < cost) best = S, cost = c;
+  for (int i = 0; 1 << i <= WARPS && 1 << i <= most; ++i) {  // 2^i warps a unit, WARPS / 2^i units at once
+    const int c = ((units_of_cta + (WARPS >> i) - 1) * (1 << i) / WARPS) * ((chunks + (1 << i) - 1) >> i);
+    if (c < cost) best = 1 << i, cost = c;
   }
   return best;
 }

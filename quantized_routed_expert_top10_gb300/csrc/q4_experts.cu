@@ -14,7 +14,6 @@ namespace {
 
 using namespace q4;
 
-constexpr int DEPTH = 4;  // chunks that a warp's ring holds
 constexpr int PAIRS_MAX = STRATA_Q4_EXPERTS_T_MAX * STRATA_Q4_EXPERTS_K_MAX;
 static_assert(PAIRS_MAX < 65536 && STRATA_Q4_EXPERTS_E_MAX <= 2 * THREADS && PAIRS_MAX <= 4 * THREADS, "sorting of the pairs");
 
@@ -28,8 +27,10 @@ struct ExpertArgs {
   int64_t x_stride;
   int T, k, E, x_type, terms;
   int columns, rows;  // of an expert's matrix; rows of `to`
-  int tokens;         // of a block
-  int row_stride, part_cols;
+  int tokens;         // pairs of a block
+  int resident;       // all tokens' (all pairs') terms lie in shared memory from the start, else a block's
+  int staged;         // rows of x in shared memory at once
+  int depth, row_stride, scale_stride, part_cols;
 };
 
 // The pairs by expert: expert[a], its pairs pair[off[a]] .. pair[off[a + 1] - 1], a < n.
@@ -95,15 +96,96 @@ __device__ __forceinline__ Sorted sort_pairs(char* smem, const ExpertArgs& a) {
   return s;
 }
 
-template <int NT, class W>
-__device__ __forceinline__ void expert_chunk(const W& w, uint32_t slot, int64_t s, int ch, uint32_t xs, int row_stride, int cols, int lane,
-                                             float (&acc)[TILES_MAX][4]) {
-  uint32_t rows[NT];
-  float (&a)[NT][4] = reinterpret_cast<float (&)[NT][4]>(acc);
+// The units of a stretch u0 .. u1 - 1 in the order in which a CTA takes them: for each expert of the stretch, for each block of its pairs,
+// its units, n_group at a time.  Walked by the copies, a ring ahead of the products.
+template <class W>
+struct Loader {
+  const Sorted& sorted;
+  const W& w;
+  int64_t expert_stride;
+  int slabs, chunks, steps, S, member, group, n_group, u1, tokens;
+  int begin, end, left;  // the expert's stretch, its blocks left
+  int u, step;
+  const uint8_t* at;
+  W we;                  // the expert's matrix
+
+  __device__ __forceinline__ void expert(int lane) {
+    begin = end;
+    if (begin >= u1) return;
+    const int e = begin / slabs;
+    end = min(u1, (e + 1) * slabs);
+    left = (sorted.off[e + 1] - sorted.off[e] + tokens - 1) / tokens;
+    we = w;
+    we.base += sorted.expert[e] * expert_stride - (int64_t)e * slabs * w.slab;
+    start(begin, lane);
+  }
+  __device__ __forceinline__ void start(int base, int lane) {
+    u = base + group;
+    step = 0;
+    at = we.at(u, member, lane);
+  }
+  __device__ __forceinline__ void next(Ring& ring, int lane) {
+    const uint32_t slot = ring.next_fill();
+    if (begin < u1) {
+      const int ch = member + step * S;
+      if (u < end && ch < chunks) we.load(slot, at, u, ch, lane);
+      at += S * W::BYTES;
+      if (++step == steps) {
+        const int base = u - group + n_group;
+        if (base < end) start(base, lane);
+        else if (--left) start(begin, lane);
+        else expert(lane);
+      }
+    }
+    copy_commit();
+  }
+};
+
+// The units begin .. end - 1 of one expert for np of its pairs (from position p0 of the sorted ones).
+template <bool DOWN, int NT, class W>
+__device__ __forceinline__ void expert_block(const W& w, const ExpertArgs& a, const Sorted& sorted, Loader<W>& loader, Ring& ring, float* part,
+                                             const float* scale, const char* rows, int begin, int end, int first_unit, int p0, int np) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = loader.S, group = loader.group, member = loader.member;
+  const int part_step = a.part_cols * PART_STRIDE;
+  uint32_t b[NT];
+  uint2 cs[NT];
+  auto row_of = [&](int j) {  // of pair j of the block among those in shared memory
+    j = min(j, np - 1);       // columns behind the last read some row; their sums are not used
+    return !a.resident ? j : DOWN ? p0 + j : sorted.pair[p0 + j] / a.k;
+  };
 #pragma unroll
-  for (int t = 0; t < NT; ++t)  // lanes behind the last column read some row; their sums are not used
-    rows[t] = xs + min(8 * t + (lane >> 2), cols - 1) * row_stride + (lane & 3) * 16;
-  chunk_products<NT>(w, slot, ch, rows, ch * W::COLUMNS, lane, a);
+  for (int t = 0; t < NT; ++t) {
+    const int c = 8 * t + (lane >> 2), j = c / a.terms;
+    b[t] = smem_u32(rows) + (row_of(j) * a.terms + (c - j * a.terms)) * a.row_stride + (lane & 3) * 16;
+    const int c2 = 8 * t + 2 * (lane & 3);
+    cs[t].x = smem_u32(scale + row_of(c2 / a.terms) * a.scale_stride);
+    cs[t].y = smem_u32(scale + row_of((c2 + 1) / a.terms) * a.scale_stride);
+  }
+  for (int base = begin; base < end; base += loader.n_group) {
+    const int u = base + group;
+    float acc[NT][4] = {};
+    for (int step = 0; step < loader.steps; ++step) {
+      ring.wait();
+      loader.next(ring, lane);  // into the slot of the step before
+      const uint32_t slot = ring.next_use();
+      const int ch = member + step * S;
+      if (u < end && ch < loader.chunks) chunk_products<NT>(w, slot, ch, ch, b, cs, lane, acc);
+    }
+    store_part<NT>(part + warp * part_step, lane, acc);
+    group_sync(group, S);
+    if (u < end) {
+      const float* sums = part + group * S * part_step;
+      constexpr int OUT = DOWN ? ROWS : 8;
+      for (int i = member * 32 + lane; i < np * OUT; i += S * 32) {
+        const int j = i / OUT, row = i % OUT;
+        float v = sum_part(sums, part_step, S, a.terms, j, row);
+        if (!DOWN) v = silu_mul(v, sum_part(sums, part_step, S, a.terms, j, row + 8));
+        a.to[(int64_t)sorted.pair[p0 + j] * a.rows + (u - first_unit) * OUT + row] = v;
+      }
+    }
+    group_sync(group, S);
+  }
 }
 
 template <bool DOWN, class W>
@@ -112,12 +194,10 @@ __global__ void __launch_bounds__(THREADS, 1) experts_kernel(W w, int64_t expert
   if (!DOWN) griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t ring = smem_u32(smem) + warp * (DEPTH * W::SLOT);
-  float* part = reinterpret_cast<float*>(smem + WARPS * DEPTH * W::SLOT);
-  const int part_step = a.part_cols * PART_STRIDE;
-  char* rows = reinterpret_cast<char*>(part + WARPS * part_step);
-  const uint32_t xs = smem_u32(rows);
-  const Sorted sorted = sort_pairs(rows + a.tokens * a.terms * a.row_stride, a);
+  float* part = reinterpret_cast<float*>(smem + WARPS * a.depth * W::SLOT);
+  float* scale = part + WARPS * a.part_cols * PART_STRIDE;
+  char* rows = reinterpret_cast<char*>(scale + a.staged * a.scale_stride);
+  const Sorted sorted = sort_pairs(rows + a.staged * a.terms * a.row_stride, a);
   if (!DOWN && blockIdx.x == 0 && threadIdx.x == 0) {
     *a.bad = sorted.bad;
     if (sorted.bad) set_status(a.status, ST_CORRUPT);
@@ -131,90 +211,38 @@ __global__ void __launch_bounds__(THREADS, 1) experts_kernel(W w, int64_t expert
   const int units = sorted.n * slabs;
   const int u0 = (int)((int64_t)blockIdx.x * units / gridDim.x), u1 = (int)((int64_t)(blockIdx.x + 1) * units / gridDim.x);
   const int S = choose_split((units + gridDim.x - 1) / gridDim.x, chunks);
-  const int group = warp / S, member = warp % S, n_group = WARPS / S;
-  const int steps = (chunks + S - 1) / S;
-
-  auto load = [&](uint32_t slot, int u, int ch) {
-    const int e = u / slabs;
-    W we = w;
-    we.base += sorted.expert[e] * expert_stride;
-    we.load(slot, u - e * slabs, ch, lane);
-  };
-  auto blocks_of = [&](int e) { return (sorted.off[e + 1] - sorted.off[e] + a.tokens - 1) / a.tokens; };
-  // the chunks this warp will need, in the order of the loops below
-  int l_begin = u0, l_end = u0, l_u = u0, l_step = 0, l_left = 0, l_slot = 0;  // an expert's stretch, its blocks left
-  auto next_expert = [&]() {
-    l_begin = l_u = l_end;
-    if (l_begin < u1) {
-      const int e = l_begin / slabs;
-      l_end = min(u1, (e + 1) * slabs);
-      l_left = blocks_of(e);
-    }
-  };
-  next_expert();
-  auto load_next = [&]() {
-    if (l_begin < u1) {
-      const int u = l_u + group, ch = member + l_step * S;
-      if (u < l_end && ch < chunks) load(ring + l_slot * W::SLOT, u, ch);
-      if (++l_step == steps) {
-        l_step = 0;
-        l_u += n_group;
-        if (l_u >= l_end) {
-          l_u = l_begin;
-          if (--l_left == 0) next_expert();
-        }
-      }
-    }
-    l_slot = l_slot + 1 == DEPTH ? 0 : l_slot + 1;
-    copy_commit();
-  };
-  for (int i = 0; i < DEPTH - 1; ++i) load_next();
+  Ring ring{smem_u32(smem) + warp * (a.depth * W::SLOT), a.depth, 0, 0, W::SLOT};
+  Loader<W> loader{sorted, w, expert_stride, slabs, chunks, (chunks + S - 1) / S, S, warp % S, warp / S, WARPS / S, u1, a.tokens, u0, u0};
+  loader.expert(lane);
+  for (int i = 0; i < a.depth - 1; ++i) loader.next(ring, lane);
   if (DOWN) griddep_wait();  // h
 
-  int slot = 0;
+  // the terms of the block's rows: source(j) is row j of x
+  auto stage = [&](int n, auto source) {
+    const int half = threadIdx.x >> 4, halves = n < 2 * WARPS ? 2 * WARPS / n : 1;
+    for (int j = half / halves; j < n; j += 2 * WARPS / halves) {
+      if (half >= 2 * WARPS / halves * halves) break;
+      stage_row<true>(a.x, source(j) * a.x_stride, a.x_type, a.columns, 0, a.columns, a.terms, rows + j * a.terms * a.row_stride,
+                      a.row_stride, scale + j * a.scale_stride, half % halves, halves);
+    }
+  };
+  if (a.resident && u0 < u1) {
+    if (DOWN) stage(sorted.off[sorted.n], [&](int j) { return (int64_t)sorted.pair[j]; });
+    else stage(a.T, [&](int j) { return (int64_t)j; });
+    __syncthreads();
+  }
   for (int begin = u0; begin < u1;) {
-    const int e = begin / slabs, end = min(u1, (e + 1) * slabs), first = sorted.off[e], last = sorted.off[e + 1];
-    for (int p0 = first; p0 < last; p0 += a.tokens) {
-      const int np = min(a.tokens, last - p0), cols = np * a.terms, eights = a.columns / 8;
-      __syncthreads();
-      for (int i = threadIdx.x; i < np * eights; i += THREADS) {
-        const int j = i / eights, c = (i - j * eights) * 8, p = sorted.pair[p0 + j];
-        stage8(a.x, (DOWN ? p : p / a.k) * a.x_stride, c, a.columns, a.x_type, a.terms, rows + j * a.terms * a.row_stride + c * 2,
-               a.row_stride);
+    const int e = begin / slabs, end = min(u1, (e + 1) * slabs), last = sorted.off[e + 1];
+    for (int p0 = sorted.off[e]; p0 < last; p0 += a.tokens) {
+      const int np = min(a.tokens, last - p0), tiles = (np * a.terms + 7) / 8;
+      if (!a.resident) {
+        __syncthreads();
+        stage(np, [&](int j) { return (int64_t)(DOWN ? sorted.pair[p0 + j] : sorted.pair[p0 + j] / a.k); });
+        __syncthreads();
       }
-      __syncthreads();
-      for (int base = begin; base < end; base += n_group) {
-        const int u = base + group;
-        float acc[TILES_MAX][4] = {};
-        for (int step = 0; step < steps; ++step) {
-          copy_wait<DEPTH - 2>();
-          load_next();  // into the slot of the step before
-          const int ch = member + step * S;
-          if (u < end && ch < chunks) {
-            const uint32_t at = ring + slot * W::SLOT;
-            if (cols <= 8) expert_chunk<1>(w, at, u, ch, xs, a.row_stride, cols, lane, acc);
-            else if (cols <= 16) expert_chunk<2>(w, at, u, ch, xs, a.row_stride, cols, lane, acc);
-            else expert_chunk<3>(w, at, u, ch, xs, a.row_stride, cols, lane, acc);
-          }
-          slot = slot + 1 == DEPTH ? 0 : slot + 1;
-        }
-        float* mine = part + warp * part_step;
-        if (cols <= 8) store_part<1>(mine, lane, reinterpret_cast<float (&)[1][4]>(acc));
-        else if (cols <= 16) store_part<2>(mine, lane, reinterpret_cast<float (&)[2][4]>(acc));
-        else store_part<3>(mine, lane, acc);
-        group_sync(group, S);
-        if (u < end) {
-          const float* sums = part + group * S * part_step;
-          const int at = (u - e * slabs) * (DOWN ? ROWS : 8);
-          for (int i = member * 32 + lane; i < np * (DOWN ? ROWS : 8); i += S * 32) {
-            const int j = DOWN ? i / ROWS : i / 8, row = DOWN ? i % ROWS : i % 8;
-            float v = sum_part(sums, part_step, S, a.terms, j, row);
-            if (!DOWN) v = silu_mul(v, sum_part(sums, part_step, S, a.terms, j, row + 8));
-            a.to[(int64_t)sorted.pair[p0 + j] * a.rows + at + row] = v;
-          }
-        }
-        group_sync(group, S);
-      }
+      if (tiles == 1) expert_block<DOWN, 1>(w, a, sorted, loader, ring, part, scale, rows, begin, end, e * slabs, p0, np);
+      else if (tiles == 2) expert_block<DOWN, 2>(w, a, sorted, loader, ring, part, scale, rows, begin, end, e * slabs, p0, np);
+      else expert_block<DOWN, 3>(w, a, sorted, loader, ring, part, scale, rows, begin, end, e * slabs, p0, np);
     }
     begin = end;
   }
@@ -259,37 +287,45 @@ cudaError_t launch(const W& w, int64_t stride, ExpertArgs a, cudaStream_t s) {
   int sms = 0;
   cudaError_t err = sm_count(&sms);
   if (err != cudaSuccess) return err;
-  const int sorted = sorted_bytes(a.E, a.T * a.k);
+  const int sorted = sorted_bytes(a.E, a.T * a.k), most = DOWN ? a.T * a.k : a.T;
   a.row_stride = row_bytes(a.columns);
-  // as many tokens at once as fit with their sums, of the pairs one expert can have
-  const int most = a.T * a.k;
-  auto bytes = [&](int tokens) {
-    return (size_t)WARPS * DEPTH * W::SLOT + sizeof(float) * WARPS * ((tokens * a.terms + 7) / 8 * 8) * PART_STRIDE +
-           (size_t)tokens * a.terms * a.row_stride + sorted;
+  a.scale_stride = ((a.columns + CHUNK - 1) / CHUNK + 3) / 4 * 4;
+  a.depth = 4;
+  a.tokens = 8 * TILES_MAX / a.terms < a.T * a.k ? 8 * TILES_MAX / a.terms : a.T * a.k;
+  auto bytes = [&]() {
+    a.part_cols = (a.tokens * a.terms + 7) / 8 * 8;
+    return (size_t)WARPS * a.depth * W::SLOT + sizeof(float) * (WARPS * a.part_cols * PART_STRIDE + (size_t)a.staged * a.scale_stride) +
+           (size_t)a.staged * a.terms * a.row_stride + sorted;
   };
-  a.tokens = 1;
-  while (a.tokens < most && (a.tokens + 1) * a.terms <= 8 * TILES_MAX && bytes(a.tokens + 1) <= SMEM_MAX - 1024) ++a.tokens;
-  a.part_cols = (a.tokens * a.terms + 7) / 8 * 8;
-  err = allow_smem<experts_kernel<DOWN, W>>(SMEM_MAX - 1024);
+  a.staged = most;
+  a.resident = bytes() <= SMEM_MAX;
+  if (!a.resident)  // as many of a block's as fit; one always does
+    for (;; --a.tokens) {
+      a.staged = a.tokens;
+      if (bytes() <= SMEM_MAX) break;
+    }
+  err = allow_smem<experts_kernel<DOWN, W>>(SMEM_MAX);
   if (err != cudaSuccess) return err;
   STRATA_LAUNCH(DOWN ? KID_Q4_DOWN : KID_Q4_GATE_UP, s,
-                err = launch_pdl(experts_kernel<DOWN, W>, sms, THREADS, bytes(a.tokens), s, w, stride, a));
+                err = launch_pdl(experts_kernel<DOWN, W>, sms, THREADS, bytes(), s, w, stride, a));
   return err;
+}
+
+template <bool DOWN, int GROUP>
+cudaError_t launch_scales(const strata_q4_t& q, const uint8_t* p, int64_t slab, int64_t stride, const ExpertArgs& a, cudaStream_t s) {
+  if (q.scale_type == STRATA_F16)
+    return q.zeros ? launch<DOWN>(Q4<GROUP, true, true>{p, slab, q.d_in}, stride, a, s)
+                   : launch<DOWN>(Q4<GROUP, false, true>{p, slab, q.d_in}, stride, a, s);
+  return q.zeros ? launch<DOWN>(Q4<GROUP, true, false>{p, slab, q.d_in}, stride, a, s)
+                 : launch<DOWN>(Q4<GROUP, false, false>{p, slab, q.d_in}, stride, a, s);
 }
 
 template <bool DOWN>
 cudaError_t launch_format(const strata_q4_t& q, const void* w, int64_t stride, const ExpertArgs& a, cudaStream_t s) {
   const int64_t slab = slab_bytes(q.d_in, q.group, q.zeros != 0);
   const uint8_t* p = (const uint8_t*)w;
-  const bool f16 = q.scale_type == STRATA_F16;
-  if (q.group == 32)
-    return q.zeros ? launch<DOWN>(Q4<32, true>{p, slab, q.d_in, f16}, stride, a, s)
-                   : launch<DOWN>(Q4<32, false>{p, slab, q.d_in, f16}, stride, a, s);
-  if (q.group == 64)
-    return q.zeros ? launch<DOWN>(Q4<64, true>{p, slab, q.d_in, f16}, stride, a, s)
-                   : launch<DOWN>(Q4<64, false>{p, slab, q.d_in, f16}, stride, a, s);
-  return q.zeros ? launch<DOWN>(Q4<128, true>{p, slab, q.d_in, f16}, stride, a, s)
-                 : launch<DOWN>(Q4<128, false>{p, slab, q.d_in, f16}, stride, a, s);
+  if (q.group == 32) return launch_scales<DOWN, 32>(q, p, slab, stride, a, s);
+  return q.group == 64 ? launch_scales<DOWN, 64>(q, p, slab, stride, a, s) : launch_scales<DOWN, 128>(q, p, slab, stride, a, s);
 }
 
 }  // namespace
@@ -304,11 +340,14 @@ cudaError_t launch_q4_experts(const strata_q4_experts_t& ex, const int32_t* ids,
   ExpertArgs a{};
   a.ids = ids, a.weights = weights, a.bad = (int*)scratch, a.status = status;
   a.T = T, a.k = ex.top_k, a.E = ex.n_expert;
-  a.x = x, a.x_stride = ex.x_stride, a.x_type = ex.x_type, a.terms = terms_of(ex.x_type);
+  a.x = x, a.x_stride = ex.x_stride, a.x_type = ex.x_type, a.terms = terms_of(ex.x_type, true);
   a.to = h, a.columns = d_model, a.rows = d_ff;
   cudaError_t err = launch_format<false>(ex.gate_up_q4, ex.gate_up, ex.gate_up_stride, a, s);
   if (err != cudaSuccess) return err;
-  a.x = h, a.x_stride = d_ff, a.x_type = STRATA_F32, a.terms = ex.out_type == STRATA_F32 ? 3 : 2;
+  a.x = h, a.x_stride = d_ff, a.x_type = STRATA_F32;
+  // one fp16 term (11 bits, an error of 2^-11 where the sum of many such is rounded to 8 bits) for a bf16 result, two for the others
+  a.terms = ex.out_type == STRATA_BF16 ? 1 : 2;
+ 
   a.to = parts, a.columns = d_ff, a.rows = d_model;
   err = launch_format<true>(ex.down_q4, ex.down, ex.down_stride, a, s);
   if (err != cudaSuccess) return err;

@@ -97,12 +97,21 @@ def additions(d_in, group):
     return 2 * (group // 16) + d_in // group + 48
 
 
+def held(x, bits):
+    """How far x [T][n] may be off when each row's 128 columns are held with `bits` bits, down to 2^-40 of the largest (half a step)."""
+    T, n = x.shape
+    full = np.zeros((T, -(-n // 128) * 128))
+    full[:, :n] = np.abs(x)
+    top = np.repeat(full.reshape(T, -1, 128).max(2), 128, 1)[:, :n]
+    return 2.0 ** -bits * np.abs(x) + 2.0 ** -39 * top
+
+
 def product(x, x_err, w, adds):
     """x w^T [T][n] in 64 bits, and how far fp32 may be off it when x is off by x_err."""
     return x @ w.T, x_err @ np.abs(w).T + adds * 2 * U * ((np.abs(x) + x_err) @ np.abs(w).T)
 
 
-def experts(x, gate_up, down, ids, weights, out_kind):
+def experts(x, gate_up, down, ids, weights, out_kind, x_kind=qre.F32):
     """out [T][d_model] in 64 bits and how far fp32 may be off; x [T][d_model]."""
     T, k = ids.shape
     d_ff, n = down.d_in, down.n_out
@@ -112,15 +121,14 @@ def experts(x, gate_up, down, ids, weights, out_kind):
         t, i = np.nonzero((ids == e) & (weights != 0))
         if len(t) == 0:
             continue
-        gu, gu_err = product(x[t], np.zeros_like(x[t]), gate_up.weights(int(e)), additions(gate_up.d_in, gate_up.group))
+        gu, gu_err = product(x[t], held(x[t], 22 if x_kind == qre.F32 else 60), gate_up.weights(int(e)), additions(gate_up.d_in, gate_up.group))
         g, u, g_err, u_err = gu[:, :d_ff], gu[:, d_ff:], gu_err[:, :d_ff], gu_err[:, d_ff:]
         with np.errstate(over="ignore"):
             silu = g / (1.0 + np.exp(-g))
         h = silu * u
         # |silu'| < 1.1; an exponential (4 u), a sum, a quotient, a product
         h_err = 1.1 * g_err * (np.abs(u) + u_err) + np.abs(silu) * u_err + 8 * U * np.abs(h)
-        if out_kind != qre.F32:
-            h_err = h_err + 2.0 ** -16 * np.abs(h)  # held in two bf16 terms
+        h_err = h_err + held(h, 11 if out_kind == qre.BF16 else 22)
         part, part_err = product(h, h_err, down.weights(int(e)), additions(down.d_in, down.group))
         w = weights[t, i][:, None]
         np.add.at(out, t, w * part)
