@@ -25,78 +25,83 @@ struct LinearArgs {
   int part_cols;      // term columns of a block, rounded up to whole tiles
 };
 
+// The chunks a warp will need, unit after unit, ahead of the products.
+template <class W>
+struct Loader {
+  const W& w;
+  const Share& share;
+  int S, member, units, pass;
+  int unit, left;  // the unit's chunks left
+  const uint8_t* at;
+
+  __device__ __forceinline__ void start(int u, int lane) {
+    unit = u;
+    left = u < units ? share.whole + share.tail : 0;
+    at = w.at(u, member, lane);
+  }
+  __device__ __forceinline__ void next(Ring& ring, int lane) {
+    if (left) {
+      const uint32_t slot = ring.next_fill();
+      const int ch = member + (share.whole + share.tail - left) * S;
+      if (left == 1 && share.tail) w.load_tail(slot, at, unit, ch, lane);
+      else w.load(slot, at, unit, ch, lane);
+      at += S * W::BYTES;
+      if (--left == 0) start(unit + pass, lane);
+    }
+    copy_commit();
+  }
+};
+
 // The units of this CTA for one block of tokens.
 template <int NT, class W>
 __device__ __forceinline__ void linear_block(const W& w, const LinearArgs& a, char* smem, int t0, int nt) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int S = a.split, group = warp / S, member = warp % S, n_group = WARPS / S;
   const int units = (a.rows + ROWS - 1) / ROWS, chunks = (a.columns + W::COLUMNS - 1) / W::COLUMNS;
-  const int steps = (chunks + S - 1) / S;  // of a unit
+  const Share share(a.columns, W::COLUMNS, chunks, member, S);
   const int first = blockIdx.x * n_group, pass = gridDim.x * n_group;
-  const int rounds = first < units ? (units - first + pass - 1) / pass : 0;
   const int cols = nt * a.terms;
 
-  Ring ring{smem_u32(smem) + warp * (a.depth * W::SLOT), a.depth, 0, 0, W::SLOT};
+  Ring ring(smem_u32(smem) + warp * (a.depth * W::SLOT), a.depth, W::SLOT);
   float* part = reinterpret_cast<float*>(smem + WARPS * a.depth * W::SLOT);
   const int part_step = a.part_cols * PART_STRIDE;
   float* scale = part + WARPS * part_step;
   char* rows = reinterpret_cast<char*>(scale + a.tokens * a.scale_stride);
 
-  // the chunks this warp will need, in the order of the loops below
-  int l_unit = first + group, l_step = 0;
-  const uint8_t* l_at = w.at(l_unit, member, lane);
-  auto load_next = [&]() {
-    const uint32_t slot = ring.next_fill();
-    if (l_unit < units) {
-      const int ch = member + l_step * S;
-      if (ch < chunks) w.load(slot, l_at, l_unit, ch, lane);
-      l_at += S * W::BYTES;
-      if (++l_step == steps) {
-        l_step = 0;
-        l_unit += pass;
-        l_at = w.at(l_unit, member, lane);
-      }
-    }
-    copy_commit();
-  };
-  for (int i = 0; i < a.depth - 1; ++i) load_next();
+  Loader<W> loader{w, share, S, member, units, pass};
+  loader.start(first + group, lane);
+  for (int i = 0; i < a.depth - 1; ++i) loader.next(ring, lane);
 
-  uint32_t b[NT];
-  uint2 cs[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {  // columns behind the last read some row; their sums are not used
-    b[t] = smem_u32(rows) + min(8 * t + (lane >> 2), cols - 1) * a.row_stride + (lane & 3) * 16;
-    const int c = 8 * t + 2 * (lane & 3);
-    cs[t].x = smem_u32(scale + min(c, cols - 1) / a.terms * a.scale_stride);
-    cs[t].y = smem_u32(scale + min(c + 1, cols - 1) / a.terms * a.scale_stride);
-  }
   const int panel_steps = a.panel / S;
   const bool panels = a.panel < chunks;
-  for (int round = 0; round < rounds; ++round) {
-    const int u = first + group + round * pass;
+  for (int base = first; base < units; base += pass) {
+    const int u = base + group;
     float acc[NT][4] = {};
-    int panel_first = 0, panel_left = 0;
-    for (int step = 0; step < steps; ++step) {
-      if (panel_left == 0) {
-        panel_left = panel_steps, panel_first = step * S;
-        if (panels || round == 0) {  // activations of the panel
-          const int c0 = panel_first * W::COLUMNS, c1 = min(c0 + a.panel * W::COLUMNS, (a.columns + BLOCK - 1) / BLOCK * BLOCK);
-          const int halves = 2 * WARPS / min(nt, 2 * WARPS);  // half warps to a token
-          const int half = threadIdx.x >> 4;
-          __syncthreads();
-          if (half < halves * nt)
-            for (int t = half / halves; t < nt; t += 2 * WARPS / halves)
-              stage_row<W::F16>(a.x, (t0 + t) * a.x_stride, a.x_type, a.columns, c0, c1, a.terms, rows + t * a.terms * a.row_stride,
-                                a.row_stride, scale + t * a.scale_stride, half % halves, halves);
-          __syncthreads();
-        }
+    for (int ch0 = 0, done = 0; ch0 < chunks; ch0 += a.panel, done += panel_steps) {
+      if (panels || base == first) {  // activations of the panel
+        const int c0 = ch0 * W::COLUMNS, c1 = min(c0 + a.panel * W::COLUMNS, (a.columns + BLOCK - 1) / BLOCK * BLOCK);
+        const int halves = 2 * WARPS / min(nt, 2 * WARPS);  // half warps to a token
+        const int half = threadIdx.x >> 4;
+        __syncthreads();
+        if (half < halves * nt)
+          stage_row<W::F16>(a.x, (t0 + half / halves) * a.x_stride, a.x_type, a.columns, c0, c1, a.terms,
+                            rows + half / halves * a.terms * a.row_stride, a.row_stride, scale + half / halves * a.scale_stride, half % halves,
+                            halves);
+        __syncthreads();
       }
-      --panel_left;
-      ring.wait();
-      load_next();  // into the slot of the step before
-      const uint32_t slot = ring.next_use();
-      const int ch = member + step * S;
-      if (u < units && ch < chunks) chunk_products<NT>(w, slot, ch, ch - panel_first, b, cs, lane, acc);
+      uint32_t b[NT];
+      uint2 cs[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {  // columns behind the last read some row; their sums are not used
+        b[t] = smem_u32(rows) + min(8 * t + (lane >> 2), cols - 1) * a.row_stride + (lane & 3) * 16 + member * 2 * W::COLUMNS;
+        const int c = 8 * t + 2 * (lane & 3);
+        cs[t].x = smem_u32(scale + min(c, cols - 1) / a.terms * a.scale_stride + member);
+        cs[t].y = smem_u32(scale + min(c + 1, cols - 1) / a.terms * a.scale_stride + member);
+      }
+      if (u < units) {
+        const int whole = min(panel_steps, share.whole - done);
+        run_chunks<NT>(w, ring, loader, whole, share.tail && done + panel_steps > share.whole && done <= share.whole, S, b, cs, lane, acc);
+      }
     }
     store_part<NT>(part + warp * part_step, lane, acc);
     group_sync(group, S);

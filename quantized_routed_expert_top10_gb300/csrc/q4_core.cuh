@@ -143,21 +143,19 @@ struct Q4 {
 
   // Where this lane's part of chunk ch of slab s begins; the next chunk is BYTES further.
   __device__ __forceinline__ const uint8_t* at(int64_t s, int ch, int lane) const { return base + s * slab + ch * BYTES + lane * 16; }
-  __device__ __forceinline__ void load(uint32_t slot, const uint8_t* p, int64_t, int ch, int lane) const {
-    const int left = columns - ch * CHUNK;
-    if (left >= CHUNK) {
-      copy_async<16>(slot + lane * 16, p);
-      copy_async<16>(slot + 512 + lane * 16, p + 512);
-      if (lane < META / 16) copy_async<16>(slot + 1024 + lane * 16, p + 1024);
-    } else {
-      const int nb = left / BLOCK;
-      p -= lane * 16;
-      for (int b = 0; b < nb; ++b) {
-        copy_async<4>(slot + lane * 16 + 4 * b, p + (lane * nb + b) * 4);
-        copy_async<4>(slot + 512 + lane * 16 + 4 * b, p + 128 * nb + (lane * nb + b) * 4);
-      }
-      if (lane < META / 16) copy_async<16>(slot + 1024 + lane * 16, p + 256 * nb + lane * 16);
+  __device__ __forceinline__ void load(uint32_t slot, const uint8_t* p, int64_t, int, int lane) const {
+    copy_async<16>(slot + lane * 16, p);
+    copy_async<16>(slot + 512 + lane * 16, p + 512);
+    if (lane < META / 16) copy_async<16>(slot + 1024 + lane * 16, p + 1024);
+  }
+  __device__ __forceinline__ void load_tail(uint32_t slot, const uint8_t* p, int64_t, int, int lane) const {
+    const int nb = columns % CHUNK / BLOCK;
+    p -= lane * 16;
+    for (int b = 0; b < nb; ++b) {
+      copy_async<4>(slot + lane * 16 + 4 * b, p + (lane * nb + b) * 4);
+      copy_async<4>(slot + 512 + lane * 16 + 4 * b, p + 128 * nb + (lane * nb + b) * 4);
     }
+    if (lane < META / 16) copy_async<16>(slot + 1024 + lane * 16, p + 256 * nb + lane * 16);
   }
 
   // acc[tile] += chunk x columns.  b[tile]: shared address of this lane's operand row at the chunk's first column; cs[tile]: the scales of
@@ -267,6 +265,9 @@ struct Bf16 {
     const int64_t row = s * ROWS + (lane >> 2);
     return base + 2 * ((row < rows ? row : 0) * stride) + ch * BYTES + (lane & 3) * 16;
   }
+  __device__ __forceinline__ void load_tail(uint32_t slot, const uint8_t* p, int64_t s, int ch, int lane) const {
+    load(slot, p, s, ch, lane);
+  }
   __device__ __forceinline__ void load(uint32_t slot, const uint8_t* p, int64_t s, int ch, int lane) const {
     const uint8_t* q = s * ROWS + (lane >> 2) + 8 < rows ? p + 16 * stride : p;
 #pragma unroll
@@ -300,48 +301,69 @@ struct Bf16 {
   }
 };
 
-// A warp's ring of `depth` chunks: filled `depth` - 1 ahead, one group of copies a step whether or not it copies anything.
+// A warp's ring of `depth` (3 or 4) chunks: filled `depth` - 1 ahead, one group of copies a chunk used, empty when none is left.
 struct Ring {
-  uint32_t at;
-  int depth, fill, use, slot_bytes;
+  uint32_t at, end, fill, use;  // shared addresses
+  int depth, slot;              // bytes of a slot
+  __device__ __forceinline__ Ring(uint32_t a, int d, int bytes) : at(a), end(a + d * bytes), fill(a), use(a), depth(d), slot(bytes) {}
   __device__ __forceinline__ uint32_t next_fill() {
-    const uint32_t a = at + fill * slot_bytes;
-    fill = fill + 1 == depth ? 0 : fill + 1;
+    const uint32_t a = fill;
+    fill = fill + slot == end ? at : fill + slot;
     return a;
   }
   __device__ __forceinline__ uint32_t next_use() {
-    const uint32_t a = at + use * slot_bytes;
-    use = use + 1 == depth ? 0 : use + 1;
+    const uint32_t a = use;
+    use = use + slot == end ? at : use + slot;
     return a;
   }
   __device__ __forceinline__ void wait() const {  // for the oldest; its scales were copied by other lanes
     if (depth == 4) copy_wait<2>();
-    else if (depth == 3) copy_wait<1>();
-    else copy_wait<0>();
+    else copy_wait<1>();
     __syncwarp();
   }
 };
 
-// One chunk's products: rows[tile] and scales[tile] are this lane's shared addresses for the activations' first column and chunk.
-template <int NT, class W>
-__device__ __forceinline__ void chunk_products(const W& w, uint32_t slot, int ch, int staged_ch, const uint32_t (&rows)[NT],
-                                               const uint2 (&scales)[NT], int lane, float (&acc)[NT][4]) {
-  uint32_t b[NT];
-  float2 cs[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    b[t] = rows[t] + staged_ch * (2 * W::COLUMNS);
-    cs[t] = make_float2(1.f, 1.f);
-    if (W::F16) {
-      cs[t].x = __uint_as_float(lds4(scales[t].x + staged_ch * 4));
-      cs[t].y = __uint_as_float(lds4(scales[t].y + staged_ch * 4));
-    }
+// A warp's share of a unit: chunks member, member + S, ...; the last of the unit may be a shorter one.
+struct Share {
+  int whole;  // its whole chunks
+  bool tail;  // and the shorter one
+  __device__ __forceinline__ Share(int columns, int chunk, int chunks, int member, int S) {
+    const bool cut = (columns + BLOCK - 1) / BLOCK % (chunk / BLOCK) != 0;  // bf16 columns end anywhere: whole when its last block has begun
+    tail = cut && (chunks - 1) % S == member;
+    whole = (chunks - member + S - 1) / S - (tail ? 1 : 0);
+    if (chunks <= member) whole = 0, tail = false;
   }
-  // columns of bf16 weights end anywhere: a chunk is whole when its last block has begun
-  const int left = (w.columns - ch * W::COLUMNS + BLOCK - 1) / BLOCK;
-  if (left >= W::COLUMNS / BLOCK) w.template products<NT>(slot, b, cs, lane, acc);
-  else w.template tail<NT>(slot, left, b, cs, lane, acc);
+};
+
+// Products of the next `whole` chunks of the ring, then of a shorter one.  b[tile] and cs[tile] are this lane's shared addresses for the
+// activations of the first of them; one chunk of this warp to the next is S of the unit's.
+template <int NT, class W, class L>
+__device__ __forceinline__ void run_chunks(const W& w, Ring& ring, L& loader, int whole, bool tail, int S, uint32_t (&b)[NT], uint2 (&cs)[NT],
+                                           int lane, float (&acc)[NT][4]) {
+  auto scales = [&](float2 (&v)[NT]) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      if (W::F16) v[t] = make_float2(__uint_as_float(lds4(cs[t].x)), __uint_as_float(lds4(cs[t].y)));
+  };
+  float2 v[NT];
+#pragma unroll 1
+  for (int i = 0; i < whole; ++i) {
+    ring.wait();
+    loader.next(ring, lane);  // into the slot of the chunk before
+    scales(v);
+    w.template products<NT>(ring.next_use(), b, v, lane, acc);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) b[t] += S * 2 * W::COLUMNS, cs[t].x += 4 * S, cs[t].y += 4 * S;
+  }
+  if (tail) {
+    ring.wait();
+    loader.next(ring, lane);
+    scales(v);
+    w.template tail<NT>(ring.next_use(), (w.columns + BLOCK - 1) / BLOCK % (W::COLUMNS / BLOCK), b, v, lane, acc);
+  }
 }
+// Of the calling thread's warp, known to be the same for all its lanes.
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0); }
 
 // A warp's sums to its place in shared memory, [column][16 rows].
 template <int NT>

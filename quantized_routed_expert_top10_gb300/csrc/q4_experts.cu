@@ -49,6 +49,36 @@ __device__ __forceinline__ Sorted sort_pairs(char* smem, const ExpertArgs& a) {
   s.off = s.expert + a.E;
   s.pair = s.off + a.E + 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pairs = a.T * a.k;
+  if (pairs <= 32) {  // one warp, a pair a lane; an expert's first pair stands for it
+    if (warp == 0) {
+      const int e = lane < pairs ? a.ids[lane] : -1;
+      const bool have = e >= 0 && e < a.E && a.weights[lane] != 0.f;
+      const uint32_t same = __match_any_sync(0xffffffffu, have ? e : -1), before = (1u << lane) - 1u;
+      const bool first = have && (same & before) == 0;
+      const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+      const int count = first ? __popc(same) : 0;
+      int off = count;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int up = __shfl_up_sync(0xffffffffu, off, o);
+        if (lane >= o) off += up;
+      }
+      off -= count;
+      const int mine = __shfl_sync(0xffffffffu, off, __ffs(same) - 1);
+      if (first) s.expert[__popc(firsts & before)] = e, s.off[__popc(firsts & before)] = off;
+      if (have) s.pair[mine + __popc(same & before)] = lane;
+      const int bad = __any_sync(0xffffffffu, lane < pairs && (e < -1 || e >= a.E));
+      const int all = __popc(__ballot_sync(0xffffffffu, have));
+      if (lane == 0) {
+        warp_sum[0] = __popc(firsts), warp_sum[1] = bad;
+        s.off[__popc(firsts)] = all;
+      }
+    }
+    __syncthreads();
+    s.n = warp_sum[0];
+    s.bad = warp_sum[1];
+    return s;
+  }
   for (int e = tid; e < a.E; e += THREADS) count[e] = 0;
   __syncthreads();
   int id[4], rank[4];
@@ -101,41 +131,40 @@ __device__ __forceinline__ Sorted sort_pairs(char* smem, const ExpertArgs& a) {
 template <class W>
 struct Loader {
   const Sorted& sorted;
-  const W& w;
+  const Share& share;
   int64_t expert_stride;
-  int slabs, chunks, steps, S, member, group, n_group, u1, tokens;
-  int begin, end, left;  // the expert's stretch, its blocks left
-  int u, step;
+  int slabs, S, member, group, n_group, u1, tokens;
+  int begin, end, blocks;  // the expert's stretch, its blocks left
+  int u, left;             // this warp's unit, its chunks left
   const uint8_t* at;
-  W we;                  // the expert's matrix
+  W w;                     // the expert's matrix, from the first unit's place
+  const uint8_t* base;     // of expert 0
 
-  __device__ __forceinline__ void expert(int lane) {
+  // The next expert (true) or block with a unit for this warp, from the unit base on.
+  __device__ __forceinline__ void expert() {
     begin = end;
     if (begin >= u1) return;
     const int e = begin / slabs;
     end = min(u1, (e + 1) * slabs);
-    left = (sorted.off[e + 1] - sorted.off[e] + tokens - 1) / tokens;
-    we = w;
-    we.base += sorted.expert[e] * expert_stride - (int64_t)e * slabs * w.slab;
-    start(begin, lane);
+    blocks = (sorted.off[e + 1] - sorted.off[e] + tokens - 1) / tokens;
+    w.base = base + sorted.expert[e] * expert_stride - (int64_t)e * slabs * w.slab;
   }
-  __device__ __forceinline__ void start(int base, int lane) {
-    u = base + group;
-    step = 0;
-    at = we.at(u, member, lane);
+  __device__ __forceinline__ void find(int from, int lane) {  // the first unit of this warp in the CTA's units from `from` on
+    u = from + group;
+    while (u >= end && begin < u1) {
+      if (--blocks == 0) expert();
+      u = begin + group;
+    }
+    left = begin < u1 ? share.whole + share.tail : 0;
+    if (left) at = w.at(u, member, lane);
   }
   __device__ __forceinline__ void next(Ring& ring, int lane) {
-    const uint32_t slot = ring.next_fill();
-    if (begin < u1) {
-      const int ch = member + step * S;
-      if (u < end && ch < chunks) we.load(slot, at, u, ch, lane);
+    if (left) {
+      const uint32_t slot = ring.next_fill();
+      if (left == 1 && share.tail) w.load_tail(slot, at, u, 0, lane);
+      else w.load(slot, at, u, 0, lane);
       at += S * W::BYTES;
-      if (++step == steps) {
-        const int base = u - group + n_group;
-        if (base < end) start(base, lane);
-        else if (--left) start(begin, lane);
-        else expert(lane);
-      }
+      if (--left == 0) find(u - group + n_group, lane);
     }
     copy_commit();
   }
@@ -145,11 +174,11 @@ struct Loader {
 template <bool DOWN, int NT, class W>
 __device__ __forceinline__ void expert_block(const W& w, const ExpertArgs& a, const Sorted& sorted, Loader<W>& loader, Ring& ring, float* part,
                                              const float* scale, const char* rows, int begin, int end, int first_unit, int p0, int np) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int S = loader.S, group = loader.group, member = loader.member;
   const int part_step = a.part_cols * PART_STRIDE;
-  uint32_t b[NT];
-  uint2 cs[NT];
+  uint32_t b0[NT];
+  uint2 cs0[NT];
   auto row_of = [&](int j) {  // of pair j of the block among those in shared memory
     j = min(j, np - 1);       // columns behind the last read some row; their sums are not used
     return !a.resident ? j : DOWN ? p0 + j : sorted.pair[p0 + j] / a.k;
@@ -157,20 +186,20 @@ __device__ __forceinline__ void expert_block(const W& w, const ExpertArgs& a, co
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int c = 8 * t + (lane >> 2), j = c / a.terms;
-    b[t] = smem_u32(rows) + (row_of(j) * a.terms + (c - j * a.terms)) * a.row_stride + (lane & 3) * 16;
+    b0[t] = smem_u32(rows) + (row_of(j) * a.terms + (c - j * a.terms)) * a.row_stride + (lane & 3) * 16 + member * 2 * W::COLUMNS;
     const int c2 = 8 * t + 2 * (lane & 3);
-    cs[t].x = smem_u32(scale + row_of(c2 / a.terms) * a.scale_stride);
-    cs[t].y = smem_u32(scale + row_of((c2 + 1) / a.terms) * a.scale_stride);
+    cs0[t].x = smem_u32(scale + row_of(c2 / a.terms) * a.scale_stride + member);
+    cs0[t].y = smem_u32(scale + row_of((c2 + 1) / a.terms) * a.scale_stride + member);
   }
   for (int base = begin; base < end; base += loader.n_group) {
     const int u = base + group;
     float acc[NT][4] = {};
-    for (int step = 0; step < loader.steps; ++step) {
-      ring.wait();
-      loader.next(ring, lane);  // into the slot of the step before
-      const uint32_t slot = ring.next_use();
-      const int ch = member + step * S;
-      if (u < end && ch < loader.chunks) chunk_products<NT>(w, slot, ch, ch, b, cs, lane, acc);
+    if (u < end) {
+      uint32_t b[NT];
+      uint2 cs[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) b[t] = b0[t], cs[t] = cs0[t];
+      run_chunks<NT>(w, ring, loader, loader.share.whole, loader.share.tail, S, b, cs, lane, acc);
     }
     store_part<NT>(part + warp * part_step, lane, acc);
     group_sync(group, S);
@@ -193,7 +222,7 @@ __global__ void __launch_bounds__(THREADS, 1) experts_kernel(W w, int64_t expert
   extern __shared__ __align__(128) char smem[];
   if (!DOWN) griddep_wait();
   griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   float* part = reinterpret_cast<float*>(smem + WARPS * a.depth * W::SLOT);
   float* scale = part + WARPS * a.part_cols * PART_STRIDE;
   char* rows = reinterpret_cast<char*>(scale + a.staged * a.scale_stride);
@@ -209,11 +238,14 @@ __global__ void __launch_bounds__(THREADS, 1) experts_kernel(W w, int64_t expert
 
   const int slabs = DOWN ? a.rows / ROWS : a.rows / 8, chunks = (a.columns + CHUNK - 1) / CHUNK;
   const int units = sorted.n * slabs;
-  const int u0 = (int)((int64_t)blockIdx.x * units / gridDim.x), u1 = (int)((int64_t)(blockIdx.x + 1) * units / gridDim.x);
-  const int S = choose_split((units + gridDim.x - 1) / gridDim.x, chunks);
-  Ring ring{smem_u32(smem) + warp * (a.depth * W::SLOT), a.depth, 0, 0, W::SLOT};
-  Loader<W> loader{sorted, w, expert_stride, slabs, chunks, (chunks + S - 1) / S, S, warp % S, warp / S, WARPS / S, u1, a.tokens, u0, u0};
-  loader.expert(lane);
+  // 2^20 units at most (1,024 experts of 1,024 slabs): 32 bits hold their products with the grid
+  const int u0 = (unsigned)(blockIdx.x * units) / gridDim.x, u1 = (unsigned)((blockIdx.x + 1) * units) / gridDim.x;
+  const int S = choose_split((unsigned)(units + gridDim.x - 1) / gridDim.x, chunks);
+  const Share share(a.columns, CHUNK, chunks, warp % S, S);
+  Ring ring(smem_u32(smem) + warp * (a.depth * W::SLOT), a.depth, W::SLOT);
+  Loader<W> loader{sorted, share, expert_stride, slabs, S, warp % S, warp / S, WARPS / S, u1, a.tokens, u0, u0, 0, 0, 0, nullptr, w, w.base};
+  loader.expert();
+  loader.find(u0, lane);
   for (int i = 0; i < a.depth - 1; ++i) loader.next(ring, lane);
   if (DOWN) griddep_wait();  // h
 
