@@ -291,11 +291,9 @@ const char* strata_status_str(strata_status s);
 #define STRATA_KERNEL_ADAPTER_EXPAND 21  /* strata_moe_adapters: base + scale * B_a (A_a x) */
 #define STRATA_KERNEL_ADAPTERS 22        /* strata_moe_adapters, short segments: both */
 #define STRATA_KERNEL_LINEAR 23          /* strata_moe_linear */
-#define STRATA_KERNEL_Q4_GATE_UP 24      /* strata_moe_q4_experts: gate, up and SwiGLU */
-#define STRATA_KERNEL_Q4_DOWN 25         /* strata_moe_q4_experts: down */
-#define STRATA_KERNEL_Q4_COMBINE 26      /* strata_moe_q4_experts: the weighted sum */
-#define STRATA_KERNEL_PACK_Q4 27         /* strata_pack_q4_device */
-#define STRATA_KERNEL_COUNT 28
+#define STRATA_KERNEL_Q4_EXPERTS 24      /* strata_moe_q4_experts, one cooperative launch */
+#define STRATA_KERNEL_PACK_Q4 25         /* strata_pack_q4_device */
+#define STRATA_KERNEL_COUNT 26
 
 /* Number of kernels this process has launched through the library so far (all threads). */
 uint64_t strata_moe_launch_count(void);

@@ -253,7 +253,7 @@ typedef struct strata_q4_experts {
   int64_t gate_up_stride;  /* bytes, multiples of 16, at least the packed matrix */
   int64_t down_stride;
   strata_q4_t gate_up_q4;  /* n_out = 2 * d_ff, d_in = d_model, paired */
-  strata_q4_t down_q4;     /* n_out = d_model, d_in = d_ff; d_model and d_ff at most 8192 */
+  strata_q4_t down_q4;     /* n_out = d_model, d_in = d_ff, at most 8192 each; group, scale_type and zeros as gate_up_q4's */
   int32_t n_expert;        /* in [1, 1024] */
   int32_t top_k;           /* experts of a token, in [1, 32] */
   int32_t x_type;          /* element types */

@@ -502,7 +502,7 @@ def strata_status_str(status: int) -> str:
 KERNELS = ("DECODE_LAYER", "ROUTE_DECODE", "ROUTER_PREP", "ROUTER_TC", "TOP_K", "GROUP_HIST", "GROUP_SCAN",
            "GROUP_SCATTER", "TC_PREPARE", "TC_GATHER",
            "TC_GATEUP", "TC_DOWN", "COMBINE", "PACK", "HOST_COPY", "WAIT_SELFTEST", "BLOB_CRC32", "SELECT", "NORM",
-           "COMBINE_NORM", "ADAPTER_SHRINK", "ADAPTER_EXPAND", "ADAPTERS", "LINEAR", "Q4_GATE_UP", "Q4_DOWN", "Q4_COMBINE", "PACK_Q4")
+           "COMBINE_NORM", "ADAPTER_SHRINK", "ADAPTER_EXPAND", "ADAPTERS", "LINEAR", "Q4_EXPERTS", "PACK_Q4")
 KERNEL_ID = {name: i for i, name in enumerate(KERNELS)}
 
 

@@ -66,7 +66,8 @@ constexpr int WS_SYNC_EPOCH = 32;  // own 128-byte line
 constexpr int WS_SYNC_SMRANK = 64;  // [256] per-SM arrival tickets (which of an SM's CTAs is which)
 constexpr int WS_SYNC_WORDS = WS_SYNC_SMRANK + 256;
 constexpr int WS_NREP = 16;        // replicas of the router dot products (every CTA reads all of them)
-static_assert(WS_SYNC + sizeof(int32_t) * WS_SYNC_WORDS <= WS_HEADER, "decode sync words must fit the header");
+constexpr size_t WS_MEET = 8192;  // uint32 [3] of strata_moe_q4_experts: CTAs that have come to each of its meetings, 0 between calls
+static_assert(WS_SYNC + sizeof(int32_t) * WS_SYNC_WORDS <= WS_MEET && WS_MEET + 128 <= WS_HEADER, "sync words must fit the header");
 // Decode exchange area, right after the header at the same offset for every T >= 1: 64-bit words
 // (value bits, call tag), each written once per call and polled by the CTAs that need it, so a
 // reader learns that a value is there from the value itself.  strata_moe_workspace_init zeroes it;

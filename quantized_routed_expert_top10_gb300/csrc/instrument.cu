@@ -22,8 +22,7 @@ static_assert(KID_DECODE_LAYER == STRATA_KERNEL_DECODE_LAYER && KID_ROUTE_DECODE
                   KID_NORM == STRATA_KERNEL_NORM && KID_COMBINE_NORM == STRATA_KERNEL_COMBINE_NORM &&
                   KID_ADAPTER_SHRINK == STRATA_KERNEL_ADAPTER_SHRINK &&
                   KID_ADAPTER_EXPAND == STRATA_KERNEL_ADAPTER_EXPAND && KID_ADAPTERS == STRATA_KERNEL_ADAPTERS &&
-                  KID_LINEAR == STRATA_KERNEL_LINEAR && KID_Q4_GATE_UP == STRATA_KERNEL_Q4_GATE_UP &&
-                  KID_Q4_DOWN == STRATA_KERNEL_Q4_DOWN && KID_Q4_COMBINE == STRATA_KERNEL_Q4_COMBINE &&
+                  KID_LINEAR == STRATA_KERNEL_LINEAR && KID_Q4_EXPERTS == STRATA_KERNEL_Q4_EXPERTS &&
                   KID_PACK_Q4 == STRATA_KERNEL_PACK_Q4 &&
                   KID_END == STRATA_KERNEL_COUNT,
               "kernel ids of the ABI and the library differ");

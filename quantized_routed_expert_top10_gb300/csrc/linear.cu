@@ -18,7 +18,6 @@ struct LinearArgs {
   int T, columns, rows, x_type, y_type;
   int tokens, terms;  // of a block
   int split;          // warps to a unit
-  int depth;          // chunks in a warp's ring
   int panel;          // chunks whose activations lie in shared memory at once, a multiple of split
   int row_stride;     // bytes between rows of terms
   int scale_stride;   // floats between tokens' scales
@@ -39,12 +38,12 @@ struct Loader {
     left = u < units ? share.whole + share.tail : 0;
     at = w.at(u, member, lane);
   }
-  __device__ __forceinline__ void next(Ring& ring, int lane) {
+  template <class R>
+  __device__ __forceinline__ void next(R& ring, int lane) {
     if (left) {
       const uint32_t slot = ring.next_fill();
       const int ch = member + (share.whole + share.tail - left) * S;
-      if (left == 1 && share.tail) w.load_tail(slot, at, unit, ch, lane);
-      else w.load(slot, at, unit, ch, lane);
+      w.load(slot, at, unit, ch, left == 1 && share.tail, lane);
       at += S * W::BYTES;
       if (--left == 0) start(unit + pass, lane);
     }
@@ -53,7 +52,7 @@ struct Loader {
 };
 
 // The units of this CTA for one block of tokens.
-template <int NT, class W>
+template <int NT, int WARPS, int DEPTH, class W>
 __device__ __forceinline__ void linear_block(const W& w, const LinearArgs& a, char* smem, int t0, int nt) {
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const int S = a.split, group = warp / S, member = warp % S, n_group = WARPS / S;
@@ -62,15 +61,15 @@ __device__ __forceinline__ void linear_block(const W& w, const LinearArgs& a, ch
   const int first = blockIdx.x * n_group, pass = gridDim.x * n_group;
   const int cols = nt * a.terms;
 
-  Ring ring(smem_u32(smem) + warp * (a.depth * W::SLOT), a.depth, W::SLOT);
-  float* part = reinterpret_cast<float*>(smem + WARPS * a.depth * W::SLOT);
+  Ring<DEPTH, W::SLOT> ring(smem_u32(smem) + warp * (DEPTH * W::SLOT));
+  float* part = reinterpret_cast<float*>(smem + WARPS * DEPTH * W::SLOT);
   const int part_step = a.part_cols * PART_STRIDE;
   float* scale = part + WARPS * part_step;
   char* rows = reinterpret_cast<char*>(scale + a.tokens * a.scale_stride);
 
   Loader<W> loader{w, share, S, member, units, pass};
   loader.start(first + group, lane);
-  for (int i = 0; i < a.depth - 1; ++i) loader.next(ring, lane);
+  for (int i = 0; i < DEPTH - 1; ++i) loader.next(ring, lane);
 
   const int panel_steps = a.panel / S;
   const bool panels = a.panel < chunks;
@@ -104,7 +103,7 @@ __device__ __forceinline__ void linear_block(const W& w, const LinearArgs& a, ch
       }
     }
     store_part<NT>(part + warp * part_step, lane, acc);
-    group_sync(group, S);
+    group_sync<WARPS>(group, S);
     if (u < units)
       for (int i = member * 32 + lane; i < nt * ROWS; i += S * 32) {
         const int t = i / ROWS, row = i % ROWS, n = u * ROWS + row;
@@ -114,57 +113,64 @@ __device__ __forceinline__ void linear_block(const W& w, const LinearArgs& a, ch
           store1(a.y, (t0 + t) * a.y_stride + n, a.y_type, v);
         }
       }
-    group_sync(group, S);
+    group_sync<WARPS>(group, S);
   }
   copy_wait<0>();
 }
 
-template <class W>
-__global__ void __launch_bounds__(THREADS, 1) linear_kernel(W w, LinearArgs a) {
+// TILES: of the largest block.
+template <class W, int TILES, int WARPS, int DEPTH>
+__global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) linear_kernel(W w, LinearArgs a) {
   extern __shared__ __align__(128) char smem[];
   griddep_wait();
   griddep_launch_dependents();
   for (int t0 = blockIdx.y * a.tokens; t0 < a.T; t0 += gridDim.y * a.tokens) {
     const int nt = min(a.tokens, a.T - t0), tiles = (nt * a.terms + 7) / 8;
     __syncthreads();
-    if (tiles == 1) linear_block<1>(w, a, smem, t0, nt);
-    else if (tiles == 2) linear_block<2>(w, a, smem, t0, nt);
-    else linear_block<3>(w, a, smem, t0, nt);
+    if (TILES == 1 || tiles == 1) linear_block<1, WARPS, DEPTH>(w, a, smem, t0, nt);
+    else if (tiles == 2) linear_block<2, WARPS, DEPTH>(w, a, smem, t0, nt);
+    else linear_block<3, WARPS, DEPTH>(w, a, smem, t0, nt);
   }
 }
 
-template <class W>
-cudaError_t launch(const W& w, LinearArgs a, cudaStream_t s) {
+template <int TILES, int WARPS, int DEPTH, class W>
+cudaError_t launch_tiles(const W& w, LinearArgs a, cudaStream_t s) {
   const int chunks = (a.columns + W::COLUMNS - 1) / W::COLUMNS, units = (a.rows + ROWS - 1) / ROWS;
   int sms = 0;
   cudaError_t err = sm_count(&sms);
   if (err != cudaSuccess) return err;
-  a.terms = terms_of(a.x_type, W::F16);
-  a.tokens = 8 * TILES_MAX / a.terms < a.T ? 8 * TILES_MAX / a.terms : a.T;
+  a.tokens = 8 * TILES / a.terms < a.T ? 8 * TILES / a.terms : a.T;
   a.part_cols = (a.tokens * a.terms + 7) / 8 * 8;
-  const int blocks = (a.T + a.tokens - 1) / a.tokens;
-  const int gy = blocks < sms ? blocks : sms, gx_most = sms / gy;
-  // a ring of 4 chunks; of 3 where that lets all columns of a block lie in shared memory at once
-  int fit = 0;
-  size_t fixed = 0;
-  for (a.depth = 4;; --a.depth) {
-    fixed = (size_t)WARPS * a.depth * W::SLOT + sizeof(float) * WARPS * a.part_cols * PART_STRIDE;
-    // a chunk of a block's terms and scales; a row's padding
-    fit = (int)((SMEM_MAX - fixed - (size_t)a.tokens * (a.terms * 64 + 16)) / (a.tokens * (a.terms * 2 * W::COLUMNS + sizeof(float))));
-    if (a.depth == 3 || fit >= (chunks + WARPS - 1) / WARPS * WARPS) break;
-  }
-  a.split = choose_split((units + gx_most - 1) / gx_most, chunks, fit);
-  a.panel = (chunks + a.split - 1) / a.split * a.split;
-  if (fit < a.panel) a.panel = fit / a.split * a.split;
-  a.row_stride = row_bytes(a.panel * W::COLUMNS);
-  a.scale_stride = (a.panel + 3) / 4 * 4;  // the rows behind the scales on 16-byte boundaries
-  const size_t smem = fixed + a.tokens * (sizeof(float) * a.scale_stride + (size_t)a.terms * a.row_stride);
-  err = allow_smem<linear_kernel<W>>(SMEM_MAX);
+  const size_t fixed = (size_t)WARPS * DEPTH * W::SLOT + sizeof(float) * WARPS * a.part_cols * PART_STRIDE;
+  auto bytes = [&]() {
+    a.row_stride = row_bytes(a.panel * W::COLUMNS);
+    a.scale_stride = (a.panel + 3) / 4 * 4;  // the rows behind the scales on 16-byte boundaries
+    return fixed + a.tokens * (sizeof(float) * a.scale_stride + (size_t)a.terms * a.row_stride);
+  };
+  // chunks of a block's terms and scales that fit beside the rings, with a row's padding
+  const int fit = (int)((SMEM_MAX - fixed - (size_t)a.tokens * (a.terms * 64 + 16)) /
+                        (a.tokens * (a.terms * 2 * W::COLUMNS + sizeof(float))));
+  a.panel = chunks;
+  const int per_sm = WARPS == 16 || bytes() > SMEM_HALF ? 1 : 2;
+  const int blocks = (a.T + a.tokens - 1) / a.tokens, ctas = sms * per_sm;
+  const int gy = blocks < ctas ? blocks : ctas, gx_most = ctas / gy;
+  a.split = choose_split(WARPS, (units + gx_most - 1) / gx_most, chunks, fit);
+  a.panel = fit < chunks ? fit / a.split * a.split : (chunks + a.split - 1) / a.split * a.split;
+  if (a.panel > fit) a.panel = fit / a.split * a.split;
+  err = allow_smem<linear_kernel<W, TILES, WARPS, DEPTH>>(SMEM_MAX);
   if (err != cudaSuccess) return err;
   const int n_group = WARPS / a.split, most = (units + n_group - 1) / n_group;
-  STRATA_LAUNCH(KID_LINEAR, s,
-                err = launch_pdl(linear_kernel<W>, dim3(most < gx_most ? most : gx_most, gy), THREADS, smem, s, w, a));
+  STRATA_LAUNCH(KID_LINEAR, s, err = launch_pdl(linear_kernel<W, TILES, WARPS, DEPTH>, dim3(most < gx_most ? most : gx_most, gy),
+                                                dim3(32 * WARPS), bytes(), s, w, a));
   return err;
+}
+
+template <class W>
+cudaError_t launch(const W& w, LinearArgs a, cudaStream_t s) {
+  a.terms = terms_of(a.x_type, W::F16);
+  // one tile: two CTAs of 8 warps an SM, one of which computes while the other lays out x or joins sums; more: one of 16, with more
+  // columns of x in shared memory and so fewer passes over the weights
+  return a.T * a.terms <= 8 ? launch_tiles<1, 8, 6>(w, a, s) : launch_tiles<TILES_MAX, 16, 3>(w, a, s);
 }
 
 template <int GROUP>

@@ -64,6 +64,7 @@ bool good_experts(const strata_q4_experts_t* ex, int32_t T) {
   const strata_q4_t &gu = ex->gate_up_q4, &dn = ex->down_q4;
   if (!q4::valid(gu) || !q4::valid(dn) || !gu.paired || dn.paired) return false;
   if (gu.n_out != 2 * (int64_t)dn.d_in || gu.d_in != dn.n_out) return false;
+  if (gu.group != dn.group || gu.scale_type != dn.scale_type || gu.zeros != dn.zeros) return false;
   if (gu.d_in > STRATA_Q4_EXPERTS_DIM_MAX || dn.d_in > STRATA_Q4_EXPERTS_DIM_MAX) return false;
   if (ex->n_expert < 1 || ex->n_expert > STRATA_Q4_EXPERTS_E_MAX || ex->top_k < 1 || ex->top_k > STRATA_Q4_EXPERTS_K_MAX)
     return false;
@@ -239,8 +240,8 @@ strata_status strata_moe_q4_experts(const strata_q4_experts_t* ex, const int32_t
   if (T == 0) return STRATA_OK;
   const int d = ex->gate_up_q4.d_in;
   if (overlap(rows_of(x, T, ex->x_stride, d, ex->x_type), rows_of(out, T, ex->out_stride, d, ex->out_type))) return STRATA_E_INVAL;
-  return launched(launch_q4_experts(*ex, ids, weights, x, T, out, (char*)ws + DX_END, (int*)((char*)ws + WS_STATUS),
-                                    (cudaStream_t)stream));
+  return launched(launch_q4_experts(*ex, ids, weights, x, T, out, (char*)ws + DX_END, (unsigned*)((char*)ws + WS_MEET),
+                                    (int*)((char*)ws + WS_STATUS), (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -10,7 +10,7 @@ namespace strata {
 // Continues KernelId.
 enum OpsKernelId : int {
   KID_SELECT = KID_COUNT, KID_NORM, KID_COMBINE_NORM, KID_ADAPTER_SHRINK, KID_ADAPTER_EXPAND, KID_ADAPTERS, KID_LINEAR,
-  KID_Q4_GATE_UP, KID_Q4_DOWN, KID_Q4_COMBINE, KID_PACK_Q4, KID_END
+  KID_Q4_EXPERTS, KID_PACK_Q4, KID_END
 };
 
 // The dynamic shared memory a kernel may use, raised once per kernel and device.
@@ -66,9 +66,9 @@ cudaError_t launch_adapters(const strata_adapters_t& ad, const int32_t* seg_off,
                             cudaStream_t s);
 
 cudaError_t launch_linear(const strata_linear_t& li, const void* x, int T, const float* bias, void* y, cudaStream_t s);
-// scratch: q4_experts_scratch() bytes.
+// scratch: q4_experts_scratch() bytes; meet: three words that are 0 before and after.
 size_t q4_experts_scratch(const strata_q4_experts_t& ex, int T);
 cudaError_t launch_q4_experts(const strata_q4_experts_t& ex, const int32_t* ids, const float* weights, const void* x, int T,
-                              void* out, char* scratch, int* status, cudaStream_t s);
+                              void* out, char* scratch, unsigned* meet, int* status, cudaStream_t s);
 
 }  // namespace strata

@@ -18,9 +18,8 @@
 namespace strata {
 namespace q4 {
 
-constexpr int WARPS = 16;           // of a CTA; one CTA an SM
-constexpr int THREADS = 32 * WARPS;
-constexpr int SMEM_MAX = 227 * 1024 - 256;  // dynamic; the rest holds the kernels' static words
+constexpr int SMEM_MAX = 227 * 1024 - 256;   // dynamic; the rest holds the kernels' static words
+constexpr int SMEM_HALF = 113 * 1024 - 256;  // of each of two CTAs an SM
 constexpr int TILES_MAX = 3;        // tiles of 8 term columns that a warp accumulates at once
 constexpr int PART_STRIDE = 20;     // floats between two columns of a warp's sums: 16 rows and 4 against bank conflicts
 
@@ -35,40 +34,51 @@ __host__ __device__ constexpr int terms_of(int type, bool f16) {
 // operand loads of 8 lanes, 64 bytes of each of two rows, meet all banks once.
 __host__ __device__ constexpr int row_bytes(int columns) { return (2 * columns) | 64; }
 
-// Columns c0 .. c1 - 1 (c0 a multiple of 128) of row `row0` elements into x, as `terms` rows at dst, by 16 lanes of 8 columns a chunk;
-// behind the last column zeros, up to a whole block of 32.  scale: of chunk c0 / 128 and on (4-bit weights).  `part` of `parts` half warps.
+// Eight columns, first i of a row, into `terms` rows at dst; F16: after their chunk's power of two, which goes to *scale.  By the 16 lanes of
+// a chunk; `all` columns in whole blocks of 32, those behind the last hold zeros.
 template <bool F16>
-__device__ __forceinline__ void stage_row(const void* x, int64_t row0, int type, int columns, int c0, int c1, int terms, char* dst, int stride,
+__device__ __forceinline__ void stage8(const Raw8& raw, int type, bool in, bool store, int terms, char* dst, int stride, float* scale) {
+  float f[8] = {};
+  if (in) widen8(raw, type, f);
+  if (F16) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = 8; o; o /= 2) top = max(top, __shfl_xor_sync(0xffffu << (threadIdx.x & 16), top, o));
+    const uint32_t e = max(top >> 23, 15u);  // 2^(e - 127) <= largest; below 2^-112 all count as 2^-112
+    const float up = __uint_as_float((268u - e) << 23);
+    if ((threadIdx.x & 15) == 0) *scale = __uint_as_float((e - 14u) << 23);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] *= up;
+  }
+  if (!store) return;
+  for (int t = 0; t < terms; ++t) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      w[j] = narrow2(f[2 * j], f[2 * j + 1], F16 ? STRATA_F16 : STRATA_BF16);
+      const float2 v = widen2(w[j], F16 ? STRATA_F16 : STRATA_BF16);
+      f[2 * j] -= v.x;  // exact: the rest has fewer bits
+      f[2 * j + 1] -= v.y;
+    }
+    *reinterpret_cast<uint4*>(dst + t * stride) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+// Columns c0 .. c1 - 1 (c0 a multiple of 128) of the row at element row0 of x, as `terms` rows at dst; behind the last column zeros, up to
+// a whole block of 32.  scale: of chunk c0 / 128 and on.  By `parts` half warps, this one `part`, a chunk each, two of them asked for at once.
+template <bool F16>
+__device__ __noinline__ void stage_row(const void* x, int64_t row0, int type, int columns, int c0, int c1, int terms, char* dst, int stride,
                                           float* scale, int part, int parts) {
-  const int lane = threadIdx.x & 15;
-  const uint32_t half = 0xffffu << (threadIdx.x & 16);
-  for (int c = part * CHUNK; c < c1 - c0; c += parts * CHUNK) {
-    const int i = c + lane * 8;
-    float f[8] = {};
-    if (c0 + i < columns) widen8(load8(x, row0 + c0 + i, type), type, f);
-    if (F16) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
-      for (int o = 8; o; o /= 2) top = max(top, __shfl_xor_sync(half, top, o));
-      const uint32_t e = max(top >> 23, 15u);  // 2^(e - 127) <= largest; below 2^-112 all count as 2^-112
-      const float up = __uint_as_float((268u - e) << 23);
-      if (lane == 0) scale[c / CHUNK] = __uint_as_float((e - 14u) << 23);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] *= up;
-    }
-    if (c0 + i >= (columns + BLOCK - 1) / BLOCK * BLOCK) continue;
-    for (int t = 0; t < terms; ++t) {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        w[j] = narrow2(f[2 * j], f[2 * j + 1], F16 ? STRATA_F16 : STRATA_BF16);
-        const float2 v = widen2(w[j], F16 ? STRATA_F16 : STRATA_BF16);
-        f[2 * j] -= v.x;  // exact: the rest has fewer bits
-        f[2 * j + 1] -= v.y;
-      }
-      *reinterpret_cast<uint4*>(dst + t * stride + i * 2) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+  const int lane = threadIdx.x & 15, all = (columns + BLOCK - 1) / BLOCK * BLOCK, n = c1 - c0;
+  for (int c = part * CHUNK; c < n; c += 2 * parts * CHUNK) {
+    const int i = c + lane * 8, j = i + parts * CHUNK;
+    const bool two = c + parts * CHUNK < n, in_i = c0 + i < columns, in_j = two && c0 + j < columns;
+    Raw8 ri{}, rj{};
+    if (in_i) ri = load8(x, row0 + c0 + i, type);
+    if (in_j) rj = load8(x, row0 + c0 + j, type);
+    stage8<F16>(ri, type, in_i, c0 + i < all, terms, dst + i * 2, stride, scale + c / CHUNK);
+    if (two) stage8<F16>(rj, type, in_j, c0 + j < all, terms, dst + j * 2, stride, scale + c / CHUNK + parts);
   }
 }
 
@@ -106,18 +116,30 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same on a sum of 0, fp16 operands.
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
   const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&d);
+}
+// (w & mask) | set, in one instruction: written out, since the compiler makes two of two constants.
+__device__ __forceinline__ uint32_t mask_set(uint32_t w, uint32_t mask, uint32_t set) {
+  uint32_t v;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(w), "r"(mask), "r"(set));
+  return v;
 }
 // A packed word as four pairs of fp16 code - zero.  In the mantissa of fp16, 0x6400 | code is 1024 + code and 0x5400 | code << 4 is
 // 64 + code, so two pairs of nibbles need no shift; z0 holds 1024 + zero twice, z1 64 + zero.
 __device__ __forceinline__ void widen_word(uint32_t w, uint32_t z0, uint32_t z1, uint32_t (&a)[4]) {
   const uint32_t v = w >> 8;
-  a[0] = sub2((w & 0x000f000fu) | 0x64006400u, z0);
-  a[1] = sub2((w & 0x00f000f0u) | 0x54005400u, z1);
-  a[2] = sub2((v & 0x000f000fu) | 0x64006400u, z0);
-  a[3] = sub2((v & 0x00f000f0u) | 0x54005400u, z1);
+  a[0] = sub2(mask_set(w, 0x000f000fu, 0x64006400u), z0);
+  a[1] = sub2(mask_set(w, 0x00f000f0u, 0x54005400u), z1);
+  a[2] = sub2(mask_set(v, 0x000f000fu, 0x64006400u), z0);
+  a[3] = sub2(mask_set(v, 0x00f000f0u, 0x54005400u), z1);
 }
 
 // z0 and z1 of rows g (byte 0 of z) and g + 8 (byte 1).
@@ -141,15 +163,18 @@ struct Q4 {
   int64_t slab;         // bytes of a slab
   int columns;
 
+  __device__ __forceinline__ void load(uint32_t slot, const uint8_t* p, int64_t, int ch, bool tail, int lane) const {
+    if (tail) load_tail(slot, p, columns % CHUNK / BLOCK, lane);
+    else load(slot, p, lane);
+  }
   // Where this lane's part of chunk ch of slab s begins; the next chunk is BYTES further.
   __device__ __forceinline__ const uint8_t* at(int64_t s, int ch, int lane) const { return base + s * slab + ch * BYTES + lane * 16; }
-  __device__ __forceinline__ void load(uint32_t slot, const uint8_t* p, int64_t, int, int lane) const {
+  static __device__ __forceinline__ void load(uint32_t slot, const uint8_t* p, int lane) {
     copy_async<16>(slot + lane * 16, p);
     copy_async<16>(slot + 512 + lane * 16, p + 512);
     if (lane < META / 16) copy_async<16>(slot + 1024 + lane * 16, p + 1024);
   }
-  __device__ __forceinline__ void load_tail(uint32_t slot, const uint8_t* p, int64_t, int, int lane) const {
-    const int nb = columns % CHUNK / BLOCK;
+  static __device__ __forceinline__ void load_tail(uint32_t slot, const uint8_t* p, int nb, int lane) {  // nb blocks
     p -= lane * 16;
     for (int b = 0; b < nb; ++b) {
       copy_async<4>(slot + lane * 16 + 4 * b, p + (lane * nb + b) * 4);
@@ -186,7 +211,7 @@ struct Q4 {
       if constexpr (ZEROS) {
         zero_pairs(zeros[gr >> 1] >> (16 * (gr & 1)), z0lo, z1lo, z0hi, z1hi);
       }
-      float part[NT][4] = {};
+      float part[NT][4];
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int k = gr * PER + i;
@@ -196,7 +221,8 @@ struct Q4 {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const uint4 x = lds16(b[t] + k * 64);
-          mma<true>(part[t], alo[0], ahi[0], alo[1], ahi[1], x.x, x.y);
+          if (i == 0) mma_first(part[t], alo[0], ahi[0], alo[1], ahi[1], x.x, x.y);
+          else mma<true>(part[t], alo[0], ahi[0], alo[1], ahi[1], x.x, x.y);
           mma<true>(part[t], alo[2], ahi[2], alo[3], ahi[3], x.z, x.w);
         }
       }
@@ -237,8 +263,8 @@ struct Q4 {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const uint4 x = lds16(b[t] + k * 64);
-        float part[4] = {};
-        mma<true>(part, alo[0], ahi[0], alo[1], ahi[1], x.x, x.y);
+        float part[4];
+        mma_first(part, alo[0], ahi[0], alo[1], ahi[1], x.x, x.y);
         mma<true>(part, alo[2], ahi[2], alo[3], ahi[3], x.z, x.w);
         acc[t][0] = fmaf(cs[t].x * s.x, part[0], acc[t][0]);
         acc[t][1] = fmaf(cs[t].y * s.x, part[1], acc[t][1]);
@@ -265,10 +291,7 @@ struct Bf16 {
     const int64_t row = s * ROWS + (lane >> 2);
     return base + 2 * ((row < rows ? row : 0) * stride) + ch * BYTES + (lane & 3) * 16;
   }
-  __device__ __forceinline__ void load_tail(uint32_t slot, const uint8_t* p, int64_t s, int ch, int lane) const {
-    load(slot, p, s, ch, lane);
-  }
-  __device__ __forceinline__ void load(uint32_t slot, const uint8_t* p, int64_t s, int ch, int lane) const {
+  __device__ __forceinline__ void load(uint32_t slot, const uint8_t* p, int64_t s, int ch, bool, int lane) const {
     const uint8_t* q = s * ROWS + (lane >> 2) + 8 < rows ? p + 16 * stride : p;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // block i / 2, row half i % 2
@@ -301,24 +324,23 @@ struct Bf16 {
   }
 };
 
-// A warp's ring of `depth` (3 or 4) chunks: filled `depth` - 1 ahead, one group of copies a chunk used, empty when none is left.
+// A warp's ring of DEPTH chunks of SLOT bytes: filled DEPTH - 1 ahead, one group of copies a chunk used, empty when none is left.
+template <int DEPTH, int SLOT>
 struct Ring {
-  uint32_t at, end, fill, use;  // shared addresses
-  int depth, slot;              // bytes of a slot
-  __device__ __forceinline__ Ring(uint32_t a, int d, int bytes) : at(a), end(a + d * bytes), fill(a), use(a), depth(d), slot(bytes) {}
+  uint32_t at, fill, use;  // shared addresses
+  __device__ __forceinline__ explicit Ring(uint32_t a) : at(a), fill(a), use(a) {}
   __device__ __forceinline__ uint32_t next_fill() {
     const uint32_t a = fill;
-    fill = fill + slot == end ? at : fill + slot;
+    fill = fill + SLOT == at + DEPTH * SLOT ? at : fill + SLOT;
     return a;
   }
   __device__ __forceinline__ uint32_t next_use() {
     const uint32_t a = use;
-    use = use + slot == end ? at : use + slot;
+    use = use + SLOT == at + DEPTH * SLOT ? at : use + SLOT;
     return a;
   }
   __device__ __forceinline__ void wait() const {  // for the oldest; its scales were copied by other lanes
-    if (depth == 4) copy_wait<2>();
-    else copy_wait<1>();
+    copy_wait<DEPTH - 2>();
     __syncwarp();
   }
 };
@@ -337,8 +359,8 @@ struct Share {
 
 // Products of the next `whole` chunks of the ring, then of a shorter one.  b[tile] and cs[tile] are this lane's shared addresses for the
 // activations of the first of them; one chunk of this warp to the next is S of the unit's.
-template <int NT, class W, class L>
-__device__ __forceinline__ void run_chunks(const W& w, Ring& ring, L& loader, int whole, bool tail, int S, uint32_t (&b)[NT], uint2 (&cs)[NT],
+template <int NT, class W, class R, class L>
+__device__ __forceinline__ void run_chunks(const W& w, R& ring, L& loader, int whole, bool tail, int S, uint32_t (&b)[NT], uint2 (&cs)[NT],
                                            int lane, float (&acc)[NT][4]) {
   auto scales = [&](float2 (&v)[NT]) {
 #pragma unroll
@@ -386,19 +408,21 @@ __device__ __forceinline__ float sum_part(const float* part, int step, int S, in
   return v;
 }
 
-// The S (1, 2, 4, 8 or 16) warps that share a unit meet.
+// The S (a power of two up to WARPS) warps that share a unit meet.
+template <int WARPS>
 __device__ __forceinline__ void group_sync(int group, int S) {
   if (S == 1) __syncwarp();
   else if (S == WARPS) __syncthreads();
   else named_barrier(1 + group, 32 * S);
 }
 
-// Warps to a unit (16 rows x all chunks): the split with the fewest chunks one after the other; equal: fewer warps a unit,
-// which leaves fewer sums to join.
-__host__ __device__ inline int choose_split(int units_of_cta, int chunks, int most = WARPS) {
+// Warps to a unit (16 rows x all chunks): the split with the fewest chunks one after the other, where a unit's end counts as one more
+// and joining several warps' sums as another; equal: fewer warps a unit.
+__host__ __device__ inline int choose_split(int warps, int units_of_cta, int chunks, int most) {
   int best = 1, cost = 1 << 30;
-  for (int i = 0; 1 << i <= WARPS && 1 << i <= most; ++i) {  // 2^i warps a unit, WARPS / 2^i units at once
-    const int c = ((units_of_cta + (WARPS >> i) - 1) * (1 << i) / WARPS) * ((chunks + (1 << i) - 1) >> i);
+  for (int i = 0; 1 << i <= warps && 1 << i <= most; ++i) {  // 2^i warps a unit, warps / 2^i units at once
+    const int rounds = (units_of_cta + (warps >> i) - 1) * (1 << i) / warps;
+    const int c = rounds * (((chunks + (1 << i) - 1) >> i) + (i ? 2 : 1));
     if (c < cost) best = 1 << i, cost = c;
   }
   return best;

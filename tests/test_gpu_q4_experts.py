@@ -22,12 +22,11 @@ def rows(T, n, pad, kind, seed):
 
 
 class Layer:
-    def __init__(self, E, d_model, d_ff, group=32, zeros=False, scale=qre.BF16, xk=qre.F32, ok=qre.F32, k=2, pad=0, apart=0, seed=1,
-                 down_group=None):
+    def __init__(self, E, d_model, d_ff, group=32, zeros=False, scale=qre.BF16, xk=qre.F32, ok=qre.F32, k=2, pad=0, apart=0, seed=1):
         self.E, self.k, self.xk, self.ok, self.pad = E, k, xk, ok, pad
         self.d_model, self.d_ff = d_model, d_ff
         self.gu = q4ref.Matrices(E, 2 * d_ff, d_model, group, zeros, scale, paired=True, seed=seed)
-        self.dn = q4ref.Matrices(E, d_model, d_ff, down_group or group, zeros, scale, seed=seed + 1)
+        self.dn = q4ref.Matrices(E, d_model, d_ff, group, zeros, scale, seed=seed + 1)
         self.pack(apart)
 
     def pack(self, apart=0):
@@ -93,10 +92,6 @@ def test_sizes(d_model, d_ff, group):
         layer = Layer(5, d_model, d_ff, group, zeros, xk=xk, ok=ok, k=2)
         layer.check(*lists(3, 5, 2))
         layer.check(*lists(1, 5, 2))
-
-
-def test_two_groups():
-    Layer(4, 256, 96, 128, True, down_group=32).check(*lists(6, 4, 2))
 
 
 def test_one_expert_for_all():

@@ -164,7 +164,8 @@ def test_experts_refusals(lib):
               dict(gate_up_stride=qre.strata_q4_bytes(gu) - 16), dict(down_stride=qre.strata_q4_bytes(dn) - 16),
               dict(gate_up_q4=with_(gu, paired=0)), dict(down_q4=with_(dn, paired=1)), dict(down_q4=with_(dn, d_in=128)),
               dict(down_q4=with_(dn, n_out=256)), dict(gate_up_q4=with_(gu, d_in=256)), dict(gate_up_q4=with_(gu, group=48)),
-              dict(down_q4=with_(dn, group=64)),
+              dict(down_q4=with_(dn, group=64)), dict(down_q4=with_(dn, scale_type=qre.F16)), dict(down_q4=with_(dn, zeros=1)),
+              dict(gate_up_q4=with_(gu, group=64)),
               dict(gate_up_q4=with_(gu, d_in=wide), down_q4=with_(dn, n_out=wide), x_stride=wide, out_stride=wide,
                    gate_up_stride=1 << 25, down_stride=1 << 25),
               dict(gate_up_q4=with_(gu, n_out=2 * wide), down_q4=with_(dn, d_in=wide), gate_up_stride=1 << 25,
