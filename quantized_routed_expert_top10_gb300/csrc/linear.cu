@@ -17,8 +17,8 @@ struct LinearArgs {
   int64_t x_stride, y_stride;
   int T, columns, rows, x_type, y_type;
   int tokens, terms;  // of a block
-  int split;          // warps to a unit
-  int panel;          // chunks whose activations lie in shared memory at once, a multiple of split
+  int log_split;      // 2^this warps to a unit
+  int panel;          // chunks whose activations lie in shared memory at once, a multiple of the unit's warps
   int row_stride;     // bytes between rows of terms
   int scale_stride;   // floats between tokens' scales
   int part_cols;      // term columns of a block, rounded up to whole tiles
@@ -55,9 +55,9 @@ struct Loader {
 template <int NT, int WARPS, int DEPTH, class W>
 __device__ __forceinline__ void linear_block(const W& w, const LinearArgs& a, char* smem, int t0, int nt) {
   const int warp = warp_index(), lane = threadIdx.x & 31;
-  const int S = a.split, group = warp / S, member = warp % S, n_group = WARPS / S;
+  const int S = 1 << a.log_split, group = warp >> a.log_split, member = warp & (S - 1), n_group = WARPS >> a.log_split;
   const int units = (a.rows + ROWS - 1) / ROWS, chunks = (a.columns + W::COLUMNS - 1) / W::COLUMNS;
-  const Share share(a.columns, W::COLUMNS, chunks, member, S);
+  const Share share(a.columns, W::COLUMNS, chunks, member, a.log_split);
   const int first = blockIdx.x * n_group, pass = gridDim.x * n_group;
   const int cols = nt * a.terms;
 
@@ -71,7 +71,7 @@ __device__ __forceinline__ void linear_block(const W& w, const LinearArgs& a, ch
   loader.start(first + group, lane);
   for (int i = 0; i < DEPTH - 1; ++i) loader.next(ring, lane);
 
-  const int panel_steps = a.panel / S;
+  const int panel_steps = a.panel >> a.log_split;
   const bool panels = a.panel < chunks;
   for (int base = first; base < units; base += pass) {
     const int u = base + group;
@@ -154,12 +154,13 @@ cudaError_t launch_tiles(const W& w, LinearArgs a, cudaStream_t s) {
   const int per_sm = WARPS == 16 || bytes() > SMEM_HALF ? 1 : 2;
   const int blocks = (a.T + a.tokens - 1) / a.tokens, ctas = sms * per_sm;
   const int gy = blocks < ctas ? blocks : ctas, gx_most = ctas / gy;
-  a.split = choose_split(WARPS, (units + gx_most - 1) / gx_most, chunks, fit);
-  a.panel = fit < chunks ? fit / a.split * a.split : (chunks + a.split - 1) / a.split * a.split;
-  if (a.panel > fit) a.panel = fit / a.split * a.split;
+  const int split = choose_split(WARPS, (units + gx_most - 1) / gx_most, chunks, fit);
+  a.panel = fit < chunks ? fit / split * split : (chunks + split - 1) / split * split;
+  if (a.panel > fit) a.panel = fit / split * split;
   err = allow_smem<linear_kernel<W, TILES, WARPS, DEPTH>>(SMEM_MAX);
   if (err != cudaSuccess) return err;
-  const int n_group = WARPS / a.split, most = (units + n_group - 1) / n_group;
+  for (a.log_split = 0; 1 << a.log_split < split;) ++a.log_split;
+  const int n_group = WARPS / split, most = (units + n_group - 1) / n_group;
   STRATA_LAUNCH(KID_LINEAR, s, err = launch_pdl(linear_kernel<W, TILES, WARPS, DEPTH>, dim3(most < gx_most ? most : gx_most, gy),
                                                 dim3(32 * WARPS), bytes(), s, w, a));
   return err;

@@ -349,10 +349,11 @@ struct Ring {
 struct Share {
   int whole;  // its whole chunks
   bool tail;  // and the shorter one
-  __device__ __forceinline__ Share(int columns, int chunk, int chunks, int member, int S) {
+  __device__ __forceinline__ Share(int columns, int chunk, int chunks, int member, int log_split) {
+    const int S = 1 << log_split;
     const bool cut = (columns + BLOCK - 1) / BLOCK % (chunk / BLOCK) != 0;  // bf16 columns end anywhere: whole when its last block has begun
-    tail = cut && (chunks - 1) % S == member;
-    whole = (chunks - member + S - 1) / S - (tail ? 1 : 0);
+    tail = cut && ((chunks - 1) & (S - 1)) == member;
+    whole = ((chunks - member + S - 1) >> log_split) - (tail ? 1 : 0);
     if (chunks <= member) whole = 0, tail = false;
   }
 };
