@@ -24,30 +24,18 @@ struct LinearArgs {
   int part_cols;      // term columns of a block, rounded up to whole tiles
 };
 
-// The chunks a warp will need, unit after unit, ahead of the products.
+// A warp's units, one after the other.
 template <class W>
-struct Loader {
+struct Units {
   const W& w;
-  const Share& share;
-  int S, member, units, pass;
-  int unit, left;  // the unit's chunks left
-  const uint8_t* at;
-
-  __device__ __forceinline__ void start(int u, int lane) {
-    unit = u;
-    left = u < units ? share.whole + share.tail : 0;
-    at = w.at(u, member, lane);
-  }
-  template <class R>
-  __device__ __forceinline__ void next(R& ring, int lane) {
-    if (left) {
-      const uint32_t slot = ring.next_fill();
-      const int ch = member + (share.whole + share.tail - left) * S;
-      w.load(slot, at, unit, ch, left == 1 && share.tail, lane);
-      at += S * W::BYTES;
-      if (--left == 0) start(unit + pass, lane);
-    }
-    copy_commit();
+  int unit, units, pass, member, lane;
+  int whole, tail, stride;
+  typename W::Cursor cursor;
+  __device__ __forceinline__ bool next() {
+    if (unit >= units || (whole == 0 && tail == 0)) return false;
+    cursor = w.cursor(unit, member, lane);
+    unit += pass;
+    return true;
   }
 };
 
@@ -57,19 +45,16 @@ __device__ __forceinline__ void linear_block(const W& w, const LinearArgs& a, ch
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const int S = 1 << a.log_split, group = warp >> a.log_split, member = warp & (S - 1), n_group = WARPS >> a.log_split;
   const int units = (a.rows + ROWS - 1) / ROWS, chunks = (a.columns + W::COLUMNS - 1) / W::COLUMNS;
-  const Share share(a.columns, W::COLUMNS, chunks, member, a.log_split);
+  const Share share(a.columns, W::COLUMNS, member, a.log_split);
   const int first = blockIdx.x * n_group, pass = gridDim.x * n_group;
   const int cols = nt * a.terms;
 
-  Ring<DEPTH, W::SLOT> ring(smem_u32(smem) + warp * (DEPTH * W::SLOT));
   float* part = reinterpret_cast<float*>(smem + WARPS * DEPTH * W::SLOT);
   const int part_step = a.part_cols * PART_STRIDE;
   float* scale = part + WARPS * part_step;
   char* rows = reinterpret_cast<char*>(scale + a.tokens * a.scale_stride);
-
-  Loader<W> loader{w, share, S, member, units, pass};
-  loader.start(first + group, lane);
-  for (int i = 0; i < DEPTH - 1; ++i) loader.next(ring, lane);
+  Feed<W, DEPTH, Units<W>> feed(Units<W>{w, first + group, units, pass, member, lane, share.whole, share.tail, S * W::BYTES},
+                                smem_u32(smem) + warp * (DEPTH * W::SLOT), lane);
 
   const int panel_steps = a.panel >> a.log_split;
   const bool panels = a.panel < chunks;
@@ -99,7 +84,7 @@ __device__ __forceinline__ void linear_block(const W& w, const LinearArgs& a, ch
       }
       if (u < units) {
         const int whole = min(panel_steps, share.whole - done);
-        run_chunks<NT>(w, ring, loader, whole, share.tail && done + panel_steps > share.whole && done <= share.whole, S, b, cs, lane, acc);
+        run_chunks<NT, W>(feed, whole, done <= share.whole && share.whole < done + panel_steps ? share.tail : 0, S, b, cs, acc);
       }
     }
     store_part<NT>(part + warp * part_step, lane, acc);
@@ -180,8 +165,8 @@ cudaError_t launch_q4(const strata_linear_t& li, const LinearArgs& a, cudaStream
   const uint8_t* p = (const uint8_t*)li.w;
   const int64_t slab = slab_bytes(q.d_in, q.group, q.zeros != 0);
   if (q.scale_type == STRATA_F16)
-    return q.zeros ? launch(Q4<GROUP, true, true>{p, slab, q.d_in}, a, s) : launch(Q4<GROUP, false, true>{p, slab, q.d_in}, a, s);
-  return q.zeros ? launch(Q4<GROUP, true, false>{p, slab, q.d_in}, a, s) : launch(Q4<GROUP, false, false>{p, slab, q.d_in}, a, s);
+    return q.zeros ? launch(Q4<GROUP, true, true>{p, slab}, a, s) : launch(Q4<GROUP, false, true>{p, slab}, a, s);
+  return q.zeros ? launch(Q4<GROUP, true, false>{p, slab}, a, s) : launch(Q4<GROUP, false, false>{p, slab}, a, s);
 }
 
 }  // namespace
@@ -191,7 +176,7 @@ cudaError_t launch_linear(const strata_linear_t& li, const void* x, int T, const
   a.x = x, a.bias = bias, a.y = y;
   a.x_stride = li.x_stride, a.y_stride = li.y_stride;
   a.T = T, a.columns = li.q4.d_in, a.rows = li.q4.n_out, a.x_type = li.x_type, a.y_type = li.y_type;
-  if (li.weight == STRATA_W_BF16) return launch(Bf16{(const uint8_t*)li.w, li.w_stride, a.columns, a.rows}, a, s);
+  if (li.weight == STRATA_W_BF16) return launch(Bf16{(const uint8_t*)li.w, li.w_stride, a.rows}, a, s);
   if (li.q4.group == 32) return launch_q4<32>(li, a, s);
   return li.q4.group == 64 ? launch_q4<64>(li, a, s) : launch_q4<128>(li, a, s);
 }

@@ -159,23 +159,23 @@ struct Q4 {
   static constexpr int SLOT = 1024 + META;
   static constexpr int BYTES = chunk_bytes(GROUP, ZEROS);
 
+  struct Cursor {  // this lane's part of a chunk
+    const uint8_t* at;
+  };
   const uint8_t* base;  // of the matrix
   int64_t slab;         // bytes of a slab
-  int columns;
 
-  __device__ __forceinline__ void load(uint32_t slot, const uint8_t* p, int64_t, int ch, bool tail, int lane) const {
-    if (tail) load_tail(slot, p, columns % CHUNK / BLOCK, lane);
-    else load(slot, p, lane);
+  __device__ __forceinline__ Cursor cursor(int64_t s, int ch, int lane) const { return {base + s * slab + ch * BYTES + lane * 16}; }
+  static __device__ __forceinline__ void load(uint32_t slot, const Cursor& c, int lane) {
+    copy_async<16>(slot + lane * 16, c.at);
+    copy_async<16>(slot + 512 + lane * 16, c.at + 512);
+    if (lane < META / 16) copy_async<16>(slot + 1024 + lane * 16, c.at + 1024);
   }
-  // Where this lane's part of chunk ch of slab s begins; the next chunk is BYTES further.
-  __device__ __forceinline__ const uint8_t* at(int64_t s, int ch, int lane) const { return base + s * slab + ch * BYTES + lane * 16; }
-  static __device__ __forceinline__ void load(uint32_t slot, const uint8_t* p, int lane) {
-    copy_async<16>(slot + lane * 16, p);
-    copy_async<16>(slot + 512 + lane * 16, p + 512);
-    if (lane < META / 16) copy_async<16>(slot + 1024 + lane * 16, p + 1024);
-  }
-  static __device__ __forceinline__ void load_tail(uint32_t slot, const uint8_t* p, int nb, int lane) {  // nb blocks
-    p -= lane * 16;
+  // A last chunk of `left` (32, 64 or 96) columns.
+  static __device__ __forceinline__ void load_tail(uint32_t slot, const Cursor& c, int left, int lane) {
+    const int nb = left / BLOCK;
+    const uint8_t* p = c.at - lane * 16;
+#pragma unroll 1
     for (int b = 0; b < nb; ++b) {
       copy_async<4>(slot + lane * 16 + 4 * b, p + (lane * nb + b) * 4);
       copy_async<4>(slot + 512 + lane * 16 + 4 * b, p + 128 * nb + (lane * nb + b) * 4);
@@ -186,8 +186,8 @@ struct Q4 {
   // acc[tile] += chunk x columns.  b[tile]: shared address of this lane's operand row at the chunk's first column; cs[tile]: the scales of
   // this lane's two result columns in this chunk.
   template <int NT>
-  __device__ __forceinline__ void products(uint32_t slot, const uint32_t (&b)[NT], const float2 (&cs)[NT], int lane,
-                                           float (&acc)[NT][4]) const {
+  static __device__ __forceinline__ void products(uint32_t slot, const uint32_t (&b)[NT], const float2 (&cs)[NT], int lane,
+                                                  float (&acc)[NT][4]) {
     const int g = lane >> 2;
     const uint4 lo4 = lds16(slot + lane * 16), hi4 = lds16(slot + 512 + lane * 16);
     const uint32_t lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
@@ -246,8 +246,8 @@ struct Q4 {
 
   // The same for a last chunk of nb (1 to 3) blocks, block by block.
   template <int NT>
-  __device__ __forceinline__ void tail(uint32_t slot, int nb, const uint32_t (&b)[NT], const float2 (&cs)[NT], int lane,
-                                       float (&acc)[NT][4]) const {
+  static __device__ __forceinline__ void tail(uint32_t slot, int nb, const uint32_t (&b)[NT], const float2 (&cs)[NT], int lane,
+                                              float (&acc)[NT][4]) {
     const int g = lane >> 2;
 #pragma unroll 1
     for (int k = 0; k < nb; ++k) {
@@ -282,38 +282,48 @@ struct Bf16 {
   static constexpr int SLOT = 2048;
   static constexpr int BYTES = 2 * COLUMNS;
 
+  struct Cursor {
+    const uint8_t* at;
+    int64_t eight;  // to the row 8 further
+  };
   const uint8_t* base;
   int64_t stride;  // elements
-  int columns, rows;
+  int rows;
 
-  __device__ __forceinline__ const uint8_t* at(int64_t s, int ch, int lane) const {
-    // a row behind the last reads row 0 and its results are not used
+  __device__ __forceinline__ Cursor cursor(int64_t s, int ch, int lane) const {
+    // rows behind the last read another, and their results are not used
     const int64_t row = s * ROWS + (lane >> 2);
-    return base + 2 * ((row < rows ? row : 0) * stride) + ch * BYTES + (lane & 3) * 16;
+    return {base + 2 * ((row < rows ? row : 0) * stride) + ch * BYTES + (lane & 3) * 16, row + 8 < rows ? 16 * stride : 0};
   }
-  __device__ __forceinline__ void load(uint32_t slot, const uint8_t* p, int64_t s, int ch, bool, int lane) const {
-    const uint8_t* q = s * ROWS + (lane >> 2) + 8 < rows ? p + 16 * stride : p;
+  static __device__ __forceinline__ void load(uint32_t slot, const Cursor& c, int lane) {
+    copy_async<16>(slot + lane * 16, c.at);
+    copy_async<16>(slot + 512 + lane * 16, c.at + c.eight);
+    copy_async<16>(slot + 1024 + lane * 16, c.at + 64);
+    copy_async<16>(slot + 1536 + lane * 16, c.at + c.eight + 64);
+  }
+  // A last chunk of `left` (8 .. 56) columns; behind them zeros.
+  static __device__ __forceinline__ void load_tail(uint32_t slot, const Cursor& c, int left, int lane) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // block i / 2, row half i % 2
-      const bool have = ch * COLUMNS + (i >> 1) * BLOCK + (lane & 3) * 8 < columns;
+      const bool have = (i >> 1) * BLOCK + (lane & 3) * 8 < left;
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + i * 512 + lane * 16),
-                   "l"(have ? (i & 1 ? q : p) + (i >> 1) * 64 : base), "r"(have ? 16 : 0)
+                   "l"(have ? c.at + (i & 1 ? c.eight : 0) + (i >> 1) * 64 : c.at - (lane & 3) * 16), "r"(have ? 16 : 0)
                    : "memory");
     }
   }
   template <int NT>
-  __device__ __forceinline__ void products(uint32_t slot, const uint32_t (&b)[NT], const float2 (&)[NT], int lane,
-                                           float (&acc)[NT][4]) const {
+  static __device__ __forceinline__ void products(uint32_t slot, const uint32_t (&b)[NT], const float2 (&)[NT], int lane,
+                                                  float (&acc)[NT][4]) {
     block<NT>(slot, 0, b, lane, acc);
     block<NT>(slot, 1, b, lane, acc);
   }
   template <int NT>
-  __device__ __forceinline__ void tail(uint32_t slot, int, const uint32_t (&b)[NT], const float2 (&)[NT], int lane,
-                                       float (&acc)[NT][4]) const {
-    block<NT>(slot, 0, b, lane, acc);  // its other block is there, zeros; its operands would not be
+  static __device__ __forceinline__ void tail(uint32_t slot, int nb, const uint32_t (&b)[NT], const float2 (&)[NT], int lane,
+                                              float (&acc)[NT][4]) {
+    for (int k = 0; k < nb; ++k) block<NT>(slot, k, b, lane, acc);
   }
   template <int NT>
-  __device__ __forceinline__ void block(uint32_t slot, int k, const uint32_t (&b)[NT], int lane, float (&acc)[NT][4]) const {
+  static __device__ __forceinline__ void block(uint32_t slot, int k, const uint32_t (&b)[NT], int lane, float (&acc)[NT][4]) {
     const uint4 lo = lds16(slot + k * 1024 + lane * 16), hi = lds16(slot + k * 1024 + 512 + lane * 16);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -324,45 +334,60 @@ struct Bf16 {
   }
 };
 
-// A warp's ring of DEPTH chunks of SLOT bytes: filled DEPTH - 1 ahead, one group of copies a chunk used, empty when none is left.
-template <int DEPTH, int SLOT>
-struct Ring {
-  uint32_t at, fill, use;  // shared addresses
-  __device__ __forceinline__ explicit Ring(uint32_t a) : at(a), fill(a), use(a) {}
-  __device__ __forceinline__ uint32_t next_fill() {
-    const uint32_t a = fill;
-    fill = fill + SLOT == at + DEPTH * SLOT ? at : fill + SLOT;
-    return a;
-  }
-  __device__ __forceinline__ uint32_t next_use() {
-    const uint32_t a = use;
-    use = use + SLOT == at + DEPTH * SLOT ? at : use + SLOT;
-    return a;
-  }
-  __device__ __forceinline__ void wait() const {  // for the oldest; its scales were copied by other lanes
-    copy_wait<DEPTH - 2>();
-    __syncwarp();
-  }
-};
-
 // A warp's share of a unit: chunks member, member + S, ...; the last of the unit may be a shorter one.
 struct Share {
   int whole;  // its whole chunks
-  bool tail;  // and the shorter one
-  __device__ __forceinline__ Share(int columns, int chunk, int chunks, int member, int log_split) {
-    const int S = 1 << log_split;
-    const bool cut = (columns + BLOCK - 1) / BLOCK % (chunk / BLOCK) != 0;  // bf16 columns end anywhere: whole when its last block has begun
-    tail = cut && ((chunks - 1) & (S - 1)) == member;
-    whole = ((chunks - member + S - 1) >> log_split) - (tail ? 1 : 0);
-    if (chunks <= member) whole = 0, tail = false;
+  int tail;   // columns of its shorter one, or 0
+  __device__ __forceinline__ Share(int columns, int chunk, int member, int log_split) {
+    const int S = 1 << log_split, wholes = columns / chunk;
+    whole = wholes > member ? (wholes - member + S - 1) >> log_split : 0;
+    tail = (wholes & (S - 1)) == member ? columns - wholes * chunk : 0;
   }
 };
 
-// Products of the next `whole` chunks of the ring, then of a shorter one.  b[tile] and cs[tile] are this lane's shared addresses for the
+// A warp's ring of DEPTH chunks of SLOT bytes, filled DEPTH - 1 ahead: one group of copies a chunk used, empty when none is left.
+// U walks the warp's units: next() sets out for the next one and tells whether there is one; its cursor, whole and tail are then taken from it.
+template <class W, int DEPTH, class U>
+struct Feed {
+  U units;
+  uint32_t ring, used;  // shared addresses: of the ring, of the slot that was used last and is filled next
+  typename W::Cursor cursor;
+  int left, tail, stride;  // of the unit: whole chunks and columns of a shorter one to copy; bytes from one chunk of this warp to its next
+  int lane;
+
+  __device__ __forceinline__ Feed(const U& u, uint32_t at, int l) : units(u), ring(at), used(at), left(0), tail(0), lane(l) {
+#pragma unroll 1
+    for (int i = 0; i < DEPTH - 1; ++i) {
+      fill();
+      used += W::SLOT;
+    }
+  }
+  __device__ __forceinline__ void fill() {
+    if (left == 0 && tail == 0 && units.next()) cursor = units.cursor, left = units.whole, tail = units.tail, stride = units.stride;
+    if (left) {
+      W::load(used, cursor, lane);
+      cursor.at += stride;
+      --left;
+    } else if (tail) {
+      W::load_tail(used, cursor, tail, lane);
+      tail = 0;
+    }
+    copy_commit();
+  }
+  // The next chunk's slot, once it is there.
+  __device__ __forceinline__ uint32_t take() {
+    copy_wait<DEPTH - 2>();
+    __syncwarp();  // its scales were copied by other lanes; and all have read the slot that is filled now
+    fill();
+    used = used == ring + (DEPTH - 1) * W::SLOT ? ring : used + W::SLOT;
+    return used;
+  }
+};
+
+// Products of a warp's next `whole` chunks, then of one of `tail` columns.  b[tile] and cs[tile] are this lane's shared addresses for the
 // activations of the first of them; one chunk of this warp to the next is S of the unit's.
-template <int NT, class W, class R, class L>
-__device__ __forceinline__ void run_chunks(const W& w, R& ring, L& loader, int whole, bool tail, int S, uint32_t (&b)[NT], uint2 (&cs)[NT],
-                                           int lane, float (&acc)[NT][4]) {
+template <int NT, class W, class F>
+__device__ __forceinline__ void run_chunks(F& feed, int whole, int tail, int S, uint32_t (&b)[NT], uint2 (&cs)[NT], float (&acc)[NT][4]) {
   auto scales = [&](float2 (&v)[NT]) {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -371,18 +396,16 @@ __device__ __forceinline__ void run_chunks(const W& w, R& ring, L& loader, int w
   float2 v[NT];
 #pragma unroll 1
   for (int i = 0; i < whole; ++i) {
-    ring.wait();
-    loader.next(ring, lane);  // into the slot of the chunk before
+    const uint32_t slot = feed.take();
     scales(v);
-    w.template products<NT>(ring.next_use(), b, v, lane, acc);
+    W::template products<NT>(slot, b, v, feed.lane, acc);
 #pragma unroll
     for (int t = 0; t < NT; ++t) b[t] += S * 2 * W::COLUMNS, cs[t].x += 4 * S, cs[t].y += 4 * S;
   }
   if (tail) {
-    ring.wait();
-    loader.next(ring, lane);
+    const uint32_t slot = feed.take();
     scales(v);
-    w.template tail<NT>(ring.next_use(), (w.columns + BLOCK - 1) / BLOCK % (W::COLUMNS / BLOCK), b, v, lane, acc);
+    W::template tail<NT>(slot, (tail + BLOCK - 1) / BLOCK, b, v, feed.lane, acc);
   }
 }
 // Of the calling thread's warp, known to be the same for all its lanes.

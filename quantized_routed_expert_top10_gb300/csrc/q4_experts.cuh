@@ -202,58 +202,46 @@ struct Window {
   }
 };
 
-// The chunks this warp will need, ahead of the products: window after window, its units, its chunks of each; then those of the second step.
+// This warp's units, window after window, of the first step and then of the second.
 template <class W>
-struct Loader {
+struct Units {
   const Sorted& sorted;
-  const Step& second;
+  const Step *step, *second;
   int warp, lane;
-  const Step* step;
   Share share, share2;
-  int tail_blocks, tail_blocks2;
   Window window;
-  int u, left;  // this warp's unit, its chunks left
-  int stride, group, n_group;
-  const uint8_t* at;
+  int u, group, member;
+  int whole, tail, stride;
+  typename W::Cursor cursor;
 
+  __device__ __forceinline__ Units(const Sorted& s, const Step& s1, const Step& s2, int w, int l, const Share& h1, const Share& h2)
+      : sorted(s), step(&s1), second(&s2), warp(w), lane(l), share(h1), share2(h2), window(0) {
+    enter();
+  }
   __device__ __forceinline__ void enter() {
-    group = warp >> step->log_split, n_group = step->n_group;
-    stride = W::BYTES << step->log_split;
+    group = warp >> step->log_split, member = warp & ((1 << step->log_split) - 1);
+    whole = share.whole, tail = share.tail, stride = W::BYTES << step->log_split;
     window = Window(step->u0);
-    u = 0;  // behind the empty window's end
+    u = step->u0;  // behind the empty window's end
   }
-  __device__ __forceinline__ void find() {  // from unit u of the window on
-    left = 0;
-    while (u >= window.end || share.whole + share.tail == 0) {
-      if (share.whole + share.tail == 0 || !window.next(*step, sorted)) {
-        if (step == &second) return;
-        step = &second, share = share2, tail_blocks = tail_blocks2;
+  __device__ __forceinline__ bool next() {
+    while (u >= window.end || (whole == 0 && tail == 0)) {
+      if ((whole == 0 && tail == 0) || !window.next(*step, sorted)) {
+        if (step == second) return false;
+        step = second, share = share2;
         enter();
-        u = window.end;
-        continue;
+      } else {
+        u = window.begin + group;
       }
-      u = window.begin + group;
     }
-    left = share.whole + share.tail;
     const int e = divide(u, step->slabs_inverse);
-    at = step->base + sorted.expert[e] * step->expert_stride + (u - e * step->slabs) * step->slab +
-         (warp & ((1 << step->log_split) - 1)) * W::BYTES + lane * 16;
-  }
-  template <class R>
-  __device__ __forceinline__ void next(R& ring, int) {
-    if (left) {
-      const uint32_t slot = ring.next_fill();
-      if (left == 1 && share.tail) W::load_tail(slot, at, tail_blocks, lane);
-      else W::load(slot, at, lane);
-      at += stride;
-      if (--left == 0) {
-        u += n_group;
-        find();
-      }
-    }
-    copy_commit();
+    cursor.at = step->base + sorted.expert[e] * step->expert_stride + (u - e * step->slabs) * step->slab + member * W::BYTES + lane * 16;
+    u += step->n_group;
+    return true;
   }
 };
+template <class W, int DEPTH>
+using ExpertFeed = Feed<W, DEPTH, Units<W>>;
 
 // All CTAs of the grid meet; false when the others did not come within the limit.
 __device__ __forceinline__ bool meet(unsigned* count, int* status) {
@@ -284,10 +272,10 @@ struct Shared {  // the CTA's dynamic shared memory behind the rings
 };
 
 // Sums of unit u of the expert whose pairs in the window are lo .. lo + np - 1.
-template <bool DOWN, int NT, class W, class R>
-__device__ __forceinline__ void unit_products(const W& w, const Q4ExpertArgs& a, const Sorted& sorted, Loader<W>& loader, const Share& share,
-                                              R& ring, const Shared& sh, int S, int member, int p0, int lo, int np) {
-  const int warp = warp_index(), lane = threadIdx.x & 31, shift = a.terms[DOWN] - 1;  // one or two terms
+template <bool DOWN, int NT, class W, class F>
+__device__ __forceinline__ void unit_products(const Q4ExpertArgs& a, const Sorted& sorted, F& feed, const Share& share, const Shared& sh, int S,
+                                              int member, int p0, int lo, int np) {
+  const int warp = warp_index(), lane = feed.lane, shift = a.terms[DOWN] - 1;  // one or two terms
   uint32_t b[NT];
   uint2 cs[NT];
   auto row_of = [&](int j) {  // of pair lo + j among those in shared memory
@@ -302,7 +290,7 @@ __device__ __forceinline__ void unit_products(const W& w, const Q4ExpertArgs& a,
     cs[t].y = smem_u32(sh.scale + row_of((c2 + 1) >> shift) * a.scale_stride + member);
   }
   float acc[NT][4] = {};
-  run_chunks<NT>(w, ring, loader, share.whole, share.tail, S, b, cs, lane, acc);
+  run_chunks<NT, W>(feed, share.whole, share.tail, S, b, cs, acc);
   store_part<NT>(sh.part + warp * (a.part_cols * PART_STRIDE), lane, acc);
 }
 
@@ -318,9 +306,9 @@ __device__ __forceinline__ void stage(const Q4ExpertArgs& a, const Shared& sh, i
 }
 
 // Step 1 or 2 for this CTA's stretch.
-template <bool DOWN, int TILES, class W, class R>
-__device__ __forceinline__ void run_step(const W& w, const Q4ExpertArgs& a, const Sorted& sorted, const Step& step, Loader<W>& loader,
-                                         const Share& share, R& ring, const Shared& sh) {
+template <bool DOWN, int TILES, class W, class F>
+__device__ __forceinline__ void run_step(const Q4ExpertArgs& a, const Sorted& sorted, const Step& step, F& feed, const Share& share,
+                                         const Shared& sh) {
   const int warp = warp_index(), lane = threadIdx.x & 31, terms = a.terms[DOWN];
   const int S = 1 << step.log_split, group = warp >> step.log_split, member = warp & (S - 1);
   const int part_step = a.part_cols * PART_STRIDE;
@@ -338,9 +326,9 @@ __device__ __forceinline__ void run_step(const W& w, const Q4ExpertArgs& a, cons
         e = divide(u, step.slabs_inverse);
         lo = max((int)sorted.off[e], win.p0), np = min((int)sorted.off[e + 1], win.p1) - lo;
         const int tiles = (np * terms + 7) / 8;
-        if (TILES == 1 || tiles == 1) unit_products<DOWN, 1>(w, a, sorted, loader, share, ring, sh, S, member, win.p0, lo, np);
-        else if (tiles == 2) unit_products<DOWN, 2>(w, a, sorted, loader, share, ring, sh, S, member, win.p0, lo, np);
-        else unit_products<DOWN, 3>(w, a, sorted, loader, share, ring, sh, S, member, win.p0, lo, np);
+        if (TILES == 1 || tiles == 1) unit_products<DOWN, 1, W>(a, sorted, feed, share, sh, S, member, win.p0, lo, np);
+        else if (tiles == 2) unit_products<DOWN, 2, W>(a, sorted, feed, share, sh, S, member, win.p0, lo, np);
+        else unit_products<DOWN, 3, W>(a, sorted, feed, share, sh, S, member, win.p0, lo, np);
       }
       group_sync<WARPS>(group, S);
       constexpr int OUT = DOWN ? ROWS : 8;
@@ -401,6 +389,7 @@ template <class W, int TILES>
 __global__ void __launch_bounds__(THREADS, 2) experts_kernel(Q4ExpertArgs a) {
   extern __shared__ __align__(128) char smem[];
   __shared__ int2 found;  // experts in use; an id outside [-1, E)
+  __shared__ Step steps[2];
   constexpr int DEPTH = depth_of(TILES);
   const int warp = warp_index(), lane = threadIdx.x & 31, pairs = a.T * a.k;
   Shared sh;
@@ -410,10 +399,17 @@ __global__ void __launch_bounds__(THREADS, 2) experts_kernel(Q4ExpertArgs a) {
   const Sorted sorted = sorted_at(sh.rows + a.staged * a.row_stride, a.E);
   const auto token = [](int j) { return j; };
   if (pairs <= 32) {
-    if (warp == 0) sort_few(sorted, &found, a.ids, a.weights, pairs, a.E);
-    else if (a.resident) stage<false>(a, sh, a.T, (threadIdx.x >> 4) - 2, 2 * WARPS - 2, token);
+    if (warp == 0) {
+      sort_few(sorted, &found, a.ids, a.weights, pairs, a.E);
+      __syncwarp();
+      if (lane < 2) steps[lane].set(a, lane, found.x);
+    } else if (a.resident) {
+      stage<false>(a, sh, a.T, (threadIdx.x >> 4) - 2, 2 * WARPS - 2, token);
+    }
   } else {
     sort_many(sorted, &found, a.ids, a.weights, pairs, a.E);
+    __syncthreads();
+    if (threadIdx.x < 2) steps[threadIdx.x].set(a, threadIdx.x, found.x);
     if (a.resident) stage<false>(a, sh, a.T, threadIdx.x >> 4, 2 * WARPS, token);
   }
   __syncthreads();
@@ -421,24 +417,14 @@ __global__ void __launch_bounds__(THREADS, 2) experts_kernel(Q4ExpertArgs a) {
     if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, ST_CORRUPT);
     return;
   }
-  const int chunks1 = (a.columns[0] + CHUNK - 1) / CHUNK, chunks2 = (a.columns[1] + CHUNK - 1) / CHUNK;
-  Step step1, step2;
-  step1.set(a, 0, found.x);
-  step2.set(a, 1, found.x);
-  const Share share1(a.columns[0], CHUNK, chunks1, warp & ((1 << step1.log_split) - 1), step1.log_split);
-  const Share share2(a.columns[1], CHUNK, chunks2, warp & ((1 << step2.log_split) - 1), step2.log_split);
-  Ring<DEPTH, W::SLOT> ring(smem_u32(smem) + warp * (DEPTH * W::SLOT));
-  Loader<W> loader{sorted, step2, warp, lane, &step1, share1, share2, a.columns[0] % CHUNK / BLOCK, a.columns[1] % CHUNK / BLOCK,
-                   Window(0)};
-  loader.enter();
-  loader.u = loader.window.end;
-  loader.find();
-  for (int i = 0; i < DEPTH - 1; ++i) loader.next(ring, lane);
+  const Step &step1 = steps[0], &step2 = steps[1];
+  const Share share1(a.columns[0], CHUNK, warp & ((1 << step1.log_split) - 1), step1.log_split);
+  const Share share2(a.columns[1], CHUNK, warp & ((1 << step2.log_split) - 1), step2.log_split);
+  ExpertFeed<W, DEPTH> feed(Units<W>(sorted, step1, step2, warp, lane, share1, share2), smem_u32(smem) + warp * (DEPTH * W::SLOT), lane);
 
-  const W w1{nullptr, 0, a.columns[0]}, w2{nullptr, 0, a.columns[1]};
-  run_step<false, TILES>(w1, a, sorted, step1, loader, share1, ring, sh);
+  run_step<false, TILES, W>(a, sorted, step1, feed, share1, sh);
   if (!meet(a.meet, a.status)) return;
-  run_step<true, TILES>(w2, a, sorted, step2, loader, share2, ring, sh);
+  run_step<true, TILES, W>(a, sorted, step2, feed, share2, sh);
   copy_wait<0>();
   const int fours = a.columns[0] / 4, items = a.T * fours;
   auto item_of = [&](int j) { return ((j >> 3) * gridDim.x + blockIdx.x) * 8 + (j & 7); };  // 128 bytes of fp32 after the other to the CTAs
