@@ -64,13 +64,10 @@ __device__ __forceinline__ void linear_block(const W& w, const LinearArgs& a, ch
     for (int ch0 = 0, done = 0; ch0 < chunks; ch0 += a.panel, done += panel_steps) {
       if (panels || base == first) {  // activations of the panel
         const int c0 = ch0 * W::COLUMNS, c1 = min(c0 + a.panel * W::COLUMNS, (a.columns + BLOCK - 1) / BLOCK * BLOCK);
-        const int halves = 2 * WARPS / min(nt, 2 * WARPS);  // half warps to a token
-        const int half = threadIdx.x >> 4;
+        const StageArgs to{static_cast<const char*>(a.x) + t0 * a.x_stride * (a.x_type == STRATA_F32 ? 4 : 2), a.x_stride, a.x_type, a.columns,
+                           a.terms, rows, a.row_stride, scale, a.scale_stride, nullptr, 0};
         __syncthreads();
-        if (half < halves * nt)
-          stage_row<W::F16>(a.x, (t0 + half / halves) * a.x_stride, a.x_type, a.columns, c0, c1, a.terms,
-                            rows + half / halves * a.terms * a.row_stride, a.row_stride, scale + half / halves * a.scale_stride, half % halves,
-                            halves);
+        stage_rows<W::F16>(to, nt, c0, c1, threadIdx.x >> 4, 2 * WARPS);
         __syncthreads();
       }
       uint32_t b[NT];

@@ -65,20 +65,47 @@ __device__ __forceinline__ void stage8(const Raw8& raw, int type, bool in, bool 
     *reinterpret_cast<uint4*>(dst + t * stride) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
-// Columns c0 .. c1 - 1 (c0 a multiple of 128) of the row at element row0 of x, as `terms` rows at dst; behind the last column zeros, up to
-// a whole block of 32.  scale: of chunk c0 / 128 and on.  By `parts` half warps, this one `part`, a chunk each, two of them asked for at once.
+// Columns c0 .. c1 - 1 (c0 a multiple of 128) of n rows of x as `terms` rows each at dst; behind the last column zeros, up to a whole block of 32.
+// Row j is x's row j, or row index[j] / d (inverse: of d, see divide) where there is an index.  By `halves` half warps, this one `half`, a chunk of
+// a row each, four of them asked for at once.
+struct StageArgs {
+  const void* x;
+  int64_t x_stride;
+  int type, columns, terms;
+  char* rows;
+  int row_stride;
+  float* scale;
+  int scale_stride;
+  const uint16_t* index;
+  uint32_t inverse;
+};
+// n / d by inverse = ceil(2^32 / d), or 0 for d = 1; exact while n * d < 2^32.
+__device__ __forceinline__ int divide(int n, uint32_t inverse) { return inverse ? __umulhi(n, inverse) : n; }
+inline uint32_t inverse_of(int d) { return d == 1 ? 0 : (uint32_t)(((1ull << 32) + d - 1) / d); }
+
 template <bool F16>
-__device__ __noinline__ void stage_row(const void* x, int64_t row0, int type, int columns, int c0, int c1, int terms, char* dst, int stride,
-                                          float* scale, int part, int parts) {
-  const int lane = threadIdx.x & 15, all = (columns + BLOCK - 1) / BLOCK * BLOCK, n = c1 - c0;
-  for (int c = part * CHUNK; c < n; c += 2 * parts * CHUNK) {
-    const int i = c + lane * 8, j = i + parts * CHUNK;
-    const bool two = c + parts * CHUNK < n, in_i = c0 + i < columns, in_j = two && c0 + j < columns;
-    Raw8 ri{}, rj{};
-    if (in_i) ri = load8(x, row0 + c0 + i, type);
-    if (in_j) rj = load8(x, row0 + c0 + j, type);
-    stage8<F16>(ri, type, in_i, c0 + i < all, terms, dst + i * 2, stride, scale + c / CHUNK);
-    if (two) stage8<F16>(rj, type, in_j, c0 + j < all, terms, dst + j * 2, stride, scale + c / CHUNK + parts);
+__device__ __noinline__ void stage_rows(const StageArgs s, int n, int c0, int c1, int half, int halves) {
+  constexpr int AHEAD = 4;
+  const int lane = threadIdx.x & 15, all = (s.columns + BLOCK - 1) / BLOCK * BLOCK, chunks = (c1 - c0 + CHUNK - 1) / CHUNK;
+  for (int first = half; first < n * chunks; first += AHEAD * halves) {
+    Raw8 raw[AHEAD];
+    int row[AHEAD], at[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int task = first + u * halves;
+      row[u] = task / chunks;
+      at[u] = (task - row[u] * chunks) * CHUNK + lane * 8;
+      raw[u] = Raw8{};
+      if (row[u] < n && c0 + at[u] < s.columns) {
+        const int from = s.index ? divide(s.index[row[u]], s.inverse) : row[u];
+        raw[u] = load8(s.x, from * s.x_stride + c0 + at[u], s.type);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (row[u] < n)
+        stage8<F16>(raw[u], s.type, c0 + at[u] < s.columns, c0 + at[u] < all, s.terms, s.rows + row[u] * s.terms * s.row_stride + at[u] * 2,
+                    s.row_stride, s.scale + row[u] * s.scale_stride + at[u] / CHUNK);
   }
 }
 
@@ -334,6 +361,10 @@ struct Bf16 {
   }
 };
 
+// A value that all lanes of the warp hold, as one that the compiler knows they do (a reduction's result).
+__device__ __forceinline__ int uniform(int v) { return __reduce_min_sync(0xffffffffu, v); }
+__device__ __forceinline__ int warp_index() { return uniform(threadIdx.x >> 5); }
+
 // A warp's share of a unit: chunks member, member + S, ...; the last of the unit may be a shorter one.
 struct Share {
   int whole;  // its whole chunks
@@ -363,14 +394,17 @@ struct Feed {
     }
   }
   __device__ __forceinline__ void fill() {
-    if (left == 0 && tail == 0 && units.next()) cursor = units.cursor, left = units.whole, tail = units.tail, stride = units.stride;
+    if (left == 0) {  // a shorter chunk, or on to the next unit
+      if (tail == 0 && units.next()) cursor = units.cursor, left = units.whole, tail = units.tail, stride = units.stride;
+      if (left == 0 && tail) {
+        W::load_tail(used, cursor, tail, lane);
+        tail = 0;
+      }
+    }
     if (left) {
       W::load(used, cursor, lane);
       cursor.at += stride;
       --left;
-    } else if (tail) {
-      W::load_tail(used, cursor, tail, lane);
-      tail = 0;
     }
     copy_commit();
   }
@@ -408,9 +442,6 @@ __device__ __forceinline__ void run_chunks(F& feed, int whole, int tail, int S, 
     W::template tail<NT>(slot, (tail + BLOCK - 1) / BLOCK, b, v, feed.lane, acc);
   }
 }
-// Of the calling thread's warp, known to be the same for all its lanes.
-__device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0); }
-
 // A warp's sums to its place in shared memory, [column][16 rows].
 template <int NT>
 __device__ __forceinline__ void store_part(float* part, int lane, const float (&acc)[NT][4]) {

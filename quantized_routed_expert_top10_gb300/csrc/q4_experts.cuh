@@ -150,10 +150,6 @@ static __device__ __noinline__ void sort_many(const Sorted& s, int2* found, cons
     if (id[j] >= 0) s.pair[s.count[id[j]] + rank[j]] = tid + j * THREADS;
 }
 
-// n / d by inverse = ceil(2^32 / d), exact while n * d < 2^32.
-__device__ __forceinline__ int divide(int n, uint32_t inverse) { return inverse ? __umulhi(n, inverse) : n; }
-inline uint32_t inverse_of(int d) { return d == 1 ? 0 : (uint32_t)(((1ull << 32) + d - 1) / d); }
-
 // A step's units as this CTA and this warp take them: of at most 2^20 (1,024 experts of 1,024) an equal contiguous stretch a CTA.
 struct Step {
   const uint8_t* base;
@@ -294,15 +290,12 @@ __device__ __forceinline__ void unit_products(const Q4ExpertArgs& a, const Sorte
   store_part<NT>(sh.part + warp * (a.part_cols * PART_STRIDE), lane, acc);
 }
 
-// The terms of n rows by `halves` half warps, this one `half`; source(j) is row j's number in x or h.
-template <bool DOWN, class F>
-__device__ __forceinline__ void stage(const Q4ExpertArgs& a, const Shared& sh, int n, int half, int halves, F source) {
-  const int per = n < halves ? halves / n : 1, at_once = halves / per;  // half warps to a row
-  if (half >= at_once * per) return;
-  for (int j = half / per; j < n; j += at_once)
-    stage_row<true>(DOWN ? a.h : a.x, (int64_t)source(j) * (DOWN ? a.columns[1] : a.x_stride), DOWN ? STRATA_F32 : a.x_type,
-                    a.columns[DOWN], 0, a.columns[DOWN], a.terms[DOWN], sh.rows + j * a.terms[DOWN] * a.row_stride, a.row_stride,
-                    sh.scale + j * a.scale_stride, half % per, per);
+// The terms of n rows of x or h by `halves` half warps, this one `half`: of all tokens, or of the sorted pairs from `pair` on.
+template <bool DOWN>
+__device__ __forceinline__ void stage(const Q4ExpertArgs& a, const Shared& sh, const uint16_t* pair, int n, int half, int halves) {
+  const StageArgs to{DOWN ? a.h : a.x, DOWN ? a.columns[1] : a.x_stride, DOWN ? STRATA_F32 : a.x_type, a.columns[DOWN], a.terms[DOWN],
+                     sh.rows, a.row_stride, sh.scale, a.scale_stride, pair, DOWN ? 0u : a.k_inverse};
+  stage_rows<true>(to, n, 0, a.columns[DOWN], half, halves);
 }
 
 // Step 1 or 2 for this CTA's stretch.
@@ -315,8 +308,7 @@ __device__ __forceinline__ void run_step(const Q4ExpertArgs& a, const Sorted& so
   for (Window win(step.u0); win.next(step, sorted);) {
     if (DOWN || !a.resident) {
       __syncthreads();
-      stage<DOWN>(a, sh, win.p1 - win.p0, threadIdx.x >> 4, 2 * WARPS,
-                  [&](int j) { return DOWN ? (int)sorted.pair[win.p0 + j] : divide(sorted.pair[win.p0 + j], a.k_inverse); });
+      stage<DOWN>(a, sh, sorted.pair + win.p0, win.p1 - win.p0, threadIdx.x >> 4, 2 * WARPS);
       __syncthreads();
     }
     for (int base = win.begin; base < win.end; base += step.n_group) {
@@ -397,20 +389,19 @@ __global__ void __launch_bounds__(THREADS, 2) experts_kernel(Q4ExpertArgs a) {
   sh.scale = sh.part + WARPS * a.part_cols * PART_STRIDE;
   sh.rows = reinterpret_cast<char*>(sh.scale + a.staged * a.scale_stride);
   const Sorted sorted = sorted_at(sh.rows + a.staged * a.row_stride, a.E);
-  const auto token = [](int j) { return j; };
   if (pairs <= 32) {
     if (warp == 0) {
       sort_few(sorted, &found, a.ids, a.weights, pairs, a.E);
       __syncwarp();
       if (lane < 2) steps[lane].set(a, lane, found.x);
     } else if (a.resident) {
-      stage<false>(a, sh, a.T, (threadIdx.x >> 4) - 2, 2 * WARPS - 2, token);
+      stage<false>(a, sh, nullptr, a.T, (threadIdx.x >> 4) - 2, 2 * WARPS - 2);
     }
   } else {
     sort_many(sorted, &found, a.ids, a.weights, pairs, a.E);
     __syncthreads();
     if (threadIdx.x < 2) steps[threadIdx.x].set(a, threadIdx.x, found.x);
-    if (a.resident) stage<false>(a, sh, a.T, threadIdx.x >> 4, 2 * WARPS, token);
+    if (a.resident) stage<false>(a, sh, nullptr, a.T, threadIdx.x >> 4, 2 * WARPS);
   }
   __syncthreads();
   if (found.y) {  // the same in every CTA
