@@ -45,7 +45,7 @@ constexpr int WARPS = 8, THREADS = 32 * WARPS;  // two CTAs an SM, one of which 
 // chunks of a warp's ring: as many as leave room for 8 rows of 2,560 columns' terms (24 where blocks are larger, one CTA an SM)
 constexpr int depth_of(int tiles) { return tiles == 1 ? 7 : 5; }
 constexpr int PAIRS_MAX = STRATA_Q4_EXPERTS_T_MAX * STRATA_Q4_EXPERTS_K_MAX;
-constexpr int PER_THREAD = PAIRS_MAX / THREADS, E_PER_THREAD = STRATA_Q4_EXPERTS_E_MAX / THREADS;
+constexpr int SORT_WARPS = 2, SORT_PER = 4;  // that sort up to 256 pairs while the others lay out x
 static_assert(PAIRS_MAX < 65536 && PAIRS_MAX % THREADS == 0 && STRATA_Q4_EXPERTS_E_MAX % THREADS == 0, "sorting of the pairs");
 
 // The pairs by expert: expert[a], its pairs pair[off[a]] .. pair[off[a + 1] - 1], a < n.
@@ -90,33 +90,37 @@ __device__ __forceinline__ void sort_few(const Sorted& s, int2* found, const int
     *found = make_int2(__popc(firsts), bad);
   }
 }
-// Any number, by the whole CTA.
+// Up to N * PER pairs, by the CTA's first N threads.
+template <int N, int PER>
 static __device__ __noinline__ void sort_many(const Sorted& s, int2* found, const int32_t* ids, const float* weights, int pairs, int E) {
-  __shared__ int warp_sum[WARPS];
+  __shared__ int warp_sum[N / 32];
+  constexpr int E_PER = STRATA_Q4_EXPERTS_E_MAX / N;
+  const auto sync = [] { named_barrier(15, N); };
   const int tid = threadIdx.x, lane = tid & 31, warp = warp_index();
-  int id[PER_THREAD], rank[PER_THREAD];
-  float weight[PER_THREAD];
+  int id[PER], rank[PER];
+  float weight[PER];
 #pragma unroll
-  for (int j = 0; j < PER_THREAD; ++j) {
-    const int p = tid + j * THREADS;
+  for (int j = 0; j < PER; ++j) {
+    const int p = tid + j * N;
     id[j] = p < pairs ? ids[p] : -1;
     weight[j] = p < pairs ? weights[p] : 0.f;
   }
-  for (int e = tid; e < E; e += THREADS) s.count[e] = 0;
-  __syncthreads();
+  for (int e = tid; e < E; e += N) s.count[e] = 0;
+  sync();
   bool bad = false;
 #pragma unroll
-  for (int j = 0; j < PER_THREAD; ++j) {
+  for (int j = 0; j < PER; ++j) {
     bad |= id[j] < -1 || id[j] >= E;
     if (id[j] < 0 || id[j] >= E || weight[j] == 0.f) id[j] = -1;
     else rank[j] = atomicAdd(&s.count[id[j]], 1);
   }
-  bad = __syncthreads_or(bad);
+  if (__any_sync(0xffffffffu, bad) && lane == 0) found->y = 1;  // 0 before
+  sync();
   // sums before each expert of the pairs (low half) and of the experts in use (high half); consecutive experts a thread
-  const int e0 = E_PER_THREAD * tid;
-  int c[E_PER_THREAD], mine = 0;
+  const int e0 = E_PER * tid;
+  int c[E_PER], mine = 0;
 #pragma unroll
-  for (int j = 0; j < E_PER_THREAD; ++j) {
+  for (int j = 0; j < E_PER; ++j) {
     c[j] = e0 + j < E ? s.count[e0 + j] : 0;
     mine += c[j] + ((c[j] > 0) << 16);
   }
@@ -127,27 +131,27 @@ static __device__ __noinline__ void sort_many(const Sorted& s, int2* found, cons
     if (lane >= o) v += up;
   }
   if (lane == 31) warp_sum[warp] = v;
-  __syncthreads();
+  sync();
   int before = v - mine, all = 0;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
+  for (int w = 0; w < N / 32; ++w) {
     if (w < warp) before += warp_sum[w];
     all += warp_sum[w];
   }
 #pragma unroll
-  for (int j = 0; j < E_PER_THREAD; ++j) {
+  for (int j = 0; j < E_PER; ++j) {
     if (c[j]) s.expert[before >> 16] = e0 + j, s.off[before >> 16] = before & 0xffff;
     if (e0 + j < E) s.count[e0 + j] = before & 0xffff;
     before += c[j] + ((c[j] > 0) << 16);
   }
   if (tid == 0) {
     s.off[all >> 16] = all & 0xffff;
-    *found = make_int2(all >> 16, bad);
+    found->x = all >> 16;
   }
-  __syncthreads();
+  sync();
 #pragma unroll
-  for (int j = 0; j < PER_THREAD; ++j)  // the order within an expert does not matter: a pair's sums are its own column's
-    if (id[j] >= 0) s.pair[s.count[id[j]] + rank[j]] = tid + j * THREADS;
+  for (int j = 0; j < PER; ++j)  // the order within an expert does not matter: a pair's sums are its own column's
+    if (id[j] >= 0) s.pair[s.count[id[j]] + rank[j]] = tid + j * N;
 }
 
 // A step's units as this CTA and this warp take them: of at most 2^20 (1,024 experts of 1,024) an equal contiguous stretch a CTA.
@@ -268,15 +272,15 @@ struct Shared {  // the CTA's dynamic shared memory behind the rings
 };
 
 // Sums of unit u of the expert whose pairs in the window are lo .. lo + np - 1.
-template <bool DOWN, int NT, class W, class F>
-__device__ __forceinline__ void unit_products(const Q4ExpertArgs& a, const Sorted& sorted, F& feed, const Share& share, const Shared& sh, int S,
-                                              int member, int p0, int lo, int np) {
-  const int warp = warp_index(), lane = feed.lane, shift = a.terms[DOWN] - 1;  // one or two terms
+template <int NT, class W, class F>
+__device__ __forceinline__ void unit_products(const Q4ExpertArgs& a, const Sorted& sorted, F& feed, const Share& share, const Shared& sh, bool down,
+                                              int S, int member, int p0, int lo, int np) {
+  const int warp = warp_index(), lane = feed.lane, shift = a.terms[down] - 1;  // one or two terms
   uint32_t b[NT];
   uint2 cs[NT];
   auto row_of = [&](int j) {  // of pair lo + j among those in shared memory
     j = min(j, np - 1);       // columns behind the last read some row; their sums are not used
-    return !DOWN && a.resident ? divide(sorted.pair[lo + j], a.k_inverse) : lo + j - p0;
+    return !down && a.resident ? divide(sorted.pair[lo + j], a.k_inverse) : lo + j - p0;
   };
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -291,24 +295,23 @@ __device__ __forceinline__ void unit_products(const Q4ExpertArgs& a, const Sorte
 }
 
 // The terms of n rows of x or h by `halves` half warps, this one `half`: of all tokens, or of the sorted pairs from `pair` on.
-template <bool DOWN>
-__device__ __forceinline__ void stage(const Q4ExpertArgs& a, const Shared& sh, const uint16_t* pair, int n, int half, int halves) {
-  const StageArgs to{DOWN ? a.h : a.x, DOWN ? a.columns[1] : a.x_stride, DOWN ? STRATA_F32 : a.x_type, a.columns[DOWN], a.terms[DOWN],
-                     sh.rows, a.row_stride, sh.scale, a.scale_stride, pair, DOWN ? 0u : a.k_inverse};
-  stage_rows<true>(to, n, 0, a.columns[DOWN], half, halves);
+__device__ __forceinline__ void stage(const Q4ExpertArgs& a, const Shared& sh, bool down, const uint16_t* pair, int n, int half, int halves) {
+  const StageArgs to{down ? a.h : a.x, down ? a.columns[1] : a.x_stride, down ? STRATA_F32 : a.x_type, a.columns[down], a.terms[down],
+                     sh.rows, a.row_stride, sh.scale, a.scale_stride, pair, down ? 0u : a.k_inverse};
+  stage_rows<true>(to, n, 0, a.columns[down], half, halves);
 }
 
-// Step 1 or 2 for this CTA's stretch.
-template <bool DOWN, int TILES, class W, class F>
+// Step 1 or 2 for this CTA's stretch: one code for both, so that the second finds its instructions at hand.
+template <int TILES, class W, class F>
 __device__ __forceinline__ void run_step(const Q4ExpertArgs& a, const Sorted& sorted, const Step& step, F& feed, const Share& share,
-                                         const Shared& sh) {
-  const int warp = warp_index(), lane = threadIdx.x & 31, terms = a.terms[DOWN];
+                                         const Shared& sh, bool down) {
+  const int warp = warp_index(), lane = threadIdx.x & 31, terms = a.terms[down];
   const int S = 1 << step.log_split, group = warp >> step.log_split, member = warp & (S - 1);
   const int part_step = a.part_cols * PART_STRIDE;
   for (Window win(step.u0); win.next(step, sorted);) {
-    if (DOWN || !a.resident) {
+    if (down || !a.resident) {
       __syncthreads();
-      stage<DOWN>(a, sh, sorted.pair + win.p0, win.p1 - win.p0, threadIdx.x >> 4, 2 * WARPS);
+      stage(a, sh, down, sorted.pair + win.p0, win.p1 - win.p0, threadIdx.x >> 4, 2 * WARPS);
       __syncthreads();
     }
     for (int base = win.begin; base < win.end; base += step.n_group) {
@@ -318,19 +321,19 @@ __device__ __forceinline__ void run_step(const Q4ExpertArgs& a, const Sorted& so
         e = divide(u, step.slabs_inverse);
         lo = max((int)sorted.off[e], win.p0), np = min((int)sorted.off[e + 1], win.p1) - lo;
         const int tiles = (np * terms + 7) / 8;
-        if (TILES == 1 || tiles == 1) unit_products<DOWN, 1, W>(a, sorted, feed, share, sh, S, member, win.p0, lo, np);
-        else if (tiles == 2) unit_products<DOWN, 2, W>(a, sorted, feed, share, sh, S, member, win.p0, lo, np);
-        else unit_products<DOWN, 3, W>(a, sorted, feed, share, sh, S, member, win.p0, lo, np);
+        if (TILES == 1 || tiles == 1) unit_products<1, W>(a, sorted, feed, share, sh, down, S, member, win.p0, lo, np);
+        else if (tiles == 2) unit_products<2, W>(a, sorted, feed, share, sh, down, S, member, win.p0, lo, np);
+        else unit_products<3, W>(a, sorted, feed, share, sh, down, S, member, win.p0, lo, np);
       }
       group_sync<WARPS>(group, S);
-      constexpr int OUT = DOWN ? ROWS : 8;
+      const int out = down ? 4 : 3;  // 16 or 8 rows
       const float* sums = sh.part + group * S * part_step;
-      const int row_len = a.columns[!DOWN];
-      float* to = (DOWN ? a.parts : a.h) + (u - e * step.slabs) * OUT;
-      for (int i = member * 32 + lane; i < np * OUT; i += S * 32) {
-        const int j = i / OUT, row = i % OUT;
+      const int row_len = a.columns[!down];
+      float* to = (down ? a.parts : a.h) + ((u - e * step.slabs) << out);
+      for (int i = member * 32 + lane; i < np << out; i += S * 32) {
+        const int j = i >> out, row = i & ((1 << out) - 1);
         float v = sum_part(sums, part_step, S, terms, j, row);
-        if (!DOWN) v = silu_mul(v, sum_part(sums, part_step, S, terms, j, row + 8));
+        if (!down) v = silu_mul(v, sum_part(sums, part_step, S, terms, j, row + 8));
         to[(int64_t)sorted.pair[lo + j] * row_len + row] = v;
       }
       group_sync<WARPS>(group, S);
@@ -395,13 +398,22 @@ __global__ void __launch_bounds__(THREADS, 2) experts_kernel(Q4ExpertArgs a) {
       __syncwarp();
       if (lane < 2) steps[lane].set(a, lane, found.x);
     } else if (a.resident) {
-      stage<false>(a, sh, nullptr, a.T, (threadIdx.x >> 4) - 2, 2 * WARPS - 2);
+      stage(a, sh, false, nullptr, a.T, (threadIdx.x >> 4) - 2, 2 * WARPS - 2);
     }
   } else {
-    sort_many(sorted, &found, a.ids, a.weights, pairs, a.E);
-    __syncthreads();
-    if (threadIdx.x < 2) steps[threadIdx.x].set(a, threadIdx.x, found.x);
-    if (a.resident) stage<false>(a, sh, nullptr, a.T, threadIdx.x >> 4, 2 * WARPS);
+    if (threadIdx.x == 0) found.y = 0;
+    if (pairs <= 32 * SORT_WARPS * SORT_PER) {
+      if (warp < SORT_WARPS) {
+        sort_many<32 * SORT_WARPS, SORT_PER>(sorted, &found, a.ids, a.weights, pairs, a.E);
+        if (threadIdx.x < 2) steps[threadIdx.x].set(a, threadIdx.x, found.x);
+      } else if (a.resident) {
+        stage(a, sh, false, nullptr, a.T, (threadIdx.x >> 4) - 2 * SORT_WARPS, 2 * (WARPS - SORT_WARPS));
+      }
+    } else {
+      sort_many<THREADS, PAIRS_MAX / THREADS>(sorted, &found, a.ids, a.weights, pairs, a.E);
+      if (threadIdx.x < 2) steps[threadIdx.x].set(a, threadIdx.x, found.x);
+      if (a.resident) stage(a, sh, false, nullptr, a.T, threadIdx.x >> 4, 2 * WARPS);
+    }
   }
   __syncthreads();
   if (found.y) {  // the same in every CTA
@@ -413,9 +425,9 @@ __global__ void __launch_bounds__(THREADS, 2) experts_kernel(Q4ExpertArgs a) {
   const Share share2(a.columns[1], CHUNK, warp & ((1 << step2.log_split) - 1), step2.log_split);
   ExpertFeed<W, DEPTH> feed(Units<W>(sorted, step1, step2, warp, lane, share1, share2), smem_u32(smem) + warp * (DEPTH * W::SLOT), lane);
 
-  run_step<false, TILES, W>(a, sorted, step1, feed, share1, sh);
+  run_step<TILES, W>(a, sorted, step1, feed, share1, sh, false);
   if (!meet(a.meet, a.status)) return;
-  run_step<true, TILES, W>(a, sorted, step2, feed, share2, sh);
+  run_step<TILES, W>(a, sorted, step2, feed, share2, sh, true);
   copy_wait<0>();
   const int fours = a.columns[0] / 4, items = a.T * fours;
   auto item_of = [&](int j) { return ((j >> 3) * gridDim.x + blockIdx.x) * 8 + (j & 7); };  // 128 bytes of fp32 after the other to the CTAs
