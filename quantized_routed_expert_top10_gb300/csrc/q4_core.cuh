@@ -41,11 +41,10 @@ __device__ __forceinline__ void stage8(const Raw8& raw, int type, bool in, bool 
   float f[8] = {};
   if (in) widen8(raw, type, f);
   if (F16) {
-    uint32_t top = 0;
+    float most = 0.f;  // a NaN counts for nothing here and stays one
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
-#pragma unroll
-    for (int o = 8; o; o /= 2) top = max(top, __shfl_xor_sync(0xffffu << (threadIdx.x & 16), top, o));
+    for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(f[j]));
+    const uint32_t top = __reduce_max_sync(0xffffu << (threadIdx.x & 16), __float_as_uint(most));
     const uint32_t e = max(top >> 23, 15u);  // 2^(e - 127) <= largest; below 2^-112 all count as 2^-112
     const float up = __uint_as_float((268u - e) << 23);
     if ((threadIdx.x & 15) == 0) *scale = __uint_as_float((e - 14u) << 23);

@@ -202,3 +202,48 @@ def test_packing_then_using_the_weights_at_once():
         qre.strata_pack_q4_device(m.q, codes, scales, None, packed)
         qre.strata_moe_linear(qre.linear_q4(m.q, packed), x, 1, None, y)
         assert torch.equal(y, want)
+
+
+def test_offsets_beyond_32_bits():
+    """Rows of x, y and bf16 weights more than 2^32 bytes apart."""
+    step = (1 << 30) + 8
+    big = torch.empty(4 * step + 4096, dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(DEV).manual_seed(3)
+    x = torch.as_strided(big, (5, 64), (step, 1))
+    x.copy_(torch.randn(5, 64, generator=g, device=DEV))
+    want_x = x.clone()
+    for n_out, w in ((40, None), (5, torch.as_strided(big, (5, 64), (step, 1), 256))):
+        y = torch.as_strided(big, (5, n_out), (step, 1), 1024)
+        if w is None:
+            m = q4ref.Matrices(1, n_out, 64, 32)
+            packed = m.packed(DEV)
+            d = qre.linear_q4(m.q, packed, qre.BF16, qre.BF16, step, step)
+            dense = qre.linear_q4(m.q, packed, qre.BF16, qre.BF16)
+        else:
+            w.copy_(torch.randn(5, 64, generator=g, device=DEV))
+            rows_w = w.contiguous()
+            d = qre.linear_bf16(w.data_ptr(), n_out, 64, qre.BF16, qre.BF16, step, step, step)
+            dense = qre.linear_bf16(rows_w, n_out, 64, qre.BF16, qre.BF16)
+        want = torch.empty(5, n_out, dtype=torch.bfloat16, device=DEV)
+        qre.strata_moe_linear(d, x.data_ptr(), 5, None, y.data_ptr())
+        qre.strata_moe_linear(dense, want_x, 5, None, want)
+        assert torch.equal(y, want)
+
+
+def test_on_a_stream_beside_others():
+    """Calls of two streams at once, each with its own rows."""
+    m = q4ref.Matrices(1, 3000, 1024, 128)
+    packed = m.packed(DEV)
+    d = qre.linear_q4(m.q, packed)
+    xs = [rows(T, 1024, 0, qre.F32, T) for T in (1, 7, 30)]
+    want = [torch.empty(x.shape[0], 3000, device=DEV) for x in xs]
+    got = [torch.empty_like(w) for w in want]
+    for x, w in zip(xs, want):
+        qre.strata_moe_linear(d, x, x.shape[0], None, w)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(10):
+        for s, x, y in zip(streams, xs, got):
+            qre.strata_moe_linear(d, x, x.shape[0], None, y, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -252,3 +252,44 @@ def test_workspace_shared_with_a_decode_layer():
     layer.call(rows(4, 128, 0, qre.F32, 5), ids, w, out, ws)
     assert qre.strata_poll_status(ws) == 0
     assert torch.equal(ws[:1 << 20], keep)
+
+
+def test_offsets_beyond_32_bits():
+    """Experts and rows more than 2^32 bytes apart."""
+    layer = Layer(3, 64, 32, k=2, xk=qre.BF16, ok=qre.BF16)
+    ids, w = lists(5, 3, 2)
+    x, want = rows(5, 64, 0, qre.BF16, 5), torch.empty(5, 64, dtype=torch.bfloat16, device=DEV)
+    layer.call(x, ids, w, want, layer.workspace(5))
+    step = (1 << 32) + 256
+    big = torch.empty(4 * step + 65536, dtype=torch.uint8, device=DEV)
+    for e in range(3):
+        for i, p in enumerate(layer.packed):
+            big[e * step + 8192 * i:e * step + 8192 * i + p.shape[1]] = p[e]
+    assert max(p.shape[1] for p in layer.packed) <= 8192
+    halves = big.view(torch.bfloat16)
+    far_x, out = (torch.as_strided(halves, (5, 64), (step // 2, 1), at) for at in (10240, 12288))
+    far_x.copy_(x)
+    d = layer.d
+    layer.d = qre.q4_experts(layer.gu.q, big.data_ptr(), layer.dn.q, big.data_ptr() + 8192, 3, 2, qre.BF16, qre.BF16, step, step,
+                             step // 2, step // 2)
+    ws = layer.workspace(5)
+    qre.strata_moe_q4_experts(layer.d, torch.from_numpy(ids).to(DEV), torch.from_numpy(w).to(DEV), far_x.data_ptr(), 5, out.data_ptr(), ws)
+    assert qre.strata_poll_status(ws) == 0
+    assert torch.equal(out, want)
+    layer.d = d
+
+
+def test_many_calls_in_a_row_on_one_workspace():
+    """Token counts, shapes and lists change from call to call: the meetings' counters are 0 again after each."""
+    layers = [Layer(6, 128, 64, k=2), Layer(9, 256, 96, k=3, xk=qre.BF16, ok=qre.BF16, zeros=True)]
+    ws = torch.zeros(max(qre.strata_moe_q4_experts_workspace_bytes(x.d, 64) for x in layers), dtype=torch.uint8, device=DEV)
+    for i in range(40):
+        layer, T = layers[i % 2], (1, 5, 64, 2, 17)[i % 5]
+        ids, w = lists(T, layer.E, layer.k, seed=i)
+        x = rows(T, layer.d_model, 0, layer.xk, i)
+        got, want = (torch.empty(T, layer.d_model, dtype=ref.TORCH[layer.ok], device=DEV) for _ in range(2))
+        layer.call(x, ids, w, got, ws)
+        layer.call(x, ids, w, want, layer.workspace(T))
+        assert torch.equal(got, want), (i, T)
+    assert qre.strata_poll_status(ws) == 0
+    assert int(ws[8192:8192 + 12].sum()) == 0
