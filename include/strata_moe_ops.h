@@ -235,7 +235,8 @@ typedef struct strata_linear {
 
 /* y[t][n] = sum over k of w[n][k] * x[t][k] + bias[n].  bias fp32 [n_out] or NULL.  x on a 16-byte boundary, y aligned to its elements;
  * y must not overlap x.  No workspace.  Products are exact and their sums fp32; an fp32 x enters them with 22 bits beside 4-bit weights (24
- * beside bf16 ones), a bf16 or fp16 x with all its bits, each down to 2^-40 of the largest of its 128 columns.  A token whose x holds a NaN or an infinity (beside bf16 weights: or a number that rounds to bf16's infinity)
+ * beside bf16 ones), a bf16 or fp16 x with all its bits, each down to 2^-40 of the
+ * largest of the 128 columns around it.  A token whose x holds a NaN or an infinity (beside bf16 weights: or a number that rounds to bf16's infinity)
  * may give NaN in its whole row; other tokens' rows do not change.
  * Built for few tokens: 4-bit weights are read once for up to 24 (16-bit x) or 12 (fp32) of them, bf16 weights for 24 (bf16), 12 (fp16) or 8 (fp32),
  * and the time of more grows in proportion. */
@@ -273,7 +274,8 @@ size_t strata_moe_q4_experts_workspace_bytes(const strata_q4_experts_t* ex, int3
  * Products are exact and summed in fp32 as in strata_moe_linear; the hidden values of an expert are held in fp32 and enter the
  * second product with 22 bits, with 11 for a bf16 out.  NaN and infinities as there.
  * An id outside [-1, n_expert) sets STRATA_E_CORRUPT in the workspace's status word and the call computes nothing (out keeps its contents).
- * Calls that share a workspace must not overlap in time. */
+ * Calls that share a workspace must not overlap in time.  One cooperative launch, whose CTAs wait for one another; a wait of more than 2 s sets
+ * STRATA_E_TIMEOUT, and the workspace must then be initialised again. */
 strata_status strata_moe_q4_experts(const strata_q4_experts_t* ex, const int32_t* ids, const float* weights, const void* x, int32_t T,
                                     void* out, void* ws, size_t ws_bytes, void* stream);
 

@@ -1,15 +1,18 @@
-// What the kernels of strata_moe_linear and strata_moe_q4_experts share: weights streamed through a ring that each lane
-// keeps for itself, 4-bit codes widened to bf16, products by mma.m16n8k16 and the activations' bf16 terms.
+// What the kernels of strata_moe_linear and strata_moe_q4_experts share: weights streamed through a ring that each warp keeps for itself, codes
+// widened in registers, products by warp-level MMAs with terms of the activations.
 //
-// Mathematics.  y[row] = sum over groups of s[row][group] * (sum over its columns of (code - zero) * x).  code - zero is a whole
-// number of magnitude below 16, exact in fp16; x enters as fp16 terms (stage_row), each a column of the products, so the products are
-// exact and their sums fp32; the scale multiplies a group's fp32 sum, the activations' power of two a chunk's.
-// What bounds it: the weights' bytes, each read once and by no other warp, and close behind them the instructions that widen the codes.
-// 16 rows x 128 columns (1 KB) leave a scheduler 176 cycles at the measured copy rate; widening takes 5 integer instructions a word of 8 codes
-// (2 cycles each) and 4 subtractions, 8 words a lane: 80 cycles of the integer pipe.  (bf16 operands, with 7 mantissa bits, take 7: at 155
-// integer instructions a chunk with everything around them 2.7 TB/s were all that came.)  An MMA takes 8 cycles (measured, with 4 warps a
-// scheduler), 8 a chunk and tile of 8 columns, so two tiles are hidden.  Warp-level MMAs take the operands where widening leaves them, in
-// registers; tcgen05 would have four times the codes' bytes pass shared memory.
+// Mathematics.  y[row] = sum over groups of s[row][group] * (sum over its columns of (code - zero) * x).  code - zero is a whole number of magnitude
+// below 16, exact in fp16; x enters as fp16 terms (stage8), each a column of the products, so the products are exact and their sums fp32; the
+// scale multiplies a group's fp32 sum, the activations' power of two a chunk's.
+// What bounds it: the instructions around the codes, close above the weights' bytes.  16 rows x 128 columns (1 KB) leave a scheduler 176 cycles at
+// the measured copy rate.  Widening takes 5 integer instructions a word of 8 codes (2 cycles each) and 4 subtractions, 8 words a lane: 80 cycles of the
+// integer pipe; with scales, sums and copies a chunk comes to 176 instructions (2,560 -> 131,072 rows, one token: 189 MB in 41.5 us, 4.6 TB/s).  bf16
+// operands, with 7 mantissa bits, take 7 integer instructions a word: 57 us.  An MMA takes 8 cycles (measured, with 4 warps a scheduler), 8 of them
+// a chunk and tile of 8 columns, so two tiles are hidden.  Warp-level MMAs take the operands where widening leaves them, in registers; tcgen05 would
+// have four times the codes' bytes pass shared memory.
+// Tried and not kept: codes as e4m3 bytes (a code in the low bits of a byte is code * 2^-9 without further work): mma.sync of e4m3 turns into
+// conversions and fp16 MMAs here, 215 instructions a chunk; codes as fp16 subnormals, with the zero point in the MMA's starting value: 157
+// instructions, the same time, and more work on x.
 #pragma once
 #include "device_common.cuh"
 #include "elements.cuh"
