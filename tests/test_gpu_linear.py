@@ -185,6 +185,12 @@ def test_weights_packed_on_the_host_and_on_the_device_agree():
     for group, zeros, paired in itertools.product((32, 64, 128), (False, True), (False, True)):
         m = q4ref.Matrices(3, 112, 640 if group == 128 else 320, group, zeros, paired=paired)
         assert torch.equal(m.packed(DEV).cpu(), m.packed_host())
+        # codes on any byte
+        odd = torch.empty(m.codes.numel() + 1, dtype=torch.uint8, device=DEV)
+        odd[1:] = m.codes.flatten().to(DEV)
+        to = torch.empty(3, qre.strata_q4_bytes(m.q), dtype=torch.uint8, device=DEV)
+        qre.strata_pack_q4_device(m.q, odd[1:], m.scales.to(DEV), None if m.zeros is None else m.zeros.to(DEV), to, 3)
+        assert torch.equal(to.cpu(), m.packed_host())
 
 
 def test_packing_then_using_the_weights_at_once():
