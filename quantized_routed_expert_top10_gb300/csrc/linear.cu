@@ -46,20 +46,21 @@ __device__ __forceinline__ void linear_block(const W& w, const LinearArgs& a, ch
   const int S = 1 << a.log_split, group = warp >> a.log_split, member = warp & (S - 1), n_group = WARPS >> a.log_split;
   const int units = (a.rows + ROWS - 1) / ROWS, chunks = (a.columns + W::COLUMNS - 1) / W::COLUMNS;
   const Share share(a.columns, W::COLUMNS, member, a.log_split);
-  const int first = blockIdx.x * n_group, pass = gridDim.x * n_group;
+  // the CTA's units lie gridDim.x apart, so that all CTAs have as many of them, or one more
+  const int first = blockIdx.x, pass = gridDim.x * n_group;
   const int cols = nt * a.terms;
 
   float* part = reinterpret_cast<float*>(smem + WARPS * DEPTH * W::SLOT);
   const int part_step = a.part_cols * PART_STRIDE;
   float* scale = part + WARPS * part_step;
   char* rows = reinterpret_cast<char*>(scale + a.tokens * a.scale_stride);
-  Feed<W, DEPTH, Units<W>> feed(Units<W>{w, first + group, units, pass, member, lane, share.whole, share.tail, S * W::BYTES},
+  Feed<W, DEPTH, Units<W>> feed(Units<W>{w, first + group * (int)gridDim.x, units, pass, member, lane, share.whole, share.tail, S * W::BYTES},
                                 smem_u32(smem) + warp * (DEPTH * W::SLOT), lane);
 
   const int panel_steps = a.panel >> a.log_split;
   const bool panels = a.panel < chunks;
   for (int base = first; base < units; base += pass) {
-    const int u = base + group;
+    const int u = base + group * (int)gridDim.x;
     float acc[NT][4] = {};
     for (int ch0 = 0, done = 0; ch0 < chunks; ch0 += a.panel, done += panel_steps) {
       if (panels || base == first) {  // activations of the panel
@@ -142,8 +143,7 @@ cudaError_t launch_tiles(const W& w, LinearArgs a, cudaStream_t s) {
   err = allow_smem<linear_kernel<W, TILES, WARPS, DEPTH>>(SMEM_MAX);
   if (err != cudaSuccess) return err;
   for (a.log_split = 0; 1 << a.log_split < split;) ++a.log_split;
-  const int n_group = WARPS / split, most = (units + n_group - 1) / n_group;
-  STRATA_LAUNCH(KID_LINEAR, s, err = launch_pdl(linear_kernel<W, TILES, WARPS, DEPTH>, dim3(most < gx_most ? most : gx_most, gy),
+  STRATA_LAUNCH(KID_LINEAR, s, err = launch_pdl(linear_kernel<W, TILES, WARPS, DEPTH>, dim3(units < gx_most ? units : gx_most, gy),
                                                 dim3(32 * WARPS), bytes(), s, w, a));
   return err;
 }
