@@ -219,7 +219,8 @@ strata_status strata_moe_linear(const strata_linear_t* li, const void* x, int32_
   if (li->x_stride % 8 || !aligned(li->w, 16) || !aligned(x, 16) || !aligned(y, type_bytes(li->y_type)) || !aligned(bias, 4))
     return STRATA_E_ALIGN;
   if (T == 0) return STRATA_OK;
-  if (overlap(rows_of(x, T, li->x_stride, q.d_in, li->x_type), rows_of(y, T, li->y_stride, q.n_out, li->y_type)))
+  const Rows sy = rows_of(y, T, li->y_stride, q.n_out, li->y_type);
+  if (overlap(rows_of(x, T, li->x_stride, q.d_in, li->x_type), sy) || overlap(rows_of(bias, 1, q.n_out, q.n_out, STRATA_F32), sy))
     return STRATA_E_INVAL;
   return launched(launch_linear(*li, x, T, bias, y, (cudaStream_t)stream));
 }
@@ -238,8 +239,11 @@ strata_status strata_moe_q4_experts(const strata_q4_experts_t* ex, const int32_t
   // the scratch lies behind the words that other calls keep in a workspace from call to call
   if (ws_bytes < DX_END + q4_experts_scratch(*ex, T)) return STRATA_E_WORKSPACE;
   if (T == 0) return STRATA_OK;
-  const int d = ex->gate_up_q4.d_in;
-  if (overlap(rows_of(x, T, ex->x_stride, d, ex->x_type), rows_of(out, T, ex->out_stride, d, ex->out_type))) return STRATA_E_INVAL;
+  const int d = ex->gate_up_q4.d_in, pairs = T * ex->top_k;
+  const Rows so = rows_of(out, T, ex->out_stride, d, ex->out_type);
+  if (overlap(rows_of(x, T, ex->x_stride, d, ex->x_type), so) || overlap(rows_of(ids, 1, pairs, pairs, STRATA_F32), so) ||
+      overlap(rows_of(weights, 1, pairs, pairs, STRATA_F32), so))
+    return STRATA_E_INVAL;
   return launched(launch_q4_experts(*ex, ids, weights, x, T, out, (char*)ws + DX_END, (unsigned*)((char*)ws + WS_MEET),
                                     (int*)((char*)ws + WS_STATUS), (cudaStream_t)stream));
 }

@@ -130,6 +130,7 @@ def test_linear_refusals(lib):
         assert call(with_(d0, w=W + 8)) == ALIGN and call(d0, x=X + 8) == ALIGN
         assert call(d0, y=Y + 2) == ALIGN and call(with_(d0, y_type=qre.BF16), y=Y + 2) == 0
         assert call(d0, bias=Z + 2) == ALIGN
+        assert call(d0, T=2, bias=Y + 64) == INVAL  # bias in y
         # y in x, and x in y
         assert call(d0, T=2, y=X + 16) == INVAL and call(d0, T=2, y=X - 16) == INVAL
     for c in BAD_FORMATS:
@@ -181,4 +182,4 @@ def test_experts_refusals(lib):
     for T in (0, 1, 64):
         need = size(ctypes.byref(d), T)
         assert need > 0 and call(d, T=T, ws_bytes=need - 1) == WORKSPACE
-    assert call(d, T=2, out=X + 16) == INVAL
+    assert call(d, T=2, out=X + 16) == INVAL and call(d, T=2, ids=V + 64) == INVAL and call(d, T=2, weights=V + 128 * 4) == INVAL
