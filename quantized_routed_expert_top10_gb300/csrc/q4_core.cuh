@@ -58,13 +58,15 @@ __device__ __forceinline__ void stage8(const Raw8& raw, int type, bool in, bool 
   for (int t = 0; t < terms; ++t) {
     uint32_t w[4];
 #pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = narrow2(f[2 * j], f[2 * j + 1], F16 ? STRATA_F16 : STRATA_BF16);
+    *reinterpret_cast<uint4*>(dst + t * stride) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (t + 1 == terms) break;
+#pragma unroll
     for (int j = 0; j < 4; ++j) {
-      w[j] = narrow2(f[2 * j], f[2 * j + 1], F16 ? STRATA_F16 : STRATA_BF16);
       const float2 v = widen2(w[j], F16 ? STRATA_F16 : STRATA_BF16);
       f[2 * j] -= v.x;  // exact: the rest has fewer bits
       f[2 * j + 1] -= v.y;
     }
-    *reinterpret_cast<uint4*>(dst + t * stride) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 // Columns c0 .. c1 - 1 (c0 a multiple of 128) of n rows of x as `terms` rows each at dst; behind the last column zeros, up to a whole block of 32.
@@ -89,13 +91,14 @@ template <bool F16>
 __device__ __noinline__ void stage_rows(const StageArgs s, int n, int c0, int c1, int half, int halves) {
   constexpr int AHEAD = 4;
   const int lane = threadIdx.x & 15, all = (s.columns + BLOCK - 1) / BLOCK * BLOCK, chunks = (c1 - c0 + CHUNK - 1) / CHUNK;
+  const uint32_t chunks_inverse = chunks == 1 ? 0u : 0xffffffffu / (uint32_t)chunks + 1u;  // inverse_of(chunks); n * chunks^2 stays far below 2^32
   for (int first = half; first < n * chunks; first += AHEAD * halves) {
     Raw8 raw[AHEAD];
     int row[AHEAD], at[AHEAD];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
       const int task = first + u * halves;
-      row[u] = task / chunks;
+      row[u] = divide(task, chunks_inverse);
       at[u] = (task - row[u] * chunks) * CHUNK + lane * 8;
       raw[u] = Raw8{};
       if (row[u] < n && c0 + at[u] < s.columns) {
