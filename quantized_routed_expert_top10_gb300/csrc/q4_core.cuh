@@ -6,7 +6,7 @@
 // scale multiplies a group's fp32 sum, the activations' power of two a chunk's.
 // What bounds it: the instructions around the codes, close above the weights' bytes.  16 rows x 128 columns (1 KB) leave a scheduler 176 cycles at
 // the measured copy rate.  Widening takes 5 integer instructions a word of 8 codes (2 cycles each) and 4 subtractions, 8 words a lane: 80 cycles of the
-// integer pipe; with scales, sums and copies a chunk comes to 176 instructions (2,560 -> 131,072 rows, one token: 189 MB in 38.7 us, 4.9 TB/s).  bf16
+// integer pipe; with scales, sums and copies a chunk comes to 176 instructions (2,560 -> 131,072 rows, one token: 189 MB in 38.2 us, 4.95 TB/s).  bf16
 // operands, with 7 mantissa bits, take 7 integer instructions a word: 57 us.  An MMA takes 8 cycles (measured, with 4 warps a scheduler), 8 of them
 // a chunk and tile of 8 columns, so two tiles are hidden.  Warp-level MMAs take the operands where widening leaves them, in registers; tcgen05 would
 // have four times the codes' bytes pass shared memory.

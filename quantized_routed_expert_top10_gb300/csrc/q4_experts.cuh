@@ -45,7 +45,7 @@ constexpr int WARPS = 8, THREADS = 32 * WARPS;  // two CTAs an SM, one of which 
 // chunks of a warp's ring: as many as leave room for 8 rows of 2,560 columns' terms (24 where blocks are larger, one CTA an SM)
 constexpr int depth_of(int tiles) { return tiles == 1 ? 7 : 5; }
 constexpr int PAIRS_MAX = STRATA_Q4_EXPERTS_T_MAX * STRATA_Q4_EXPERTS_K_MAX;
-constexpr int SORT_WARPS = 2, SORT_PER = 4;  // that sort up to 256 pairs while the others lay out x
+constexpr int SOME = 128, SOME_THREADS = 64;  // pairs that two warps sort while the others lay out x
 static_assert(PAIRS_MAX < 65536 && PAIRS_MAX % THREADS == 0 && STRATA_Q4_EXPERTS_E_MAX % THREADS == 0, "sorting of the pairs");
 
 // The pairs by expert: expert[a], its pairs pair[off[a]] .. pair[off[a + 1] - 1], a < n.
@@ -90,12 +90,71 @@ __device__ __forceinline__ void sort_few(const Sorted& s, int2* found, const int
     *found = make_int2(__popc(firsts), bad);
   }
 }
-// Up to N * PER pairs, by the CTA's first N threads.
-template <int N, int PER>
+// Up to 128 pairs, by the CTA's first 64 threads: each looks through all pairs for its own expert, then for the experts that come before it (in the
+// order in which their first pairs come).
+static __device__ __noinline__ void sort_some(const Sorted& s, int2* found, int* scratch, const int32_t* ids, const float* weights, int pairs,
+                                              int E) {
+  constexpr int NONE = 1000;
+  int *key = scratch, *lead = scratch + SOME;  // expert; its first pair
+  const int tid = threadIdx.x;
+  bool bad = false;
+  for (int p = tid; p < SOME; p += SOME_THREADS) {
+    const int e = p < pairs ? ids[p] : -1;
+    const float weight = p < pairs ? weights[p] : 0.f;
+    bad |= e < -1 || e >= E;
+    key[p] = e >= 0 && e < E && weight != 0.f ? e : -1;
+  }
+  named_barrier(15, SOME_THREADS);
+  if (__any_sync(0xffffffffu, bad) && (tid & 31) == 0) found->y = 1;  // 0 before the barrier
+  int first[SOME / SOME_THREADS], rank[SOME / SOME_THREADS];
+#pragma unroll
+  for (int i = 0; i < SOME / SOME_THREADS; ++i) {
+    const int p = tid + i * SOME_THREADS;
+    first[i] = NONE, rank[i] = 0;
+    if (i * SOME_THREADS >= pairs) break;
+    const int mine = key[p];
+    for (int q0 = 0; q0 < pairs; q0 += 4) {  // behind the last pair keys are -1
+      const int4 k = *reinterpret_cast<const int4*>(key + q0);
+      const int v[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (v[j] == mine && q0 + j <= p) {
+          first[i] = min(first[i], q0 + j);
+          rank[i] += q0 + j < p;
+        }
+    }
+    if (mine < 0) first[i] = NONE;
+  }
+#pragma unroll
+  for (int i = 0; i < SOME / SOME_THREADS; ++i) lead[tid + i * SOME_THREADS] = first[i];
+  named_barrier(15, SOME_THREADS);
+#pragma unroll
+  for (int i = 0; i < SOME / SOME_THREADS; ++i) {
+    const int p = tid + i * SOME_THREADS;
+    if (i * SOME_THREADS >= pairs) break;
+    int before = 0, experts = 0, all = 0, used = 0;
+    for (int q0 = 0; q0 < pairs; q0 += 4) {
+      const int4 k = *reinterpret_cast<const int4*>(lead + q0);
+      const int v[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        before += v[j] < first[i];
+        experts += v[j] == q0 + j && v[j] < first[i];
+        all += v[j] != NONE;
+        used += v[j] == q0 + j;
+      }
+    }
+    if (first[i] != NONE) {
+      s.pair[before + rank[i]] = p;
+      if (first[i] == p) s.expert[experts] = key[p], s.off[experts] = before;
+    }
+    if (p == 0) s.off[used] = all, found->x = used;
+  }
+}
+// Any number, by the whole CTA: counted, summed over all experts, dealt out.
 static __device__ __noinline__ void sort_many(const Sorted& s, int2* found, const int32_t* ids, const float* weights, int pairs, int E) {
-  __shared__ int warp_sum[N / 32];
-  constexpr int E_PER = STRATA_Q4_EXPERTS_E_MAX / N;
-  const auto sync = [] { named_barrier(15, N); };
+  __shared__ int warp_sum[WARPS];
+  constexpr int N = THREADS, PER = PAIRS_MAX / N, E_PER = STRATA_Q4_EXPERTS_E_MAX / N;
   const int tid = threadIdx.x, lane = tid & 31, warp = warp_index();
   int id[PER], rank[PER];
   float weight[PER];
@@ -106,7 +165,7 @@ static __device__ __noinline__ void sort_many(const Sorted& s, int2* found, cons
     weight[j] = p < pairs ? weights[p] : 0.f;
   }
   for (int e = tid; e < E; e += N) s.count[e] = 0;
-  sync();
+  __syncthreads();
   bool bad = false;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
@@ -115,7 +174,7 @@ static __device__ __noinline__ void sort_many(const Sorted& s, int2* found, cons
     else rank[j] = atomicAdd(&s.count[id[j]], 1);
   }
   if (__any_sync(0xffffffffu, bad) && lane == 0) found->y = 1;  // 0 before
-  sync();
+  __syncthreads();
   // sums before each expert of the pairs (low half) and of the experts in use (high half); consecutive experts a thread
   const int e0 = E_PER * tid;
   int c[E_PER], mine = 0;
@@ -131,10 +190,10 @@ static __device__ __noinline__ void sort_many(const Sorted& s, int2* found, cons
     if (lane >= o) v += up;
   }
   if (lane == 31) warp_sum[warp] = v;
-  sync();
+  __syncthreads();
   int before = v - mine, all = 0;
 #pragma unroll
-  for (int w = 0; w < N / 32; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w < warp) before += warp_sum[w];
     all += warp_sum[w];
   }
@@ -148,7 +207,7 @@ static __device__ __noinline__ void sort_many(const Sorted& s, int2* found, cons
     s.off[all >> 16] = all & 0xffff;
     found->x = all >> 16;
   }
-  sync();
+  __syncthreads();
 #pragma unroll
   for (int j = 0; j < PER; ++j)  // the order within an expert does not matter: a pair's sums are its own column's
     if (id[j] >= 0) s.pair[s.count[id[j]] + rank[j]] = tid + j * N;
@@ -402,15 +461,17 @@ __global__ void __launch_bounds__(THREADS, 2) experts_kernel(Q4ExpertArgs a) {
     }
   } else {
     if (threadIdx.x == 0) found.y = 0;
-    if (pairs <= 32 * SORT_WARPS * SORT_PER) {
-      if (warp < SORT_WARPS) {
-        sort_many<32 * SORT_WARPS, SORT_PER>(sorted, &found, a.ids, a.weights, pairs, a.E);
+    if (pairs <= SOME) {
+      if (warp < SOME_THREADS / 32) {
+        // (the units' sums are not in use yet)
+        sort_some(sorted, &found, reinterpret_cast<int*>(sh.part), a.ids, a.weights, pairs, a.E);
+        __syncwarp();
         if (threadIdx.x < 2) steps[threadIdx.x].set(a, threadIdx.x, found.x);
       } else if (a.resident) {
-        stage(a, sh, false, nullptr, a.T, (threadIdx.x >> 4) - 2 * SORT_WARPS, 2 * (WARPS - SORT_WARPS));
+        stage(a, sh, false, nullptr, a.T, (threadIdx.x >> 4) - SOME_THREADS / 16, 2 * WARPS - SOME_THREADS / 16);
       }
     } else {
-      sort_many<THREADS, PAIRS_MAX / THREADS>(sorted, &found, a.ids, a.weights, pairs, a.E);
+      sort_many(sorted, &found, a.ids, a.weights, pairs, a.E);
       if (threadIdx.x < 2) steps[threadIdx.x].set(a, threadIdx.x, found.x);
       if (a.resident) stage(a, sh, false, nullptr, a.T, threadIdx.x >> 4, 2 * WARPS);
     }
