@@ -44,14 +44,15 @@ template <int NT, int WARPS, int DEPTH, class W>
 __device__ __forceinline__ void linear_block(const W& w, const LinearArgs& a, char* smem, int t0, int nt) {
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const int S = 1 << a.log_split, group = warp >> a.log_split, member = warp & (S - 1), n_group = WARPS >> a.log_split;
-  const int units = (a.rows + ROWS - 1) / ROWS, chunks = (a.columns + W::COLUMNS - 1) / W::COLUMNS;
+  constexpr int UNIT = ROWS * W::SLABS;
+  const int units = (a.rows + UNIT - 1) / UNIT, chunks = (a.columns + W::COLUMNS - 1) / W::COLUMNS;
   const Share share(a.columns, W::COLUMNS, member, a.log_split);
   // the CTA's units lie gridDim.x apart, so that all CTAs have as many of them, or one more
   const int first = blockIdx.x, pass = gridDim.x * n_group;
   const int cols = nt * a.terms;
 
   float* part = reinterpret_cast<float*>(smem + WARPS * DEPTH * W::SLOT);
-  const int part_step = a.part_cols * PART_STRIDE;
+  const int part_step = a.part_cols * part_stride(W::SLABS);
   float* scale = part + WARPS * part_step;
   char* rows = reinterpret_cast<char*>(scale + a.tokens * a.scale_stride);
   Feed<W, DEPTH, Units<W>> feed(Units<W>{w, first + group * (int)gridDim.x, units, pass, member, lane, share.whole, share.tail, S * W::BYTES},
@@ -61,7 +62,7 @@ __device__ __forceinline__ void linear_block(const W& w, const LinearArgs& a, ch
   const bool panels = a.panel < chunks;
   for (int base = first; base < units; base += pass) {
     const int u = base + group * (int)gridDim.x;
-    float acc[NT][4] = {};
+    float acc[W::SLABS * NT][4] = {};
     for (int ch0 = 0, done = 0; ch0 < chunks; ch0 += a.panel, done += panel_steps) {
       if (panels || base == first) {  // activations of the panel
         const int c0 = ch0 * W::COLUMNS, c1 = min(c0 + a.panel * W::COLUMNS, (a.columns + BLOCK - 1) / BLOCK * BLOCK);
@@ -85,13 +86,13 @@ __device__ __forceinline__ void linear_block(const W& w, const LinearArgs& a, ch
         run_chunks<NT, W>(feed, whole, done <= share.whole && share.whole < done + panel_steps ? share.tail : 0, S, b, cs, acc);
       }
     }
-    store_part<NT>(part + warp * part_step, lane, acc);
+    store_part<NT, W::SLABS>(part + warp * part_step, lane, acc);
     group_sync<WARPS>(group, S);
     if (u < units)
-      for (int i = member * 32 + lane; i < nt * ROWS; i += S * 32) {
-        const int t = i / ROWS, row = i % ROWS, n = u * ROWS + row;
+      for (int i = member * 32 + lane; i < nt * UNIT; i += S * 32) {
+        const int t = i / UNIT, row = i % UNIT, n = u * UNIT + row;
         if (n < a.rows) {
-          float v = sum_part(part + group * S * part_step, part_step, S, a.terms, t, row);
+          float v = sum_part<W::SLABS>(part + group * S * part_step, part_step, S, a.terms, t, row);
           if (a.bias) v += a.bias[n];
           store1(a.y, (t0 + t) * a.y_stride + n, a.y_type, v);
         }
@@ -118,13 +119,13 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) linear_kernel(W w, Lin
 
 template <int TILES, int WARPS, int DEPTH, class W>
 cudaError_t launch_tiles(const W& w, LinearArgs a, cudaStream_t s) {
-  const int chunks = (a.columns + W::COLUMNS - 1) / W::COLUMNS, units = (a.rows + ROWS - 1) / ROWS;
+  const int chunks = (a.columns + W::COLUMNS - 1) / W::COLUMNS, units = (a.rows + ROWS * W::SLABS - 1) / (ROWS * W::SLABS);
   int sms = 0;
   cudaError_t err = sm_count(&sms);
   if (err != cudaSuccess) return err;
   a.tokens = 8 * TILES / a.terms < a.T ? 8 * TILES / a.terms : a.T;
   a.part_cols = (a.tokens * a.terms + 7) / 8 * 8;
-  const size_t fixed = (size_t)WARPS * DEPTH * W::SLOT + sizeof(float) * WARPS * a.part_cols * PART_STRIDE;
+  const size_t fixed = (size_t)WARPS * DEPTH * W::SLOT + sizeof(float) * WARPS * a.part_cols * part_stride(W::SLABS);
   auto bytes = [&]() {
     a.row_stride = row_bytes(a.panel * W::COLUMNS);
     a.scale_stride = (a.panel + 3) / 4 * 4;  // the rows behind the scales on 16-byte boundaries
@@ -148,12 +149,26 @@ cudaError_t launch_tiles(const W& w, LinearArgs a, cudaStream_t s) {
   return err;
 }
 
-template <class W>
-cudaError_t launch(const W& w, LinearArgs a, cudaStream_t s) {
-  a.terms = terms_of(a.x_type, W::F16);
-  // one tile: two CTAs of 8 warps an SM, one of which computes while the other lays out x or joins sums; more: one of 16, with more
-  // columns of x in shared memory and so fewer passes over the weights
+// One tile: two CTAs of 8 warps an SM, one of which computes while the other lays out x or joins sums; more: one of 16, with more columns of x in
+// shared memory and so fewer passes over the weights.
+cudaError_t launch_bf16(const Bf16& w, LinearArgs a, cudaStream_t s) {
+  a.terms = terms_of(a.x_type, false);
   return a.T * a.terms <= 8 ? launch_tiles<1, 8, 6>(w, a, s) : launch_tiles<TILES_MAX, 16, 3>(w, a, s);
+}
+
+// 4-bit weights, one tile: units of 32 rows where each CTA has 8 of them or more, one for each of its warps (131,072 rows, 27 of 16 rows a CTA: 38.2 us in
+// units of 16, 36.9 in units of 32); of 16 where that would leave warps without work.
+template <int GROUP, bool ZEROS, bool SCALE_F16>
+cudaError_t launch_format(const uint8_t* p, int64_t slab, LinearArgs a, cudaStream_t s) {
+  int sms = 0;
+  cudaError_t err = sm_count(&sms);
+  if (err != cudaSuccess) return err;
+  a.terms = terms_of(a.x_type, true);
+  const int slabs = (a.rows + ROWS - 1) / ROWS;
+  const Q4<GROUP, ZEROS, SCALE_F16, 1> w{p, slab, slabs};
+  if (a.T * a.terms > 8) return launch_tiles<TILES_MAX, 16, 3>(w, a, s);
+  if (slabs / (2 * sms) >= 16) return launch_tiles<1, 8, 4>(Q4<GROUP, ZEROS, SCALE_F16, 2>{p, slab, slabs}, a, s);
+  return launch_tiles<1, 8, 6>(w, a, s);
 }
 
 template <int GROUP>
@@ -161,9 +176,8 @@ cudaError_t launch_q4(const strata_linear_t& li, const LinearArgs& a, cudaStream
   const strata_q4_t& q = li.q4;
   const uint8_t* p = (const uint8_t*)li.w;
   const int64_t slab = slab_bytes(q.d_in, q.group, q.zeros != 0);
-  if (q.scale_type == STRATA_F16)
-    return q.zeros ? launch(Q4<GROUP, true, true>{p, slab}, a, s) : launch(Q4<GROUP, false, true>{p, slab}, a, s);
-  return q.zeros ? launch(Q4<GROUP, true, false>{p, slab}, a, s) : launch(Q4<GROUP, false, false>{p, slab}, a, s);
+  if (q.scale_type == STRATA_F16) return q.zeros ? launch_format<GROUP, true, true>(p, slab, a, s) : launch_format<GROUP, false, true>(p, slab, a, s);
+  return q.zeros ? launch_format<GROUP, true, false>(p, slab, a, s) : launch_format<GROUP, false, false>(p, slab, a, s);
 }
 
 }  // namespace
@@ -173,7 +187,7 @@ cudaError_t launch_linear(const strata_linear_t& li, const void* x, int T, const
   a.x = x, a.bias = bias, a.y = y;
   a.x_stride = li.x_stride, a.y_stride = li.y_stride;
   a.T = T, a.columns = li.q4.d_in, a.rows = li.q4.n_out, a.x_type = li.x_type, a.y_type = li.y_type;
-  if (li.weight == STRATA_W_BF16) return launch(Bf16{(const uint8_t*)li.w, li.w_stride, a.rows}, a, s);
+  if (li.weight == STRATA_W_BF16) return launch_bf16(Bf16{(const uint8_t*)li.w, li.w_stride, a.rows}, a, s);
   if (li.q4.group == 32) return launch_q4<32>(li, a, s);
   return li.q4.group == 64 ? launch_q4<64>(li, a, s) : launch_q4<128>(li, a, s);
 }

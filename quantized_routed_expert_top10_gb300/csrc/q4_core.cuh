@@ -24,7 +24,6 @@ namespace q4 {
 constexpr int SMEM_MAX = 227 * 1024 - 256;   // dynamic; the rest holds the kernels' static words
 constexpr int SMEM_HALF = 113 * 1024 - 256;  // of each of two CTAs an SM
 constexpr int TILES_MAX = 3;        // tiles of 8 term columns that a warp accumulates at once
-constexpr int PART_STRIDE = 20;     // floats between two columns of a warp's sums: 16 rows and 4 against bank conflicts
 
 // ---- activations ------------------------------------------------------------------------------------
 // How x enters the products.  Beside 4-bit codes: fp16 terms of x divided by a power of two for each token and chunk of 128 columns, so
@@ -181,127 +180,158 @@ __device__ __forceinline__ void zero_pairs(uint32_t z, uint32_t& z0lo, uint32_t&
   z0hi = h | 0x64006400u, z1hi = h << 4 | 0x54005400u;
 }
 
-// 4-bit weights of groups of GROUP columns: a chunk's bytes in the ring and its products.
-template <int GROUP, bool ZEROS, bool SCALE_F16>
+// 4-bit weights of groups of GROUP columns, units of SLABS (1 or 2) slabs: their chunk's bytes in the ring and its products.
+template <int GROUP, bool ZEROS, bool SCALE_F16, int SLABS_ = 1>
 struct Q4 {
   static constexpr bool F16 = true;  // the products' operands
+  static constexpr int SLABS = SLABS_;
   static constexpr int COLUMNS = CHUNK;
   static constexpr int SB = scale_bytes(GROUP), ZB = ZEROS ? zero_bytes(GROUP) : 0;
   static constexpr int META = meta_bytes(GROUP, ZEROS);
-  static constexpr int SLOT = 1024 + META;
+  static constexpr int ONE = 1024 + META;  // of a slab
+  static constexpr int SLOT = SLABS * ONE;
   static constexpr int BYTES = chunk_bytes(GROUP, ZEROS);
 
   struct Cursor {  // this lane's part of a chunk
     const uint8_t* at;
+    int64_t second;  // bytes to the second slab's (0 behind the last slab: the first again, and its results are not used)
   };
   const uint8_t* base;  // of the matrix
   int64_t slab;         // bytes of a slab
+  int slabs;
 
-  __device__ __forceinline__ Cursor cursor(int64_t s, int ch, int lane) const { return {base + s * slab + ch * BYTES + lane * 16}; }
+  __device__ __forceinline__ Cursor cursor(int64_t unit, int ch, int lane) const {
+    return {base + unit * SLABS * slab + ch * BYTES + lane * 16, SLABS == 2 && unit * 2 + 1 < slabs ? slab : 0};
+  }
   static __device__ __forceinline__ void load(uint32_t slot, const Cursor& c, int lane) {
-    copy_async<16>(slot + lane * 16, c.at);
-    copy_async<16>(slot + 512 + lane * 16, c.at + 512);
-    if (lane < META / 16) copy_async<16>(slot + 1024 + lane * 16, c.at + 1024);
+#pragma unroll
+    for (int h = 0; h < SLABS; ++h) {
+      const uint8_t* p = h ? c.at + c.second : c.at;
+      copy_async<16>(slot + h * ONE + lane * 16, p);
+      copy_async<16>(slot + h * ONE + 512 + lane * 16, p + 512);
+      if (lane < META / 16) copy_async<16>(slot + h * ONE + 1024 + lane * 16, p + 1024);
+    }
   }
   // A last chunk of `left` (32, 64 or 96) columns.
   static __device__ __forceinline__ void load_tail(uint32_t slot, const Cursor& c, int left, int lane) {
     const int nb = left / BLOCK;
-    const uint8_t* p = c.at - lane * 16;
 #pragma unroll 1
-    for (int b = 0; b < nb; ++b) {
-      copy_async<4>(slot + lane * 16 + 4 * b, p + (lane * nb + b) * 4);
-      copy_async<4>(slot + 512 + lane * 16 + 4 * b, p + 128 * nb + (lane * nb + b) * 4);
+    for (int h = 0; h < SLABS; ++h) {
+      const uint8_t* p = c.at - lane * 16 + (h ? c.second : 0);
+      const uint32_t to = slot + h * ONE;
+#pragma unroll 1
+      for (int b = 0; b < nb; ++b) {
+        copy_async<4>(to + lane * 16 + 4 * b, p + (lane * nb + b) * 4);
+        copy_async<4>(to + 512 + lane * 16 + 4 * b, p + 128 * nb + (lane * nb + b) * 4);
+      }
+      if (lane < META / 16) copy_async<16>(to + 1024 + lane * 16, p + 256 * nb + lane * 16);
     }
-    if (lane < META / 16) copy_async<16>(slot + 1024 + lane * 16, p + 256 * nb + lane * 16);
   }
+  static __device__ __forceinline__ float2 scales_of(uint32_t w) { return widen2(w, SCALE_F16 ? STRATA_F16 : STRATA_BF16); }
 
-  // acc[tile] += chunk x columns.  b[tile]: shared address of this lane's operand row at the chunk's first column; cs[tile]: the scales of
-  // this lane's two result columns in this chunk.
+  // acc[slab * NT + tile] += chunk x columns.  b[tile]: shared address of this lane's operand row at the chunk's first column; cs[tile]: the powers
+  // of two of this lane's two result columns in this chunk.  An operand of x is loaded once for all slabs.
   template <int NT>
   static __device__ __forceinline__ void products(uint32_t slot, const uint32_t (&b)[NT], const float2 (&cs)[NT], int lane,
-                                                  float (&acc)[NT][4]) {
+                                                  float (&acc)[SLABS * NT][4]) {
     const int g = lane >> 2;
-    const uint4 lo4 = lds16(slot + lane * 16), hi4 = lds16(slot + 512 + lane * 16);
-    const uint32_t lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
-    uint32_t scales[4], zeros[2];
-    if constexpr (SB == 16) {
-      const uint4 v = lds16(slot + 1024 + g * 16);
-      scales[0] = v.x, scales[1] = v.y, scales[2] = v.z, scales[3] = v.w;
-    } else {
+    uint32_t codes[SLABS][8], scales[SLABS][4], zeros[SLABS][2];
 #pragma unroll
-      for (int i = 0; i < SB / 4; ++i) scales[i] = lds4(slot + 1024 + g * SB + 4 * i);
-    }
-    if constexpr (ZEROS) {
+    for (int h = 0; h < SLABS; ++h) {
+      const uint32_t at = slot + h * ONE;
+      const uint4 lo = lds16(at + lane * 16), hi = lds16(at + 512 + lane * 16);
+      codes[h][0] = lo.x, codes[h][1] = lo.y, codes[h][2] = lo.z, codes[h][3] = lo.w;
+      codes[h][4] = hi.x, codes[h][5] = hi.y, codes[h][6] = hi.z, codes[h][7] = hi.w;
+      if constexpr (SB == 16) {
+        const uint4 v = lds16(at + 1024 + g * 16);
+        scales[h][0] = v.x, scales[h][1] = v.y, scales[h][2] = v.z, scales[h][3] = v.w;
+      } else {
 #pragma unroll
-      for (int i = 0; i < ZB / 4; ++i) zeros[i] = lds4(slot + 1024 + 8 * SB + g * ZB + 4 * i);
+        for (int i = 0; i < SB / 4; ++i) scales[h][i] = lds4(at + 1024 + g * SB + 4 * i);
+      }
+      if constexpr (ZEROS) {
+#pragma unroll
+        for (int i = 0; i < ZB / 4; ++i) zeros[h][i] = lds4(at + 1024 + 8 * SB + g * ZB + 4 * i);
+      }
     }
     constexpr int PER = GROUP / BLOCK;
-    float sum[NT][4] = {};
+    float sum[SLABS * NT][4] = {};
 #pragma unroll
     for (int gr = 0; gr < groups_of(GROUP); ++gr) {
-      uint32_t z0lo = 0x64086408u, z1lo = 0x54805480u, z0hi = z0lo, z1hi = z1lo;  // zero point 8
-      if constexpr (ZEROS) {
-        zero_pairs(zeros[gr >> 1] >> (16 * (gr & 1)), z0lo, z1lo, z0hi, z1hi);
-      }
-      float part[NT][4];
+      float part[SLABS * NT][4];
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int k = gr * PER + i;
-        uint32_t alo[4], ahi[4];
-        widen_word(lo[k], z0lo, z1lo, alo);
-        widen_word(hi[k], z0hi, z1hi, ahi);
+        uint4 x[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const uint4 x = lds16(b[t] + k * 64);
-          if (i == 0) mma_first(part[t], alo[0], ahi[0], alo[1], ahi[1], x.x, x.y);
-          else mma<true>(part[t], alo[0], ahi[0], alo[1], ahi[1], x.x, x.y);
-          mma<true>(part[t], alo[2], ahi[2], alo[3], ahi[3], x.z, x.w);
+        for (int t = 0; t < NT; ++t) x[t] = lds16(b[t] + k * 64);
+#pragma unroll
+        for (int h = 0; h < SLABS; ++h) {
+          uint32_t z0lo = 0x64086408u, z1lo = 0x54805480u, z0hi = z0lo, z1hi = z1lo;  // zero point 8
+          if constexpr (ZEROS) zero_pairs(zeros[h][gr >> 1] >> (16 * (gr & 1)), z0lo, z1lo, z0hi, z1hi);
+          uint32_t alo[4], ahi[4];
+          widen_word(codes[h][k], z0lo, z1lo, alo);
+          widen_word(codes[h][4 + k], z0hi, z1hi, ahi);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            float(&d)[4] = part[h * NT + t];
+            if (i == 0) mma_first(d, alo[0], ahi[0], alo[1], ahi[1], x[t].x, x[t].y);
+            else mma<true>(d, alo[0], ahi[0], alo[1], ahi[1], x[t].x, x[t].y);
+            mma<true>(d, alo[2], ahi[2], alo[3], ahi[3], x[t].z, x[t].w);
+          }
         }
       }
-      const float2 s = SCALE_F16 ? widen2(scales[gr], STRATA_F16) : widen2(scales[gr], STRATA_BF16);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        sum[t][0] = fmaf(s.x, part[t][0], sum[t][0]);
-        sum[t][1] = fmaf(s.x, part[t][1], sum[t][1]);
-        sum[t][2] = fmaf(s.y, part[t][2], sum[t][2]);
-        sum[t][3] = fmaf(s.y, part[t][3], sum[t][3]);
+      for (int h = 0; h < SLABS; ++h) {
+        const float2 s = scales_of(scales[h][gr]);
+#pragma unroll
+        for (int t = h * NT; t < (h + 1) * NT; ++t) {
+          sum[t][0] = fmaf(s.x, part[t][0], sum[t][0]);
+          sum[t][1] = fmaf(s.x, part[t][1], sum[t][1]);
+          sum[t][2] = fmaf(s.y, part[t][2], sum[t][2]);
+          sum[t][3] = fmaf(s.y, part[t][3], sum[t][3]);
+        }
       }
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      acc[t][0] = fmaf(cs[t].x, sum[t][0], acc[t][0]);
-      acc[t][1] = fmaf(cs[t].y, sum[t][1], acc[t][1]);
-      acc[t][2] = fmaf(cs[t].x, sum[t][2], acc[t][2]);
-      acc[t][3] = fmaf(cs[t].y, sum[t][3], acc[t][3]);
+    for (int i = 0; i < SLABS * NT; ++i) {
+      const float2 c = cs[i % NT];
+      acc[i][0] = fmaf(c.x, sum[i][0], acc[i][0]);
+      acc[i][1] = fmaf(c.y, sum[i][1], acc[i][1]);
+      acc[i][2] = fmaf(c.x, sum[i][2], acc[i][2]);
+      acc[i][3] = fmaf(c.y, sum[i][3], acc[i][3]);
     }
   }
 
   // The same for a last chunk of nb (1 to 3) blocks, block by block.
   template <int NT>
   static __device__ __forceinline__ void tail(uint32_t slot, int nb, const uint32_t (&b)[NT], const float2 (&cs)[NT], int lane,
-                                              float (&acc)[NT][4]) {
+                                              float (&acc)[SLABS * NT][4]) {
     const int g = lane >> 2;
 #pragma unroll 1
     for (int k = 0; k < nb; ++k) {
       const int gr = k * BLOCK / GROUP;
-      const uint32_t w = lds4(slot + 1024 + g * SB + 4 * gr);
-      const float2 s = SCALE_F16 ? widen2(w, STRATA_F16) : widen2(w, STRATA_BF16);
-      uint32_t z0lo = 0x64086408u, z1lo = 0x54805480u, z0hi = z0lo, z1hi = z1lo;
-      if constexpr (ZEROS)
-        zero_pairs(lds4(slot + 1024 + 8 * SB + g * ZB + 4 * (gr >> 1)) >> (16 * (gr & 1)), z0lo, z1lo, z0hi, z1hi);
-      uint32_t alo[4], ahi[4];
-      widen_word(lds4(slot + lane * 16 + 4 * k), z0lo, z1lo, alo);
-      widen_word(lds4(slot + 512 + lane * 16 + 4 * k), z0hi, z1hi, ahi);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const uint4 x = lds16(b[t] + k * 64);
-        float part[4];
-        mma_first(part, alo[0], ahi[0], alo[1], ahi[1], x.x, x.y);
-        mma<true>(part, alo[2], ahi[2], alo[3], ahi[3], x.z, x.w);
-        acc[t][0] = fmaf(cs[t].x * s.x, part[0], acc[t][0]);
-        acc[t][1] = fmaf(cs[t].y * s.x, part[1], acc[t][1]);
-        acc[t][2] = fmaf(cs[t].x * s.y, part[2], acc[t][2]);
-        acc[t][3] = fmaf(cs[t].y * s.y, part[3], acc[t][3]);
+      for (int h = 0; h < SLABS; ++h) {
+        const uint32_t at = slot + h * ONE;
+        const float2 s = scales_of(lds4(at + 1024 + g * SB + 4 * gr));
+        uint32_t z0lo = 0x64086408u, z1lo = 0x54805480u, z0hi = z0lo, z1hi = z1lo;
+        if constexpr (ZEROS) zero_pairs(lds4(at + 1024 + 8 * SB + g * ZB + 4 * (gr >> 1)) >> (16 * (gr & 1)), z0lo, z1lo, z0hi, z1hi);
+        uint32_t alo[4], ahi[4];
+        widen_word(lds4(at + lane * 16 + 4 * k), z0lo, z1lo, alo);
+        widen_word(lds4(at + 512 + lane * 16 + 4 * k), z0hi, z1hi, ahi);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const uint4 x = lds16(b[t] + k * 64);
+          float part[4];
+          mma_first(part, alo[0], ahi[0], alo[1], ahi[1], x.x, x.y);
+          mma<true>(part, alo[2], ahi[2], alo[3], ahi[3], x.z, x.w);
+          float(&d)[4] = acc[h * NT + t];
+          d[0] = fmaf(cs[t].x * s.x, part[0], d[0]);
+          d[1] = fmaf(cs[t].y * s.x, part[1], d[1]);
+          d[2] = fmaf(cs[t].x * s.y, part[2], d[2]);
+          d[3] = fmaf(cs[t].y * s.y, part[3], d[3]);
+        }
       }
     }
   }
@@ -310,6 +340,7 @@ struct Q4 {
 // bf16 weights, rows as they are: 64 columns of 16 rows a chunk, 16 bytes a lane, row and block of 32 columns.
 struct Bf16 {
   static constexpr bool F16 = false;
+  static constexpr int SLABS = 1;
   static constexpr int COLUMNS = 64;
   static constexpr int SLOT = 2048;
   static constexpr int BYTES = 2 * COLUMNS;
@@ -426,7 +457,8 @@ struct Feed {
 // Products of a warp's next `whole` chunks, then of one of `tail` columns.  b[tile] and cs[tile] are this lane's shared addresses for the
 // activations of the first of them; one chunk of this warp to the next is S of the unit's.
 template <int NT, class W, class F>
-__device__ __forceinline__ void run_chunks(F& feed, int whole, int tail, int S, uint32_t (&b)[NT], uint2 (&cs)[NT], float (&acc)[NT][4]) {
+__device__ __forceinline__ void run_chunks(F& feed, int whole, int tail, int S, uint32_t (&b)[NT], uint2 (&cs)[NT],
+                                           float (&acc)[W::SLABS * NT][4]) {
   auto scales = [&](float2 (&v)[NT]) {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -447,24 +479,28 @@ __device__ __forceinline__ void run_chunks(F& feed, int whole, int tail, int S, 
     W::template tail<NT>(slot, (tail + BLOCK - 1) / BLOCK, b, v, feed.lane, acc);
   }
 }
-// A warp's sums to its place in shared memory, [column][16 rows].
-template <int NT>
-__device__ __forceinline__ void store_part(float* part, int lane, const float (&acc)[NT][4]) {
+// Floats between two columns of a warp's sums: a unit's rows and 4 against bank conflicts.
+__host__ __device__ constexpr int part_stride(int slabs) { return slabs * ROWS + 4; }
+// A warp's sums to its place in shared memory, [column][rows of the unit].
+template <int NT, int SLABS>
+__device__ __forceinline__ void store_part(float* part, int lane, const float (&acc)[SLABS * NT][4]) {
   const int g = lane >> 2, c = lane & 3;
+  constexpr int STRIDE = part_stride(SLABS);
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    float* p = part + (8 * t + 2 * c) * PART_STRIDE + g;
-    p[0] = acc[t][0];
-    p[PART_STRIDE] = acc[t][1];
-    p[8] = acc[t][2];
-    p[PART_STRIDE + 8] = acc[t][3];
+  for (int i = 0; i < SLABS * NT; ++i) {
+    float* p = part + (8 * (i % NT) + 2 * c) * STRIDE + i / NT * ROWS + g;
+    p[0] = acc[i][0];
+    p[STRIDE] = acc[i][1];
+    p[8] = acc[i][2];
+    p[STRIDE + 8] = acc[i][3];
   }
 }
 // Row `row` of token j of a block over its terms and the S warps of its group (the first warp's part, parts `step` floats apart).
+template <int SLABS>
 __device__ __forceinline__ float sum_part(const float* part, int step, int S, int terms, int j, int row) {
   float v = 0.f;
   for (int s = 0; s < S; ++s)
-    for (int t = terms - 1; t >= 0; --t) v += part[s * step + (j * terms + t) * PART_STRIDE + row];
+    for (int t = terms - 1; t >= 0; --t) v += part[s * step + (j * terms + t) * part_stride(SLABS) + row];
   return v;
 }
 

@@ -43,7 +43,7 @@ using namespace q4;
 
 constexpr int WARPS = 8, THREADS = 32 * WARPS;  // two CTAs an SM, one of which computes while the other lays out x or joins sums
 // chunks of a warp's ring: as many as leave room for 8 rows of 2,560 columns' terms (24 where blocks are larger, one CTA an SM)
-constexpr int depth_of(int tiles) { return tiles == 1 ? 7 : 5; }
+constexpr int depth_of(int tiles, int slabs) { return slabs == 2 ? 3 : tiles == 1 ? 7 : 5; }
 constexpr int PAIRS_MAX = STRATA_Q4_EXPERTS_T_MAX * STRATA_Q4_EXPERTS_K_MAX;
 constexpr int SOME = 128, SOME_THREADS = 64;  // pairs that two warps sort while the others lay out x
 static_assert(PAIRS_MAX < 65536 && PAIRS_MAX % THREADS == 0 && STRATA_Q4_EXPERTS_E_MAX % THREADS == 0, "sorting of the pairs");
@@ -294,7 +294,8 @@ struct Units {
       }
     }
     const int e = divide(u, step->slabs_inverse);
-    cursor.at = step->base + sorted.expert[e] * step->expert_stride + (u - e * step->slabs) * step->slab + member * W::BYTES + lane * 16;
+    cursor.at = step->base + sorted.expert[e] * step->expert_stride + (u - e * step->slabs) * (W::SLABS * step->slab) + member * W::BYTES + lane * 16;
+    cursor.second = step->slab;
     u += step->n_group;
     return true;
   }
@@ -348,9 +349,9 @@ __device__ __forceinline__ void unit_products(const Q4ExpertArgs& a, const Sorte
     cs[t].x = smem_u32(sh.scale + row_of(c2 >> shift) * a.scale_stride + member);
     cs[t].y = smem_u32(sh.scale + row_of((c2 + 1) >> shift) * a.scale_stride + member);
   }
-  float acc[NT][4] = {};
+  float acc[W::SLABS * NT][4] = {};
   run_chunks<NT, W>(feed, share.whole, share.tail, S, b, cs, acc);
-  store_part<NT>(sh.part + warp * (a.part_cols * PART_STRIDE), lane, acc);
+  store_part<NT, W::SLABS>(sh.part + warp * (a.part_cols * part_stride(W::SLABS)), lane, acc);
 }
 
 // The terms of n rows of x or h by `halves` half warps, this one `half`: of all tokens, or of the sorted pairs from `pair` on.
@@ -366,7 +367,7 @@ __device__ __forceinline__ void run_step(const Q4ExpertArgs& a, const Sorted& so
                                          const Shared& sh, bool down) {
   const int warp = warp_index(), lane = threadIdx.x & 31, terms = a.terms[down];
   const int S = 1 << step.log_split, group = warp >> step.log_split, member = warp & (S - 1);
-  const int part_step = a.part_cols * PART_STRIDE;
+  const int part_step = a.part_cols * part_stride(W::SLABS);
   for (Window win(step.u0); win.next(step, sorted);) {
     if (down || !a.resident) {
       __syncthreads();
@@ -385,14 +386,14 @@ __device__ __forceinline__ void run_step(const Q4ExpertArgs& a, const Sorted& so
         else unit_products<3, W>(a, sorted, feed, share, sh, down, S, member, win.p0, lo, np);
       }
       group_sync<WARPS>(group, S);
-      const int out = down ? 4 : 3;  // 16 or 8 rows
+      const int out = (down ? 4 : 3) + (W::SLABS == 2);  // 16 or 8 rows a slab
       const float* sums = sh.part + group * S * part_step;
       const int row_len = a.columns[!down];
       float* to = (down ? a.parts : a.h) + ((u - e * step.slabs) << out);
       for (int i = member * 32 + lane; i < np << out; i += S * 32) {
-        const int j = i >> out, row = i & ((1 << out) - 1);
-        float v = sum_part(sums, part_step, S, terms, j, row);
-        if (!down) v = silu_mul(v, sum_part(sums, part_step, S, terms, j, row + 8));
+        const int j = i >> out, row = i & ((1 << out) - 1), at = down ? row : row + (row & 8);  // a slab's 8 rows of gate, then its 8 of up
+        float v = sum_part<W::SLABS>(sums, part_step, S, terms, j, at);
+        if (!down) v = silu_mul(v, sum_part<W::SLABS>(sums, part_step, S, terms, j, at + 8));
         to[(int64_t)sorted.pair[lo + j] * row_len + row] = v;
       }
       group_sync<WARPS>(group, S);
@@ -444,11 +445,11 @@ __global__ void __launch_bounds__(THREADS, 2) experts_kernel(Q4ExpertArgs a) {
   extern __shared__ __align__(128) char smem[];
   __shared__ int2 found;  // experts in use; an id outside [-1, E)
   __shared__ Step steps[2];
-  constexpr int DEPTH = depth_of(TILES);
+  constexpr int DEPTH = depth_of(TILES, W::SLABS);
   const int warp = warp_index(), lane = threadIdx.x & 31, pairs = a.T * a.k;
   Shared sh;
   sh.part = reinterpret_cast<float*>(smem + WARPS * DEPTH * W::SLOT);
-  sh.scale = sh.part + WARPS * a.part_cols * PART_STRIDE;
+  sh.scale = sh.part + WARPS * a.part_cols * part_stride(W::SLABS);
   sh.rows = reinterpret_cast<char*>(sh.scale + a.staged * a.scale_stride);
   const Sorted sorted = sorted_at(sh.rows + a.staged * a.row_stride, a.E);
   if (pairs <= 32) {
@@ -517,7 +518,7 @@ cudaError_t launch(Q4ExpertArgs a, cudaStream_t s) {
   a.row_stride = row_bytes(wide);
   a.scale_stride = ((wide + CHUNK - 1) / CHUNK + 3) / 4 * 4;
   a.part_cols = 8 * TILES;
-  const size_t fixed = (size_t)WARPS * depth_of(TILES) * W::SLOT + sizeof(float) * WARPS * a.part_cols * PART_STRIDE + sorted_bytes(a.E, pairs);
+  const size_t fixed = (size_t)WARPS * depth_of(TILES, W::SLABS) * W::SLOT + sizeof(float) * WARPS * a.part_cols * part_stride(W::SLABS) + sorted_bytes(a.E, pairs);
   const size_t row = a.row_stride + sizeof(float) * a.scale_stride;
   auto fit = [&](size_t room) { return room > fixed ? (int)((room - fixed) / row < 8 * TILES ? (room - fixed) / row : 8 * TILES) : 0; };
   // two CTAs an SM where their rows of terms are half of a block's or more, else one
@@ -527,7 +528,7 @@ cudaError_t launch(Q4ExpertArgs a, cudaStream_t s) {
   for (int i = 0; i < 2; ++i) a.block[i] = a.rows[i] = a.staged / a.terms[i];
   a.resident = a.T * a.terms[0] <= a.staged;
   if (a.resident) a.block[0] = 8 * TILES / a.terms[0];
-  a.slabs[0] = a.columns[1] / 8, a.slabs[1] = a.columns[0] / ROWS;
+  a.slabs[0] = a.columns[1] / (8 * W::SLABS), a.slabs[1] = a.columns[0] / (ROWS * W::SLABS);  // d_ff and d_model are multiples of 32
   for (int i = 0; i < 2; ++i) a.slabs_inverse[i] = inverse_of(a.slabs[i]);
   a.grid_inverse = inverse_of(sms * per_sm), a.k_inverse = inverse_of(a.k);
   err = allow_smem<experts_kernel<W, TILES>>(SMEM_MAX);
@@ -539,21 +540,26 @@ cudaError_t launch(Q4ExpertArgs a, cudaStream_t s) {
   return err;
 }
 
-// The kernel of one format: blocks of a single tile of 8 columns, with a deeper ring, where an expert has two columns or fewer on average (or can have no
+// The kernel of one format.  Blocks of a single tile of 8 columns, with a deeper ring, where an expert has two columns or fewer on average (or can have no
 // more than 8); else of up to three tiles.  An expert with more columns than a block is passed over again: 16 tokens, 6 of 64 experts, fp16 (3 columns
-// on average) 66 to 73 us in single tiles, 62 in up to three.
+// on average) 66 to 73 us in single tiles, 62 in up to three.  Single tiles in units of 32 rows where a CTA will have 8 or more of them in step 1, of 16 where
+// that would leave warps without work: 64 tokens, 10 of 512 experts (75 units of 16 a CTA) 218 us in units of 16, 197 in units of 32.
+template <int GROUP, bool ZEROS, bool SCALE_F16>
+cudaError_t launch_format(const Q4ExpertArgs& a, cudaStream_t s) {
+  int sms = 0;
+  cudaError_t err = sm_count(&sms);
+  if (err != cudaSuccess) return err;
+  const int terms = a.terms[0] > a.terms[1] ? a.terms[0] : a.terms[1];
+  const int64_t pairs = a.T * a.k, used = pairs * a.E / (pairs + a.E);  // experts in use, about
+  if (a.T * terms > 8 && pairs * terms > 2 * a.E) return launch<Q4<GROUP, ZEROS, SCALE_F16>, TILES_MAX>(a, s);
+  if (used * (a.columns[1] / 8) >= 16 * 2 * sms) return launch<Q4<GROUP, ZEROS, SCALE_F16, 2>, 1>(a, s);
+  return launch<Q4<GROUP, ZEROS, SCALE_F16>, 1>(a, s);
+}
 template <int GROUP>
 cudaError_t launch_group(const strata_q4_experts_t& ex, const Q4ExpertArgs& a, cudaStream_t s) {
-  const strata_q4_t& q = ex.gate_up_q4;
-  const int terms = a.terms[0] > a.terms[1] ? a.terms[0] : a.terms[1];
-  const bool one = a.T * terms <= 8 || (int64_t)a.T * a.k * terms <= 2 * (int64_t)a.E;
-  const bool f16 = q.scale_type == STRATA_F16;
-  if (one) {
-    if (q.zeros) return f16 ? launch<Q4<GROUP, true, true>, 1>(a, s) : launch<Q4<GROUP, true, false>, 1>(a, s);
-    return f16 ? launch<Q4<GROUP, false, true>, 1>(a, s) : launch<Q4<GROUP, false, false>, 1>(a, s);
-  }
-  if (q.zeros) return f16 ? launch<Q4<GROUP, true, true>, TILES_MAX>(a, s) : launch<Q4<GROUP, true, false>, TILES_MAX>(a, s);
-  return f16 ? launch<Q4<GROUP, false, true>, TILES_MAX>(a, s) : launch<Q4<GROUP, false, false>, TILES_MAX>(a, s);
+  const bool f16 = ex.gate_up_q4.scale_type == STRATA_F16;
+  if (ex.gate_up_q4.zeros) return f16 ? launch_format<GROUP, true, true>(a, s) : launch_format<GROUP, true, false>(a, s);
+  return f16 ? launch_format<GROUP, false, true>(a, s) : launch_format<GROUP, false, false>(a, s);
 }
 
 }  // namespace q4x

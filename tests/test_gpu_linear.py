@@ -103,6 +103,13 @@ def test_many_rows(n_out, d_in, T):
     check(Bf16Rows(n_out, d_in), T, qre.BF16, qre.F32)
 
 
+@pytest.mark.parametrize("n_out", [77823, 77825, 77840, 77856, 100001])
+def test_units_of_32_rows(n_out):
+    """Enough rows for units of two slabs, an odd number of slabs, and one slab less."""
+    for group, d_in, T, xk, zeros in ((32, 96, 1, qre.F32, True), (64, 320, 3, qre.BF16, False), (128, 256, 4, qre.F32, True), (32, 32, 8, qre.F16, False)):
+        check(q4ref.Matrices(1, n_out, d_in, group, zeros, qre.F16 if zeros else qre.BF16), T, xk, qre.F32)
+
+
 @pytest.mark.parametrize("T,xk,d_in", [(64, qre.F32, 2560), (24, qre.BF16, 8192), (8, qre.F32, 16384), (1, qre.F32, 32768), (3, qre.F32, 28672),
                                        (30, qre.F16, 4096)])
 def test_activations_in_panels(T, xk, d_in):

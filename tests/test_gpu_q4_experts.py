@@ -109,6 +109,20 @@ def test_many_experts():
     Layer(512, 128, 64, k=10).check(*lists(1, 512, 10))
 
 
+@pytest.mark.parametrize("group,zeros", list(itertools.product((32, 64), (False, True))))
+def test_units_of_32_rows(group, zeros):
+    """Enough experts and rows for units of two slabs."""
+    scale = qre.F16 if zeros else qre.BF16
+    Layer(128, 64, 512, group, zeros, scale, qre.BF16, qre.BF16, k=4).check(*lists(64, 128, 4))
+    Layer(256, 192, 320, group, zeros, scale, qre.F32, qre.F32, k=4).check(*lists(60, 256, 4))
+    Layer(200, 128, 512, group, zeros, scale, qre.F32, qre.F16, k=32).check(*lists(4, 200, 32))
+    layer = Layer(256, 64, 448, group, zeros, scale, qre.F16, qre.BF16, k=4)
+    ids, w = lists(64, 256, 4)
+    ids[:40, 0] = 7  # one expert of many pairs among them: blocks over the same weights
+    w[3] = 0.0
+    layer.check(ids, w)
+
+
 def test_the_same_expert_twice():
     Layer(4, 128, 64, k=5).check(*lists(9, 4, 5, distinct=False))
     Layer(4, 128, 64, k=3).check(np.full((4, 3), 2), np.full((4, 3), 0.3))
