@@ -6,7 +6,8 @@
 // scale multiplies a group's fp32 sum, the activations' power of two a chunk's.
 // What bounds it: the instructions around the codes, close above the weights' bytes.  16 rows x 128 columns (1 KB) leave a scheduler 176 cycles at
 // the measured copy rate.  Widening takes 5 integer instructions a word of 8 codes (2 cycles each) and 4 subtractions, 8 words a lane: 80 cycles of the
-// integer pipe; with scales, sums and copies a chunk comes to 176 instructions (2,560 -> 131,072 rows, one token: 189 MB in 38.2 us, 4.95 TB/s).  bf16
+// integer pipe; with scales, sums and copies a chunk comes to 176 instructions, fewer in units of 32 rows (2,560 -> 131,072 rows, one token: 189 MB in 38.2
+// and 36.9 us, 5.1 TB/s).  bf16
 // operands, with 7 mantissa bits, take 7 integer instructions a word: 57 us.  An MMA takes 8 cycles (measured, with 4 warps a scheduler), 8 of them
 // a chunk and tile of 8 columns, so two tiles are hidden.  Warp-level MMAs take the operands where widening leaves them, in registers; tcgen05 would
 // have four times the codes' bytes pass shared memory.
@@ -421,8 +422,9 @@ struct Feed {
   typename W::Cursor cursor;
   int left, tail, stride;  // of the unit: whole chunks and columns of a shorter one to copy; bytes from one chunk of this warp to its next
   int lane;
+  bool more;  // units, as far as is known
 
-  __device__ __forceinline__ Feed(const U& u, uint32_t at, int l) : units(u), ring(at), used(at), left(0), tail(0), lane(l) {
+  __device__ __forceinline__ Feed(const U& u, uint32_t at, int l) : units(u), ring(at), used(at), left(0), tail(0), lane(l), more(true) {
 #pragma unroll 1
     for (int i = 0; i < DEPTH - 1; ++i) {
       fill();
@@ -431,7 +433,10 @@ struct Feed {
   }
   __device__ __forceinline__ void fill() {
     if (left == 0) {  // a shorter chunk, or on to the next unit
-      if (tail == 0 && units.next()) cursor = units.cursor, left = units.whole, tail = units.tail, stride = units.stride;
+      if (tail == 0 && more) {
+        more = units.next();
+        if (more) cursor = units.cursor, left = units.whole, tail = units.tail, stride = units.stride;
+      }
       if (left == 0 && tail) {
         W::load_tail(used, cursor, tail, lane);
         tail = 0;

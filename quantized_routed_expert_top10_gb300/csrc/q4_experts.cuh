@@ -8,6 +8,10 @@
 // weights.  The units of step 1 (16 rows of one expert: 8 of gate with the same 8 of up) and then those of step 2 (16 rows of down) are dealt in
 // equal contiguous stretches, one of each to a CTA; S warps share a unit.  All CTAs are resident (a cooperative launch) and meet between the
 // steps; the copies of weights run ahead across the meeting, so step 2 finds its first chunks in shared memory.
+//
+// What bounds it: 64 tokens of 512 experts (1.03 GB in 194 us, 5.3 TB/s of 6.8) the instructions around the codes, see q4_core.cuh; one token (26 MB in 22 us,
+// 3.9 at the copy rate) a chain of latencies: launch 4 us, sort 1, first chunks 2, step 1 5, meeting 2, h 1.3, step 2 2.5, meeting 2, step 3 2.
+// Three kernels with programmatic launches instead of the meetings took 30 us for one token.
 #pragma once
 #include "q4_core.cuh"
 
@@ -543,7 +547,7 @@ cudaError_t launch(Q4ExpertArgs a, cudaStream_t s) {
 // The kernel of one format.  Blocks of a single tile of 8 columns, with a deeper ring, where an expert has two columns or fewer on average (or can have no
 // more than 8); else of up to three tiles.  An expert with more columns than a block is passed over again: 16 tokens, 6 of 64 experts, fp16 (3 columns
 // on average) 66 to 73 us in single tiles, 62 in up to three.  Single tiles in units of 32 rows where a CTA will have 8 or more of them in step 1, of 16 where
-// that would leave warps without work: 64 tokens, 10 of 512 experts (75 units of 16 a CTA) 218 us in units of 16, 197 in units of 32.
+// that would leave warps without work: 64 tokens, 10 of 512 experts (75 units of 16 a CTA) 218 us in units of 16, 194 in units of 32.
 template <int GROUP, bool ZEROS, bool SCALE_F16>
 cudaError_t launch_format(const Q4ExpertArgs& a, cudaStream_t s) {
   int sms = 0;
