@@ -2,7 +2,8 @@
 //
 // One persistent kernel.  A unit is 16 rows of W (a slab) for one block of tokens (up to 24 term columns); S warps share it, each taking
 // every S-th chunk of columns, and join their sums over shared memory.  The grid is units x blocks, so that a CTA lays out the terms of
-// one block once, for all its units: at once where they fit beside the rings, else in panels of columns, unit by unit.
+// one block once, for all its units: at once where they fit beside the rings, else in panels of columns, unit by unit.  Where that is
+// much work two CTAs, a cluster, do it together.
 #include "q4_core.cuh"
 
 namespace strata {
@@ -40,7 +41,7 @@ struct Units {
 };
 
 // The units of this CTA for one block of tokens.
-template <int NT, int WARPS, int DEPTH, class W>
+template <int NT, int WARPS, int DEPTH, bool PAIR, class W>
 __device__ __forceinline__ void linear_block(const W& w, const LinearArgs& a, char* smem, int t0, int nt) {
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const int S = 1 << a.log_split, group = warp >> a.log_split, member = warp & (S - 1), n_group = WARPS >> a.log_split;
@@ -67,10 +68,16 @@ __device__ __forceinline__ void linear_block(const W& w, const LinearArgs& a, ch
       if (panels || base == first) {  // activations of the panel
         const int c0 = ch0 * W::COLUMNS, c1 = min(c0 + a.panel * W::COLUMNS, (a.columns + BLOCK - 1) / BLOCK * BLOCK);
         const StageArgs to{static_cast<const char*>(a.x) + t0 * a.x_stride * (a.x_type == STRATA_F32 ? 4 : 2), a.x_stride, a.x_type, a.columns,
-                           a.terms, rows, a.row_stride, scale, a.scale_stride, nullptr, 0};
-        __syncthreads();
-        stage_rows<W::F16>(to, nt, c0, c1, threadIdx.x >> 4, 2 * WARPS);
-        __syncthreads();
+                           a.terms, rows, a.row_stride, scale, a.scale_stride, nullptr, 0, (int)(~blockIdx.x & 1)};
+        if (PAIR) {
+          cluster_meet();
+          stage_rows<W::F16, true>(to, nt, c0, c1, (blockIdx.x & 1) * 2 * WARPS + (threadIdx.x >> 4), 4 * WARPS);
+          cluster_meet();
+        } else {
+          __syncthreads();
+          stage_rows<W::F16>(to, nt, c0, c1, threadIdx.x >> 4, 2 * WARPS);
+          __syncthreads();
+        }
       }
       uint32_t b[NT];
       uint2 cs[NT];
@@ -88,22 +95,21 @@ __device__ __forceinline__ void linear_block(const W& w, const LinearArgs& a, ch
     }
     store_part<NT, W::SLABS>(part + warp * part_step, lane, acc);
     group_sync<WARPS>(group, S);
-    if (u < units)
-      for (int i = member * 32 + lane; i < nt * UNIT; i += S * 32) {
-        const int t = i / UNIT, row = i % UNIT, n = u * UNIT + row;
-        if (n < a.rows) {
-          float v = sum_part<W::SLABS>(part + group * S * part_step, part_step, S, a.terms, t, row);
-          if (a.bias) v += a.bias[n];
-          store1(a.y, (t0 + t) * a.y_stride + n, a.y_type, v);
-        }
+    const int row = lane % UNIT, n = u * UNIT + row;  // UNIT is 16 or 32
+    if (u < units && n < a.rows) {
+      const float bias = a.bias ? a.bias[n] : 0.f;
+      for (int t = (member * 32 + lane) / UNIT; t < nt; t += S * 32 / UNIT) {
+        const float v = sum_part<W::SLABS>(part + group * S * part_step, part_step, S, a.terms, t, row);
+        store1(a.y, (t0 + t) * a.y_stride + n, a.y_type, v + bias);
       }
+    }
     group_sync<WARPS>(group, S);
   }
   copy_wait<0>();
 }
 
-// TILES: of the largest block.
-template <class W, int TILES, int WARPS, int DEPTH>
+// TILES: of the largest block.  PAIR: two neighbouring CTAs, a cluster, lay out x for one another: each half of it, into both.
+template <class W, int TILES, int WARPS, int DEPTH, bool PAIR>
 __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) linear_kernel(W w, LinearArgs a) {
   extern __shared__ __align__(128) char smem[];
   griddep_wait();
@@ -111,9 +117,9 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) linear_kernel(W w, Lin
   for (int t0 = blockIdx.y * a.tokens; t0 < a.T; t0 += gridDim.y * a.tokens) {
     const int nt = min(a.tokens, a.T - t0), tiles = (nt * a.terms + 7) / 8;
     __syncthreads();
-    if (TILES == 1 || tiles == 1) linear_block<1, WARPS, DEPTH>(w, a, smem, t0, nt);
-    else if (tiles == 2) linear_block<2, WARPS, DEPTH>(w, a, smem, t0, nt);
-    else linear_block<3, WARPS, DEPTH>(w, a, smem, t0, nt);
+    if (TILES == 1 || tiles == 1) linear_block<1, WARPS, DEPTH, PAIR>(w, a, smem, t0, nt);
+    else if (tiles == 2) linear_block<2, WARPS, DEPTH, PAIR>(w, a, smem, t0, nt);
+    else linear_block<3, WARPS, DEPTH, PAIR>(w, a, smem, t0, nt);
   }
 }
 
@@ -141,11 +147,32 @@ cudaError_t launch_tiles(const W& w, LinearArgs a, cudaStream_t s) {
   const int split = choose_split(WARPS, (units + gx_most - 1) / gx_most, chunks, fit);
   a.panel = fit < chunks ? fit / split * split : (chunks + split - 1) / split * split;
   if (a.panel > fit) a.panel = fit / split * split;
-  err = allow_smem<linear_kernel<W, TILES, WARPS, DEPTH>>(SMEM_MAX);
-  if (err != cudaSuccess) return err;
   for (a.log_split = 0; 1 << a.log_split < split;) ++a.log_split;
-  STRATA_LAUNCH(KID_LINEAR, s, err = launch_pdl(linear_kernel<W, TILES, WARPS, DEPTH>, dim3(units < gx_most ? units : gx_most, gy),
-                                                dim3(32 * WARPS), bytes(), s, w, a));
+  // where a half warp would lay out eight terms of chunks or more, and all of x at once, neighbouring CTAs share that (15 of them, 64 tokens to 10,240
+  // bf16: 28.5 us alone, 24.9 in pairs); with fewer the two meetings cost more (5 of them, 4 tokens to 10,240: 9.6 and 9.9)
+  const int most = units < gx_most ? units : gx_most, even = most & ~1;
+  const bool pair = TILES > 1 && a.panel >= chunks && even > 0 && (units + even - 1) / even == (units + most - 1) / most &&
+                    a.tokens * a.terms * ((a.columns + CHUNK - 1) / CHUNK) >= 8 * 2 * WARPS;
+  const int gx = pair ? even : most;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(gx, gy), cfg.blockDim = dim3(32 * WARPS), cfg.dynamicSmemBytes = bytes(), cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr, cfg.numAttrs = pair ? 2 : 1;
+  auto launch = [&](auto paired) {
+    constexpr auto kernel = linear_kernel<W, TILES, WARPS, DEPTH, decltype(paired)::value>;
+    const cudaError_t e = allow_smem<linear_kernel<W, TILES, WARPS, DEPTH, decltype(paired)::value>>(SMEM_MAX);
+    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kernel, w, a);
+  };
+  if constexpr (TILES > 1)
+    if (pair) {
+      STRATA_LAUNCH(KID_LINEAR, s, err = launch(std::true_type{}));
+      return err;
+    }
+  STRATA_LAUNCH(KID_LINEAR, s, err = launch(std::false_type{}));
   return err;
 }
 

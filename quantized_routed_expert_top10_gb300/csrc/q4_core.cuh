@@ -7,8 +7,7 @@
 // What bounds it: the instructions around the codes, close above the weights' bytes.  16 rows x 128 columns (1 KB) leave a scheduler 176 cycles at
 // the measured copy rate.  Widening takes 5 integer instructions a word of 8 codes (2 cycles each) and 4 subtractions, 8 words a lane: 80 cycles of the
 // integer pipe; with scales, sums and copies a chunk comes to 176 instructions, fewer in units of 32 rows (2,560 -> 131,072 rows, one token: 189 MB in 38.2
-// and 36.9 us, 5.1 TB/s).  bf16
-// operands, with 7 mantissa bits, take 7 integer instructions a word: 57 us.  An MMA takes 8 cycles (measured, with 4 warps a scheduler), 8 of them
+// and 36.9 us, 5.1 TB/s).  bf16 operands, with 7 mantissa bits, take 7 integer instructions a word: 57 us.  An MMA takes 8 cycles (measured, with 4 warps a scheduler), 8 of them
 // a chunk and tile of 8 columns, so two tiles are hidden.  Warp-level MMAs take the operands where widening leaves them, in registers; tcgen05 would
 // have four times the codes' bytes pass shared memory.
 // Tried and not kept: codes as e4m3 bytes (a code in the low bits of a byte is code * 2^-9 without further work): mma.sync of e4m3 turns into
@@ -37,10 +36,23 @@ __host__ __device__ constexpr int terms_of(int type, bool f16) {
 // operand loads of 8 lanes, 64 bytes of each of two rows, meet all banks once.
 __host__ __device__ constexpr int row_bytes(int columns) { return (2 * columns) | 64; }
 
+// The place in shared memory of CTA `peer` of the cluster where this CTA has p.
+__device__ __forceinline__ uint32_t peer_address(const void* p, int peer) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(peer));
+  return at;
+}
+// All threads of the cluster meet, and see what was stored to one another's shared memory.
+__device__ __forceinline__ void cluster_meet() {
+  __syncwarp();  // .aligned: all lanes together
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Eight columns, first i of a row, into `terms` rows at dst; F16: after their chunk's power of two, which goes to *scale.  By the 16 lanes of
-// a chunk; `all` columns in whole blocks of 32, those behind the last hold zeros.
-template <bool F16>
-__device__ __forceinline__ void stage8(const Raw8& raw, int type, bool in, bool store, int terms, char* dst, int stride, float* scale) {
+// a chunk; `all` columns in whole blocks of 32, those behind the last hold zeros.  PAIR: to the same places of CTA `peer` too.
+// The terms unrolled: 64 tokens to a router's 512, three terms each, 11.0 us with a loop and 9.9 without.
+template <bool F16, bool PAIR>
+__device__ __forceinline__ void stage8(const Raw8& raw, int type, bool in, bool store, int terms, char* dst, int stride, float* scale, int peer) {
   float f[8] = {};
   if (in) widen8(raw, type, f);
   if (F16) {
@@ -50,16 +62,25 @@ __device__ __forceinline__ void stage8(const Raw8& raw, int type, bool in, bool 
     const uint32_t top = __reduce_max_sync(0xffffu << (threadIdx.x & 16), __float_as_uint(most));
     const uint32_t e = max(top >> 23, 15u);  // 2^(e - 127) <= largest; below 2^-112 all count as 2^-112
     const float up = __uint_as_float((268u - e) << 23);
-    if ((threadIdx.x & 15) == 0) *scale = __uint_as_float((e - 14u) << 23);
+    if ((threadIdx.x & 15) == 0) {
+      *scale = __uint_as_float((e - 14u) << 23);
+      if (PAIR) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_address(scale, peer)), "r"((e - 14u) << 23) : "memory");
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] *= up;
   }
   if (!store) return;
-  for (int t = 0; t < terms; ++t) {
+#pragma unroll
+  for (int t = 0; t < (F16 ? 2 : 3); ++t) {
+    if (t == terms) break;
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j] = narrow2(f[2 * j], f[2 * j + 1], F16 ? STRATA_F16 : STRATA_BF16);
     *reinterpret_cast<uint4*>(dst + t * stride) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (PAIR)
+      asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(peer_address(dst + t * stride, peer)), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                   "r"(w[3])
+                   : "memory");
     if (t + 1 == terms) break;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -71,7 +92,7 @@ __device__ __forceinline__ void stage8(const Raw8& raw, int type, bool in, bool 
 }
 // Columns c0 .. c1 - 1 (c0 a multiple of 128) of n rows of x as `terms` rows each at dst; behind the last column zeros, up to a whole block of 32.
 // Row j is x's row j, or row index[j] / d (inverse: of d, see divide) where there is an index.  By `halves` half warps, this one `half`, a chunk of
-// a row each, four of them asked for at once.
+// a row each, four of them asked for at once.  PAIR: see stage8.
 struct StageArgs {
   const void* x;
   int64_t x_stride;
@@ -82,12 +103,13 @@ struct StageArgs {
   int scale_stride;
   const uint16_t* index;
   uint32_t inverse;
+  int peer;  // PAIR: the CTA of the cluster that gets the same rows
 };
 // n / d by inverse = ceil(2^32 / d), or 0 for d = 1; exact while n * d < 2^32.
 __device__ __forceinline__ int divide(int n, uint32_t inverse) { return inverse ? __umulhi(n, inverse) : n; }
 inline uint32_t inverse_of(int d) { return d == 1 ? 0 : (uint32_t)(((1ull << 32) + d - 1) / d); }
 
-template <bool F16>
+template <bool F16, bool PAIR = false>
 __device__ __noinline__ void stage_rows(const StageArgs s, int n, int c0, int c1, int half, int halves) {
   constexpr int AHEAD = 4;
   const int lane = threadIdx.x & 15, all = (s.columns + BLOCK - 1) / BLOCK * BLOCK, chunks = (c1 - c0 + CHUNK - 1) / CHUNK;
@@ -109,8 +131,8 @@ __device__ __noinline__ void stage_rows(const StageArgs s, int n, int c0, int c1
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u)
       if (row[u] < n)
-        stage8<F16>(raw[u], s.type, c0 + at[u] < s.columns, c0 + at[u] < all, s.terms, s.rows + row[u] * s.terms * s.row_stride + at[u] * 2,
-                    s.row_stride, s.scale + row[u] * s.scale_stride + at[u] / CHUNK);
+        stage8<F16, PAIR>(raw[u], s.type, c0 + at[u] < s.columns, c0 + at[u] < all, s.terms, s.rows + row[u] * s.terms * s.row_stride + at[u] * 2,
+                    s.row_stride, s.scale + row[u] * s.scale_stride + at[u] / CHUNK, s.peer);
   }
 }
 

@@ -361,7 +361,7 @@ __device__ __forceinline__ void unit_products(const Q4ExpertArgs& a, const Sorte
 // The terms of n rows of x or h by `halves` half warps, this one `half`: of all tokens, or of the sorted pairs from `pair` on.
 __device__ __forceinline__ void stage(const Q4ExpertArgs& a, const Shared& sh, bool down, const uint16_t* pair, int n, int half, int halves) {
   const StageArgs to{down ? a.h : a.x, down ? a.columns[1] : a.x_stride, down ? STRATA_F32 : a.x_type, a.columns[down], a.terms[down],
-                     sh.rows, a.row_stride, sh.scale, a.scale_stride, pair, down ? 0u : a.k_inverse};
+                     sh.rows, a.row_stride, sh.scale, a.scale_stride, pair, down ? 0u : a.k_inverse, 0};
   stage_rows<true>(to, n, 0, a.columns[down], half, halves);
 }
 

@@ -119,6 +119,52 @@ def test_activations_in_panels(T, xk, d_in):
     check(Bf16Rows(40, d_in), T, xk, qre.F32)
 
 
+@pytest.mark.parametrize("T,xk,d_in,n_out", [(24, qre.BF16, 1408, 32), (24, qre.F16, 1440, 33), (25, qre.BF16, 2560, 2432), (33, qre.F16, 1376, 2416),
+                                             (64, qre.BF16, 2560, 10240), (65, qre.BF16, 2592, 10241), (12, qre.F32, 1440, 512), (13, qre.F32, 1408, 496),
+                                             (200, qre.F32, 1472, 48), (64, qre.F32, 1440, 4880), (4000, qre.BF16, 1408, 40)])
+def test_activations_laid_out_by_two(T, xk, d_in, n_out):
+    """Enough of x for neighbouring CTAs to share its layout, with last blocks of one token, even and odd numbers of units."""
+    check(q4ref.Matrices(1, n_out, d_in, 32, True, qre.BF16), T, xk, qre.F32)
+
+
+@pytest.mark.parametrize("T,xk", [(24, qre.BF16), (25, qre.BF16), (12, qre.F16), (49, qre.F16), (8, qre.F32), (17, qre.F32)])
+@pytest.mark.parametrize("n_out", [32, 497])
+def test_activations_of_bf16_rows_laid_out_by_two(T, xk, n_out):
+    check(Bf16Rows(n_out, 1416), T, xk, qre.F32)
+
+
+def test_layout_by_two_again_in_graphs_and_beside_others():
+    m = q4ref.Matrices(1, 2560, 2560, 64, False, qre.BF16)
+    keep = m.packed(DEV)
+    d = qre.linear_q4(m.q, keep, qre.BF16, qre.BF16)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    x = [rows(64, 2560, 0, qre.BF16, 11 + i) for i in range(3)]
+    y = [rows(64, 2560, 0, qre.BF16, 21 + i) for i in range(3)]
+    for i in range(3):
+        qre.strata_moe_linear(d, x[i], 64, None, y[i])
+    torch.cuda.synchronize()
+    want = [v.clone() for v in y]
+    for v in y:
+        v.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                qre.strata_moe_linear(d, x[i], 64, None, y[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(y, want))
+    for v in y:
+        v.zero_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for i in range(3):
+            qre.strata_moe_linear(d, x[i], 64, None, y[i])
+    g.replay()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(y, want))
+
+
 @pytest.mark.parametrize("yk", KINDS)
 def test_strides(yk):
     check(q4ref.Matrices(1, 51, 320, 64), 6, qre.F16, yk, xpad=24, ypad=3)
