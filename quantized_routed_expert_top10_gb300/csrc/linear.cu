@@ -19,7 +19,7 @@ struct LinearArgs {
   int T, columns, rows, x_type, y_type;
   int tokens, terms;  // of a block
   int log_split;      // 2^this warps to a unit
-  int panel;          // chunks whose activations lie in shared memory at once, a multiple of the unit's warps
+  int panel;          // chunks whose activations lie in shared memory at once
   int row_stride;     // bytes between rows of terms
   int scale_stride;   // floats between tokens' scales
   int part_cols;      // term columns of a block, rounded up to whole tiles
@@ -125,50 +125,27 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) linear_kernel(W w, Lin
 
 template <int TILES, int WARPS, int DEPTH, class W>
 cudaError_t launch_tiles(const W& w, LinearArgs a, cudaStream_t s) {
-  const int chunks = (a.columns + W::COLUMNS - 1) / W::COLUMNS, units = (a.rows + ROWS * W::SLABS - 1) / (ROWS * W::SLABS);
   int sms = 0;
   cudaError_t err = sm_count(&sms);
   if (err != cudaSuccess) return err;
-  a.tokens = 8 * TILES / a.terms < a.T ? 8 * TILES / a.terms : a.T;
-  a.part_cols = (a.tokens * a.terms + 7) / 8 * 8;
-  const size_t fixed = (size_t)WARPS * DEPTH * W::SLOT + sizeof(float) * WARPS * a.part_cols * part_stride(W::SLABS);
-  auto bytes = [&]() {
-    a.row_stride = row_bytes(a.panel * W::COLUMNS);
-    a.scale_stride = (a.panel + 3) / 4 * 4;  // the rows behind the scales on 16-byte boundaries
-    return fixed + a.tokens * (sizeof(float) * a.scale_stride + (size_t)a.terms * a.row_stride);
-  };
-  // chunks of a block's terms and scales that fit beside the rings, with a row's padding
-  const int fit = (int)((SMEM_MAX - fixed - (size_t)a.tokens * (a.terms * 64 + 16)) /
-                        (a.tokens * (a.terms * 2 * W::COLUMNS + sizeof(float))));
-  a.panel = chunks;
-  const int per_sm = WARPS == 16 || bytes() > SMEM_HALF ? 1 : 2;
-  const int blocks = (a.T + a.tokens - 1) / a.tokens, ctas = sms * per_sm;
-  const int gy = blocks < ctas ? blocks : ctas, gx_most = ctas / gy;
-  const int split = choose_split(WARPS, (units + gx_most - 1) / gx_most, chunks, fit);
-  a.panel = fit < chunks ? fit / split * split : (chunks + split - 1) / split * split;
-  if (a.panel > fit) a.panel = fit / split * split;
-  for (a.log_split = 0; 1 << a.log_split < split;) ++a.log_split;
-  // where a half warp would lay out eight terms of chunks or more, and all of x at once, neighbouring CTAs share that (15 of them, 64 tokens to 10,240
-  // bf16: 28.5 us alone, 24.9 in pairs); with fewer the two meetings cost more (5 of them, 4 tokens to 10,240: 9.6 and 9.9)
-  const int most = units < gx_most ? units : gx_most, even = most & ~1;
-  const bool pair = TILES > 1 && a.panel >= chunks && even > 0 && (units + even - 1) / even == (units + most - 1) / most &&
-                    a.tokens * a.terms * ((a.columns + CHUNK - 1) / CHUNK) >= 8 * 2 * WARPS;
-  const int gx = pair ? even : most;
+  const LinearPlan p = linear_plan({TILES, WARPS, DEPTH, W::SLOT, W::COLUMNS, W::SLABS}, a.T, a.columns, a.rows, a.terms, sms);
+  a.tokens = p.tokens, a.log_split = p.log_split, a.panel = p.panel;
+  a.row_stride = p.row_stride, a.scale_stride = p.scale_stride, a.part_cols = p.part_cols;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(gx, gy), cfg.blockDim = dim3(32 * WARPS), cfg.dynamicSmemBytes = bytes(), cfg.stream = s;
+  cfg.gridDim = dim3(p.grid_x, p.grid_y), cfg.blockDim = dim3(32 * WARPS), cfg.dynamicSmemBytes = p.bytes, cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = 2, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr, cfg.numAttrs = pair ? 2 : 1;
+  cfg.attrs = attr, cfg.numAttrs = p.pair ? 2 : 1;
   auto launch = [&](auto paired) {
     constexpr auto kernel = linear_kernel<W, TILES, WARPS, DEPTH, decltype(paired)::value>;
     const cudaError_t e = allow_smem<linear_kernel<W, TILES, WARPS, DEPTH, decltype(paired)::value>>(SMEM_MAX);
     return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kernel, w, a);
   };
   if constexpr (TILES > 1)
-    if (pair) {
+    if (p.pair) {
       STRATA_LAUNCH(KID_LINEAR, s, err = launch(std::true_type{}));
       return err;
     }

@@ -21,10 +21,6 @@
 namespace strata {
 namespace q4 {
 
-constexpr int SMEM_MAX = 227 * 1024 - 256;   // dynamic; the rest holds the kernels' static words
-constexpr int SMEM_HALF = 113 * 1024 - 256;  // of each of two CTAs an SM
-constexpr int TILES_MAX = 3;        // tiles of 8 term columns that a warp accumulates at once
-
 // ---- activations ------------------------------------------------------------------------------------
 // How x enters the products.  Beside 4-bit codes: fp16 terms of x divided by a power of two for each token and chunk of 128 columns, so
 // that the largest lies in [2^14, 2^15); one term holds all bits of a bf16 or fp16 (down to 2^-40 of the chunk's largest), two hold 22 of an
@@ -32,9 +28,6 @@ constexpr int TILES_MAX = 3;        // tiles of 8 term columns that a warp accum
 __host__ __device__ constexpr int terms_of(int type, bool f16) {
   return type == STRATA_BF16 ? 1 : type == STRATA_F16 ? (f16 ? 1 : 2) : (f16 ? 2 : 3);
 }
-// Bytes between rows of `columns` (a multiple of 32) terms in shared memory: 64 past a multiple of 128, so that the 16-byte
-// operand loads of 8 lanes, 64 bytes of each of two rows, meet all banks once.
-__host__ __device__ constexpr int row_bytes(int columns) { return (2 * columns) | 64; }
 
 // The place in shared memory of CTA `peer` of the cluster where this CTA has p.
 __device__ __forceinline__ uint32_t peer_address(const void* p, int peer) {
@@ -49,7 +42,7 @@ __device__ __forceinline__ void cluster_meet() {
 }
 
 // Eight columns, first i of a row, into `terms` rows at dst; F16: after their chunk's power of two, which goes to *scale.  By the 16 lanes of
-// a chunk; `all` columns in whole blocks of 32, those behind the last hold zeros.  PAIR: to the same places of CTA `peer` too.
+// a chunk; in: they are columns of x, else zeros; store: they are laid out.  PAIR: to the same places of CTA `peer` too.
 // The terms unrolled: 64 tokens to a router's 512, three terms each, 11.0 us with a loop and 9.9 without.
 template <bool F16, bool PAIR>
 __device__ __forceinline__ void stage8(const Raw8& raw, int type, bool in, bool store, int terms, char* dst, int stride, float* scale, int peer) {
@@ -90,7 +83,8 @@ __device__ __forceinline__ void stage8(const Raw8& raw, int type, bool in, bool 
     }
   }
 }
-// Columns c0 .. c1 - 1 (c0 a multiple of 128) of n rows of x as `terms` rows each at dst; behind the last column zeros, up to a whole block of 32.
+// Columns c0 .. c1 - 1 (c0 a multiple of 128, c1 of 32) of n rows of x as `terms` rows each at dst; behind the last column zeros.  Nothing is stored
+// behind c1, where the next row begins.
 // Row j is x's row j, or row index[j] / d (inverse: of d, see divide) where there is an index.  By `halves` half warps, this one `half`, a chunk of
 // a row each, four of them asked for at once.  PAIR: see stage8.
 struct StageArgs {
@@ -112,7 +106,7 @@ inline uint32_t inverse_of(int d) { return d == 1 ? 0 : (uint32_t)(((1ull << 32)
 template <bool F16, bool PAIR = false>
 __device__ __noinline__ void stage_rows(const StageArgs s, int n, int c0, int c1, int half, int halves) {
   constexpr int AHEAD = 4;
-  const int lane = threadIdx.x & 15, all = (s.columns + BLOCK - 1) / BLOCK * BLOCK, chunks = (c1 - c0 + CHUNK - 1) / CHUNK;
+  const int lane = threadIdx.x & 15, last = min(s.columns, c1), chunks = (c1 - c0 + CHUNK - 1) / CHUNK;
   const uint32_t chunks_inverse = chunks == 1 ? 0u : 0xffffffffu / (uint32_t)chunks + 1u;  // inverse_of(chunks); n * chunks^2 stays far below 2^32
   for (int first = half; first < n * chunks; first += AHEAD * halves) {
     Raw8 raw[AHEAD];
@@ -123,7 +117,7 @@ __device__ __noinline__ void stage_rows(const StageArgs s, int n, int c0, int c1
       row[u] = divide(task, chunks_inverse);
       at[u] = (task - row[u] * chunks) * CHUNK + lane * 8;
       raw[u] = Raw8{};
-      if (row[u] < n && c0 + at[u] < s.columns) {
+      if (row[u] < n && c0 + at[u] < last) {
         const int from = s.index ? divide(s.index[row[u]], s.inverse) : row[u];
         raw[u] = load8(s.x, from * s.x_stride + c0 + at[u], s.type);
       }
@@ -131,7 +125,7 @@ __device__ __noinline__ void stage_rows(const StageArgs s, int n, int c0, int c1
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u)
       if (row[u] < n)
-        stage8<F16, PAIR>(raw[u], s.type, c0 + at[u] < s.columns, c0 + at[u] < all, s.terms, s.rows + row[u] * s.terms * s.row_stride + at[u] * 2,
+        stage8<F16, PAIR>(raw[u], s.type, c0 + at[u] < last, c0 + at[u] < c1, s.terms, s.rows + row[u] * s.terms * s.row_stride + at[u] * 2,
                     s.row_stride, s.scale + row[u] * s.scale_stride + at[u] / CHUNK, s.peer);
   }
 }
@@ -506,8 +500,6 @@ __device__ __forceinline__ void run_chunks(F& feed, int whole, int tail, int S, 
     W::template tail<NT>(slot, (tail + BLOCK - 1) / BLOCK, b, v, feed.lane, acc);
   }
 }
-// Floats between two columns of a warp's sums: a unit's rows and 4 against bank conflicts.
-__host__ __device__ constexpr int part_stride(int slabs) { return slabs * ROWS + 4; }
 // A warp's sums to its place in shared memory, [column][rows of the unit].
 template <int NT, int SLABS>
 __device__ __forceinline__ void store_part(float* part, int lane, const float (&acc)[SLABS * NT][4]) {
@@ -537,18 +529,6 @@ __device__ __forceinline__ void group_sync(int group, int S) {
   if (S == 1) __syncwarp();
   else if (S == WARPS) __syncthreads();
   else named_barrier(1 + group, 32 * S);
-}
-
-// Warps to a unit (16 rows x all chunks): the split with the fewest chunks one after the other, where a unit's end counts as one more
-// and joining several warps' sums as another; equal: fewer warps a unit.
-__host__ __device__ inline int choose_split(int warps, int units_of_cta, int chunks, int most) {
-  int best = 1, cost = 1 << 30;
-  for (int i = 0; 1 << i <= warps && 1 << i <= most; ++i) {  // 2^i warps a unit, warps / 2^i units at once
-    const int rounds = (units_of_cta + (warps >> i) - 1) * (1 << i) / warps;
-    const int c = rounds * (((chunks + (1 << i) - 1) >> i) + (i ? 2 : 1));
-    if (c < cost) best = 1 << i, cost = c;
-  }
-  return best;
 }
 
 }  // namespace q4

@@ -6,11 +6,10 @@
 // 32 columns (a block) it holds columns 8c .. 8c + 7, one 32-bit word a row: four blocks are 16 bytes a row, one wide load.
 #pragma once
 #include "ops_common.cuh"
+#include "q4_sizes.h"
 
 namespace strata {
 namespace q4 {
-
-constexpr int ROWS = 16, CHUNK = 128, BLOCK = 32;
 
 __host__ __device__ constexpr int groups_of(int group) { return CHUNK / group; }             // in a chunk
 __host__ __device__ constexpr int scale_bytes(int group) { return 4 * groups_of(group); }    // rows g, g + 8 of a chunk
