@@ -26,7 +26,7 @@
  *
  * Element types (the framework's own activations are fp32): arithmetic is in 32 bits or more whatever the
  * type, and a result is rounded once, when it is stored.  Some values between are held in fewer: the adapters' A_a x has 16
- * bits where y is of a 16-bit type, an fp32 x beside 4-bit weights 22, the experts' hidden values 22 or 11 (the calls say so again). */
+ * bits where y is of a 16-bit type, an fp32 x beside 4-bit weights and the experts' hidden values 22 (the calls say so again). */
 #ifndef STRATA_MOE_OPS_H_
 #define STRATA_MOE_OPS_H_
 
@@ -272,7 +272,7 @@ size_t strata_moe_q4_experts_workspace_bytes(const strata_q4_experts_t* ex, int3
  * nothing of it is read; a token without any gets zeros.  An expert may stand twice in a token's list.  A shared expert is one more expert that every
  * token lists.  T in [0, 64].  x and out on 16-byte boundaries; out must not overlap x, ids or weights.
  * Products are exact and summed in fp32 as in strata_moe_linear; the hidden values of an expert are held in fp32 and enter the
- * second product with 22 bits, with 11 for a bf16 out.  NaN and infinities as there.
+ * second product with 22 bits.  NaN and infinities as there.
  * An id outside [-1, n_expert) sets STRATA_E_CORRUPT in the workspace's status word and the call computes nothing (out keeps its contents).
  * Calls that share a workspace must not overlap in time.  One cooperative launch, whose CTAs wait for one another; a wait of more than 2 s sets
  * STRATA_E_TIMEOUT, and the workspace must then be initialised again. */

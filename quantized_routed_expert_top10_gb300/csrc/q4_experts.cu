@@ -35,8 +35,7 @@ cudaError_t launch_q4_experts(const strata_q4_experts_t& ex, const int32_t* ids,
   a.T = T, a.k = ex.top_k, a.E = ex.n_expert;
   a.columns[0] = gu.d_in, a.columns[1] = dn.d_in;
   a.terms[0] = q4::terms_of(ex.x_type, true);
-  // one fp16 term (11 bits, an error of 2^-11 where the sum of many such is rounded to 8 bits) for a bf16 result, two for the others
-  a.terms[1] = ex.out_type == STRATA_BF16 ? 1 : 2;
+  a.terms[1] = q4::terms_of(STRATA_F32, true);  // the hidden values are fp32
   return gu.group == 32 ? launch_q4_experts_32(ex, a, s) : gu.group == 64 ? launch_q4_experts_64(ex, a, s) : launch_q4_experts_128(ex, a, s);
 }
 

@@ -9,7 +9,7 @@
 // equal contiguous stretches, one of each to a CTA; S warps share a unit.  All CTAs are resident (a cooperative launch) and meet between the
 // steps; the copies of weights run ahead across the meeting, so step 2 finds its first chunks in shared memory.
 //
-// What bounds it: 64 tokens of 512 experts (1.03 GB in 194 us, 5.3 TB/s of 6.8) the instructions around the codes, see q4_core.cuh; one token (26 MB in 22 us,
+// What bounds it: 64 tokens of 512 experts (1.03 GB in 209 us, 4.9 TB/s of 6.8) the instructions around the codes, see q4_core.cuh; one token (26 MB in 22 us,
 // 3.9 at the copy rate) a chain of latencies: launch 4 us, sort 1, first chunks 2, step 1 5, meeting 2, h 1.3, step 2 2.5, meeting 2, step 3 2.
 // Three kernels with programmatic launches instead of the meetings took 30 us for one token.
 #pragma once
@@ -37,8 +37,9 @@ struct Q4ExpertArgs {
   int block[2];            // pairs whose columns one unit takes at once
   int rows[2];             // rows of x or h in shared memory at once
   int resident;            // step 1: the rows are all tokens', there from the start
-  int staged;              // rows of terms
-  int row_stride, scale_stride, part_cols;
+  int staged[2];           // rows of terms
+  int row_stride[2], scale_stride[2], part_cols[2];
+  int sorted_at;           // bytes before the sorted pairs: rings, then a step's sums, scales and rows of terms
 };
 
 namespace q4x {
@@ -330,9 +331,13 @@ __device__ __forceinline__ bool meet(unsigned* count, int* status) {
   return !__syncthreads_or(late);
 }
 
-struct Shared {  // the CTA's dynamic shared memory behind the rings
+struct Shared {  // the CTA's dynamic shared memory behind the rings, in step 1 or 2
   float *part, *scale;
   char* rows;
+  __device__ __forceinline__ Shared(const Q4ExpertArgs& a, char* behind, bool down, int slabs)
+      : part(reinterpret_cast<float*>(behind)),
+        scale(part + WARPS * a.part_cols[down] * part_stride(slabs)),
+        rows(reinterpret_cast<char*>(scale + a.staged[down] * a.scale_stride[down])) {}
 };
 
 // Sums of unit u of the expert whose pairs in the window are lo .. lo + np - 1.
@@ -340,6 +345,7 @@ template <int NT, class W, class F>
 __device__ __forceinline__ void unit_products(const Q4ExpertArgs& a, const Sorted& sorted, F& feed, const Share& share, const Shared& sh, bool down,
                                               int S, int member, int p0, int lo, int np) {
   const int warp = warp_index(), lane = feed.lane, shift = a.terms[down] - 1;  // one or two terms
+  const int row_stride = a.row_stride[down], scale_stride = a.scale_stride[down];
   uint32_t b[NT];
   uint2 cs[NT];
   auto row_of = [&](int j) {  // of pair lo + j among those in shared memory
@@ -349,19 +355,19 @@ __device__ __forceinline__ void unit_products(const Q4ExpertArgs& a, const Sorte
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int c = 8 * t + (lane >> 2), c2 = 8 * t + 2 * (lane & 3);
-    b[t] = smem_u32(sh.rows) + ((row_of(c >> shift) << shift) + (c & shift)) * a.row_stride + (lane & 3) * 16 + member * 2 * W::COLUMNS;
-    cs[t].x = smem_u32(sh.scale + row_of(c2 >> shift) * a.scale_stride + member);
-    cs[t].y = smem_u32(sh.scale + row_of((c2 + 1) >> shift) * a.scale_stride + member);
+    b[t] = smem_u32(sh.rows) + ((row_of(c >> shift) << shift) + (c & shift)) * row_stride + (lane & 3) * 16 + member * 2 * W::COLUMNS;
+    cs[t].x = smem_u32(sh.scale + row_of(c2 >> shift) * scale_stride + member);
+    cs[t].y = smem_u32(sh.scale + row_of((c2 + 1) >> shift) * scale_stride + member);
   }
   float acc[W::SLABS * NT][4] = {};
   run_chunks<NT, W>(feed, share.whole, share.tail, S, b, cs, acc);
-  store_part<NT, W::SLABS>(sh.part + warp * (a.part_cols * part_stride(W::SLABS)), lane, acc);
+  store_part<NT, W::SLABS>(sh.part + warp * (a.part_cols[down] * part_stride(W::SLABS)), lane, acc);
 }
 
 // The terms of n rows of x or h by `halves` half warps, this one `half`: of all tokens, or of the sorted pairs from `pair` on.
 __device__ __forceinline__ void stage(const Q4ExpertArgs& a, const Shared& sh, bool down, const uint16_t* pair, int n, int half, int halves) {
   const StageArgs to{down ? a.h : a.x, down ? a.columns[1] : a.x_stride, down ? STRATA_F32 : a.x_type, a.columns[down], a.terms[down],
-                     sh.rows, a.row_stride, sh.scale, a.scale_stride, pair, down ? 0u : a.k_inverse, 0};
+                     sh.rows, a.row_stride[down], sh.scale, a.scale_stride[down], pair, down ? 0u : a.k_inverse, 0};
   stage_rows<true>(to, n, 0, a.columns[down], half, halves);
 }
 
@@ -371,7 +377,7 @@ __device__ __forceinline__ void run_step(const Q4ExpertArgs& a, const Sorted& so
                                          const Shared& sh, bool down) {
   const int warp = warp_index(), lane = threadIdx.x & 31, terms = a.terms[down];
   const int S = 1 << step.log_split, group = warp >> step.log_split, member = warp & (S - 1);
-  const int part_step = a.part_cols * part_stride(W::SLABS);
+  const int part_step = a.part_cols[down] * part_stride(W::SLABS);
   for (Window win(step.u0); win.next(step, sorted);) {
     if (down || !a.resident) {
       __syncthreads();
@@ -386,8 +392,8 @@ __device__ __forceinline__ void run_step(const Q4ExpertArgs& a, const Sorted& so
         lo = max((int)sorted.off[e], win.p0), np = min((int)sorted.off[e + 1], win.p1) - lo;
         const int tiles = (np * terms + 7) / 8;
         if (TILES == 1 || tiles == 1) unit_products<1, W>(a, sorted, feed, share, sh, down, S, member, win.p0, lo, np);
-        else if (tiles == 2) unit_products<2, W>(a, sorted, feed, share, sh, down, S, member, win.p0, lo, np);
-        else unit_products<3, W>(a, sorted, feed, share, sh, down, S, member, win.p0, lo, np);
+        else if (TILES == 2 || tiles == 2) unit_products<2, W>(a, sorted, feed, share, sh, down, S, member, win.p0, lo, np);
+        else unit_products<TILES < 3 ? 1 : 3, W>(a, sorted, feed, share, sh, down, S, member, win.p0, lo, np);
       }
       group_sync<WARPS>(group, S);
       const int out = (down ? 4 : 3) + (W::SLABS == 2);  // 16 or 8 rows a slab
@@ -443,19 +449,16 @@ __device__ __forceinline__ void combine4(const Q4ExpertArgs& a, int t, int c, fl
         make_uint2(narrow2(sum[0], sum[1], a.out_type), narrow2(sum[2], sum[3], a.out_type));
 }
 
-// TILES: of the largest block.
-template <class W, int TILES>
+// TILES, TILES2: of the largest block of step 1 and of step 2.
+template <class W, int TILES, int TILES2>
 __global__ void __launch_bounds__(THREADS, 2) experts_kernel(Q4ExpertArgs a) {
   extern __shared__ __align__(128) char smem[];
   __shared__ int2 found;  // experts in use; an id outside [-1, E)
   __shared__ Step steps[2];
   constexpr int DEPTH = depth_of(TILES, W::SLABS);
   const int warp = warp_index(), lane = threadIdx.x & 31, pairs = a.T * a.k;
-  Shared sh;
-  sh.part = reinterpret_cast<float*>(smem + WARPS * DEPTH * W::SLOT);
-  sh.scale = sh.part + WARPS * a.part_cols * part_stride(W::SLABS);
-  sh.rows = reinterpret_cast<char*>(sh.scale + a.staged * a.scale_stride);
-  const Sorted sorted = sorted_at(sh.rows + a.staged * a.row_stride, a.E);
+  const Shared sh(a, smem + WARPS * DEPTH * W::SLOT, false, W::SLABS), sh2(a, smem + WARPS * DEPTH * W::SLOT, true, W::SLABS);
+  const Sorted sorted = sorted_at(smem + a.sorted_at, a.E);
   if (pairs <= 32) {
     if (warp == 0) {
       sort_few(sorted, &found, a.ids, a.weights, pairs, a.E);
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(THREADS, 2) experts_kernel(Q4ExpertArgs a) {
 
   run_step<TILES, W>(a, sorted, step1, feed, share1, sh, false);
   if (!meet(a.meet, a.status)) return;
-  run_step<TILES, W>(a, sorted, step2, feed, share2, sh, true);
+  run_step<TILES2, W>(a, sorted, step2, feed, share2, sh2, true);
   copy_wait<0>();
   const int fours = a.columns[0] / 4, items = a.T * fours;
   auto item_of = [&](int j) { return ((j >> 3) * gridDim.x + blockIdx.x) * 8 + (j & 7); };  // 128 bytes of fp32 after the other to the CTAs
@@ -513,51 +516,66 @@ __global__ void __launch_bounds__(THREADS, 2) experts_kernel(Q4ExpertArgs a) {
   }
 }
 
-template <class W, int TILES>
+template <class W, int TILES, int TILES2>
 cudaError_t launch(Q4ExpertArgs a, cudaStream_t s) {
   int sms = 0;
   cudaError_t err = sm_count(&sms);
   if (err != cudaSuccess) return err;
-  const int pairs = a.T * a.k, wide = a.columns[0] > a.columns[1] ? a.columns[0] : a.columns[1];
-  a.row_stride = row_bytes(wide);
-  a.scale_stride = ((wide + CHUNK - 1) / CHUNK + 3) / 4 * 4;
-  a.part_cols = 8 * TILES;
-  const size_t fixed = (size_t)WARPS * depth_of(TILES, W::SLABS) * W::SLOT + sizeof(float) * WARPS * a.part_cols * part_stride(W::SLABS) + sorted_bytes(a.E, pairs);
-  const size_t row = a.row_stride + sizeof(float) * a.scale_stride;
-  auto fit = [&](size_t room) { return room > fixed ? (int)((room - fixed) / row < 8 * TILES ? (room - fixed) / row : 8 * TILES) : 0; };
-  // two CTAs an SM where their rows of terms are half of a block's or more, else one
+  constexpr int tiles[2] = {TILES, TILES2};
+  constexpr size_t rings = (size_t)WARPS * depth_of(TILES, W::SLABS) * W::SLOT;
+  const size_t sorted = sorted_bytes(a.E, a.T * a.k);
+  size_t sums[2], row[2];  // bytes of the units' sums; of a row of terms and its scales
+  for (int i = 0; i < 2; ++i) {
+    a.row_stride[i] = row_bytes(a.columns[i]);
+    a.scale_stride[i] = ((a.columns[i] + CHUNK - 1) / CHUNK + 3) / 4 * 4;
+    a.part_cols[i] = 8 * tiles[i];
+    sums[i] = sizeof(float) * WARPS * a.part_cols[i] * part_stride(W::SLABS);
+    row[i] = a.row_stride[i] + sizeof(float) * a.scale_stride[i];
+  }
+  // two CTAs an SM where their rows of terms are half of a block's or more in both steps, else one
   int per_sm = 2;
-  a.staged = fit(SMEM_HALF);
-  if (a.staged < 4 * TILES) per_sm = 1, a.staged = fit(SMEM_MAX);
-  for (int i = 0; i < 2; ++i) a.block[i] = a.rows[i] = a.staged / a.terms[i];
-  a.resident = a.T * a.terms[0] <= a.staged;
+  auto fit = [&](size_t room) {
+    bool half = true;
+    for (int i = 0; i < 2; ++i) {
+      const size_t taken = rings + sums[i] + sorted, rows = room > taken ? (room - taken) / row[i] : 0;
+      a.staged[i] = rows < 8u * tiles[i] ? (int)rows : 8 * tiles[i];
+      half = half && a.staged[i] >= 4 * tiles[i];
+    }
+    return half;
+  };
+  if (!fit(SMEM_HALF)) per_sm = 1, fit(SMEM_MAX);
+  for (int i = 0; i < 2; ++i) a.block[i] = a.rows[i] = a.staged[i] / a.terms[i];
+  a.resident = a.T * a.terms[0] <= a.staged[0];
   if (a.resident) a.block[0] = 8 * TILES / a.terms[0];
+  const size_t step1 = sums[0] + a.staged[0] * row[0], step2 = sums[1] + a.staged[1] * row[1];  // one after the other in the same place
+  a.sorted_at = (int)(rings + (step1 > step2 ? step1 : step2));
   a.slabs[0] = a.columns[1] / (8 * W::SLABS), a.slabs[1] = a.columns[0] / (ROWS * W::SLABS);  // d_ff and d_model are multiples of 32
   for (int i = 0; i < 2; ++i) a.slabs_inverse[i] = inverse_of(a.slabs[i]);
   a.grid_inverse = inverse_of(sms * per_sm), a.k_inverse = inverse_of(a.k);
-  err = allow_smem<experts_kernel<W, TILES>>(SMEM_MAX);
+  err = allow_smem<experts_kernel<W, TILES, TILES2>>(SMEM_MAX);
   if (err != cudaSuccess) return err;
   void* args[] = {&a};
   STRATA_LAUNCH(KID_Q4_EXPERTS, s,
-                err = cudaLaunchCooperativeKernel((const void*)experts_kernel<W, TILES>, dim3(sms * per_sm), dim3(THREADS), args,
-                                                  fixed + a.staged * row, s));
+                err = cudaLaunchCooperativeKernel((const void*)experts_kernel<W, TILES, TILES2>, dim3(sms * per_sm), dim3(THREADS), args,
+                                                  a.sorted_at + sorted, s));
   return err;
 }
 
-// The kernel of one format.  Blocks of a single tile of 8 columns, with a deeper ring, where an expert has two columns or fewer on average (or can have no
-// more than 8); else of up to three tiles.  An expert with more columns than a block is passed over again: 16 tokens, 6 of 64 experts, fp16 (3 columns
-// on average) 66 to 73 us in single tiles, 62 in up to three.  Single tiles in units of 32 rows where a CTA will have 8 or more of them in step 1, of 16 where
-// that would leave warps without work: 64 tokens, 10 of 512 experts (75 units of 16 a CTA) 218 us in units of 16, 194 in units of 32.
+// The kernel of one format.  Blocks of a single tile of 8 columns in step 1 (two in step 2, where a pair has two), with a deeper ring, where an expert
+// has two columns or fewer on average over both steps or where one block can hold all; else of up to three tiles.  An expert with more columns than a
+// block is passed over again: 64 tokens, 10 of 512 experts and one more that all list, bf16 (2.1 columns on average) 1,043 us in single tiles, 980 in up
+// to three; 16 tokens, 6 of 64, fp16 (2.25) 60 us either way.  Single tiles in units of 32 rows where a CTA will have 8 or more of them in step 1, of 16
+// where that would leave warps without work: 64 tokens, 10 of 512 experts (75 units of 16 a CTA) 218 us in units of 16, 194 in units of 32.
 template <int GROUP, bool ZEROS, bool SCALE_F16>
 cudaError_t launch_format(const Q4ExpertArgs& a, cudaStream_t s) {
   int sms = 0;
   cudaError_t err = sm_count(&sms);
   if (err != cudaSuccess) return err;
-  const int terms = a.terms[0] > a.terms[1] ? a.terms[0] : a.terms[1];
+  const bool one_block = a.T * a.terms[0] <= 8 && a.T * a.terms[1] <= 16;
   const int64_t pairs = a.T * a.k, used = pairs * a.E / (pairs + a.E);  // experts in use, about
-  if (a.T * terms > 8 && pairs * terms > 2 * a.E) return launch<Q4<GROUP, ZEROS, SCALE_F16>, TILES_MAX>(a, s);
-  if (used * (a.columns[1] / 8) >= 16 * 2 * sms) return launch<Q4<GROUP, ZEROS, SCALE_F16, 2>, 1>(a, s);
-  return launch<Q4<GROUP, ZEROS, SCALE_F16>, 1>(a, s);
+  if (!one_block && pairs * (a.terms[0] + a.terms[1]) > 4 * a.E) return launch<Q4<GROUP, ZEROS, SCALE_F16>, TILES_MAX, TILES_MAX>(a, s);
+  if (used * (a.columns[1] / 8) >= 16 * 2 * sms) return launch<Q4<GROUP, ZEROS, SCALE_F16, 2>, 1, 2>(a, s);
+  return launch<Q4<GROUP, ZEROS, SCALE_F16>, 1, 2>(a, s);
 }
 template <int GROUP>
 cudaError_t launch_group(const strata_q4_experts_t& ex, const Q4ExpertArgs& a, cudaStream_t s) {
