@@ -220,11 +220,12 @@ strata_status strata_moe_stack_host(const strata_experts_t* ex, const uint16_t* 
 /* Failure-detection self-test (no counterpart on the pages).  Every wait in the library's kernels is
  * bounded: past a limit (2 s) it records STRATA_E_TIMEOUT in the workspace's status word and the
  * kernel returns instead of hanging.  This call runs the decode layer's two kinds of wait -- a poll of
- * an exchange word for a tag, and an mbarrier phase -- in one CTA on conditions that never hold, with
- * the limit limit_ns (in [1000, 2e9]), so both expire: afterwards strata_poll_status returns
- * STRATA_E_TIMEOUT, strata_clear_status clears it, and the context stays usable.  Uses the first 8
- * bytes of the workspace's logits area as the never-written word (set to 0 first); ws as for T = 1.
- * Enqueued on stream; takes about 2 x limit_ns on the device. */
+ * an exchange word for a tag, and an mbarrier phase -- and the meeting of strata_moe_q4_experts' CTAs
+ * (strata_moe_ops.h), each in one CTA on a condition that never holds, with the limit limit_ns (in
+ * [1000, 2e9]), so all three expire: afterwards strata_poll_status returns STRATA_E_TIMEOUT,
+ * strata_clear_status clears it, and the context stays usable.  Uses the first 48 bytes of the
+ * workspace's logits area for the words that are waited on (set to 0 first); ws as for T = 1.
+ * Enqueued on stream; takes about 3 x limit_ns on the device. */
 strata_status strata_moe_wait_selftest(void* ws, size_t ws_bytes, uint64_t limit_ns, void* stream);
 
 /* Blob checksums, for verifying an upload or a device pack against the bytes it came from.

@@ -300,6 +300,8 @@ cudaError_t launch_blob_crc32(const uint8_t* blobs, int64_t stride, int64_t n_bl
 // The decode layer's bounded waits on conditions that never hold, with limit_ns (decode_fused.cu).
 cudaError_t launch_wait_selftest(const uint64_t* word, uint32_t tag, unsigned long long limit_ns, int* status,
                                  cudaStream_t s);
+// A meeting of strata_moe_q4_experts that nobody else comes to, with copies in flight (q4_experts.cu); words: 36 bytes of zeros.
+cudaError_t launch_meet_selftest(char* words, unsigned long long limit_ns, int* status, cudaStream_t s);
 cudaError_t launch_route_decode(const float* x, int T, int apply_rmsnorm, const uint16_t* w_router,
                                 const float* bias, int E, int q2_offset, int32_t* ids, float* weights,
                                 float* logits_out, const WsLayout& L, char* ws, cudaStream_t s);

@@ -16,7 +16,26 @@ Scratch scratch_of(const strata_q4_experts_t& ex, int T) {
   return s;
 }
 
+// Part of the wait self-test: one CTA with copies on their way comes to a meeting of two.  words: 16 bytes of zeros, then the meeting's count.
+// It must run out, and the copies be there afterwards (else ST_CORRUPT too).
+__global__ void __launch_bounds__(q4x::THREADS) meet_selftest_kernel(char* words, unsigned long long limit_ns, int* status) {
+  __shared__ uint4 slots[q4x::THREADS];
+  const uint32_t slot = smem_u32(slots + threadIdx.x);
+  slots[threadIdx.x] = make_uint4(~0u, ~0u, ~0u, ~0u);
+  __syncthreads();
+  q4::copy_async<16>(slot, words);
+  q4::copy_commit();
+  const bool met = q4x::meet(reinterpret_cast<unsigned*>(words + 16), 2, status, limit_ns);
+  const uint4 v = q4::lds16(slot);
+  if (met || (v.x | v.y | v.z | v.w)) set_status(status, ST_CORRUPT);
+}
+
 }  // namespace
+
+cudaError_t launch_meet_selftest(char* words, unsigned long long limit_ns, int* status, cudaStream_t s) {
+  STRATA_LAUNCH(KID_WAIT_SELFTEST, s, meet_selftest_kernel<<<1, q4x::THREADS, 0, s>>>(words, limit_ns, status));
+  return cudaGetLastError();
+}
 
 size_t q4_experts_scratch(const strata_q4_experts_t& ex, int T) { return scratch_of(ex, T).total; }
 

@@ -308,8 +308,9 @@ struct Units {
 template <class W, int DEPTH>
 using ExpertFeed = Feed<W, DEPTH, Units<W>>;
 
-// All CTAs of the grid meet; false when the others did not come within the limit.
-__device__ __forceinline__ bool meet(unsigned* count, int* status) {
+// `ctas` CTAs meet.  False (and ST_TIMEOUT) when the others did not come within the limit (the experts' kernel uses the library's; the wait self-test
+// passes a short one): the kernel then returns, so copies still on their way to shared memory are waited for.
+__device__ __forceinline__ bool meet(unsigned* count, unsigned ctas, int* status, unsigned long long limit_ns = kWaitLimitNs) {
   __syncthreads();
   bool late = false;
   if (threadIdx.x == 0) {
@@ -319,8 +320,8 @@ __device__ __forceinline__ bool meet(unsigned* count, int* status) {
     for (unsigned i = 1;; ++i) {
       unsigned n;
       asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(count) : "memory");
-      if (n >= gridDim.x) break;
-      if ((i & 1023u) == 0 && globaltimer() - t0 > kWaitLimitNs) {
+      if (n >= ctas) break;
+      if ((i & 1023u) == 0 && globaltimer() - t0 > limit_ns) {
         set_status(status, ST_TIMEOUT);
         late = true;
         break;
@@ -328,7 +329,9 @@ __device__ __forceinline__ bool meet(unsigned* count, int* status) {
     }
     __threadfence();
   }
-  return !__syncthreads_or(late);
+  if (!__syncthreads_or(late)) return true;
+  copy_wait<0>();
+  return false;
 }
 
 struct Shared {  // the CTA's dynamic shared memory behind the rings, in step 1 or 2
@@ -495,7 +498,7 @@ __global__ void __launch_bounds__(THREADS, 2) experts_kernel(Q4ExpertArgs a) {
   ExpertFeed<W, DEPTH> feed(Units<W>(sorted, step1, step2, warp, lane, share1, share2), smem_u32(smem) + warp * (DEPTH * W::SLOT), lane);
 
   run_step<TILES, W>(a, sorted, step1, feed, share1, sh, false);
-  if (!meet(a.meet, a.status)) return;
+  if (!meet(a.meet, gridDim.x, a.status)) return;
   run_step<TILES2, W>(a, sorted, step2, feed, share2, sh2, true);
   copy_wait<0>();
   const int fours = a.columns[0] / 4, items = a.T * fours;
@@ -503,7 +506,7 @@ __global__ void __launch_bounds__(THREADS, 2) experts_kernel(Q4ExpertArgs a) {
   float weights[WEIGHTS];
   int item = item_of(threadIdx.x);
   if (item < items) slot_weights(a, item / fours, 0, weights);
-  if (!meet(a.meet + 1, a.status)) return;
+  if (!meet(a.meet + 1, gridDim.x, a.status)) return;
   for (int j = threadIdx.x; item < items;) {
     combine4(a, item / fours, item % fours * 4, weights);
     item = item_of(j += THREADS);
