@@ -236,7 +236,8 @@ typedef struct strata_linear {
 /* y[t][n] = sum over k of w[n][k] * x[t][k] + bias[n].  bias fp32 [n_out] or NULL.  x on a 16-byte boundary, y aligned to its elements;
  * y must not overlap x or bias.  No workspace.  Products are exact and their sums fp32; an fp32 x enters them with 22 bits beside 4-bit weights (24
  * beside bf16 ones), a bf16 or fp16 x with all its bits, each down to 2^-40 of the
- * largest of the 128 columns around it.  A token whose x holds a NaN or an infinity (beside bf16 weights: or a number that rounds to bf16's infinity)
+ * largest of the 128 columns around it.  Scales are below 2^100 in magnitude: with larger ones sums may pass fp32's range where the results do not.
+ * A token whose x holds a NaN or an infinity (beside bf16 weights: or a number that rounds to bf16's infinity)
  * may give NaN in its whole row; other tokens' rows do not change.
  * Built for few tokens: 4-bit weights are read once for up to 24 (16-bit x) or 12 (fp32) of them, bf16 weights for 24 (bf16), 12 (fp16) or 8 (fp32),
  * and the time of more grows in proportion. */
@@ -270,7 +271,9 @@ size_t strata_moe_q4_experts_workspace_bytes(const strata_q4_experts_t* ex, int3
 /* out[t] = sum over i of weights[t][i] * D_e (silu(G_e x[t]) * (U_e x[t])), e = ids[t][i], in the order of i, silu(z) = z / (1 + exp(-z)).
  * ids int32 [T][top_k], weights fp32 [T][top_k] (strata_moe_select's).  A slot with an id of -1 or a weight of 0 has no expert:
  * nothing of it is read; a token without any gets zeros.  An expert may stand twice in a token's list.  A shared expert is one more expert that every
- * token lists.  T in [0, 64].  x and out on 16-byte boundaries; out must not overlap x, ids or weights.
+ * token lists.  T in [0, 64].  Made for lists that spread over the experts: one that more tokens list than a block holds (8 of them with a 16-bit x, 4
+ * with fp32, up to three times as many where lists are crowded) is passed over again for each further block, by the same few CTAs.  64 tokens of 512
+ * experts take four times as long with a shared expert as without.  x and out on 16-byte boundaries; out must not overlap x, ids or weights.
  * Products are exact and summed in fp32 as in strata_moe_linear; the hidden values of an expert are held in fp32 and enter the
  * second product with 22 bits.  NaN and infinities as there.
  * An id outside [-1, n_expert) sets STRATA_E_CORRUPT in the workspace's status word and the call computes nothing (out keeps its contents).
