@@ -4,10 +4,11 @@
 // Mathematics.  y[row] = sum over groups of s[row][group] * (sum over its columns of (code - zero) * x).  code - zero is a whole number of magnitude
 // below 16, exact in fp16; x enters as fp16 terms (stage8), each a column of the products, so the products are exact and their sums fp32; the
 // scale multiplies a group's fp32 sum, the activations' power of two a chunk's.
-// What bounds it: the instructions around the codes, close above the weights' bytes.  16 rows x 128 columns (1 KB) leave a scheduler 176 cycles at
-// the measured copy rate.  Widening takes 5 integer instructions a word of 8 codes (2 cycles each) and 4 subtractions, 8 words a lane: 80 cycles of the
-// integer pipe; with scales, sums and copies a chunk comes to 176 instructions, fewer in units of 32 rows (2,560 -> 131,072 rows, one token: 189 MB in 38.2
-// and 36.9 us, 5.1 TB/s).  bf16 operands, with 7 mantissa bits, take 7 integer instructions a word: 57 us.  An MMA takes 8 cycles (measured, with 4 warps a scheduler), 8 of them
+// What bounds it: no pipe alone.  16 rows x 128 columns leave a scheduler 190 cycles at the measured copy rate (1 KB of codes; 214 with the scales of
+// groups of 32).  Widening takes 5 integer instructions a word of 8 codes (2 cycles each) and 4 subtractions, 8 words a lane: 80 cycles of the
+// integer pipe; with scales, sums and copies a chunk comes to 176 instructions, 152 in units of 32 rows (2,560 -> 131,072 rows, one token: 189 MB in 38.2
+// and 36.6 us, 5.2 TB/s).  There a chunk takes a scheduler 280 cycles: its four warps issue in 67% of the cycles in which the SM is active, and wait for
+// the integer and tensor pipes, for dispatch and for fixed latencies in the others; a fifth of the call is its start and its end.  bf16 operands, with 7 mantissa bits, take 7 integer instructions a word: 57 us.  An MMA takes 8 cycles (measured, with 4 warps a scheduler), 8 of them
 // a chunk and tile of 8 columns, so two tiles are hidden.  Warp-level MMAs take the operands where widening leaves them, in registers; tcgen05 would
 // have four times the codes' bytes pass shared memory.
 // Tried and not kept: codes as e4m3 bytes (a code in the low bits of a byte is code * 2^-9 without further work): mma.sync of e4m3 turns into

@@ -9,8 +9,13 @@
 // equal contiguous stretches, one of each to a CTA; S warps share a unit.  All CTAs are resident (a cooperative launch) and meet between the
 // steps; the copies of weights run ahead across the meeting, so step 2 finds its first chunks in shared memory.
 //
-// What bounds it: 64 tokens of 512 experts (1.03 GB in 209 us, 4.9 TB/s of 6.8) the instructions around the codes, see q4_core.cuh; one token (26 MB in 22 us,
-// 3.9 at the copy rate) a chain of latencies: launch 4 us, sort 1, first chunks 2, step 1 5, meeting 2, h 1.3, step 2 2.5, meeting 2, step 3 2.
+// The stretches are equal in units, and a unit is passed over once for each block of its expert's pairs: an expert of many pairs keeps its few CTAs while the
+// others wait at the meeting (64 tokens of 512 experts, by events after a flush of L2: 236 us with even lists, 656 with a hottest expert of 54 tokens and 235 in
+// use, 980 to 1,016 with one more expert that all list; fp32 335 and 1,289).
+//
+// What bounds it: 64 tokens of 512 experts (1.03 GB in 209 us, 4.9 TB/s of 6.8) no pipe alone, see q4_core.cuh (issue in 57% of the cycles; a fifth of the
+// warps' time at barriers, for windows, meetings and the stretch that holds an expert of two blocks); one token (26 MB in 22 us, 3.9 at the copy rate)
+// a chain of latencies: launch 4 us, sort 1, first chunks 2, step 1 5, meeting 2, h 1.3, step 2 2.5, meeting 2, step 3 2.
 // Three kernels with programmatic launches instead of the meetings took 30 us for one token.
 #pragma once
 #include "q4_core.cuh"
@@ -568,7 +573,7 @@ cudaError_t launch(Q4ExpertArgs a, cudaStream_t s) {
 // has two columns or fewer on average over both steps or where one block can hold all; else of up to three tiles.  An expert with more columns than a
 // block is passed over again: 64 tokens, 10 of 512 experts and one more that all list, bf16 (2.1 columns on average) 1,043 us in single tiles, 980 in up
 // to three; 16 tokens, 6 of 64, fp16 (2.25) 60 us either way.  Single tiles in units of 32 rows where a CTA will have 8 or more of them in step 1, of 16
-// where that would leave warps without work: 64 tokens, 10 of 512 experts (75 units of 16 a CTA) 218 us in units of 16, 194 in units of 32.
+// where that would leave warps without work: 64 tokens, 10 of 512 experts (75 units of 16 a CTA) 234 us in units of 16, 209 in units of 32.
 template <int GROUP, bool ZEROS, bool SCALE_F16>
 cudaError_t launch_format(const Q4ExpertArgs& a, cudaStream_t s) {
   int sms = 0;
